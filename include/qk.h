@@ -105,9 +105,19 @@ typedef enum qk_glu_layout {
 } qk_glu_layout;
 
 typedef enum qk_wtype {
-    QK_W_Q4_0 = 0, /* 18-byte blocks: half d, 16 nibble bytes; value (nibble - 8) * d */
-    QK_W_Q8_0 = 1  /* 34-byte blocks: half d, 32 int8; value q * d                    */
+    QK_W_Q4_0 = 0,   /* 18-byte blocks: half d, 16 nibble bytes; value (nibble - 8) * d */
+    QK_W_Q8_0 = 1,   /* 34-byte blocks: half d, 32 int8; value q * d                    */
+    QK_W_Q4_G64 = 2, /* groups of 64 with a scale and a zero point, 36-byte blocks:
+                        half d, uint8 z, one unread byte, 32 nibble bytes;
+                        value (nibble - z) * d                                          */
+    QK_W_Q4_G128 = 3 /* the same for groups of 128, 68-byte blocks (64 nibble bytes)    */
 } qk_wtype;
+
+/* Element type of rows that a call takes in more than one precision. */
+typedef enum qk_elem {
+    QK_ELEM_F32 = 0, /* binary32 */
+    QK_ELEM_BF16 = 1 /* bfloat16 */
+} qk_elem;
 
 /* ------------------------------------------------------------------ misc */
 
@@ -259,10 +269,18 @@ QK_API qk_status qk_glu_q8_1_ex(qk_glu_kind kind, qk_glu_layout layout,
 /*
  * Weights arrive as canonical row-major blocks ([N][K/32] blocks of
  * QK_W_Q4_0 or QK_W_Q8_0 bytes; Q4_0 element j < 16 is the low nibble of byte
- * j, element j+16 its high nibble). qk_weight_pack rearranges them once into
+ * j, element j+16 its high nibble). The group-scaled types arrive as [N][K/G]
+ * blocks, G = 64 or 128; their nibble bytes are G/32 runs of 16 bytes, each run
+ * ordered like a Q4_0 block's. A zero point is 0..15: the byte's upper four
+ * bits are not read. qk_weight_pack rearranges them once into
  * the device layout the projection kernels stream with 128-bit loads. The
  * packed layout is private to this library and may change between versions;
- * its size is qk_weight_packed_bytes(). K must be a multiple of 32.
+ * its size is qk_weight_packed_bytes(). K must be a multiple of 32 (Q4_0,
+ * Q8_0) or of G.
+ * Q4_0 and Q8_0 are read by qk_mmvq, qk_mmvq_static_ws, qk_mmvq_id and
+ * qk_mmvq_id_slots, Q4_0 also by qk_mmq; the group-scaled types by the same
+ * calls except qk_mmq; Q4_0 and the group-scaled types by qk_mmq_id and
+ * qk_mmq_id_slots.
  */
 QK_API size_t qk_weight_packed_bytes(qk_wtype wtype, int64_t N, int64_t K);
 
@@ -289,6 +307,9 @@ typedef struct qk_proj {
  * Per 32-block b, from the stored halves (exact integer block dot D):
  *   Q4_0: y += d_w * (d_a * D - 8 * s_a),  D = sum nibble_i * q_i
  *   Q8_0: y += d_w * d_a * D,              D = sum w_i * q_i
+ * and per group g of the group-scaled types (the blocks b inside it):
+ *   y += d_g * sum_b d_a * D_b,            D_b = sum (nibble_i - z_g) * q_i
+ * (the image's s is not read; every D is exact, the sums are binary32).
  *   img  [T][img_row_blocks] Q8_1; every projection's K <= 32*img_row_blocks
  *   T    1..8 image rows (tokens); rows >= *d_live_rows are not written
  *   projs host array of n_proj (1..8) descriptors; outputs must not share a
@@ -300,13 +321,14 @@ typedef struct qk_proj {
  *        to zero before its kernels finish, and scratch partial sums; so it
  *        can be reused by later calls (and graph replays) on the same stream
  *        without zeroing again. Calls that may run concurrently need
- *        separate workspaces.
+ *        separate workspaces. The group-scaled types use none: with only those
+ *        the size is 0 and ws may be NULL.
  * The work is split by bytes over the device's SMs; partial sums of a row
  * tile shared by several CTAs go through ws and are added in a fixed order,
  * so outputs are deterministic on a given device.
  * Errors: QK_ERR_ARG, QK_ERR_UNSUPPORTED (T > 8 or n_proj > 8),
- * QK_ERR_SHAPE (K % 32, K beyond the image, y_stride < N), QK_ERR_ALIAS,
- * QK_ERR_WORKSPACE (ws null or too small).
+ * QK_ERR_SHAPE (K % 32 or K % G, K beyond the image, y_stride < N), QK_ERR_ALIAS,
+ * QK_ERR_WORKSPACE (ws null or too small where one is needed).
  */
 QK_API size_t qk_mmvq_workspace_bytes(int32_t n_proj, const qk_proj *projs);
 
@@ -449,7 +471,38 @@ QK_API qk_status qk_moe_combine(const float *expert_out, int64_t out_stride, con
                                 int32_t k, int64_t N, float *y, int64_t y_stride, const int32_t *d_live_rows,
                                 qk_stream stream);
 
+/*
+ * qk_moe_combine_bf16 -- qk_moe_combine over bfloat16 expert outputs (the pair
+ * rows that qk_mmq_id_slots writes); the same binary32 sum in slot order.
+ *   expert_out [rows*k][out_stride] bfloat16 bits, 8-byte aligned; y 16-byte
+ *   aligned; strides and N multiples of 4; N <= 2^25.
+ * Errors: as qk_moe_combine.
+ */
+QK_API qk_status qk_moe_combine_bf16(const uint16_t *expert_out, int64_t out_stride, const float *wts, int64_t rows,
+                                     int32_t k, int64_t N, float *y, int64_t y_stride, const int32_t *d_live_rows,
+                                     qk_stream stream);
+
 /* ---------------------------------------------------------- prefill */
+
+/*
+ * qk_glu_q8_0 -- the GLU producer emitting the prefill Q8_0 planes that qk_mmq
+ * and qk_mmq_id_slots read (the kinds, layouts, alpha and limit of
+ * qk_glu_q8_1_ex).
+ *   elem  type of the a and b rows: binary32 (qk_mmq's outputs) or bfloat16
+ *         (qk_mmq_id's); strides in elements
+ *   out   [T][out_stride] F32 = act(g) * u in binary32, columns 0..N-1 of live
+ *         rows; NULL when only the planes are wanted
+ *   qs    [T][row_blocks*32] int8 codes, 4-byte aligned; d [T][row_blocks] half
+ *         scales: bit-identical to qk_quantize_q8_0 of the out values (blocks
+ *         from N/32 up to row_blocks are zero)
+ * T = 0 launches nothing. Errors: QK_ERR_ARG (null, bad enum, N > 2^25,
+ * row_blocks > 2^20, alpha not finite, limit not positive and finite),
+ * QK_ERR_SHAPE (N % 32 != 0, strides or row_blocks too small), QK_ERR_ALIAS.
+ */
+QK_API qk_status qk_glu_q8_0(qk_glu_kind kind, qk_glu_layout layout, qk_elem elem, const void *a, int64_t a_stride,
+                             const void *b, int64_t b_stride, int64_t T, int64_t N, float *out, int64_t out_stride,
+                             int8_t *qs, uint16_t *d, int64_t row_blocks, float alpha, float limit,
+                             const int32_t *d_live_rows, qk_stream stream);
 
 /*
  * qk_mmq -- prefill dense contraction on a Q8_0 image (minfer doc 52,
@@ -520,6 +573,61 @@ QK_API size_t qk_mmq_workspace_bytes(int64_t T, int32_t n_proj, const qk_proj *p
 QK_API qk_status qk_mmq(const int8_t *qs, const uint16_t *d, int64_t row_blocks, int64_t T,
                  int32_t n_proj, const qk_proj *projs, void *ws, size_t ws_bytes,
                  qk_stream stream);
+
+/* One routed prefill projection: E experts' packed weights back to back, bfloat16 outputs. */
+typedef struct qk_proj_id16 {
+    int32_t wtype;          /* QK_W_Q4_0, QK_W_Q4_G64 or QK_W_Q4_G128 */
+    int32_t n_experts;      /* E */
+    const void *w;          /* expert e at w + e * qk_weight_packed_bytes(wtype, N, K) */
+    int64_t N;              /* output features per expert */
+    int64_t K;              /* input features */
+    uint16_t *y;            /* [rows*k][y_stride] bfloat16 bits, pair p at row p */
+    int64_t y_stride;       /* >= N */
+} qk_proj_id16;
+
+/*
+ * qk_mmq_id -- routed prefill: the projections of qk_mmvq_id for prompts, as
+ * matrix products grouped by expert with ragged sizes, on a Q8_0 image.
+ *   qs [rows][row_blocks*32] int8 and d [rows][row_blocks] half, as for qk_mmq
+ * For every expert e and every planned item p in items[offsets[e] ..
+ * offsets[e] + counts[e] - 1]: y[p][:] = W_e * image row (p / k). Experts with
+ * no items read no weights; pairs not in the plan are not written. The plan is
+ * qk_moe_plan's (or qk_route_plan's); a plan from anywhere else gives
+ * unspecified outputs but no access outside the buffers: counts are clamped to
+ * [0, rows * k], and an item position outside items or a pair outside the
+ * bucket is skipped. Plans that name a pair twice are such plans.
+ * Runs on the tensor cores: operands (nibble - z) * d_w and q * d_a, each
+ * rounded once to binary16 (by at most 2^-11, relative), accumulated in binary32
+ * over all of K and rounded once to bfloat16 (by at most 2^-8, which the
+ * operands' rounding stays well below); 16-bit rows halve the traffic between
+ * the routed products.
+ *   projs  host array of n_proj (1..8) descriptors with one n_experts; outputs
+ *          must not share a byte (disjoint column windows of one buffer with one
+ *          y_stride are allowed: gate and up as the packed rows of a GLU)
+ *   ws     workspace of qk_mmq_id_workspace_bytes bytes, 128-byte aligned:
+ *          scratch, no state kept. Calls that may run concurrently need separate
+ *          ones.
+ *   rows   1..2^24 bucket rows, k 1..64, n_experts 1..1024
+ * Errors: QK_ERR_ARG, QK_ERR_SHAPE, QK_ERR_UNSUPPORTED (also Q8_0 weights),
+ * QK_ERR_ALIAS (also an output over counts, offsets or items),
+ * QK_ERR_WORKSPACE.
+ */
+/* img_rows: the image's row count, rows for qk_mmq_id and rows * k for qk_mmq_id_slots. */
+QK_API size_t qk_mmq_id_workspace_bytes(int64_t img_rows, int32_t n_proj, const qk_proj_id16 *projs);
+QK_API qk_status qk_mmq_id(const int8_t *qs, const uint16_t *d, int64_t row_blocks, int64_t rows, int32_t k,
+                           int32_t n_proj, const qk_proj_id16 *projs, const int32_t *counts, const int32_t *offsets,
+                           const int32_t *items, void *ws, size_t ws_bytes, qk_stream stream);
+
+/*
+ * qk_mmq_id_slots -- qk_mmq_id with one image row per pair: y[p][:] = W_e *
+ * image row p (the down projection of a routed FFN, whose planes come from
+ * qk_glu_q8_0 over the rows * k pair rows with offsets + E as its d_live_rows).
+ * The image has rows * k rows. Errors: as qk_mmq_id.
+ */
+QK_API qk_status qk_mmq_id_slots(const int8_t *qs, const uint16_t *d, int64_t row_blocks, int64_t rows, int32_t k,
+                                 int32_t n_proj, const qk_proj_id16 *projs, const int32_t *counts,
+                                 const int32_t *offsets, const int32_t *items, void *ws, size_t ws_bytes,
+                                 qk_stream stream);
 
 #ifdef __cplusplus
 }

@@ -274,3 +274,35 @@ def nmse(a, ref) -> float:
     ref = np.asarray(ref, dtype=np.float64)
     den = float(np.sum(ref * ref))
     return float(np.sum((a - ref) ** 2)) / den if den > 0 else float(np.sum((a - ref) ** 2))
+
+
+# ------------------------------------------------------------------ group-scaled weights, routed prefill
+def dequant_group(W: np.ndarray, N: int, K: int) -> np.ndarray:
+    """Group-scaled blocks [N, K/G, 4 + G/2] -> float64 [N][K], value (nibble - z) * d.
+
+    A block's nibble bytes are runs of 16: element j of a run's 32 is the low nibble of byte j for
+    j < 16, else the high nibble of byte j - 16; z is the low four bits of the third byte."""
+    blocks = W.reshape(N, -1, W.shape[-1])
+    G = 2 * (blocks.shape[-1] - 4)
+    assert blocks.shape[1] * G == K
+    d = np.ascontiguousarray(blocks[:, :, 0:2]).view(np.float16).astype(np.float64)
+    z = (blocks[:, :, 2:3] & 15).astype(np.float64)
+    runs = blocks[:, :, 4:].reshape(N, K // G, G // 32, 16)
+    c = np.concatenate([runs & 15, runs >> 4], axis=-1).reshape(N, K // G, G).astype(np.float64)
+    return ((c - z) * d).reshape(N, K)
+
+
+def image_values(img: np.ndarray, K: int) -> np.ndarray:
+    """Q8_1 image rows (uint8 [T][row_blocks*36]) -> float64 [T][K], value d * q."""
+    T = img.shape[0]
+    b = img.reshape(T, -1, 36)[:, :K // 32]
+    d = np.ascontiguousarray(b[:, :, 0:2]).view(np.float16).astype(np.float64)
+    return (b[:, :, 4:].view(np.int8).astype(np.float64) * d).reshape(T, K)
+
+
+def plane_values(qs: np.ndarray, dh: np.ndarray, K: int) -> np.ndarray:
+    """Q8_0 planes (int8 [T][row_blocks*32], uint16 [T][row_blocks]) -> float64 [T][K]."""
+    T = qs.shape[0]
+    q = qs.reshape(T, -1, 32)[:, :K // 32].astype(np.float64)
+    d = np.ascontiguousarray(dh.reshape(T, -1)[:, :K // 32]).view(np.float16).astype(np.float64)
+    return (q * d[:, :, None]).reshape(T, K)

@@ -24,7 +24,8 @@ NORM = {"plain": 0, "mul": 1, "mul_add": 2, "scale": 3}
 GLU = {"swiglu": 0, "geglu_tanh": 1, "reglu": 2, "geglu_erf": 3, "geglu_quick": 4, "swiglu_oai": 5,
        "swiglu_clamp": 6}
 LAYOUT = {"separate": 0, "packed": 1, "packed_swapped": 2}
-WTYPE = {"q4_0": 0, "q8_0": 1}
+WTYPE = {"q4_0": 0, "q8_0": 1, "q4_g64": 2, "q4_g128": 3}
+ELEM = {"f32": 0, "bf16": 1}
 Q8_1_BLOCK_BYTES = 36
 
 
@@ -43,6 +44,11 @@ class qk_proj(C.Structure):
 class qk_proj_id(C.Structure):
     _fields_ = [("wtype", C.c_int32), ("n_experts", C.c_int32), ("w", C.c_void_p), ("N", C.c_int64),
                 ("K", C.c_int64), ("y", C.c_void_p)]
+
+
+class qk_proj_id16(C.Structure):
+    _fields_ = [("wtype", C.c_int32), ("n_experts", C.c_int32), ("w", C.c_void_p), ("N", C.c_int64),
+                ("K", C.c_int64), ("y", C.c_void_p), ("y_stride", C.c_int64)]
 
 
 class qk_image_memo(C.Structure):
@@ -90,6 +96,11 @@ _SIGS = {
                                     C.c_int),
     "qk_image_memo_quantize_q8_1": ([C.POINTER(qk_image_memo), P, I64, I64, I64, P, I64, C.POINTER(I32), P],
                                     C.c_int),
+    "qk_moe_combine_bf16": ([P, I64, P, I64, I32, I64, P, I64, P, P], C.c_int),
+    "qk_glu_q8_0": ([C.c_int, C.c_int, C.c_int, P, I64, P, I64, I64, I64, P, I64, P, P, I64, F32, F32, P, P], C.c_int),
+    "qk_mmq_id_workspace_bytes": ([I64, I32, C.POINTER(qk_proj_id16)], SZ),
+    "qk_mmq_id": ([P, P, I64, I64, I32, I32, C.POINTER(qk_proj_id16), P, P, P, P, SZ, P], C.c_int),
+    "qk_mmq_id_slots": ([P, P, I64, I64, I32, I32, C.POINTER(qk_proj_id16), P, P, P, P, SZ, P], C.c_int),
     "qk_mmq": ([P, P, I64, I64, I32, C.POINTER(qk_proj), P, C.c_size_t, P], C.c_int),
 }
 
@@ -198,6 +209,16 @@ def qk_glu_q8_1_ex(kind, layout, a, a_stride, b, b_stride, T, N, out, out_stride
                                                    _stream(stream)))
 
 
+def qk_glu_q8_0(kind, layout, elem, a, a_stride, b, b_stride, T, N, out, out_stride, qs, d, row_blocks,
+                alpha=1.702, limit=7.0, d_live_rows=None, stream=None):
+    kind = GLU[kind] if isinstance(kind, str) else int(kind)
+    layout = LAYOUT[layout] if isinstance(layout, str) else int(layout)
+    elem = ELEM[elem] if isinstance(elem, str) else int(elem)
+    _check("qk_glu_q8_0", load().qk_glu_q8_0(kind, layout, elem, _ptr(a), a_stride, _ptr(b), b_stride, T, N, _ptr(out),
+                                             out_stride, _ptr(qs), _ptr(d), row_blocks, float(alpha), float(limit),
+                                             _ptr(d_live_rows), _stream(stream)))
+
+
 # ------------------------------------------------------------------ weights
 def qk_weight_packed_bytes(wtype, N, K) -> int:
     wtype = WTYPE[wtype] if isinstance(wtype, str) else int(wtype)
@@ -219,6 +240,11 @@ def make_proj(wtype, w, N, K, y, y_stride) -> qk_proj:
 def make_proj_id(wtype, n_experts, w, N, K, y) -> qk_proj_id:
     wtype = WTYPE[wtype] if isinstance(wtype, str) else int(wtype)
     return qk_proj_id(wtype, n_experts, _ptr(w), N, K, _ptr(y))
+
+
+def make_proj_id16(wtype, n_experts, w, N, K, y, y_stride) -> qk_proj_id16:
+    wtype = WTYPE[wtype] if isinstance(wtype, str) else int(wtype)
+    return qk_proj_id16(wtype, n_experts, _ptr(w), N, K, _ptr(y), y_stride)
 
 
 def qk_mmvq_workspace_bytes(projs) -> int:
@@ -266,6 +292,11 @@ def qk_moe_combine(expert_out, out_stride, wts, rows, k, N, y, y_stride, d_live_
                                                    y_stride, _ptr(d_live_rows), _stream(stream)))
 
 
+def qk_moe_combine_bf16(expert_out, out_stride, wts, rows, k, N, y, y_stride, d_live_rows=None, stream=None):
+    _check("qk_moe_combine_bf16", load().qk_moe_combine_bf16(_ptr(expert_out), out_stride, _ptr(wts), rows, k, N,
+                                                             _ptr(y), y_stride, _ptr(d_live_rows), _stream(stream)))
+
+
 def qk_mmq_workspace_bytes(T, projs) -> int:
     arr = (qk_proj * len(projs))(*projs)
     return int(load().qk_mmq_workspace_bytes(T, len(projs), arr))
@@ -296,6 +327,24 @@ def qk_mmq(qs, d, row_blocks, T, projs, ws, ws_bytes, stream=None):
     arr = (qk_proj * len(projs))(*projs)
     _check("qk_mmq", load().qk_mmq(_ptr(qs), _ptr(d), row_blocks, T, len(projs), arr, _ptr(ws), ws_bytes,
                                    _stream(stream)))
+
+
+def qk_mmq_id_workspace_bytes(img_rows, projs) -> int:
+    arr = (qk_proj_id16 * len(projs))(*projs)
+    return int(load().qk_mmq_id_workspace_bytes(img_rows, len(projs), arr))
+
+
+def qk_mmq_id(qs, d, row_blocks, rows, k, projs, counts, offsets, items, ws, ws_bytes, stream=None):
+    arr = (qk_proj_id16 * len(projs))(*projs)
+    _check("qk_mmq_id", load().qk_mmq_id(_ptr(qs), _ptr(d), row_blocks, rows, k, len(projs), arr, _ptr(counts),
+                                         _ptr(offsets), _ptr(items), _ptr(ws), ws_bytes, _stream(stream)))
+
+
+def qk_mmq_id_slots(qs, d, row_blocks, rows, k, projs, counts, offsets, items, ws, ws_bytes, stream=None):
+    arr = (qk_proj_id16 * len(projs))(*projs)
+    _check("qk_mmq_id_slots", load().qk_mmq_id_slots(_ptr(qs), _ptr(d), row_blocks, rows, k, len(projs), arr,
+                                                     _ptr(counts), _ptr(offsets), _ptr(items), _ptr(ws), ws_bytes,
+                                                     _stream(stream)))
 
 
 # ------------------------------------------------------------------ routing

@@ -332,6 +332,73 @@ __global__ void __launch_bounds__(256) glu_q8_1_kernel(
     }
 }
 
+// The GLU producer of the prefill planes: input rows of binary32 or bfloat16 (BF16), output codes
+// and half scales as qk_quantize_q8_0 of the binary32 products, which are stored only when `out`
+// is given. Grid and columns as glu_q8_1_kernel.
+template <bool BF16>
+__device__ __forceinline__ void load4_elem(const void *p, int64_t i, float v[4]) {
+    if (BF16) {
+        const uint16_t *q = static_cast<const uint16_t *>(p) + i;
+        if ((reinterpret_cast<uintptr_t>(q) & 7u) == 0) {
+            const uint2 w = __ldg(reinterpret_cast<const uint2 *>(q));
+            v[0] = __uint_as_float(w.x << 16);
+            v[1] = __uint_as_float(w.x & 0xffff0000u);
+            v[2] = __uint_as_float(w.y << 16);
+            v[3] = __uint_as_float(w.y & 0xffff0000u);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; j++) v[j] = __uint_as_float((uint32_t)__ldg(q + j) << 16);
+        }
+    } else {
+        load4(static_cast<const float *>(p) + i, 4, v);
+    }
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(256) glu_q8_0_kernel(
+    int kind, int layout, const void *__restrict__ a, int64_t a_stride, const void *__restrict__ b, int64_t b_stride,
+    int N, float *__restrict__ out, int64_t out_stride, int8_t *__restrict__ qs, uint16_t *__restrict__ dh,
+    int64_t row_blocks, int T, float alpha, float limit, const int32_t *live) {
+    pdl_trigger();
+    pdl_wait();
+    const int64_t t = blockIdx.x;
+    const int tid = threadIdx.x, j8 = tid & 7;
+    const int c = blockIdx.y * 1024 + 4 * tid;
+    const bool ok = c < N;
+    float gv[4] = {0.f, 0.f, 0.f, 0.f}, uv[4] = {0.f, 0.f, 0.f, 0.f};
+    if (ok) {
+        const int64_t first = t * a_stride + c;
+        load4_elem<BF16>(a, layout == QK_GLU_PACKED_SWAPPED ? first + N : first, gv);
+        if (layout == QK_GLU_SEPARATE)
+            load4_elem<BF16>(b, t * b_stride + c, uv);
+        else
+            load4_elem<BF16>(a, layout == QK_GLU_PACKED ? first + N : first, uv);
+    }
+    if (t >= live_rows(live, T)) return;
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    if (ok) {
+#pragma unroll
+        for (int i = 0; i < 4; i++) v[i] = glu_out(kind, gv[i], uv[i], alpha, limit);
+        if (out) store4(out + t * out_stride + c, v);
+    }
+    uint32_t codes;
+    int sum;
+    const float d = kind == QK_GLU_REGLU ? q8_block<true>(v, &codes, &sum) : q8_block(v, &codes, &sum);
+    if (ok) {
+        const int64_t blk = t * row_blocks + c / QB;
+        reinterpret_cast<uint32_t *>(qs + blk * QB)[j8] = codes;
+        if (j8 == 0) dh[blk] = __half_as_ushort(__float2half_rn(d));
+    }
+    if (blockIdx.y == 0) {  // zero blocks of the row padding
+        for (int64_t bb = N / QB + tid; bb < row_blocks; bb += 256) {
+            uint32_t *p = reinterpret_cast<uint32_t *>(qs + (t * row_blocks + bb) * QB);
+#pragma unroll
+            for (int i = 0; i < 8; i++) p[i] = 0u;
+            dh[t * row_blocks + bb] = 0;
+        }
+    }
+}
+
 constexpr int64_t QUANT_BIG_BLOCKS = 1 << 17;   // blocks per call from which QPB = 4 is used
 
 }  // namespace
@@ -420,6 +487,16 @@ qk_status launch_glu_q8_1(int kind, int layout, const float *a, int64_t a_stride
     dim3 grid((unsigned)T, (unsigned)ceil_div(N, 1024));
     return launch_pdl("glu_q8_1", glu_q8_1_kernel, grid, dim3(256), 0, s, kind, layout, a, a_stride, b, b_stride,
                       N, out, out_stride, img, row_blocks, T, alpha, limit, live);
+}
+
+qk_status launch_glu_q8_0(int kind, int layout, int elem, const void *a, int64_t a_stride, const void *b,
+                          int64_t b_stride, int T, int N, float *out, int64_t out_stride, int8_t *qs, uint16_t *d,
+                          int64_t row_blocks, float alpha, float limit, const int32_t *live, cudaStream_t s) {
+    if (T == 0) return QK_OK;
+    dim3 grid((unsigned)T, (unsigned)ceil_div(N, 1024));
+    return launch_pdl("glu_q8_0", elem == QK_ELEM_BF16 ? glu_q8_0_kernel<true> : glu_q8_0_kernel<false>, grid,
+                      dim3(256), 0, s, kind, layout, a, a_stride, b, b_stride, N, out, out_stride, qs, d, row_blocks,
+                      T, alpha, limit, live);
 }
 
 }  // namespace qk

@@ -243,6 +243,29 @@ __global__ void __launch_bounds__(256) combine_kernel(const float *__restrict__ 
     *reinterpret_cast<float4 *>(y + (int64_t)r * y_stride + c) = acc;
 }
 
+// The same sum over bfloat16 expert outputs: four columns per 8-byte load.
+__global__ void __launch_bounds__(256) combine_bf16_kernel(const uint16_t *__restrict__ eo, int64_t eo_stride,
+                                                           const float *__restrict__ wts, int rows, int k, int N,
+                                                           float *__restrict__ y, int64_t y_stride,
+                                                           const int32_t *live) {
+    pdl_trigger();
+    pdl_wait();
+    const int r = blockIdx.x;
+    if (r >= live_rows(live, rows)) return;
+    const int c = (blockIdx.y * 256 + threadIdx.x) * 4;
+    if (c >= N) return;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s = 0; s < k; s++) {
+        const float w = wts[(int64_t)r * k + s];
+        const uint2 e = *reinterpret_cast<const uint2 *>(eo + ((int64_t)r * k + s) * eo_stride + c);
+        acc.x = fmaf(w, __uint_as_float(e.x << 16), acc.x);
+        acc.y = fmaf(w, __uint_as_float(e.x & 0xffff0000u), acc.y);
+        acc.z = fmaf(w, __uint_as_float(e.y << 16), acc.z);
+        acc.w = fmaf(w, __uint_as_float(e.y & 0xffff0000u), acc.w);
+    }
+    *reinterpret_cast<float4 *>(y + (int64_t)r * y_stride + c) = acc;
+}
+
 }  // namespace
 
 qk_status launch_topk_route(const float *logits, int rows, int E, int k, int32_t *ids, float *wts,
@@ -286,4 +309,10 @@ qk_status launch_moe_combine(const float *expert_out, int64_t out_stride, const 
     return launch_pdl("moe_combine", combine_kernel, grid, dim3(256), 0, s, expert_out, out_stride, wts, rows, k, N,
                       y, y_stride, live);
 }
+qk_status launch_moe_combine_bf16(const uint16_t *expert_out, int64_t out_stride, const float *wts, int rows, int k,
+                                  int N, float *y, int64_t y_stride, const int32_t *live, cudaStream_t s) {
+    return launch_pdl("moe_combine_bf16", combine_bf16_kernel, dim3((unsigned)rows, (unsigned)ceil_div(N, 1024)),
+                      dim3(256), 0, s, expert_out, out_stride, wts, rows, k, N, y, y_stride, live);
+}
+
 }  // namespace qk

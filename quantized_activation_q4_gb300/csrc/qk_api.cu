@@ -44,14 +44,17 @@ using namespace qk;
         if (!(cond)) return fail(status, __VA_ARGS__); \
     } while (0)
 
+constexpr int QK_W_LAST = QK_W_Q4_G128;
+
 static bool aligned(const void *p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 static qk_status check_proj_common(int32_t wtype, const void *w, int64_t N, int64_t K, int64_t img_row_blocks) {
-    REQUIRE(wtype == QK_W_Q4_0 || wtype == QK_W_Q8_0, QK_ERR_ARG, "bad wtype %d", (int)wtype);
+    REQUIRE(wtype >= QK_W_Q4_0 && wtype <= QK_W_LAST, QK_ERR_ARG, "bad wtype %d", (int)wtype);
     REQUIRE(w, QK_ERR_ARG, "null weight pointer");
     REQUIRE(aligned(w, 16), QK_ERR_ARG, "packed weights must be 16-byte aligned");
     REQUIRE(N >= 1 && N <= INT32_MAX && K >= 32 && K <= INT32_MAX, QK_ERR_ARG, "N or K out of range");
-    REQUIRE(K % QB == 0, QK_ERR_SHAPE, "K=%lld is not a multiple of 32", (long long)K);
+    REQUIRE(K % group_size(wtype) == 0, QK_ERR_SHAPE, "K=%lld is not a multiple of %d", (long long)K,
+            group_size(wtype));
     REQUIRE(K / QB <= img_row_blocks, QK_ERR_SHAPE, "K=%lld reaches past the image row (%lld blocks)",
             (long long)K, (long long)img_row_blocks);
     return QK_OK;
@@ -299,23 +302,61 @@ qk_status qk_glu_q8_1_ex(qk_glu_kind kind, qk_glu_layout layout, const float *a,
                            (cudaStream_t)stream);
 }
 
+qk_status qk_glu_q8_0(qk_glu_kind kind, qk_glu_layout layout, qk_elem elem, const void *a, int64_t a_stride,
+                      const void *b, int64_t b_stride, int64_t T, int64_t N, float *out, int64_t out_stride,
+                      int8_t *qs, uint16_t *d, int64_t row_blocks, float alpha, float limit,
+                      const int32_t *d_live_rows, qk_stream stream) {
+    REQUIRE(kind >= QK_GLU_SWIGLU && kind <= QK_GLU_SWIGLU_CLAMP, QK_ERR_ARG, "bad glu kind %d", (int)kind);
+    REQUIRE(std::isfinite(alpha) && std::isfinite(limit) && limit > 0.0f, QK_ERR_ARG,
+            "alpha must be finite and limit positive and finite");
+    REQUIRE(layout >= QK_GLU_SEPARATE && layout <= QK_GLU_PACKED_SWAPPED, QK_ERR_ARG, "bad glu layout %d", (int)layout);
+    REQUIRE(elem == QK_ELEM_F32 || elem == QK_ELEM_BF16, QK_ERR_ARG, "bad element type %d", (int)elem);
+    REQUIRE(T >= 0 && T <= INT32_MAX && N >= 1 && N <= (1LL << 25), QK_ERR_ARG, "T or N out of range");
+    REQUIRE(N % QB == 0, QK_ERR_SHAPE, "N=%lld is not a whole number of 32-blocks", (long long)N);
+    const bool separate = layout == QK_GLU_SEPARATE;
+    REQUIRE((a && qs && d && (!separate || b)) || T == 0, QK_ERR_ARG, "null pointer");
+    const int64_t es = elem == QK_ELEM_F32 ? 4 : 2, a_row = separate ? N : 2 * N;
+    REQUIRE(a_stride >= a_row, QK_ERR_SHAPE, "a_stride too small");
+    REQUIRE(!separate || b_stride >= N, QK_ERR_SHAPE, "b_stride < N");
+    REQUIRE((!out || out_stride >= N) && row_blocks >= N / QB, QK_ERR_SHAPE, "out_stride or row_blocks too small");
+    REQUIRE(row_blocks <= (1 << 20), QK_ERR_ARG, "row_blocks > 2^20");
+    REQUIRE(aligned(a, es) && (!separate || aligned(b, es)) && aligned(out, 4) && aligned(qs, 4) && aligned(d, 2),
+            QK_ERR_ARG, "misaligned pointer");
+    Span sa = span(a, rows_span(T, a_stride * es, a_row * es));
+    Span sb = span(separate ? b : nullptr, separate ? rows_span(T, b_stride * es, N * es) : 0);
+    Span so = span(out, out ? rows_span(T, out_stride * 4, N * 4) : 0);
+    Span sq = span(qs, (size_t)(T * row_blocks * QB)), sd = span(d, (size_t)(T * row_blocks * 2));
+    const Span outs[3] = {so, sq, sd};
+    for (int o = 0; o < 3; o++) {
+        REQUIRE(!overlap(outs[o], sa) && !overlap(outs[o], sb), QK_ERR_ALIAS, "an output overlaps an input");
+        for (int q = 0; q < o; q++) REQUIRE(!overlap(outs[o], outs[q]), QK_ERR_ALIAS, "outputs overlap each other");
+    }
+    return launch_glu_q8_0((int)kind, (int)layout, (int)elem, a, a_stride, b, b_stride, (int)T, (int)N, out, out_stride,
+                           qs, d, row_blocks, alpha, limit, d_live_rows, (cudaStream_t)stream);
+}
+
 // ------------------------------------------------------------------ weights
 size_t qk_weight_packed_bytes(qk_wtype wtype, int64_t N, int64_t K) {
-    if ((wtype != QK_W_Q4_0 && wtype != QK_W_Q8_0) || N < 0 || K < 0) return 0;
+    if (wtype < QK_W_Q4_0 || (int)wtype > QK_W_LAST || N < 0 || K < 0) return 0;
     return (size_t)packed_bytes(wtype, N, K);
 }
 
 qk_status qk_weight_pack(qk_wtype wtype, const void *blocks, int64_t N, int64_t K, void *packed,
                          size_t packed_bytes_, qk_stream stream) {
-    REQUIRE(wtype == QK_W_Q4_0 || wtype == QK_W_Q8_0, QK_ERR_ARG, "bad wtype %d", (int)wtype);
+    REQUIRE(wtype >= QK_W_Q4_0 && (int)wtype <= QK_W_LAST, QK_ERR_ARG, "bad wtype %d", (int)wtype);
     REQUIRE(N >= 1 && K >= 32 && N <= INT32_MAX && K <= INT32_MAX, QK_ERR_ARG, "N or K out of range");
-    REQUIRE(K % QB == 0, QK_ERR_SHAPE, "K=%lld is not a multiple of 32", (long long)K);
+    const int G = group_size(wtype);
+    REQUIRE(K % G == 0, QK_ERR_SHAPE, "K=%lld is not a multiple of %d", (long long)K, G);
     REQUIRE(blocks && packed, QK_ERR_ARG, "null pointer");
     REQUIRE(aligned(packed, 16), QK_ERR_ARG, "packed must be 16-byte aligned");
     const size_t need = (size_t)packed_bytes(wtype, N, K);
     REQUIRE(packed_bytes_ >= need, QK_ERR_WORKSPACE, "packed_bytes=%zu < %zu", packed_bytes_, need);
-    const size_t src = (size_t)(N * (K / QB) * (wtype == QK_W_Q4_0 ? Q4_0_BYTES : Q8_0_BYTES));
+    const int64_t block = wtype == QK_W_Q4_0 ? Q4_0_BYTES : wtype == QK_W_Q8_0 ? Q8_0_BYTES : 4 + G / 2;
+    const size_t src = (size_t)(N * (K / G) * block);
     REQUIRE(!overlap(span(blocks, src), span(packed, need)), QK_ERR_ALIAS, "packed overlaps blocks");
+    if (group_scaled(wtype))
+        return launch_weight_pack_g(wtype, static_cast<const uint8_t *>(blocks), N, K,
+                                    static_cast<uint8_t *>(packed), (cudaStream_t)stream);
     return launch_weight_pack(wtype, static_cast<const uint8_t *>(blocks), N, K, static_cast<uint8_t *>(packed),
                               (cudaStream_t)stream);
 }
@@ -353,7 +394,9 @@ qk_status qk_mmvq(const void *img, int64_t img_row_blocks, int64_t T, int32_t n_
     qk_status vs = mmvq_validate(img, img_row_blocks, T, n_proj, projs);
     if (vs != QK_OK) return vs;
     Span si = span(img, (size_t)(T * img_row_blocks * Q8_1_BYTES));
-    REQUIRE(ws && aligned(ws, 16), QK_ERR_WORKSPACE, "workspace null or not 16-byte aligned");
+    bool need_ws = false;
+    for (int j = 0; j < n_proj; j++) need_ws |= !group_scaled(projs[j].wtype);
+    REQUIRE(!need_ws || (ws && aligned(ws, 16)), QK_ERR_WORKSPACE, "workspace null or not 16-byte aligned");
     // one launch per weight type present, in order on the stream; they share ws
     for (int wt = QK_W_Q4_0; wt <= QK_W_Q8_0; wt++) {
         qk_proj group[8];
@@ -378,6 +421,16 @@ qk_status qk_mmvq(const void *img, int64_t img_row_blocks, int64_t T, int32_t n_
         if (n == 0) continue;
         qk_status st = launch_mmvq(static_cast<const uint8_t *>(img), img_row_blocks, (int)T, n, group,
                                    d_live_rows, ws, ws_bytes, (cudaStream_t)stream);
+        if (st != QK_OK) return st;
+    }
+    for (int wt = QK_W_Q4_G64; wt <= QK_W_Q4_G128; wt++) {
+        qk_proj group[8];
+        int n = 0;
+        for (int j = 0; j < n_proj; j++)
+            if (projs[j].wtype == wt) group[n++] = projs[j];
+        if (n == 0) continue;
+        qk_status st = launch_mmvq_g(static_cast<const uint8_t *>(img), img_row_blocks, (int)T, n, group, d_live_rows,
+                                     (cudaStream_t)stream);
         if (st != QK_OK) return st;
     }
     return QK_OK;
@@ -417,14 +470,15 @@ static qk_status mmvq_id_common(const void *img, int64_t img_row_blocks, int64_t
     for (int j = 0; j < n_proj; j++) tiles += ceil_div(projs[j].N, UNIT_ROWS);
     REQUIRE(((rows * k + 7) / 8 + E) * tiles < (1LL << 31), QK_ERR_UNSUPPORTED,
             "rows * k * row tiles too large for one routed launch");
-    for (int wt = QK_W_Q4_0; wt <= QK_W_Q8_0; wt++) {
+    for (int wt = QK_W_Q4_0; wt <= QK_W_LAST; wt++) {
         qk_proj_id group[8];
         int n = 0;
         for (int j = 0; j < n_proj; j++)
             if (projs[j].wtype == wt) group[n++] = projs[j];
         if (n == 0) continue;
-        qk_status st = launch_mmvq_id(static_cast<const uint8_t *>(img), img_row_blocks, (int)rows, k, n, group,
-                                      counts, offsets, items, per_pair, (cudaStream_t)stream);
+        qk_status st = (group_scaled(wt) ? launch_mmvq_g_id : launch_mmvq_id)(
+            static_cast<const uint8_t *>(img), img_row_blocks, (int)rows, k, n, group, counts, offsets, items, per_pair,
+            (cudaStream_t)stream);
         if (st != QK_OK) return st;
     }
     return QK_OK;
@@ -457,6 +511,25 @@ qk_status qk_moe_combine(const float *expert_out, int64_t out_stride, const floa
     if (rows == 0) return QK_OK;
     return launch_moe_combine(expert_out, out_stride, wts, (int)rows, k, (int)N, y, y_stride, d_live_rows,
                               (cudaStream_t)stream);
+}
+
+qk_status qk_moe_combine_bf16(const uint16_t *expert_out, int64_t out_stride, const float *wts, int64_t rows,
+                              int32_t k, int64_t N, float *y, int64_t y_stride, const int32_t *d_live_rows,
+                              qk_stream stream) {
+    REQUIRE(expert_out && wts && y, QK_ERR_ARG, "null pointer");
+    REQUIRE(rows >= 0 && rows <= (1 << 24) && k >= 1 && k <= 64 && N >= 1 && N <= (1LL << 25), QK_ERR_ARG,
+            "rows, k or N out of range");
+    REQUIRE(out_stride >= N && y_stride >= N, QK_ERR_SHAPE, "out_stride or y_stride < N");
+    REQUIRE(aligned(expert_out, 8) && aligned(wts, 4) && aligned(y, 16) && out_stride % 4 == 0 && y_stride % 4 == 0 &&
+                N % 4 == 0,
+            QK_ERR_ARG, "expert_out must be 8-byte and y 16-byte aligned with strides and N multiples of 4");
+    Span se = span(expert_out, rows_span(rows * k, out_stride * 2, N * 2));
+    Span sw = span(wts, (size_t)(rows * k * 4));
+    Span sy = span(y, rows_span(rows, y_stride * 4, N * 4));
+    REQUIRE(!overlap(sy, se) && !overlap(sy, sw), QK_ERR_ALIAS, "y overlaps expert_out or wts");
+    if (rows == 0) return QK_OK;
+    return launch_moe_combine_bf16(expert_out, out_stride, wts, (int)rows, k, (int)N, y, y_stride, d_live_rows,
+                                   (cudaStream_t)stream);
 }
 
 // ------------------------------------------------------------------ routing
@@ -545,6 +618,76 @@ qk_status qk_mmq(const int8_t *qs, const uint16_t *d, int64_t row_blocks, int64_
                     !overlap(sws, span(projs[j].w, (size_t)packed_bytes(projs[j].wtype, projs[j].N, projs[j].K))),
                 QK_ERR_ALIAS, "workspace overlaps projection %d", j);
     return launch_mmq(qs, d, row_blocks, (int)T, n_proj, projs, ws, ws_bytes, (cudaStream_t)stream);
+}
+
+// ------------------------------------------------------------------ routed prefill
+size_t qk_mmq_id_workspace_bytes(int64_t img_rows, int32_t n_proj, const qk_proj_id16 *projs) {
+    if (img_rows < 1 || n_proj < 1 || n_proj > 8 || !projs) return 0;
+    int64_t kmax = 0;
+    for (int j = 0; j < n_proj; j++) kmax = projs[j].K > kmax ? projs[j].K : kmax;
+    return (size_t)mmq_id_workspace_bytes(img_rows, kmax);
+}
+
+static qk_status mmq_id_common(const int8_t *qs, const uint16_t *d, int64_t row_blocks, int64_t rows, int32_t k,
+                               int32_t n_proj, const qk_proj_id16 *projs, const int32_t *counts,
+                               const int32_t *offsets, const int32_t *items, void *ws, size_t ws_bytes, bool per_pair,
+                               qk_stream stream) {
+    REQUIRE(qs && d && projs && counts && offsets && items, QK_ERR_ARG, "null pointer");
+    REQUIRE(rows >= 1 && rows <= (1 << 24) && k >= 1 && k <= 64 && row_blocks >= 1, QK_ERR_ARG,
+            "rows, k or row_blocks out of range");
+    REQUIRE(n_proj >= 1 && n_proj <= 8, QK_ERR_UNSUPPORTED, "n_proj=%d not in 1..8", (int)n_proj);
+    REQUIRE(aligned(qs, 16) && aligned(d, 4), QK_ERR_ARG, "qs must be 16-byte and d 4-byte aligned");
+    REQUIRE(aligned(counts, 4) && aligned(offsets, 4) && aligned(items, 4), QK_ERR_ARG, "misaligned plan pointer");
+    const int64_t pairs = rows * k, img_rows = per_pair ? pairs : rows;
+    const int64_t E = projs[0].n_experts;
+    REQUIRE(E >= 1 && E <= 1024, QK_ERR_UNSUPPORTED, "n_experts=%lld", (long long)E);
+    const Span sq = span(qs, (size_t)(img_rows * row_blocks * QB)), sd = span(d, (size_t)(img_rows * row_blocks * 2));
+    const Span ins[5] = {sq, sd, span(counts, (size_t)E * 4), span(offsets, (size_t)(E + 1) * 4),
+                         span(items, (size_t)(pairs * 4))};
+    int64_t tiles = 0;
+    for (int j = 0; j < n_proj; j++) {
+        const qk_proj_id16 &p = projs[j];
+        qk_status st = check_proj_common(p.wtype, p.w, p.N, p.K, row_blocks);
+        if (st != QK_OK) return st;
+        REQUIRE(p.wtype != QK_W_Q8_0, QK_ERR_UNSUPPORTED, "projection %d: Q8_0 weights are not taken", j);
+        REQUIRE(p.n_experts == E, QK_ERR_ARG, "projections disagree on n_experts");
+        REQUIRE(p.y && aligned(p.y, 2), QK_ERR_ARG, "projection %d: y is null or misaligned", j);
+        REQUIRE(p.y_stride >= p.N, QK_ERR_SHAPE, "projection %d: y_stride < N", j);
+        const Span sy = span(p.y, rows_span(pairs, p.y_stride * 2, p.N * 2));
+        REQUIRE(!overlap(sy, span(p.w, (size_t)(packed_bytes(p.wtype, p.N, p.K) * E))), QK_ERR_ALIAS,
+                "projection %d: y overlaps its weights", j);
+        for (int i = 0; i < 5; i++)
+            REQUIRE(!overlap(sy, ins[i]), QK_ERR_ALIAS, "projection %d: y overlaps the image or the plan", j);
+        for (int i = 0; i < j; i++)
+            REQUIRE(!rows_overlap(projs[i].y, projs[i].y_stride * 2, projs[i].N * 2, p.y, p.y_stride * 2, p.N * 2, pairs),
+                    QK_ERR_ALIAS, "outputs of projections %d and %d overlap", i, j);
+        tiles += ceil_div(p.N, UNIT_ROWS);
+    }
+    // work items (passes of any plan x row tiles) are counted in int
+    REQUIRE((pairs / 16 + E) * tiles < (1LL << 31), QK_ERR_UNSUPPORTED, "rows * k * row tiles too large for one launch");
+    const size_t need = qk_mmq_id_workspace_bytes(img_rows, n_proj, projs);
+    REQUIRE(ws && aligned(ws, 128), QK_ERR_WORKSPACE, "workspace null or not 128-byte aligned");
+    REQUIRE(ws_bytes >= need, QK_ERR_WORKSPACE, "workspace %zu < %zu bytes", ws_bytes, need);
+    const Span sws = span(ws, need);
+    for (int i = 0; i < 5; i++) REQUIRE(!overlap(sws, ins[i]), QK_ERR_ALIAS, "workspace overlaps the image or the plan");
+    for (int j = 0; j < n_proj; j++)
+        REQUIRE(!overlap(sws, span(projs[j].y, rows_span(pairs, projs[j].y_stride * 2, projs[j].N * 2))) &&
+                    !overlap(sws, span(projs[j].w, (size_t)(packed_bytes(projs[j].wtype, projs[j].N, projs[j].K) * E))),
+                QK_ERR_ALIAS, "workspace overlaps projection %d", j);
+    return launch_mmq_id(qs, d, row_blocks, img_rows, (int)rows, k, n_proj, projs, counts, offsets, items, per_pair, ws,
+                         (cudaStream_t)stream);
+}
+
+qk_status qk_mmq_id(const int8_t *qs, const uint16_t *d, int64_t row_blocks, int64_t rows, int32_t k, int32_t n_proj,
+                    const qk_proj_id16 *projs, const int32_t *counts, const int32_t *offsets, const int32_t *items,
+                    void *ws, size_t ws_bytes, qk_stream stream) {
+    return mmq_id_common(qs, d, row_blocks, rows, k, n_proj, projs, counts, offsets, items, ws, ws_bytes, false, stream);
+}
+
+qk_status qk_mmq_id_slots(const int8_t *qs, const uint16_t *d, int64_t row_blocks, int64_t rows, int32_t k,
+                          int32_t n_proj, const qk_proj_id16 *projs, const int32_t *counts, const int32_t *offsets,
+                          const int32_t *items, void *ws, size_t ws_bytes, qk_stream stream) {
+    return mmq_id_common(qs, d, row_blocks, rows, k, n_proj, projs, counts, offsets, items, ws, ws_bytes, true, stream);
 }
 
 }  // extern "C"

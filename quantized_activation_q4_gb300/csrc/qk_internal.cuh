@@ -85,7 +85,23 @@ constexpr int Q8_BLOCK_STRIDE = 4096;
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 inline int64_t unit_bytes(int wtype) { return wtype == QK_W_Q4_0 ? Q4_UNIT_BYTES : Q8_UNIT_BYTES; }
+
+// Packed group-scaled weights: units of 32 rows (a strip) x 128 columns, ordered (strip, column
+// chunk), so that one warp streams a strip with 512-byte loads and a span of chunks is contiguous.
+//   Block jb (32 columns) at jb*512; lane l = 4g + t holds 16 B = word t of rows g, g+8, 16+g,
+//   24+g (word t of a 16-byte run = bytes 4t..4t+3: elements 4t..4t+3 in the low nibbles, 16+4t..
+//   in the high ones).
+//   Group headers at 2048 + 128*group + 16*g + 4*i, row g + 8i: half d | half(z - 8) << 16.
+// Rows past N and columns past K have d = 0 and zero nibbles.
+constexpr int STRIP_ROWS = 32;
+constexpr int STRIP_DATA = 2048;
+inline bool group_scaled(int wtype) { return wtype == QK_W_Q4_G64 || wtype == QK_W_Q4_G128; }
+inline int group_size(int wtype) { return wtype == QK_W_Q4_G64 ? 64 : wtype == QK_W_Q4_G128 ? 128 : QB; }
+__host__ __device__ constexpr int strip_unit_bytes(int G) { return STRIP_DATA + 128 * (UNIT_COLS / G); }
+
 inline int64_t packed_bytes(int wtype, int64_t N, int64_t K) {
+    if (group_scaled(wtype))
+        return ceil_div(N, STRIP_ROWS) * ceil_div(K, UNIT_COLS) * strip_unit_bytes(group_size(wtype));
     return ceil_div(N, UNIT_ROWS) * ceil_div(K, UNIT_COLS) * unit_bytes(wtype);
 }
 
@@ -151,6 +167,23 @@ qk_status launch_mmvq_id(const uint8_t *img, int64_t row_blocks, int rows, int k
                          const int32_t *items, bool per_pair, cudaStream_t s);
 qk_status launch_moe_combine(const float *expert_out, int64_t out_stride, const float *wts, int rows, int k, int N,
                              float *y, int64_t y_stride, const int32_t *live, cudaStream_t s);
+qk_status launch_moe_combine_bf16(const uint16_t *expert_out, int64_t out_stride, const float *wts, int rows, int k,
+                                  int N, float *y, int64_t y_stride, const int32_t *live, cudaStream_t s);
+qk_status launch_glu_q8_0(int kind, int layout, int elem, const void *a, int64_t a_stride, const void *b,
+                          int64_t b_stride, int T, int N, float *out, int64_t out_stride, int8_t *qs, uint16_t *d,
+                          int64_t row_blocks, float alpha, float limit, const int32_t *live, cudaStream_t s);
+// Group-scaled weights (projections of one wtype per call).
+qk_status launch_weight_pack_g(int wtype, const uint8_t *blocks, int64_t N, int64_t K, uint8_t *packed,
+                               cudaStream_t s);
+qk_status launch_mmvq_g(const uint8_t *img, int64_t row_blocks, int T, int n_proj, const qk_proj *projs,
+                        const int32_t *live, cudaStream_t s);
+qk_status launch_mmvq_g_id(const uint8_t *img, int64_t row_blocks, int rows, int k, int n_proj,
+                           const qk_proj_id *projs, const int32_t *counts, const int32_t *offsets,
+                           const int32_t *items, bool per_pair, cudaStream_t s);
+qk_status launch_mmq_id(const int8_t *qs, const uint16_t *d, int64_t row_blocks, int64_t img_rows, int rows, int k,
+                        int n_proj, const qk_proj_id16 *projs, const int32_t *counts, const int32_t *offsets,
+                        const int32_t *items, bool per_pair, void *ws, cudaStream_t s);
+int64_t mmq_id_workspace_bytes(int64_t img_rows, int64_t kmax);
 qk_status launch_topk_route(const float *logits, int rows, int E, int k, int32_t *ids,
                             float *wts, const int32_t *live, cudaStream_t s);
 qk_status launch_moe_plan(const int32_t *ids, int rows, int k, int E, int32_t *counts,

@@ -60,6 +60,20 @@ def q4_0_weight(seed: int, N: int, K: int) -> np.ndarray:
     return out
 
 
+def q4_group_weight(seed: int, N: int, K: int, G: int) -> np.ndarray:
+    """Canonical group-scaled blocks (G = 64 or 128), uint8 array of shape [N, K/G, 4 + G/2].
+
+    Block bytes: [half d][zero point 0..15][a byte nothing reads][nibbles]. Nibbles and zero points
+    are uniform on 0..15, the upper bits of the zero point's byte and the unread byte are noise; d is
+    U[0.002, 0.02] rounded to half.
+    """
+    assert G in (64, 128) and K % G == 0
+    g = rng(seed)
+    out = g.integers(0, 256, size=(N, K // G, 4 + G // 2), dtype=np.uint8)
+    out[:, :, 0:2] = half_scales(g, (N, K // G)).view(np.uint8).reshape(N, K // G, 2)
+    return out
+
+
 def q8_0_weight(seed: int, N: int, K: int) -> np.ndarray:
     """Canonical Q8_0 blocks, uint8 array of shape [N, K/32, 34]: [half d][32 int8]."""
     assert K % 32 == 0
