@@ -41,10 +41,8 @@
 // store a packed weight word (column 2t+p: elements 4t+p and 4t+p+2; column
 // 8+2t+p: elements 16+4t+p and 18+4t+p); dequant_b writes B in the same order.
 
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
 #include "qk_internal.cuh"
+#include "qk_tc.cuh"
 
 namespace qk {
 namespace {
@@ -66,8 +64,6 @@ constexpr int THREADS = (EPI0 + N_EPI) * 32;
 constexpr uint32_t A_TMEM = TN;           // A stages follow the accumulator
 constexpr uint32_t TMEM_COLS = 512;
 static_assert(A_TMEM + NS * A_COLS <= TMEM_COLS, "tensor memory");
-constexpr uint32_t SPIN_LIMIT = 1u << 16;
-constexpr uint32_t SUSPEND_NS = 20000;
 
 // shared memory: [B tiles][units][barriers][tensor-memory address]
 constexpr int OFF_B = 0;
@@ -77,11 +73,6 @@ constexpr int OFF_BAR = OFF_U + NU * Q4_UNIT_BYTES;
 constexpr int N_BARS = 3 * NS + 2 * NU + 3;
 constexpr int SMEM_BYTES = OFF_BAR + N_BARS * 8 + 16 + 1024;   // + slack to align the base to 1024
 static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
-
-// instruction descriptor: f32 accumulator, f16 A and B, both K-major, N = 256, M = 128
-constexpr uint32_t IDESC = (1u << 4) | ((uint32_t)(TN >> 3) << 17) | ((uint32_t)(TM >> 4) << 24);
-
-__device__ unsigned int g_mmq_faults = 0;
 
 struct MmqProj {
     const uint8_t *w;
@@ -107,85 +98,6 @@ __device__ __forceinline__ Tile tile_of(const MmqArgs &a, int tau) {
     t.rt = r - a.p[j].rt_begin;
     t.nkc = (a.p[j].K + SK - 1) / SK;   // stages = packed units
     return t;
-}
-
-// ------------------------------------------------------------------ PTX helpers
-__device__ __forceinline__ uint32_t smem_u32(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
-__device__ __forceinline__ void mbar_init(uint32_t a, uint32_t n) {
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(a), "r"(n) : "memory");
-}
-__device__ __forceinline__ void mbar_arrive(uint32_t a) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(a) : "memory");
-}
-__device__ __forceinline__ void mbar_expect_tx(uint32_t a, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(a), "r"(bytes) : "memory");
-}
-// Bounded wait: suspends until the phase completes (or SUSPEND_NS), gives up
-// after SPIN_LIMIT tries (about a second at most), records a fault and
-// returns false.
-__device__ __forceinline__ bool mbar_wait(uint32_t a, uint32_t parity) {
-    for (uint32_t i = 0; i < SPIN_LIMIT; i++) {
-        uint32_t ok;
-        asm volatile(
-            "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
-            : "=r"(ok)
-            : "r"(a), "r"(parity), "r"(SUSPEND_NS)
-            : "memory");
-        if (ok) return true;
-    }
-    atomicOr(&g_mmq_faults, 1u);
-    return false;
-}
-__device__ __forceinline__ void bulk_g2s(uint32_t dst, const void *src, uint32_t bytes, uint32_t mbar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-                 ::"r"(dst), "l"(src), "r"(bytes), "r"(mbar)
-                 : "memory");
-}
-__device__ __forceinline__ void prefetch_l2(const void *src, uint32_t bytes) {
-    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t mbar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
-        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(mbar)
-        : "memory");
-}
-// shared-memory matrix descriptor: K-major, 128-byte swizzle, 8-row groups 1024 B apart
-__device__ __forceinline__ uint64_t sdesc(uint32_t addr) {
-    return (uint64_t)((addr & 0x3FFFFu) >> 4) | (1ull << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) |
-           (2ull << 61);
-}
-// D (tensor memory) (+)= A (tensor memory) x B (shared memory)
-__device__ __forceinline__ void tc_mma(uint32_t tmem, uint32_t a_tmem, uint64_t b, uint32_t accumulate) {
-    asm volatile(
-        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(tmem),
-        "r"(a_tmem), "l"(b), "r"(IDESC), "r"(accumulate)
-        : "memory");
-}
-__device__ __forceinline__ void tc_commit(uint32_t mbar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(mbar)
-                 : "memory");
-}
-__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-
-// Four weight bytes (word t of one row of a Q4_0 block) -> 16 bytes of f16
-// A values (nibble - 8) * dw, K order: e(4t), e(4t+2), e(4t+1), e(4t+3),
-// e(16+4t), e(16+4t+2), e(16+4t+1), e(16+4t+3). The nibble becomes an exact
-// half by OR-ing it under an exponent (1024 + lo, 64 + hi); subtracting
-// 1032 / 72 leaves the exact nibble - 8; one rounding in the multiply by dw.
-__device__ __forceinline__ uint32_t a_pair(uint32_t v, __half2 bias, __half2 dw) {
-    const __half2 r = __hmul2(__hsub2(*reinterpret_cast<const __half2 *>(&v), bias), dw);
-    return *reinterpret_cast<const uint32_t *>(&r);
-}
-__device__ __forceinline__ uint4 a_word(uint32_t w, __half2 dw) {
-    const uint32_t w8 = w >> 8;
-    const __half2 blo = __halves2half2(__ushort_as_half(0x6408), __ushort_as_half(0x6408));   // 1032
-    const __half2 bhi = __halves2half2(__ushort_as_half(0x5480), __ushort_as_half(0x5480));   // 72
-    return make_uint4(a_pair((w & 0x000F000Fu) | 0x64006400u, blo, dw), a_pair((w8 & 0x000F000Fu) | 0x64006400u, blo, dw),
-                      a_pair((w & 0x00F000F0u) | 0x54005400u, bhi, dw),
-                      a_pair((w8 & 0x00F000F0u) | 0x54005400u, bhi, dw));
 }
 
 // ------------------------------------------------------------------ B = dequantised image
@@ -343,7 +255,7 @@ __global__ void __launch_bounds__(THREADS, 1) mmq_tc_kernel(const __grid_constan
                     const uint32_t at = tmem + A_TMEM + s * A_COLS, bt = sbase + OFF_B + s * B_TILE;
 #pragma unroll
                     for (int ks = 0; ks < SK / 16; ks++)   // K = 16 per MMA: 8 A columns, 32 B bytes of a box
-                        tc_mma(acc, at + 8 * ks, sdesc(bt + (ks >> 2) * B_BOX + 32 * (ks & 3)), (kc | ks) != 0);
+                        tc_mma(acc, at + 8 * ks, sdesc(bt + (ks >> 2) * B_BOX + 32 * (ks & 3)), mma_idesc(TN), (kc | ks) != 0);
                     tc_commit(empty + 8 * s);   // frees the stage once these MMAs are done
                 }
                 if (ok) tc_commit(acc_full);   // the accumulator is final once its MMAs are done
@@ -447,30 +359,24 @@ __global__ void __launch_bounds__(THREADS, 1) mmq_tc_kernel(const __grid_constan
                      : "memory");
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    if (!fn) {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    }
-    return fn;
-}
-
 }  // namespace
 
 int64_t mmq_workspace_bytes(int64_t T, int64_t kmax) { return (T * kmax * 2 + 127) / 128 * 128; }
 
 qk_status read_mmq_faults(uint32_t *faults) {
     unsigned int v = 0, zero = 0;
-    cudaError_t e = cudaMemcpyFromSymbol(&v, g_mmq_faults, sizeof v);
-    if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_mmq_faults, &zero, sizeof zero);
+    cudaError_t e = cudaMemcpyFromSymbol(&v, g_tc_faults, sizeof v);
+    if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_tc_faults, &zero, sizeof zero);
     if (e != cudaSuccess) return fail(QK_ERR_CUDA, "qk_device_faults: %s", cudaGetErrorString(e));
     *faults = v;
     return QK_OK;
+}
+
+qk_status launch_dequant_b(const char *name, const int8_t *qs, const uint16_t *d, int64_t row_blocks, int T, int K,
+                           void *B, cudaStream_t s) {
+    const int kb = K / QB;
+    return launch_pdl(name, dequant_b_kernel, dim3((unsigned)T, (unsigned)ceil_div(kb, 64)), dim3(256), 0, s, qs, d,
+                      row_blocks, T, kb, static_cast<__half *>(B));
 }
 
 qk_status launch_mmq(const int8_t *qs, const uint16_t *d, int64_t row_blocks, int T, int n_proj,
@@ -505,9 +411,7 @@ qk_status launch_mmq(const int8_t *qs, const uint16_t *d, int64_t row_blocks, in
                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return fail(QK_ERR_CUDA, "mmq: tensor map encoding failed (%d)", (int)r);
 
-    const int kb = kmax / QB;
-    qk_status st = launch_pdl("mmq_dequant_b", dequant_b_kernel, dim3((unsigned)T, (unsigned)ceil_div(kb, 64)),
-                              dim3(256), 0, s, qs, d, row_blocks, T, kb, static_cast<__half *>(ws));
+    qk_status st = launch_dequant_b("mmq_dequant_b", qs, d, row_blocks, T, kmax, ws, s);
     if (st != QK_OK) return st;
     static bool configured = false;
     if (!configured) {

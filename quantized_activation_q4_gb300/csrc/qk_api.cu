@@ -380,10 +380,11 @@ size_t qk_mmvq_workspace_bytes(int32_t n_proj, const qk_proj *projs) {
 
 qk_status qk_device_faults(uint32_t *faults) {
     REQUIRE(faults, QK_ERR_ARG, "faults is null");
-    uint32_t a = 0, b = 0;
+    uint32_t a = 0, b = 0, c = 0;
     qk_status st = read_device_faults(&a);
     if (st == QK_OK) st = read_mmq_faults(&b);
-    *faults = a | b;
+    if (st == QK_OK) st = read_mmq_id_faults(&c);
+    *faults = a | b | c;
     return st;
 }
 
@@ -664,7 +665,7 @@ static qk_status mmq_id_common(const int8_t *qs, const uint16_t *d, int64_t row_
         tiles += ceil_div(p.N, UNIT_ROWS);
     }
     // work items (passes of any plan x row tiles) are counted in int
-    REQUIRE((pairs / 16 + E) * tiles < (1LL << 31), QK_ERR_UNSUPPORTED, "rows * k * row tiles too large for one launch");
+    REQUIRE((pairs / 256 + E) * tiles < (1LL << 31), QK_ERR_UNSUPPORTED, "rows * k * row tiles too large for one launch");
     const size_t need = qk_mmq_id_workspace_bytes(img_rows, n_proj, projs);
     REQUIRE(ws && aligned(ws, 128), QK_ERR_WORKSPACE, "workspace null or not 128-byte aligned");
     REQUIRE(ws_bytes >= need, QK_ERR_WORKSPACE, "workspace %zu < %zu bytes", ws_bytes, need);

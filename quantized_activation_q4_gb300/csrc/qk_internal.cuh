@@ -195,5 +195,10 @@ qk_status launch_mmq(const int8_t *qs, const uint16_t *d, int64_t row_blocks, in
                      const qk_proj *projs, void *ws, size_t ws_bytes, cudaStream_t s);
 int64_t mmq_workspace_bytes(int64_t T, int64_t kmax);
 qk_status read_mmq_faults(uint32_t *faults);
+qk_status read_mmq_id_faults(uint32_t *faults);
+// The image's first K columns as binary16 q * d_a, [T][K], in the K order of the prefill kernels'
+// A stages (see dequant_b_kernel).
+qk_status launch_dequant_b(const char *name, const int8_t *qs, const uint16_t *d, int64_t row_blocks, int T, int K,
+                           void *B, cudaStream_t s);
 
 }  // namespace qk
