@@ -612,8 +612,8 @@ typedef struct qk_proj_id16 {
  * QK_ERR_ALIAS (also an output over counts, offsets or items),
  * QK_ERR_WORKSPACE.
  */
-/* img_rows: the image's row count, rows for qk_mmq_id and rows * k for qk_mmq_id_slots. */
-QK_API size_t qk_mmq_id_workspace_bytes(int64_t img_rows, int32_t n_proj, const qk_proj_id16 *projs);
+/* The workspace of either call: every pair's activation row in binary16 (0 for arguments out of range). */
+QK_API size_t qk_mmq_id_workspace_bytes(int64_t rows, int32_t k, int32_t n_proj, const qk_proj_id16 *projs);
 QK_API qk_status qk_mmq_id(const int8_t *qs, const uint16_t *d, int64_t row_blocks, int64_t rows, int32_t k,
                            int32_t n_proj, const qk_proj_id16 *projs, const int32_t *counts, const int32_t *offsets,
                            const int32_t *items, void *ws, size_t ws_bytes, qk_stream stream);

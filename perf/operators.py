@@ -233,7 +233,7 @@ def _prepare_own(s):
         s["ws_bytes"] = qk.qk_mmvq_workspace_bytes(s["projs"])
         s["ws"] = torch.zeros((max(16, s["ws_bytes"]),), dtype=torch.uint8, device="cuda")
     elif op == "mmq_id":
-        s["ws_bytes"] = qk.qk_mmq_id_workspace_bytes(s["q"].shape[0], s["projs"])
+        s["ws_bytes"] = qk.qk_mmq_id_workspace_bytes(case["rows"], case["k"], s["projs"])
         s["ws"] = torch.empty((s["ws_bytes"],), dtype=torch.uint8, device="cuda")
 
 

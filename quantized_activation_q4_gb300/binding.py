@@ -98,7 +98,7 @@ _SIGS = {
                                     C.c_int),
     "qk_moe_combine_bf16": ([P, I64, P, I64, I32, I64, P, I64, P, P], C.c_int),
     "qk_glu_q8_0": ([C.c_int, C.c_int, C.c_int, P, I64, P, I64, I64, I64, P, I64, P, P, I64, F32, F32, P, P], C.c_int),
-    "qk_mmq_id_workspace_bytes": ([I64, I32, C.POINTER(qk_proj_id16)], SZ),
+    "qk_mmq_id_workspace_bytes": ([I64, I32, I32, C.POINTER(qk_proj_id16)], SZ),
     "qk_mmq_id": ([P, P, I64, I64, I32, I32, C.POINTER(qk_proj_id16), P, P, P, P, SZ, P], C.c_int),
     "qk_mmq_id_slots": ([P, P, I64, I64, I32, I32, C.POINTER(qk_proj_id16), P, P, P, P, SZ, P], C.c_int),
     "qk_mmq": ([P, P, I64, I64, I32, C.POINTER(qk_proj), P, C.c_size_t, P], C.c_int),
@@ -329,9 +329,9 @@ def qk_mmq(qs, d, row_blocks, T, projs, ws, ws_bytes, stream=None):
                                    _stream(stream)))
 
 
-def qk_mmq_id_workspace_bytes(img_rows, projs) -> int:
+def qk_mmq_id_workspace_bytes(rows, k, projs) -> int:
     arr = (qk_proj_id16 * len(projs))(*projs)
-    return int(load().qk_mmq_id_workspace_bytes(img_rows, len(projs), arr))
+    return int(load().qk_mmq_id_workspace_bytes(rows, k, len(projs), arr))
 
 
 def qk_mmq_id(qs, d, row_blocks, rows, k, projs, counts, offsets, items, ws, ws_bytes, stream=None):

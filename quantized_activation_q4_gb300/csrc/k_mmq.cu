@@ -101,23 +101,6 @@ __device__ __forceinline__ Tile tile_of(const MmqArgs &a, int tau) {
 }
 
 // ------------------------------------------------------------------ B = dequantised image
-// Two codes of word v (bytes k and k + 2, k = 0 or 1) -> f16 pair q * d_a. A code becomes an
-// exact half by placing its biased byte (q + 128) under the exponent of 1024 (PRMT); subtracting
-// 1152 leaves q exactly; the binary16 multiply by d_a rounds the exact product once, as the
-// binary32 product rounded to binary16 would.
-__device__ __forceinline__ uint32_t b_pair(uint32_t u, uint32_t sel, __half2 d2) {
-    uint32_t h;
-    asm("prmt.b32 %0, %1, 0x64646464, %2;" : "=r"(h) : "r"(u), "r"(sel));
-    const __half2 bias = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));   // 1152
-    const __half2 r = __hmul2(__hsub2(*reinterpret_cast<const __half2 *>(&h), bias), d2);
-    return *reinterpret_cast<const uint32_t *>(&r);
-}
-// four codes (one word, elements e .. e+3) -> halves in the order e, e+2, e+1, e+3
-__device__ __forceinline__ uint2 b_word(uint32_t v, __half2 d2) {
-    const uint32_t u = v ^ 0x80808080u;   // q + 128 in each byte
-    return make_uint2(b_pair(u, 0x4240u, d2), b_pair(u, 0x4341u, d2));
-}
-
 // grid (T, ceil(4 kb / 256)), tokens on x: thread j of CTA (t, y) takes word w = j & 3 of block
 // b = 64 y + j / 4 of token t: codes 4w .. 4w+3 and 16+4w .. 16+4w+3 -> f16 q * d_a at columns
 // 2w, 2w+1 (halves 4w .. 4w+3) and 8+2w, 9+2w (halves 16+4w ..), the K order of the A stages.
@@ -127,14 +110,7 @@ __global__ void __launch_bounds__(256) dequant_b_kernel(const int8_t *__restrict
     pdl_wait();
     const int t = blockIdx.x, w = threadIdx.x & 3, b = blockIdx.y * 64 + (threadIdx.x >> 2);
     if (b >= kb) return;
-    const int8_t *src = qs + ((int64_t)t * row_blocks + b) * QB;
-    const uint32_t lo = __ldg(reinterpret_cast<const unsigned int *>(src + 4 * w));
-    const uint32_t hi = __ldg(reinterpret_cast<const unsigned int *>(src + 16 + 4 * w));
-    const __half dah = __ushort_as_half(__ldg(d + (int64_t)t * row_blocks + b));
-    const __half2 d2 = __halves2half2(dah, dah);
-    __half *dst = B + ((int64_t)t * kb + b) * QB;
-    *reinterpret_cast<uint2 *>(dst + 4 * w) = b_word(lo, d2);
-    *reinterpret_cast<uint2 *>(dst + 16 + 4 * w) = b_word(hi, d2);
+    dequant_word(qs, d, (int64_t)t * row_blocks + b, w, B + ((int64_t)t * kb + b) * QB);
 }
 
 // ------------------------------------------------------------------ the GEMM
@@ -372,13 +348,6 @@ qk_status read_mmq_faults(uint32_t *faults) {
     return QK_OK;
 }
 
-qk_status launch_dequant_b(const char *name, const int8_t *qs, const uint16_t *d, int64_t row_blocks, int T, int K,
-                           void *B, cudaStream_t s) {
-    const int kb = K / QB;
-    return launch_pdl(name, dequant_b_kernel, dim3((unsigned)T, (unsigned)ceil_div(kb, 64)), dim3(256), 0, s, qs, d,
-                      row_blocks, T, kb, static_cast<__half *>(B));
-}
-
 qk_status launch_mmq(const int8_t *qs, const uint16_t *d, int64_t row_blocks, int T, int n_proj,
                      const qk_proj *projs, void *ws, size_t ws_bytes, cudaStream_t s) {
     MmqArgs a = {};
@@ -411,7 +380,9 @@ qk_status launch_mmq(const int8_t *qs, const uint16_t *d, int64_t row_blocks, in
                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return fail(QK_ERR_CUDA, "mmq: tensor map encoding failed (%d)", (int)r);
 
-    qk_status st = launch_dequant_b("mmq_dequant_b", qs, d, row_blocks, T, kmax, ws, s);
+    const int kb = kmax / QB;
+    qk_status st = launch_pdl("mmq_dequant_b", dequant_b_kernel, dim3((unsigned)T, (unsigned)ceil_div(kb, 64)),
+                              dim3(256), 0, s, qs, d, row_blocks, T, kb, static_cast<__half *>(ws));
     if (st != QK_OK) return st;
     static bool configured = false;
     if (!configured) {

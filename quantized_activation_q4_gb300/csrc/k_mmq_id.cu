@@ -9,8 +9,9 @@
 // accumulation over all of K in tensor memory. (Exact operands would need W and x in two halves and
 // three MMAs; the outputs are bfloat16, whose rounding is eight times the operands'.)
 //
-// Two kernels per call: dequant_b writes the image as binary16 rows (in the caller's workspace, once,
-// read by every weight row tile of every expert that a row goes to), then mmq_id_kernel.
+// Two kernels per call: dequant_pairs_kernel writes the planned pairs' image rows as binary16 in plan
+// order (in the caller's workspace), so that an expert's pairs are consecutive rows and a pass is a
+// plain tile; then mmq_id_kernel.
 //
 // Work items are (expert, 128-row weight tile, pass): a pass is up to 256 of the expert's pairs. An
 // expert with c pairs has ceil(c / 256) passes of nearly equal size, so that no pass is a small
@@ -18,12 +19,19 @@
 // the ragged counts. Items are taken round-robin, passes fastest, so that the CTAs that run at one
 // time share weight tiles through L2. Every CTA derives the item list from the counts.
 //
-//   warp 0:       TMA: the packed weights of a stage (128 rows x 128 K) by bulk copies, and the pass's
-//                 activation rows by four-row gathers (each lane holds the row numbers of its groups)
+//   warp 0:       looks the items up one ahead (descriptor and pair list into a two-entry ring) and
+//                 streams the packed weights (stages of 128 rows x 128 K) by bulk copies
 //   warp 1:       allocates tensor memory, issues the MMAs (one thread)
-//   warps 2-9:    packed nibbles -> binary16 A stages in tensor memory
-//   warps 10-25:  accumulator -> bfloat16 rows, scattered to the pairs' output rows
-// The stage layout, the conversion and the barriers are those of the dense prefill kernel (k_mmq.cu).
+//   warps 2-17:   packed nibbles -> binary16 A stages in tensor memory; four groups of four warps take
+//                 turns at the stages
+//   warps 18-25:  accumulator -> bfloat16 rows, scattered to the pairs' output rows
+//   warp 26:      the pass's activation rows by tensor copies, 64 K columns x 32 rows each
+// A pass of up to 128 pairs uses one half of the accumulator's 256 columns, so that the next item's
+// MMAs run while it is read; a wider one uses both.
+// The conversion of the weights is that of the dense prefill kernel (k_mmq.cu).
+// Measured and dropped: gathering the rows out of the unsorted image, by four-row tensor copies (their
+// operands are uniform per instruction, so the rows of a warp go one by one, about 85 cycles each:
+// 4096-row gate/up 1338 us) and by 16-byte asynchronous copies of six warps (685 us).
 
 #include <cuda_bf16.h>
 
@@ -37,28 +45,43 @@ constexpr int MAX_PROJ = 8;
 constexpr int MAX_E = 1024;
 constexpr int TM = 128;              // weight rows per item (MMA M)
 constexpr int TN = 256;              // most pairs of a pass (MMA N)
-constexpr int KC = 64;               // K elements of one activation box (a 128-byte swizzle row)
-constexpr int SK = 128;              // K elements per stage
-constexpr int NS = 3;                // stages (A in tensor memory, B in shared memory)
-constexpr int NU = 3;                // packed-weight slots
+constexpr int KC = 64;               // K elements of one activation slot (a 128-byte swizzle row)
+constexpr int SK = 128;              // K elements per weight stage
+constexpr int NS = 4;                // A stages in tensor memory, one per converter group
+constexpr int NB = 5;                // activation slots
+constexpr int BOX_ROWS = 32;         // rows of one activation copy
+constexpr int NU = NS;               // packed-weight slots: a slot always meets the same converter group
 constexpr int PF = 10;               // stages of weights prefetched into L2 ahead
-constexpr int B_BOX = TN * KC * 2;   // 32 KB
-constexpr int B_TILE = TN * SK * 2;  // 64 KB
+constexpr int B_SLOT = TN * KC * 2;  // 32 KB
 constexpr int U_SLOT = Q4_UNIT_BYTES;
 constexpr uint32_t A_COLS = SK / 2;
 constexpr uint32_t A_TMEM = TN;      // A stages follow the accumulator
 constexpr uint32_t TMEM_COLS = 512;
-constexpr int EPI0 = 10, N_EPI = 16;
-constexpr int THREADS = (EPI0 + N_EPI) * 32;
+constexpr int CONV0 = 2, EPI0 = CONV0 + 4 * NS, N_EPI = 8, ACT_WARP = EPI0 + N_EPI;
+constexpr int HALF = TN / 2;         // accumulator columns of one half
+constexpr int N_READERS = 2 + 4 * NS + N_EPI;   // warps that read an item's descriptor
+constexpr int THREADS = (ACT_WARP + 1) * 32;
 static_assert(A_TMEM + NS * A_COLS <= TMEM_COLS, "tensor memory");
 static_assert(4 * strip_unit_bytes(64) <= U_SLOT, "a weight stage fits its slot");
 
-// shared memory: [B tiles][weights][barriers][tensor-memory address, item count][pass prefix]
-constexpr int OFF_U = NS * B_TILE;
+struct Item {
+    int e, j, rt;        // expert, projection, row tile of the projection
+    int pass, passes;
+};
+struct Info {            // what the other warps need of an item
+    int j, rt, n, first; // projection, row tile, pairs of the pass and the plan position of the first
+    int pair[TN];        // their pair numbers, -1 where the plan names none of this bucket
+};
+
+// shared memory: [activation slots][weights][barriers][tensor-memory address, item count][descriptors]
+// [pass prefix]
+constexpr int OFF_U = NB * B_SLOT;
 constexpr int OFF_BAR = OFF_U + NU * U_SLOT;
-// full_a[NS] full_b[NS] empty[NS] ufull[NU] uempty[NU] acc_full acc_empty mma_done
-constexpr int N_BARS = 3 * NS + 2 * NU + 3;
-constexpr int OFF_PRE = OFF_BAR + N_BARS * 8 + 16;
+// full_a[NS] empty_a[NS] full_b[NB] empty_b[NB] ufull[NU] uempty[NU] acc_full[2] acc_empty[2]
+// info_full[2] info_empty[2] mma_done
+constexpr int N_BARS = 2 * NS + 2 * NB + 2 * NU + 9;
+constexpr int OFF_INFO = (OFF_BAR + N_BARS * 8 + 8 + 15) / 16 * 16;
+constexpr int OFF_PRE = OFF_INFO + 2 * (int)sizeof(Info);
 constexpr int SMEM_BYTES = OFF_PRE + (MAX_E + 1) * 4 + 1024;   // + slack to align the base to 1024
 static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
 
@@ -69,17 +92,12 @@ struct IdProj {
     int N, K, chunks, rt_begin;   // rt_begin: first row tile of this projection in the launch
 };
 struct IdArgs {
-    CUtensorMap bmap;             // activations [image rows][K] binary16, box 64 x 1, 128-byte swizzle
+    CUtensorMap bmap;             // activations [pairs][K] binary16 in plan order, box 64 x 32, swizzled
     const int32_t *counts, *offsets, *items;
     int pairs, k, E, per_pair, n_proj, row_tiles;
     IdProj p[MAX_PROJ];
 };
 
-struct Item {
-    int e, j, rt;     // expert, projection, row tile of the projection
-    int pass, passes;
-    int nkc;          // stages
-};
 __device__ __forceinline__ int clamped_count(const IdArgs &a, int e) {
     const int c = __ldg(a.counts + e);
     return c < 0 ? 0 : (c > a.pairs ? a.pairs : c);
@@ -103,10 +121,9 @@ __device__ __forceinline__ Item item_of(const IdArgs &a, const int *pre, int tau
     t.j = 0;
     while (t.j + 1 < a.n_proj && r >= a.p[t.j + 1].rt_begin) t.j++;
     t.rt = r - a.p[t.j].rt_begin;
-    t.nkc = a.p[t.j].chunks;
     return t;
 }
-// Pairs of the item's pass: `first` is their position in the plan, n > 0 their number.
+// Pairs of the item's pass: `first` is their position in the plan, n (1..256) their number.
 struct Pairs {
     int64_t first;
     int n;
@@ -128,27 +145,17 @@ __device__ __forceinline__ int pair_at(const IdArgs &a, int64_t pos) {
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity));
 }
-__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap *map, int x, int4 r, uint32_t mbar) {
+// 16 accumulator columns of this warp's lane quarter, packed to bfloat16 pairs of columns
+__device__ __forceinline__ void load_columns(uint32_t taddr, uint32_t *h) {
+    uint32_t v[16];
     asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes [%0], "
-        "[%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w), "r"(mbar)
-        : "memory");
-}
-// 32 accumulator columns of this warp's lane quarter, packed to bfloat16 pairs of columns
-__device__ __forceinline__ void load_columns(uint32_t taddr, uint32_t h[16]) {
-    uint32_t v[32];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
         : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
-          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
-          "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
-          "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
         : "r"(taddr));
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-    for (int i = 0; i < 16; i++)
+    for (int i = 0; i < 8; i++)
         asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(h[i]) : "f"(__uint_as_float(v[2 * i + 1])), "f"(__uint_as_float(v[2 * i])));
 }
 
@@ -194,6 +201,23 @@ __device__ __forceinline__ uint4 load_words(const uint8_t *unit, int quad, int j
     return *reinterpret_cast<const uint4 *>(unit + quad * strip_unit_bytes(G) + jb * 512 + lane * 16);
 }
 
+// grid (plan positions, ceil(4 kb / 256)): CTA (pos, y) writes row pos of the activations from the image
+// row of the pair there; thread j takes word j & 3 of block 64 y + j / 4 (as dequant_b_kernel).
+__global__ void __launch_bounds__(256) dequant_pairs_kernel(const int8_t *__restrict__ qs,
+                                                            const uint16_t *__restrict__ d, int64_t row_blocks,
+                                                            const int32_t *__restrict__ offsets,
+                                                            const int32_t *__restrict__ items, int E, int pairs, int k,
+                                                            int per_pair, int kb, __half *__restrict__ B) {
+    pdl_trigger();
+    pdl_wait();
+    const int pos = blockIdx.x, w = threadIdx.x & 3, b = blockIdx.y * 64 + (threadIdx.x >> 2);
+    if (b >= kb || pos >= __ldg(offsets + E)) return;   // positions past the plan hold no pair
+    const int p = __ldg(items + pos);
+    if (p < 0 || p >= pairs) return;
+    const int64_t row = per_pair ? p : p / k;
+    dequant_word(qs, d, row * row_blocks + b, w, B + ((int64_t)pos * kb + b) * QB);
+}
+
 template <int WT>
 __global__ void __launch_bounds__(THREADS, 1) mmq_id_kernel(const __grid_constant__ IdArgs a) {
     constexpr bool GROUPED = WT != QK_W_Q4_0;
@@ -201,11 +225,13 @@ __global__ void __launch_bounds__(THREADS, 1) mmq_id_kernel(const __grid_constan
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     const uint32_t sbase = smem_u32(smem);
-    const uint32_t full_a = sbase + OFF_BAR, full_b = full_a + NS * 8, empty = full_b + NS * 8;
-    const uint32_t ufull = empty + NS * 8, uempty = ufull + NU * 8, acc_full = uempty + NU * 8,
-                   acc_empty = acc_full + 8, mma_done = acc_empty + 8;
+    const uint32_t full_a = sbase + OFF_BAR, empty_a = full_a + NS * 8, full_b = empty_a + NS * 8,
+                   empty_b = full_b + NB * 8, ufull = empty_b + NB * 8, uempty = ufull + NU * 8,
+                   acc_full = uempty + NU * 8, acc_empty = acc_full + 16, info_full = acc_empty + 16,
+                   info_empty = info_full + 16, mma_done = info_empty + 16;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + OFF_BAR + N_BARS * 8);
     int *n_items = reinterpret_cast<int *>(tmem_slot + 1);
+    Info *info = reinterpret_cast<Info *>(smem + OFF_INFO);
     int *pre = reinterpret_cast<int *>(smem + OFF_PRE);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -213,17 +239,24 @@ __global__ void __launch_bounds__(THREADS, 1) mmq_id_kernel(const __grid_constan
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < NS; s++) {
-            mbar_init(full_a + 8 * s, 256);   // the eight converter warps
-            mbar_init(full_b + 8 * s, 1);     // the producer, with the bytes
-            mbar_init(empty + 8 * s, 1);      // the MMA commit
+            mbar_init(full_a + 8 * s, 4);     // the converter warps of its group
+            mbar_init(empty_a + 8 * s, 1);    // the MMA commit
+        }
+        for (int b = 0; b < NB; b++) {
+            mbar_init(full_b + 8 * b, 1);     // the activation warp, with the bytes
+            mbar_init(empty_b + 8 * b, 1);    // the MMA commit
         }
         for (int u = 0; u < NU; u++) {
-            mbar_init(ufull + 8 * u, 1);
-            mbar_init(uempty + 8 * u, 256);
+            mbar_init(ufull + 8 * u, 1);      // the weight warp, with the bytes
+            mbar_init(uempty + 8 * u, 4);     // the converter warps of the stage's group
         }
-        mbar_init(acc_full, 1);             // the MMA commit after an item's last stage
-        mbar_init(acc_empty, N_EPI * 32);   // the epilogue warps, once they have read it
-        mbar_init(mma_done, 1);             // the MMA thread's last commit
+        for (int h = 0; h < 2; h++) {
+            mbar_init(acc_full + 8 * h, 1);         // the MMA commit after an item's last stage
+            mbar_init(acc_empty + 8 * h, N_EPI);    // the epilogue warps, once they have read it
+            mbar_init(info_full + 8 * h, 1);        // the weight warp
+            mbar_init(info_empty + 8 * h, N_READERS);
+        }
+        mbar_init(mma_done, 1);               // the MMA thread's last commit
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) {
@@ -265,8 +298,17 @@ __global__ void __launch_bounds__(THREADS, 1) mmq_id_kernel(const __grid_constan
     const uint32_t tmem = *tmem_slot;
     const int items = *n_items;
 
-    if (warp == 0) {   // ---------------- producer
-        uint32_t g = 0, gu = 0;   // activation stages and weight stages issued by this CTA
+    // Item i of this CTA (items blockIdx.x + i * gridDim.x): entry i & 1 of the descriptor ring. A
+    // warp waits for it, and arrives on info_empty when it needs it no more.
+    auto await_info = [&](int i) { return warp_wait(info_full + 8 * (i & 1), (i >> 1) & 1); };
+    auto release_info = [&](int i) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(info_empty + 8 * (i & 1));
+    };
+    const int mine = items > (int)blockIdx.x ? (items - (int)blockIdx.x + G - 1) / G : 0;   // this CTA's items
+
+    if (warp == 0) {   // ---------------- items and weights
+        uint32_t gu = 0;   // weight stages issued by this CTA
         bool ok = true;
         // stage kc's weights of an item into L2
         auto prefetch = [&](const Item &t, int kc) {
@@ -280,33 +322,42 @@ __global__ void __launch_bounds__(THREADS, 1) mmq_id_kernel(const __grid_constan
                 prefetch_l2(w + ((int64_t)t.rt * P.chunks + kc) * Q4_UNIT_BYTES, Q4_UNIT_BYTES);
             }
         };
-        Item next = {};
-        if ((int)blockIdx.x < items) {
-            next = item_of(a, pre, blockIdx.x);
-            for (int kc = 0; kc < PF && kc < next.nkc; kc++) prefetch(next, kc);
-        }
-        for (int tau = blockIdx.x; tau < items && ok; tau += G) {
-            const Item t = next;
-            const bool more = tau + G < items;
-            if (more) next = item_of(a, pre, tau + G);
-            const IdProj &P = a.p[t.j];
-            const uint8_t *w = P.w + t.e * P.expert_bytes;
+        auto publish = [&](int i, const Item &t) {
+            if (i >= 2 && !warp_wait(info_empty + 8 * (i & 1), ((i >> 1) - 1) & 1)) return false;
+            Info &f = info[i & 1];
             const Pairs pr = pairs_of(a, t);
-            const int groups = ((pr.n + 15) & ~15) / 4;   // four rows each; rows past n repeat the last one
-            int4 r[2];
 #pragma unroll
-            for (int h = 0; h < 2; h++) {
-                int v[4];
-#pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    const int p = max(0, pair_at(a, pr.first + min(4 * (lane + 32 * h) + i, pr.n - 1)));
-                    v[i] = a.per_pair ? p : p / a.k;
-                }
-                r[h] = make_int4(v[0], v[1], v[2], v[3]);
+            for (int j = 0; j < TN / 32; j++) {
+                const int c = 32 * j + lane;
+                f.pair[c] = c < pr.n ? pair_at(a, pr.first + c) : -1;
             }
+            if (lane == 0) {
+                f.j = t.j;
+                f.rt = t.rt;
+                f.n = pr.n;
+                // rows outside the plan's read as zeros (a plan from elsewhere: none of them is stored)
+                f.first = (int)(pr.first < -TN ? -TN : (pr.first > a.pairs ? a.pairs : pr.first));
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(info_full + 8 * (i & 1));
+            return true;
+        };
+        Item next = {};
+        if (mine > 0) {
+            next = item_of(a, pre, blockIdx.x);
+            ok = publish(0, next);
+            for (int kc = 0; kc < PF && kc < a.p[next.j].chunks; kc++) prefetch(next, kc);
+        }
+        for (int i = 0; i < mine && ok; i++) {
+            const Item t = next;
+            const IdProj &P = a.p[t.j];
+            const bool more = i + 1 < mine;
+            if (more) next = item_of(a, pre, blockIdx.x + (i + 1) * G);
+            const int next_chunks = more ? a.p[next.j].chunks : 0;
+            const uint8_t *w = P.w + t.e * P.expert_bytes;
             const int strips = GROUPED ? min(4, (P.N - t.rt * TM + STRIP_ROWS - 1) / STRIP_ROWS) : 0;
-            for (int kc = 0; kc < t.nkc; kc++, g++) {
-                const uint32_t s = g % NS, us = gu % NU;
+            for (int kc = 0; kc < P.chunks; kc++) {
+                const uint32_t us = gu % NU;
                 if (gu >= NU && !warp_wait(uempty + 8 * us, ((gu / NU) - 1) & 1u)) {
                     ok = false;
                     break;
@@ -323,85 +374,113 @@ __global__ void __launch_bounds__(THREADS, 1) mmq_id_kernel(const __grid_constan
                 }
                 gu++;
                 // keep the weights PF stages ahead (in this item or the next one) on their way into L2
-                if (kc + PF < t.nkc)
+                if (kc + PF < P.chunks)
                     prefetch(t, kc + PF);
-                else if (more && kc + PF - t.nkc < next.nkc)
-                    prefetch(next, kc + PF - t.nkc);
-                if (g >= NS && !warp_wait(empty + 8 * s, ((g / NS) - 1) & 1u)) {
-                    ok = false;
-                    break;
-                }
-                // the stage's activations: one or two 64-column boxes of `groups` x 4 rows
-                const int boxes = P.K - kc * SK > KC ? 2 : 1;
-                if (lane == 0) mbar_expect_tx(full_b + 8 * s, (uint32_t)(boxes * groups * 4 * KC * 2));
-                __syncwarp();
-                for (int b = 0; b < boxes; b++) {
-                    const uint32_t dst = sbase + s * B_TILE + b * B_BOX + lane * (4 * KC * 2);
-                    if (lane < groups) tma_gather4(dst, &a.bmap, kc * SK + b * KC, r[0], full_b + 8 * s);
-                    if (lane + 32 < groups)
-                        tma_gather4(dst + 32 * (4 * KC * 2), &a.bmap, kc * SK + b * KC, r[1], full_b + 8 * s);
-                }
-                __syncwarp();
+                else if (kc + PF - P.chunks < next_chunks)
+                    prefetch(next, kc + PF - P.chunks);
             }
+            if (ok && more) ok = publish(i + 1, next);
         }
         // Every copy this warp issued has landed before the CTA can exit, also after a wait above ran
         // out (a barrier whose phase completed long ago passes at once; a wait that runs out here ends
         // the drain).
-        for (uint32_t x = g > NS ? g - NS : 0; x < g; x++)
-            if (!warp_wait(full_b + 8 * (x % NS), (x / NS) & 1u)) break;
         for (uint32_t x = gu > NU ? gu - NU : 0; x < gu; x++)
             if (!warp_wait(ufull + 8 * (x % NU), (x / NU) & 1u)) break;
-    } else if (warp == 1) {   // ---------------- MMA issue (one thread)
-        if (lane == 0) {
-            uint32_t g = 0;
-            int i = 0;
-            bool ok = true;
-            for (int tau = blockIdx.x; tau < items && ok; tau += G, i++) {
-                const Item t = item_of(a, pre, tau);
-                const uint32_t idesc = mma_idesc((pairs_of(a, t).n + 15) & ~15);
-                const int K = a.p[t.j].K;
-                if (i >= 1 && !mbar_wait(acc_empty, (i - 1) & 1u)) break;
-                tc_fence_after();
-                for (int kc = 0; kc < t.nkc; kc++, g++) {
-                    const uint32_t s = g % NS, par = (g / NS) & 1u;
-                    if (!mbar_wait(full_a + 8 * s, par) || !mbar_wait(full_b + 8 * s, par)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t at = tmem + A_TMEM + s * A_COLS, bt = sbase + s * B_TILE;
-                    const int steps = min(SK, K - kc * SK) / 16;   // nothing past K enters the sum
-#pragma unroll
-                    for (int ks = 0; ks < SK / 16; ks++)
-                        if (ks < steps)
-                            tc_mma(tmem, at + 8 * ks, sdesc(bt + (ks >> 2) * B_BOX + 32 * (ks & 3)), idesc,
-                                   (kc | ks) != 0);
-                    tc_commit(empty + 8 * s);
+    } else if (warp == ACT_WARP) {   // ---------------- activations
+        uint32_t gb = 0;   // slots filled by this CTA
+        bool ok = true;
+        for (int i = 0; i < mine && ok; i++) {
+            if (!await_info(i)) break;
+            const Info &f = info[i & 1];
+            const int K = a.p[f.j].K, first = f.first, boxes = (((f.n + 15) & ~15) + BOX_ROWS - 1) / BOX_ROWS;
+            release_info(i);
+            for (int k0 = 0; k0 < K; k0 += KC, gb++) {
+                const uint32_t bs = gb % NB;
+                if (gb >= NB && !warp_wait(empty_b + 8 * bs, ((gb / NB) - 1) & 1u)) {
+                    ok = false;
+                    break;
                 }
-                if (ok) tc_commit(acc_full);
+                if (lane == 0) {
+                    mbar_expect_tx(full_b + 8 * bs, (uint32_t)(boxes * BOX_ROWS * KC * 2));
+                    for (int b = 0; b < boxes; b++)
+                        tma_2d(sbase + bs * B_SLOT + b * (BOX_ROWS * KC * 2), &a.bmap, k0, first + b * BOX_ROWS,
+                               full_b + 8 * bs);
+                }
+                __syncwarp();
             }
+        }
+        for (uint32_t x = gb > NB ? gb - NB : 0; x < gb; x++)   // as above: all copies have landed
+            if (!warp_wait(full_b + 8 * (x % NB), (x / NB) & 1u)) break;
+    } else if (warp == 1) {   // ---------------- MMA issue (one thread)
+        uint32_t g = 0, gb = 0;         // A stages and activation slots consumed
+        uint32_t uses[2] = {0, 0};      // of the accumulator halves
+        int side = 0;                   // the half that the next narrow item takes
+        bool ok = lane == 0;
+        for (int i = 0; i < mine && ok; i++) {
+            if (!mbar_wait(info_full + 8 * (i & 1), (i >> 1) & 1)) break;
+            const int n = info[i & 1].n, K = a.p[info[i & 1].j].K, nkc = (K + SK - 1) / SK;
+            mbar_arrive(info_empty + 8 * (i & 1));
+            const uint32_t idesc = mma_idesc((n + 15) & ~15);
+            const bool wide = n > HALF;
+            const int h = wide ? 0 : side;
+            if (uses[h] > 0) ok = mbar_wait(acc_empty + 8 * h, (uses[h] - 1) & 1u);
+            if (wide && uses[1] > 0) ok = ok && mbar_wait(acc_empty + 8, (uses[1] - 1) & 1u);
+            if (!ok) break;
+            const uint32_t acc = tmem + h * HALF;
+            tc_fence_after();
+            for (int kc = 0; kc < nkc && ok; kc++, g++) {
+                const uint32_t s = g % NS, at = tmem + A_TMEM + s * A_COLS;
+                ok = mbar_wait(full_a + 8 * s, (g / NS) & 1u);
+#pragma unroll
+                for (int half = 0; half < 2; half++) {
+                    const int left = K - kc * SK - half * KC;   // nothing past K enters the sum
+                    if (left <= 0 || !ok) break;
+                    const uint32_t bs = gb % NB;
+                    ok = mbar_wait(full_b + 8 * bs, (gb / NB) & 1u);
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int ks = 0; ks < KC / 16; ks++)
+                        if (16 * ks < left)
+                            tc_mma(acc, at + 32 * half + 8 * ks, sdesc(sbase + bs * B_SLOT + 32 * ks), idesc,
+                                   (kc | half | ks) != 0);
+                    tc_commit(empty_b + 8 * bs);
+                    gb++;
+                }
+                if (ok) tc_commit(empty_a + 8 * s);
+            }
+            if (!ok) break;
+            tc_commit(acc_full + 8 * h);
+            uses[h]++;
+            if (wide) {
+                tc_commit(acc_full + 8);
+                uses[1]++;
+            }
+            side = wide ? 0 : side ^ 1;
+        }
+        if (lane == 0) {
             tc_commit(mma_done);   // every MMA issued here is complete before the tensor memory is freed
             mbar_wait(mma_done, 0u);
         }
-    } else if (warp < EPI0) {   // ---------------- warps 2..9: A conversion into tensor memory
-        // lanes 32 (warp % 4) .. +31 of tensor memory are tile rows 32 (warp % 4) ..; qb: this warp
-        // takes blocks qb and qb + 2 of the stage
-        const int quad = warp & 3, qb = (warp - 2) >> 2, gq = lane >> 2;
-        const uint32_t arow = tmem + ((uint32_t)(32 * quad) << 16) + A_TMEM;
-        uint32_t g = 0;
+    } else if (warp < EPI0) {   // ---------------- A conversion into tensor memory
+        // lanes 32 (warp % 4) .. +31 of tensor memory are tile rows 32 (warp % 4) ..; a group of four
+        // warps takes every NS-th stage and always the same A stage
+        const int quad = warp & 3, group = (warp - CONV0) >> 2, gq = lane >> 2;
+        const uint32_t abase = tmem + ((uint32_t)(32 * quad) << 16) + A_TMEM + group * A_COLS;
+        uint32_t g0 = 0, use = 0;   // the item's first stage; stages this group has filled
         bool ok = true;
-        for (int tau = blockIdx.x; tau < items && ok; tau += G) {
-            const Item t = item_of(a, pre, tau);
-            for (int kc = 0; kc < t.nkc; kc++, g++) {
-                const uint32_t s = g % NS, us = g % NU;
-                ok = warp_wait(ufull + 8 * us, (g / NU) & 1u);
-                if (ok && g >= NS) ok = warp_wait(empty + 8 * s, ((g / NS) - 1) & 1u);
+        for (int i = 0; i < mine && ok; i++) {
+            if (!await_info(i)) break;
+            const uint32_t nkc = a.p[info[i & 1].j].chunks;
+            release_info(i);
+            for (uint32_t g = g0 + ((group - g0) & (NS - 1)); g < g0 + nkc; g += NS, use++) {
+                ok = warp_wait(ufull + 8 * group, use & 1u);
+                if (ok && use > 0) ok = warp_wait(empty_a + 8 * group, (use - 1) & 1u);
                 if (!ok) break;
                 tc_fence_after();
-                const uint8_t *unit = smem + OFF_U + us * U_SLOT;
+                const uint8_t *unit = smem + OFF_U + group * U_SLOT;
 #pragma unroll
-                for (int h = 0; h < 2; h++) {
-                    const int jb = 2 * h + qb;
+                for (int jb = 0; jb < 4; jb++) {
                     const uint4 wv = load_words<WT>(unit, quad, jb, lane);
                     RowHeads<WT> hd;
                     load_heads<WT>(unit, quad, jb, gq, hd);
@@ -409,7 +488,7 @@ __global__ void __launch_bounds__(THREADS, 1) mmq_id_kernel(const __grid_constan
                     const uint4 a1 = a_word(wv.y, hd.dw[1], hd.blo[1], hd.bhi[1]);
                     const uint4 a2 = a_word(wv.z, hd.dw[2], hd.blo[2], hd.bhi[2]);
                     const uint4 a3 = a_word(wv.w, hd.dw[3], hd.blo[3], hd.bhi[3]);
-                    const uint32_t base = arow + s * A_COLS + 16 * jb;
+                    const uint32_t base = abase + 16 * jb;
                     asm volatile(
                         "tcgen05.st.sync.aligned.16x256b.x2.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(base),
                         "r"(a0.x), "r"(a0.y), "r"(a1.x), "r"(a1.y), "r"(a0.z), "r"(a0.w), "r"(a1.z), "r"(a1.w)
@@ -421,48 +500,61 @@ __global__ void __launch_bounds__(THREADS, 1) mmq_id_kernel(const __grid_constan
                 }
                 asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                 tc_fence_before();
-                mbar_arrive(full_a + 8 * s);
-                mbar_arrive(uempty + 8 * us);
-            }
-        }
-    } else {   // ---------------- warps 10..25: epilogue (accumulator lane = weight row, column = pair)
-        const int quad = warp & 3, c0 = ((warp - EPI0) >> 2) * 64, odd = lane & 1;
-        const uint32_t taddr = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)c0;
-        int i = 0;
-        for (int tau = blockIdx.x; tau < items; tau += G, i++) {
-            const Item t = item_of(a, pre, tau);
-            const IdProj &P = a.p[t.j];
-            const Pairs pr = pairs_of(a, t);
-            const int n = pr.n - c0;   // pairs of this column quarter
-            const int id0 = lane < n ? pair_at(a, pr.first + c0 + lane) : -1;
-            const int id1 = lane + 32 < n ? pair_at(a, pr.first + c0 + 32 + lane) : -1;
-            if (!warp_wait(acc_full, i & 1u)) break;
-            tc_fence_after();
-            uint32_t h[32];
-            if (n > 0) load_columns(taddr, h);
-            if (n > 32) load_columns(taddr + 32u, h + 16);
-            tc_fence_before();
-            mbar_arrive(acc_empty);   // read: the MMAs of the next item may start
-            // Rows come two at a time: lanes l and l ^ 1 exchange columns, so that the even lane holds
-            // rows (l, l+1) of column 2k and the odd lane the same rows of column 2k+1: 4-byte stores.
-            const int row = t.rt * TM + quad * 32 + (lane & ~1);
-            const bool two = row + 1 < P.N && ((reinterpret_cast<uintptr_t>(P.y) | (uintptr_t)(P.y_stride * 2)) & 3) == 0;
-            uint16_t *yr = P.y + row;
-#pragma unroll
-            for (int kk = 0; kk < 32; kk++) {
-                if (2 * kk >= n) break;   // uniform
-                const uint32_t other = __shfl_xor_sync(0xffffffffu, h[kk], 1);
-                const uint32_t v = odd ? __byte_perm(other, h[kk], 0x7632) : __byte_perm(h[kk], other, 0x5410);
-                const int id = __shfl_sync(0xffffffffu, kk < 16 ? id0 : id1, (2 * kk + odd) & 31);
-                if (id < 0 || row >= P.N) continue;
-                uint16_t *dst = yr + id * P.y_stride;
-                if (two) {
-                    *reinterpret_cast<uint32_t *>(dst) = v;
-                } else {
-                    dst[0] = (uint16_t)v;
-                    if (row + 1 < P.N) dst[1] = (uint16_t)(v >> 16);
+                __syncwarp();
+                if (lane == 0) {   // one arrival per warp: a lane's arrivals on one barrier go one by one
+                    mbar_arrive(full_a + 8 * group);
+                    mbar_arrive(uempty + 8 * group);
                 }
             }
+            g0 += nkc;
+        }
+    } else {   // ---------------- epilogue (accumulator lane = weight row, column = pair)
+        const int quad = warp & 3, c0 = ((warp - EPI0) >> 2) * 64, odd = lane & 1;
+        uint32_t uses = 0;   // bit h: parity of the uses of accumulator half h
+        int side = 0;
+        bool ok = true;
+        for (int i = 0; i < mine && ok; i++) {
+            if (!await_info(i)) break;
+            const Info &f = info[i & 1];
+            const IdProj &P = a.p[f.j];
+            const int all = f.n, row = f.rt * TM + quad * 32 + (lane & ~1);
+            const bool wide = all > HALF;
+            const bool two = row + 1 < P.N && ((reinterpret_cast<uintptr_t>(P.y) | (uintptr_t)(P.y_stride * 2)) & 3) == 0;
+            uint16_t *yr = P.y + row;
+            for (int h = wide ? 0 : side, end = wide ? 2 : side + 1; h < end; h++) {
+                ok = warp_wait(acc_full + 8 * h, (uses >> h) & 1u);
+                if (!ok) break;
+                uses ^= 1u << h;
+                tc_fence_after();
+                const int from = c0 + (wide ? HALF * h : 0), n = all - from;   // the first pair here, pairs here and past
+                const uint32_t taddr = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(h * HALF + c0);
+                uint32_t v[32];
+#pragma unroll
+                for (int q = 0; q < 4; q++)
+                    if (n > 16 * q) load_columns(taddr + 16u * q, v + 8 * q);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(acc_empty + 8 * h);   // read: a later item's MMAs may use it
+                // Rows come two at a time: lanes l and l ^ 1 exchange columns, so that the even lane holds
+                // rows (l, l+1) of column 2k and the odd lane the same rows of column 2k+1: 4-byte stores.
+#pragma unroll
+                for (int kk = 0; kk < 32; kk++) {
+                    if (2 * kk >= n) break;   // uniform
+                    const uint32_t other = __shfl_xor_sync(0xffffffffu, v[kk], 1);
+                    const uint32_t o = odd ? __byte_perm(other, v[kk], 0x7632) : __byte_perm(v[kk], other, 0x5410);
+                    const int id = f.pair[from + 2 * kk + odd];
+                    if (id < 0 || row >= P.N) continue;
+                    uint16_t *dst = yr + id * P.y_stride;
+                    if (two) {
+                        *reinterpret_cast<uint32_t *>(dst) = o;
+                    } else {
+                        dst[0] = (uint16_t)o;
+                        if (row + 1 < P.N) dst[1] = (uint16_t)(o >> 16);
+                    }
+                }
+            }
+            side = wide ? 0 : side ^ 1;
+            release_info(i);
         }
     }
     tc_fence_before();
@@ -483,7 +575,7 @@ qk_status launch_type(const IdArgs &a, cudaStream_t s) {
 
 }  // namespace
 
-int64_t mmq_id_workspace_bytes(int64_t img_rows, int64_t kmax) { return (img_rows * kmax * 2 + 127) / 128 * 128; }
+int64_t mmq_id_workspace_bytes(int64_t pairs, int64_t kmax) { return (pairs * kmax * 2 + 127) / 128 * 128; }
 
 qk_status read_mmq_id_faults(uint32_t *faults) {
     unsigned int v = 0, zero = 0;
@@ -494,27 +586,30 @@ qk_status read_mmq_id_faults(uint32_t *faults) {
     return QK_OK;
 }
 
-qk_status launch_mmq_id(const int8_t *qs, const uint16_t *d, int64_t row_blocks, int64_t img_rows, int rows, int k,
+qk_status launch_mmq_id(const int8_t *qs, const uint16_t *d, int64_t row_blocks, int rows, int k,
                         int n_proj, const qk_proj_id16 *projs, const int32_t *counts, const int32_t *offsets,
                         const int32_t *items, bool per_pair, void *ws, cudaStream_t s) {
     int64_t kmax = 0;
     for (int j = 0; j < n_proj; j++) kmax = projs[j].K > kmax ? projs[j].K : kmax;
+    IdArgs a = {};
+    const int pairs = rows * k, kb = (int)(kmax / QB);
     PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
     if (!enc) return fail(QK_ERR_CUDA, "mmq_id: cuTensorMapEncodeTiled is not available");
-    IdArgs a = {};
-    const cuuint64_t dims[2] = {(cuuint64_t)kmax, (cuuint64_t)img_rows};
+    const cuuint64_t dims[2] = {(cuuint64_t)kmax, (cuuint64_t)pairs};
     const cuuint64_t strides[1] = {(cuuint64_t)kmax * 2};
-    const cuuint32_t box[2] = {KC, 1}, estr[2] = {1, 1};
+    const cuuint32_t box[2] = {KC, BOX_ROWS}, estr[2] = {1, 1};
     const CUresult r = enc(&a.bmap, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, ws, dims, strides, box, estr,
                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return fail(QK_ERR_CUDA, "mmq_id: tensor map encoding failed (%d)", (int)r);
-    qk_status st = launch_dequant_b("mmq_id_dequant_b", qs, d, row_blocks, (int)img_rows, (int)kmax, ws, s);
+    qk_status st = launch_pdl("mmq_id_dequant", dequant_pairs_kernel, dim3((unsigned)pairs, (unsigned)ceil_div(kb, 64)),
+                              dim3(256), 0, s, qs, d, row_blocks, offsets, items, (int)projs[0].n_experts, pairs, k,
+                              (int)per_pair, kb, static_cast<__half *>(ws));
     if (st != QK_OK) return st;
     a.counts = counts;
     a.offsets = offsets;
     a.items = items;
-    a.pairs = rows * k;
+    a.pairs = pairs;
     a.k = k;
     a.E = projs[0].n_experts;
     a.per_pair = per_pair;

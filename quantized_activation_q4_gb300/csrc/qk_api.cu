@@ -622,11 +622,11 @@ qk_status qk_mmq(const int8_t *qs, const uint16_t *d, int64_t row_blocks, int64_
 }
 
 // ------------------------------------------------------------------ routed prefill
-size_t qk_mmq_id_workspace_bytes(int64_t img_rows, int32_t n_proj, const qk_proj_id16 *projs) {
-    if (img_rows < 1 || n_proj < 1 || n_proj > 8 || !projs) return 0;
+size_t qk_mmq_id_workspace_bytes(int64_t rows, int32_t k, int32_t n_proj, const qk_proj_id16 *projs) {
+    if (rows < 1 || rows > (1 << 24) || k < 1 || k > 64 || n_proj < 1 || n_proj > 8 || !projs) return 0;
     int64_t kmax = 0;
     for (int j = 0; j < n_proj; j++) kmax = projs[j].K > kmax ? projs[j].K : kmax;
-    return (size_t)mmq_id_workspace_bytes(img_rows, kmax);
+    return (size_t)mmq_id_workspace_bytes(rows * k, kmax);
 }
 
 static qk_status mmq_id_common(const int8_t *qs, const uint16_t *d, int64_t row_blocks, int64_t rows, int32_t k,
@@ -666,7 +666,7 @@ static qk_status mmq_id_common(const int8_t *qs, const uint16_t *d, int64_t row_
     }
     // work items (passes of any plan x row tiles) are counted in int
     REQUIRE((pairs / 256 + E) * tiles < (1LL << 31), QK_ERR_UNSUPPORTED, "rows * k * row tiles too large for one launch");
-    const size_t need = qk_mmq_id_workspace_bytes(img_rows, n_proj, projs);
+    const size_t need = qk_mmq_id_workspace_bytes(rows, k, n_proj, projs);
     REQUIRE(ws && aligned(ws, 128), QK_ERR_WORKSPACE, "workspace null or not 128-byte aligned");
     REQUIRE(ws_bytes >= need, QK_ERR_WORKSPACE, "workspace %zu < %zu bytes", ws_bytes, need);
     const Span sws = span(ws, need);
@@ -675,7 +675,7 @@ static qk_status mmq_id_common(const int8_t *qs, const uint16_t *d, int64_t row_
         REQUIRE(!overlap(sws, span(projs[j].y, rows_span(pairs, projs[j].y_stride * 2, projs[j].N * 2))) &&
                     !overlap(sws, span(projs[j].w, (size_t)(packed_bytes(projs[j].wtype, projs[j].N, projs[j].K) * E))),
                 QK_ERR_ALIAS, "workspace overlaps projection %d", j);
-    return launch_mmq_id(qs, d, row_blocks, img_rows, (int)rows, k, n_proj, projs, counts, offsets, items, per_pair, ws,
+    return launch_mmq_id(qs, d, row_blocks, (int)rows, k, n_proj, projs, counts, offsets, items, per_pair, ws,
                          (cudaStream_t)stream);
 }
 

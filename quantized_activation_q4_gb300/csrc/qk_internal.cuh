@@ -180,10 +180,10 @@ qk_status launch_mmvq_g(const uint8_t *img, int64_t row_blocks, int T, int n_pro
 qk_status launch_mmvq_g_id(const uint8_t *img, int64_t row_blocks, int rows, int k, int n_proj,
                            const qk_proj_id *projs, const int32_t *counts, const int32_t *offsets,
                            const int32_t *items, bool per_pair, cudaStream_t s);
-qk_status launch_mmq_id(const int8_t *qs, const uint16_t *d, int64_t row_blocks, int64_t img_rows, int rows, int k,
+qk_status launch_mmq_id(const int8_t *qs, const uint16_t *d, int64_t row_blocks, int rows, int k,
                         int n_proj, const qk_proj_id16 *projs, const int32_t *counts, const int32_t *offsets,
                         const int32_t *items, bool per_pair, void *ws, cudaStream_t s);
-int64_t mmq_id_workspace_bytes(int64_t img_rows, int64_t kmax);
+int64_t mmq_id_workspace_bytes(int64_t pairs, int64_t kmax);
 qk_status launch_topk_route(const float *logits, int rows, int E, int k, int32_t *ids,
                             float *wts, const int32_t *live, cudaStream_t s);
 qk_status launch_moe_plan(const int32_t *ids, int rows, int k, int E, int32_t *counts,
@@ -196,9 +196,5 @@ qk_status launch_mmq(const int8_t *qs, const uint16_t *d, int64_t row_blocks, in
 int64_t mmq_workspace_bytes(int64_t T, int64_t kmax);
 qk_status read_mmq_faults(uint32_t *faults);
 qk_status read_mmq_id_faults(uint32_t *faults);
-// The image's first K columns as binary16 q * d_a, [T][K], in the K order of the prefill kernels'
-// A stages (see dequant_b_kernel).
-qk_status launch_dequant_b(const char *name, const int8_t *qs, const uint16_t *d, int64_t row_blocks, int T, int K,
-                           void *B, cudaStream_t s);
 
 }  // namespace qk

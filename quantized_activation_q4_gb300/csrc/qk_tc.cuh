@@ -101,6 +101,36 @@ __device__ __forceinline__ uint4 a_word(uint32_t w, __half2 dw) {
     return a_word(w, dw, half2_bits(0x64086408u), half2_bits(0x54805480u));
 }
 
+// Two codes of word v (bytes k and k + 2, k = 0 or 1) -> f16 pair q * d_a. A code becomes an
+// exact half by placing its biased byte (q + 128) under the exponent of 1024 (PRMT); subtracting
+// 1152 leaves q exactly; the binary16 multiply by d_a rounds the exact product once, as the
+// binary32 product rounded to binary16 would.
+__device__ __forceinline__ uint32_t b_pair(uint32_t u, uint32_t sel, __half2 d2) {
+    uint32_t h;
+    asm("prmt.b32 %0, %1, 0x64646464, %2;" : "=r"(h) : "r"(u), "r"(sel));
+    const __half2 bias = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));   // 1152
+    const __half2 r = __hmul2(__hsub2(*reinterpret_cast<const __half2 *>(&h), bias), d2);
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+// four codes (one word, elements e .. e+3) -> halves in the order e, e+2, e+1, e+3
+__device__ __forceinline__ uint2 b_word(uint32_t v, __half2 d2) {
+    const uint32_t u = v ^ 0x80808080u;   // q + 128 in each byte
+    return make_uint2(b_pair(u, 0x4240u, d2), b_pair(u, 0x4341u, d2));
+}
+
+// Word w of an image block (codes 4w .. 4w+3 and 16+4w .. 16+4w+3) -> f16 q * d_a at dst's columns 2w,
+// 2w+1 (halves 4w .. 4w+3) and 8+2w, 9+2w (halves 16+4w ..), the K order of the A stages.
+__device__ __forceinline__ void dequant_word(const int8_t *__restrict__ qs, const uint16_t *__restrict__ d, int64_t block,
+                                             int w, __half *dst) {
+    const int8_t *src = qs + block * QB;
+    const uint32_t lo = __ldg(reinterpret_cast<const unsigned int *>(src + 4 * w));
+    const uint32_t hi = __ldg(reinterpret_cast<const unsigned int *>(src + 16 + 4 * w));
+    const __half dah = __ushort_as_half(__ldg(d + block));
+    const __half2 d2 = __halves2half2(dah, dah);
+    *reinterpret_cast<uint2 *>(dst + 4 * w) = b_word(lo, d2);
+    *reinterpret_cast<uint2 *>(dst + 16 + 4 * w) = b_word(hi, d2);
+}
+
 inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
     static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
     if (!fn) {

@@ -58,9 +58,9 @@ def bhost(t):
     return host(t.float()).astype(np.float64)
 
 
-def workspace(img_rows, projs, fill=0xFF):
+def workspace(rows, k, projs, fill=0xFF):
     import torch
-    n = qk.qk_mmq_id_workspace_bytes(img_rows, projs)
+    n = qk.qk_mmq_id_workspace_bytes(rows, k, projs)
     return torch.full((n,), fill, dtype=torch.uint8, device="cuda"), n
 
 
@@ -91,7 +91,7 @@ def run(wtype, rows, k, E, K, Ns, live, slots, ids=None, seed=12000, rb=None, pa
         Ws.append((ws_, pw))
         projs.append(qk.make_proj_id16(wtype, E, pw, N, K, y[:, at:], width))
         at += N
-    ws, n = workspace(n_img, projs)
+    ws, n = workspace(rows, k, projs)
     call = qk.qk_mmq_id_slots if slots else qk.qk_mmq_id
     call(dev(qs), dev(dh.view(np.int16)), qs.shape[1] // 32, rows, k, projs, counts, offsets, items, ws, n)
     assert qk.qk_device_faults() == 0
@@ -175,7 +175,7 @@ def test_projections_of_different_types_and_widths_of_k():
         keep.append((Ws, pw))
         ys.append(y)
         projs.append(qk.make_proj_id16(wt, E, pw, N, K, y, N))
-    ws, n = workspace(rows, projs)
+    ws, n = workspace(rows, k, projs)
     qk.qk_mmq_id(dev(qs), dev(dh.view(np.int16)), rb, rows, k, projs, *p, ws, n)
     flat = ids.reshape(-1)
     for (wt, N, K), (Ws, _), y in zip(specs, keep, ys):
@@ -202,7 +202,7 @@ def test_deterministic_and_replayed():
     pw = pack_experts(Ws, "q4_g64", N, K)
     y = out(rows * k, N)
     projs = [qk.make_proj_id16("q4_g64", E, pw, N, K, y, N)]
-    ws, n = workspace(rows, projs)
+    ws, n = workspace(rows, k, projs)
     logits = dev(synth.router_logits(12801, rows, E))
     ids = torch.zeros((rows, k), dtype=torch.int32, device="cuda")
     wts = torch.zeros((rows, k), device="cuda")
@@ -253,7 +253,7 @@ def test_a_plan_from_elsewhere_reads_and_writes_inside_its_buffers():
     guard = torch.full((rows * k + 64, N), SENTINEL, dtype=torch.bfloat16, device="cuda")
     y = guard[32:32 + rows * k]
     projs = [qk.make_proj_id16("q4_0", E, pw, N, K, y, N)]
-    ws, n = workspace(rows, projs)
+    ws, n = workspace(rows, k, projs)
     qk.qk_mmq_id(dev(qs), dev(dh.view(np.int16)), K // 32, rows, k, projs, counts, offsets, dev(it), ws, n)
     got, x = bhost(guard), O.plane_values(qs, dh, K)
     assert np.all(got[:32] == SENTINEL) and np.all(got[32 + rows * k:] == SENTINEL)

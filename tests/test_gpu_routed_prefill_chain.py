@@ -152,7 +152,7 @@ def test_routed_prefill_ffn(wtype):
     dn, y = z(rows * k, K, dtype=torch.bfloat16), z(rows, K)
     gate_up = [qk.make_proj_id16(wtype, E, pg, F, K, gu, 2 * F), qk.make_proj_id16(wtype, E, pu, F, K, gu[:, F:], 2 * F)]
     down = [qk.make_proj_id16(wtype, E, pd, K, F, dn, K)]
-    n = max(qk.qk_mmq_id_workspace_bytes(rows, gate_up), qk.qk_mmq_id_workspace_bytes(rows * k, down))
+    n = max(qk.qk_mmq_id_workspace_bytes(rows, k, gate_up), qk.qk_mmq_id_workspace_bytes(rows, k, down))
     ws, live = torch.empty((n,), dtype=torch.uint8, device="cuda"), live_ptr(rows)
 
     def ffn():

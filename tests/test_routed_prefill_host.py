@@ -96,8 +96,8 @@ def _mmq_id(lib, slots=False, n=1, rows=4, k=2, rb=8, ws=WS, ws_bytes=1 << 20, q
 @pytest.mark.parametrize("slots", [False, True])
 def test_routed_prefill_checks(lib, slots):
     go = lambda **kw: _mmq_id(lib, slots=slots, **kw)
-    need = qk.qk_mmq_id_workspace_bytes(4 * (2 if slots else 1), [qk.qk_proj_id16(3, 4, W, 64, 256, Y, 64)])
-    assert need >= 4 * (2 if slots else 1) * 256 * 2
+    need = qk.qk_mmq_id_workspace_bytes(4, 2, [qk.qk_proj_id16(3, 4, W, 64, 256, Y, 64)])
+    assert need >= 4 * 2 * 256 * 2
     assert go(t=1, K=256) == 5                     # Q8_0 weights
     assert go(t=4) == 1 and go(t=-1) == 1          # no such type
     assert go(K=256 + 32) == 2                     # not whole groups
