@@ -21,7 +21,7 @@
 //
 //   warp 0:       looks the items up one ahead (descriptor and pair list into a two-entry ring) and
 //                 streams the packed weights (stages of 128 rows x 128 K) by bulk copies
-//   warp 1:       allocates tensor memory, issues the MMAs (one thread)
+//   warp 1:       allocates tensor memory, issues the MMAs (one elected thread)
 //   warps 2-17:   packed nibbles -> binary16 A stages in tensor memory; four groups of four warps take
 //                 turns at the stages
 //   warps 18-25:  accumulator -> bfloat16 rows, scattered to the pairs' output rows
@@ -141,6 +141,14 @@ __device__ __forceinline__ int pair_at(const IdArgs &a, int64_t pos) {
     return p >= 0 && p < a.pairs ? p : -1;
 }
 
+// One lane of a converged warp. Tensor copies, MMAs and commits take their operands from uniform
+// registers: under elect.sync the compiler issues them directly (an MMA about 17 cycles), under a
+// test of the lane number in a loop over the lanes (about 150).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+    return p != 0;
+}
 // A whole warp's wait: every lane gets the same answer.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity));
@@ -314,12 +322,14 @@ __global__ void __launch_bounds__(THREADS, 1) mmq_id_kernel(const __grid_constan
         auto prefetch = [&](const Item &t, int kc) {
             const IdProj &P = a.p[t.j];
             const uint8_t *w = P.w + t.e * P.expert_bytes;
-            if (GROUPED) {
-                const int strip = 4 * t.rt + lane;
-                if (lane < 4 && strip * STRIP_ROWS < P.N)
-                    prefetch_l2(w + ((int64_t)strip * P.chunks + kc) * STRIP, STRIP);
-            } else if (lane == 0) {
-                prefetch_l2(w + ((int64_t)t.rt * P.chunks + kc) * Q4_UNIT_BYTES, Q4_UNIT_BYTES);
+            if (elect_one()) {
+                if (GROUPED) {
+                    for (int q = 0; q < 4; q++)
+                        if ((4 * t.rt + q) * STRIP_ROWS < P.N)
+                            prefetch_l2(w + ((int64_t)(4 * t.rt + q) * P.chunks + kc) * STRIP, STRIP);
+                } else {
+                    prefetch_l2(w + ((int64_t)t.rt * P.chunks + kc) * Q4_UNIT_BYTES, Q4_UNIT_BYTES);
+                }
             }
         };
         auto publish = [&](int i, const Item &t) {
@@ -362,16 +372,20 @@ __global__ void __launch_bounds__(THREADS, 1) mmq_id_kernel(const __grid_constan
                     ok = false;
                     break;
                 }
-                if (lane == 0) mbar_expect_tx(ufull + 8 * us, GROUPED ? strips * STRIP : Q4_UNIT_BYTES);
-                __syncwarp();
-                if (GROUPED) {
-                    if (lane < strips)
-                        bulk_g2s(sbase + OFF_U + us * U_SLOT + lane * STRIP,
-                                 w + ((int64_t)(4 * t.rt + lane) * P.chunks + kc) * STRIP, STRIP, ufull + 8 * us);
-                } else if (lane == 0) {
-                    bulk_g2s(sbase + OFF_U + us * U_SLOT, w + ((int64_t)t.rt * P.chunks + kc) * Q4_UNIT_BYTES,
-                             Q4_UNIT_BYTES, ufull + 8 * us);
+                if (elect_one()) {
+                    const uint32_t dst = sbase + OFF_U + us * U_SLOT;
+                    if (GROUPED) {
+                        mbar_expect_tx(ufull + 8 * us, strips * STRIP);
+                        for (int q = 0; q < 4; q++)
+                            if (q < strips)
+                                bulk_g2s(dst + q * STRIP, w + ((int64_t)(4 * t.rt + q) * P.chunks + kc) * STRIP, STRIP,
+                                         ufull + 8 * us);
+                    } else {
+                        mbar_expect_tx(ufull + 8 * us, Q4_UNIT_BYTES);
+                        bulk_g2s(dst, w + ((int64_t)t.rt * P.chunks + kc) * Q4_UNIT_BYTES, Q4_UNIT_BYTES, ufull + 8 * us);
+                    }
                 }
+                __syncwarp();
                 gu++;
                 // keep the weights PF stages ahead (in this item or the next one) on their way into L2
                 if (kc + PF < P.chunks)
@@ -400,7 +414,7 @@ __global__ void __launch_bounds__(THREADS, 1) mmq_id_kernel(const __grid_constan
                     ok = false;
                     break;
                 }
-                if (lane == 0) {
+                if (elect_one()) {
                     mbar_expect_tx(full_b + 8 * bs, (uint32_t)(boxes * BOX_ROWS * KC * 2));
                     for (int b = 0; b < boxes; b++)
                         tma_2d(sbase + bs * B_SLOT + b * (BOX_ROWS * KC * 2), &a.bmap, k0, first + b * BOX_ROWS,
@@ -411,57 +425,60 @@ __global__ void __launch_bounds__(THREADS, 1) mmq_id_kernel(const __grid_constan
         }
         for (uint32_t x = gb > NB ? gb - NB : 0; x < gb; x++)   // as above: all copies have landed
             if (!warp_wait(full_b + 8 * (x % NB), (x / NB) & 1u)) break;
-    } else if (warp == 1) {   // ---------------- MMA issue (one thread)
+    } else if (warp == 1) {   // ---------------- MMA issue (one elected thread, always the same)
         uint32_t g = 0, gb = 0;         // A stages and activation slots consumed
         uint32_t uses[2] = {0, 0};      // of the accumulator halves
         int side = 0;                   // the half that the next narrow item takes
-        bool ok = lane == 0;
+        bool ok = true;
         for (int i = 0; i < mine && ok; i++) {
-            if (!mbar_wait(info_full + 8 * (i & 1), (i >> 1) & 1)) break;
+            if (!await_info(i)) break;
             const int n = info[i & 1].n, K = a.p[info[i & 1].j].K, nkc = (K + SK - 1) / SK;
-            mbar_arrive(info_empty + 8 * (i & 1));
+            release_info(i);
             const uint32_t idesc = mma_idesc((n + 15) & ~15);
             const bool wide = n > HALF;
             const int h = wide ? 0 : side;
-            if (uses[h] > 0) ok = mbar_wait(acc_empty + 8 * h, (uses[h] - 1) & 1u);
-            if (wide && uses[1] > 0) ok = ok && mbar_wait(acc_empty + 8, (uses[1] - 1) & 1u);
+            if (uses[h] > 0) ok = warp_wait(acc_empty + 8 * h, (uses[h] - 1) & 1u);
+            if (wide && uses[1] > 0) ok = ok && warp_wait(acc_empty + 8, (uses[1] - 1) & 1u);
             if (!ok) break;
             const uint32_t acc = tmem + h * HALF;
             tc_fence_after();
             for (int kc = 0; kc < nkc && ok; kc++, g++) {
                 const uint32_t s = g % NS, at = tmem + A_TMEM + s * A_COLS;
-                ok = mbar_wait(full_a + 8 * s, (g / NS) & 1u);
+                ok = warp_wait(full_a + 8 * s, (g / NS) & 1u);
 #pragma unroll
                 for (int half = 0; half < 2; half++) {
                     const int left = K - kc * SK - half * KC;   // nothing past K enters the sum
                     if (left <= 0 || !ok) break;
                     const uint32_t bs = gb % NB;
-                    ok = mbar_wait(full_b + 8 * bs, (gb / NB) & 1u);
+                    ok = warp_wait(full_b + 8 * bs, (gb / NB) & 1u);
                     if (!ok) break;
                     tc_fence_after();
+                    if (elect_one()) {
 #pragma unroll
-                    for (int ks = 0; ks < KC / 16; ks++)
-                        if (16 * ks < left)
-                            tc_mma(acc, at + 32 * half + 8 * ks, sdesc(sbase + bs * B_SLOT + 32 * ks), idesc,
-                                   (kc | half | ks) != 0);
-                    tc_commit(empty_b + 8 * bs);
+                        for (int ks = 0; ks < KC / 16; ks++)
+                            if (16 * ks < left)
+                                tc_mma(acc, at + 32 * half + 8 * ks, sdesc(sbase + bs * B_SLOT + 32 * ks), idesc,
+                                       (kc | half | ks) != 0);
+                        tc_commit(empty_b + 8 * bs);
+                        if (half == 1 || left <= KC) tc_commit(empty_a + 8 * s);
+                    }
+                    __syncwarp();
                     gb++;
                 }
-                if (ok) tc_commit(empty_a + 8 * s);
             }
             if (!ok) break;
-            tc_commit(acc_full + 8 * h);
-            uses[h]++;
-            if (wide) {
-                tc_commit(acc_full + 8);
-                uses[1]++;
+            if (elect_one()) {
+                tc_commit(acc_full + 8 * h);
+                if (wide) tc_commit(acc_full + 8);
             }
+            __syncwarp();
+            uses[h]++;
+            if (wide) uses[1]++;
             side = wide ? 0 : side ^ 1;
         }
-        if (lane == 0) {
-            tc_commit(mma_done);   // every MMA issued here is complete before the tensor memory is freed
-            mbar_wait(mma_done, 0u);
-        }
+        if (elect_one()) tc_commit(mma_done);   // every MMA issued here is complete before the tensor memory is freed
+        __syncwarp();
+        warp_wait(mma_done, 0u);
     } else if (warp < EPI0) {   // ---------------- A conversion into tensor memory
         // lanes 32 (warp % 4) .. +31 of tensor memory are tile rows 32 (warp % 4) ..; a group of four
         // warps takes every NS-th stage and always the same A stage
