@@ -13,25 +13,30 @@
 // order (in the caller's workspace), so that an expert's pairs are consecutive rows and a pass is a
 // plain tile; then mmq_id_kernel.
 //
-// Work items are (expert, 128-row weight tile, pass): a pass is up to 256 of the expert's pairs. An
-// expert with c pairs has ceil(c / 256) passes of nearly equal size, so that no pass is a small
+// Work items are (expert, 128-row weight tile, pass): a pass is up to 128 of the expert's pairs. An
+// expert with c pairs has ceil(c / 128) passes of nearly equal size, so that no pass is a small
 // remainder, and a pass of n pairs runs MMAs of N = n rounded up to 16 columns: the tensor work follows
 // the ragged counts. Items are taken round-robin, passes fastest, so that the CTAs that run at one
 // time share weight tiles through L2. Every CTA derives the item list from the counts.
 //
-//   warp 0:       looks the items up one ahead (descriptor and pair list into a two-entry ring) and
-//                 streams the packed weights (stages of 128 rows x 128 K) by bulk copies
+// A stage is 128 K elements: A as 64 tensor-memory columns, B as two 64-column boxes (32 KB); four of
+// them. The accumulator is double (2 x 128 columns): the next item's MMAs run while one is read.
+//   warp 0:       streams the packed weights (one stage's 128 rows x 128 K per slot) by bulk copies
 //   warp 1:       allocates tensor memory, issues the MMAs (one elected thread)
-//   warps 2-17:   packed nibbles -> binary16 A stages in tensor memory; four groups of four warps take
-//                 turns at the stages
+//   warps 2-17:   packed nibbles -> binary16 A stages; four groups of four warps take turns at the
+//                 stages, since one stage takes a group about 620 cycles and its waits
 //   warps 18-25:  accumulator -> bfloat16 rows, scattered to the pairs' output rows
 //   warp 26:      the pass's activation rows by tensor copies, 64 K columns x 32 rows each
-// A pass of up to 128 pairs uses one half of the accumulator's 256 columns, so that the next item's
-// MMAs run while it is read; a wider one uses both.
+//   warp 27:      looks the items up, up to four ahead of the epilogue (a descriptor and the pass's pair
+//                 list per item), so that no other warp waits for the plan's words
+// A wait on a barrier costs 90 to 200 cycles even when its phase is complete, so a stage has one full
+// barrier (converters and activation bytes together) and one empty one, and the MMA warp looks at the
+// next stage's before it issues this one's MMAs. With separate barriers for A and for each half of B
+// the MMA warp took 1450 cycles a stage however few columns it had: 512-row gate/up 177 us.
 // The conversion of the weights is that of the dense prefill kernel (k_mmq.cu).
-// Measured and dropped: gathering the rows out of the unsorted image, by four-row tensor copies (their
-// operands are uniform per instruction, so the rows of a warp go one by one, about 85 cycles each:
-// 4096-row gate/up 1338 us) and by 16-byte asynchronous copies of six warps (685 us).
+// Measured and dropped: gathering the rows out of the unsorted image, by four-row tensor copies (issued
+// lane by lane, about 85 cycles each: 4096-row gate/up 1338 us) and by 16-byte asynchronous copies of
+// six warps (685 us).
 
 #include <cuda_bf16.h>
 
@@ -44,44 +49,46 @@ namespace {
 constexpr int MAX_PROJ = 8;
 constexpr int MAX_E = 1024;
 constexpr int TM = 128;              // weight rows per item (MMA M)
-constexpr int TN = 256;              // most pairs of a pass (MMA N)
-constexpr int KC = 64;               // K elements of one activation slot (a 128-byte swizzle row)
-constexpr int SK = 128;              // K elements per weight stage
-constexpr int NS = 4;                // A stages in tensor memory, one per converter group
-constexpr int NB = 5;                // activation slots
+constexpr int TN = 128;              // most pairs of a pass (MMA N)
+constexpr int KC = 64;               // K elements of one activation box (a 128-byte swizzle row)
+constexpr int SK = 128;              // K elements per stage
+constexpr int NS = 4;                // stages: A in tensor memory, B in shared memory; converter groups
 constexpr int BOX_ROWS = 32;         // rows of one activation copy
-constexpr int NU = NS;               // packed-weight slots: a slot always meets the same converter group
-constexpr int PF = 10;               // stages of weights prefetched into L2 ahead
-constexpr int B_SLOT = TN * KC * 2;  // 32 KB
+constexpr int NU = 8;                // packed-weight slots, a multiple of NS: a slot always meets one group
+constexpr int PF = 12;               // stages of weights prefetched into L2 ahead
+constexpr int B_BOX = TN * KC * 2;   // 16 KB
+constexpr int B_STAGE = TN * SK * 2; // 32 KB
 constexpr int U_SLOT = Q4_UNIT_BYTES;
 constexpr uint32_t A_COLS = SK / 2;
-constexpr uint32_t A_TMEM = TN;      // A stages follow the accumulator
+constexpr uint32_t A_TMEM = 2 * TN;  // A stages follow the two accumulators
 constexpr uint32_t TMEM_COLS = 512;
-constexpr int CONV0 = 2, EPI0 = CONV0 + 4 * NS, N_EPI = 8, ACT_WARP = EPI0 + N_EPI;
-constexpr int HALF = TN / 2;         // accumulator columns of one half
-constexpr int N_READERS = 2 + 4 * NS + N_EPI;   // warps that read an item's descriptor
-constexpr int THREADS = (ACT_WARP + 1) * 32;
+constexpr int CONV0 = 2, EPI0 = CONV0 + 4 * NS, N_EPI = 8, ACT_WARP = EPI0 + N_EPI, ITEM_WARP = ACT_WARP + 1;
+constexpr int THREADS = (ITEM_WARP + 1) * 32;
+constexpr int N_READERS = 3 + 4 * NS + N_EPI;   // warps that read an item's descriptor
+constexpr int NI = 4;                // item descriptors
 static_assert(A_TMEM + NS * A_COLS <= TMEM_COLS, "tensor memory");
 static_assert(4 * strip_unit_bytes(64) <= U_SLOT, "a weight stage fits its slot");
+static_assert(NU % NS == 0, "weight slots");
 
 struct Item {
     int e, j, rt;        // expert, projection, row tile of the projection
     int pass, passes;
 };
 struct Info {            // what the other warps need of an item
-    int j, rt, n, first; // projection, row tile, pairs of the pass and the plan position of the first
+    int e, j, rt;        // expert, projection, row tile of the projection
+    int n, first;        // pairs of the pass, plan position of the first
+    int pad[3];
     int pair[TN];        // their pair numbers, -1 where the plan names none of this bucket
 };
 
-// shared memory: [activation slots][weights][barriers][tensor-memory address, item count][descriptors]
+// shared memory: [activation stages][weights][barriers][tensor-memory address, item count][descriptors]
 // [pass prefix]
-constexpr int OFF_U = NB * B_SLOT;
+constexpr int OFF_U = NS * B_STAGE;
 constexpr int OFF_BAR = OFF_U + NU * U_SLOT;
-// full_a[NS] empty_a[NS] full_b[NB] empty_b[NB] ufull[NU] uempty[NU] acc_full[2] acc_empty[2]
-// info_full[2] info_empty[2] mma_done
-constexpr int N_BARS = 2 * NS + 2 * NB + 2 * NU + 9;
+// full[NS] empty[NS] ufull[NU] uempty[NU] acc_full[2] acc_empty[2] info_full[NI] info_empty[NI] mma_done
+constexpr int N_BARS = 2 * NS + 2 * NU + 2 * NI + 5;
 constexpr int OFF_INFO = (OFF_BAR + N_BARS * 8 + 8 + 15) / 16 * 16;
-constexpr int OFF_PRE = OFF_INFO + 2 * (int)sizeof(Info);
+constexpr int OFF_PRE = OFF_INFO + NI * (int)sizeof(Info);
 constexpr int SMEM_BYTES = OFF_PRE + (MAX_E + 1) * 4 + 1024;   // + slack to align the base to 1024
 static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
 
@@ -123,14 +130,14 @@ __device__ __forceinline__ Item item_of(const IdArgs &a, const int *pre, int tau
     t.rt = r - a.p[t.j].rt_begin;
     return t;
 }
-// Pairs of the item's pass: `first` is their position in the plan, n (1..256) their number.
+// Pairs of the item's pass: `first` is their position in the plan, n (1..TN) their number.
 struct Pairs {
     int64_t first;
     int n;
 };
 __device__ __forceinline__ Pairs pairs_of(const IdArgs &a, const Item &t) {
     const int cnt = clamped_count(a, t.e);
-    const int tn = ((cnt + t.passes - 1) / t.passes + 15) & ~15;   // <= 256: passes = ceil(cnt / 256)
+    const int tn = ((cnt + t.passes - 1) / t.passes + 15) & ~15;   // <= TN: passes = ceil(cnt / TN)
     const int start = t.pass * tn;
     return {(int64_t)__ldg(a.offsets + t.e) + start, min(tn, cnt - start)};
 }
@@ -148,6 +155,16 @@ __device__ __forceinline__ bool elect_one() {
     uint32_t p;
     asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
     return p != 0;
+}
+// Whether the phase is complete, without waiting.
+__device__ __forceinline__ bool mbar_test(uint32_t a, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(a), "r"(parity)
+        : "memory");
+    return ok != 0;
 }
 // A whole warp's wait: every lane gets the same answer.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
@@ -209,8 +226,8 @@ __device__ __forceinline__ uint4 load_words(const uint8_t *unit, int quad, int j
     return *reinterpret_cast<const uint4 *>(unit + quad * strip_unit_bytes(G) + jb * 512 + lane * 16);
 }
 
-// grid (plan positions, ceil(4 kb / 256)): CTA (pos, y) writes row pos of the activations from the image
-// row of the pair there; thread j takes word j & 3 of block 64 y + j / 4 (as dequant_b_kernel).
+// A warp per plan position: row pos of the activations from the image row of the pair there, eight
+// blocks per step (lane l: word l & 3 of block l / 4).
 __global__ void __launch_bounds__(256) dequant_pairs_kernel(const int8_t *__restrict__ qs,
                                                             const uint16_t *__restrict__ d, int64_t row_blocks,
                                                             const int32_t *__restrict__ offsets,
@@ -218,12 +235,14 @@ __global__ void __launch_bounds__(256) dequant_pairs_kernel(const int8_t *__rest
                                                             int per_pair, int kb, __half *__restrict__ B) {
     pdl_trigger();
     pdl_wait();
-    const int pos = blockIdx.x, w = threadIdx.x & 3, b = blockIdx.y * 64 + (threadIdx.x >> 2);
-    if (b >= kb || pos >= __ldg(offsets + E)) return;   // positions past the plan hold no pair
+    const int pos = blockIdx.x * 8 + (threadIdx.x >> 5), w = threadIdx.x & 3, b0 = (threadIdx.x & 31) >> 2;
+    if (pos >= pairs || pos >= __ldg(offsets + E)) return;   // positions past the plan hold no pair
     const int p = __ldg(items + pos);
     if (p < 0 || p >= pairs) return;
-    const int64_t row = per_pair ? p : p / k;
-    dequant_word(qs, d, row * row_blocks + b, w, B + ((int64_t)pos * kb + b) * QB);
+    const int64_t first = (per_pair ? p : p / k) * row_blocks;
+    __half *dst = B + (int64_t)pos * kb * QB;
+#pragma unroll 4
+    for (int b = b0; b < kb; b += 8) dequant_word(qs, d, first + b, w, dst + (int64_t)b * QB);
 }
 
 template <int WT>
@@ -233,10 +252,9 @@ __global__ void __launch_bounds__(THREADS, 1) mmq_id_kernel(const __grid_constan
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     const uint32_t sbase = smem_u32(smem);
-    const uint32_t full_a = sbase + OFF_BAR, empty_a = full_a + NS * 8, full_b = empty_a + NS * 8,
-                   empty_b = full_b + NB * 8, ufull = empty_b + NB * 8, uempty = ufull + NU * 8,
+    const uint32_t full = sbase + OFF_BAR, empty = full + NS * 8, ufull = empty + NS * 8, uempty = ufull + NU * 8,
                    acc_full = uempty + NU * 8, acc_empty = acc_full + 16, info_full = acc_empty + 16,
-                   info_empty = info_full + 16, mma_done = info_empty + 16;
+                   info_empty = info_full + 8 * NI, mma_done = info_empty + 8 * NI;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + OFF_BAR + N_BARS * 8);
     int *n_items = reinterpret_cast<int *>(tmem_slot + 1);
     Info *info = reinterpret_cast<Info *>(smem + OFF_INFO);
@@ -247,12 +265,8 @@ __global__ void __launch_bounds__(THREADS, 1) mmq_id_kernel(const __grid_constan
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < NS; s++) {
-            mbar_init(full_a + 8 * s, 4);     // the converter warps of its group
-            mbar_init(empty_a + 8 * s, 1);    // the MMA commit
-        }
-        for (int b = 0; b < NB; b++) {
-            mbar_init(full_b + 8 * b, 1);     // the activation warp, with the bytes
-            mbar_init(empty_b + 8 * b, 1);    // the MMA commit
+            mbar_init(full + 8 * s, 5);      // its group's four converter warps; the activation warp, with the bytes
+            mbar_init(empty + 8 * s, 1);     // the MMA commit
         }
         for (int u = 0; u < NU; u++) {
             mbar_init(ufull + 8 * u, 1);      // the weight warp, with the bytes
@@ -261,8 +275,10 @@ __global__ void __launch_bounds__(THREADS, 1) mmq_id_kernel(const __grid_constan
         for (int h = 0; h < 2; h++) {
             mbar_init(acc_full + 8 * h, 1);         // the MMA commit after an item's last stage
             mbar_init(acc_empty + 8 * h, N_EPI);    // the epilogue warps, once they have read it
-            mbar_init(info_full + 8 * h, 1);        // the weight warp
-            mbar_init(info_empty + 8 * h, N_READERS);
+        }
+        for (int i = 0; i < NI; i++) {
+            mbar_init(info_full + 8 * i, 1);        // the item warp
+            mbar_init(info_empty + 8 * i, N_READERS);
         }
         mbar_init(mma_done, 1);               // the MMA thread's last commit
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -277,7 +293,7 @@ __global__ void __launch_bounds__(THREADS, 1) mmq_id_kernel(const __grid_constan
     pdl_wait();   // the plan and the binary16 rows come from the kernels before
     if (warp == 0) {
         // prefix of the experts' pass counts: lane l sums experts l * per .. l * per + per - 1. Plans of
-        // this bucket have at most pairs / 256 + E passes; counts with more are refused (fault bit 1).
+        // this bucket have at most pairs / TN + E passes; counts with more are refused (fault bit 1).
         const int per = (a.E + 31) / 32, e0 = min(a.E, lane * per), e1 = min(a.E, e0 + per);
         int64_t sum = 0;
         for (int e = e0; e < e1; e++) sum += (clamped_count(a, e) + TN - 1) / TN;
@@ -306,42 +322,29 @@ __global__ void __launch_bounds__(THREADS, 1) mmq_id_kernel(const __grid_constan
     const uint32_t tmem = *tmem_slot;
     const int items = *n_items;
 
-    // Item i of this CTA (items blockIdx.x + i * gridDim.x): entry i & 1 of the descriptor ring. A
+    // Item i of this CTA (items blockIdx.x + i * gridDim.x): entry i % NI of the descriptor ring. A
     // warp waits for it, and arrives on info_empty when it needs it no more.
-    auto await_info = [&](int i) { return warp_wait(info_full + 8 * (i & 1), (i >> 1) & 1); };
+    auto await_info = [&](int i) { return warp_wait(info_full + 8 * (i % NI), (i / NI) & 1); };
     auto release_info = [&](int i) {
         __syncwarp();
-        if (lane == 0) mbar_arrive(info_empty + 8 * (i & 1));
+        if (lane == 0) mbar_arrive(info_empty + 8 * (i % NI));
     };
     const int mine = items > (int)blockIdx.x ? (items - (int)blockIdx.x + G - 1) / G : 0;   // this CTA's items
 
-    if (warp == 0) {   // ---------------- items and weights
-        uint32_t gu = 0;   // weight stages issued by this CTA
-        bool ok = true;
-        // stage kc's weights of an item into L2
-        auto prefetch = [&](const Item &t, int kc) {
-            const IdProj &P = a.p[t.j];
-            const uint8_t *w = P.w + t.e * P.expert_bytes;
-            if (elect_one()) {
-                if (GROUPED) {
-                    for (int q = 0; q < 4; q++)
-                        if ((4 * t.rt + q) * STRIP_ROWS < P.N)
-                            prefetch_l2(w + ((int64_t)(4 * t.rt + q) * P.chunks + kc) * STRIP, STRIP);
-                } else {
-                    prefetch_l2(w + ((int64_t)t.rt * P.chunks + kc) * Q4_UNIT_BYTES, Q4_UNIT_BYTES);
-                }
-            }
-        };
-        auto publish = [&](int i, const Item &t) {
-            if (i >= 2 && !warp_wait(info_empty + 8 * (i & 1), ((i >> 1) - 1) & 1)) return false;
-            Info &f = info[i & 1];
+    if (warp == ITEM_WARP) {   // ---------------- items
+        for (int i = 0; i < mine; i++) {
+            const Item t = item_of(a, pre, blockIdx.x + i * G);
             const Pairs pr = pairs_of(a, t);
+            int p[TN / 32];
 #pragma unroll
-            for (int j = 0; j < TN / 32; j++) {
-                const int c = 32 * j + lane;
-                f.pair[c] = c < pr.n ? pair_at(a, pr.first + c) : -1;
-            }
+            for (int j = 0; j < TN / 32; j++)
+                p[j] = 32 * j + lane < pr.n ? pair_at(a, pr.first + 32 * j + lane) : -1;
+            if (i >= NI && !warp_wait(info_empty + 8 * (i % NI), ((i / NI) - 1) & 1)) break;
+            Info &f = info[i % NI];
+#pragma unroll
+            for (int j = 0; j < TN / 32; j++) f.pair[32 * j + lane] = p[j];
             if (lane == 0) {
+                f.e = t.e;
                 f.j = t.j;
                 f.rt = t.rt;
                 f.n = pr.n;
@@ -349,23 +352,30 @@ __global__ void __launch_bounds__(THREADS, 1) mmq_id_kernel(const __grid_constan
                 f.first = (int)(pr.first < -TN ? -TN : (pr.first > a.pairs ? a.pairs : pr.first));
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(info_full + 8 * (i & 1));
-            return true;
-        };
-        Item next = {};
-        if (mine > 0) {
-            next = item_of(a, pre, blockIdx.x);
-            ok = publish(0, next);
-            for (int kc = 0; kc < PF && kc < a.p[next.j].chunks; kc++) prefetch(next, kc);
+            if (lane == 0) mbar_arrive(info_full + 8 * (i % NI));
         }
+    } else if (warp == 0) {   // ---------------- weights
+        uint32_t gu = 0;   // weight stages issued by this CTA
+        bool ok = true;
         for (int i = 0; i < mine && ok; i++) {
-            const Item t = next;
-            const IdProj &P = a.p[t.j];
-            const bool more = i + 1 < mine;
-            if (more) next = item_of(a, pre, blockIdx.x + (i + 1) * G);
-            const int next_chunks = more ? a.p[next.j].chunks : 0;
-            const uint8_t *w = P.w + t.e * P.expert_bytes;
-            const int strips = GROUPED ? min(4, (P.N - t.rt * TM + STRIP_ROWS - 1) / STRIP_ROWS) : 0;
+            if (!await_info(i)) break;
+            const Info &f = info[i % NI];
+            const IdProj &P = a.p[f.j];
+            const uint8_t *w = P.w + f.e * P.expert_bytes;
+            const int rt = f.rt, strips = GROUPED ? min(4, (P.N - rt * TM + STRIP_ROWS - 1) / STRIP_ROWS) : 0;
+            release_info(i);
+            // stage kc's weights into L2, PF stages ahead of their copy
+            auto prefetch = [&](int kc) {
+                if (elect_one()) {
+                    if (GROUPED) {
+                        for (int q = 0; q < 4; q++)
+                            if (q < strips) prefetch_l2(w + ((int64_t)(4 * rt + q) * P.chunks + kc) * STRIP, STRIP);
+                    } else {
+                        prefetch_l2(w + ((int64_t)rt * P.chunks + kc) * Q4_UNIT_BYTES, Q4_UNIT_BYTES);
+                    }
+                }
+            };
+            for (int kc = NU; kc < PF && kc < P.chunks; kc++) prefetch(kc);
             for (int kc = 0; kc < P.chunks; kc++) {
                 const uint32_t us = gu % NU;
                 if (gu >= NU && !warp_wait(uempty + 8 * us, ((gu / NU) - 1) & 1u)) {
@@ -378,22 +388,17 @@ __global__ void __launch_bounds__(THREADS, 1) mmq_id_kernel(const __grid_constan
                         mbar_expect_tx(ufull + 8 * us, strips * STRIP);
                         for (int q = 0; q < 4; q++)
                             if (q < strips)
-                                bulk_g2s(dst + q * STRIP, w + ((int64_t)(4 * t.rt + q) * P.chunks + kc) * STRIP, STRIP,
+                                bulk_g2s(dst + q * STRIP, w + ((int64_t)(4 * rt + q) * P.chunks + kc) * STRIP, STRIP,
                                          ufull + 8 * us);
                     } else {
                         mbar_expect_tx(ufull + 8 * us, Q4_UNIT_BYTES);
-                        bulk_g2s(dst, w + ((int64_t)t.rt * P.chunks + kc) * Q4_UNIT_BYTES, Q4_UNIT_BYTES, ufull + 8 * us);
+                        bulk_g2s(dst, w + ((int64_t)rt * P.chunks + kc) * Q4_UNIT_BYTES, Q4_UNIT_BYTES, ufull + 8 * us);
                     }
                 }
                 __syncwarp();
                 gu++;
-                // keep the weights PF stages ahead (in this item or the next one) on their way into L2
-                if (kc + PF < P.chunks)
-                    prefetch(t, kc + PF);
-                else if (kc + PF - P.chunks < next_chunks)
-                    prefetch(next, kc + PF - P.chunks);
+                if (kc + PF < P.chunks) prefetch(kc + PF);
             }
-            if (ok && more) ok = publish(i + 1, next);
         }
         // Every copy this warp issued has landed before the CTA can exit, also after a wait above ran
         // out (a barrier whose phase completed long ago passes at once; a wait that runs out here ends
@@ -401,80 +406,61 @@ __global__ void __launch_bounds__(THREADS, 1) mmq_id_kernel(const __grid_constan
         for (uint32_t x = gu > NU ? gu - NU : 0; x < gu; x++)
             if (!warp_wait(ufull + 8 * (x % NU), (x / NU) & 1u)) break;
     } else if (warp == ACT_WARP) {   // ---------------- activations
-        uint32_t gb = 0;   // slots filled by this CTA
+        uint32_t g = 0;   // stages filled by this CTA
         bool ok = true;
         for (int i = 0; i < mine && ok; i++) {
             if (!await_info(i)) break;
-            const Info &f = info[i & 1];
-            const int K = a.p[f.j].K, first = f.first, boxes = (((f.n + 15) & ~15) + BOX_ROWS - 1) / BOX_ROWS;
+            const Info &f = info[i % NI];
+            const int K = a.p[f.j].K, first = f.first, rows = ((f.n + 15) & ~15), boxes = (rows + BOX_ROWS - 1) / BOX_ROWS;
             release_info(i);
-            for (int k0 = 0; k0 < K; k0 += KC, gb++) {
-                const uint32_t bs = gb % NB;
-                if (gb >= NB && !warp_wait(empty_b + 8 * bs, ((gb / NB) - 1) & 1u)) {
+            for (int k0 = 0; k0 < K; k0 += SK, g++) {
+                const uint32_t s = g % NS, dst = sbase + s * B_STAGE, bar = full + 8 * s;
+                if (g >= NS && !warp_wait(empty + 8 * s, ((g / NS) - 1) & 1u)) {
                     ok = false;
                     break;
                 }
+                const int halves = K - k0 > KC ? 2 : 1;
                 if (elect_one()) {
-                    mbar_expect_tx(full_b + 8 * bs, (uint32_t)(boxes * BOX_ROWS * KC * 2));
-                    for (int b = 0; b < boxes; b++)
-                        tma_2d(sbase + bs * B_SLOT + b * (BOX_ROWS * KC * 2), &a.bmap, k0, first + b * BOX_ROWS,
-                               full_b + 8 * bs);
+                    mbar_expect_tx(bar, (uint32_t)(halves * boxes * BOX_ROWS * KC * 2));
+                    for (int h = 0; h < halves; h++)
+                        for (int b = 0; b < boxes; b++)
+                            tma_2d(dst + h * B_BOX + b * (BOX_ROWS * KC * 2), &a.bmap, k0 + h * KC, first + b * BOX_ROWS, bar);
                 }
                 __syncwarp();
             }
         }
-        for (uint32_t x = gb > NB ? gb - NB : 0; x < gb; x++)   // as above: all copies have landed
-            if (!warp_wait(full_b + 8 * (x % NB), (x / NB) & 1u)) break;
+        // As for the weights: every copy has landed, and then the stages' MMAs are done. A stage whose
+        // converters stopped early never completes; its wait runs out.
+        for (uint32_t x = g > NS ? g - NS : 0; x < g; x++)
+            if (!warp_wait(full + 8 * (x % NS), (x / NS) & 1u)) break;
     } else if (warp == 1) {   // ---------------- MMA issue (one elected thread, always the same)
-        uint32_t g = 0, gb = 0;         // A stages and activation slots consumed
-        uint32_t uses[2] = {0, 0};      // of the accumulator halves
-        int side = 0;                   // the half that the next narrow item takes
-        bool ok = true;
+        uint32_t g = 0;   // stages consumed
+        bool ok = true, ready = false;
         for (int i = 0; i < mine && ok; i++) {
             if (!await_info(i)) break;
-            const int n = info[i & 1].n, K = a.p[info[i & 1].j].K, nkc = (K + SK - 1) / SK;
+            const int n = info[i % NI].n, K = a.p[info[i % NI].j].K, nkc = (K + SK - 1) / SK;
             release_info(i);
-            const uint32_t idesc = mma_idesc((n + 15) & ~15);
-            const bool wide = n > HALF;
-            const int h = wide ? 0 : side;
-            if (uses[h] > 0) ok = warp_wait(acc_empty + 8 * h, (uses[h] - 1) & 1u);
-            if (wide && uses[1] > 0) ok = ok && warp_wait(acc_empty + 8, (uses[1] - 1) & 1u);
-            if (!ok) break;
-            const uint32_t acc = tmem + h * HALF;
-            tc_fence_after();
-            for (int kc = 0; kc < nkc && ok; kc++, g++) {
-                const uint32_t s = g % NS, at = tmem + A_TMEM + s * A_COLS;
-                ok = warp_wait(full_a + 8 * s, (g / NS) & 1u);
-#pragma unroll
-                for (int half = 0; half < 2; half++) {
-                    const int left = K - kc * SK - half * KC;   // nothing past K enters the sum
-                    if (left <= 0 || !ok) break;
-                    const uint32_t bs = gb % NB;
-                    ok = warp_wait(full_b + 8 * bs, (gb / NB) & 1u);
-                    if (!ok) break;
-                    tc_fence_after();
-                    if (elect_one()) {
-#pragma unroll
-                        for (int ks = 0; ks < KC / 16; ks++)
-                            if (16 * ks < left)
-                                tc_mma(acc, at + 32 * half + 8 * ks, sdesc(sbase + bs * B_SLOT + 32 * ks), idesc,
-                                       (kc | half | ks) != 0);
-                        tc_commit(empty_b + 8 * bs);
-                        if (half == 1 || left <= KC) tc_commit(empty_a + 8 * s);
-                    }
-                    __syncwarp();
-                    gb++;
+            const uint32_t idesc = mma_idesc((n + 15) & ~15), acc = tmem + (i & 1) * TN;
+            if (i >= 2 && !warp_wait(acc_empty + 8 * (i & 1), ((i >> 1) - 1) & 1)) break;
+            for (int kc = 0; kc < nkc; kc++, g++) {
+                const uint32_t s = g % NS, at = tmem + A_TMEM + s * A_COLS, bt = sbase + s * B_STAGE;
+                if (!ready && !warp_wait(full + 8 * s, (g / NS) & 1u)) {
+                    ok = false;
+                    break;
                 }
+                ready = __all_sync(0xffffffffu, mbar_test(full + 8 * ((g + 1) % NS), ((g + 1) / NS) & 1u));
+                tc_fence_after();
+                const int steps = min(SK, K - kc * SK) / 16;   // nothing past K enters the sum
+                if (elect_one()) {
+#pragma unroll
+                    for (int ks = 0; ks < SK / 16; ks++)
+                        if (ks < steps)
+                            tc_mma(acc, at + 8 * ks, sdesc(bt + (ks >> 2) * B_BOX + 32 * (ks & 3)), idesc, (kc | ks) != 0);
+                    tc_commit(empty + 8 * s);
+                    if (kc == nkc - 1) tc_commit(acc_full + 8 * (i & 1));
+                }
+                __syncwarp();
             }
-            if (!ok) break;
-            if (elect_one()) {
-                tc_commit(acc_full + 8 * h);
-                if (wide) tc_commit(acc_full + 8);
-            }
-            __syncwarp();
-            uses[h]++;
-            if (wide) uses[1]++;
-            side = wide ? 0 : side ^ 1;
         }
         if (elect_one()) tc_commit(mma_done);   // every MMA issued here is complete before the tensor memory is freed
         __syncwarp();
@@ -488,14 +474,17 @@ __global__ void __launch_bounds__(THREADS, 1) mmq_id_kernel(const __grid_constan
         bool ok = true;
         for (int i = 0; i < mine && ok; i++) {
             if (!await_info(i)) break;
-            const uint32_t nkc = a.p[info[i & 1].j].chunks;
+            const uint32_t nkc = a.p[info[i % NI].j].chunks;
             release_info(i);
             for (uint32_t g = g0 + ((group - g0) & (NS - 1)); g < g0 + nkc; g += NS, use++) {
-                ok = warp_wait(ufull + 8 * group, use & 1u);
-                if (ok && use > 0) ok = warp_wait(empty_a + 8 * group, (use - 1) & 1u);
+                const uint32_t us = g % NU;
+                // both looks first, so that their latencies overlap
+                const bool have = mbar_test(ufull + 8 * us, (g / NU) & 1u), free_a = use == 0 || mbar_test(empty + 8 * group, (use - 1) & 1u);
+                ok = (__all_sync(0xffffffffu, have) || warp_wait(ufull + 8 * us, (g / NU) & 1u)) &&
+                     (__all_sync(0xffffffffu, free_a) || warp_wait(empty + 8 * group, (use - 1) & 1u));
                 if (!ok) break;
                 tc_fence_after();
-                const uint8_t *unit = smem + OFF_U + group * U_SLOT;
+                const uint8_t *unit = smem + OFF_U + us * U_SLOT;
 #pragma unroll
                 for (int jb = 0; jb < 4; jb++) {
                     const uint4 wv = load_words<WT>(unit, quad, jb, lane);
@@ -519,58 +508,48 @@ __global__ void __launch_bounds__(THREADS, 1) mmq_id_kernel(const __grid_constan
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {   // one arrival per warp: a lane's arrivals on one barrier go one by one
-                    mbar_arrive(full_a + 8 * group);
-                    mbar_arrive(uempty + 8 * group);
+                    mbar_arrive(full + 8 * group);
+                    mbar_arrive(uempty + 8 * us);
                 }
             }
             g0 += nkc;
         }
     } else {   // ---------------- epilogue (accumulator lane = weight row, column = pair)
         const int quad = warp & 3, c0 = ((warp - EPI0) >> 2) * 64, odd = lane & 1;
-        uint32_t uses = 0;   // bit h: parity of the uses of accumulator half h
-        int side = 0;
-        bool ok = true;
-        for (int i = 0; i < mine && ok; i++) {
+        for (int i = 0; i < mine; i++) {
             if (!await_info(i)) break;
-            const Info &f = info[i & 1];
+            const Info &f = info[i % NI];
             const IdProj &P = a.p[f.j];
-            const int all = f.n, row = f.rt * TM + quad * 32 + (lane & ~1);
-            const bool wide = all > HALF;
+            const int n = f.n - c0, row = f.rt * TM + quad * 32 + (lane & ~1);   // n: pairs here and past
             const bool two = row + 1 < P.N && ((reinterpret_cast<uintptr_t>(P.y) | (uintptr_t)(P.y_stride * 2)) & 3) == 0;
             uint16_t *yr = P.y + row;
-            for (int h = wide ? 0 : side, end = wide ? 2 : side + 1; h < end; h++) {
-                ok = warp_wait(acc_full + 8 * h, (uses >> h) & 1u);
-                if (!ok) break;
-                uses ^= 1u << h;
-                tc_fence_after();
-                const int from = c0 + (wide ? HALF * h : 0), n = all - from;   // the first pair here, pairs here and past
-                const uint32_t taddr = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(h * HALF + c0);
-                uint32_t v[32];
+            if (!warp_wait(acc_full + 8 * (i & 1), (i >> 1) & 1)) break;
+            tc_fence_after();
+            const uint32_t taddr = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)((i & 1) * TN + c0);
+            uint32_t v[32];
 #pragma unroll
-                for (int q = 0; q < 4; q++)
-                    if (n > 16 * q) load_columns(taddr + 16u * q, v + 8 * q);
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(acc_empty + 8 * h);   // read: a later item's MMAs may use it
-                // Rows come two at a time: lanes l and l ^ 1 exchange columns, so that the even lane holds
-                // rows (l, l+1) of column 2k and the odd lane the same rows of column 2k+1: 4-byte stores.
+            for (int q = 0; q < 4; q++)
+                if (n > 16 * q) load_columns(taddr + 16u * q, v + 8 * q);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(acc_empty + 8 * (i & 1));   // read: a later item's MMAs may use it
+            // Rows come two at a time: lanes l and l ^ 1 exchange columns, so that the even lane holds
+            // rows (l, l+1) of column 2k and the odd lane the same rows of column 2k+1: 4-byte stores.
 #pragma unroll
-                for (int kk = 0; kk < 32; kk++) {
-                    if (2 * kk >= n) break;   // uniform
-                    const uint32_t other = __shfl_xor_sync(0xffffffffu, v[kk], 1);
-                    const uint32_t o = odd ? __byte_perm(other, v[kk], 0x7632) : __byte_perm(v[kk], other, 0x5410);
-                    const int id = f.pair[from + 2 * kk + odd];
-                    if (id < 0 || row >= P.N) continue;
-                    uint16_t *dst = yr + id * P.y_stride;
-                    if (two) {
-                        *reinterpret_cast<uint32_t *>(dst) = o;
-                    } else {
-                        dst[0] = (uint16_t)o;
-                        if (row + 1 < P.N) dst[1] = (uint16_t)(o >> 16);
-                    }
+            for (int kk = 0; kk < 32; kk++) {
+                if (2 * kk >= n) break;   // uniform
+                const uint32_t other = __shfl_xor_sync(0xffffffffu, v[kk], 1);
+                const uint32_t o = odd ? __byte_perm(other, v[kk], 0x7632) : __byte_perm(v[kk], other, 0x5410);
+                const int id = f.pair[c0 + 2 * kk + odd];
+                if (id < 0 || row >= P.N) continue;
+                uint16_t *dst = yr + id * P.y_stride;
+                if (two) {
+                    *reinterpret_cast<uint32_t *>(dst) = o;
+                } else {
+                    dst[0] = (uint16_t)o;
+                    if (row + 1 < P.N) dst[1] = (uint16_t)(o >> 16);
                 }
             }
-            side = wide ? 0 : side ^ 1;
             release_info(i);
         }
     }
@@ -619,7 +598,7 @@ qk_status launch_mmq_id(const int8_t *qs, const uint16_t *d, int64_t row_blocks,
                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return fail(QK_ERR_CUDA, "mmq_id: tensor map encoding failed (%d)", (int)r);
-    qk_status st = launch_pdl("mmq_id_dequant", dequant_pairs_kernel, dim3((unsigned)pairs, (unsigned)ceil_div(kb, 64)),
+    qk_status st = launch_pdl("mmq_id_dequant", dequant_pairs_kernel, dim3((unsigned)ceil_div(pairs, 8)),
                               dim3(256), 0, s, qs, d, row_blocks, offsets, items, (int)projs[0].n_experts, pairs, k,
                               (int)per_pair, kb, static_cast<__half *>(ws));
     if (st != QK_OK) return st;
