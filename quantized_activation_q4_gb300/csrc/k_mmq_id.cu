@@ -170,6 +170,14 @@ __device__ __forceinline__ bool mbar_test(uint32_t a, uint32_t parity) {
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity));
 }
+// D += A x B (see tc_mma)
+__device__ __forceinline__ void tc_mma_add(uint32_t tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.eq.u32 p, 0, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(tmem),
+        "r"(a_tmem), "l"(b), "r"(idesc)
+        : "memory");
+}
 // 16 accumulator columns of this warp's lane quarter, packed to bfloat16 pairs of columns
 __device__ __forceinline__ void load_columns(uint32_t taddr, uint32_t *h) {
     uint32_t v[16];
@@ -452,10 +460,18 @@ __global__ void __launch_bounds__(THREADS, 1) mmq_id_kernel(const __grid_constan
                 tc_fence_after();
                 const int steps = min(SK, K - kc * SK) / 16;   // nothing past K enters the sum
                 if (elect_one()) {
+                    // a descriptor's address field counts 16-byte units
+                    const uint64_t bd = sdesc(bt);
+                    tc_mma(acc, at, bd, idesc, kc != 0);
+                    if (steps == SK / 16) {
 #pragma unroll
-                    for (int ks = 0; ks < SK / 16; ks++)
-                        if (ks < steps)
-                            tc_mma(acc, at + 8 * ks, sdesc(bt + (ks >> 2) * B_BOX + 32 * (ks & 3)), idesc, (kc | ks) != 0);
+                        for (int ks = 1; ks < SK / 16; ks++)
+                            tc_mma_add(acc, at + 8 * ks, bd + (uint64_t)((ks >> 2) * (B_BOX / 16) + 2 * (ks & 3)), idesc);
+                    } else {
+#pragma unroll 1
+                        for (int ks = 1; ks < steps; ks++)
+                            tc_mma_add(acc, at + 8 * ks, bd + (uint64_t)((ks >> 2) * (B_BOX / 16) + 2 * (ks & 3)), idesc);
+                    }
                     tc_commit(empty + 8 * s);
                     if (kc == nkc - 1) tc_commit(acc_full + 8 * (i & 1));
                 }
@@ -485,7 +501,7 @@ __global__ void __launch_bounds__(THREADS, 1) mmq_id_kernel(const __grid_constan
                 if (!ok) break;
                 tc_fence_after();
                 const uint8_t *unit = smem + OFF_U + us * U_SLOT;
-#pragma unroll
+#pragma unroll 1   // a short body: the roles share the SM's instruction caches
                 for (int jb = 0; jb < 4; jb++) {
                     const uint4 wv = load_words<WT>(unit, quad, jb, lane);
                     RowHeads<WT> hd;
@@ -526,30 +542,30 @@ __global__ void __launch_bounds__(THREADS, 1) mmq_id_kernel(const __grid_constan
             if (!warp_wait(acc_full + 8 * (i & 1), (i >> 1) & 1)) break;
             tc_fence_after();
             const uint32_t taddr = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)((i & 1) * TN + c0);
-            uint32_t v[32];
-#pragma unroll
-            for (int q = 0; q < 4; q++)
-                if (n > 16 * q) load_columns(taddr + 16u * q, v + 8 * q);
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(acc_empty + 8 * (i & 1));   // read: a later item's MMAs may use it
             // Rows come two at a time: lanes l and l ^ 1 exchange columns, so that the even lane holds
             // rows (l, l+1) of column 2k and the odd lane the same rows of column 2k+1: 4-byte stores.
+#pragma unroll 1   // as above
+            for (int q = 0; 16 * q < min(n, 64); q++) {
+                uint32_t v[8];
+                load_columns(taddr + 16u * q, v);
 #pragma unroll
-            for (int kk = 0; kk < 32; kk++) {
-                if (2 * kk >= n) break;   // uniform
-                const uint32_t other = __shfl_xor_sync(0xffffffffu, v[kk], 1);
-                const uint32_t o = odd ? __byte_perm(other, v[kk], 0x7632) : __byte_perm(v[kk], other, 0x5410);
-                const int id = f.pair[c0 + 2 * kk + odd];
-                if (id < 0 || row >= P.N) continue;
-                uint16_t *dst = yr + id * P.y_stride;
-                if (two) {
-                    *reinterpret_cast<uint32_t *>(dst) = o;
-                } else {
-                    dst[0] = (uint16_t)o;
-                    if (row + 1 < P.N) dst[1] = (uint16_t)(o >> 16);
+                for (int kk = 0; kk < 8; kk++) {
+                    const uint32_t other = __shfl_xor_sync(0xffffffffu, v[kk], 1);
+                    const uint32_t o = odd ? __byte_perm(other, v[kk], 0x7632) : __byte_perm(v[kk], other, 0x5410);
+                    const int id = f.pair[c0 + 16 * q + 2 * kk + odd];
+                    if (id < 0 || row >= P.N) continue;
+                    uint16_t *dst = yr + id * P.y_stride;
+                    if (two) {
+                        *reinterpret_cast<uint32_t *>(dst) = o;
+                    } else {
+                        dst[0] = (uint16_t)o;
+                        if (row + 1 < P.N) dst[1] = (uint16_t)(o >> 16);
+                    }
                 }
             }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(acc_empty + 8 * (i & 1));
             release_info(i);
         }
     }
