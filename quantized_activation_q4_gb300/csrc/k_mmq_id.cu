@@ -13,26 +13,23 @@
 // order (in the caller's workspace), so that an expert's pairs are consecutive rows and a pass is a
 // plain tile; then mmq_id_kernel.
 //
-// Work items are (expert, 128-row weight tile, pass): a pass is up to 128 of the expert's pairs. An
-// expert with c pairs has ceil(c / 128) passes of nearly equal size, so that no pass is a small
+// Work items are (expert, 128-row weight tile, pass): a pass is up to TN (64 or 128) of the expert's pairs. An
+// expert with c pairs has ceil(c / TN) passes of nearly equal size, so that no pass is a small
 // remainder, and a pass of n pairs runs MMAs of N = n rounded up to 16 columns: the tensor work follows
 // the ragged counts. Items are taken round-robin, passes fastest, so that the CTAs that run at one
 // time share weight tiles through L2. Every CTA derives the item list from the counts.
 //
-// A stage is 128 K elements: A as 64 tensor-memory columns, B as two 64-column boxes (32 KB); four of
-// them. The accumulator is double (2 x 128 columns): the next item's MMAs run while one is read.
+// A stage is 128 K elements: A as 64 tensor-memory columns, B as two 64-column boxes. The accumulator is
+// double: the next item's MMAs run while one is read.
 //   warp 0:       streams the packed weights (one stage's 128 rows x 128 K per slot) by bulk copies
 //   warp 1:       allocates tensor memory, issues the MMAs (one elected thread)
-//   warps 2-17:   packed nibbles -> binary16 A stages; four groups of four warps take turns at the
-//                 stages, since one stage takes a group about 620 cycles and its waits
+//   warps 2-17:   packed nibbles -> binary16 A stages, two groups of eight warps in turn
 //   warps 18-25:  accumulator -> bfloat16 rows, scattered to the pairs' output rows
 //   warp 26:      the pass's activation rows by tensor copies, 64 K columns x 32 rows each
 //   warp 27:      looks the items up, up to four ahead of the epilogue (a descriptor and the pass's pair
 //                 list per item), so that no other warp waits for the plan's words
-// A wait on a barrier costs 90 to 200 cycles even when its phase is complete, so a stage has one full
-// barrier (converters and activation bytes together) and one empty one, and the MMA warp looks at the
-// next stage's before it issues this one's MMAs. With separate barriers for A and for each half of B
-// the MMA warp took 1450 cycles a stage however few columns it had: 512-row gate/up 177 us.
+// A wait on a barrier costs 90 to 200 cycles even when its phase is complete, so the MMA warp looks at
+// the barriers of four stages at once, and copies and converters run on rings.
 // The conversion of the weights is that of the dense prefill kernel (k_mmq.cu).
 // Measured and dropped: gathering the rows out of the unsorted image, by four-row tensor copies (issued
 // lane by lane, about 85 cycles each: 4096-row gate/up 1338 us) and by 16-byte asynchronous copies of
@@ -49,26 +46,19 @@ namespace {
 constexpr int MAX_PROJ = 8;
 constexpr int MAX_E = 1024;
 constexpr int TM = 128;              // weight rows per item (MMA M)
-constexpr int TN = 128;              // most pairs of a pass (MMA N)
 constexpr int KC = 64;               // K elements of one activation box (a 128-byte swizzle row)
 constexpr int SK = 128;              // K elements per stage
-constexpr int NS = 4;                // stages: A in tensor memory, B in shared memory; converter groups
 constexpr int BOX_ROWS = 32;         // rows of one activation copy
-constexpr int NU = 8;                // packed-weight slots, a multiple of NS: a slot always meets one group
-constexpr int PF = 12;               // stages of weights prefetched into L2 ahead
-constexpr int B_BOX = TN * KC * 2;   // 16 KB
-constexpr int B_STAGE = TN * SK * 2; // 32 KB
 constexpr int U_SLOT = Q4_UNIT_BYTES;
-constexpr uint32_t A_COLS = SK / 2;
-constexpr uint32_t A_TMEM = 2 * TN;  // A stages follow the two accumulators
+constexpr uint32_t A_COLS = SK / 2;  // tensor-memory columns of an A stage
 constexpr uint32_t TMEM_COLS = 512;
-constexpr int CONV0 = 2, EPI0 = CONV0 + 4 * NS, N_EPI = 8, ACT_WARP = EPI0 + N_EPI, ITEM_WARP = ACT_WARP + 1;
+constexpr int GROUPS = 2, GROUP_WARPS = 8;   // converter groups take turns at the stages
+constexpr int CONV0 = 2, EPI0 = CONV0 + GROUPS * GROUP_WARPS, N_EPI = 8, ACT_WARP = EPI0 + N_EPI, ITEM_WARP = ACT_WARP + 1;
 constexpr int THREADS = (ITEM_WARP + 1) * 32;
-constexpr int N_READERS = 3 + 4 * NS + N_EPI;   // warps that read an item's descriptor
+constexpr int N_READERS = 3 + GROUPS * GROUP_WARPS + N_EPI;   // warps that read an item's descriptor
 constexpr int NI = 4;                // item descriptors
-static_assert(A_TMEM + NS * A_COLS <= TMEM_COLS, "tensor memory");
+constexpr int FEW_PAIRS = 64;        // pairs per expert (of a full bucket) up to which passes hold 64
 static_assert(4 * strip_unit_bytes(64) <= U_SLOT, "a weight stage fits its slot");
-static_assert(NU % NS == 0, "weight slots");
 
 struct Item {
     int e, j, rt;        // expert, projection, row tile of the projection
@@ -78,19 +68,34 @@ struct Info {            // what the other warps need of an item
     int e, j, rt;        // expert, projection, row tile of the projection
     int n, first;        // pairs of the pass, plan position of the first
     int pad[3];
-    int pair[TN];        // their pair numbers, -1 where the plan names none of this bucket
+    int pair[128];       // their pair numbers, -1 where the plan names none of this bucket
 };
 
-// shared memory: [activation stages][weights][barriers][tensor-memory address, item count][descriptors]
-// [pass prefix]
-constexpr int OFF_U = NS * B_STAGE;
-constexpr int OFF_BAR = OFF_U + NU * U_SLOT;
-// full[NS] empty[NS] ufull[NU] uempty[NU] acc_full[2] acc_empty[2] info_full[NI] info_empty[NI] mma_done
-constexpr int N_BARS = 2 * NS + 2 * NU + 2 * NI + 5;
-constexpr int OFF_INFO = (OFF_BAR + N_BARS * 8 + 8 + 15) / 16 * 16;
-constexpr int OFF_PRE = OFF_INFO + NI * (int)sizeof(Info);
-constexpr int SMEM_BYTES = OFF_PRE + (MAX_E + 1) * 4 + 1024;   // + slack to align the base to 1024
-static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
+// TN_: most pairs of a pass (MMA N), 64 or 128. Tensor memory: two accumulators of TN columns, then the
+// A stages, as many as fit. A commit arrives 900 to 1300 cycles after its MMAs were issued and a converter
+// group needs 600 more to refill the stage, so a pass of few pairs is bound by the stages in flight: with
+// four (TN = 128) about 700 cycles a stage, with six (TN = 64) about 460.
+template <int TN_>
+struct Shape {
+    static constexpr int TN = TN_;
+    static constexpr int NA = (512 - 2 * TN) / 64;      // A stages: 6 or 4
+    static constexpr int NB = TN == 64 ? 8 : 5;         // B stages
+    static constexpr int NU = 6;                        // packed-weight slots
+    static constexpr int B_BOX = TN * KC * 2, B_STAGE = TN * SK * 2;
+    static constexpr uint32_t A_TMEM = 2 * TN;
+    // shared memory: [B stages][weights][barriers][tensor-memory address, item count][descriptors][pass prefix]
+    static constexpr int OFF_U = NB * B_STAGE;
+    static constexpr int OFF_BAR = OFF_U + NU * U_SLOT;
+    // full_a[NA] empty_a[NA] full_b[NB] empty_b[NB] ufull[NU] uempty[NU] acc_full[2] acc_empty[2]
+    // info_full[NI] info_empty[NI] mma_done
+    static constexpr int N_BARS = 2 * NA + 2 * NB + 2 * NU + 2 * NI + 5;
+    static constexpr int OFF_INFO = (OFF_BAR + N_BARS * 8 + 8 + 15) / 16 * 16;
+    static constexpr int OFF_PRE = OFF_INFO + NI * (int)sizeof(Info);
+    static constexpr int SMEM_BYTES = OFF_PRE + (MAX_E + 1) * 4 + 1024;   // + slack to align the base to 1024
+    static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
+    // a stage or slot always meets the same group, so that no barrier is waited on a phase too early
+    static_assert(NA % GROUPS == 0 && NU % GROUPS == 0, "rings");
+};
 
 struct IdProj {
     const uint8_t *w;
@@ -135,11 +140,12 @@ struct Pairs {
     int64_t first;
     int n;
 };
+template <int TN>
 __device__ __forceinline__ Pairs pairs_of(const IdArgs &a, const Item &t) {
     const int cnt = clamped_count(a, t.e);
-    const int tn = ((cnt + t.passes - 1) / t.passes + 15) & ~15;   // <= TN: passes = ceil(cnt / TN)
-    const int start = t.pass * tn;
-    return {(int64_t)__ldg(a.offsets + t.e) + start, min(tn, cnt - start)};
+    const int per = ((cnt + t.passes - 1) / t.passes + 15) & ~15;   // <= TN: passes = ceil(cnt / TN)
+    const int start = t.pass * per;
+    return {(int64_t)__ldg(a.offsets + t.e) + start, min(per, cnt - start)};
 }
 // The pair at plan position pos, -1 outside the plan or the bucket (a plan from elsewhere).
 __device__ __forceinline__ int pair_at(const IdArgs &a, int64_t pos) {
@@ -166,10 +172,31 @@ __device__ __forceinline__ bool mbar_test(uint32_t a, uint32_t parity) {
         : "memory");
     return ok != 0;
 }
-// A whole warp's wait: every lane gets the same answer.
+// A whole warp's wait: every lane gets the same answer. A phase that is complete costs one look.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
+    if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
     return __all_sync(0xffffffffu, mbar_wait(bar, parity));
 }
+// Both of two barriers; their looks overlap.
+__device__ __forceinline__ bool warp_wait2(uint32_t bar0, uint32_t parity0, uint32_t bar1, uint32_t parity1) {
+    const bool d0 = mbar_test(bar0, parity0), d1 = mbar_test(bar1, parity1);
+    if (__all_sync(0xffffffffu, d0 && d1)) return true;
+    const bool w = mbar_wait(bar0, parity0) && mbar_wait(bar1, parity1);
+    return __all_sync(0xffffffffu, w);
+}
+// A position in a ring of N entries: barriers 8 bytes apart, the parity of the phase that is filled
+// next. Single warps run these loops, a dependent instruction every five cycles or so: the positions
+// advance by additions. An entry's empty barrier is waited for with parity ^ 1: the first round passes.
+struct Ring {
+    uint32_t at, parity;
+    __device__ __forceinline__ void next(int n, int step = 1) {
+        at += step;
+        if (at >= (uint32_t)n) {
+            at -= n;
+            parity ^= 1;
+        }
+    }
+};
 // D += A x B (see tc_mma)
 __device__ __forceinline__ void tc_mma_add(uint32_t tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc) {
     asm volatile(
@@ -253,32 +280,38 @@ __global__ void __launch_bounds__(256) dequant_pairs_kernel(const int8_t *__rest
     for (int b = b0; b < kb; b += 8) dequant_word(qs, d, first + b, w, dst + (int64_t)b * QB);
 }
 
-template <int WT>
+template <int WT, typename S>
 __global__ void __launch_bounds__(THREADS, 1) mmq_id_kernel(const __grid_constant__ IdArgs a) {
+    constexpr int TN = S::TN, NA = S::NA, NB = S::NB, NU = S::NU;
     constexpr bool GROUPED = WT != QK_W_Q4_0;
     constexpr int STRIP = strip_unit_bytes(WT == QK_W_Q4_G64 ? 64 : 128);
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     const uint32_t sbase = smem_u32(smem);
-    const uint32_t full = sbase + OFF_BAR, empty = full + NS * 8, ufull = empty + NS * 8, uempty = ufull + NU * 8,
+    const uint32_t full_a = sbase + S::OFF_BAR, empty_a = full_a + NA * 8, full_b = empty_a + NA * 8,
+                   empty_b = full_b + NB * 8, ufull = empty_b + NB * 8, uempty = ufull + NU * 8,
                    acc_full = uempty + NU * 8, acc_empty = acc_full + 16, info_full = acc_empty + 16,
                    info_empty = info_full + 8 * NI, mma_done = info_empty + 8 * NI;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + OFF_BAR + N_BARS * 8);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + S::OFF_BAR + S::N_BARS * 8);
     int *n_items = reinterpret_cast<int *>(tmem_slot + 1);
-    Info *info = reinterpret_cast<Info *>(smem + OFF_INFO);
-    int *pre = reinterpret_cast<int *>(smem + OFF_PRE);
+    Info *info = reinterpret_cast<Info *>(smem + S::OFF_INFO);
+    int *pre = reinterpret_cast<int *>(smem + S::OFF_PRE);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int G = gridDim.x;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < NS; s++) {
-            mbar_init(full + 8 * s, 5);      // its group's four converter warps; the activation warp, with the bytes
-            mbar_init(empty + 8 * s, 1);     // the MMA commit
+        for (int s = 0; s < NA; s++) {
+            mbar_init(full_a + 8 * s, GROUP_WARPS);   // the converter warps of its group
+            mbar_init(empty_a + 8 * s, 1);            // the MMA commit
+        }
+        for (int s = 0; s < NB; s++) {
+            mbar_init(full_b + 8 * s, 1);             // the activation warp, with the bytes
+            mbar_init(empty_b + 8 * s, 1);            // the MMA commit
         }
         for (int u = 0; u < NU; u++) {
-            mbar_init(ufull + 8 * u, 1);      // the weight warp, with the bytes
-            mbar_init(uempty + 8 * u, 4);     // the converter warps of the stage's group
+            mbar_init(ufull + 8 * u, 1);              // the weight warp, with the bytes
+            mbar_init(uempty + 8 * u, GROUP_WARPS);
         }
         for (int h = 0; h < 2; h++) {
             mbar_init(acc_full + 8 * h, 1);         // the MMA commit after an item's last stage
@@ -342,7 +375,7 @@ __global__ void __launch_bounds__(THREADS, 1) mmq_id_kernel(const __grid_constan
     if (warp == ITEM_WARP) {   // ---------------- items
         for (int i = 0; i < mine; i++) {
             const Item t = item_of(a, pre, blockIdx.x + i * G);
-            const Pairs pr = pairs_of(a, t);
+            const Pairs pr = pairs_of<TN>(a, t);
             int p[TN / 32];
 #pragma unroll
             for (int j = 0; j < TN / 32; j++)
@@ -363,146 +396,133 @@ __global__ void __launch_bounds__(THREADS, 1) mmq_id_kernel(const __grid_constan
             if (lane == 0) mbar_arrive(info_full + 8 * (i % NI));
         }
     } else if (warp == 0) {   // ---------------- weights
-        uint32_t gu = 0;   // weight stages issued by this CTA
+        Ring u = {0, 0};
+        uint32_t issued = 0;   // weight stages issued by this CTA
         bool ok = true;
         for (int i = 0; i < mine && ok; i++) {
             if (!await_info(i)) break;
             const Info &f = info[i % NI];
             const IdProj &P = a.p[f.j];
-            const uint8_t *w = P.w + f.e * P.expert_bytes;
-            const int rt = f.rt, strips = GROUPED ? min(4, (P.N - rt * TM + STRIP_ROWS - 1) / STRIP_ROWS) : 0;
+            const int chunks = P.chunks, strips = GROUPED ? min(4, (P.N - f.rt * TM + STRIP_ROWS - 1) / STRIP_ROWS) : 1;
+            constexpr uint32_t PIECE = GROUPED ? STRIP : Q4_UNIT_BYTES;   // one strip's or the whole tile's stage
+            const int64_t row_bytes = (int64_t)chunks * PIECE;            // strips are this far apart
+            const uint8_t *w = P.w + f.e * P.expert_bytes + (int64_t)f.rt * (GROUPED ? 4 : 1) * row_bytes;
             release_info(i);
-            // stage kc's weights into L2, PF stages ahead of their copy
-            auto prefetch = [&](int kc) {
-                if (elect_one()) {
-                    if (GROUPED) {
-                        for (int q = 0; q < 4; q++)
-                            if (q < strips) prefetch_l2(w + ((int64_t)(4 * rt + q) * P.chunks + kc) * STRIP, STRIP);
-                    } else {
-                        prefetch_l2(w + ((int64_t)rt * P.chunks + kc) * Q4_UNIT_BYTES, Q4_UNIT_BYTES);
-                    }
-                }
-            };
-            for (int kc = NU; kc < PF && kc < P.chunks; kc++) prefetch(kc);
-            for (int kc = 0; kc < P.chunks; kc++) {
-                const uint32_t us = gu % NU;
-                if (gu >= NU && !warp_wait(uempty + 8 * us, ((gu / NU) - 1) & 1u)) {
+            for (int kc = 0; kc < chunks; kc++, w += PIECE, issued++) {
+                if (!warp_wait(uempty + 8 * u.at, u.parity ^ 1)) {
                     ok = false;
                     break;
                 }
                 if (elect_one()) {
-                    const uint32_t dst = sbase + OFF_U + us * U_SLOT;
+                    const uint32_t dst = sbase + S::OFF_U + u.at * U_SLOT, bar = ufull + 8 * u.at;
+                    mbar_expect_tx(bar, strips * PIECE);
+                    bulk_g2s(dst, w, PIECE, bar);
                     if (GROUPED) {
-                        mbar_expect_tx(ufull + 8 * us, strips * STRIP);
-                        for (int q = 0; q < 4; q++)
-                            if (q < strips)
-                                bulk_g2s(dst + q * STRIP, w + ((int64_t)(4 * rt + q) * P.chunks + kc) * STRIP, STRIP,
-                                         ufull + 8 * us);
-                    } else {
-                        mbar_expect_tx(ufull + 8 * us, Q4_UNIT_BYTES);
-                        bulk_g2s(dst, w + ((int64_t)rt * P.chunks + kc) * Q4_UNIT_BYTES, Q4_UNIT_BYTES, ufull + 8 * us);
+                        if (strips > 1) bulk_g2s(dst + PIECE, w + row_bytes, PIECE, bar);
+                        if (strips > 2) bulk_g2s(dst + 2 * PIECE, w + 2 * row_bytes, PIECE, bar);
+                        if (strips > 3) bulk_g2s(dst + 3 * PIECE, w + 3 * row_bytes, PIECE, bar);
                     }
                 }
                 __syncwarp();
-                gu++;
-                if (kc + PF < P.chunks) prefetch(kc + PF);
+                u.next(NU);
             }
         }
         // Every copy this warp issued has landed before the CTA can exit, also after a wait above ran
         // out (a barrier whose phase completed long ago passes at once; a wait that runs out here ends
         // the drain).
-        for (uint32_t x = gu > NU ? gu - NU : 0; x < gu; x++)
+        for (uint32_t x = issued > NU ? issued - NU : 0; x < issued; x++)
             if (!warp_wait(ufull + 8 * (x % NU), (x / NU) & 1u)) break;
     } else if (warp == ACT_WARP) {   // ---------------- activations
-        uint32_t g = 0;   // stages filled by this CTA
+        Ring r = {0, 0};
+        uint32_t issued = 0;   // stages filled by this CTA
         bool ok = true;
         for (int i = 0; i < mine && ok; i++) {
             if (!await_info(i)) break;
             const Info &f = info[i % NI];
-            const int K = a.p[f.j].K, first = f.first, rows = ((f.n + 15) & ~15), boxes = (rows + BOX_ROWS - 1) / BOX_ROWS;
+            const int K = a.p[f.j].K, first = f.first, boxes = (((f.n + 15) & ~15) + BOX_ROWS - 1) / BOX_ROWS;
             release_info(i);
-            for (int k0 = 0; k0 < K; k0 += SK, g++) {
-                const uint32_t s = g % NS, dst = sbase + s * B_STAGE, bar = full + 8 * s;
-                if (g >= NS && !warp_wait(empty + 8 * s, ((g / NS) - 1) & 1u)) {
+            for (int k0 = 0; k0 < K; k0 += SK, issued++) {
+                if (!warp_wait(empty_b + 8 * r.at, r.parity ^ 1)) {
                     ok = false;
                     break;
                 }
-                const int halves = K - k0 > KC ? 2 : 1;
                 if (elect_one()) {
-                    mbar_expect_tx(bar, (uint32_t)(halves * boxes * BOX_ROWS * KC * 2));
-                    for (int h = 0; h < halves; h++)
-                        for (int b = 0; b < boxes; b++)
-                            tma_2d(dst + h * B_BOX + b * (BOX_ROWS * KC * 2), &a.bmap, k0 + h * KC, first + b * BOX_ROWS, bar);
+                    const uint32_t dst = sbase + r.at * S::B_STAGE, bar = full_b + 8 * r.at;
+                    const bool two = K - k0 > KC;
+                    mbar_expect_tx(bar, (uint32_t)(boxes * BOX_ROWS * KC * 2) << (two ? 1 : 0));
+#pragma unroll
+                    for (int b = 0; b < TN / BOX_ROWS; b++) {
+                        if (b >= boxes) break;
+                        tma_2d(dst + b * (BOX_ROWS * KC * 2), &a.bmap, k0, first + b * BOX_ROWS, bar);
+                        if (two) tma_2d(dst + S::B_BOX + b * (BOX_ROWS * KC * 2), &a.bmap, k0 + KC, first + b * BOX_ROWS, bar);
+                    }
                 }
                 __syncwarp();
+                r.next(NB);
             }
         }
-        // As for the weights: every copy has landed, and then the stages' MMAs are done. A stage whose
-        // converters stopped early never completes; its wait runs out.
-        for (uint32_t x = g > NS ? g - NS : 0; x < g; x++)
-            if (!warp_wait(full + 8 * (x % NS), (x / NS) & 1u)) break;
+        for (uint32_t x = issued > NB ? issued - NB : 0; x < issued; x++)   // as for the weights: all copies have landed
+            if (!warp_wait(full_b + 8 * (x % NB), (x / NB) & 1u)) break;
     } else if (warp == 1) {   // ---------------- MMA issue (one elected thread, always the same)
-        uint32_t g = 0;   // stages consumed
-        bool ok = true, ready = false;
+        Ring ra = {0, 0}, rb = {0, 0};
+        bool ok = true;
         for (int i = 0; i < mine && ok; i++) {
             if (!await_info(i)) break;
-            const int n = info[i % NI].n, K = a.p[info[i % NI].j].K, nkc = (K + SK - 1) / SK;
+            const int n = info[i % NI].n, K = a.p[info[i % NI].j].K;
             release_info(i);
             const uint32_t idesc = mma_idesc((n + 15) & ~15), acc = tmem + (i & 1) * TN;
             if (i >= 2 && !warp_wait(acc_empty + 8 * (i & 1), ((i >> 1) - 1) & 1)) break;
-            for (int kc = 0; kc < nkc; kc++, g++) {
-                const uint32_t s = g % NS, at = tmem + A_TMEM + s * A_COLS, bt = sbase + s * B_STAGE;
-                if (!ready && !warp_wait(full + 8 * s, (g / NS) & 1u)) {
+            for (int left = K; left > 0; left -= SK) {   // nothing past K enters the sum
+                if (!warp_wait2(full_a + 8 * ra.at, ra.parity, full_b + 8 * rb.at, rb.parity)) {
                     ok = false;
                     break;
                 }
-                ready = __all_sync(0xffffffffu, mbar_test(full + 8 * ((g + 1) % NS), ((g + 1) / NS) & 1u));
                 tc_fence_after();
-                const int steps = min(SK, K - kc * SK) / 16;   // nothing past K enters the sum
                 if (elect_one()) {
                     // a descriptor's address field counts 16-byte units
-                    const uint64_t bd = sdesc(bt);
-                    tc_mma(acc, at, bd, idesc, kc != 0);
-                    if (steps == SK / 16) {
+                    const uint32_t at = tmem + S::A_TMEM + ra.at * A_COLS;
+                    const uint64_t bd = sdesc(sbase + rb.at * S::B_STAGE);
+                    tc_mma(acc, at, bd, idesc, left != K);
+                    if (left >= SK) {
 #pragma unroll
                         for (int ks = 1; ks < SK / 16; ks++)
-                            tc_mma_add(acc, at + 8 * ks, bd + (uint64_t)((ks >> 2) * (B_BOX / 16) + 2 * (ks & 3)), idesc);
+                            tc_mma_add(acc, at + 8 * ks, bd + (uint64_t)((ks >> 2) * (S::B_BOX / 16) + 2 * (ks & 3)), idesc);
                     } else {
 #pragma unroll 1
-                        for (int ks = 1; ks < steps; ks++)
-                            tc_mma_add(acc, at + 8 * ks, bd + (uint64_t)((ks >> 2) * (B_BOX / 16) + 2 * (ks & 3)), idesc);
+                        for (int ks = 1; 16 * ks < left; ks++)
+                            tc_mma_add(acc, at + 8 * ks, bd + (uint64_t)((ks >> 2) * (S::B_BOX / 16) + 2 * (ks & 3)), idesc);
                     }
-                    tc_commit(empty + 8 * s);
-                    if (kc == nkc - 1) tc_commit(acc_full + 8 * (i & 1));
+                    tc_commit(empty_a + 8 * ra.at);
+                    tc_commit(empty_b + 8 * rb.at);
+                    if (left <= SK) tc_commit(acc_full + 8 * (i & 1));
                 }
                 __syncwarp();
+                ra.next(NA);
+                rb.next(NB);
             }
         }
         if (elect_one()) tc_commit(mma_done);   // every MMA issued here is complete before the tensor memory is freed
         __syncwarp();
         warp_wait(mma_done, 0u);
     } else if (warp < EPI0) {   // ---------------- A conversion into tensor memory
-        // lanes 32 (warp % 4) .. +31 of tensor memory are tile rows 32 (warp % 4) ..; a group of four
-        // warps takes every NS-th stage and always the same A stage
-        const int quad = warp & 3, group = (warp - CONV0) >> 2, gq = lane >> 2;
-        const uint32_t abase = tmem + ((uint32_t)(32 * quad) << 16) + A_TMEM + group * A_COLS;
-        uint32_t g0 = 0, use = 0;   // the item's first stage; stages this group has filled
+        // lanes 32 (warp % 4) .. +31 of tensor memory are tile rows 32 (warp % 4) ..; a warp takes two of
+        // the four 32-column blocks of its group's stages
+        const int quad = warp & 3, group = (warp - CONV0) / GROUP_WARPS, jb0 = 2 * (((warp - CONV0) / 4) & 1), gq = lane >> 2;
+        const uint32_t abase = tmem + ((uint32_t)(32 * quad) << 16) + S::A_TMEM;
+        Ring ra = {(uint32_t)group, 0}, u = {(uint32_t)group, 0};
+        int ahead = group;   // stages until this group's next one
         bool ok = true;
         for (int i = 0; i < mine && ok; i++) {
             if (!await_info(i)) break;
-            const uint32_t nkc = a.p[info[i % NI].j].chunks;
+            const int chunks = a.p[info[i % NI].j].chunks;
             release_info(i);
-            for (uint32_t g = g0 + ((group - g0) & (NS - 1)); g < g0 + nkc; g += NS, use++) {
-                const uint32_t us = g % NU;
-                // both looks first, so that their latencies overlap
-                const bool have = mbar_test(ufull + 8 * us, (g / NU) & 1u), free_a = use == 0 || mbar_test(empty + 8 * group, (use - 1) & 1u);
-                ok = (__all_sync(0xffffffffu, have) || warp_wait(ufull + 8 * us, (g / NU) & 1u)) &&
-                     (__all_sync(0xffffffffu, free_a) || warp_wait(empty + 8 * group, (use - 1) & 1u));
+            for (; ahead < chunks; ahead += GROUPS) {
+                ok = warp_wait2(ufull + 8 * u.at, u.parity, empty_a + 8 * ra.at, ra.parity ^ 1);
                 if (!ok) break;
                 tc_fence_after();
-                const uint8_t *unit = smem + OFF_U + us * U_SLOT;
-#pragma unroll 1   // a short body: the roles share the SM's instruction caches
-                for (int jb = 0; jb < 4; jb++) {
+                const uint8_t *unit = smem + S::OFF_U + u.at * U_SLOT;
+#pragma unroll
+                for (int jb = jb0; jb < jb0 + 2; jb++) {
                     const uint4 wv = load_words<WT>(unit, quad, jb, lane);
                     RowHeads<WT> hd;
                     load_heads<WT>(unit, quad, jb, gq, hd);
@@ -510,7 +530,7 @@ __global__ void __launch_bounds__(THREADS, 1) mmq_id_kernel(const __grid_constan
                     const uint4 a1 = a_word(wv.y, hd.dw[1], hd.blo[1], hd.bhi[1]);
                     const uint4 a2 = a_word(wv.z, hd.dw[2], hd.blo[2], hd.bhi[2]);
                     const uint4 a3 = a_word(wv.w, hd.dw[3], hd.blo[3], hd.bhi[3]);
-                    const uint32_t base = abase + 16 * jb;
+                    const uint32_t base = abase + ra.at * A_COLS + 16 * jb;
                     asm volatile(
                         "tcgen05.st.sync.aligned.16x256b.x2.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(base),
                         "r"(a0.x), "r"(a0.y), "r"(a1.x), "r"(a1.y), "r"(a0.z), "r"(a0.w), "r"(a1.z), "r"(a1.w)
@@ -524,14 +544,16 @@ __global__ void __launch_bounds__(THREADS, 1) mmq_id_kernel(const __grid_constan
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {   // one arrival per warp: a lane's arrivals on one barrier go one by one
-                    mbar_arrive(full + 8 * group);
-                    mbar_arrive(uempty + 8 * us);
+                    mbar_arrive(full_a + 8 * ra.at);
+                    mbar_arrive(uempty + 8 * u.at);
                 }
+                ra.next(NA, GROUPS);
+                u.next(NU, GROUPS);
             }
-            g0 += nkc;
+            ahead -= chunks;
         }
     } else {   // ---------------- epilogue (accumulator lane = weight row, column = pair)
-        const int quad = warp & 3, c0 = ((warp - EPI0) >> 2) * 64, odd = lane & 1;
+        const int quad = warp & 3, c0 = ((warp - EPI0) >> 2) * (TN / 2), odd = lane & 1;
         for (int i = 0; i < mine; i++) {
             if (!await_info(i)) break;
             const Info &f = info[i % NI];
@@ -545,7 +567,7 @@ __global__ void __launch_bounds__(THREADS, 1) mmq_id_kernel(const __grid_constan
             // Rows come two at a time: lanes l and l ^ 1 exchange columns, so that the even lane holds
             // rows (l, l+1) of column 2k and the odd lane the same rows of column 2k+1: 4-byte stores.
 #pragma unroll 1   // as above
-            for (int q = 0; 16 * q < min(n, 64); q++) {
+            for (int q = 0; 16 * q < min(n, TN / 2); q++) {
                 uint32_t v[8];
                 load_columns(taddr + 16u * q, v);
 #pragma unroll
@@ -577,12 +599,16 @@ __global__ void __launch_bounds__(THREADS, 1) mmq_id_kernel(const __grid_constan
                      : "memory");
 }
 
+template <int WT, typename S>
+qk_status launch_shape(const IdArgs &a, cudaStream_t s) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(mmq_id_kernel<WT, S>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM_BYTES);
+    if (e != cudaSuccess) return fail(QK_ERR_CUDA, "mmq_id: shared memory attribute: %s", cudaGetErrorString(e));
+    return launch_pdl("mmq_id", mmq_id_kernel<WT, S>, dim3((unsigned)sm_count()), dim3(THREADS), (size_t)S::SMEM_BYTES, s, a);
+}
 template <int WT>
 qk_status launch_type(const IdArgs &a, cudaStream_t s) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(mmq_id_kernel<WT>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
-    if (e != cudaSuccess) return fail(QK_ERR_CUDA, "mmq_id: shared memory attribute: %s", cudaGetErrorString(e));
-    return launch_pdl("mmq_id", mmq_id_kernel<WT>, dim3((unsigned)sm_count()), dim3(THREADS), (size_t)SMEM_BYTES, s, a);
+    return (int64_t)a.pairs <= (int64_t)FEW_PAIRS * a.E ? launch_shape<WT, Shape<64>>(a, s) : launch_shape<WT, Shape<128>>(a, s);
 }
 
 }  // namespace
