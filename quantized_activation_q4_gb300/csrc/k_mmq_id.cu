@@ -57,6 +57,7 @@ constexpr int CONV0 = 2, EPI0 = CONV0 + GROUPS * GROUP_WARPS, N_EPI = 8, ACT_WAR
 constexpr int THREADS = (ITEM_WARP + 1) * 32;
 constexpr int N_READERS = 3 + GROUPS * GROUP_WARPS + N_EPI;   // warps that read an item's descriptor
 constexpr int NI = 4;                // item descriptors
+constexpr int EPI_BYTES = 1024;      // an epilogue warp's 16 pairs x 32 rows of bfloat16
 constexpr int FEW_PAIRS = 64;        // pairs per expert (of a full bucket) up to which passes hold 64
 static_assert(4 * strip_unit_bytes(64) <= U_SLOT, "a weight stage fits its slot");
 
@@ -66,35 +67,33 @@ struct Item {
 };
 struct Info {            // what the other warps need of an item
     int e, j, rt;        // expert, projection, row tile of the projection
-    int n, first;        // pairs of the pass, plan position of the first
-    int pad[3];
+    int n, first, K;     // pairs of the pass, plan position of the first; inner size
+    int pad[2];
     int pair[128];       // their pair numbers, -1 where the plan names none of this bucket
 };
 
 // TN_: most pairs of a pass (MMA N), 64 or 128. Tensor memory: two accumulators of TN columns, then the
-// A stages, as many as fit. A commit arrives 900 to 1300 cycles after its MMAs were issued and a converter
-// group needs 600 more to refill the stage, so a pass of few pairs is bound by the stages in flight: with
-// four (TN = 128) about 700 cycles a stage, with six (TN = 64) about 460.
+// A stages, as many as fit: six or four.
 template <int TN_>
 struct Shape {
     static constexpr int TN = TN_;
-    static constexpr int NA = (512 - 2 * TN) / 64;      // A stages: 6 or 4
-    static constexpr int NB = TN == 64 ? 8 : 5;         // B stages
+    static constexpr int NS = (512 - 2 * TN) / 64;      // stages
     static constexpr int NU = 6;                        // packed-weight slots
     static constexpr int B_BOX = TN * KC * 2, B_STAGE = TN * SK * 2;
     static constexpr uint32_t A_TMEM = 2 * TN;
-    // shared memory: [B stages][weights][barriers][tensor-memory address, item count][descriptors][pass prefix]
-    static constexpr int OFF_U = NB * B_STAGE;
-    static constexpr int OFF_BAR = OFF_U + NU * U_SLOT;
-    // full_a[NA] empty_a[NA] full_b[NB] empty_b[NB] ufull[NU] uempty[NU] acc_full[2] acc_empty[2]
-    // info_full[NI] info_empty[NI] mma_done
-    static constexpr int N_BARS = 2 * NA + 2 * NB + 2 * NU + 2 * NI + 5;
-    static constexpr int OFF_INFO = (OFF_BAR + N_BARS * 8 + 8 + 15) / 16 * 16;
+    // shared memory: [B stages][weights][epilogue][descriptors][pass prefix][barriers][tensor-memory address,
+    // item count]
+    static constexpr int OFF_U = NS * B_STAGE;
+    static constexpr int OFF_EPI = OFF_U + NU * U_SLOT;
+    static constexpr int OFF_INFO = OFF_EPI + N_EPI * EPI_BYTES;
     static constexpr int OFF_PRE = OFF_INFO + NI * (int)sizeof(Info);
-    static constexpr int SMEM_BYTES = OFF_PRE + (MAX_E + 1) * 4 + 1024;   // + slack to align the base to 1024
+    static constexpr int OFF_BAR = (OFF_PRE + (MAX_E + 1) * 4 + 7) / 8 * 8;
+    // full[NS] empty[NS] ufull[NU] uempty[NU] acc_full[2] acc_empty[2] info_full[NI] info_empty[NI] mma_done
+    static constexpr int N_BARS = 2 * NS + 2 * NU + 2 * NI + 5;
+    static constexpr int SMEM_BYTES = OFF_BAR + N_BARS * 8 + 8 + 1024;   // + slack to align the base to 1024
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
     // a stage or slot always meets the same group, so that no barrier is waited on a phase too early
-    static_assert(NA % GROUPS == 0 && NU % GROUPS == 0, "rings");
+    static_assert(NS % GROUPS == 0 && NU % GROUPS == 0, "rings");
 };
 
 struct IdProj {
@@ -205,18 +204,33 @@ __device__ __forceinline__ void tc_mma_add(uint32_t tmem, uint32_t a_tmem, uint6
         "r"(a_tmem), "l"(b), "r"(idesc)
         : "memory");
 }
-// 16 accumulator columns of this warp's lane quarter, packed to bfloat16 pairs of columns
-__device__ __forceinline__ void load_columns(uint32_t taddr, uint32_t *h) {
+// 16 accumulator columns of this warp's 32 rows to bfloat16 in shared memory, 64 bytes per column: with
+// the 16x256b shape lane 4g + t holds rows g and g + 8 of columns 2t, 2t+1 (and 8+2t, 9+2t), the fragments
+// that stmatrix transposes, so that 8 rows of a column are 16 consecutive bytes. Piece c (rows 8c..) of
+// column j is stored at place c ^ (j / 2 % 4): no two rows of a matrix share banks.
+__device__ __forceinline__ uint32_t pack_bf16(uint32_t lo, uint32_t hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(__uint_as_float(hi)), "f"(__uint_as_float(lo)));
+    return r;
+}
+__device__ __forceinline__ void columns_to_smem(uint32_t taddr, uint32_t buf, int lane) {
     uint32_t v[16];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
-          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-        : "r"(taddr));
+#pragma unroll
+    for (int h = 0; h < 2; h++)
+        asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=r"(v[8 * h]), "=r"(v[8 * h + 1]), "=r"(v[8 * h + 2]), "=r"(v[8 * h + 3]), "=r"(v[8 * h + 4]),
+                       "=r"(v[8 * h + 5]), "=r"(v[8 * h + 6]), "=r"(v[8 * h + 7])
+                     : "r"(taddr + (uint32_t)(h << 20)));   // lanes 0-15, then 16-31
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-    for (int i = 0; i < 8; i++)
-        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(h[i]) : "f"(__uint_as_float(v[2 * i + 1])), "f"(__uint_as_float(v[2 * i])));
+    for (int c = 0; c < 2; c++) {   // columns 8c .. 8c+7; lane 8m + j addresses piece m of column j
+        const int col = 8 * c + (lane & 7);
+        const uint32_t dst = buf + col * 64 + (((lane >> 3) ^ ((col >> 1) & 3)) << 4);
+        asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(dst),
+                     "r"(pack_bf16(v[4 * c], v[4 * c + 1])), "r"(pack_bf16(v[4 * c + 2], v[4 * c + 3])),
+                     "r"(pack_bf16(v[8 + 4 * c], v[8 + 4 * c + 1])), "r"(pack_bf16(v[8 + 4 * c + 2], v[8 + 4 * c + 3]))
+                     : "memory");
+    }
 }
 
 // The converters' words of one 32-column block for a warp's 32 rows: lane (g, t) gets word t of rows
@@ -282,14 +296,13 @@ __global__ void __launch_bounds__(256) dequant_pairs_kernel(const int8_t *__rest
 
 template <int WT, typename S>
 __global__ void __launch_bounds__(THREADS, 1) mmq_id_kernel(const __grid_constant__ IdArgs a) {
-    constexpr int TN = S::TN, NA = S::NA, NB = S::NB, NU = S::NU;
+    constexpr int TN = S::TN, NS = S::NS, NU = S::NU;
     constexpr bool GROUPED = WT != QK_W_Q4_0;
     constexpr int STRIP = strip_unit_bytes(WT == QK_W_Q4_G64 ? 64 : 128);
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     const uint32_t sbase = smem_u32(smem);
-    const uint32_t full_a = sbase + S::OFF_BAR, empty_a = full_a + NA * 8, full_b = empty_a + NA * 8,
-                   empty_b = full_b + NB * 8, ufull = empty_b + NB * 8, uempty = ufull + NU * 8,
+    const uint32_t full = sbase + S::OFF_BAR, empty = full + NS * 8, ufull = empty + NS * 8, uempty = ufull + NU * 8,
                    acc_full = uempty + NU * 8, acc_empty = acc_full + 16, info_full = acc_empty + 16,
                    info_empty = info_full + 8 * NI, mma_done = info_empty + 8 * NI;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + S::OFF_BAR + S::N_BARS * 8);
@@ -301,13 +314,9 @@ __global__ void __launch_bounds__(THREADS, 1) mmq_id_kernel(const __grid_constan
     const int G = gridDim.x;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < NA; s++) {
-            mbar_init(full_a + 8 * s, GROUP_WARPS);   // the converter warps of its group
-            mbar_init(empty_a + 8 * s, 1);            // the MMA commit
-        }
-        for (int s = 0; s < NB; s++) {
-            mbar_init(full_b + 8 * s, 1);             // the activation warp, with the bytes
-            mbar_init(empty_b + 8 * s, 1);            // the MMA commit
+        for (int s = 0; s < NS; s++) {
+            mbar_init(full + 8 * s, GROUP_WARPS + 1); // its group's converter warps; the activation warp, with the bytes
+            mbar_init(empty + 8 * s, 1);              // the MMA commit
         }
         for (int u = 0; u < NU; u++) {
             mbar_init(ufull + 8 * u, 1);              // the weight warp, with the bytes
@@ -389,6 +398,7 @@ __global__ void __launch_bounds__(THREADS, 1) mmq_id_kernel(const __grid_constan
                 f.j = t.j;
                 f.rt = t.rt;
                 f.n = pr.n;
+                f.K = a.p[t.j].K;
                 // rows outside the plan's read as zeros (a plan from elsewhere: none of them is stored)
                 f.first = (int)(pr.first < -TN ? -TN : (pr.first > a.pairs ? a.pairs : pr.first));
             }
@@ -439,15 +449,15 @@ __global__ void __launch_bounds__(THREADS, 1) mmq_id_kernel(const __grid_constan
         for (int i = 0; i < mine && ok; i++) {
             if (!await_info(i)) break;
             const Info &f = info[i % NI];
-            const int K = a.p[f.j].K, first = f.first, boxes = (((f.n + 15) & ~15) + BOX_ROWS - 1) / BOX_ROWS;
+            const int K = f.K, first = f.first, boxes = (((f.n + 15) & ~15) + BOX_ROWS - 1) / BOX_ROWS;
             release_info(i);
             for (int k0 = 0; k0 < K; k0 += SK, issued++) {
-                if (!warp_wait(empty_b + 8 * r.at, r.parity ^ 1)) {
+                if (!warp_wait(empty + 8 * r.at, r.parity ^ 1)) {
                     ok = false;
                     break;
                 }
                 if (elect_one()) {
-                    const uint32_t dst = sbase + r.at * S::B_STAGE, bar = full_b + 8 * r.at;
+                    const uint32_t dst = sbase + r.at * S::B_STAGE, bar = full + 8 * r.at;
                     const bool two = K - k0 > KC;
                     mbar_expect_tx(bar, (uint32_t)(boxes * BOX_ROWS * KC * 2) << (two ? 1 : 0));
 #pragma unroll
@@ -458,30 +468,36 @@ __global__ void __launch_bounds__(THREADS, 1) mmq_id_kernel(const __grid_constan
                     }
                 }
                 __syncwarp();
-                r.next(NB);
+                r.next(NS);
             }
         }
-        for (uint32_t x = issued > NB ? issued - NB : 0; x < issued; x++)   // as for the weights: all copies have landed
-            if (!warp_wait(full_b + 8 * (x % NB), (x / NB) & 1u)) break;
+        // as for the weights: all copies have landed (a stage whose converters stopped never completes: the
+        // wait runs out, long after its copies)
+        for (uint32_t x = issued > NS ? issued - NS : 0; x < issued; x++)
+            if (!warp_wait(full + 8 * (x % NS), (x / NS) & 1u)) break;
     } else if (warp == 1) {   // ---------------- MMA issue (one elected thread, always the same)
-        Ring ra = {0, 0}, rb = {0, 0};
-        bool ok = true;
+        Ring r = {0, 0};
+        bool ok = true, ready = false;
         for (int i = 0; i < mine && ok; i++) {
-            if (!await_info(i)) break;
-            const int n = info[i % NI].n, K = a.p[info[i % NI].j].K;
+            const uint32_t entry = 8 * (i % NI), side = 8 * (i & 1);
+            if (!warp_wait2(info_full + entry, (i / NI) & 1, acc_empty + side, ((i >> 1) & 1) ^ 1)) break;
+            const int n = info[i % NI].n, K = info[i % NI].K;
             release_info(i);
             const uint32_t idesc = mma_idesc((n + 15) & ~15), acc = tmem + (i & 1) * TN;
-            if (i >= 2 && !warp_wait(acc_empty + 8 * (i & 1), ((i >> 1) - 1) & 1)) break;
+            tc_fence_after();
             for (int left = K; left > 0; left -= SK) {   // nothing past K enters the sum
-                if (!warp_wait2(full_a + 8 * ra.at, ra.parity, full_b + 8 * rb.at, rb.parity)) {
+                if (!ready && !warp_wait(full + 8 * r.at, r.parity)) {
                     ok = false;
                     break;
                 }
+                const Ring cur = r;
+                r.next(NS);
+                const bool look = mbar_test(full + 8 * r.at, r.parity);   // the next stage's, while this one's are issued
                 tc_fence_after();
                 if (elect_one()) {
                     // a descriptor's address field counts 16-byte units
-                    const uint32_t at = tmem + S::A_TMEM + ra.at * A_COLS;
-                    const uint64_t bd = sdesc(sbase + rb.at * S::B_STAGE);
+                    const uint32_t at = tmem + S::A_TMEM + cur.at * A_COLS;
+                    const uint64_t bd = sdesc(sbase + cur.at * S::B_STAGE);
                     tc_mma(acc, at, bd, idesc, left != K);
                     if (left >= SK) {
 #pragma unroll
@@ -492,13 +508,10 @@ __global__ void __launch_bounds__(THREADS, 1) mmq_id_kernel(const __grid_constan
                         for (int ks = 1; 16 * ks < left; ks++)
                             tc_mma_add(acc, at + 8 * ks, bd + (uint64_t)((ks >> 2) * (S::B_BOX / 16) + 2 * (ks & 3)), idesc);
                     }
-                    tc_commit(empty_a + 8 * ra.at);
-                    tc_commit(empty_b + 8 * rb.at);
-                    if (left <= SK) tc_commit(acc_full + 8 * (i & 1));
+                    tc_commit(empty + 8 * cur.at);
+                    if (left <= SK) tc_commit(acc_full + side);
                 }
-                __syncwarp();
-                ra.next(NA);
-                rb.next(NB);
+                ready = __all_sync(0xffffffffu, look);
             }
         }
         if (elect_one()) tc_commit(mma_done);   // every MMA issued here is complete before the tensor memory is freed
@@ -514,10 +527,10 @@ __global__ void __launch_bounds__(THREADS, 1) mmq_id_kernel(const __grid_constan
         bool ok = true;
         for (int i = 0; i < mine && ok; i++) {
             if (!await_info(i)) break;
-            const int chunks = a.p[info[i % NI].j].chunks;
+            const int chunks = (info[i % NI].K + SK - 1) / SK;
             release_info(i);
             for (; ahead < chunks; ahead += GROUPS) {
-                ok = warp_wait2(ufull + 8 * u.at, u.parity, empty_a + 8 * ra.at, ra.parity ^ 1);
+                ok = warp_wait2(ufull + 8 * u.at, u.parity, empty + 8 * ra.at, ra.parity ^ 1);
                 if (!ok) break;
                 tc_fence_after();
                 const uint8_t *unit = smem + S::OFF_U + u.at * U_SLOT;
@@ -544,44 +557,46 @@ __global__ void __launch_bounds__(THREADS, 1) mmq_id_kernel(const __grid_constan
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {   // one arrival per warp: a lane's arrivals on one barrier go one by one
-                    mbar_arrive(full_a + 8 * ra.at);
+                    mbar_arrive(full + 8 * ra.at);
                     mbar_arrive(uempty + 8 * u.at);
                 }
-                ra.next(NA, GROUPS);
+                ra.next(NS, GROUPS);
                 u.next(NU, GROUPS);
             }
             ahead -= chunks;
         }
     } else {   // ---------------- epilogue (accumulator lane = weight row, column = pair)
-        const int quad = warp & 3, c0 = ((warp - EPI0) >> 2) * (TN / 2), odd = lane & 1;
+        const int quad = warp & 3, c0 = ((warp - EPI0) >> 2) * (TN / 2), piece = lane & 3;
+        const uint32_t buf = sbase + S::OFF_EPI + (warp - EPI0) * EPI_BYTES;
         for (int i = 0; i < mine; i++) {
-            if (!await_info(i)) break;
+            if (!warp_wait2(info_full + 8 * (i % NI), (i / NI) & 1, acc_full + 8 * (i & 1), (i >> 1) & 1)) break;
+            tc_fence_after();
             const Info &f = info[i % NI];
             const IdProj &P = a.p[f.j];
-            const int n = f.n - c0, row = f.rt * TM + quad * 32 + (lane & ~1);   // n: pairs here and past
-            const bool two = row + 1 < P.N && ((reinterpret_cast<uintptr_t>(P.y) | (uintptr_t)(P.y_stride * 2)) & 3) == 0;
+            const int n = min(f.n - c0, TN / 2), row = f.rt * TM + quad * 32 + 8 * piece, rows = P.N - row;
+            const bool wide = rows >= 8 && ((reinterpret_cast<uintptr_t>(P.y) | (uintptr_t)(P.y_stride * 2)) & 15) == 0;
             uint16_t *yr = P.y + row;
-            if (!warp_wait(acc_full + 8 * (i & 1), (i >> 1) & 1)) break;
-            tc_fence_after();
             const uint32_t taddr = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)((i & 1) * TN + c0);
-            // Rows come two at a time: lanes l and l ^ 1 exchange columns, so that the even lane holds
-            // rows (l, l+1) of column 2k and the odd lane the same rows of column 2k+1: 4-byte stores.
-#pragma unroll 1   // as above
-            for (int q = 0; 16 * q < min(n, TN / 2); q++) {
-                uint32_t v[8];
-                load_columns(taddr + 16u * q, v);
+#pragma unroll 1   // a short body: the roles share the SM's instruction caches
+            for (int q = 0; q < n; q += 16) {
+                __syncwarp();   // the previous columns have been read
+                columns_to_smem(taddr + q, buf, lane);
+                __syncwarp();
 #pragma unroll
-                for (int kk = 0; kk < 8; kk++) {
-                    const uint32_t other = __shfl_xor_sync(0xffffffffu, v[kk], 1);
-                    const uint32_t o = odd ? __byte_perm(other, v[kk], 0x7632) : __byte_perm(v[kk], other, 0x5410);
-                    const int id = f.pair[c0 + 16 * q + 2 * kk + odd];
-                    if (id < 0 || row >= P.N) continue;
+                for (int c = 0; c < 16; c += 8) {
+                    const int col = c + (lane >> 2), id = f.pair[c0 + q + col];   // -1 past the pass's pairs
+                    uint32_t x[4];
+                    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                                 : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                                 : "r"(buf + col * 64 + ((piece ^ ((col >> 1) & 3)) << 4)));
+                    if (id < 0) continue;
                     uint16_t *dst = yr + id * P.y_stride;
-                    if (two) {
-                        *reinterpret_cast<uint32_t *>(dst) = o;
+                    if (wide) {
+                        *reinterpret_cast<uint4 *>(dst) = make_uint4(x[0], x[1], x[2], x[3]);
                     } else {
-                        dst[0] = (uint16_t)o;
-                        if (row + 1 < P.N) dst[1] = (uint16_t)(o >> 16);
+#pragma unroll
+                        for (int e = 0; e < 8; e++)
+                            if (e < rows) dst[e] = (uint16_t)(x[e >> 1] >> (16 * (e & 1)));
                     }
                 }
             }
