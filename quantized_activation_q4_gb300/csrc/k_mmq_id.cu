@@ -477,41 +477,53 @@ __global__ void __launch_bounds__(THREADS, 1) mmq_id_kernel(const __grid_constan
             if (!warp_wait(full + 8 * (x % NS), (x / NS) & 1u)) break;
     } else if (warp == 1) {   // ---------------- MMA issue (one elected thread, always the same)
         Ring r = {0, 0};
-        bool ok = true, ready = false;
+        bool ok = true;
         for (int i = 0; i < mine && ok; i++) {
             const uint32_t entry = 8 * (i % NI), side = 8 * (i & 1);
             if (!warp_wait2(info_full + entry, (i / NI) & 1, acc_empty + side, ((i >> 1) & 1) ^ 1)) break;
             const int n = info[i % NI].n, K = info[i % NI].K;
             release_info(i);
             const uint32_t idesc = mma_idesc((n + 15) & ~15), acc = tmem + (i & 1) * TN;
-            tc_fence_after();
-            for (int left = K; left > 0; left -= SK) {   // nothing past K enters the sum
-                if (!ready && !warp_wait(full + 8 * r.at, r.parity)) {
-                    ok = false;
-                    break;
+            for (int left = K; left > 0;) {   // nothing past K enters the sum
+                // one look at the next four stages, a lane for each: how many are complete, at least one
+                Ring q = r;
+                q.next(NS, lane & 3);
+                const uint32_t late = ~__ballot_sync(0xffffffffu, mbar_test(full + 8 * q.at, q.parity)) & 0xfu;
+                int batch = min(late ? __ffs(late) - 1 : 4, (left + SK - 1) / SK);
+                if (batch == 0) {
+                    if (!warp_wait(full + 8 * r.at, r.parity)) {
+                        ok = false;
+                        break;
+                    }
+                    batch = 1;
                 }
-                const Ring cur = r;
-                r.next(NS);
-                const bool look = mbar_test(full + 8 * r.at, r.parity);   // the next stage's, while this one's are issued
                 tc_fence_after();
                 if (elect_one()) {
-                    // a descriptor's address field counts 16-byte units
-                    const uint32_t at = tmem + S::A_TMEM + cur.at * A_COLS;
-                    const uint64_t bd = sdesc(sbase + cur.at * S::B_STAGE);
-                    tc_mma(acc, at, bd, idesc, left != K);
-                    if (left >= SK) {
-#pragma unroll
-                        for (int ks = 1; ks < SK / 16; ks++)
-                            tc_mma_add(acc, at + 8 * ks, bd + (uint64_t)((ks >> 2) * (S::B_BOX / 16) + 2 * (ks & 3)), idesc);
-                    } else {
+                    uint32_t at = r.at;
+                    int l = left;
 #pragma unroll 1
-                        for (int ks = 1; 16 * ks < left; ks++)
-                            tc_mma_add(acc, at + 8 * ks, bd + (uint64_t)((ks >> 2) * (S::B_BOX / 16) + 2 * (ks & 3)), idesc);
+                    for (int j = 0; j < batch; j++, l -= SK) {
+                        // a descriptor's address field counts 16-byte units
+                        const uint32_t ta = tmem + S::A_TMEM + at * A_COLS;
+                        const uint64_t bd = sdesc(sbase + at * S::B_STAGE);
+                        tc_mma(acc, ta, bd, idesc, l != K);
+                        if (l >= SK) {
+#pragma unroll
+                            for (int ks = 1; ks < SK / 16; ks++)
+                                tc_mma_add(acc, ta + 8 * ks, bd + (uint64_t)((ks >> 2) * (S::B_BOX / 16) + 2 * (ks & 3)), idesc);
+                        } else {
+#pragma unroll 1
+                            for (int ks = 1; 16 * ks < l; ks++)
+                                tc_mma_add(acc, ta + 8 * ks, bd + (uint64_t)((ks >> 2) * (S::B_BOX / 16) + 2 * (ks & 3)), idesc);
+                        }
+                        tc_commit(empty + 8 * at);
+                        at = at + 1 == NS ? 0 : at + 1;
                     }
-                    tc_commit(empty + 8 * cur.at);
-                    if (left <= SK) tc_commit(acc_full + side);
+                    if (l <= 0) tc_commit(acc_full + side);
                 }
-                ready = __all_sync(0xffffffffu, look);
+                __syncwarp();
+                left -= batch * SK;
+                r.next(NS, batch);
             }
         }
         if (elect_one()) tc_commit(mma_done);   // every MMA issued here is complete before the tensor memory is freed
