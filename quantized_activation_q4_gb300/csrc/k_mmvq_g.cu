@@ -14,6 +14,8 @@ namespace {
 constexpr int MAX_PROJ = 8;
 constexpr unsigned FULL = 0xffffffffu;
 
+__device__ unsigned int g_mmvq_g_faults = 0;   // bits as qk_device_faults
+
 // ---------------------------------------------------------------- weight pack
 // One CTA per unit (32 rows x 128 columns). Source block: half d, z, unread, G/2 nibble bytes.
 template <int G>
@@ -51,100 +53,410 @@ __global__ void __launch_bounds__(256) pack_g_kernel(const uint8_t *__restrict__
 }
 
 // ---------------------------------------------------------------- matvec
+// Bound by the weight stream. A warp multiplies a strip of 32 rows by up to eight tokens with
+// mma.sync m16n8k16 (weights as A, straight from global memory: the packed order is the fragment order;
+// tokens as B). A nibble becomes a half by one logic operation, 1024 + c or 64 + c; the biases and the
+// 8 of a middle zero point leave with the accumulator's start value, so every block sum is exact:
+//   D_b = sum (c - 8) q,   group = sum_b d_a D_b,   y += d (group - (z - 8) sum_b d_a sum q)
+// About 150 instructions per 32 x 128 weights, so that the 2176 bytes take as long from memory as from
+// the issue slots of a quarter of the SM at half rate.
+//
+// CTAs of eight warps in clusters of `split` along K: a CTA turns its share of the image into B
+// fragments in shared memory once (for every row block it then takes), its warps take wr = 8 / wk
+// strips times wk pieces of the share, and the partial sums meet in shared memory, the cluster's in
+// distributed shared memory, added in the order of K. Work items are (pass, row block); a pass is the
+// call's tokens, or up to eight planned pairs of one expert. Every cluster takes a contiguous range of
+// items, and the loads of the next item's weights are in flight while one is finished.
+constexpr int WARPS = 8;
+constexpr int THREADS = WARPS * 32;
+constexpr int MAXC = 32;             // chunks of K whose fragments are held at a time
+constexpr int RED_STRIDE = 36;       // floats between two tokens' 32 rows of partial sums: no bank conflicts
+constexpr int RED = 8 * RED_STRIDE;  // floats of one warp's partial sums
+
 struct GProj {
     const uint8_t *w;
     float *y;
     int64_t y_stride, expert_bytes;
-    int N, K, chunks, strip_base;   // strip_base: first strip of this projection in the launch
+    int N, K, chunks, rb_base;   // rb_base: first row block of this projection in the launch
 };
 struct GArgs {
     const uint8_t *img;
     int64_t img_row_bytes;
     const int32_t *live, *counts, *offsets, *items;
-    int T, k, E, per_pair, n_proj;
+    int T, k, E, per_pair, n_proj, routed;   // T: tokens, or bucket rows of a routed call
+    int row_blocks, wk_log2, max_chunks;     // wk = 1 << wk_log2 warps share a strip
     GProj p[MAX_PROJ];
 };
 
-// One row n of one projection against one image row: lane l takes blocks l, l + 32, ...
+// Fragments of one 128-column chunk: B (per block a 16-byte entry per lane), d_a and the start value of
+// eight tokens per block, sum_b d_a sum q per group and token.
 template <int G>
-__device__ float row_dot(const uint8_t *w, int chunks, int K, int n, const uint8_t *img, int lane) {
-    constexpr int UNIT = strip_unit_bytes(G);
-    const int r = n % STRIP_ROWS, g = r & 7, i = r >> 3;
-    const uint8_t *strip = w + (int64_t)(n / STRIP_ROWS) * chunks * UNIT;
-    float acc = 0.0f;
-    for (int b = lane; b < K / QB; b += 32) {
-        const uint8_t *unit = strip + (int64_t)(b >> 2) * UNIT;
-        const uint32_t head = *reinterpret_cast<const uint32_t *>(unit + STRIP_DATA + 128 * ((b & 3) * QB / G) +
-                                                                  16 * g + 4 * i);
-        const int z = 8 + (int)__half2float(__ushort_as_half((unsigned short)(head >> 16)));
-        const uint8_t *blk = img + (int64_t)b * Q8_1_BYTES;
-        const int8_t *q = reinterpret_cast<const int8_t *>(blk + 4);
-        int D = 0;
-        for (int t = 0; t < 4; t++) {
-            const uint32_t v = *reinterpret_cast<const uint32_t *>(unit + (b & 3) * 512 + (4 * g + t) * 16 + 4 * i);
-            for (int j = 0; j < 4; j++) {
-                D += ((int)((v >> (8 * j)) & 15) - z) * q[4 * t + j];
-                D += ((int)((v >> (8 * j + 4)) & 15) - z) * q[16 + 4 * t + j];
+struct Rec {
+    uint4 b[4][32];
+    float da[4][8], start[4][8], xs[128 / G][8];
+};
+template <int G>
+struct Chunk {
+    uint4 w[4], head[128 / G];
+};
+
+__device__ __forceinline__ uint4 ldg_stream16(const void *p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+template <int G>
+__device__ __forceinline__ void load_chunk(Chunk<G> &c, const uint8_t *unit, int lane) {
+#pragma unroll
+    for (int jb = 0; jb < 4; jb++) c.w[jb] = ldg_stream16(unit + jb * 512 + lane * 16);
+#pragma unroll
+    for (int g = 0; g < 128 / G; g++) c.head[g] = ldg_stream16(unit + STRIP_DATA + 128 * g + 16 * (lane >> 2));
+}
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float &lo, float &hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+// D = A_lo B_lo + A_hi B_hi + start for 16 rows (words w0 of row g, w1 of row g + 8) x 8 tokens
+__device__ __forceinline__ void block_dot(uint32_t w0, uint32_t w1, uint4 b, float s0, float s1, uint64_t &d01,
+                                          uint64_t &d23) {
+    float e0, e1, e2, e3;
+    asm("{\n"
+        ".reg .b32 v0, v1, l0, l1, l2, l3, h0, h1, h2, h3;\n"
+        ".reg .f32 c0, c1, c2, c3;\n"
+        "shr.b32 v0, %4, 8;\n"
+        "shr.b32 v1, %5, 8;\n"
+        "lop3.b32 l0, %4, 0x000F000F, 0x64006400, 0xEA;\n"
+        "lop3.b32 l1, %5, 0x000F000F, 0x64006400, 0xEA;\n"
+        "lop3.b32 l2, v0, 0x000F000F, 0x64006400, 0xEA;\n"
+        "lop3.b32 l3, v1, 0x000F000F, 0x64006400, 0xEA;\n"
+        "lop3.b32 h0, %4, 0x00F000F0, 0x54005400, 0xEA;\n"
+        "lop3.b32 h1, %5, 0x00F000F0, 0x54005400, 0xEA;\n"
+        "lop3.b32 h2, v0, 0x00F000F0, 0x54005400, 0xEA;\n"
+        "lop3.b32 h3, v1, 0x00F000F0, 0x54005400, 0xEA;\n"
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {c0,c1,c2,c3}, {l0,l1,l2,l3}, {%6,%7}, {%10,%11,%10,%11};\n"
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {h0,h1,h2,h3}, {%8,%9}, {c0,c1,c2,c3};\n"
+        "}\n"
+        : "=f"(e0), "=f"(e1), "=f"(e2), "=f"(e3)
+        : "r"(w0), "r"(w1), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w), "f"(s0), "f"(s1));
+    d01 = pack2(e0, e1);
+    d23 = pack2(e2, e3);
+}
+
+// y (rows g, g+8, 16+g, 24+g of the strip x tokens 2t, 2t+1) += the chunk's products
+template <int G>
+__device__ __forceinline__ void chunk_product(const Chunk<G> &c, const Rec<G> &r, int lane, uint64_t y[4]) {
+    constexpr int BG = G / 32;   // blocks per group
+    const int t2 = 2 * (lane & 3);
+#pragma unroll
+    for (int grp = 0; grp < 128 / G; grp++) {
+        uint64_t acc[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < BG; i++) {
+            const int jb = grp * BG + i;
+            const uint4 b = r.b[jb][lane];
+            const float2 da = *reinterpret_cast<const float2 *>(&r.da[jb][t2]);
+            const float2 st = *reinterpret_cast<const float2 *>(&r.start[jb][t2]);
+            const uint64_t da2 = pack2(da.x, da.y);
+            uint64_t d01, d23;
+            block_dot(c.w[jb].x, c.w[jb].y, b, st.x, st.y, d01, d23);
+            acc[0] = fma2(da2, d01, acc[0]);
+            acc[1] = fma2(da2, d23, acc[1]);
+            block_dot(c.w[jb].z, c.w[jb].w, b, st.x, st.y, d01, d23);
+            acc[2] = fma2(da2, d01, acc[2]);
+            acc[3] = fma2(da2, d23, acc[3]);
+        }
+        const float2 xs = *reinterpret_cast<const float2 *>(&r.xs[grp][t2]);
+        const uint64_t xs2 = pack2(xs.x, xs.y);
+        const uint32_t h[4] = {c.head[grp].x, c.head[grp].y, c.head[grp].z, c.head[grp].w};
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const float2 dz = __half22float2(*reinterpret_cast<const __half2 *>(&h[i]));   // d, z - 8
+            y[i] = fma2(pack2(dz.x, dz.x), fma2(pack2(-dz.y, -dz.y), xs2, acc[i]), y[i]);
+        }
+    }
+}
+
+// A warp's fragments of one chunk: lane (g, t) converts words t of token g's blocks. Columns past K and
+// absent tokens (row < 0) are zeros; nothing of them is read.
+template <int G>
+__device__ __forceinline__ void make_rec(Rec<G> &r, const uint8_t *img_row, int chunk, int K, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+    uint32_t lo[4], hi[4], ds[4];
+#pragma unroll
+    for (int jb = 0; jb < 4; jb++) {
+        lo[jb] = hi[jb] = ds[jb] = 0;
+        if (img_row && chunk * UNIT_COLS + jb * QB < K) {
+            const uint8_t *blk = img_row + (int64_t)(4 * chunk + jb) * Q8_1_BYTES;
+            ds[jb] = __ldg(reinterpret_cast<const unsigned int *>(blk));
+            lo[jb] = __ldg(reinterpret_cast<const unsigned int *>(blk + 4 + 4 * t));
+            hi[jb] = __ldg(reinterpret_cast<const unsigned int *>(blk + 20 + 4 * t));
+        }
+    }
+    float xs = 0.0f;
+#pragma unroll
+    for (int jb = 0; jb < 4; jb++) {
+        // codes -> exact halves: q + 128 under the exponent of 1024, minus 1152
+        const uint32_t u = lo[jb] ^ 0x80808080u, v = hi[jb] ^ 0x80808080u;
+        const __half2 bias = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
+        const uint32_t p[4] = {__byte_perm(u, 0x64646464u, 0x4240), __byte_perm(u, 0x64646464u, 0x4341),
+                               __byte_perm(v, 0x64646464u, 0x4240), __byte_perm(v, 0x64646464u, 0x4341)};
+        uint32_t o[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const __half2 x = __hsub2(*reinterpret_cast<const __half2 *>(&p[i]), bias);
+            o[i] = *reinterpret_cast<const uint32_t *>(&x);
+        }
+        r.b[jb][lane] = make_uint4(o[0], o[1], o[2], o[3]);
+        int sl = __dp4a((int)lo[jb], 0x01010101, 0), sh = __dp4a((int)hi[jb], 0x01010101, 0);
+#pragma unroll
+        for (int m = 1; m <= 2; m <<= 1) {
+            sl += __shfl_xor_sync(FULL, sl, m);
+            sh += __shfl_xor_sync(FULL, sh, m);
+        }
+        const float da = __half2float(__ushort_as_half((unsigned short)ds[jb]));
+        xs = fmaf(da, (float)(sl + sh), (jb * QB) % G == 0 ? 0.0f : xs);
+        if (t == 0) {
+            r.da[jb][g] = da;
+            r.start[jb][g] = -(float)((1024 + 8) * sl + (64 + 8) * sh);
+            r.xs[jb * QB / G][g] = xs;
+        }
+    }
+}
+
+// Pass q of a routed call: its expert and the position of its first pair among the expert's.
+__device__ __forceinline__ void find_pass(const int *pre, int E, int q, int &e, int &first) {
+    int lo = 0, hi = E;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (pre[mid] <= q)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    e = lo;
+    first = 8 * (q - pre[lo]);
+}
+__device__ __forceinline__ int clamped_count(const GArgs &a, int e) {
+    const int c = __ldg(a.counts + e), pairs = a.T * a.k;
+    return c < 0 ? 0 : (c > pairs ? pairs : c);
+}
+
+template <int G, bool ROUTED>
+__global__ void __launch_bounds__(THREADS, 2) mmvq_g_kernel(const __grid_constant__ GArgs a) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    Rec<G> *rec = reinterpret_cast<Rec<G> *>(smem);
+    float *red = reinterpret_cast<float *>(rec + a.max_chunks);   // [2][WARPS][RED]
+    int *pre = reinterpret_cast<int *>(red + 2 * WARPS * RED);    // [E + 1], routed calls
+    __shared__ int tok_row[8], tok_out[8], n_pass;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint32_t rank, split;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(split));
+    const int clusters = gridDim.x / split, cluster = blockIdx.x / split;
+    const int wk = 1 << a.wk_log2, wr = WARPS >> a.wk_log2, kw = warp & (wk - 1), ws = warp >> a.wk_log2;
+    pdl_trigger();
+
+    int passes = 1;
+    if (ROUTED) {
+        pdl_wait();   // the plan decides which weights are read
+        if (warp == 0) {
+            // prefix of the experts' passes: lane l sums experts l * per ..; no plan of this bucket has
+            // more than pairs / 8 + E passes (counts with more: no work)
+            const int per = (a.E + 31) / 32, e0 = min(a.E, lane * per), e1 = min(a.E, e0 + per);
+            int64_t sum = 0;
+            for (int e = e0; e < e1; e++) sum += (clamped_count(a, e) + 7) / 8;
+            int64_t incl = sum;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t v = __shfl_up_sync(FULL, incl, o);
+                if (lane >= o) incl += v;
+            }
+            const int64_t total = __shfl_sync(FULL, incl, 31);
+            const bool sound = total <= (int64_t)a.T * a.k / 8 + a.E;
+            int64_t at = incl - sum;
+            for (int e = e0; e < e1; e++) {
+                pre[e] = sound ? (int)at : 0;
+                at += (clamped_count(a, e) + 7) / 8;
+            }
+            if (lane == 31) {
+                pre[a.E] = sound ? (int)total : 0;
+                n_pass = sound ? (int)total : 0;
+                if (!sound) atomicOr(&g_mmvq_g_faults, 2u);
             }
         }
-        const float da = __half2float(*reinterpret_cast<const __half *>(blk));
-        acc = fmaf(__half2float(__ushort_as_half((unsigned short)head)), da * (float)D, acc);
+        __syncthreads();
+        passes = n_pass;
     }
-    for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(FULL, acc, o);
-    return acc;
-}
+    // this cluster's items [it0, it1)
+    const int64_t items = (int64_t)passes * a.row_blocks;
+    const int it0 = (int)(items * cluster / clusters), it1 = (int)(items * (cluster + 1) / clusters);
 
-// grid (strips of every projection), 8 warps; warp w takes rows w, w + 8, ... of the strip.
-template <int G>
-__global__ void __launch_bounds__(256) mmvq_g_kernel(const __grid_constant__ GArgs a) {
-    pdl_trigger();
-    pdl_wait();
-    int j = 0;
-    while (j + 1 < a.n_proj && (int)blockIdx.x >= a.p[j + 1].strip_base) j++;
-    const GProj &P = a.p[j];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, live = live_rows(a.live, a.T);
-    for (int r = warp; r < STRIP_ROWS; r += 8) {
-        const int n = ((int)blockIdx.x - P.strip_base) * STRIP_ROWS + r;
-        if (n >= P.N) break;
-        for (int t = 0; t < live; t++) {
-            const float v = row_dot<G>(P.w, P.chunks, P.K, n, a.img + t * a.img_row_bytes, lane);
-            if (lane == 0) P.y[t * P.y_stride + n] = v;
+    // item -> projection, strip of this warp, and [c0, c1) = the CTA's share of K
+    auto item_proj = [&](int it, int &pass, int &rb) {
+        pass = ROUTED ? it / a.row_blocks : 0;
+        rb = it - pass * a.row_blocks;
+        int j = 0;
+        while (j + 1 < a.n_proj && rb >= a.p[j + 1].rb_base) j++;
+        rb -= a.p[j].rb_base;
+        return j;
+    };
+    auto sub_range = [&](int chunks, int sub, int &s0, int &s1) {   // chunks of sub-share `sub`; false past the last
+        const int c0 = (int)((int64_t)chunks * rank / split), c1 = (int)((int64_t)chunks * (rank + 1) / split);
+        s0 = min(c1, c0 + sub * MAXC);
+        s1 = min(c1, s0 + MAXC);
+    };
+    // the walk: (item, sub-share, chunk) of the next load
+    const uint8_t *wp = nullptr;
+    int w_left = 0, w_item = it0 - 1, w_sub = 0, w_subs = 1;
+    auto seek = [&]() {   // to the next non-empty run of chunks; w_item == it1 at the end
+        while (w_left == 0 && w_item < it1) {
+            if (w_item < it0 || ++w_sub >= w_subs) {
+                if (++w_item >= it1) return;
+                w_sub = 0;
+            }
+            int pass, rb;
+            const GProj &P = a.p[item_proj(w_item, pass, rb)];
+            int e = 0, first = 0, s0, s1;
+            if (ROUTED) find_pass(pre, a.E, pass, e, first);
+            const int share = (int)((int64_t)P.chunks * (rank + 1) / split) - (int)((int64_t)P.chunks * rank / split);
+            w_subs = (share + MAXC - 1) / MAXC;
+            sub_range(P.chunks, w_sub, s0, s1);
+            const int strip = rb * wr + ws, b = s0 + (s1 - s0) * kw / wk, n = s0 + (s1 - s0) * (kw + 1) / wk - b;
+            if (strip * STRIP_ROWS >= P.N) continue;
+            w_left = n;
+            wp = P.w + e * P.expert_bytes + ((int64_t)strip * P.chunks + b) * strip_unit_bytes(G);
         }
+    };
+    auto fetch = [&](Chunk<G> &c) {
+        if (w_left == 0) seek();
+        if (w_left > 0) {
+            load_chunk<G>(c, wp, lane);
+            wp += strip_unit_bytes(G);
+            w_left--;
+        }
+    };
+    Chunk<G> c0, c1;   // the next two chunks of the walk
+    fetch(c0);
+    fetch(c1);
+    if (!ROUTED) pdl_wait();   // weights are never written by the kernel before (see the header); the image may be
+
+    int cur_pass = -1, cur_s0 = -1, cur_cols = -1;
+    const int live = ROUTED ? 0 : live_rows(a.live, a.T);
+    for (int it = it0; it < it1; it++) {
+        int pass, rb;
+        const int j = item_proj(it, pass, rb);
+        const GProj &P = a.p[j];
+        const bool new_pass = pass != cur_pass;
+        if (new_pass) {
+            __syncthreads();   // the token list of the pass before has been used
+            if (threadIdx.x < 8) {
+                int row = -1, out = -1;
+                if (ROUTED) {
+                    int e, first;
+                    find_pass(pre, a.E, pass, e, first);
+                    const int64_t pos = (int64_t)__ldg(a.offsets + e) + first + threadIdx.x;
+                    const int pairs = a.T * a.k;
+                    if (first + (int)threadIdx.x < clamped_count(a, e) && pos >= 0 && pos < pairs) {
+                        const int pr = __ldg(a.items + pos);
+                        if (pr >= 0 && pr < pairs) {
+                            out = pr;
+                            row = a.per_pair ? pr : pr / a.k;
+                        }
+                    }
+                } else if ((int)threadIdx.x < live) {
+                    row = out = threadIdx.x;
+                }
+                tok_row[threadIdx.x] = row;
+                tok_out[threadIdx.x] = out;
+            }
+            __syncthreads();
+            cur_pass = pass;
+        }
+        uint64_t y[4] = {0, 0, 0, 0};
+        const bool mine = (rb * wr + ws) * STRIP_ROWS < P.N;
+        const int c_lo = (int)((int64_t)P.chunks * rank / split), c_hi = (int)((int64_t)P.chunks * (rank + 1) / split);
+        for (int sub = 0; sub == 0 || c_lo + sub * MAXC < c_hi; sub++) {
+            int s0, s1;
+            sub_range(P.chunks, sub, s0, s1);
+            const int cols = min(P.K, s1 * UNIT_COLS);
+            if (new_pass || s0 != cur_s0 || cols != cur_cols) {   // other tokens or columns than the fragments hold
+                __syncthreads();   // every warp is done with the fragments before
+                const int row = tok_row[lane >> 2];
+                const uint8_t *img_row = row < 0 ? nullptr : a.img + row * a.img_row_bytes;
+                for (int c = s0 + warp; c < s1; c += WARPS) make_rec<G>(rec[c - s0], img_row, c, P.K, lane);
+                __syncthreads();
+                cur_s0 = s0;
+                cur_cols = cols;
+            }
+            const int b = s0 + (s1 - s0) * kw / wk, e = s0 + (s1 - s0) * (kw + 1) / wk;
+            for (int c = b; mine && c < e; c++) {
+                const Chunk<G> now = c0;
+                c0 = c1;
+                fetch(c1);
+                chunk_product<G>(now, rec[c - s0], lane, y);
+            }
+        }
+        // partial sums: [token][32 rows] per warp, then over wk and over the cluster in the order of K
+        float *out = red + (it & 1) * WARPS * RED + warp * RED;
+        const int g = lane >> 2, t2 = 2 * (lane & 3);
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            float v0, v1;
+            unpack2(y[i], v0, v1);
+            out[t2 * RED_STRIDE + g + 8 * i] = v0;
+            out[(t2 + 1) * RED_STRIDE + g + 8 * i] = v1;
+        }
+        __syncwarp();
+        if (split > 1) {
+            asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+            asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+        } else {
+            __syncthreads();
+        }
+        // the wr strips' 256 sums each, spread over the cluster's threads; rows run fastest
+        const uint32_t base = (uint32_t)__cvta_generic_to_shared(red + (it & 1) * WARPS * RED);
+        for (int v = rank * THREADS + threadIdx.x; v < wr * 256; v += split * THREADS) {
+            const int s = v >> 8, tok = (v >> 5) & 7, r = v & 31, n = (rb * wr + s) * STRIP_ROWS + r;
+            const int o = tok_out[tok];
+            if (n >= P.N || o < 0) continue;
+            float sum = 0.0f;
+            for (uint32_t q = 0; q < split; q++) {
+                for (int w = 0; w < wk; w++) {
+                    const uint32_t at = base + 4u * ((s * wk + w) * RED + tok * RED_STRIDE + r);
+                    uint32_t far;
+                    float x;
+                    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(far) : "r"(at), "r"(q));
+                    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(far) : "memory");
+                    sum += x;
+                }
+            }
+            P.y[o * P.y_stride + n] = sum;
+        }
+        // red is double: its next use is after the next item's barrier
     }
-}
-
-// grid (strips of every projection, experts); the pairs of the expert one after another.
-template <int G>
-__global__ void __launch_bounds__(256) mmvq_g_id_kernel(const __grid_constant__ GArgs a) {
-    pdl_trigger();
-    pdl_wait();
-    int j = 0;
-    while (j + 1 < a.n_proj && (int)blockIdx.x >= a.p[j + 1].strip_base) j++;
-    const GProj &P = a.p[j];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, e = blockIdx.y, pairs = a.T * a.k;
-    const int cnt = min(max(a.counts[e], 0), pairs);
-    const int64_t first = a.offsets[e];
-    for (int r = warp; r < STRIP_ROWS; r += 8) {
-        const int n = ((int)blockIdx.x - P.strip_base) * STRIP_ROWS + r;
-        if (n >= P.N) break;
-        for (int c = 0; c < cnt; c++) {
-            const int64_t pos = first + c;
-            if (pos < 0 || pos >= pairs) continue;
-            const int p = a.items[pos];
-            if (p < 0 || p >= pairs) continue;
-            const int row = a.per_pair ? p : p / a.k;
-            const float v = row_dot<G>(P.w + e * P.expert_bytes, P.chunks, P.K, n, a.img + row * a.img_row_bytes, lane);
-            if (lane == 0) P.y[p * P.y_stride + n] = v;
-        }
+    __syncwarp();
+    if (split > 1) {   // no CTA leaves while another may read its sums
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     }
 }
 
 template <typename Proj>
-int fill(GArgs &a, const uint8_t *img, int64_t row_blocks, int n_proj, const Proj *projs) {
+void fill(GArgs &a, const uint8_t *img, int64_t row_blocks, int n_proj, const Proj *projs) {
     a.img = img;
     a.img_row_bytes = row_blocks * Q8_1_BYTES;
     a.n_proj = n_proj;
-    int strips = 0;
     for (int j = 0; j < n_proj; j++) {
         GProj &p = a.p[j];
         p.w = static_cast<const uint8_t *>(projs[j].w);
@@ -153,11 +465,59 @@ int fill(GArgs &a, const uint8_t *img, int64_t row_blocks, int n_proj, const Pro
         p.K = (int)projs[j].K;
         p.y_stride = p.N;
         p.chunks = (int)ceil_div(p.K, UNIT_COLS);
-        p.strip_base = strips;
         p.expert_bytes = packed_bytes(projs[j].wtype, p.N, p.K);
-        strips += (int)ceil_div(p.N, STRIP_ROWS);
     }
-    return strips;
+}
+
+// passes: at most this many.
+template <int G, bool ROUTED>
+qk_status launch_matvec(GArgs &a, int64_t passes, cudaStream_t s) {
+    const int sms = sm_count();
+    int chunks = 0;
+    for (int j = 0; j < a.n_proj; j++) chunks = a.p[j].chunks > chunks ? a.p[j].chunks : chunks;
+    // K over the CTAs of a cluster: the most CTAs (up to 8) whose equal shares waste at most a tenth
+    int split = 1;
+    for (int q = 2; q <= 8 && q <= chunks; q++)
+        if (ceil_div(chunks, q) * q * 10 <= (int64_t)chunks * 11) split = q;
+    // warps over rows; over K as well while the row blocks leave SMs without work
+    a.wk_log2 = 0;
+    const int share = (int)ceil_div(chunks, split);
+    for (;; a.wk_log2++) {
+        const int wr = WARPS >> a.wk_log2;
+        int64_t rbs = 0;
+        for (int j = 0; j < a.n_proj; j++) {
+            a.p[j].rb_base = (int)rbs;
+            rbs += ceil_div(ceil_div(a.p[j].N, STRIP_ROWS), wr);
+        }
+        a.row_blocks = (int)rbs;
+        if (a.wk_log2 == 3 || (share >> (a.wk_log2 + 1)) < 2 || passes * rbs * split >= sms + sms / 2) break;
+    }
+    if (passes * a.row_blocks > INT32_MAX) return fail(QK_ERR_UNSUPPORTED, "mmvq: too many rows for one launch");
+    const int64_t most = 2 * sms / split, need = passes * a.row_blocks;
+    const int clusters = (int)(need < most ? need : most);
+    a.max_chunks = share < MAXC ? share : MAXC;
+    const size_t smem = a.max_chunks * sizeof(Rec<G>) + 2 * WARPS * RED * sizeof(float) + (ROUTED ? (a.E + 1) * 4 : 0);
+    auto kernel = mmvq_g_kernel<G, ROUTED>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return fail(QK_ERR_CUDA, "mmvq: shared memory attribute: %s", cudaGetErrorString(e));
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    cfg.gridDim = dim3((unsigned)(clusters * split));
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = split;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = split > 1 ? 2 : 1;
+    e = cudaLaunchKernelEx(&cfg, kernel, a);
+    count_launch();
+    if (e != cudaSuccess) return fail(QK_ERR_CUDA, "mmvq: %s", cudaGetErrorString(e));
+    return check_launch("mmvq");
 }
 
 }  // namespace
@@ -177,19 +537,18 @@ qk_status launch_weight_pack_g(int wtype, const uint8_t *blocks, int64_t N, int6
 qk_status launch_mmvq_g(const uint8_t *img, int64_t row_blocks, int T, int n_proj, const qk_proj *projs,
                         const int32_t *live, cudaStream_t s) {
     GArgs a = {};
-    const int strips = fill(a, img, row_blocks, n_proj, projs);
+    fill(a, img, row_blocks, n_proj, projs);
     for (int j = 0; j < n_proj; j++) a.p[j].y_stride = projs[j].y_stride;
     a.T = T;
     a.live = live;
-    return launch_pdl("mmvq_g", projs[0].wtype == QK_W_Q4_G64 ? mmvq_g_kernel<64> : mmvq_g_kernel<128>,
-                      dim3((unsigned)strips), dim3(256), 0, s, a);
+    return projs[0].wtype == QK_W_Q4_G64 ? launch_matvec<64, false>(a, 1, s) : launch_matvec<128, false>(a, 1, s);
 }
 
 qk_status launch_mmvq_g_id(const uint8_t *img, int64_t row_blocks, int rows, int k, int n_proj,
                            const qk_proj_id *projs, const int32_t *counts, const int32_t *offsets,
                            const int32_t *items, bool per_pair, cudaStream_t s) {
     GArgs a = {};
-    const int strips = fill(a, img, row_blocks, n_proj, projs);
+    fill(a, img, row_blocks, n_proj, projs);
     a.T = rows;
     a.k = k;
     a.E = projs[0].n_experts;
@@ -197,8 +556,17 @@ qk_status launch_mmvq_g_id(const uint8_t *img, int64_t row_blocks, int rows, int
     a.counts = counts;
     a.offsets = offsets;
     a.items = items;
-    return launch_pdl("mmvq_g_id", projs[0].wtype == QK_W_Q4_G64 ? mmvq_g_id_kernel<64> : mmvq_g_id_kernel<128>,
-                      dim3((unsigned)strips, (unsigned)a.E), dim3(256), 0, s, a);
+    const int64_t pairs = (int64_t)rows * k, passes = pairs < pairs / 8 + a.E ? pairs : pairs / 8 + a.E;
+    return projs[0].wtype == QK_W_Q4_G64 ? launch_matvec<64, true>(a, passes, s) : launch_matvec<128, true>(a, passes, s);
+}
+
+qk_status read_mmvq_g_faults(uint32_t *faults) {
+    unsigned int v = 0, zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(&v, g_mmvq_g_faults, sizeof v);
+    if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_mmvq_g_faults, &zero, sizeof zero);
+    if (e != cudaSuccess) return fail(QK_ERR_CUDA, "qk_device_faults: %s", cudaGetErrorString(e));
+    *faults = v;
+    return QK_OK;
 }
 
 }  // namespace qk

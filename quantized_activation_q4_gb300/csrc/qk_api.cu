@@ -380,11 +380,12 @@ size_t qk_mmvq_workspace_bytes(int32_t n_proj, const qk_proj *projs) {
 
 qk_status qk_device_faults(uint32_t *faults) {
     REQUIRE(faults, QK_ERR_ARG, "faults is null");
-    uint32_t a = 0, b = 0, c = 0;
+    uint32_t a = 0, b = 0, c = 0, d = 0;
     qk_status st = read_device_faults(&a);
     if (st == QK_OK) st = read_mmq_faults(&b);
     if (st == QK_OK) st = read_mmq_id_faults(&c);
-    *faults = a | b | c;
+    if (st == QK_OK) st = read_mmvq_g_faults(&d);
+    *faults = a | b | c | d;
     return st;
 }
 

@@ -196,5 +196,6 @@ qk_status launch_mmq(const int8_t *qs, const uint16_t *d, int64_t row_blocks, in
 int64_t mmq_workspace_bytes(int64_t T, int64_t kmax);
 qk_status read_mmq_faults(uint32_t *faults);
 qk_status read_mmq_id_faults(uint32_t *faults);
+qk_status read_mmvq_g_faults(uint32_t *faults);
 
 }  // namespace qk
