@@ -6,6 +6,8 @@
 //
 // Every block sum is exact (integers); the sums over blocks and groups are binary32.
 
+#include <atomic>
+
 #include "qk_internal.cuh"
 
 namespace qk {
@@ -258,7 +260,7 @@ __global__ void __launch_bounds__(THREADS, 2) mmvq_g_kernel(const __grid_constan
     Rec<G> *rec = reinterpret_cast<Rec<G> *>(smem);
     float *red = reinterpret_cast<float *>(rec + a.max_chunks);   // [2][WARPS][RED]
     int *pre = reinterpret_cast<int *>(red + 2 * WARPS * RED);    // [E + 1], routed calls
-    __shared__ int tok_row[8], tok_out[8], n_pass;
+    __shared__ int tok_row[8], tok_out[8], n_pass, share_lo[MAX_PROJ], share_hi[MAX_PROJ];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint32_t rank, split;
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
@@ -266,6 +268,11 @@ __global__ void __launch_bounds__(THREADS, 2) mmvq_g_kernel(const __grid_constan
     const int clusters = gridDim.x / split, cluster = blockIdx.x / split;
     const int wk = 1 << a.wk_log2, wr = WARPS >> a.wk_log2, kw = warp & (wk - 1), ws = warp >> a.wk_log2;
     pdl_trigger();
+    if (threadIdx.x < a.n_proj) {   // this CTA's chunks of K (chunks < 2^24)
+        const uint32_t n = a.p[threadIdx.x].chunks;
+        share_lo[threadIdx.x] = n * rank / split;
+        share_hi[threadIdx.x] = n * (rank + 1) / split;
+    }
 
     int passes = 1;
     if (ROUTED) {
@@ -295,14 +302,14 @@ __global__ void __launch_bounds__(THREADS, 2) mmvq_g_kernel(const __grid_constan
                 if (!sound) atomicOr(&g_mmvq_g_faults, 2u);
             }
         }
-        __syncthreads();
-        passes = n_pass;
     }
+    __syncthreads();
+    if (ROUTED) passes = n_pass;
     // this cluster's items [it0, it1)
     const int64_t items = (int64_t)passes * a.row_blocks;
     const int it0 = (int)(items * cluster / clusters), it1 = (int)(items * (cluster + 1) / clusters);
 
-    // item -> projection, strip of this warp, and [c0, c1) = the CTA's share of K
+    // item -> pass, projection, row block of the projection
     auto item_proj = [&](int it, int &pass, int &rb) {
         pass = ROUTED ? it / a.row_blocks : 0;
         rb = it - pass * a.row_blocks;
@@ -311,30 +318,30 @@ __global__ void __launch_bounds__(THREADS, 2) mmvq_g_kernel(const __grid_constan
         rb -= a.p[j].rb_base;
         return j;
     };
-    auto sub_range = [&](int chunks, int sub, int &s0, int &s1) {   // chunks of sub-share `sub`; false past the last
-        const int c0 = (int)((int64_t)chunks * rank / split), c1 = (int)((int64_t)chunks * (rank + 1) / split);
-        s0 = min(c1, c0 + sub * MAXC);
-        s1 = min(c1, s0 + MAXC);
-    };
-    // the walk: (item, sub-share, chunk) of the next load
+    // The walk of this warp over its weights: the chunks of its strip and its piece of K, item after item,
+    // sub-share (MAXC chunks) after sub-share.
     const uint8_t *wp = nullptr;
-    int w_left = 0, w_item = it0 - 1, w_sub = 0, w_subs = 1;
-    auto seek = [&]() {   // to the next non-empty run of chunks; w_item == it1 at the end
+    int w_left = 0, w_item = it0 - 1, w_from = 0, w_to = 0;   // w_from .. w_to: the CTA's chunks not yet walked
+    auto seek = [&]() {   // to the next non-empty run; w_item == it1 at the end
         while (w_left == 0 && w_item < it1) {
-            if (w_item < it0 || ++w_sub >= w_subs) {
+            if (w_from >= w_to) {
                 if (++w_item >= it1) return;
-                w_sub = 0;
+                w_from = w_to = 0;
             }
             int pass, rb;
-            const GProj &P = a.p[item_proj(w_item, pass, rb)];
-            int e = 0, first = 0, s0, s1;
+            const int j = item_proj(w_item, pass, rb);
+            const GProj &P = a.p[j];
+            if (w_to == 0) {
+                w_from = share_lo[j];
+                w_to = share_hi[j];
+            }
+            int e = 0, first = 0;
             if (ROUTED) find_pass(pre, a.E, pass, e, first);
-            const int share = (int)((int64_t)P.chunks * (rank + 1) / split) - (int)((int64_t)P.chunks * rank / split);
-            w_subs = (share + MAXC - 1) / MAXC;
-            sub_range(P.chunks, w_sub, s0, s1);
-            const int strip = rb * wr + ws, b = s0 + (s1 - s0) * kw / wk, n = s0 + (s1 - s0) * (kw + 1) / wk - b;
+            const int strip = rb * wr + ws, n = min(w_to - w_from, MAXC);
+            const int b = w_from + ((n * kw) >> a.wk_log2), end = w_from + ((n * (kw + 1)) >> a.wk_log2);
+            w_from += n;
             if (strip * STRIP_ROWS >= P.N) continue;
-            w_left = n;
+            w_left = end - b;
             wp = P.w + e * P.expert_bytes + ((int64_t)strip * P.chunks + b) * strip_unit_bytes(G);
         }
     };
@@ -346,9 +353,10 @@ __global__ void __launch_bounds__(THREADS, 2) mmvq_g_kernel(const __grid_constan
             w_left--;
         }
     };
-    Chunk<G> c0, c1;   // the next two chunks of the walk
-    fetch(c0);
-    fetch(c1);
+    Chunk<G> even, odd;   // the next two chunks of the walk; `turn`: which comes first
+    int turn = 0;
+    fetch(even);
+    fetch(odd);
     if (!ROUTED) pdl_wait();   // weights are never written by the kernel before (see the header); the image may be
 
     int cur_pass = -1, cur_s0 = -1, cur_cols = -1;
@@ -385,11 +393,9 @@ __global__ void __launch_bounds__(THREADS, 2) mmvq_g_kernel(const __grid_constan
         }
         uint64_t y[4] = {0, 0, 0, 0};
         const bool mine = (rb * wr + ws) * STRIP_ROWS < P.N;
-        const int c_lo = (int)((int64_t)P.chunks * rank / split), c_hi = (int)((int64_t)P.chunks * (rank + 1) / split);
-        for (int sub = 0; sub == 0 || c_lo + sub * MAXC < c_hi; sub++) {
-            int s0, s1;
-            sub_range(P.chunks, sub, s0, s1);
-            const int cols = min(P.K, s1 * UNIT_COLS);
+        const int c_hi = share_hi[j];
+        for (int s0 = share_lo[j]; s0 < c_hi; s0 += MAXC) {
+            const int s1 = min(c_hi, s0 + MAXC), cols = min(P.K, s1 * UNIT_COLS);
             if (new_pass || s0 != cur_s0 || cols != cur_cols) {   // other tokens or columns than the fragments hold
                 __syncthreads();   // every warp is done with the fragments before
                 const int row = tok_row[lane >> 2];
@@ -399,12 +405,20 @@ __global__ void __launch_bounds__(THREADS, 2) mmvq_g_kernel(const __grid_constan
                 cur_s0 = s0;
                 cur_cols = cols;
             }
-            const int b = s0 + (s1 - s0) * kw / wk, e = s0 + (s1 - s0) * (kw + 1) / wk;
-            for (int c = b; mine && c < e; c++) {
-                const Chunk<G> now = c0;
-                c0 = c1;
-                fetch(c1);
-                chunk_product<G>(now, rec[c - s0], lane, y);
+            if (!mine) continue;
+            const Rec<G> *r = rec + (((s1 - s0) * kw) >> a.wk_log2);
+            const Rec<G> *end = rec + (((s1 - s0) * (kw + 1)) >> a.wk_log2);
+#pragma unroll 1
+            while (r < end) {   // each chunk's registers are refilled as soon as they are used
+                if (turn == 0) {
+                    chunk_product<G>(even, *r++, lane, y);
+                    fetch(even);
+                    turn = 1;
+                    if (r >= end) break;
+                }
+                chunk_product<G>(odd, *r++, lane, y);
+                fetch(odd);
+                turn = 0;
             }
         }
         // partial sums: [token][32 rows] per warp, then over wk and over the cluster in the order of K
@@ -469,20 +483,54 @@ void fill(GArgs &a, const uint8_t *img, int64_t row_blocks, int n_proj, const Pr
     }
 }
 
+// Clusters of `split` CTAs that are resident at once (two CTAs per SM by registers), per device.
+template <int G, bool ROUTED>
+int resident_clusters(int split, size_t smem) {
+    constexpr int MAXDEV = 64;
+    static std::atomic<int> cache[MAXDEV][9];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= MAXDEV) return 0;
+    int n = cache[dev][split].load(std::memory_order_relaxed);
+    if (n == 0) {
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr[1];
+        cfg.gridDim = dim3(split * 64);
+        cfg.blockDim = dim3(THREADS);
+        cfg.dynamicSmemBytes = smem;
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = split;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(&n, mmvq_g_kernel<G, ROUTED>, &cfg) != cudaSuccess) return 0;
+        cache[dev][split].store(n, std::memory_order_relaxed);
+    }
+    return n;
+}
+
 // passes: at most this many.
 template <int G, bool ROUTED>
 qk_status launch_matvec(GArgs &a, int64_t passes, cudaStream_t s) {
-    const int sms = sm_count();
+    // shared memory for MAXC chunks' fragments at most: two CTAs per SM whatever the sizes
+    constexpr size_t SMEM_MOST = MAXC * sizeof(Rec<G>) + 2 * WARPS * RED * sizeof(float) + (ROUTED ? 1025 * 4 : 0);
+    static_assert(2 * (SMEM_MOST + 2048) <= 227 * 1024, "two CTAs per SM");
+    auto kernel = mmvq_g_kernel<G, ROUTED>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_MOST);
+    if (e != cudaSuccess) return fail(QK_ERR_CUDA, "mmvq: shared memory attribute: %s", cudaGetErrorString(e));
     int chunks = 0;
     for (int j = 0; j < a.n_proj; j++) chunks = a.p[j].chunks > chunks ? a.p[j].chunks : chunks;
     // K over the CTAs of a cluster: the most CTAs (up to 8) whose equal shares waste at most a tenth
     int split = 1;
     for (int q = 2; q <= 8 && q <= chunks; q++)
         if (ceil_div(chunks, q) * q * 10 <= (int64_t)chunks * 11) split = q;
-    // warps over rows; over K as well while the row blocks leave SMs without work
-    a.wk_log2 = 0;
+    const int resident = resident_clusters<G, ROUTED>(split, SMEM_MOST);
+    if (resident < 1) return fail(QK_ERR_CUDA, "mmvq: no cluster of %d fits", split);
+    // Warps over rows; over K as well while that leaves clusters without work or the last round of items
+    // more than a tenth empty (a routed call's number of passes is not known here).
     const int share = (int)ceil_div(chunks, split);
-    for (;; a.wk_log2++) {
+    int64_t items = 0;
+    for (a.wk_log2 = 0;; a.wk_log2++) {
         const int wr = WARPS >> a.wk_log2;
         int64_t rbs = 0;
         for (int j = 0; j < a.n_proj; j++) {
@@ -490,16 +538,14 @@ qk_status launch_matvec(GArgs &a, int64_t passes, cudaStream_t s) {
             rbs += ceil_div(ceil_div(a.p[j].N, STRIP_ROWS), wr);
         }
         a.row_blocks = (int)rbs;
-        if (a.wk_log2 == 3 || (share >> (a.wk_log2 + 1)) < 2 || passes * rbs * split >= sms + sms / 2) break;
+        items = passes * rbs;
+        const bool full = items >= resident && (ROUTED || ceil_div(items, resident) * resident * 10 <= items * 11);
+        if (a.wk_log2 == 3 || (share >> (a.wk_log2 + 1)) < 2 || full) break;
     }
-    if (passes * a.row_blocks > INT32_MAX) return fail(QK_ERR_UNSUPPORTED, "mmvq: too many rows for one launch");
-    const int64_t most = 2 * sms / split, need = passes * a.row_blocks;
-    const int clusters = (int)(need < most ? need : most);
+    if (items > INT32_MAX) return fail(QK_ERR_UNSUPPORTED, "mmvq: too many rows for one launch");
+    const int clusters = (int)(items < resident ? items : resident);
     a.max_chunks = share < MAXC ? share : MAXC;
     const size_t smem = a.max_chunks * sizeof(Rec<G>) + 2 * WARPS * RED * sizeof(float) + (ROUTED ? (a.E + 1) * 4 : 0);
-    auto kernel = mmvq_g_kernel<G, ROUTED>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return fail(QK_ERR_CUDA, "mmvq: shared memory attribute: %s", cudaGetErrorString(e));
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     cfg.gridDim = dim3((unsigned)(clusters * split));
