@@ -63,17 +63,22 @@ __global__ void __launch_bounds__(256) pack_g_kernel(const uint8_t *__restrict__
 // About 150 instructions per 32 x 128 weights, so that the 2176 bytes take as long from memory as from
 // the issue slots of a quarter of the SM at half rate.
 //
-// CTAs of eight warps in clusters of `split` along K: a CTA turns its share of the image into B
-// fragments in shared memory once (for every row block it then takes), its warps take wr = 8 / wk
-// strips times wk pieces of the share, and the partial sums meet in shared memory, the cluster's in
-// distributed shared memory, added in the order of K. Work items are (pass, row block); a pass is the
-// call's tokens, or up to eight planned pairs of one expert. Every cluster takes a contiguous range of
-// items, and the loads of the next item's weights are in flight while one is finished.
-constexpr int WARPS = 8;
-constexpr int THREADS = WARPS * 32;
-constexpr int MAXC = 32;             // chunks of K whose fragments are held at a time
+// A CTA turns its share of the image into B fragments in shared memory once (for every row block it then
+// takes), its warps take wr = WARPS / wk strips times wk pieces of the share, and the partial sums meet in
+// shared memory, added in the order of K. Work items are (pass, row block); a pass is the call's tokens, or
+// up to eight planned pairs of one expert. Every CTA takes a contiguous range of items, and the loads of
+// the next item's weights are in flight while one is finished. Two forms:
+//   many items: a CTA takes all of K. Two CTAs of eight warps per SM while K's fragments fit twice, else one
+//     of sixteen.
+//   few items: clusters of `split` CTAs share K, and sum in distributed shared memory.
+// With clusters for all, the release of a cluster's barrier waited for the weight loads in flight: 8192 x
+// 65536 took 105 us.
 constexpr int RED_STRIDE = 36;       // floats between two tokens' 32 rows of partial sums: no bank conflicts
 constexpr int RED = 8 * RED_STRIDE;  // floats of one warp's partial sums
+constexpr int FEW_WARPS = 8, MANY_WARPS = 16;
+// chunks of K whose fragments a CTA holds at a time
+__host__ __device__ constexpr int max_chunks(int warps) { return warps == FEW_WARPS ? 36 : 76; }
+constexpr uint32_t SPIN_LIMIT = 1u << 16, SUSPEND_NS = 20000;   // a wait gives up after about a second
 
 struct GProj {
     const uint8_t *w;
@@ -86,7 +91,7 @@ struct GArgs {
     int64_t img_row_bytes;
     const int32_t *live, *counts, *offsets, *items;
     int T, k, E, per_pair, n_proj, routed;   // T: tokens, or bucket rows of a routed call
-    int row_blocks, wk_log2, max_chunks;     // wk = 1 << wk_log2 warps share a strip
+    int row_blocks, wk_log2, held;           // wk = 1 << wk_log2 warps share a strip; held: chunks of fragments
     GProj p[MAX_PROJ];
 };
 
@@ -254,13 +259,24 @@ __device__ __forceinline__ int clamped_count(const GArgs &a, int e) {
     return c < 0 ? 0 : (c > pairs ? pairs : c);
 }
 
-template <int G, bool ROUTED>
-__global__ void __launch_bounds__(THREADS, 2) mmvq_g_kernel(const __grid_constant__ GArgs a) {
+__device__ __forceinline__ void cluster_arrive() {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+    __syncwarp();
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+template <int G, bool ROUTED, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) mmvq_g_kernel(const __grid_constant__ GArgs a) {
+    constexpr int THREADS = WARPS * 32, MAXC = max_chunks(WARPS);
     extern __shared__ __align__(16) uint8_t smem[];
     Rec<G> *rec = reinterpret_cast<Rec<G> *>(smem);
-    float *red = reinterpret_cast<float *>(rec + a.max_chunks);   // [2][WARPS][RED]
+    float *red = reinterpret_cast<float *>(rec + a.held);   // [2][WARPS][RED]
     int *pre = reinterpret_cast<int *>(red + 2 * WARPS * RED);    // [E + 1], routed calls
-    __shared__ int tok_row[8], tok_out[8], n_pass, share_lo[MAX_PROJ], share_hi[MAX_PROJ];
+    __shared__ __align__(8) uint64_t written;   // a CTA that sums alone: its warps' arrivals, item after item
+    __shared__ int tok_row[8], tok_out[2][8], n_pass, share_lo[MAX_PROJ], share_hi[MAX_PROJ];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint32_t rank, split;
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
@@ -268,6 +284,8 @@ __global__ void __launch_bounds__(THREADS, 2) mmvq_g_kernel(const __grid_constan
     const int clusters = gridDim.x / split, cluster = blockIdx.x / split;
     const int wk = 1 << a.wk_log2, wr = WARPS >> a.wk_log2, kw = warp & (wk - 1), ws = warp >> a.wk_log2;
     pdl_trigger();
+    const uint32_t bar = (uint32_t)__cvta_generic_to_shared(&written);
+    if (threadIdx.x == 0) asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(WARPS) : "memory");
     if (threadIdx.x < a.n_proj) {   // this CTA's chunks of K (chunks < 2^24)
         const uint32_t n = a.p[threadIdx.x].chunks;
         share_lo[threadIdx.x] = n * rank / split;
@@ -359,6 +377,58 @@ __global__ void __launch_bounds__(THREADS, 2) mmvq_g_kernel(const __grid_constan
     fetch(odd);
     if (!ROUTED) pdl_wait();   // weights are never written by the kernel before (see the header); the image may be
 
+    auto announce = [&]() {
+        if (split > 1) {
+            cluster_arrive();
+        } else {
+            __syncwarp();
+            if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+        }
+    };
+    auto await_sums = [&](int n) {   // the n-th announcement of every warp (of the cluster)
+        if (split > 1) {
+            cluster_wait();
+            return;
+        }
+        for (uint32_t i = 0;; i++) {
+            uint32_t ok;
+            asm volatile(
+                "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
+                : "=r"(ok)
+                : "r"(bar), "r"(n & 1), "r"(SUSPEND_NS)
+                : "memory");
+            if (__all_sync(FULL, ok)) break;
+            if (i == SPIN_LIMIT) {
+                if (lane == 0) atomicOr(&g_mmvq_g_faults, 1u);
+                break;
+            }
+        }
+    };
+    // An item's sums over wk and over the cluster, in the order of K: the wr strips' 256 each, spread over
+    // the cluster's threads; rows run fastest.
+    auto sum_item = [&](int it) {
+        int pass, rb;
+        const GProj &P = a.p[item_proj(it, pass, rb)];
+        const uint32_t base = (uint32_t)__cvta_generic_to_shared(red + (it & 1) * WARPS * RED);
+        for (int v = rank * THREADS + threadIdx.x; v < wr * 256; v += split * THREADS) {
+            const int s = v >> 8, tok = (v >> 5) & 7, r = v & 31, n = (rb * wr + s) * STRIP_ROWS + r;
+            const int o = tok_out[pass & 1][tok];
+            if (n >= P.N || o < 0) continue;
+            float sum = 0.0f;
+            for (uint32_t q = 0; q < split; q++) {
+                uint32_t far;
+                asm("mapa.shared::cluster.u32 %0, %1, %2;"
+                    : "=r"(far)
+                    : "r"(base + 4u * (s * wk * RED + tok * RED_STRIDE + r)), "r"(q));
+                for (int w = 0; w < wk; w++) {
+                    float x;
+                    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(far + 4u * w * RED) : "memory");
+                    sum += x;
+                }
+            }
+            P.y[o * P.y_stride + n] = sum;
+        }
+    };
     int cur_pass = -1, cur_s0 = -1, cur_cols = -1;
     const int live = ROUTED ? 0 : live_rows(a.live, a.T);
     for (int it = it0; it < it1; it++) {
@@ -386,7 +456,7 @@ __global__ void __launch_bounds__(THREADS, 2) mmvq_g_kernel(const __grid_constan
                     row = out = threadIdx.x;
                 }
                 tok_row[threadIdx.x] = row;
-                tok_out[threadIdx.x] = out;
+                tok_out[pass & 1][threadIdx.x] = out;   // the pass before is still to be summed
             }
             __syncthreads();
             cur_pass = pass;
@@ -421,8 +491,14 @@ __global__ void __launch_bounds__(THREADS, 2) mmvq_g_kernel(const __grid_constan
                 turn = 0;
             }
         }
-        // partial sums: [token][32 rows] per warp, then over wk and over the cluster in the order of K
-        float *out = red + (it & 1) * WARPS * RED + warp * RED;
+        // Warps announce an item's partial sums and wait for the others' an item later, so that none stands
+        // still for the slowest. When the wait for item it - 1 is over, item it - 2 has been summed by all,
+        // and its buffer may be written.
+        if (it > it0) {
+            await_sums(it - 1 - it0);
+            sum_item(it - 1);
+        }
+        float *out = red + (it & 1) * WARPS * RED + warp * RED;   // [token][32 rows]
         const int g = lane >> 2, t2 = 2 * (lane & 3);
 #pragma unroll
         for (int i = 0; i < 4; i++) {
@@ -431,38 +507,15 @@ __global__ void __launch_bounds__(THREADS, 2) mmvq_g_kernel(const __grid_constan
             out[t2 * RED_STRIDE + g + 8 * i] = v0;
             out[(t2 + 1) * RED_STRIDE + g + 8 * i] = v1;
         }
-        __syncwarp();
-        if (split > 1) {
-            asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-            asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-        } else {
-            __syncthreads();
-        }
-        // the wr strips' 256 sums each, spread over the cluster's threads; rows run fastest
-        const uint32_t base = (uint32_t)__cvta_generic_to_shared(red + (it & 1) * WARPS * RED);
-        for (int v = rank * THREADS + threadIdx.x; v < wr * 256; v += split * THREADS) {
-            const int s = v >> 8, tok = (v >> 5) & 7, r = v & 31, n = (rb * wr + s) * STRIP_ROWS + r;
-            const int o = tok_out[tok];
-            if (n >= P.N || o < 0) continue;
-            float sum = 0.0f;
-            for (uint32_t q = 0; q < split; q++) {
-                for (int w = 0; w < wk; w++) {
-                    const uint32_t at = base + 4u * ((s * wk + w) * RED + tok * RED_STRIDE + r);
-                    uint32_t far;
-                    float x;
-                    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(far) : "r"(at), "r"(q));
-                    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(far) : "memory");
-                    sum += x;
-                }
-            }
-            P.y[o * P.y_stride + n] = sum;
-        }
-        // red is double: its next use is after the next item's barrier
+        announce();
     }
-    __syncwarp();
-    if (split > 1) {   // no CTA leaves while another may read its sums
-        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (it1 > it0) {
+        await_sums(it1 - 1 - it0);
+        sum_item(it1 - 1);
+        if (split > 1) {   // no CTA leaves while another may read its sums
+            cluster_arrive();
+            cluster_wait();
+        }
     }
 }
 
@@ -483,19 +536,28 @@ void fill(GArgs &a, const uint8_t *img, int64_t row_blocks, int n_proj, const Pr
     }
 }
 
-// Clusters of `split` CTAs that are resident at once (two CTAs per SM by registers), per device.
-template <int G, bool ROUTED>
-int resident_clusters(int split, size_t smem) {
+template <int G, bool ROUTED, int WARPS>
+constexpr size_t most_smem() {   // whatever the sizes, the same CTAs fit an SM
+    return max_chunks(WARPS) * sizeof(Rec<G>) + 2 * WARPS * RED * sizeof(float) + (ROUTED ? 1025 * 4 : 0);
+}
+
+// Clusters of `split` CTAs that are resident at once, per device (0: the query failed).
+template <int G, bool ROUTED, int WARPS>
+int resident_clusters(int split) {
     constexpr int MAXDEV = 64;
     static std::atomic<int> cache[MAXDEV][9];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= MAXDEV) return 0;
     int n = cache[dev][split].load(std::memory_order_relaxed);
     if (n == 0) {
+        constexpr size_t smem = most_smem<G, ROUTED, WARPS>();
+        static_assert(16 / WARPS * (smem + 2048) <= 227 * 1024, "shared memory");
+        auto kernel = mmvq_g_kernel<G, ROUTED, WARPS>;
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return 0;
         cudaLaunchConfig_t cfg = {};
         cudaLaunchAttribute attr[1];
         cfg.gridDim = dim3(split * 64);
-        cfg.blockDim = dim3(THREADS);
+        cfg.blockDim = dim3(WARPS * 32);
         cfg.dynamicSmemBytes = smem;
         attr[0].id = cudaLaunchAttributeClusterDimension;
         attr[0].val.clusterDim.x = split;
@@ -503,49 +565,43 @@ int resident_clusters(int split, size_t smem) {
         attr[0].val.clusterDim.z = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        if (cudaOccupancyMaxActiveClusters(&n, mmvq_g_kernel<G, ROUTED>, &cfg) != cudaSuccess) return 0;
+        if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) return 0;
         cache[dev][split].store(n, std::memory_order_relaxed);
     }
     return n;
 }
 
-// passes: at most this many.
-template <int G, bool ROUTED>
-qk_status launch_matvec(GArgs &a, int64_t passes, cudaStream_t s) {
-    // shared memory for MAXC chunks' fragments at most: two CTAs per SM whatever the sizes
-    constexpr size_t SMEM_MOST = MAXC * sizeof(Rec<G>) + 2 * WARPS * RED * sizeof(float) + (ROUTED ? 1025 * 4 : 0);
-    static_assert(2 * (SMEM_MOST + 2048) <= 227 * 1024, "two CTAs per SM");
-    auto kernel = mmvq_g_kernel<G, ROUTED>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_MOST);
-    if (e != cudaSuccess) return fail(QK_ERR_CUDA, "mmvq: shared memory attribute: %s", cudaGetErrorString(e));
-    int chunks = 0;
-    for (int j = 0; j < a.n_proj; j++) chunks = a.p[j].chunks > chunks ? a.p[j].chunks : chunks;
-    // K over the CTAs of a cluster: the most CTAs (up to 8) whose equal shares waste at most a tenth
-    int split = 1;
-    for (int q = 2; q <= 8 && q <= chunks; q++)
-        if (ceil_div(chunks, q) * q * 10 <= (int64_t)chunks * 11) split = q;
-    const int resident = resident_clusters<G, ROUTED>(split, SMEM_MOST);
-    if (resident < 1) return fail(QK_ERR_CUDA, "mmvq: no cluster of %d fits", split);
-    // Warps over rows; over K as well while that leaves clusters without work or the last round of items
-    // more than a tenth empty (a routed call's number of passes is not known here).
-    const int share = (int)ceil_div(chunks, split);
+// Row blocks of the launch with wk = 1 << wk_log2 warps to a strip.
+int64_t place_rows(GArgs &a, int warps, int wk_log2) {
+    int64_t rbs = 0;
+    for (int j = 0; j < a.n_proj; j++) {
+        a.p[j].rb_base = (int)rbs;
+        rbs += ceil_div(ceil_div(a.p[j].N, STRIP_ROWS), warps >> wk_log2);
+    }
+    a.wk_log2 = wk_log2;
+    a.row_blocks = (int)rbs;
+    return rbs;
+}
+
+template <int G, bool ROUTED, int WARPS>
+qk_status launch_form(GArgs &a, int64_t passes, int split, int chunks, cudaStream_t s) {
+    const int64_t resident = resident_clusters<G, ROUTED, WARPS>(split);
+    if (resident < 1) return fail(QK_ERR_CUDA, "mmvq: no cluster of %d CTAs fits", split);
+    // Warps over rows; over K as well while that leaves CTAs without work or the last round of items more
+    // than a tenth empty (a routed call's passes are not known here: `passes` is the most of them).
+    const int share = (int)ceil_div(chunks, split), held = share < max_chunks(WARPS) ? share : max_chunks(WARPS);
     int64_t items = 0;
-    for (a.wk_log2 = 0;; a.wk_log2++) {
-        const int wr = WARPS >> a.wk_log2;
-        int64_t rbs = 0;
-        for (int j = 0; j < a.n_proj; j++) {
-            a.p[j].rb_base = (int)rbs;
-            rbs += ceil_div(ceil_div(a.p[j].N, STRIP_ROWS), wr);
-        }
-        a.row_blocks = (int)rbs;
-        items = passes * rbs;
-        const bool full = items >= resident && (ROUTED || ceil_div(items, resident) * resident * 10 <= items * 11);
-        if (a.wk_log2 == 3 || (share >> (a.wk_log2 + 1)) < 2 || full) break;
+    for (int wk = 0; (WARPS >> wk) >= 1; wk++) {
+        if (wk > 0 && (held >> wk) < 2) break;
+        items = passes * place_rows(a, WARPS, wk);
+        if (items >= resident && (ROUTED || ceil_div(items, resident) * resident * 10 <= items * 11)) break;
     }
     if (items > INT32_MAX) return fail(QK_ERR_UNSUPPORTED, "mmvq: too many rows for one launch");
     const int clusters = (int)(items < resident ? items : resident);
-    a.max_chunks = share < MAXC ? share : MAXC;
-    const size_t smem = a.max_chunks * sizeof(Rec<G>) + 2 * WARPS * RED * sizeof(float) + (ROUTED ? (a.E + 1) * 4 : 0);
+    a.held = held;
+    const size_t smem = held * sizeof(Rec<G>) + 2 * WARPS * RED * sizeof(float) + (ROUTED ? (a.E + 1) * 4 : 0);
+    auto kernel = mmvq_g_kernel<G, ROUTED, WARPS>;
+    constexpr int THREADS = WARPS * 32;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     cfg.gridDim = dim3((unsigned)(clusters * split));
@@ -560,10 +616,29 @@ qk_status launch_matvec(GArgs &a, int64_t passes, cudaStream_t s) {
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = split > 1 ? 2 : 1;
-    e = cudaLaunchKernelEx(&cfg, kernel, a);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
     count_launch();
     if (e != cudaSuccess) return fail(QK_ERR_CUDA, "mmvq: %s", cudaGetErrorString(e));
     return check_launch("mmvq");
+}
+
+// passes: at most this many.
+template <int G, bool ROUTED>
+qk_status launch_matvec(GArgs &a, int64_t passes, cudaStream_t s) {
+    int chunks = 0;
+    for (int j = 0; j < a.n_proj; j++) chunks = a.p[j].chunks > chunks ? a.p[j].chunks : chunks;
+    // Many items (two and more for every CTA, with warps over rows alone or two to a strip): a CTA takes all
+    // of K. Else, or where K's fragments do not fit, K is shared by the most CTAs (up to 8) whose equal
+    // shares waste at most a tenth.
+    const int sms = sm_count();
+    if (chunks <= max_chunks(FEW_WARPS) && passes * place_rows(a, FEW_WARPS, 1) >= 4 * sms)
+        return launch_form<G, ROUTED, FEW_WARPS>(a, passes, 1, chunks, s);
+    if (chunks <= max_chunks(MANY_WARPS) && passes * place_rows(a, MANY_WARPS, 2) >= 2 * sms)
+        return launch_form<G, ROUTED, MANY_WARPS>(a, passes, 1, chunks, s);
+    int split = 1;
+    for (int q = 2; q <= 8 && q <= chunks; q++)
+        if (ceil_div(chunks, q) * q * 10 <= (int64_t)chunks * 11) split = q;
+    return launch_form<G, ROUTED, FEW_WARPS>(a, passes, split, chunks, s);
 }
 
 }  // namespace
