@@ -77,21 +77,22 @@ constexpr int RED_STRIDE = 36;       // floats between two tokens' 32 rows of pa
 constexpr int RED = 8 * RED_STRIDE;  // floats of one warp's partial sums
 constexpr int FEW_WARPS = 8, MANY_WARPS = 16;
 // chunks of K whose fragments a CTA holds at a time
-__host__ __device__ constexpr int max_chunks(int warps) { return warps == FEW_WARPS ? 36 : 76; }
+__host__ __device__ constexpr int max_chunks(int warps) { return warps == FEW_WARPS ? 34 : 72; }
+constexpr int PFD = 2;                // chunks
 constexpr uint32_t SPIN_LIMIT = 1u << 16, SUSPEND_NS = 20000;   // a wait gives up after about a second
 
 struct GProj {
     const uint8_t *w;
     float *y;
     int64_t y_stride, expert_bytes;
-    int N, K, chunks, rb_base;   // rb_base: first row block of this projection in the launch
+    int N, K, chunks;
 };
 struct GArgs {
     const uint8_t *img;
     int64_t img_row_bytes;
     const int32_t *live, *counts, *offsets, *items;
     int T, k, E, per_pair, n_proj, routed;   // T: tokens, or bucket rows of a routed call
-    int row_blocks, wk_log2, held;           // wk = 1 << wk_log2 warps share a strip; held: chunks of fragments
+    int wk_log2, held;                       // wk = 1 << wk_log2 warps share a strip (ordinary calls); chunks of fragments
     GProj p[MAX_PROJ];
 };
 
@@ -100,7 +101,8 @@ struct GArgs {
 template <int G>
 struct Rec {
     uint4 b[4][32];
-    float da[4][8], start[4][8], xs[128 / G][8];
+    float4 start[4][4];              // (s, s') of tokens 2t, 2t+1, twice: an accumulator's four registers
+    float da[4][8], xs[128 / G][8];
 };
 template <int G>
 struct Chunk {
@@ -135,8 +137,7 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     return r;
 }
 // D = A_lo B_lo + A_hi B_hi + start for 16 rows (words w0 of row g, w1 of row g + 8) x 8 tokens
-__device__ __forceinline__ void block_dot(uint32_t w0, uint32_t w1, uint4 b, float s0, float s1, uint64_t &d01,
-                                          uint64_t &d23) {
+__device__ __forceinline__ void block_dot(uint32_t w0, uint32_t w1, uint4 b, float4 s, uint64_t &d01, uint64_t &d23) {
     float e0, e1, e2, e3;
     asm("{\n"
         ".reg .b32 v0, v1, l0, l1, l2, l3, h0, h1, h2, h3;\n"
@@ -151,11 +152,12 @@ __device__ __forceinline__ void block_dot(uint32_t w0, uint32_t w1, uint4 b, flo
         "lop3.b32 h1, %5, 0x00F000F0, 0x54005400, 0xEA;\n"
         "lop3.b32 h2, v0, 0x00F000F0, 0x54005400, 0xEA;\n"
         "lop3.b32 h3, v1, 0x00F000F0, 0x54005400, 0xEA;\n"
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {c0,c1,c2,c3}, {l0,l1,l2,l3}, {%6,%7}, {%10,%11,%10,%11};\n"
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {c0,c1,c2,c3}, {l0,l1,l2,l3}, {%6,%7}, {%10,%11,%12,%13};\n"
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {h0,h1,h2,h3}, {%8,%9}, {c0,c1,c2,c3};\n"
         "}\n"
         : "=f"(e0), "=f"(e1), "=f"(e2), "=f"(e3)
-        : "r"(w0), "r"(w1), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w), "f"(s0), "f"(s1));
+        : "r"(w0), "r"(w1), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w), "f"(s.x), "f"(s.y), "f"(s.z),
+          "f"(s.w));
     d01 = pack2(e0, e1);
     d23 = pack2(e2, e3);
 }
@@ -173,13 +175,13 @@ __device__ __forceinline__ void chunk_product(const Chunk<G> &c, const Rec<G> &r
             const int jb = grp * BG + i;
             const uint4 b = r.b[jb][lane];
             const float2 da = *reinterpret_cast<const float2 *>(&r.da[jb][t2]);
-            const float2 st = *reinterpret_cast<const float2 *>(&r.start[jb][t2]);
+            const float4 st = r.start[jb][lane & 3];
             const uint64_t da2 = pack2(da.x, da.y);
             uint64_t d01, d23;
-            block_dot(c.w[jb].x, c.w[jb].y, b, st.x, st.y, d01, d23);
+            block_dot(c.w[jb].x, c.w[jb].y, b, st, d01, d23);
             acc[0] = fma2(da2, d01, acc[0]);
             acc[1] = fma2(da2, d23, acc[1]);
-            block_dot(c.w[jb].z, c.w[jb].w, b, st.x, st.y, d01, d23);
+            block_dot(c.w[jb].z, c.w[jb].w, b, st, d01, d23);
             acc[2] = fma2(da2, d01, acc[2]);
             acc[3] = fma2(da2, d23, acc[3]);
         }
@@ -235,7 +237,8 @@ __device__ __forceinline__ void make_rec(Rec<G> &r, const uint8_t *img_row, int 
         xs = fmaf(da, (float)(sl + sh), (jb * QB) % G == 0 ? 0.0f : xs);
         if (t == 0) {
             r.da[jb][g] = da;
-            r.start[jb][g] = -(float)((1024 + 8) * sl + (64 + 8) * sh);
+            float *st = reinterpret_cast<float *>(&r.start[jb][g >> 1]) + (g & 1);
+            st[0] = st[2] = -(float)((1024 + 8) * sl + (64 + 8) * sh);
             r.xs[jb * QB / G][g] = xs;
         }
     }
@@ -259,6 +262,24 @@ __device__ __forceinline__ int clamped_count(const GArgs &a, int e) {
     return c < 0 ? 0 : (c > pairs ? pairs : c);
 }
 
+template <int WARPS>
+__host__ __device__ inline int row_blocks_of(int N, int wk_log2) {
+    const int strips = (N + STRIP_ROWS - 1) / STRIP_ROWS, wr = WARPS >> wk_log2;
+    return (strips + wr - 1) / wr;
+}
+// Warps over rows; over K as well (two, four.. to a strip) while that leaves CTAs without work or the last
+// round of items more than a tenth empty, and a warp has two chunks of K.
+template <int WARPS>
+__host__ __device__ inline int choose_wk(const GArgs &a, int64_t passes, int64_t clusters) {
+    for (int wk = 0;; wk++) {
+        int64_t items = 0;
+        for (int j = 0; j < a.n_proj; j++) items += row_blocks_of<WARPS>(a.p[j].N, wk);
+        items *= passes;
+        const int64_t rounds = (items + clusters - 1) / clusters;
+        if ((items >= clusters && rounds * clusters * 10 <= items * 11) || (WARPS >> wk) == 1 || (a.held >> (wk + 1)) < 2)
+            return wk;
+    }
+}
 __device__ __forceinline__ void cluster_arrive() {
     __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
@@ -276,13 +297,12 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) mmvq_g_kernel(const __
     float *red = reinterpret_cast<float *>(rec + a.held);   // [2][WARPS][RED]
     int *pre = reinterpret_cast<int *>(red + 2 * WARPS * RED);    // [E + 1], routed calls
     __shared__ __align__(8) uint64_t written;   // a CTA that sums alone: its warps' arrivals, item after item
-    __shared__ int tok_row[8], tok_out[2][8], n_pass, share_lo[MAX_PROJ], share_hi[MAX_PROJ];
+    __shared__ int tok_row[2][8], tok_out[4][8], n_pass, share_lo[MAX_PROJ], share_hi[MAX_PROJ], rb_base[MAX_PROJ + 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint32_t rank, split;
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
     asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(split));
     const int clusters = gridDim.x / split, cluster = blockIdx.x / split;
-    const int wk = 1 << a.wk_log2, wr = WARPS >> a.wk_log2, kw = warp & (wk - 1), ws = warp >> a.wk_log2;
     pdl_trigger();
     const uint32_t bar = (uint32_t)__cvta_generic_to_shared(&written);
     if (threadIdx.x == 0) asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(WARPS) : "memory");
@@ -322,18 +342,33 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) mmvq_g_kernel(const __
         }
     }
     __syncthreads();
-    if (ROUTED) passes = n_pass;
+    int wk_log2 = a.wk_log2;
+    if (ROUTED) {
+        passes = n_pass;
+        wk_log2 = choose_wk<WARPS>(a, passes, clusters);
+    }
+    if (threadIdx.x == 0) {
+        int rbs = 0;
+        for (int j = 0; j < a.n_proj; j++) {
+            rb_base[j] = rbs;
+            rbs += row_blocks_of<WARPS>(a.p[j].N, wk_log2);
+        }
+        rb_base[a.n_proj] = rbs;
+    }
+    __syncthreads();
+    const int row_blocks = rb_base[a.n_proj];
+    const int wk = 1 << wk_log2, wr = WARPS >> wk_log2, kw = warp & (wk - 1), ws = warp >> wk_log2;
     // this cluster's items [it0, it1)
-    const int64_t items = (int64_t)passes * a.row_blocks;
+    const int64_t items = (int64_t)passes * row_blocks;
     const int it0 = (int)(items * cluster / clusters), it1 = (int)(items * (cluster + 1) / clusters);
 
     // item -> pass, projection, row block of the projection
     auto item_proj = [&](int it, int &pass, int &rb) {
-        pass = ROUTED ? it / a.row_blocks : 0;
-        rb = it - pass * a.row_blocks;
+        pass = ROUTED ? it / row_blocks : 0;
+        rb = it - pass * row_blocks;
         int j = 0;
-        while (j + 1 < a.n_proj && rb >= a.p[j + 1].rb_base) j++;
-        rb -= a.p[j].rb_base;
+        while (j + 1 < a.n_proj && rb >= rb_base[j + 1]) j++;
+        rb -= rb_base[j];
         return j;
     };
     // The walk of this warp over its weights: the chunks of its strip and its piece of K, item after item,
@@ -356,7 +391,7 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) mmvq_g_kernel(const __
             int e = 0, first = 0;
             if (ROUTED) find_pass(pre, a.E, pass, e, first);
             const int strip = rb * wr + ws, n = min(w_to - w_from, MAXC);
-            const int b = w_from + ((n * kw) >> a.wk_log2), end = w_from + ((n * (kw + 1)) >> a.wk_log2);
+            const int b = w_from + ((n * kw) >> wk_log2), end = w_from + ((n * (kw + 1)) >> wk_log2);
             w_from += n;
             if (strip * STRIP_ROWS >= P.N) continue;
             w_left = end - b;
@@ -366,6 +401,9 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) mmvq_g_kernel(const __
     auto fetch = [&](Chunk<G> &c) {
         if (w_left == 0) seek();
         if (w_left > 0) {
+            // the run's chunk PFD further on, on its way into L2 without registers
+            if (w_left > PFD && lane * 128 < strip_unit_bytes(G))
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(wp + PFD * strip_unit_bytes(G) + lane * 128));
             load_chunk<G>(c, wp, lane);
             wp += strip_unit_bytes(G);
             w_left--;
@@ -377,6 +415,28 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) mmvq_g_kernel(const __
     fetch(odd);
     if (!ROUTED) pdl_wait();   // weights are never written by the kernel before (see the header); the image may be
 
+    // Pass q's tokens: image rows and output rows, -1 for none (of a warp: its first eight lanes)
+    auto list_tokens = [&](int q) {
+        if (lane >= 8 || q >= passes) return;
+        int row = -1, out = -1;
+        if (ROUTED) {
+            int e, first;
+            find_pass(pre, a.E, q, e, first);
+            const int64_t pos = (int64_t)__ldg(a.offsets + e) + first + lane;
+            const int pairs = a.T * a.k;
+            if (first + lane < clamped_count(a, e) && pos >= 0 && pos < pairs) {
+                const int pr = __ldg(a.items + pos);
+                if (pr >= 0 && pr < pairs) {
+                    out = pr;
+                    row = a.per_pair ? pr : pr / a.k;
+                }
+            }
+        } else if (lane < live_rows(a.live, a.T)) {
+            row = out = lane;
+        }
+        tok_row[q & 1][lane] = row;
+        tok_out[q & 3][lane] = out;
+    };
     auto announce = [&]() {
         if (split > 1) {
             cluster_arrive();
@@ -412,7 +472,7 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) mmvq_g_kernel(const __
         const uint32_t base = (uint32_t)__cvta_generic_to_shared(red + (it & 1) * WARPS * RED);
         for (int v = rank * THREADS + threadIdx.x; v < wr * 256; v += split * THREADS) {
             const int s = v >> 8, tok = (v >> 5) & 7, r = v & 31, n = (rb * wr + s) * STRIP_ROWS + r;
-            const int o = tok_out[pass & 1][tok];
+            const int o = tok_out[pass & 3][tok];
             if (n >= P.N || o < 0) continue;
             float sum = 0.0f;
             for (uint32_t q = 0; q < split; q++) {
@@ -430,45 +490,21 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) mmvq_g_kernel(const __
         }
     };
     int cur_pass = -1, cur_s0 = -1, cur_cols = -1;
-    const int live = ROUTED ? 0 : live_rows(a.live, a.T);
+    if (warp == WARPS - 1 && it0 < it1) list_tokens(ROUTED ? it0 / row_blocks : 0);   // the first item's syncs follow
     for (int it = it0; it < it1; it++) {
         int pass, rb;
         const int j = item_proj(it, pass, rb);
         const GProj &P = a.p[j];
         const bool new_pass = pass != cur_pass;
-        if (new_pass) {
-            __syncthreads();   // the token list of the pass before has been used
-            if (threadIdx.x < 8) {
-                int row = -1, out = -1;
-                if (ROUTED) {
-                    int e, first;
-                    find_pass(pre, a.E, pass, e, first);
-                    const int64_t pos = (int64_t)__ldg(a.offsets + e) + first + threadIdx.x;
-                    const int pairs = a.T * a.k;
-                    if (first + (int)threadIdx.x < clamped_count(a, e) && pos >= 0 && pos < pairs) {
-                        const int pr = __ldg(a.items + pos);
-                        if (pr >= 0 && pr < pairs) {
-                            out = pr;
-                            row = a.per_pair ? pr : pr / a.k;
-                        }
-                    }
-                } else if ((int)threadIdx.x < live) {
-                    row = out = threadIdx.x;
-                }
-                tok_row[threadIdx.x] = row;
-                tok_out[pass & 1][threadIdx.x] = out;   // the pass before is still to be summed
-            }
-            __syncthreads();
-            cur_pass = pass;
-        }
+        cur_pass = pass;
         uint64_t y[4] = {0, 0, 0, 0};
         const bool mine = (rb * wr + ws) * STRIP_ROWS < P.N;
         const int c_hi = share_hi[j];
         for (int s0 = share_lo[j]; s0 < c_hi; s0 += MAXC) {
             const int s1 = min(c_hi, s0 + MAXC), cols = min(P.K, s1 * UNIT_COLS);
             if (new_pass || s0 != cur_s0 || cols != cur_cols) {   // other tokens or columns than the fragments hold
-                __syncthreads();   // every warp is done with the fragments before
-                const int row = tok_row[lane >> 2];
+                __syncthreads();   // every warp is done with the fragments before; the pass's tokens are listed
+                const int row = tok_row[pass & 1][lane >> 2];
                 const uint8_t *img_row = row < 0 ? nullptr : a.img + row * a.img_row_bytes;
                 for (int c = s0 + warp; c < s1; c += WARPS) make_rec<G>(rec[c - s0], img_row, c, P.K, lane);
                 __syncthreads();
@@ -476,8 +512,8 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) mmvq_g_kernel(const __
                 cur_cols = cols;
             }
             if (!mine) continue;
-            const Rec<G> *r = rec + (((s1 - s0) * kw) >> a.wk_log2);
-            const Rec<G> *end = rec + (((s1 - s0) * (kw + 1)) >> a.wk_log2);
+            const Rec<G> *r = rec + (((s1 - s0) * kw) >> wk_log2);
+            const Rec<G> *end = rec + (((s1 - s0) * (kw + 1)) >> wk_log2);
 #pragma unroll 1
             while (r < end) {   // each chunk's registers are refilled as soon as they are used
                 if (turn == 0) {
@@ -491,6 +527,9 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) mmvq_g_kernel(const __
                 turn = 0;
             }
         }
+        // The next pass's tokens, after the first item of this one: the rows of the pass before have been read
+        // (its fragments are made), the outputs of the one before are in another place of four.
+        if (ROUTED && new_pass && warp == WARPS - 1) list_tokens(pass + 1);
         // Warps announce an item's partial sums and wait for the others' an item later, so that none stands
         // still for the slowest. When the wait for item it - 1 is over, item it - 2 has been summed by all,
         // and its buffer may be written.
@@ -571,15 +610,10 @@ int resident_clusters(int split) {
     return n;
 }
 
-// Row blocks of the launch with wk = 1 << wk_log2 warps to a strip.
-int64_t place_rows(GArgs &a, int warps, int wk_log2) {
+template <int WARPS>
+int64_t row_blocks_of_all(const GArgs &a, int wk_log2) {
     int64_t rbs = 0;
-    for (int j = 0; j < a.n_proj; j++) {
-        a.p[j].rb_base = (int)rbs;
-        rbs += ceil_div(ceil_div(a.p[j].N, STRIP_ROWS), warps >> wk_log2);
-    }
-    a.wk_log2 = wk_log2;
-    a.row_blocks = (int)rbs;
+    for (int j = 0; j < a.n_proj; j++) rbs += row_blocks_of<WARPS>(a.p[j].N, wk_log2);
     return rbs;
 }
 
@@ -587,19 +621,13 @@ template <int G, bool ROUTED, int WARPS>
 qk_status launch_form(GArgs &a, int64_t passes, int split, int chunks, cudaStream_t s) {
     const int64_t resident = resident_clusters<G, ROUTED, WARPS>(split);
     if (resident < 1) return fail(QK_ERR_CUDA, "mmvq: no cluster of %d CTAs fits", split);
-    // Warps over rows; over K as well while that leaves CTAs without work or the last round of items more
-    // than a tenth empty (a routed call's passes are not known here: `passes` is the most of them).
-    const int share = (int)ceil_div(chunks, split), held = share < max_chunks(WARPS) ? share : max_chunks(WARPS);
-    int64_t items = 0;
-    for (int wk = 0; (WARPS >> wk) >= 1; wk++) {
-        if (wk > 0 && (held >> wk) < 2) break;
-        items = passes * place_rows(a, WARPS, wk);
-        if (items >= resident && (ROUTED || ceil_div(items, resident) * resident * 10 <= items * 11)) break;
-    }
+    const int share = (int)ceil_div(chunks, split);
+    a.held = share < max_chunks(WARPS) ? share : max_chunks(WARPS);
+    a.wk_log2 = choose_wk<WARPS>(a, passes, resident);   // a routed kernel chooses again by the passes there are
+    const int64_t items = passes * row_blocks_of_all<WARPS>(a, ROUTED ? 3 : a.wk_log2);
     if (items > INT32_MAX) return fail(QK_ERR_UNSUPPORTED, "mmvq: too many rows for one launch");
     const int clusters = (int)(items < resident ? items : resident);
-    a.held = held;
-    const size_t smem = held * sizeof(Rec<G>) + 2 * WARPS * RED * sizeof(float) + (ROUTED ? (a.E + 1) * 4 : 0);
+    const size_t smem = a.held * sizeof(Rec<G>) + 2 * WARPS * RED * sizeof(float) + (ROUTED ? (a.E + 1) * 4 : 0);
     auto kernel = mmvq_g_kernel<G, ROUTED, WARPS>;
     constexpr int THREADS = WARPS * 32;
     cudaLaunchConfig_t cfg = {};
@@ -631,9 +659,9 @@ qk_status launch_matvec(GArgs &a, int64_t passes, cudaStream_t s) {
     // of K. Else, or where K's fragments do not fit, K is shared by the most CTAs (up to 8) whose equal
     // shares waste at most a tenth.
     const int sms = sm_count();
-    if (chunks <= max_chunks(FEW_WARPS) && passes * place_rows(a, FEW_WARPS, 1) >= 4 * sms)
+    if (chunks <= max_chunks(FEW_WARPS) && passes * row_blocks_of_all<FEW_WARPS>(a, 1) >= 4 * sms)
         return launch_form<G, ROUTED, FEW_WARPS>(a, passes, 1, chunks, s);
-    if (chunks <= max_chunks(MANY_WARPS) && passes * place_rows(a, MANY_WARPS, 2) >= 2 * sms)
+    if (chunks <= max_chunks(MANY_WARPS) && passes * row_blocks_of_all<MANY_WARPS>(a, 2) >= 2 * sms)
         return launch_form<G, ROUTED, MANY_WARPS>(a, passes, 1, chunks, s);
     int split = 1;
     for (int q = 2; q <= 8 && q <= chunks; q++)
