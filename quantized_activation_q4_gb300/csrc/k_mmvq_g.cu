@@ -197,26 +197,32 @@ __device__ __forceinline__ void chunk_product(const Chunk<G> &c, const Rec<G> &r
 }
 
 // A warp's fragments of one chunk: lane (g, t) converts words t of token g's blocks. Columns past K and
-// absent tokens (row < 0) are zeros; nothing of them is read.
-template <int G>
-__device__ __forceinline__ void make_rec(Rec<G> &r, const uint8_t *img_row, int chunk, int K, int lane) {
-    const int g = lane >> 2, t = lane & 3;
+// absent tokens (no row) are zeros; nothing of them is read. Loads and conversion apart, so that two
+// chunks' loads are in flight at once.
+struct Words {
     uint32_t lo[4], hi[4], ds[4];
+};
+__device__ __forceinline__ void load_words(Words &w, const uint8_t *img_row, int chunk, int K, int lane) {
+    const int t = lane & 3;
 #pragma unroll
     for (int jb = 0; jb < 4; jb++) {
-        lo[jb] = hi[jb] = ds[jb] = 0;
+        w.lo[jb] = w.hi[jb] = w.ds[jb] = 0;
         if (img_row && chunk * UNIT_COLS + jb * QB < K) {
             const uint8_t *blk = img_row + (int64_t)(4 * chunk + jb) * Q8_1_BYTES;
-            ds[jb] = __ldg(reinterpret_cast<const unsigned int *>(blk));
-            lo[jb] = __ldg(reinterpret_cast<const unsigned int *>(blk + 4 + 4 * t));
-            hi[jb] = __ldg(reinterpret_cast<const unsigned int *>(blk + 20 + 4 * t));
+            w.ds[jb] = __ldg(reinterpret_cast<const unsigned int *>(blk));
+            w.lo[jb] = __ldg(reinterpret_cast<const unsigned int *>(blk + 4 + 4 * t));
+            w.hi[jb] = __ldg(reinterpret_cast<const unsigned int *>(blk + 20 + 4 * t));
         }
     }
+}
+template <int G>
+__device__ __forceinline__ void make_rec(Rec<G> &r, const Words &w, int lane) {
+    const int g = lane >> 2, t = lane & 3;
     float xs = 0.0f;
 #pragma unroll
     for (int jb = 0; jb < 4; jb++) {
         // codes -> exact halves: q + 128 under the exponent of 1024, minus 1152
-        const uint32_t u = lo[jb] ^ 0x80808080u, v = hi[jb] ^ 0x80808080u;
+        const uint32_t u = w.lo[jb] ^ 0x80808080u, v = w.hi[jb] ^ 0x80808080u;
         const __half2 bias = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
         const uint32_t p[4] = {__byte_perm(u, 0x64646464u, 0x4240), __byte_perm(u, 0x64646464u, 0x4341),
                                __byte_perm(v, 0x64646464u, 0x4240), __byte_perm(v, 0x64646464u, 0x4341)};
@@ -227,13 +233,13 @@ __device__ __forceinline__ void make_rec(Rec<G> &r, const uint8_t *img_row, int 
             o[i] = *reinterpret_cast<const uint32_t *>(&x);
         }
         r.b[jb][lane] = make_uint4(o[0], o[1], o[2], o[3]);
-        int sl = __dp4a((int)lo[jb], 0x01010101, 0), sh = __dp4a((int)hi[jb], 0x01010101, 0);
+        int sl = __dp4a((int)w.lo[jb], 0x01010101, 0), sh = __dp4a((int)w.hi[jb], 0x01010101, 0);
 #pragma unroll
         for (int m = 1; m <= 2; m <<= 1) {
             sl += __shfl_xor_sync(FULL, sl, m);
             sh += __shfl_xor_sync(FULL, sh, m);
         }
-        const float da = __half2float(__ushort_as_half((unsigned short)ds[jb]));
+        const float da = __half2float(__ushort_as_half((unsigned short)w.ds[jb]));
         xs = fmaf(da, (float)(sl + sh), (jb * QB) % G == 0 ? 0.0f : xs);
         if (t == 0) {
             r.da[jb][g] = da;
@@ -506,7 +512,14 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) mmvq_g_kernel(const __
                 __syncthreads();   // every warp is done with the fragments before; the pass's tokens are listed
                 const int row = tok_row[pass & 1][lane >> 2];
                 const uint8_t *img_row = row < 0 ? nullptr : a.img + row * a.img_row_bytes;
-                for (int c = s0 + warp; c < s1; c += WARPS) make_rec<G>(rec[c - s0], img_row, c, P.K, lane);
+#pragma unroll 1
+                for (int c = s0 + warp; c < s1; c += 2 * WARPS) {
+                    Words w0, w1;
+                    load_words(w0, img_row, c, P.K, lane);
+                    load_words(w1, c + WARPS < s1 ? img_row : nullptr, c + WARPS, P.K, lane);
+                    make_rec<G>(rec[c - s0], w0, lane);
+                    if (c + WARPS < s1) make_rec<G>(rec[c + WARPS - s0], w1, lane);
+                }
                 __syncthreads();
                 cur_s0 = s0;
                 cur_cols = cols;
