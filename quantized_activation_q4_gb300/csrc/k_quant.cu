@@ -332,69 +332,176 @@ __global__ void __launch_bounds__(256) glu_q8_1_kernel(
     }
 }
 
-// The GLU producer of the prefill planes: input rows of binary32 or bfloat16 (BF16), output codes
-// and half scales as qk_quantize_q8_0 of the binary32 products, which are stored only when `out`
-// is given. Grid and columns as glu_q8_1_kernel.
+// ---------------------------------------------------------------- GLU producer of the prefill planes
+// Input rows of binary32 or bfloat16, codes and half scales as qk_quantize_q8_0 of the binary32 products,
+// which are stored only when `out` is given.
+//
+// Bound by memory once an element costs about 20 instructions (with IEEE divisions and expf it cost 90:
+// 26600 x 768 bfloat16 pairs took 59 us):
+//   - the sigmoid kinds are g / (1 + 2^(-c g)) with ex2.approx and rcp.approx. Relative errors: the
+//     exponent's rounding |c g| 2^-24 and 2^-22 of ex2, weighted by the sigmoid's share e / (1 + e), and
+//     2^-23 each of rcp and the products: below 1e-6 of the result or 3e-7 of |g u| everywhere.
+//     GeGLU-tanh is one of them: 0.5 (1 + tanh z) = 1 / (1 + e^(-2z)), with no cancellation;
+//   - codes are rint(x * (1 / d)), d's reciprocal once per block. It differs from rint(x / d) only where
+//     the quotient is within 127 * 2^-23 of a tie: blocks with an element that near (and scales outside
+//     1e-30 .. 1e30) divide, so the bytes are qk_quantize_q8_0's.
+// A group of four lanes has a quant block, eight columns a lane; a thread has two blocks' loads in flight.
+// A CTA of 64 groups takes 128 consecutive blocks of a row, or as many whole rows as 128 blocks hold.
+// Eight columns as they are in memory, and their binary32 values: loads in flight cost few registers.
 template <bool BF16>
-__device__ __forceinline__ void load4_elem(const void *p, int64_t i, float v[4]) {
-    if (BF16) {
-        const uint16_t *q = static_cast<const uint16_t *>(p) + i;
-        if ((reinterpret_cast<uintptr_t>(q) & 7u) == 0) {
-            const uint2 w = __ldg(reinterpret_cast<const uint2 *>(q));
-            v[0] = __uint_as_float(w.x << 16);
-            v[1] = __uint_as_float(w.x & 0xffff0000u);
-            v[2] = __uint_as_float(w.y << 16);
-            v[3] = __uint_as_float(w.y & 0xffff0000u);
-        } else {
+struct Raw8 {
+    uint4 w[BF16 ? 1 : 2];
+    __device__ __forceinline__ void load(const void *p, int64_t i) {
+        const uint8_t *q = static_cast<const uint8_t *>(p) + i * (BF16 ? 2 : 4);
+        if ((reinterpret_cast<uintptr_t>(q) & 15u) == 0) {
 #pragma unroll
-            for (int j = 0; j < 4; j++) v[j] = __uint_as_float((uint32_t)__ldg(q + j) << 16);
+            for (int h = 0; h < (BF16 ? 1 : 2); h++) w[h] = __ldg(reinterpret_cast<const uint4 *>(q) + h);
+        } else {
+            uint32_t x[BF16 ? 4 : 8];
+#pragma unroll
+            for (int j = 0; j < (BF16 ? 4 : 8); j++) {
+                if (BF16)
+                    x[j] = __ldg(reinterpret_cast<const unsigned short *>(q) + 2 * j) |
+                           (uint32_t)__ldg(reinterpret_cast<const unsigned short *>(q) + 2 * j + 1) << 16;
+                else
+                    x[j] = __ldg(reinterpret_cast<const unsigned int *>(q) + j);
+            }
+#pragma unroll
+            for (int h = 0; h < (BF16 ? 1 : 2); h++) w[h] = make_uint4(x[4 * h], x[4 * h + 1], x[4 * h + 2], x[4 * h + 3]);
         }
-    } else {
-        load4(static_cast<const float *>(p) + i, 4, v);
     }
+    __device__ __forceinline__ float operator[](int j) const {
+        const uint4 v = w[BF16 ? 0 : j >> 2];
+        const int k = BF16 ? j >> 1 : j & 3;
+        const uint32_t x = k == 0 ? v.x : k == 1 ? v.y : k == 2 ? v.z : v.w;
+        return __uint_as_float(!BF16 ? x : (j & 1) ? x & 0xffff0000u : x << 16);
+    }
+};
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float rcp(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+// x / (1 + e^-y), c = -log2(e) y
+__device__ __forceinline__ float gated(float x, float c) { return x * rcp(1.0f + ex2(c)); }
+constexpr float LOG2E = 1.4426950408889634f;
+
+template <int KIND>
+__device__ __forceinline__ float glu_fast(float g, float u, float alpha_log2e, float limit) {
+    if (KIND == QK_GLU_SWIGLU) return gated(g, -LOG2E * g) * u;
+    if (KIND == QK_GLU_GEGLU_TANH) {   // 2 sqrt(2/pi) log2(e) (g + 0.044715 g^3)
+        const float c = -2.0f * 0.7978845608028654f * LOG2E;
+        return gated(g, c * g * fmaf(0.044715f * g, g, 1.0f)) * u;
+    }
+    if (KIND == QK_GLU_GEGLU_QUICK) return gated(g, -1.702f * LOG2E * g) * u;
+    if (KIND == QK_GLU_SWIGLU_OAI || KIND == QK_GLU_SWIGLU_CLAMP) {
+        const float x = fminf(g, limit), v = fminf(fmaxf(u, -limit), limit);
+        return KIND == QK_GLU_SWIGLU_OAI ? gated(x, -alpha_log2e * x) * (v + 1.0f) : gated(x, -LOG2E * x) * v;
+    }
+    return glu_out(KIND, g, u, 0.0f, 0.0f);   // GeGLU-erf, ReGLU
 }
 
-template <bool BF16>
-__global__ void __launch_bounds__(256) glu_q8_0_kernel(
-    int kind, int layout, const void *__restrict__ a, int64_t a_stride, const void *__restrict__ b, int64_t b_stride,
-    int N, float *__restrict__ out, int64_t out_stride, int8_t *__restrict__ qs, uint16_t *__restrict__ dh,
-    int64_t row_blocks, int T, float alpha, float limit, const int32_t *live) {
+template <int KIND, bool BF16>
+__global__ void __launch_bounds__(256, BF16 ? 6 : 4) glu_q8_0_kernel(
+    int layout, const void *__restrict__ a, int64_t a_stride, const void *__restrict__ b, int64_t b_stride, int N,
+    float *__restrict__ out, int64_t out_stride, int8_t *__restrict__ qs, uint16_t *__restrict__ dh,
+    int64_t row_blocks, int T, int rows_per_cta, int step_row, int step_blk, float alpha, float limit,
+    const int32_t *live) {
     pdl_trigger();
     pdl_wait();
-    const int64_t t = blockIdx.x;
-    const int tid = threadIdx.x, j8 = tid & 7;
-    const int c = blockIdx.y * 1024 + 4 * tid;
-    const bool ok = c < N;
-    float gv[4] = {0.f, 0.f, 0.f, 0.f}, uv[4] = {0.f, 0.f, 0.f, 0.f};
-    if (ok) {
-        const int64_t first = t * a_stride + c;
-        load4_elem<BF16>(a, layout == QK_GLU_PACKED_SWAPPED ? first + N : first, gv);
-        if (layout == QK_GLU_SEPARATE)
-            load4_elem<BF16>(b, t * b_stride + c, uv);
-        else
-            load4_elem<BF16>(a, layout == QK_GLU_PACKED ? first + N : first, uv);
+    const int kb = N / QB, group = threadIdx.x >> 2, l4 = threadIdx.x & 3;
+    int64_t row[2];
+    int blk[2];
+    Raw8<BF16> g[2], u[2];
+    int r0 = 0;
+    blk[0] = blockIdx.y * 128 + group;
+    if (rows_per_cta > 1) {   // groups run over whole rows; the second block is 64 groups on
+        r0 = group / kb;
+        blk[0] = group - r0 * kb;
     }
-    if (t >= live_rows(live, T)) return;
-    float v[4] = {0.f, 0.f, 0.f, 0.f};
-    if (ok) {
 #pragma unroll
-        for (int i = 0; i < 4; i++) v[i] = glu_out(kind, gv[i], uv[i], alpha, limit);
-        if (out) store4(out + t * out_stride + c, v);
+    for (int h = 0; h < 2; h++) {   // row -1: nothing for this group
+        if (h == 1) {
+            blk[1] = blk[0] + step_blk;
+            r0 += step_row;
+            if (rows_per_cta > 1 && blk[1] >= kb) {
+                blk[1] -= kb;
+                r0++;
+            }
+        }
+        row[h] = (int64_t)blockIdx.x * rows_per_cta + r0;
+        if (r0 >= rows_per_cta || row[h] >= T || blk[h] >= kb) row[h] = -1;
+        // loaded together with the live count (row < T is in the caller's buffers even when it is padding)
+        if (row[h] >= 0) {
+            const int64_t c = blk[h] * QB + 8 * l4, first = row[h] * a_stride + c;
+            g[h].load(a, layout == QK_GLU_PACKED_SWAPPED ? first + N : first);
+            if (layout == QK_GLU_SEPARATE)
+                u[h].load(b, row[h] * b_stride + c);
+            else
+                u[h].load(a, layout == QK_GLU_PACKED ? first + N : first);
+        }
     }
-    uint32_t codes;
-    int sum;
-    const float d = kind == QK_GLU_REGLU ? q8_block<true>(v, &codes, &sum) : q8_block(v, &codes, &sum);
-    if (ok) {
-        const int64_t blk = t * row_blocks + c / QB;
-        reinterpret_cast<uint32_t *>(qs + blk * QB)[j8] = codes;
-        if (j8 == 0) dh[blk] = __half_as_ushort(__float2half_rn(d));
-    }
-    if (blockIdx.y == 0) {  // zero blocks of the row padding
-        for (int64_t bb = N / QB + tid; bb < row_blocks; bb += 256) {
-            uint32_t *p = reinterpret_cast<uint32_t *>(qs + (t * row_blocks + bb) * QB);
+    const int n_live = live_rows(live, T);
+    const float alpha_log2e = alpha * LOG2E;
 #pragma unroll
-            for (int i = 0; i < 8; i++) p[i] = 0u;
-            dh[t * row_blocks + bb] = 0;
+    for (int h = 0; h < 2; h++) {
+        const bool on = row[h] >= 0 && row[h] < n_live;
+        float v[8], m = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            v[i] = on ? glu_fast<KIND>(g[h][i], u[h][i], alpha_log2e, limit) : 0.0f;
+            m = fmaxf(m, fabsf(v[i]));
+        }
+        m = fmaxf(m, __shfl_xor_sync(FULL, m, 1));
+        m = fmaxf(m, __shfl_xor_sync(FULL, m, 2));
+        if (!on) continue;   // a block's four lanes agree
+        const float d = m / 127.0f, inv = 1.0f / d;
+        constexpr float MAGIC = 12582912.0f;   // 1.5 * 2^23: the sum's low byte is the rounded code
+        uint32_t t[8];
+        bool clear = d > 1e-30f && d < 1e30f;   // false for NaN as well
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            const float r = v[i] * inv, s = r + MAGIC;
+            t[i] = __float_as_uint(s);
+            clear = clear && fabsf(r - (s - MAGIC)) < 0.5f - 4.0e-5f;
+        }
+        // |x / d| <= 127 and two roundings of 2^-24 each (inv, r) against one (x / d)
+        if (!clear) {
+#pragma unroll
+            for (int i = 0; i < 8; i++) t[i] = m != 0.0f ? (uint32_t)__float2int_rn(v[i] / d) : 0u;
+        }
+        const uint32_t lo = __byte_perm(__byte_perm(t[0], t[1], 0x0040), __byte_perm(t[2], t[3], 0x0040), 0x5410);
+        const uint32_t hi = __byte_perm(__byte_perm(t[4], t[5], 0x0040), __byte_perm(t[6], t[7], 0x0040), 0x5410);
+        if (out) {
+            float *o = out + row[h] * out_stride + blk[h] * QB + 8 * l4;
+            store4(o, v);
+            store4(o + 4, v + 4);
+        }
+        const int64_t at = row[h] * row_blocks + blk[h];
+        uint32_t *q = reinterpret_cast<uint32_t *>(qs + at * QB) + 2 * l4;
+        if ((reinterpret_cast<uintptr_t>(q) & 7u) == 0) {
+            *reinterpret_cast<uint2 *>(q) = make_uint2(lo, hi);
+        } else {
+            q[0] = lo;
+            q[1] = hi;
+        }
+        if (l4 == 0) dh[at] = __half_as_ushort(__float2half_rn(d));
+    }
+    if (blockIdx.y == 0 && kb < row_blocks) {   // zero blocks of the rows' padding
+        for (int r = 0; r < rows_per_cta; r++) {
+            const int64_t t = (int64_t)blockIdx.x * rows_per_cta + r;
+            if (t >= n_live) break;
+            for (int64_t bb = kb + threadIdx.x; bb < row_blocks; bb += 256) {
+                uint32_t *p = reinterpret_cast<uint32_t *>(qs + (t * row_blocks + bb) * QB);
+#pragma unroll
+                for (int i = 0; i < 8; i++) p[i] = 0u;
+                dh[t * row_blocks + bb] = 0;
+            }
         }
     }
 }
@@ -489,14 +596,28 @@ qk_status launch_glu_q8_1(int kind, int layout, const float *a, int64_t a_stride
                       N, out, out_stride, img, row_blocks, T, alpha, limit, live);
 }
 
+template <bool BF16>
+static auto glu_q8_0_of(int kind) -> decltype(&glu_q8_0_kernel<0, BF16>) {
+    switch (kind) {
+        case QK_GLU_SWIGLU: return glu_q8_0_kernel<QK_GLU_SWIGLU, BF16>;
+        case QK_GLU_GEGLU_TANH: return glu_q8_0_kernel<QK_GLU_GEGLU_TANH, BF16>;
+        case QK_GLU_REGLU: return glu_q8_0_kernel<QK_GLU_REGLU, BF16>;
+        case QK_GLU_GEGLU_ERF: return glu_q8_0_kernel<QK_GLU_GEGLU_ERF, BF16>;
+        case QK_GLU_GEGLU_QUICK: return glu_q8_0_kernel<QK_GLU_GEGLU_QUICK, BF16>;
+        case QK_GLU_SWIGLU_OAI: return glu_q8_0_kernel<QK_GLU_SWIGLU_OAI, BF16>;
+        default: return glu_q8_0_kernel<QK_GLU_SWIGLU_CLAMP, BF16>;
+    }
+}
+
 qk_status launch_glu_q8_0(int kind, int layout, int elem, const void *a, int64_t a_stride, const void *b,
                           int64_t b_stride, int T, int N, float *out, int64_t out_stride, int8_t *qs, uint16_t *d,
                           int64_t row_blocks, float alpha, float limit, const int32_t *live, cudaStream_t s) {
     if (T == 0) return QK_OK;
-    dim3 grid((unsigned)T, (unsigned)ceil_div(N, 1024));
-    return launch_pdl("glu_q8_0", elem == QK_ELEM_BF16 ? glu_q8_0_kernel<true> : glu_q8_0_kernel<false>, grid,
-                      dim3(256), 0, s, kind, layout, a, a_stride, b, b_stride, N, out, out_stride, qs, d, row_blocks,
-                      T, alpha, limit, live);
+    const int kb = N / QB, rows = kb >= 128 ? 1 : 128 / kb;   // rows of a CTA
+    dim3 grid((unsigned)ceil_div(T, rows), (unsigned)(rows > 1 ? 1 : ceil_div(kb, 128)));
+    return launch_pdl("glu_q8_0", elem == QK_ELEM_BF16 ? glu_q8_0_of<true>(kind) : glu_q8_0_of<false>(kind), grid,
+                      dim3(256), 0, s, layout, a, a_stride, b, b_stride, N, out, out_stride, qs, d, row_blocks, T, rows,
+                      rows > 1 ? 64 / kb : 0, rows > 1 ? 64 % kb : 64, alpha, limit, live);
 }
 
 }  // namespace qk

@@ -106,6 +106,33 @@ def test_glu_parameters_and_zero_blocks():
     assert np.all(host(qs) == 0) and np.all((host(dh) & 0x7FFF) == 0)
 
 
+@pytest.mark.parametrize("elem", ["f32", "bf16"])
+def test_glu_codes_at_ties_and_extremes(elem):
+    """Quotients at and next to ties, scales from subnormal to near overflow, infinities and NaN: the
+    planes are the bytes that qk_quantize_q8_0 makes of the output."""
+    import torch
+    rng = synth.rng(13250)
+    N, rows = 256, 64
+    g = np.zeros((rows, N), dtype=np.float32)
+    for r in range(rows):
+        half = rng.integers(0, 127, size=N).astype(np.float32) + 0.5
+        step = np.float32(2.0) ** rng.integers(-140, 110)
+        nudge = rng.integers(-2, 3, size=N, dtype=np.int32)   # up to two units in the last place off a tie
+        v = (half * step).astype(np.float32)
+        g[r] = (v.view(np.int32) + nudge).view(np.float32) if r % 2 else v
+        g[r, ::32] = np.float32(127.0) * step                 # the block's largest: d is `step`
+    g[60, 5], g[61, 7], g[62, ::3] = np.inf, np.nan, np.inf
+    g[63, 64:96] = np.nan
+    a = dev(g).to(torch.bfloat16 if elem == "bf16" else torch.float32)
+    b = torch.ones_like(a)
+    out = torch.zeros((rows, N), device="cuda")
+    qs, d = torch.zeros((rows, N), dtype=torch.int8, device="cuda"), torch.zeros((rows, N // 32), dtype=torch.int16, device="cuda")
+    qk.qk_glu_q8_0("reglu", "separate", elem, a, N, b, N, rows, N, out, N, qs, d, N // 32)
+    q2, d2 = torch.zeros_like(qs), torch.zeros_like(d)
+    qk.qk_quantize_q8_0(out, rows, N, N, q2, d2, N // 32)
+    assert torch.equal(qs, q2) and torch.equal(d, d2)
+
+
 # ------------------------------------------------------------------ combine
 @pytest.mark.parametrize("rows,k,N,live,pad", [(1, 1, 4, 1, 0), (24, 8, 2560, 17, 0), (7, 3, 1028, 7, 4), (300, 2, 64, 0, 8),
                                                (2000, 8, 96, 1999, 0), (3, 64, 4100, 3, 12)])
