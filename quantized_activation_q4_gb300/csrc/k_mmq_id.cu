@@ -25,7 +25,7 @@
 //   warp 1:       allocates tensor memory, issues the MMAs (one elected thread)
 //   warps 2-17:   packed nibbles -> binary16 A stages, two groups of eight warps in turn
 //   warps 18-25:  accumulator -> bfloat16 rows, scattered to the pairs' output rows
-//   warp 26:      the pass's activation rows by tensor copies, 64 K columns x 32 rows each
+//   warp 26:      the pass's activation rows, a tensor copy per stage
 //   warp 27:      looks the items up, up to four ahead of the epilogue (a descriptor and the pass's pair
 //                 list per item), so that no other warp waits for the plan's words
 // A wait on a barrier costs 90 to 200 cycles even when its phase is complete, so the MMA warp looks at
@@ -48,7 +48,7 @@ constexpr int MAX_E = 1024;
 constexpr int TM = 128;              // weight rows per item (MMA M)
 constexpr int KC = 64;               // K elements of one activation box (a 128-byte swizzle row)
 constexpr int SK = 128;              // K elements per stage
-constexpr int BOX_ROWS = 32;         // rows of one activation copy
+constexpr int BOX_ROWS = 32;         // activation copies come in multiples of so many rows
 constexpr int U_SLOT = Q4_UNIT_BYTES;
 constexpr uint32_t A_COLS = SK / 2;  // tensor-memory columns of an A stage
 constexpr uint32_t TMEM_COLS = 512;
@@ -79,7 +79,7 @@ struct Shape {
     static constexpr int TN = TN_;
     static constexpr int NS = (512 - 2 * TN) / 64;      // stages
     static constexpr int NU = 6;                        // packed-weight slots
-    static constexpr int B_BOX = TN * KC * 2, B_STAGE = TN * SK * 2;
+    static constexpr int B_STAGE = TN * SK * 2;
     static constexpr uint32_t A_TMEM = 2 * TN;
     // shared memory: [B stages][weights][epilogue][descriptors][pass prefix][barriers][tensor-memory address,
     // item count]
@@ -103,7 +103,9 @@ struct IdProj {
     int N, K, chunks, rt_begin;   // rt_begin: first row tile of this projection in the launch
 };
 struct IdArgs {
-    CUtensorMap bmap;             // activations [pairs][K] binary16 in plan order, box 64 x 32, swizzled
+    // activations [pairs][K] binary16 in plan order, seen as [K / 64][pairs][64]: boxes of two 64-column
+    // slabs x 32, 64, 96 or 128 rows, swizzled
+    CUtensorMap bmap[4];
     const int32_t *counts, *offsets, *items;
     int pairs, k, E, per_pair, n_proj, row_tiles;
     IdProj p[MAX_PROJ];
@@ -204,6 +206,13 @@ __device__ __forceinline__ void tc_mma_add(uint32_t tmem, uint32_t a_tmem, uint6
         "r"(a_tmem), "l"(b), "r"(idesc)
         : "memory");
 }
+// a box at column 0, row y, slab z
+__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap *map, int y, int z, uint32_t mbar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(y), "r"(z), "r"(mbar)
+        : "memory");
+}
 // 16 accumulator columns of this warp's 32 rows to bfloat16 in shared memory, 64 bytes per column: with
 // the 16x256b shape lane 4g + t holds rows g and g + 8 of columns 2t, 2t+1 (and 8+2t, 9+2t), the fragments
 // that stmatrix transposes, so that 8 rows of a column are 16 consecutive bytes. Piece c (rows 8c..) of
@@ -281,7 +290,7 @@ __global__ void __launch_bounds__(256) dequant_pairs_kernel(const int8_t *__rest
                                                             const uint16_t *__restrict__ d, int64_t row_blocks,
                                                             const int32_t *__restrict__ offsets,
                                                             const int32_t *__restrict__ items, int E, int pairs, int k,
-                                                            int per_pair, int kb, __half *__restrict__ B) {
+                                                            int per_pair, int kb, int64_t pitch, __half *__restrict__ B) {
     pdl_trigger();
     pdl_wait();
     const int pos = blockIdx.x * 8 + (threadIdx.x >> 5), w = threadIdx.x & 3, b0 = (threadIdx.x & 31) >> 2;
@@ -289,7 +298,7 @@ __global__ void __launch_bounds__(256) dequant_pairs_kernel(const int8_t *__rest
     const int p = __ldg(items + pos);
     if (p < 0 || p >= pairs) return;
     const int64_t first = (per_pair ? p : p / k) * row_blocks;
-    __half *dst = B + (int64_t)pos * kb * QB;
+    __half *dst = B + pos * pitch;
 #pragma unroll 4
     for (int b = b0; b < kb; b += 8) dequant_word(qs, d, first + b, w, dst + (int64_t)b * QB);
 }
@@ -449,23 +458,19 @@ __global__ void __launch_bounds__(THREADS, 1) mmq_id_kernel(const __grid_constan
         for (int i = 0; i < mine && ok; i++) {
             if (!await_info(i)) break;
             const Info &f = info[i % NI];
-            const int K = f.K, first = f.first, boxes = (((f.n + 15) & ~15) + BOX_ROWS - 1) / BOX_ROWS;
+            const int slabs = (f.K + KC - 1) / KC, first = f.first, boxes = (f.n + BOX_ROWS - 1) / BOX_ROWS;
+            const CUtensorMap *map = &a.bmap[boxes - 1];
+            const uint32_t bytes = boxes * BOX_ROWS * SK * 2;   // a slab past K counts, filled with zeros
             release_info(i);
-            for (int k0 = 0; k0 < K; k0 += SK, issued++) {
+            for (int slab = 0; slab < slabs; slab += 2, issued++) {
                 if (!warp_wait(empty + 8 * r.at, r.parity ^ 1)) {
                     ok = false;
                     break;
                 }
                 if (elect_one()) {
-                    const uint32_t dst = sbase + r.at * S::B_STAGE, bar = full + 8 * r.at;
-                    const bool two = K - k0 > KC;
-                    mbar_expect_tx(bar, (uint32_t)(boxes * BOX_ROWS * KC * 2) << (two ? 1 : 0));
-#pragma unroll
-                    for (int b = 0; b < TN / BOX_ROWS; b++) {
-                        if (b >= boxes) break;
-                        tma_2d(dst + b * (BOX_ROWS * KC * 2), &a.bmap, k0, first + b * BOX_ROWS, bar);
-                        if (two) tma_2d(dst + S::B_BOX + b * (BOX_ROWS * KC * 2), &a.bmap, k0 + KC, first + b * BOX_ROWS, bar);
-                    }
+                    const uint32_t bar = full + 8 * r.at;
+                    mbar_expect_tx(bar, bytes);
+                    tma_3d(sbase + r.at * S::B_STAGE, map, first, slab, bar);
                 }
                 __syncwarp();
                 r.next(NS);
@@ -484,6 +489,7 @@ __global__ void __launch_bounds__(THREADS, 1) mmq_id_kernel(const __grid_constan
             const int n = info[i % NI].n, K = info[i % NI].K;
             release_info(i);
             const uint32_t idesc = mma_idesc((n + 15) & ~15), acc = tmem + (i & 1) * TN;
+            const uint32_t slab16 = (n + BOX_ROWS - 1) / BOX_ROWS * (BOX_ROWS * KC * 2 / 16);   // a slab's rows, in descriptor units
             for (int left = K; left > 0;) {   // nothing past K enters the sum
                 // one look at the next four stages, a lane for each: how many are complete, at least one
                 Ring q = r;
@@ -510,11 +516,11 @@ __global__ void __launch_bounds__(THREADS, 1) mmq_id_kernel(const __grid_constan
                         if (l >= SK) {
 #pragma unroll
                             for (int ks = 1; ks < SK / 16; ks++)
-                                tc_mma_add(acc, ta + 8 * ks, bd + (uint64_t)((ks >> 2) * (S::B_BOX / 16) + 2 * (ks & 3)), idesc);
+                                tc_mma_add(acc, ta + 8 * ks, bd + (uint64_t)((ks >> 2) * slab16 + 2 * (ks & 3)), idesc);
                         } else {
 #pragma unroll 1
                             for (int ks = 1; 16 * ks < l; ks++)
-                                tc_mma_add(acc, ta + 8 * ks, bd + (uint64_t)((ks >> 2) * (S::B_BOX / 16) + 2 * (ks & 3)), idesc);
+                                tc_mma_add(acc, ta + 8 * ks, bd + (uint64_t)((ks >> 2) * slab16 + 2 * (ks & 3)), idesc);
                         }
                         tc_commit(empty + 8 * at);
                         at = at + 1 == NS ? 0 : at + 1;
@@ -640,7 +646,9 @@ qk_status launch_type(const IdArgs &a, cudaStream_t s) {
 
 }  // namespace
 
-int64_t mmq_id_workspace_bytes(int64_t pairs, int64_t kmax) { return (pairs * kmax * 2 + 127) / 128 * 128; }
+// columns of an activation row in the workspace: whole 64-column slabs
+static int64_t act_pitch(int64_t kmax) { return (kmax + KC - 1) / KC * KC; }
+int64_t mmq_id_workspace_bytes(int64_t pairs, int64_t kmax) { return pairs * act_pitch(kmax) * 2; }
 
 qk_status read_mmq_id_faults(uint32_t *faults) {
     unsigned int v = 0, zero = 0;
@@ -658,18 +666,21 @@ qk_status launch_mmq_id(const int8_t *qs, const uint16_t *d, int64_t row_blocks,
     for (int j = 0; j < n_proj; j++) kmax = projs[j].K > kmax ? projs[j].K : kmax;
     IdArgs a = {};
     const int pairs = rows * k, kb = (int)(kmax / QB);
+    const int64_t pitch = act_pitch(kmax), slabs = pitch / KC;
     PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
     if (!enc) return fail(QK_ERR_CUDA, "mmq_id: cuTensorMapEncodeTiled is not available");
-    const cuuint64_t dims[2] = {(cuuint64_t)kmax, (cuuint64_t)pairs};
-    const cuuint64_t strides[1] = {(cuuint64_t)kmax * 2};
-    const cuuint32_t box[2] = {KC, BOX_ROWS}, estr[2] = {1, 1};
-    const CUresult r = enc(&a.bmap, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, ws, dims, strides, box, estr,
-                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    if (r != CUDA_SUCCESS) return fail(QK_ERR_CUDA, "mmq_id: tensor map encoding failed (%d)", (int)r);
+    for (int h = 0; h < 4; h++) {
+        const cuuint64_t dims[3] = {KC, (cuuint64_t)pairs, (cuuint64_t)slabs};
+        const cuuint64_t strides[2] = {(cuuint64_t)pitch * 2, KC * 2};
+        const cuuint32_t box[3] = {KC, (cuuint32_t)(BOX_ROWS * (h + 1)), 2}, estr[3] = {1, 1, 1};
+        const CUresult r = enc(&a.bmap[h], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, ws, dims, strides, box, estr,
+                               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+        if (r != CUDA_SUCCESS) return fail(QK_ERR_CUDA, "mmq_id: tensor map encoding failed (%d)", (int)r);
+    }
     qk_status st = launch_pdl("mmq_id_dequant", dequant_pairs_kernel, dim3((unsigned)ceil_div(pairs, 8)),
                               dim3(256), 0, s, qs, d, row_blocks, offsets, items, (int)projs[0].n_experts, pairs, k,
-                              (int)per_pair, kb, static_cast<__half *>(ws));
+                              (int)per_pair, kb, pitch, static_cast<__half *>(ws));
     if (st != QK_OK) return st;
     a.counts = counts;
     a.offsets = offsets;
