@@ -28,8 +28,9 @@
 //   warp 26:      the pass's activation rows, a tensor copy per stage
 //   warp 27:      looks the items up, up to four ahead of the epilogue (a descriptor and the pass's pair
 //                 list per item), so that no other warp waits for the plan's words
-// A wait on a barrier costs 90 to 200 cycles even when its phase is complete, so the MMA warp looks at
-// the barriers of four stages at once, and copies and converters run on rings.
+// The single warps run their whole loops in one elected thread: votes and re-elections at every stage cost
+// the MMA warp 700 cycles a batch of two stages. A look at a barrier takes 90 cycles or more even when its
+// phase is complete, so the MMA thread looks at the next stage's before it issues this one's MMAs.
 // The conversion of the weights is that of the dense prefill kernel (k_mmq.cu).
 // Measured and dropped: gathering the rows out of the unsorted image, by four-row tensor copies (issued
 // lane by lane, about 85 cycles each: 4096-row gate/up 1338 us) and by 16-byte asynchronous copies of
@@ -415,24 +416,24 @@ __global__ void __launch_bounds__(THREADS, 1) mmq_id_kernel(const __grid_constan
             if (lane == 0) mbar_arrive(info_full + 8 * (i % NI));
         }
     } else if (warp == 0) {   // ---------------- weights
-        Ring u = {0, 0};
-        uint32_t issued = 0;   // weight stages issued by this CTA
-        bool ok = true;
-        for (int i = 0; i < mine && ok; i++) {
-            if (!await_info(i)) break;
-            const Info &f = info[i % NI];
-            const IdProj &P = a.p[f.j];
-            const int chunks = P.chunks, strips = GROUPED ? min(4, (P.N - f.rt * TM + STRIP_ROWS - 1) / STRIP_ROWS) : 1;
-            constexpr uint32_t PIECE = GROUPED ? STRIP : Q4_UNIT_BYTES;   // one strip's or the whole tile's stage
-            const int64_t row_bytes = (int64_t)chunks * PIECE;            // strips are this far apart
-            const uint8_t *w = P.w + f.e * P.expert_bytes + (int64_t)f.rt * (GROUPED ? 4 : 1) * row_bytes;
-            release_info(i);
-            for (int kc = 0; kc < chunks; kc++, w += PIECE, issued++) {
-                if (!warp_wait(uempty + 8 * u.at, u.parity ^ 1)) {
-                    ok = false;
-                    break;
-                }
-                if (elect_one()) {
+        if (elect_one()) {
+            Ring u = {0, 0};
+            uint32_t issued = 0;   // weight stages issued by this CTA
+            bool ok = true;
+            for (int i = 0; i < mine && ok; i++) {
+                if (!mbar_wait(info_full + 8 * (i % NI), (i / NI) & 1)) break;
+                const Info &f = info[i % NI];
+                const IdProj &P = a.p[f.j];
+                const int chunks = P.chunks, strips = GROUPED ? min(4, (P.N - f.rt * TM + STRIP_ROWS - 1) / STRIP_ROWS) : 1;
+                constexpr uint32_t PIECE = GROUPED ? STRIP : Q4_UNIT_BYTES;   // one strip's or the whole tile's stage
+                const int64_t row_bytes = (int64_t)chunks * PIECE;            // strips are this far apart
+                const uint8_t *w = P.w + f.e * P.expert_bytes + (int64_t)f.rt * (GROUPED ? 4 : 1) * row_bytes;
+                mbar_arrive(info_empty + 8 * (i % NI));
+                for (int kc = 0; kc < chunks; kc++, w += PIECE, issued++) {
+                    if (!mbar_wait(uempty + 8 * u.at, u.parity ^ 1)) {
+                        ok = false;
+                        break;
+                    }
                     const uint32_t dst = sbase + S::OFF_U + u.at * U_SLOT, bar = ufull + 8 * u.at;
                     mbar_expect_tx(bar, strips * PIECE);
                     bulk_g2s(dst, w, PIECE, bar);
@@ -441,100 +442,87 @@ __global__ void __launch_bounds__(THREADS, 1) mmq_id_kernel(const __grid_constan
                         if (strips > 2) bulk_g2s(dst + 2 * PIECE, w + 2 * row_bytes, PIECE, bar);
                         if (strips > 3) bulk_g2s(dst + 3 * PIECE, w + 3 * row_bytes, PIECE, bar);
                     }
+                    u.next(NU);
                 }
-                __syncwarp();
-                u.next(NU);
             }
+            // Every copy this thread issued has landed before the CTA can exit, also after a wait above ran
+            // out (a barrier whose phase completed long ago passes at once; a wait that runs out here ends
+            // the drain).
+            for (uint32_t x = issued > NU ? issued - NU : 0; x < issued; x++)
+                if (!mbar_wait(ufull + 8 * (x % NU), (x / NU) & 1u)) break;
         }
-        // Every copy this warp issued has landed before the CTA can exit, also after a wait above ran
-        // out (a barrier whose phase completed long ago passes at once; a wait that runs out here ends
-        // the drain).
-        for (uint32_t x = issued > NU ? issued - NU : 0; x < issued; x++)
-            if (!warp_wait(ufull + 8 * (x % NU), (x / NU) & 1u)) break;
+        __syncwarp();
     } else if (warp == ACT_WARP) {   // ---------------- activations
-        Ring r = {0, 0};
-        uint32_t issued = 0;   // stages filled by this CTA
-        bool ok = true;
-        for (int i = 0; i < mine && ok; i++) {
-            if (!await_info(i)) break;
-            const Info &f = info[i % NI];
-            const int slabs = (f.K + KC - 1) / KC, first = f.first, boxes = (f.n + BOX_ROWS - 1) / BOX_ROWS;
-            const CUtensorMap *map = &a.bmap[boxes - 1];
-            const uint32_t bytes = boxes * BOX_ROWS * SK * 2;   // a slab past K counts, filled with zeros
-            release_info(i);
-            for (int slab = 0; slab < slabs; slab += 2, issued++) {
-                if (!warp_wait(empty + 8 * r.at, r.parity ^ 1)) {
-                    ok = false;
-                    break;
-                }
-                if (elect_one()) {
-                    const uint32_t bar = full + 8 * r.at;
-                    mbar_expect_tx(bar, bytes);
-                    tma_3d(sbase + r.at * S::B_STAGE, map, first, slab, bar);
-                }
-                __syncwarp();
-                r.next(NS);
-            }
-        }
-        // as for the weights: all copies have landed (a stage whose converters stopped never completes: the
-        // wait runs out, long after its copies)
-        for (uint32_t x = issued > NS ? issued - NS : 0; x < issued; x++)
-            if (!warp_wait(full + 8 * (x % NS), (x / NS) & 1u)) break;
-    } else if (warp == 1) {   // ---------------- MMA issue (one elected thread, always the same)
-        Ring r = {0, 0};
-        bool ok = true;
-        for (int i = 0; i < mine && ok; i++) {
-            const uint32_t entry = 8 * (i % NI), side = 8 * (i & 1);
-            if (!warp_wait2(info_full + entry, (i / NI) & 1, acc_empty + side, ((i >> 1) & 1) ^ 1)) break;
-            const int n = info[i % NI].n, K = info[i % NI].K;
-            release_info(i);
-            const uint32_t idesc = mma_idesc((n + 15) & ~15), acc = tmem + (i & 1) * TN;
-            const uint32_t slab16 = (n + BOX_ROWS - 1) / BOX_ROWS * (BOX_ROWS * KC * 2 / 16);   // a slab's rows, in descriptor units
-            for (int left = K; left > 0;) {   // nothing past K enters the sum
-                // one look at the next four stages, a lane for each: how many are complete, at least one
-                Ring q = r;
-                q.next(NS, lane & 3);
-                const uint32_t late = ~__ballot_sync(0xffffffffu, mbar_test(full + 8 * q.at, q.parity)) & 0xfu;
-                int batch = min(late ? __ffs(late) - 1 : 4, (left + SK - 1) / SK);
-                if (batch == 0) {
-                    if (!warp_wait(full + 8 * r.at, r.parity)) {
+        if (elect_one()) {
+            Ring r = {0, 0};
+            uint32_t issued = 0;   // stages filled by this CTA
+            bool ok = true;
+            for (int i = 0; i < mine && ok; i++) {
+                if (!mbar_wait(info_full + 8 * (i % NI), (i / NI) & 1)) break;
+                const Info &f = info[i % NI];
+                const int slabs = (f.K + KC - 1) / KC, first = f.first, boxes = (f.n + BOX_ROWS - 1) / BOX_ROWS;
+                const CUtensorMap *map = &a.bmap[boxes - 1];
+                const uint32_t bytes = boxes * BOX_ROWS * SK * 2;   // a slab past K counts, filled with zeros
+                mbar_arrive(info_empty + 8 * (i % NI));
+                for (int slab = 0; slab < slabs; slab += 2, issued++) {
+                    if (!mbar_wait(empty + 8 * r.at, r.parity ^ 1)) {
                         ok = false;
                         break;
                     }
-                    batch = 1;
+                    const uint32_t bar = full + 8 * r.at;
+                    mbar_expect_tx(bar, bytes);
+                    tma_3d(sbase + r.at * S::B_STAGE, map, first, slab, bar);
+                    r.next(NS);
                 }
-                tc_fence_after();
-                if (elect_one()) {
-                    uint32_t at = r.at;
-                    int l = left;
-#pragma unroll 1
-                    for (int j = 0; j < batch; j++, l -= SK) {
-                        // a descriptor's address field counts 16-byte units
-                        const uint32_t ta = tmem + S::A_TMEM + at * A_COLS;
-                        const uint64_t bd = sdesc(sbase + at * S::B_STAGE);
-                        tc_mma(acc, ta, bd, idesc, l != K);
-                        if (l >= SK) {
-#pragma unroll
-                            for (int ks = 1; ks < SK / 16; ks++)
-                                tc_mma_add(acc, ta + 8 * ks, bd + (uint64_t)((ks >> 2) * slab16 + 2 * (ks & 3)), idesc);
-                        } else {
-#pragma unroll 1
-                            for (int ks = 1; 16 * ks < l; ks++)
-                                tc_mma_add(acc, ta + 8 * ks, bd + (uint64_t)((ks >> 2) * slab16 + 2 * (ks & 3)), idesc);
-                        }
-                        tc_commit(empty + 8 * at);
-                        at = at + 1 == NS ? 0 : at + 1;
-                    }
-                    if (l <= 0) tc_commit(acc_full + side);
-                }
-                __syncwarp();
-                left -= batch * SK;
-                r.next(NS, batch);
             }
+            // as for the weights: all copies have landed (a stage whose converters stopped never completes:
+            // the wait runs out, long after its copies)
+            for (uint32_t x = issued > NS ? issued - NS : 0; x < issued; x++)
+                if (!mbar_wait(full + 8 * (x % NS), (x / NS) & 1u)) break;
         }
-        if (elect_one()) tc_commit(mma_done);   // every MMA issued here is complete before the tensor memory is freed
         __syncwarp();
-        warp_wait(mma_done, 0u);
+    } else if (warp == 1) {   // ---------------- MMA issue (one elected thread, always the same)
+        if (elect_one()) {
+            Ring r = {0, 0};
+            bool ok = true, ready = false;
+            for (int i = 0; i < mine && ok; i++) {
+                const uint32_t entry = 8 * (i % NI), side = 8 * (i & 1);
+                if (!mbar_wait(info_full + entry, (i / NI) & 1)) break;
+                const int n = info[i % NI].n, K = info[i % NI].K;
+                mbar_arrive(info_empty + entry);
+                const uint32_t idesc = mma_idesc((n + 15) & ~15), acc = tmem + (i & 1) * TN;
+                const uint32_t slab16 = (n + BOX_ROWS - 1) / BOX_ROWS * (BOX_ROWS * KC * 2 / 16);   // a slab's rows, in descriptor units
+                if (!mbar_wait(acc_empty + side, ((i >> 1) & 1) ^ 1)) break;
+                for (int left = K; left > 0; left -= SK) {   // nothing past K enters the sum
+                    if (!ready && !mbar_wait(full + 8 * r.at, r.parity)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t at = r.at;
+                    r.next(NS);
+                    ready = mbar_test(full + 8 * r.at, r.parity);   // the next stage's look overlaps this one's MMAs
+                    tc_fence_after();
+                    // a descriptor's address field counts 16-byte units
+                    const uint32_t ta = tmem + S::A_TMEM + at * A_COLS;
+                    const uint64_t bd = sdesc(sbase + at * S::B_STAGE);
+                    tc_mma(acc, ta, bd, idesc, left != K);
+                    if (left >= SK) {
+#pragma unroll
+                        for (int ks = 1; ks < SK / 16; ks++)
+                            tc_mma_add(acc, ta + 8 * ks, bd + (uint64_t)((ks >> 2) * slab16 + 2 * (ks & 3)), idesc);
+                    } else {
+#pragma unroll 1
+                        for (int ks = 1; 16 * ks < left; ks++)
+                            tc_mma_add(acc, ta + 8 * ks, bd + (uint64_t)((ks >> 2) * slab16 + 2 * (ks & 3)), idesc);
+                    }
+                    tc_commit(empty + 8 * at);
+                    if (left <= SK) tc_commit(acc_full + side);
+                }
+            }
+            tc_commit(mma_done);   // every MMA issued here is complete before the tensor memory is freed
+            mbar_wait(mma_done, 0u);
+        }
+        __syncwarp();
     } else if (warp < EPI0) {   // ---------------- A conversion into tensor memory
         // lanes 32 (warp % 4) .. +31 of tensor memory are tile rows 32 (warp % 4) ..; a warp takes two of
         // the four 32-column blocks of its group's stages
