@@ -13,28 +13,41 @@
 // order (in the caller's workspace), so that an expert's pairs are consecutive rows and a pass is a
 // plain tile; then mmq_id_kernel.
 //
-// Work items are (expert, 128-row weight tile, pass): a pass is up to TN (64 or 128) of the expert's pairs. An
-// expert with c pairs has ceil(c / TN) passes of nearly equal size, so that no pass is a small
+// Work items are (expert, 128-row weight tile, pass): a pass is up to 128 of the expert's pairs. An
+// expert with c pairs has ceil(c / 128) passes of nearly equal size, so that no pass is a small
 // remainder, and a pass of n pairs runs MMAs of N = n rounded up to 16 columns: the tensor work follows
 // the ragged counts. Items are taken round-robin, passes fastest, so that the CTAs that run at one
 // time share weight tiles through L2. Every CTA derives the item list from the counts.
 //
-// A stage is 128 K elements: A as 64 tensor-memory columns, B as two 64-column boxes. The accumulator is
+// A stage is 128 K elements: A as 64 tensor-memory columns, B as two 64-column slabs. The accumulator is
 // double: the next item's MMAs run while one is read.
 //   warp 0:       streams the packed weights (one stage's 128 rows x 128 K per slot) by bulk copies
-//   warp 1:       allocates tensor memory, issues the MMAs (one elected thread)
-//   warps 2-17:   packed nibbles -> binary16 A stages, two groups of eight warps in turn
-//   warps 18-25:  accumulator -> bfloat16 rows, scattered to the pairs' output rows
-//   warp 26:      the pass's activation rows, a tensor copy per stage
-//   warp 27:      looks the items up, up to four ahead of the epilogue (a descriptor and the pass's pair
+//   warp 1:       allocates tensor memory, issues the MMAs
+//   warps 2-9:    packed nibbles -> binary16 A stages, two groups of four warps in turn
+//   warps 10-17:  accumulator -> bfloat16 rows, scattered to the pairs' output rows
+//   warp 18:      the pass's activation rows, a tensor copy per stage
+//   warp 19:      looks the items up, up to four ahead of the epilogue (a descriptor and the pass's pair
 //                 list per item), so that no other warp waits for the plan's words
-// The single warps run their whole loops in one elected thread: votes and re-elections at every stage cost
-// the MMA warp 700 cycles a batch of two stages. A look at a barrier takes 90 cycles or more even when its
-// phase is complete, so the MMA thread looks at the next stage's before it issues this one's MMAs.
+//
+// What bounds it: with many pairs the MMAs (8 x n / 2 cycles a stage) and, beside them, the instructions of
+// the conversion, about 1100 a stage; with few pairs the conversion and the weight stream. What the steps
+// there gave (gate/up of 128 experts, K 2560, 2 x 768 rows, top 8 of 512 / of 4096 rows, us):
+//   - rows gathered out of the unsorted image by four-row tensor copies 394 / 1338, by 16-byte asynchronous
+//     copies of six warps 239 / 714, in plan order through the workspace 212 / 476;
+//   - copies and MMAs issued under elect.sync and not under a test of the lane number, which costs a loop
+//     over the lanes: 177 / 433;
+//   - one full and one empty barrier per stage 137 / 416 (a look at a barrier takes 90 cycles and more even
+//     when its phase is complete);
+//   - short bodies for the roles' loops 125 / 390: twenty warps in five roles share the instruction caches,
+//     and unrolling the MMA loop over the ring cost a quarter;
+//   - ring positions by additions 109 / 297: a lone warp issues a dependent instruction every five to ten
+//     cycles, so a division in its loop is 200 cycles of its stage;
+//   - stmatrix and 16-byte stores in the epilogue 101 / 284 (down projection 193 -> 127);
+//   - the single warps' loops in one elected thread, the MMA thread looking at the next stage's barrier
+//     before it issues this one's MMAs 92 / 276; eight converter warps for sixteen 88 / 242.
+// Passes of 64 pairs with six stages for few pairs per expert were 5% slower, two pipelines with an MMA
+// thread each no faster.
 // The conversion of the weights is that of the dense prefill kernel (k_mmq.cu).
-// Measured and dropped: gathering the rows out of the unsorted image, by four-row tensor copies (issued
-// lane by lane, about 85 cycles each: 4096-row gate/up 1338 us) and by 16-byte asynchronous copies of
-// six warps (685 us).
 
 #include <cuda_bf16.h>
 
@@ -47,20 +60,27 @@ namespace {
 constexpr int MAX_PROJ = 8;
 constexpr int MAX_E = 1024;
 constexpr int TM = 128;              // weight rows per item (MMA M)
-constexpr int KC = 64;               // K elements of one activation box (a 128-byte swizzle row)
+constexpr int TN = 128;              // most pairs of a pass (MMA N)
+constexpr int KC = 64;               // K elements of one slab of activations (a 128-byte swizzle row)
 constexpr int SK = 128;              // K elements per stage
+constexpr int NS = 4;                // stages: A in tensor memory, B in shared memory
+constexpr int NU = 8;                // packed-weight slots
 constexpr int BOX_ROWS = 32;         // activation copies come in multiples of so many rows
+constexpr int B_STAGE = TN * SK * 2; // 32 KB
 constexpr int U_SLOT = Q4_UNIT_BYTES;
 constexpr uint32_t A_COLS = SK / 2;  // tensor-memory columns of an A stage
+constexpr uint32_t A_TMEM = 2 * TN;  // the A stages follow the two accumulators
 constexpr uint32_t TMEM_COLS = 512;
-constexpr int GROUPS = 2, GROUP_WARPS = 8;   // converter groups take turns at the stages
+constexpr int GROUPS = 2, GROUP_WARPS = 4;   // converter groups take turns at the stages
 constexpr int CONV0 = 2, EPI0 = CONV0 + GROUPS * GROUP_WARPS, N_EPI = 8, ACT_WARP = EPI0 + N_EPI, ITEM_WARP = ACT_WARP + 1;
 constexpr int THREADS = (ITEM_WARP + 1) * 32;
 constexpr int N_READERS = 3 + GROUPS * GROUP_WARPS + N_EPI;   // warps that read an item's descriptor
 constexpr int NI = 4;                // item descriptors
 constexpr int EPI_BYTES = 1024;      // an epilogue warp's 16 pairs x 32 rows of bfloat16
-constexpr int FEW_PAIRS = 64;        // pairs per expert (of a full bucket) up to which passes hold 64
+static_assert(A_TMEM + NS * A_COLS <= TMEM_COLS, "tensor memory");
 static_assert(4 * strip_unit_bytes(64) <= U_SLOT, "a weight stage fits its slot");
+// a stage or slot always meets the same group, so that no barrier is waited on a phase too early
+static_assert(NS % GROUPS == 0 && NU % GROUPS == 0, "rings");
 
 struct Item {
     int e, j, rt;        // expert, projection, row tile of the projection
@@ -70,32 +90,20 @@ struct Info {            // what the other warps need of an item
     int e, j, rt;        // expert, projection, row tile of the projection
     int n, first, K;     // pairs of the pass, plan position of the first; inner size
     int pad[2];
-    int pair[128];       // their pair numbers, -1 where the plan names none of this bucket
+    int pair[TN];        // their pair numbers, -1 where the plan names none of this bucket
 };
 
-// TN_: most pairs of a pass (MMA N), 64 or 128. Tensor memory: two accumulators of TN columns, then the
-// A stages, as many as fit: six or four.
-template <int TN_>
-struct Shape {
-    static constexpr int TN = TN_;
-    static constexpr int NS = (512 - 2 * TN) / 64;      // stages
-    static constexpr int NU = 6;                        // packed-weight slots
-    static constexpr int B_STAGE = TN * SK * 2;
-    static constexpr uint32_t A_TMEM = 2 * TN;
-    // shared memory: [B stages][weights][epilogue][descriptors][pass prefix][barriers][tensor-memory address,
-    // item count]
-    static constexpr int OFF_U = NS * B_STAGE;
-    static constexpr int OFF_EPI = OFF_U + NU * U_SLOT;
-    static constexpr int OFF_INFO = OFF_EPI + N_EPI * EPI_BYTES;
-    static constexpr int OFF_PRE = OFF_INFO + NI * (int)sizeof(Info);
-    static constexpr int OFF_BAR = (OFF_PRE + (MAX_E + 1) * 4 + 7) / 8 * 8;
-    // full[NS] empty[NS] ufull[NU] uempty[NU] acc_full[2] acc_empty[2] info_full[NI] info_empty[NI] mma_done
-    static constexpr int N_BARS = 2 * NS + 2 * NU + 2 * NI + 5;
-    static constexpr int SMEM_BYTES = OFF_BAR + N_BARS * 8 + 8 + 1024;   // + slack to align the base to 1024
-    static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
-    // a stage or slot always meets the same group, so that no barrier is waited on a phase too early
-    static_assert(NS % GROUPS == 0 && NU % GROUPS == 0, "rings");
-};
+// shared memory: [B stages][weights][epilogue][descriptors][pass prefix][barriers][tensor-memory address,
+// item count]
+constexpr int OFF_U = NS * B_STAGE;
+constexpr int OFF_EPI = OFF_U + NU * U_SLOT;
+constexpr int OFF_INFO = OFF_EPI + N_EPI * EPI_BYTES;
+constexpr int OFF_PRE = OFF_INFO + NI * (int)sizeof(Info);
+constexpr int OFF_BAR = (OFF_PRE + (MAX_E + 1) * 4 + 7) / 8 * 8;
+// full[NS] empty[NS] ufull[NU] uempty[NU] acc_full[2] acc_empty[2] info_full[NI] info_empty[NI] mma_done
+constexpr int N_BARS = 2 * NS + 2 * NU + 2 * NI + 5;
+constexpr int SMEM_BYTES = OFF_BAR + N_BARS * 8 + 8 + 1024;   // + slack to align the base to 1024
+static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
 
 struct IdProj {
     const uint8_t *w;
@@ -142,7 +150,6 @@ struct Pairs {
     int64_t first;
     int n;
 };
-template <int TN>
 __device__ __forceinline__ Pairs pairs_of(const IdArgs &a, const Item &t) {
     const int cnt = clamped_count(a, t.e);
     const int per = ((cnt + t.passes - 1) / t.passes + 15) & ~15;   // <= TN: passes = ceil(cnt / TN)
@@ -304,21 +311,20 @@ __global__ void __launch_bounds__(256) dequant_pairs_kernel(const int8_t *__rest
     for (int b = b0; b < kb; b += 8) dequant_word(qs, d, first + b, w, dst + (int64_t)b * QB);
 }
 
-template <int WT, typename S>
+template <int WT>
 __global__ void __launch_bounds__(THREADS, 1) mmq_id_kernel(const __grid_constant__ IdArgs a) {
-    constexpr int TN = S::TN, NS = S::NS, NU = S::NU;
     constexpr bool GROUPED = WT != QK_W_Q4_0;
     constexpr int STRIP = strip_unit_bytes(WT == QK_W_Q4_G64 ? 64 : 128);
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     const uint32_t sbase = smem_u32(smem);
-    const uint32_t full = sbase + S::OFF_BAR, empty = full + NS * 8, ufull = empty + NS * 8, uempty = ufull + NU * 8,
+    const uint32_t full = sbase + OFF_BAR, empty = full + NS * 8, ufull = empty + NS * 8, uempty = ufull + NU * 8,
                    acc_full = uempty + NU * 8, acc_empty = acc_full + 16, info_full = acc_empty + 16,
                    info_empty = info_full + 8 * NI, mma_done = info_empty + 8 * NI;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + S::OFF_BAR + S::N_BARS * 8);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + OFF_BAR + N_BARS * 8);
     int *n_items = reinterpret_cast<int *>(tmem_slot + 1);
-    Info *info = reinterpret_cast<Info *>(smem + S::OFF_INFO);
-    int *pre = reinterpret_cast<int *>(smem + S::OFF_PRE);
+    Info *info = reinterpret_cast<Info *>(smem + OFF_INFO);
+    int *pre = reinterpret_cast<int *>(smem + OFF_PRE);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int G = gridDim.x;
@@ -394,7 +400,7 @@ __global__ void __launch_bounds__(THREADS, 1) mmq_id_kernel(const __grid_constan
     if (warp == ITEM_WARP) {   // ---------------- items
         for (int i = 0; i < mine; i++) {
             const Item t = item_of(a, pre, blockIdx.x + i * G);
-            const Pairs pr = pairs_of<TN>(a, t);
+            const Pairs pr = pairs_of(a, t);
             int p[TN / 32];
 #pragma unroll
             for (int j = 0; j < TN / 32; j++)
@@ -434,7 +440,7 @@ __global__ void __launch_bounds__(THREADS, 1) mmq_id_kernel(const __grid_constan
                         ok = false;
                         break;
                     }
-                    const uint32_t dst = sbase + S::OFF_U + u.at * U_SLOT, bar = ufull + 8 * u.at;
+                    const uint32_t dst = sbase + OFF_U + u.at * U_SLOT, bar = ufull + 8 * u.at;
                     mbar_expect_tx(bar, strips * PIECE);
                     bulk_g2s(dst, w, PIECE, bar);
                     if (GROUPED) {
@@ -471,7 +477,7 @@ __global__ void __launch_bounds__(THREADS, 1) mmq_id_kernel(const __grid_constan
                     }
                     const uint32_t bar = full + 8 * r.at;
                     mbar_expect_tx(bar, bytes);
-                    tma_3d(sbase + r.at * S::B_STAGE, map, first, slab, bar);
+                    tma_3d(sbase + r.at * B_STAGE, map, first, slab, bar);
                     r.next(NS);
                 }
             }
@@ -503,8 +509,8 @@ __global__ void __launch_bounds__(THREADS, 1) mmq_id_kernel(const __grid_constan
                     ready = mbar_test(full + 8 * r.at, r.parity);   // the next stage's look overlaps this one's MMAs
                     tc_fence_after();
                     // a descriptor's address field counts 16-byte units
-                    const uint32_t ta = tmem + S::A_TMEM + at * A_COLS;
-                    const uint64_t bd = sdesc(sbase + at * S::B_STAGE);
+                    const uint32_t ta = tmem + A_TMEM + at * A_COLS;
+                    const uint64_t bd = sdesc(sbase + at * B_STAGE);
                     tc_mma(acc, ta, bd, idesc, left != K);
                     if (left >= SK) {
 #pragma unroll
@@ -524,10 +530,10 @@ __global__ void __launch_bounds__(THREADS, 1) mmq_id_kernel(const __grid_constan
         }
         __syncwarp();
     } else if (warp < EPI0) {   // ---------------- A conversion into tensor memory
-        // lanes 32 (warp % 4) .. +31 of tensor memory are tile rows 32 (warp % 4) ..; a warp takes two of
-        // the four 32-column blocks of its group's stages
-        const int quad = warp & 3, group = (warp - CONV0) / GROUP_WARPS, jb0 = 2 * (((warp - CONV0) / 4) & 1), gq = lane >> 2;
-        const uint32_t abase = tmem + ((uint32_t)(32 * quad) << 16) + S::A_TMEM;
+        // lanes 32 (warp % 4) .. +31 of tensor memory are tile rows 32 (warp % 4) ..; a warp takes them in its
+        // group's stages
+        const int quad = warp & 3, group = (warp - CONV0) / GROUP_WARPS, gq = lane >> 2;
+        const uint32_t abase = tmem + ((uint32_t)(32 * quad) << 16) + A_TMEM;
         Ring ra = {(uint32_t)group, 0}, u = {(uint32_t)group, 0};
         int ahead = group;   // stages until this group's next one
         bool ok = true;
@@ -539,9 +545,9 @@ __global__ void __launch_bounds__(THREADS, 1) mmq_id_kernel(const __grid_constan
                 ok = warp_wait2(ufull + 8 * u.at, u.parity, empty + 8 * ra.at, ra.parity ^ 1);
                 if (!ok) break;
                 tc_fence_after();
-                const uint8_t *unit = smem + S::OFF_U + u.at * U_SLOT;
+                const uint8_t *unit = smem + OFF_U + u.at * U_SLOT;
 #pragma unroll
-                for (int jb = jb0; jb < jb0 + 2; jb++) {
+                for (int jb = 0; jb < 4; jb++) {
                     const uint4 wv = load_words<WT>(unit, quad, jb, lane);
                     RowHeads<WT> hd;
                     load_heads<WT>(unit, quad, jb, gq, hd);
@@ -573,7 +579,7 @@ __global__ void __launch_bounds__(THREADS, 1) mmq_id_kernel(const __grid_constan
         }
     } else {   // ---------------- epilogue (accumulator lane = weight row, column = pair)
         const int quad = warp & 3, c0 = ((warp - EPI0) >> 2) * (TN / 2), piece = lane & 3;
-        const uint32_t buf = sbase + S::OFF_EPI + (warp - EPI0) * EPI_BYTES;
+        const uint32_t buf = sbase + OFF_EPI + (warp - EPI0) * EPI_BYTES;
         for (int i = 0; i < mine; i++) {
             if (!warp_wait2(info_full + 8 * (i % NI), (i / NI) & 1, acc_full + 8 * (i & 1), (i >> 1) & 1)) break;
             tc_fence_after();
@@ -620,16 +626,12 @@ __global__ void __launch_bounds__(THREADS, 1) mmq_id_kernel(const __grid_constan
                      : "memory");
 }
 
-template <int WT, typename S>
-qk_status launch_shape(const IdArgs &a, cudaStream_t s) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(mmq_id_kernel<WT, S>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM_BYTES);
-    if (e != cudaSuccess) return fail(QK_ERR_CUDA, "mmq_id: shared memory attribute: %s", cudaGetErrorString(e));
-    return launch_pdl("mmq_id", mmq_id_kernel<WT, S>, dim3((unsigned)sm_count()), dim3(THREADS), (size_t)S::SMEM_BYTES, s, a);
-}
 template <int WT>
 qk_status launch_type(const IdArgs &a, cudaStream_t s) {
-    return (int64_t)a.pairs <= (int64_t)FEW_PAIRS * a.E ? launch_shape<WT, Shape<64>>(a, s) : launch_shape<WT, Shape<128>>(a, s);
+    const cudaError_t e =
+        cudaFuncSetAttribute(mmq_id_kernel<WT>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+    if (e != cudaSuccess) return fail(QK_ERR_CUDA, "mmq_id: shared memory attribute: %s", cudaGetErrorString(e));
+    return launch_pdl("mmq_id", mmq_id_kernel<WT>, dim3((unsigned)sm_count()), dim3(THREADS), (size_t)SMEM_BYTES, s, a);
 }
 
 }  // namespace

@@ -666,7 +666,7 @@ static qk_status mmq_id_common(const int8_t *qs, const uint16_t *d, int64_t row_
         tiles += ceil_div(p.N, UNIT_ROWS);
     }
     // work items (passes of any plan x row tiles) are counted in int
-    REQUIRE((pairs / 64 + E) * tiles < (1LL << 31), QK_ERR_UNSUPPORTED, "rows * k * row tiles too large for one launch");
+    REQUIRE((pairs / 128 + E) * tiles < (1LL << 31), QK_ERR_UNSUPPORTED, "rows * k * row tiles too large for one launch");
     const size_t need = qk_mmq_id_workspace_bytes(rows, k, n_proj, projs);
     REQUIRE(ws && aligned(ws, 128), QK_ERR_WORKSPACE, "workspace null or not 128-byte aligned");
     REQUIRE(ws_bytes >= need, QK_ERR_WORKSPACE, "workspace %zu < %zu bytes", ws_bytes, need);
