@@ -136,9 +136,10 @@ QK_API uint64_t qk_launch_count(void);
 /*
  * Device-side fault word of the current device, then cleared. Bit 0: a
  * kernel's bounded wait on a shared-memory barrier gave up (the kernel then
- * stopped early and its outputs are not valid). Covers qk_mmvq, qk_mmvq_id
- * and qk_mmq. Bit 1: a routed projection's counts held more passes than any
- * plan of its bucket can (not the output of qk_moe_plan); it did no work.
+ * stopped early and its outputs are not valid). Covers qk_mmvq, qk_mmvq_id,
+ * qk_mmq and qk_mmq_id, each with its variants. Bit 1: a routed projection's
+ * counts held more passes than any plan of its bucket can (not the output of
+ * qk_moe_plan); it did no work.
  * Synchronises the device.
  */
 QK_API qk_status qk_device_faults(uint32_t *faults);
@@ -600,7 +601,8 @@ typedef struct qk_proj_id16 {
  * rounded once to binary16 (by at most 2^-11, relative), accumulated in binary32
  * over all of K and rounded once to bfloat16 (by at most 2^-8, which the
  * operands' rounding stays well below); 16-bit rows halve the traffic between
- * the routed products.
+ * the routed products. Activations and weights beyond binary16's range (65504)
+ * become infinities, as for qk_mmq.
  *   projs  host array of n_proj (1..8) descriptors with one n_experts; outputs
  *          must not share a byte (disjoint column windows of one buffer with one
  *          y_stride are allowed: gate and up as the packed rows of a GLU)

@@ -637,7 +637,8 @@ qk_status launch_form(GArgs &a, int64_t passes, int split, int chunks, cudaStrea
     const int share = (int)ceil_div(chunks, split);
     a.held = share < max_chunks(WARPS) ? share : max_chunks(WARPS);
     a.wk_log2 = choose_wk<WARPS>(a, passes, resident);   // a routed kernel chooses again by the passes there are
-    const int64_t items = passes * row_blocks_of_all<WARPS>(a, ROUTED ? 3 : a.wk_log2);
+    constexpr int MOST_WK = WARPS == FEW_WARPS ? 3 : 4;
+    const int64_t items = passes * row_blocks_of_all<WARPS>(a, ROUTED ? MOST_WK : a.wk_log2);
     if (items > INT32_MAX) return fail(QK_ERR_UNSUPPORTED, "mmvq: too many rows for one launch");
     const int clusters = (int)(items < resident ? items : resident);
     const size_t smem = a.held * sizeof(Rec<G>) + 2 * WARPS * RED * sizeof(float) + (ROUTED ? (a.E + 1) * 4 : 0);
