@@ -233,6 +233,7 @@ def _prepare_own(s):
         s["ws_bytes"] = qk.qk_mmvq_workspace_bytes(s["projs"])
         s["ws"] = torch.zeros((max(16, s["ws_bytes"]),), dtype=torch.uint8, device="cuda")
     elif op == "mmq_id":
+        # room for every pair's activation row, so the size depends on the rows and the slots per row
         s["ws_bytes"] = qk.qk_mmq_id_workspace_bytes(case["rows"], case["k"], s["projs"])
         s["ws"] = torch.empty((s["ws_bytes"],), dtype=torch.uint8, device="cuda")
 
