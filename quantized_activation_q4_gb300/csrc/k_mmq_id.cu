@@ -116,7 +116,7 @@ struct IdArgs {
     // slabs x 32, 64, 96 or 128 rows, swizzled
     CUtensorMap bmap[4];
     const int32_t *counts, *offsets, *items;
-    int pairs, k, E, per_pair, n_proj, row_tiles;
+    int pairs, E, n_proj, row_tiles;
     IdProj p[MAX_PROJ];
 };
 
@@ -676,9 +676,7 @@ qk_status launch_mmq_id(const int8_t *qs, const uint16_t *d, int64_t row_blocks,
     a.offsets = offsets;
     a.items = items;
     a.pairs = pairs;
-    a.k = k;
     a.E = projs[0].n_experts;
-    a.per_pair = per_pair;
     for (int wt = QK_W_Q4_0; wt <= QK_W_Q4_G128; wt++) {   // one launch per weight type present
         a.n_proj = 0;
         a.row_tiles = 0;

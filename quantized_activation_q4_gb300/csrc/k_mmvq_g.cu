@@ -502,13 +502,16 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) mmvq_g_kernel(const __
         const int j = item_proj(it, pass, rb);
         const GProj &P = a.p[j];
         const bool new_pass = pass != cur_pass;
-        cur_pass = pass;
+        if (new_pass) {
+            cur_pass = pass;
+            cur_s0 = -1;   // no fragments of this pass yet; its first items may have no share of K here
+        }
         uint64_t y[4] = {0, 0, 0, 0};
         const bool mine = (rb * wr + ws) * STRIP_ROWS < P.N;
         const int c_hi = share_hi[j];
         for (int s0 = share_lo[j]; s0 < c_hi; s0 += MAXC) {
             const int s1 = min(c_hi, s0 + MAXC), cols = min(P.K, s1 * UNIT_COLS);
-            if (new_pass || s0 != cur_s0 || cols != cur_cols) {   // other tokens or columns than the fragments hold
+            if (s0 != cur_s0 || cols != cur_cols) {   // other tokens or columns than the fragments hold
                 __syncthreads();   // every warp is done with the fragments before; the pass's tokens are listed
                 const int row = tok_row[pass & 1][lane >> 2];
                 const uint8_t *img_row = row < 0 ? nullptr : a.img + row * a.img_row_bytes;
@@ -638,8 +641,7 @@ qk_status launch_form(GArgs &a, int64_t passes, int split, int chunks, cudaStrea
     a.held = share < max_chunks(WARPS) ? share : max_chunks(WARPS);
     a.wk_log2 = choose_wk<WARPS>(a, passes, resident);   // a routed kernel chooses again by the passes there are
     constexpr int MOST_WK = WARPS == FEW_WARPS ? 3 : 4;
-    const int64_t items = passes * row_blocks_of_all<WARPS>(a, ROUTED ? MOST_WK : a.wk_log2);
-    if (items > INT32_MAX) return fail(QK_ERR_UNSUPPORTED, "mmvq: too many rows for one launch");
+    const int64_t items = passes * row_blocks_of_all<WARPS>(a, ROUTED ? MOST_WK : a.wk_log2);   // fit an int (qk_api.cu)
     const int clusters = (int)(items < resident ? items : resident);
     const size_t smem = a.held * sizeof(Rec<G>) + 2 * WARPS * RED * sizeof(float) + (ROUTED ? (a.E + 1) * 4 : 0);
     auto kernel = mmvq_g_kernel<G, ROUTED, WARPS>;

@@ -467,9 +467,9 @@ static qk_status mmvq_id_common(const void *img, int64_t img_row_blocks, int64_t
             REQUIRE(!overlap(sy, span(projs[i].y, (size_t)(rows * k * projs[i].N * 4))), QK_ERR_ALIAS,
                     "outputs of projections %d and %d overlap", i, j);
     }
-    // the routed kernel counts its work items in int: (passes of any plan) x (row tiles) < 2^31
+    // the routed kernels count their work items in int: (passes of any plan) x (row tiles or strips) < 2^31
     int64_t tiles = 0;
-    for (int j = 0; j < n_proj; j++) tiles += ceil_div(projs[j].N, UNIT_ROWS);
+    for (int j = 0; j < n_proj; j++) tiles += ceil_div(projs[j].N, group_scaled(projs[j].wtype) ? STRIP_ROWS : UNIT_ROWS);
     REQUIRE(((rows * k + 7) / 8 + E) * tiles < (1LL << 31), QK_ERR_UNSUPPORTED,
             "rows * k * row tiles too large for one routed launch");
     for (int wt = QK_W_Q4_0; wt <= QK_W_LAST; wt++) {

@@ -239,7 +239,8 @@ def test_routed_matches_float64(slots, G, rows, k, E, K, Ns, live):
 
 
 def test_routed_row_equals_the_ordinary_matvec_of_its_expert():
-    """One token, every expert picked once: each pair's row has the bits of qk_mmvq of that expert."""
+    """One token, every expert picked once: each pair's row is qk_mmvq's of that expert (binary32 sums
+    in another order)."""
     rows, k, E, N, K = 1, 8, 8, 200, 640
     img = image(11800, rows, K)
     ids = np.array([[3, 1, 7, 0, 2, 6, 5, 4]], dtype=np.int32)
@@ -254,3 +255,92 @@ def test_routed_row_equals_the_ordinary_matvec_of_its_expert():
         qk.qk_mmvq(dev(img.reshape(-1)), K // 32, 1,
                    [qk.make_proj("q4_g128", pack_weight(Ws[e], "q4_g128", N, K), N, K, y1, N)], None, 0)
         assert_exact_path(got[p:p + 1], host(y1), nmse_max=1e-12, rel_max=1e-6, what=f"expert {e}")
+
+
+@pytest.mark.parametrize("G,Ks", [(64, (64, 1024)), (128, (2048, 128)), (64, (1088, 64, 192))])
+def test_routed_projections_of_different_inner_sizes(G, Ks):
+    """K of one or two chunks beside a long one: the CTAs that share the long K have nothing of the short one,
+    which comes first in every pass of some of them."""
+    import torch
+    rows, k, E, N = 64, 2, 4, 96
+    rb = max(Ks) // 32
+    img = image(11900, rows, rb * 32)
+    ids = synth.rng(11901).integers(0, E, size=(rows, k), dtype=np.int32)
+    p = plan(ids, E, rows)
+    Ws = [[synth.q4_group_weight(11910 + 100 * j + e, N, K, G) for e in range(E)] for j, K in enumerate(Ks)]
+    pw = [pack_experts(w, f"q4_g{G}", N, K) for w, K in zip(Ws, Ks)]
+    ys = [out(rows * k, N) for _ in Ks]
+    qk.qk_mmvq_id(dev(img.reshape(-1)), rb, rows, k,
+                  [qk.make_proj_id(f"q4_g{G}", E, w, N, K, y) for w, K, y in zip(pw, Ks, ys)], *p)
+    assert qk.qk_device_faults() == 0
+    flat = ids.reshape(-1)
+    for w, K, y in zip(Ws, Ks, ys):
+        x = O.image_values(img, K)
+        want = np.stack([x[i // k] @ O.dequant_group(w[e], N, K).T for i, e in enumerate(flat)])
+        assert_exact_path(host(y), want, what=f"K={K}")
+
+
+@pytest.mark.parametrize("G,T,K,Ns", [
+    (64, 8, 256, (120000,)),             # items for every CTA several times over, all of K in eight warps' CTAs
+    (128, 3, 4352, (20000, 19003, 33)),  # the longest K of that form
+    (64, 5, 4416, (40000,)),             # one chunk more: sixteen warps
+    (128, 8, 9216, (25001, 15000)),      # the longest of that one
+    (64, 2, 9280, (20000,)),             # K shared by a cluster, in two pieces each
+])
+def test_matvec_with_many_rows(G, T, K, Ns):
+    import torch
+    img = image(12000 + K, T, K)
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(12001)
+    x = dev(O.image_values(img, K))
+    projs, keep = [], []
+    for N in Ns:
+        w = torch.randint(0, 256, (N, K // G, 4 + G // 2), dtype=torch.uint8, device="cuda", generator=gen)
+        d = (torch.rand((N, K // G, 1), device="cuda", generator=gen) * 0.02 + 0.001).half()
+        w[..., 0:2] = d.view(torch.uint8)
+        n = qk.qk_weight_packed_bytes(f"q4_g{G}", N, K)
+        p = torch.empty((n,), dtype=torch.uint8, device="cuda")
+        qk.qk_weight_pack(f"q4_g{G}", w, N, K, p, n)
+        nib = w[..., 4:].reshape(N, K // G, G // 32, 16)
+        v = torch.stack([nib & 15, nib >> 4], dim=3).reshape(N, K // G, G).double()
+        W = ((v - (w[..., 2:3] & 15).double()) * d.double()).reshape(N, K)
+        y = out(T, N)
+        keep.append((p, x @ W.T, y))
+        projs.append(qk.make_proj(f"q4_g{G}", p, N, K, y, N))
+        del nib, v, W, w
+    qk.qk_mmvq(dev(img.reshape(-1)), K // 32, T, projs, None, 0)
+    assert qk.qk_device_faults() == 0
+    for _, want, y in keep:
+        assert_exact_path(host(y), host(want), what=f"{K} -> {y.shape[1]}")
+
+
+@pytest.mark.parametrize("slots", [False, True])
+def test_routed_with_long_rows_and_many_passes(slots):
+    """K beyond the eight-warp form and items for every CTA: the sixteen-warp routed form."""
+    import torch
+    rows, k, E, K, N, live = 300, 2, 5, 4608, 2400, 287
+    img = image(12100, rows * k if slots else rows, K)
+    ids = synth.rng(12101).integers(0, E, size=(rows, k), dtype=np.int32)
+    Ws = [synth.q4_group_weight(12110 + e, N, K, 64) for e in range(E)]
+    y = out(rows * k, N)
+    pw = pack_experts(Ws, "q4_g64", N, K)
+    call = qk.qk_mmvq_id_slots if slots else qk.qk_mmvq_id
+    call(dev(img.reshape(-1)), K // 32, rows, k, [qk.make_proj_id("q4_g64", E, pw, N, K, y)], *plan(ids, E, live))
+    assert qk.qk_device_faults() == 0
+    x, flat, got = O.image_values(img, K), ids.reshape(-1), host(y)
+    want = np.zeros((live * k, N))
+    for e in range(E):
+        p = np.nonzero(flat[:live * k] == e)[0]
+        want[p] = x[p if slots else p // k] @ O.dequant_group(Ws[e], N, K).T
+    assert_exact_path(got[:live * k], want)
+    assert np.all(got[live * k:] == SENTINEL)
+
+
+def test_static_workspace_call_takes_group_scaled_projections():
+    T, N, K = 3, 200, 512
+    img = image(12200, T, K)
+    W = synth.q4_group_weight(12201, N, K, 128)
+    y = out(T, N)
+    qk.qk_mmvq_static_ws(dev(img.reshape(-1)), K // 32, T,
+                         [qk.make_proj("q4_g128", pack_weight(W, "q4_g128", N, K), N, K, y, N)])
+    assert_exact_path(host(y), ref(img, W, N, K))
