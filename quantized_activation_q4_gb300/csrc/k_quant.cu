@@ -336,24 +336,101 @@ __global__ void __launch_bounds__(256) glu_q8_1_kernel(
 // Input rows of binary32 or bfloat16, codes and half scales as qk_quantize_q8_0 of the binary32 products,
 // which are stored only when `out` is given.
 //
-// Bound by memory once an element costs about 20 instructions (with IEEE divisions and expf it cost 90:
-// 26600 x 768 bfloat16 pairs took 59 us):
-//   - the sigmoid kinds are g / (1 + 2^(-c g)) with ex2.approx and rcp.approx. Relative errors: the
-//     exponent's rounding |c g| 2^-24 and 2^-22 of ex2, weighted by the sigmoid's share e / (1 + e), and
-//     2^-23 each of rcp and the products: below 1e-6 of the result or 3e-7 of |g u| everywhere.
-//     GeGLU-tanh is one of them: 0.5 (1 + tanh z) = 1 / (1 + e^(-2z)), with no cancellation;
-//   - codes are rint(x * (1 / d)), d's reciprocal once per block. It differs from rint(x / d) only where
-//     the quotient is within 127 * 2^-23 of a tie: blocks with an element that near (and scales outside
-//     1e-30 .. 1e30) divide, so the bytes are qk_quantize_q8_0's.
+// Bound by issue slots and, once those are few, by memory. 26600 x 768 bfloat16 pairs (103 MB, 15.3 us at
+// the copy rate): with IEEE divisions and expf 90 instructions an element, 59 us; with approximate functions
+// 37, 27 us; with two elements to an instruction 29, 23 us (issue 78%). 700 x 18944 binary32 pairs with
+// their products stored (161 MB, 23.8 us): 36, 27.4 and 24.5 us. One, three or four blocks a thread and
+// other numbers of CTAs per SM change less than 2%.
+//   - the sigmoid kinds are g / (1 + 2^(-c g)) with ex2.approx and rcp.approx, two elements to an
+//     instruction elsewhere. Relative errors: the exponent's rounding |c g| 2^-24 and 2^-22 of ex2, weighted
+//     by the sigmoid's share e / (1 + e), and 2^-23 each of rcp and the products: below 1e-6 of the result or
+//     3e-7 of |g u| everywhere. GeGLU-tanh is one of them: 0.5 (1 + tanh z) = 1 / (1 + e^(-2z)), with no
+//     cancellation;
+//   - d = m / 127 by a product and one correction step (Brisebarre, Muller, Raina, "Accelerating correctly
+//     rounded floating-point division when the divisor is known in advance"): the same as a division for
+//     every significand where nothing under- or overflows;
+//   - codes are rint(x * r), r the approximate reciprocal of d. x r is off x / d by at most 127 (2^-23 + 2^-24
+//     + 2^-24) = 3.1e-5 and so gives another code only that near to a tie: blocks with an element within
+//     4e-5 of one (and scales outside 1e-30 .. 1e30) divide, so the bytes are qk_quantize_q8_0's.
 // A group of four lanes has a quant block, eight columns a lane; a thread has two blocks' loads in flight.
 // A CTA of 64 groups takes 128 consecutive blocks of a row, or as many whole rows as 128 blocks hold.
-// Eight columns as they are in memory, and their binary32 values: loads in flight cost few registers.
+
+// Two binary32 values in a register pair, and operations on both.
+typedef uint64_t F2;
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float lo(F2 v) { return __uint_as_float((uint32_t)v); }
+__device__ __forceinline__ float hi(F2 v) { return __uint_as_float((uint32_t)(v >> 32)); }
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ F2 both(float v) { return f2(v, v); }
+// max(|m|, |v|, |w|): NaN is left out, or (NAN_TOO) the result
+template <bool NAN_TOO>
+__device__ __forceinline__ float max3(float m, F2 v) {
+    float r;
+    if (NAN_TOO)
+        asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(lo(v)), "f"(hi(v)));
+    else
+        asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(lo(v)), "f"(hi(v)));
+    return r;
+}
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float rcp(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+// x / (1 + e^-y), c = -log2(e) y
+__device__ __forceinline__ F2 gated(F2 x, F2 c) {
+    const F2 s = add2(f2(ex2(lo(c)), ex2(hi(c))), both(1.0f));
+    return mul2(x, f2(rcp(lo(s)), rcp(hi(s))));
+}
+constexpr float LOG2E = 1.4426950408889634f;
+
+template <int KIND>
+__device__ __forceinline__ F2 glu_pair(F2 g, F2 u, float alpha_log2e, float limit) {
+    if (KIND == QK_GLU_SWIGLU) return mul2(gated(g, mul2(g, both(-LOG2E))), u);
+    if (KIND == QK_GLU_GEGLU_TANH) {   // 2 sqrt(2/pi) log2(e) (g + 0.044715 g^3)
+        const F2 t = fma2(mul2(g, both(0.044715f)), g, both(1.0f));
+        return mul2(gated(g, mul2(mul2(g, both(-2.0f * 0.7978845608028654f * LOG2E)), t)), u);
+    }
+    if (KIND == QK_GLU_GEGLU_QUICK) return mul2(gated(g, mul2(g, both(-1.702f * LOG2E))), u);
+    if (KIND == QK_GLU_SWIGLU_OAI || KIND == QK_GLU_SWIGLU_CLAMP) {
+        const F2 x = f2(fminf(lo(g), limit), fminf(hi(g), limit));
+        const F2 v = f2(fminf(fmaxf(lo(u), -limit), limit), fminf(fmaxf(hi(u), -limit), limit));
+        return KIND == QK_GLU_SWIGLU_OAI ? mul2(gated(x, mul2(x, both(-alpha_log2e))), add2(v, both(1.0f)))
+                                         : mul2(gated(x, mul2(x, both(-LOG2E))), v);
+    }
+    return f2(glu_out(KIND, lo(g), lo(u), 0.0f, 0.0f), glu_out(KIND, hi(g), hi(u), 0.0f, 0.0f));   // GeGLU-erf, ReGLU
+}
+
+// Eight columns as they are in memory: loads in flight cost few registers.
 template <bool BF16>
 struct Raw8 {
     uint4 w[BF16 ? 1 : 2];
-    __device__ __forceinline__ void load(const void *p, int64_t i) {
+    __device__ __forceinline__ void load(const void *p, int64_t i, bool wide) {
         const uint8_t *q = static_cast<const uint8_t *>(p) + i * (BF16 ? 2 : 4);
-        if ((reinterpret_cast<uintptr_t>(q) & 15u) == 0) {
+        if (wide) {
 #pragma unroll
             for (int h = 0; h < (BF16 ? 1 : 2); h++) w[h] = __ldg(reinterpret_cast<const uint4 *>(q) + h);
         } else {
@@ -370,47 +447,23 @@ struct Raw8 {
             for (int h = 0; h < (BF16 ? 1 : 2); h++) w[h] = make_uint4(x[4 * h], x[4 * h + 1], x[4 * h + 2], x[4 * h + 3]);
         }
     }
-    __device__ __forceinline__ float operator[](int j) const {
-        const uint4 v = w[BF16 ? 0 : j >> 2];
-        const int k = BF16 ? j >> 1 : j & 3;
-        const uint32_t x = k == 0 ? v.x : k == 1 ? v.y : k == 2 ? v.z : v.w;
-        return __uint_as_float(!BF16 ? x : (j & 1) ? x & 0xffff0000u : x << 16);
+    __device__ __forceinline__ F2 pair(int i) const {   // columns 2i, 2i + 1
+        const uint4 v = w[BF16 ? 0 : i >> 1];
+        if (BF16) {
+            const uint32_t x = i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+            return f2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
+        }
+        return i & 1 ? f2(__uint_as_float(v.z), __uint_as_float(v.w)) : f2(__uint_as_float(v.x), __uint_as_float(v.y));
     }
 };
-__device__ __forceinline__ float ex2(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-__device__ __forceinline__ float rcp(float x) {
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-// x / (1 + e^-y), c = -log2(e) y
-__device__ __forceinline__ float gated(float x, float c) { return x * rcp(1.0f + ex2(c)); }
-constexpr float LOG2E = 1.4426950408889634f;
 
-template <int KIND>
-__device__ __forceinline__ float glu_fast(float g, float u, float alpha_log2e, float limit) {
-    if (KIND == QK_GLU_SWIGLU) return gated(g, -LOG2E * g) * u;
-    if (KIND == QK_GLU_GEGLU_TANH) {   // 2 sqrt(2/pi) log2(e) (g + 0.044715 g^3)
-        const float c = -2.0f * 0.7978845608028654f * LOG2E;
-        return gated(g, c * g * fmaf(0.044715f * g, g, 1.0f)) * u;
-    }
-    if (KIND == QK_GLU_GEGLU_QUICK) return gated(g, -1.702f * LOG2E * g) * u;
-    if (KIND == QK_GLU_SWIGLU_OAI || KIND == QK_GLU_SWIGLU_CLAMP) {
-        const float x = fminf(g, limit), v = fminf(fmaxf(u, -limit), limit);
-        return KIND == QK_GLU_SWIGLU_OAI ? gated(x, -alpha_log2e * x) * (v + 1.0f) : gated(x, -LOG2E * x) * v;
-    }
-    return glu_out(KIND, g, u, 0.0f, 0.0f);   // GeGLU-erf, ReGLU
-}
-
+// wide: every eight columns of a and b are 16-byte aligned. Groups over whole rows (rows_per_cta > 1):
+// row_mul = ceil(2^16 / blocks of a row), exact for the quotients of 0..63 here.
 template <int KIND, bool BF16>
 __global__ void __launch_bounds__(256, BF16 ? 6 : 4) glu_q8_0_kernel(
-    int layout, const void *__restrict__ a, int64_t a_stride, const void *__restrict__ b, int64_t b_stride, int N,
-    float *__restrict__ out, int64_t out_stride, int8_t *__restrict__ qs, uint16_t *__restrict__ dh,
-    int64_t row_blocks, int T, int rows_per_cta, int step_row, int step_blk, float alpha, float limit,
+    int layout, bool wide, const void *__restrict__ a, int64_t a_stride, const void *__restrict__ b, int64_t b_stride,
+    int N, float *__restrict__ out, int64_t out_stride, int8_t *__restrict__ qs, uint16_t *__restrict__ dh,
+    int64_t row_blocks, int T, int rows_per_cta, uint32_t row_mul, int step_row, int step_blk, float alpha, float limit,
     const int32_t *live) {
     pdl_trigger();
     pdl_wait();
@@ -420,12 +473,13 @@ __global__ void __launch_bounds__(256, BF16 ? 6 : 4) glu_q8_0_kernel(
     Raw8<BF16> g[2], u[2];
     int r0 = 0;
     blk[0] = blockIdx.y * 128 + group;
-    if (rows_per_cta > 1) {   // groups run over whole rows; the second block is 64 groups on
-        r0 = group / kb;
+    if (rows_per_cta > 1) {   // the second block is 64 groups on
+        r0 = (group * row_mul) >> 16;
         blk[0] = group - r0 * kb;
     }
+    bool on[2];
 #pragma unroll
-    for (int h = 0; h < 2; h++) {   // row -1: nothing for this group
+    for (int h = 0; h < 2; h++) {
         if (h == 1) {
             blk[1] = blk[0] + step_blk;
             r0 += step_row;
@@ -435,60 +489,67 @@ __global__ void __launch_bounds__(256, BF16 ? 6 : 4) glu_q8_0_kernel(
             }
         }
         row[h] = (int64_t)blockIdx.x * rows_per_cta + r0;
-        if (r0 >= rows_per_cta || row[h] >= T || blk[h] >= kb) row[h] = -1;
-        // loaded together with the live count (row < T is in the caller's buffers even when it is padding)
-        if (row[h] >= 0) {
-            const int64_t c = blk[h] * QB + 8 * l4, first = row[h] * a_stride + c;
-            g[h].load(a, layout == QK_GLU_PACKED_SWAPPED ? first + N : first);
-            if (layout == QK_GLU_SEPARATE)
-                u[h].load(b, row[h] * b_stride + c);
-            else
-                u[h].load(a, layout == QK_GLU_PACKED ? first + N : first);
-        }
+        on[h] = r0 < rows_per_cta && row[h] < T && blk[h] < kb;
+        // loaded together with the live count (row < T is in the caller's buffers even when it is padding);
+        // a group without a block loads the first one's columns again
+        const int64_t r = on[h] ? row[h] : 0, c = (on[h] ? blk[h] : 0) * QB + 8 * l4, first = r * a_stride + c;
+        g[h].load(a, layout == QK_GLU_PACKED_SWAPPED ? first + N : first, wide);
+        if (layout == QK_GLU_SEPARATE)
+            u[h].load(b, r * b_stride + c, wide);
+        else
+            u[h].load(a, layout == QK_GLU_PACKED ? first + N : first, wide);
     }
     const int n_live = live_rows(live, T);
     const float alpha_log2e = alpha * LOG2E;
 #pragma unroll
     for (int h = 0; h < 2; h++) {
-        const bool on = row[h] >= 0 && row[h] < n_live;
-        float v[8], m = 0.0f;
+        F2 v[4];
+        float m = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; i++) {
-            v[i] = on ? glu_fast<KIND>(g[h][i], u[h][i], alpha_log2e, limit) : 0.0f;
-            m = fmaxf(m, fabsf(v[i]));
+        for (int i = 0; i < 4; i++) {
+            v[i] = glu_pair<KIND>(g[h].pair(i), u[h].pair(i), alpha_log2e, limit);
+            m = max3<false>(m, v[i]);
         }
         m = fmaxf(m, __shfl_xor_sync(FULL, m, 1));
         m = fmaxf(m, __shfl_xor_sync(FULL, m, 2));
-        if (!on) continue;   // a block's four lanes agree
-        const float d = m / 127.0f, inv = 1.0f / d;
+        if (!on[h] || row[h] >= n_live) continue;   // a block's four lanes agree
+        constexpr float C = 1.0f / 127.0f;
+        float d = m * C;
+        d = fmaf(fmaf(-127.0f, d, m), C, d);
+        const F2 inv = both(rcp(d));
         constexpr float MAGIC = 12582912.0f;   // 1.5 * 2^23: the sum's low byte is the rounded code
         uint32_t t[8];
-        bool clear = d > 1e-30f && d < 1e30f;   // false for NaN as well
+        float off = 0.0f;   // the farthest from a code
 #pragma unroll
-        for (int i = 0; i < 8; i++) {
-            const float r = v[i] * inv, s = r + MAGIC;
-            t[i] = __float_as_uint(s);
-            clear = clear && fabsf(r - (s - MAGIC)) < 0.5f - 4.0e-5f;
+        for (int i = 0; i < 4; i++) {
+            const F2 r = mul2(v[i], inv), s = add2(r, both(MAGIC));
+            t[2 * i] = __float_as_uint(lo(s));
+            t[2 * i + 1] = __float_as_uint(hi(s));
+            off = max3<true>(off, fma2(add2(s, both(-MAGIC)), both(-1.0f), r));
         }
-        // |x / d| <= 127 and two roundings of 2^-24 each (inv, r) against one (x / d)
-        if (!clear) {
+        if (!(d > 1e-30f && d < 1e30f && off < 0.5f - 4.0e-5f)) {   // also with a NaN anywhere
+            d = m / 127.0f;
 #pragma unroll
-            for (int i = 0; i < 8; i++) t[i] = m != 0.0f ? (uint32_t)__float2int_rn(v[i] / d) : 0u;
+            for (int i = 0; i < 4; i++) {
+                t[2 * i] = m != 0.0f ? (uint32_t)__float2int_rn(lo(v[i]) / d) : 0u;
+                t[2 * i + 1] = m != 0.0f ? (uint32_t)__float2int_rn(hi(v[i]) / d) : 0u;
+            }
         }
-        const uint32_t lo = __byte_perm(__byte_perm(t[0], t[1], 0x0040), __byte_perm(t[2], t[3], 0x0040), 0x5410);
-        const uint32_t hi = __byte_perm(__byte_perm(t[4], t[5], 0x0040), __byte_perm(t[6], t[7], 0x0040), 0x5410);
+        const uint32_t c0 = __byte_perm(__byte_perm(t[0], t[1], 0x0040), __byte_perm(t[2], t[3], 0x0040), 0x5410);
+        const uint32_t c1 = __byte_perm(__byte_perm(t[4], t[5], 0x0040), __byte_perm(t[6], t[7], 0x0040), 0x5410);
         if (out) {
             float *o = out + row[h] * out_stride + blk[h] * QB + 8 * l4;
-            store4(o, v);
-            store4(o + 4, v + 4);
+            const float w[8] = {lo(v[0]), hi(v[0]), lo(v[1]), hi(v[1]), lo(v[2]), hi(v[2]), lo(v[3]), hi(v[3])};
+            store4(o, w);
+            store4(o + 4, w + 4);
         }
         const int64_t at = row[h] * row_blocks + blk[h];
         uint32_t *q = reinterpret_cast<uint32_t *>(qs + at * QB) + 2 * l4;
         if ((reinterpret_cast<uintptr_t>(q) & 7u) == 0) {
-            *reinterpret_cast<uint2 *>(q) = make_uint2(lo, hi);
+            *reinterpret_cast<uint2 *>(q) = make_uint2(c0, c1);
         } else {
-            q[0] = lo;
-            q[1] = hi;
+            q[0] = c0;
+            q[1] = c1;
         }
         if (l4 == 0) dh[at] = __half_as_ushort(__float2half_rn(d));
     }
@@ -614,10 +675,16 @@ qk_status launch_glu_q8_0(int kind, int layout, int elem, const void *a, int64_t
                           int64_t row_blocks, float alpha, float limit, const int32_t *live, cudaStream_t s) {
     if (T == 0) return QK_OK;
     const int kb = N / QB, rows = kb >= 128 ? 1 : 128 / kb;   // rows of a CTA
+    const int64_t es = elem == QK_ELEM_BF16 ? 2 : 4;
+    const bool separate = layout == QK_GLU_SEPARATE;
+    const bool wide = ((reinterpret_cast<uintptr_t>(a) | (uintptr_t)(a_stride * es) |   // N * es is a multiple of 64
+                        (separate ? reinterpret_cast<uintptr_t>(b) | (uintptr_t)(b_stride * es) : 0)) &
+                       15u) == 0;
     dim3 grid((unsigned)ceil_div(T, rows), (unsigned)(rows > 1 ? 1 : ceil_div(kb, 128)));
     return launch_pdl("glu_q8_0", elem == QK_ELEM_BF16 ? glu_q8_0_of<true>(kind) : glu_q8_0_of<false>(kind), grid,
-                      dim3(256), 0, s, layout, a, a_stride, b, b_stride, N, out, out_stride, qs, d, row_blocks, T, rows,
-                      rows > 1 ? 64 / kb : 0, rows > 1 ? 64 % kb : 64, alpha, limit, live);
+                      dim3(256), 0, s, layout, wide, a, a_stride, b, b_stride, N, out, out_stride, qs, d, row_blocks, T,
+                      rows, (uint32_t)((65536 + kb - 1) / kb), rows > 1 ? 64 / kb : 0, rows > 1 ? 64 % kb : 64, alpha,
+                      limit, live);
 }
 
 }  // namespace qk
