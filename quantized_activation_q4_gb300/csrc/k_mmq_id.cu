@@ -121,7 +121,7 @@ struct IdArgs {
 };
 
 __device__ __forceinline__ int clamped_count(const IdArgs &a, int e) {
-    const int c = __ldg(a.counts + e);
+    const int c = __ldcg(a.counts + e);
     return c < 0 ? 0 : (c > a.pairs ? a.pairs : c);
 }
 // Item tau: its expert is the last e with pre[e] <= tau / row_tiles (pre: prefix of the pass counts).
@@ -154,12 +154,12 @@ __device__ __forceinline__ Pairs pairs_of(const IdArgs &a, const Item &t) {
     const int cnt = clamped_count(a, t.e);
     const int per = ((cnt + t.passes - 1) / t.passes + 15) & ~15;   // <= TN: passes = ceil(cnt / TN)
     const int start = t.pass * per;
-    return {(int64_t)__ldg(a.offsets + t.e) + start, min(per, cnt - start)};
+    return {(int64_t)__ldcg(a.offsets + t.e) + start, min(per, cnt - start)};
 }
 // The pair at plan position pos, -1 outside the plan or the bucket (a plan from elsewhere).
 __device__ __forceinline__ int pair_at(const IdArgs &a, int64_t pos) {
     if (pos < 0 || pos >= a.pairs) return -1;
-    const int p = __ldg(a.items + pos);
+    const int p = __ldcg(a.items + pos);
     return p >= 0 && p < a.pairs ? p : -1;
 }
 
@@ -299,8 +299,8 @@ __global__ void __launch_bounds__(256) dequant_pairs_kernel(const int8_t *__rest
                                                             const int32_t *__restrict__ offsets,
                                                             const int32_t *__restrict__ items, int E, int pairs, int k,
                                                             int per_pair, int kb, int64_t pitch, __half *__restrict__ B) {
-    pdl_trigger();
     pdl_wait();
+    pdl_trigger();   // after the wait: when mmq_id_kernel starts, the kernel that wrote the plan has completed
     const int pos = blockIdx.x * 8 + (threadIdx.x >> 5), w = threadIdx.x & 3, b0 = (threadIdx.x & 31) >> 2;
     if (pos >= pairs || pos >= __ldg(offsets + E)) return;   // positions past the plan hold no pair
     const int p = __ldg(items + pos);
@@ -356,7 +356,6 @@ __global__ void __launch_bounds__(THREADS, 1) mmq_id_kernel(const __grid_constan
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     pdl_trigger();
-    pdl_wait();   // the plan and the binary16 rows come from the kernels before
     if (warp == 0) {
         // prefix of the experts' pass counts: lane l sums experts l * per .. l * per + per - 1. Plans of
         // this bucket have at most pairs / TN + E passes; counts with more are refused (fault bit 1).
@@ -460,6 +459,7 @@ __global__ void __launch_bounds__(THREADS, 1) mmq_id_kernel(const __grid_constan
         __syncwarp();
     } else if (warp == ACT_WARP) {   // ---------------- activations
         if (elect_one()) {
+            pdl_wait();   // the binary16 rows; in every CTA, so that this kernel completes after that one
             Ring r = {0, 0};
             uint32_t issued = 0;   // stages filled by this CTA
             bool ok = true;
