@@ -44,9 +44,17 @@
 //     cycles, so a division in its loop is 200 cycles of its stage;
 //   - stmatrix and 16-byte stores in the epilogue 101 / 284 (down projection 193 -> 127);
 //   - the single warps' loops in one elected thread, the MMA thread looking at the next stage's barrier
-//     before it issues this one's MMAs 92 / 276; eight converter warps for sixteen 88 / 242.
-// Passes of 64 pairs with six stages for few pairs per expert were 5% slower, two pipelines with an MMA
-// thread each no faster.
+//     before it issues this one's MMAs 92 / 276; eight converter warps for sixteen 88 / 242;
+//   - the plan read and weights in flight while dequant_pairs_kernel runs 84 / 237 (of which that kernel takes
+//     9 / 31, mostly the writing of 21 / 168 MB).
+// What is left: with the conversion's arithmetic taken out 73 / 197, with two MMAs a stage of eight 82 / 212, with
+// both 70 / 173; the tensor pipe is 22% / 59% active, the issue slots 59% / 68%. A stage's hand-overs from role
+// to role cost about 450 cycles that no arrangement tried here hides:
+//   - passes of 64 pairs with six stages for few pairs per expert 5% slower; passes of up to 256 pairs (a converted
+//     weight serves twice the products) with stages of 64 K 117 / 243;
+//   - two pipelines with an MMA thread each, or four converter groups: the same;
+//   - image rows converted once (21 MB for 168) and gathered by four-row copies from two warps' elected threads
+//     108 / 352: a gather takes the copy engine 20 cycles.
 // The conversion of the weights is that of the dense prefill kernel (k_mmq.cu).
 
 #include <cuda_bf16.h>
