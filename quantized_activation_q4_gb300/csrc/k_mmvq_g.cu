@@ -67,17 +67,16 @@ __global__ void __launch_bounds__(256) pack_g_kernel(const uint8_t *__restrict__
 // takes), its warps take wr = WARPS / wk strips times wk pieces of the share, and the partial sums meet in
 // shared memory, added in the order of K. Work items are (pass, row block); a pass is the call's tokens, or
 // up to eight planned pairs of one expert. Every CTA takes a contiguous range of items, and the loads of
-// the next item's weights are in flight while one is finished. Two forms:
-//   many items: a CTA takes all of K. Two CTAs of eight warps per SM while K's fragments fit twice, else one
-//     of sixteen.
-//   few items: clusters of `split` CTAs share K, and sum in distributed shared memory.
-// With clusters for all, the release of a cluster's barrier waited for the weight loads in flight: 8192 x
-// 65536 took 105 us.
+// the next item's weights are in flight while one is finished. A CTA has all of K, or a cluster of `split` CTAs
+// shares it and sums in distributed shared memory; the release of a cluster's barrier waits for the weight
+// loads in flight, so that an item of a cluster costs about 4 us and clusters pay only for few items
+// (launch_matvec has the figures).
 constexpr int RED_STRIDE = 36;       // floats between two tokens' 32 rows of partial sums: no bank conflicts
 constexpr int RED = 8 * RED_STRIDE;  // floats of one warp's partial sums
 constexpr int FEW_WARPS = 8, MANY_WARPS = 16;
 // chunks of K whose fragments a CTA holds at a time
 __host__ __device__ constexpr int max_chunks(int warps) { return warps == FEW_WARPS ? 34 : 72; }
+constexpr int SHORT_CHUNKS = 20;     // K up to 2560
 constexpr int PFD = 2;                // chunks
 constexpr uint32_t SPIN_LIMIT = 1u << 16, SUSPEND_NS = 20000;   // a wait gives up after about a second
 
@@ -475,21 +474,32 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) mmvq_g_kernel(const __
     auto sum_item = [&](int it) {
         int pass, rb;
         const GProj &P = a.p[item_proj(it, pass, rb)];
-        const uint32_t base = (uint32_t)__cvta_generic_to_shared(red + (it & 1) * WARPS * RED);
+        const float *base = red + (it & 1) * WARPS * RED;
         for (int v = rank * THREADS + threadIdx.x; v < wr * 256; v += split * THREADS) {
             const int s = v >> 8, tok = (v >> 5) & 7, r = v & 31, n = (rb * wr + s) * STRIP_ROWS + r;
             const int o = tok_out[pass & 3][tok];
             if (n >= P.N || o < 0) continue;
+            const float *part = base + s * wk * RED + tok * RED_STRIDE + r;
             float sum = 0.0f;
-            for (uint32_t q = 0; q < split; q++) {
-                uint32_t far;
-                asm("mapa.shared::cluster.u32 %0, %1, %2;"
-                    : "=r"(far)
-                    : "r"(base + 4u * (s * wk * RED + tok * RED_STRIDE + r)), "r"(q));
-                for (int w = 0; w < wk; w++) {
-                    float x;
-                    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(far + 4u * w * RED) : "memory");
-                    sum += x;
+            if (split == 1) {
+                for (int w = 0; w < wk; w++) sum += part[w * RED];
+            } else {   // eight loads in flight: one after another 64 of them took 8 us
+                const uint32_t own = (uint32_t)__cvta_generic_to_shared(part);
+                const int parts = split << wk_log2;
+                for (int i0 = 0; i0 < parts; i0 += 8) {
+                    float x[8];
+#pragma unroll
+                    for (int i = 0; i < 8; i++) {
+                        x[i] = 0.0f;
+                        if (i0 + i >= parts) continue;
+                        uint32_t far;
+                        asm("mapa.shared::cluster.u32 %0, %1, %2;"
+                            : "=r"(far)
+                            : "r"(own + 4u * ((i0 + i) & (wk - 1)) * RED), "r"((i0 + i) >> wk_log2));
+                        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x[i]) : "r"(far) : "memory");
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; i++) sum += x[i];
                 }
             }
             P.y[o * P.y_stride + n] = sum;
@@ -671,18 +681,25 @@ template <int G, bool ROUTED>
 qk_status launch_matvec(GArgs &a, int64_t passes, cudaStream_t s) {
     int chunks = 0;
     for (int j = 0; j < a.n_proj; j++) chunks = a.p[j].chunks > chunks ? a.p[j].chunks : chunks;
-    // Many items (two and more for every CTA, with warps over rows alone or two to a strip): a CTA takes all
-    // of K. Else, or where K's fragments do not fit, K is shared by the most CTAs (up to 8) whose equal
-    // shares waste at most a tenth.
-    const int sms = sm_count();
-    if (chunks <= max_chunks(FEW_WARPS) && passes * row_blocks_of_all<FEW_WARPS>(a, 1) >= 4 * sms)
-        return launch_form<G, ROUTED, FEW_WARPS>(a, passes, 1, chunks, s);
-    if (chunks <= max_chunks(MANY_WARPS) && passes * row_blocks_of_all<MANY_WARPS>(a, 2) >= 2 * sms)
-        return launch_form<G, ROUTED, MANY_WARPS>(a, passes, 1, chunks, s);
-    int split = 1;
-    for (int q = 2; q <= 8 && q <= chunks; q++)
-        if (ceil_div(chunks, q) * q * 10 <= (int64_t)chunks * 11) split = q;
-    return launch_form<G, ROUTED, FEW_WARPS>(a, passes, split, chunks, s);
+    // Which form (us for eight warps alone / sixteen alone / clusters of up to eight CTAs, T = 4):
+    //   short K, fragments made soon: eight warps, two CTAs per SM. 1024 -> 4096: 4.3 / 4.8 / 5.2, 2560 -> 512:
+    //     5.4 / 5.8 / 5.7, 2560 -> 16384: 10.7 / 10.7 / 12.9.
+    //   fewer than two units for every warp of the GPU: K shared by the most CTAs (up to 8) whose equal shares
+    //     waste at most a tenth. 4096 -> 512: 6.6 / 6.0 / 5.1, 8192 -> 2048: 12.5 / 9.6 / 7.2.
+    //   else sixteen warps, and K shared only as far as its fragments do not fit one CTA: 8192 -> 4096:
+    //     17 / 10.2 / 12.4, 8192 -> 16384: 35 / 24 / 38; 18944 -> 16384 in clusters of 1, 2, 3, 4, 8 CTAs of
+    //     sixteen: 84, 84, 43, 75, 60 (one and two make fragments for every item anew).
+    int64_t units = 0;
+    for (int j = 0; j < a.n_proj; j++) units += ceil_div(a.p[j].N, STRIP_ROWS) * a.p[j].chunks;
+    if (chunks <= SHORT_CHUNKS) return launch_form<G, ROUTED, FEW_WARPS>(a, passes, 1, chunks, s);
+    if (passes * units < 2 * MANY_WARPS * sm_count()) {
+        int split = 1;
+        for (int q = 2; q <= 8 && q <= chunks; q++)
+            if (ceil_div(chunks, q) * q * 10 <= (int64_t)chunks * 11) split = q;
+        return launch_form<G, ROUTED, FEW_WARPS>(a, passes, split, chunks, s);
+    }
+    const int64_t split = ceil_div(chunks, max_chunks(MANY_WARPS));
+    return launch_form<G, ROUTED, MANY_WARPS>(a, passes, (int)(split < 8 ? split : 8), chunks, s);
 }
 
 }  // namespace

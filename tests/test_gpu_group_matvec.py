@@ -281,11 +281,15 @@ def test_routed_projections_of_different_inner_sizes(G, Ks):
 
 
 @pytest.mark.parametrize("G,T,K,Ns", [
-    (64, 8, 256, (120000,)),             # items for every CTA several times over, all of K in eight warps' CTAs
-    (128, 3, 4352, (20000, 19003, 33)),  # the longest K of that form
-    (64, 5, 4416, (40000,)),             # one chunk more: sixteen warps
-    (128, 8, 9216, (25001, 15000)),      # the longest of that one
-    (64, 2, 9280, (20000,)),             # K shared by a cluster, in two pieces each
+    (64, 8, 256, (120000,)),             # short K: eight warps, items for every CTA several times over
+    (128, 3, 2560, (20000, 19003, 33)),  # the longest of that form
+    (64, 5, 2624, (40000,)),             # one chunk more: sixteen warps
+    (128, 8, 9216, (25001, 15000)),      # the longest K whose fragments a CTA holds
+    (64, 2, 9280, (20000,)),             # shared by two CTAs of sixteen warps
+    (128, 4, 18944, (9000, 40)),         # by three
+    (64, 3, 75776, (1000,)),             # by eight, with two pieces each
+    (128, 3, 4352, (20000, 19003, 33)),
+    (64, 5, 4416, (40000,)),
 ])
 def test_matvec_with_many_rows(G, T, K, Ns):
     import torch
@@ -316,7 +320,7 @@ def test_matvec_with_many_rows(G, T, K, Ns):
 
 @pytest.mark.parametrize("slots", [False, True])
 def test_routed_with_long_rows_and_many_passes(slots):
-    """K beyond the eight-warp form and items for every CTA: the sixteen-warp routed form."""
+    """K beyond the eight-warp form and items for every CTA several times over: the sixteen-warp routed form."""
     import torch
     rows, k, E, K, N, live = 300, 2, 5, 4608, 2400, 287
     img = image(12100, rows * k if slots else rows, K)
