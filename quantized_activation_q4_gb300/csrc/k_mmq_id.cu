@@ -57,6 +57,8 @@
 //     108 / 352: a gather takes the copy engine 20 cycles.
 // The conversion of the weights is that of the dense prefill kernel (k_mmq.cu).
 
+#include <atomic>
+
 #include <cuda_bf16.h>
 
 #include "qk_internal.cuh"
@@ -636,8 +638,14 @@ __global__ void __launch_bounds__(THREADS, 1) mmq_id_kernel(const __grid_constan
 
 template <int WT>
 qk_status launch_type(const IdArgs &a, cudaStream_t s) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(mmq_id_kernel<WT>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+    constexpr int MAXDEV = 64;
+    static std::atomic<bool> set[MAXDEV];   // the kernel's attribute, once per device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && (dev < 0 || dev >= MAXDEV || !set[dev].load(std::memory_order_relaxed))) {
+        e = cudaFuncSetAttribute(mmq_id_kernel<WT>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+        if (e == cudaSuccess && dev >= 0 && dev < MAXDEV) set[dev].store(true, std::memory_order_relaxed);
+    }
     if (e != cudaSuccess) return fail(QK_ERR_CUDA, "mmq_id: shared memory attribute: %s", cudaGetErrorString(e));
     return launch_pdl("mmq_id", mmq_id_kernel<WT>, dim3((unsigned)sm_count()), dim3(THREADS), (size_t)SMEM_BYTES, s, a);
 }
@@ -667,7 +675,7 @@ qk_status launch_mmq_id(const int8_t *qs, const uint16_t *d, int64_t row_blocks,
     const int64_t pitch = act_pitch(kmax), slabs = pitch / KC;
     PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
     if (!enc) return fail(QK_ERR_CUDA, "mmq_id: cuTensorMapEncodeTiled is not available");
-    for (int h = 0; h < 4; h++) {
+    for (int h = 0; h < 4 && BOX_ROWS * h < pairs; h++) {   // no pass needs a larger box
         const cuuint64_t dims[3] = {KC, (cuuint64_t)pairs, (cuuint64_t)slabs};
         const cuuint64_t strides[2] = {(cuuint64_t)pitch * 2, KC * 2};
         const cuuint32_t box[3] = {KC, (cuuint32_t)(BOX_ROWS * (h + 1)), 2}, estr[3] = {1, 1, 1};
