@@ -367,34 +367,42 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) mmvq_g_kernel(const __
     const int64_t items = (int64_t)passes * row_blocks;
     const int it0 = (int)(items * cluster / clusters), it1 = (int)(items * (cluster + 1) / clusters);
 
-    // item -> pass, projection, row block of the projection
-    auto item_proj = [&](int it, int &pass, int &rb) {
-        pass = ROUTED ? it / row_blocks : 0;
-        rb = it - pass * row_blocks;
+    // Items are walked by additions: a place is a pass and one of its row blocks. Row block -> projection and
+    // row block of the projection.
+    auto proj_of = [&](int at, int &rb) {
         int j = 0;
-        while (j + 1 < a.n_proj && rb >= rb_base[j + 1]) j++;
-        rb -= rb_base[j];
+        while (j + 1 < a.n_proj && at >= rb_base[j + 1]) j++;
+        rb = at - rb_base[j];
         return j;
+    };
+    const int pass0 = ROUTED && it0 < it1 ? it0 / row_blocks : 0, at0 = it0 - pass0 * row_blocks;
+    auto next_place = [&](int &pass, int &at) {
+        if (++at == row_blocks) {
+            at = 0;
+            pass++;
+        }
     };
     // The walk of this warp over its weights: the chunks of its strip and its piece of K, item after item,
     // sub-share (MAXC chunks) after sub-share.
     const uint8_t *wp = nullptr;
-    int w_left = 0, w_item = it0 - 1, w_from = 0, w_to = 0;   // w_from .. w_to: the CTA's chunks not yet walked
-    auto seek = [&]() {   // to the next non-empty run; w_item == it1 at the end
-        while (w_left == 0 && w_item < it1) {
+    int w_left = 0, w_items = it1 - it0 + 1, w_from = 0, w_to = 0;   // w_from .. w_to: the CTA's chunks not yet walked
+    int w_pass = pass0, w_at = at0 - 1;
+    auto seek = [&]() {   // to the next non-empty run; no items left at the end
+        while (w_left == 0 && w_items > 0) {
             if (w_from >= w_to) {
-                if (++w_item >= it1) return;
+                if (--w_items == 0) return;
+                next_place(w_pass, w_at);
                 w_from = w_to = 0;
             }
-            int pass, rb;
-            const int j = item_proj(w_item, pass, rb);
+            int rb;
+            const int j = proj_of(w_at, rb);
             const GProj &P = a.p[j];
             if (w_to == 0) {
                 w_from = share_lo[j];
                 w_to = share_hi[j];
             }
             int e = 0, first = 0;
-            if (ROUTED) find_pass(pre, a.E, pass, e, first);
+            if (ROUTED) find_pass(pre, a.E, w_pass, e, first);
             const int strip = rb * wr + ws, n = min(w_to - w_from, MAXC);
             const int b = w_from + ((n * kw) >> wk_log2), end = w_from + ((n * (kw + 1)) >> wk_log2);
             w_from += n;
@@ -416,9 +424,12 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) mmvq_g_kernel(const __
     };
     Chunk<G> even, odd;   // the next two chunks of the walk; `turn`: which comes first
     int turn = 0;
-    fetch(even);
-    fetch(odd);
-    if (!ROUTED) pdl_wait();   // weights are never written by the kernel before (see the header); the image may be
+    bool streaming = !ROUTED;
+    if (!ROUTED) {
+        fetch(even);
+        fetch(odd);
+        pdl_wait();   // weights are never written by the kernel before (see the header); the image may be
+    }
 
     // Pass q's tokens: image rows and output rows, -1 for none (of a warp: its first eight lanes)
     auto list_tokens = [&](int q) {
@@ -471,9 +482,9 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) mmvq_g_kernel(const __
     };
     // An item's sums over wk and over the cluster, in the order of K: the wr strips' 256 each, spread over
     // the cluster's threads; rows run fastest.
-    auto sum_item = [&](int it) {
-        int pass, rb;
-        const GProj &P = a.p[item_proj(it, pass, rb)];
+    auto sum_item = [&](int it, int pass, int at) {
+        int rb;
+        const GProj &P = a.p[proj_of(at, rb)];
         const float *base = red + (it & 1) * WARPS * RED;
         for (int v = rank * THREADS + threadIdx.x; v < wr * 256; v += split * THREADS) {
             const int s = v >> 8, tok = (v >> 5) & 7, r = v & 31, n = (rb * wr + s) * STRIP_ROWS + r;
@@ -482,6 +493,7 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) mmvq_g_kernel(const __
             const float *part = base + s * wk * RED + tok * RED_STRIDE + r;
             float sum = 0.0f;
             if (split == 1) {
+#pragma unroll 4
                 for (int w = 0; w < wk; w++) sum += part[w * RED];
             } else {   // eight loads in flight: one after another 64 of them took 8 us
                 const uint32_t own = (uint32_t)__cvta_generic_to_shared(part);
@@ -505,11 +517,11 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) mmvq_g_kernel(const __
             P.y[o * P.y_stride + n] = sum;
         }
     };
-    int cur_pass = -1, cur_s0 = -1, cur_cols = -1;
-    if (warp == WARPS - 1 && it0 < it1) list_tokens(ROUTED ? it0 / row_blocks : 0);   // the first item's syncs follow
+    int cur_pass = -1, cur_s0 = -1, cur_cols = -1, pass = pass0, at = at0, last_pass = 0, last_at = 0;
+    if (warp == WARPS - 1 && it0 < it1) list_tokens(pass0);   // the first item's syncs follow
     for (int it = it0; it < it1; it++) {
-        int pass, rb;
-        const int j = item_proj(it, pass, rb);
+        int rb;
+        const int j = proj_of(at, rb);
         const GProj &P = a.p[j];
         const bool new_pass = pass != cur_pass;
         if (new_pass) {
@@ -526,12 +538,20 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) mmvq_g_kernel(const __
                 const int row = tok_row[pass & 1][lane >> 2];
                 const uint8_t *img_row = row < 0 ? nullptr : a.img + row * a.img_row_bytes;
 #pragma unroll 1
-                for (int c = s0 + warp; c < s1; c += 2 * WARPS) {
-                    Words w0, w1;
-                    load_words(w0, img_row, c, P.K, lane);
-                    load_words(w1, c + WARPS < s1 ? img_row : nullptr, c + WARPS, P.K, lane);
-                    make_rec<G>(rec[c - s0], w0, lane);
-                    if (c + WARPS < s1) make_rec<G>(rec[c + WARPS - s0], w1, lane);
+                for (int c = s0 + warp;; c += 2 * WARPS) {
+                    Words w[2];
+#pragma unroll
+                    for (int i = 0; i < 2; i++)
+                        load_words(w[i], c + i * WARPS < s1 ? img_row : nullptr, c + i * WARPS, P.K, lane);
+                    if (ROUTED && !streaming) {   // behind the image's words, which are waited for first
+                        streaming = true;
+                        fetch(even);
+                        fetch(odd);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 2; i++)
+                        if (c + i * WARPS < s1) make_rec<G>(rec[c + i * WARPS - s0], w[i], lane);
+                    if (c + 2 * WARPS >= s1) break;
                 }
                 __syncthreads();
                 cur_s0 = s0;
@@ -561,8 +581,10 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) mmvq_g_kernel(const __
         // and its buffer may be written.
         if (it > it0) {
             await_sums(it - 1 - it0);
-            sum_item(it - 1);
+            sum_item(it - 1, last_pass, last_at);
         }
+        last_pass = pass;
+        last_at = at;
         float *out = red + (it & 1) * WARPS * RED + warp * RED;   // [token][32 rows]
         const int g = lane >> 2, t2 = 2 * (lane & 3);
 #pragma unroll
@@ -573,10 +595,11 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) mmvq_g_kernel(const __
             out[(t2 + 1) * RED_STRIDE + g + 8 * i] = v1;
         }
         announce();
+        next_place(pass, at);
     }
     if (it1 > it0) {
         await_sums(it1 - 1 - it0);
-        sum_item(it1 - 1);
+        sum_item(it1 - 1, last_pass, last_at);
         if (split > 1) {   // no CTA leaves while another may read its sums
             cluster_arrive();
             cluster_wait();
