@@ -13,7 +13,7 @@
 namespace qk {
 namespace {
 
-constexpr int MAX_PROJ = 8;
+constexpr int MAX_PROJ = 8, MAX_E = 1024;
 constexpr unsigned FULL = 0xffffffffu;
 
 __device__ unsigned int g_mmvq_g_faults = 0;   // bits as qk_device_faults
@@ -199,25 +199,27 @@ __device__ __forceinline__ void chunk_product(const Chunk<G> &c, const Rec<G> &r
 // absent tokens (no row) are zeros; nothing of them is read. Loads and conversion apart, so that two
 // chunks' loads are in flight at once.
 struct Words {
-    uint32_t lo[4], hi[4], ds[4];
+    uint32_t lo[4], hi[4], ds;   // ds: the head of block t
 };
 __device__ __forceinline__ void load_words(Words &w, const uint8_t *img_row, int chunk, int K, int lane) {
     const int t = lane & 3;
+    w.ds = 0;
 #pragma unroll
     for (int jb = 0; jb < 4; jb++) {
-        w.lo[jb] = w.hi[jb] = w.ds[jb] = 0;
+        w.lo[jb] = w.hi[jb] = 0;
         if (img_row && chunk * UNIT_COLS + jb * QB < K) {
             const uint8_t *blk = img_row + (int64_t)(4 * chunk + jb) * Q8_1_BYTES;
-            w.ds[jb] = __ldg(reinterpret_cast<const unsigned int *>(blk));
             w.lo[jb] = __ldg(reinterpret_cast<const unsigned int *>(blk + 4 + 4 * t));
             w.hi[jb] = __ldg(reinterpret_cast<const unsigned int *>(blk + 20 + 4 * t));
         }
     }
+    if (img_row && chunk * UNIT_COLS + t * QB < K)
+        w.ds = __ldg(reinterpret_cast<const unsigned int *>(img_row + (int64_t)(4 * chunk + t) * Q8_1_BYTES));
 }
 template <int G>
 __device__ __forceinline__ void make_rec(Rec<G> &r, const Words &w, int lane) {
     const int g = lane >> 2, t = lane & 3;
-    float xs = 0.0f;
+    int sums[4];   // of a block's low and high halves, 16 bits each (|sum| <= 16 * 128)
 #pragma unroll
     for (int jb = 0; jb < 4; jb++) {
         // codes -> exact halves: q + 128 under the exponent of 1024, minus 1152
@@ -232,21 +234,23 @@ __device__ __forceinline__ void make_rec(Rec<G> &r, const Words &w, int lane) {
             o[i] = *reinterpret_cast<const uint32_t *>(&x);
         }
         r.b[jb][lane] = make_uint4(o[0], o[1], o[2], o[3]);
-        int sl = __dp4a((int)w.lo[jb], 0x01010101, 0), sh = __dp4a((int)w.hi[jb], 0x01010101, 0);
-#pragma unroll
-        for (int m = 1; m <= 2; m <<= 1) {
-            sl += __shfl_xor_sync(FULL, sl, m);
-            sh += __shfl_xor_sync(FULL, sh, m);
-        }
-        const float da = __half2float(__ushort_as_half((unsigned short)w.ds[jb]));
-        xs = fmaf(da, (float)(sl + sh), (jb * QB) % G == 0 ? 0.0f : xs);
-        if (t == 0) {
-            r.da[jb][g] = da;
-            float *st = reinterpret_cast<float *>(&r.start[jb][g >> 1]) + (g & 1);
-            st[0] = st[2] = -(float)((1024 + 8) * sl + (64 + 8) * sh);
-            r.xs[jb * QB / G][g] = xs;
-        }
+        sums[jb] = __dp4a((int)w.lo[jb], 0x01010101, 0) + (__dp4a((int)w.hi[jb], 0x01010101, 0) << 16);
     }
+    // four lanes' sums of four blocks, in three shuffles: lane t ends with block t's
+    const bool odd = t & 1, high = t & 2;
+    int s0 = odd ? sums[1] : sums[0], s1 = odd ? sums[3] : sums[2];
+    s0 += __shfl_xor_sync(FULL, odd ? sums[0] : sums[1], 1);
+    s1 += __shfl_xor_sync(FULL, odd ? sums[2] : sums[3], 1);
+    const int s = (high ? s1 : s0) + __shfl_xor_sync(FULL, high ? s0 : s1, 2);
+    const int sl = (short)s, sh = (s - sl) >> 16;
+    const float da = __half2float(__ushort_as_half((unsigned short)w.ds));
+    r.da[t][g] = da;
+    float *st = reinterpret_cast<float *>(&r.start[t][g >> 1]) + (g & 1);
+    st[0] = st[2] = -(float)((1024 + 8) * sl + (64 + 8) * sh);
+    float xs = da * (float)(sl + sh);
+    xs += __shfl_xor_sync(FULL, xs, 1);
+    if (G == 128) xs += __shfl_xor_sync(FULL, xs, 2);
+    if (t % (G / QB) == 0) r.xs[t * QB / G][g] = xs;
 }
 
 // Pass q of a routed call: its expert and the position of its first pair among the expert's.
@@ -269,19 +273,20 @@ __device__ __forceinline__ int clamped_count(const GArgs &a, int e) {
 
 template <int WARPS>
 __host__ __device__ inline int row_blocks_of(int N, int wk_log2) {
-    const int strips = (N + STRIP_ROWS - 1) / STRIP_ROWS, wr = WARPS >> wk_log2;
-    return (strips + wr - 1) / wr;
+    const int strips = (N + STRIP_ROWS - 1) / STRIP_ROWS, wr_log2 = (WARPS == FEW_WARPS ? 3 : 4) - wk_log2;
+    return (strips + (1 << wr_log2) - 1) >> wr_log2;
 }
 // Warps over rows; over K as well (two, four.. to a strip) while that leaves CTAs without work or the last
 // round of items more than a tenth empty, and a warp has two chunks of K.
 template <int WARPS>
-__host__ __device__ inline int choose_wk(const GArgs &a, int64_t passes, int64_t clusters) {
+__host__ __device__ inline int choose_wk(const GArgs &a, uint32_t passes, uint32_t clusters) {
     for (int wk = 0;; wk++) {
-        int64_t items = 0;
+        uint32_t items = 0;   // below 2^31 (qk_api.cu)
         for (int j = 0; j < a.n_proj; j++) items += row_blocks_of<WARPS>(a.p[j].N, wk);
         items *= passes;
-        const int64_t rounds = (items + clusters - 1) / clusters;
-        if ((items >= clusters && rounds * clusters * 10 <= items * 11) || (WARPS >> wk) == 1 || (a.held >> (wk + 1)) < 2)
+        const uint32_t rounds = (items + clusters - 1) / clusters;
+        if ((items >= clusters && (uint64_t)rounds * clusters * 10 <= (uint64_t)items * 11) || (WARPS >> wk) == 1 ||
+            (a.held >> (wk + 1)) < 2)
             return wk;
     }
 }
@@ -297,12 +302,13 @@ __device__ __forceinline__ void cluster_wait() {
 template <int G, bool ROUTED, int WARPS>
 __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) mmvq_g_kernel(const __grid_constant__ GArgs a) {
     constexpr int THREADS = WARPS * 32, MAXC = max_chunks(WARPS);
+    constexpr int FLIGHT = WARPS == FEW_WARPS ? 8 : 2;   // remote loads; sixteen warps have no registers for more
     extern __shared__ __align__(16) uint8_t smem[];
     Rec<G> *rec = reinterpret_cast<Rec<G> *>(smem);
     float *red = reinterpret_cast<float *>(rec + a.held);   // [2][WARPS][RED]
     int *pre = reinterpret_cast<int *>(red + 2 * WARPS * RED);    // [E + 1], routed calls
     __shared__ __align__(8) uint64_t written;   // a CTA that sums alone: its warps' arrivals, item after item
-    __shared__ int tok_row[2][8], tok_out[4][8], n_pass, share_lo[MAX_PROJ], share_hi[MAX_PROJ], rb_base[MAX_PROJ + 1];
+    __shared__ int tok_row[2][8], tok_out[4][8], warp_passes[WARPS], n_pass, share_lo[MAX_PROJ], share_hi[MAX_PROJ], rb_base[MAX_PROJ + 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint32_t rank, split;
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
@@ -320,30 +326,39 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) mmvq_g_kernel(const __
     int passes = 1;
     if (ROUTED) {
         pdl_wait();   // the plan decides which weights are read
-        if (warp == 0) {
-            // prefix of the experts' passes: lane l sums experts l * per ..; no plan of this bucket has
-            // more than pairs / 8 + E passes (counts with more: no work)
-            const int per = (a.E + 31) / 32, e0 = min(a.E, lane * per), e1 = min(a.E, e0 + per);
-            int64_t sum = 0;
-            for (int e = e0; e < e1; e++) sum += (clamped_count(a, e) + 7) / 8;
-            int64_t incl = sum;
+        // Prefix of the experts' passes: a thread has PER experts in a row. No plan of this bucket has more
+        // than pairs / 8 + E passes; sums stop one above (counts with more: no work).
+        constexpr int PER = MAX_E / THREADS;
+        const int most = a.T * a.k / 8 + a.E, e0 = threadIdx.x * PER;
+        int n[PER], sum = 0;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int64_t v = __shfl_up_sync(FULL, incl, o);
-                if (lane >= o) incl += v;
-            }
-            const int64_t total = __shfl_sync(FULL, incl, 31);
-            const bool sound = total <= (int64_t)a.T * a.k / 8 + a.E;
-            int64_t at = incl - sum;
-            for (int e = e0; e < e1; e++) {
-                pre[e] = sound ? (int)at : 0;
-                at += (clamped_count(a, e) + 7) / 8;
-            }
-            if (lane == 31) {
-                pre[a.E] = sound ? (int)total : 0;
-                n_pass = sound ? (int)total : 0;
-                if (!sound) atomicOr(&g_mmvq_g_faults, 2u);
-            }
+        for (int i = 0; i < PER; i++) n[i] = e0 + i < a.E ? (clamped_count(a, e0 + i) + 7) / 8 : 0;
+#pragma unroll
+        for (int i = 0; i < PER; i++) sum = min(sum + n[i], most + 1);
+        int incl = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(FULL, incl, o);
+            if (lane >= o) incl = min(incl + v, most + 1);
+        }
+        if (lane == 31) warp_passes[warp] = incl;
+        __syncthreads();
+        int total = 0, at = 0;
+#pragma unroll
+        for (int w = 0; w < WARPS; w++) {
+            if (w == warp) at = total;
+            total = min(total + warp_passes[w], most + 1);
+        }
+        at += incl - sum;
+        const bool sound = total <= most;
+#pragma unroll
+        for (int i = 0; i < PER; i++) {
+            if (e0 + i < a.E) pre[e0 + i] = sound ? at : 0;
+            at += n[i];
+        }
+        if (threadIdx.x == 0) {
+            pre[a.E] = n_pass = sound ? total : 0;
+            if (!sound) atomicOr(&g_mmvq_g_faults, 2u);
         }
     }
     __syncthreads();
@@ -364,8 +379,8 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) mmvq_g_kernel(const __
     const int row_blocks = rb_base[a.n_proj];
     const int wk = 1 << wk_log2, wr = WARPS >> wk_log2, kw = warp & (wk - 1), ws = warp >> wk_log2;
     // this cluster's items [it0, it1)
-    const int64_t items = (int64_t)passes * row_blocks;
-    const int it0 = (int)(items * cluster / clusters), it1 = (int)(items * (cluster + 1) / clusters);
+    const uint32_t items = (uint32_t)passes * row_blocks, per = items / clusters, more = items % clusters;
+    const int it0 = per * cluster + min((uint32_t)cluster, more), it1 = it0 + per + ((uint32_t)cluster < more ? 1 : 0);
 
     // Items are walked by additions: a place is a pass and one of its row blocks. Row block -> projection and
     // row block of the projection.
@@ -495,13 +510,14 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) mmvq_g_kernel(const __
             if (split == 1) {
 #pragma unroll 4
                 for (int w = 0; w < wk; w++) sum += part[w * RED];
-            } else {   // eight loads in flight: one after another 64 of them took 8 us
+            } else {   // several loads in flight: one after another 64 of them took 8 us
                 const uint32_t own = (uint32_t)__cvta_generic_to_shared(part);
                 const int parts = split << wk_log2;
-                for (int i0 = 0; i0 < parts; i0 += 8) {
-                    float x[8];
+#pragma unroll 1
+                for (int i0 = 0; i0 < parts; i0 += FLIGHT) {
+                    float x[FLIGHT];
 #pragma unroll
-                    for (int i = 0; i < 8; i++) {
+                    for (int i = 0; i < FLIGHT; i++) {
                         x[i] = 0.0f;
                         if (i0 + i >= parts) continue;
                         uint32_t far;
@@ -511,7 +527,7 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) mmvq_g_kernel(const __
                         asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x[i]) : "r"(far) : "memory");
                     }
 #pragma unroll
-                    for (int i = 0; i < 8; i++) sum += x[i];
+                    for (int i = 0; i < FLIGHT; i++) sum += x[i];
                 }
             }
             P.y[o * P.y_stride + n] = sum;
@@ -626,7 +642,7 @@ void fill(GArgs &a, const uint8_t *img, int64_t row_blocks, int n_proj, const Pr
 
 template <int G, bool ROUTED, int WARPS>
 constexpr size_t most_smem() {   // whatever the sizes, the same CTAs fit an SM
-    return max_chunks(WARPS) * sizeof(Rec<G>) + 2 * WARPS * RED * sizeof(float) + (ROUTED ? 1025 * 4 : 0);
+    return max_chunks(WARPS) * sizeof(Rec<G>) + 2 * WARPS * RED * sizeof(float) + (ROUTED ? (MAX_E + 1) * 4 : 0);
 }
 
 // Clusters of `split` CTAs that are resident at once, per device (0: the query failed).
@@ -672,7 +688,7 @@ qk_status launch_form(GArgs &a, int64_t passes, int split, int chunks, cudaStrea
     if (resident < 1) return fail(QK_ERR_CUDA, "mmvq: no cluster of %d CTAs fits", split);
     const int share = (int)ceil_div(chunks, split);
     a.held = share < max_chunks(WARPS) ? share : max_chunks(WARPS);
-    a.wk_log2 = choose_wk<WARPS>(a, passes, resident);   // a routed kernel chooses again by the passes there are
+    a.wk_log2 = choose_wk<WARPS>(a, (uint32_t)passes, (uint32_t)resident);   // a routed kernel chooses again by the passes there are
     constexpr int MOST_WK = WARPS == FEW_WARPS ? 3 : 4;
     const int64_t items = passes * row_blocks_of_all<WARPS>(a, ROUTED ? MOST_WK : a.wk_log2);   // fit an int (qk_api.cu)
     const int clusters = (int)(items < resident ? items : resident);
