@@ -277,7 +277,7 @@ QK_API qk_status qk_glu_q8_1_ex(qk_glu_kind kind, qk_glu_layout layout,
  * the device layout the projection kernels stream with 128-bit loads. The
  * packed layout is private to this library and may change between versions;
  * its size is qk_weight_packed_bytes(). K must be a multiple of 32 (Q4_0,
- * Q8_0) or of G.
+ * Q8_0) or of G; N and K of the group-scaled types are at most 2^31 - 1024.
  * Q4_0 and Q8_0 are read by qk_mmvq, qk_mmvq_static_ws, qk_mmvq_id and
  * qk_mmvq_id_slots, Q4_0 also by qk_mmq; the group-scaled types by the same
  * calls except qk_mmq; Q4_0 and the group-scaled types by qk_mmq_id and
@@ -609,7 +609,8 @@ typedef struct qk_proj_id16 {
  *   ws     workspace of qk_mmq_id_workspace_bytes bytes, 128-byte aligned:
  *          scratch, no state kept. Calls that may run concurrently need separate
  *          ones.
- *   rows   1..2^24 bucket rows, k 1..64, n_experts 1..1024
+ *   rows   1..2^24 bucket rows, k 1..64, n_experts 1..1024; N and K at most
+ *          2^31 - 1024
  * Errors: QK_ERR_ARG, QK_ERR_SHAPE, QK_ERR_UNSUPPORTED (also Q8_0 weights),
  * QK_ERR_ALIAS (also an output over counts, offsets or items),
  * QK_ERR_WORKSPACE.

@@ -45,6 +45,8 @@ using namespace qk;
     } while (0)
 
 constexpr int QK_W_LAST = QK_W_Q4_G128;
+// Largest N and K of the group-scaled weights and of the routed prefill: indices of whole units past them fit an int.
+constexpr int64_t MOST_NK = INT32_MAX - 1023;
 
 static bool aligned(const void *p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
@@ -52,7 +54,8 @@ static qk_status check_proj_common(int32_t wtype, const void *w, int64_t N, int6
     REQUIRE(wtype >= QK_W_Q4_0 && wtype <= QK_W_LAST, QK_ERR_ARG, "bad wtype %d", (int)wtype);
     REQUIRE(w, QK_ERR_ARG, "null weight pointer");
     REQUIRE(aligned(w, 16), QK_ERR_ARG, "packed weights must be 16-byte aligned");
-    REQUIRE(N >= 1 && N <= INT32_MAX && K >= 32 && K <= INT32_MAX, QK_ERR_ARG, "N or K out of range");
+    const int64_t most = group_scaled(wtype) ? MOST_NK : INT32_MAX;
+    REQUIRE(N >= 1 && N <= most && K >= 32 && K <= most, QK_ERR_ARG, "N or K out of range");
     REQUIRE(K % group_size(wtype) == 0, QK_ERR_SHAPE, "K=%lld is not a multiple of %d", (long long)K,
             group_size(wtype));
     REQUIRE(K / QB <= img_row_blocks, QK_ERR_SHAPE, "K=%lld reaches past the image row (%lld blocks)",
@@ -74,7 +77,7 @@ qk_status mmvq_validate(const void *img, int64_t img_row_blocks, int64_t T, int3
         const qk_proj &p = projs[j];
         qk_status st = check_proj_common(p.wtype, p.w, p.N, p.K, img_row_blocks);
         if (st != QK_OK) return st;
-        REQUIRE(p.y, QK_ERR_ARG, "projection %d: y is null", j);
+        REQUIRE(p.y && aligned(p.y, 4), QK_ERR_ARG, "projection %d: y is null or misaligned", j);
         REQUIRE(p.y_stride >= p.N, QK_ERR_SHAPE, "projection %d: y_stride < N", j);
         Span sy = span(p.y, rows_span(T, p.y_stride * 4, p.N * 4));
         Span sw = span(p.w, (size_t)packed_bytes(p.wtype, p.N, p.K));
@@ -344,7 +347,8 @@ size_t qk_weight_packed_bytes(qk_wtype wtype, int64_t N, int64_t K) {
 qk_status qk_weight_pack(qk_wtype wtype, const void *blocks, int64_t N, int64_t K, void *packed,
                          size_t packed_bytes_, qk_stream stream) {
     REQUIRE(wtype >= QK_W_Q4_0 && (int)wtype <= QK_W_LAST, QK_ERR_ARG, "bad wtype %d", (int)wtype);
-    REQUIRE(N >= 1 && K >= 32 && N <= INT32_MAX && K <= INT32_MAX, QK_ERR_ARG, "N or K out of range");
+    const int64_t most = group_scaled(wtype) ? MOST_NK : INT32_MAX;
+    REQUIRE(N >= 1 && K >= 32 && N <= most && K <= most, QK_ERR_ARG, "N or K out of range");
     const int G = group_size(wtype);
     REQUIRE(K % G == 0, QK_ERR_SHAPE, "K=%lld is not a multiple of %d", (long long)K, G);
     REQUIRE(blocks && packed, QK_ERR_ARG, "null pointer");
@@ -443,6 +447,7 @@ static qk_status mmvq_id_common(const void *img, int64_t img_row_blocks, int64_t
                                 const int32_t *items, bool per_pair, qk_stream stream) {
     REQUIRE(img && projs && counts && offsets && items, QK_ERR_ARG, "null pointer");
     REQUIRE(aligned(img, 4), QK_ERR_ARG, "img not 4-byte aligned");
+    REQUIRE(aligned(counts, 4) && aligned(offsets, 4) && aligned(items, 4), QK_ERR_ARG, "misaligned plan pointer");
     REQUIRE(rows >= 1 && rows <= (1 << 24) && k >= 1 && k <= 64 && img_row_blocks >= 1, QK_ERR_ARG,
             "rows, k or img_row_blocks out of range");
     REQUIRE(n_proj >= 1 && n_proj <= 8, QK_ERR_UNSUPPORTED, "n_proj=%d not in 1..8", (int)n_proj);
@@ -456,7 +461,7 @@ static qk_status mmvq_id_common(const void *img, int64_t img_row_blocks, int64_t
         qk_status st = check_proj_common(p.wtype, p.w, p.N, p.K, img_row_blocks);
         if (st != QK_OK) return st;
         REQUIRE(p.n_experts >= 1 && p.n_experts <= 1024, QK_ERR_UNSUPPORTED, "n_experts=%d", (int)p.n_experts);
-        REQUIRE(p.y, QK_ERR_ARG, "projection %d: y is null", j);
+        REQUIRE(p.y && aligned(p.y, 4), QK_ERR_ARG, "projection %d: y is null or misaligned", j);
         REQUIRE(projs[0].n_experts == p.n_experts, QK_ERR_ARG, "projections disagree on n_experts");
         Span sy = span(p.y, (size_t)(rows * k * p.N * 4));
         Span sw = span(p.w, (size_t)packed_bytes(p.wtype, p.N, p.K) * p.n_experts);
@@ -652,6 +657,7 @@ static qk_status mmq_id_common(const int8_t *qs, const uint16_t *d, int64_t row_
         qk_status st = check_proj_common(p.wtype, p.w, p.N, p.K, row_blocks);
         if (st != QK_OK) return st;
         REQUIRE(p.wtype != QK_W_Q8_0, QK_ERR_UNSUPPORTED, "projection %d: Q8_0 weights are not taken", j);
+        REQUIRE(p.N <= MOST_NK && p.K <= MOST_NK, QK_ERR_ARG, "projection %d: N or K out of range", j);
         REQUIRE(p.n_experts == E, QK_ERR_ARG, "projections disagree on n_experts");
         REQUIRE(p.y && aligned(p.y, 2), QK_ERR_ARG, "projection %d: y is null or misaligned", j);
         REQUIRE(p.y_stride >= p.N, QK_ERR_SHAPE, "projection %d: y_stride < N", j);
@@ -665,6 +671,11 @@ static qk_status mmq_id_common(const int8_t *qs, const uint16_t *d, int64_t row_
                     QK_ERR_ALIAS, "outputs of projections %d and %d overlap", i, j);
         tiles += ceil_div(p.N, UNIT_ROWS);
     }
+    for (int j = 0; j < n_proj; j++)
+        for (int i = 0; i < n_proj; i++)
+            REQUIRE(i == j || !overlap(span(projs[j].y, rows_span(pairs, projs[j].y_stride * 2, projs[j].N * 2)),
+                                       span(projs[i].w, (size_t)(packed_bytes(projs[i].wtype, projs[i].N, projs[i].K) * E))),
+                    QK_ERR_ALIAS, "y of projection %d overlaps the weights of projection %d", j, i);
     // work items (passes of any plan x row tiles) are counted in int
     REQUIRE((pairs / 128 + E) * tiles < (1LL << 31), QK_ERR_UNSUPPORTED, "rows * k * row tiles too large for one launch");
     const size_t need = qk_mmq_id_workspace_bytes(rows, k, n_proj, projs);

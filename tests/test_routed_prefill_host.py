@@ -120,6 +120,33 @@ def test_routed_prefill_checks(lib, slots):
     assert go(s=128, second=other(), ws_bytes=16) == 4
 
 
+def test_rows_and_columns_whose_units_pass_an_int_are_refused(lib):
+    """Indices are counted in whole units of 32 or 128 rows and 128 columns, past N and K."""
+    big, far = (1 << 31) - 1024, 1 << 60
+    for n, k in ((big + 1, 256), (64, (1 << 31) - 128)):
+        assert _mmq_id(lib, N=n, s=n, K=k, rb=1 << 26, y=far) == 1
+        one = (qk.qk_proj * 1)(qk.qk_proj(3, 0, W, n, k, far, n))
+        assert lib.qk_mmvq(P(IMG), 1 << 26, 1, 1, one, None, None, 0, None) == 1
+        routed = (qk.qk_proj_id * 1)(qk.qk_proj_id(3, 4, W, n, k, far))
+        assert lib.qk_mmvq_id(P(IMG), 1 << 26, 4, 2, 1, routed, P(PL), P(PL + 64), P(PL + 256), None) == 1
+        assert lib.qk_weight_pack(3, P(X), n, k, P(far), 1 << 62, None) == 1
+
+
+def test_misaligned_outputs_and_plans_are_refused(lib):
+    one = lambda y: (qk.qk_proj * 1)(qk.qk_proj(3, 0, W, 64, 256, y, 64))
+    assert lib.qk_mmvq(P(IMG), 8, 8, 1, one(Y + 2), None, None, 0, None) == 1
+    routed = lambda y: (qk.qk_proj_id * 1)(qk.qk_proj_id(3, 4, W, 64, 256, y))
+    assert lib.qk_mmvq_id(P(IMG), 8, 4, 2, 1, routed(Y + 2), P(PL), P(PL + 64), P(PL + 256), None) == 1
+    assert lib.qk_mmvq_id(P(IMG), 8, 4, 2, 1, routed(Y), P(PL), P(PL + 66), P(PL + 256), None) == 1
+
+
+def test_routed_prefill_outputs_stay_off_every_projections_weights(lib):
+    second = qk.qk_proj_id16(3, 4, W + 0x100000, 64, 256, W + 0x40, 64)     # over the first one's weights
+    assert _mmq_id(lib, second=second) == 3
+    second = qk.qk_proj_id16(3, 4, Y + 0x100, 64, 256, Y + 0x100000, 64)    # the first one's output over these
+    assert _mmq_id(lib, second=second) == 3
+
+
 def test_routed_prefill_work_items_fit_an_int(lib):
     assert _mmq_id(lib, rows=1 << 24, k=64, N=1 << 20, s=1 << 20, K=128, y=1 << 60) == 5
 
