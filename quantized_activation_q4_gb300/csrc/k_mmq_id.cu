@@ -556,11 +556,12 @@ __global__ void __launch_bounds__(THREADS, 1) mmq_id_kernel(const __grid_constan
                 if (!ok) break;
                 tc_fence_after();
                 const uint8_t *unit = smem + OFF_U + u.at * U_SLOT;
+                constexpr int HEAD_BLOCKS = WT == QK_W_Q4_0 ? 1 : WT == QK_W_Q4_G64 ? 2 : 4;   // blocks of one scale
+                RowHeads<WT> hd;
 #pragma unroll
                 for (int jb = 0; jb < 4; jb++) {
                     const uint4 wv = load_words<WT>(unit, quad, jb, lane);
-                    RowHeads<WT> hd;
-                    load_heads<WT>(unit, quad, jb, gq, hd);
+                    if (jb % HEAD_BLOCKS == 0) load_heads<WT>(unit, quad, jb, gq, hd);
                     const uint4 a0 = a_word(wv.x, hd.dw[0], hd.blo[0], hd.bhi[0]);
                     const uint4 a1 = a_word(wv.y, hd.dw[1], hd.blo[1], hd.bhi[1]);
                     const uint4 a2 = a_word(wv.z, hd.dw[2], hd.blo[2], hd.bhi[2]);
