@@ -265,3 +265,64 @@ def test_calls_on_two_streams_at_once():
     for _, yb, ym, _ in (a, b):
         assert torch.equal(yb, yb0) and torch.equal(ym, ym0)
     assert qk.qk_device_faults() == 0
+
+
+def test_plans_rewritten_between_calls():
+    """Plan, products, another plan into the same buffers, products .. without a wait in between: the products
+    read the plan early, so every result has to be that of its own plan, also in one captured graph."""
+    import torch
+    rows, k, E, K, N = 96, 2, 12, 128, 136
+    qs, dh = O.quantize_q8_0(synth.activations(14900, rows, K))
+    d_qs, d_dh = dev(qs), dev(dh.view(np.int16))
+    img = dev(O.quantize_q8_1(synth.activations(14901, rows, K)).reshape(-1))
+    Ws = [synth.q4_group_weight(14910 + e, N, K, 64) for e in range(E)]
+    pw = pack_experts(Ws, "q4_g64", N, K)
+    g = synth.rng(14902)
+    ids = [g.integers(0, E, size=(rows, k), dtype=np.int32) for _ in range(4)]
+    ids[1][:] = 7                                                            # one expert has everything
+    d_ids = [dev(i) for i in ids]
+    c, o, it = (torch.zeros((n,), dtype=torch.int32, device="cuda") for n in (E, E + 1, rows * k))
+    yb = [torch.zeros((rows * k, N), dtype=torch.bfloat16, device="cuda") for _ in ids]
+    ym = [torch.zeros((rows * k, N), device="cuda") for _ in ids]
+    n = qk.qk_mmq_id_workspace_bytes(rows, k, [qk.make_proj_id16("q4_g64", E, pw, N, K, yb[0], N)])
+    ws = torch.zeros((n,), dtype=torch.uint8, device="cuda")
+
+    def step(i, wait):
+        qk.qk_moe_plan(d_ids[i], rows, k, E, c, o, it)
+        qk.qk_mmq_id(d_qs, d_dh, K // 32, rows, k, [qk.make_proj_id16("q4_g64", E, pw, N, K, yb[i], N)], c, o, it, ws, n)
+        qk.qk_mmvq_id(img, K // 32, rows, k, [qk.make_proj_id("q4_g64", E, pw, N, K, ym[i])], c, o, it)
+        if wait:
+            torch.cuda.synchronize()
+
+    for i in range(4):
+        step(i, True)
+    want = [(a.clone(), b.clone()) for a, b in zip(yb, ym)]
+    x = O.plane_values(qs.reshape(rows, -1), dh.reshape(rows, -1), K)
+    Wd = [O.dequant_group(W, N, K) for W in Ws]
+    for i, (a, _) in enumerate(want):
+        ref = np.stack([x[p // k] @ Wd[e].T for p, e in enumerate(ids[i].reshape(-1))])
+        S = np.stack([np.abs(x[p // k]) @ np.abs(Wd[e]).T for p, e in enumerate(ids[i].reshape(-1))])
+        assert np.all(np.abs(host(a.float()) - ref) <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -9 * S)
+
+    def check(what):
+        torch.cuda.synchronize()
+        for i in range(4):
+            assert torch.equal(yb[i], want[i][0]) and torch.equal(ym[i], want[i][1]), (what, i)
+            yb[i].zero_()
+            ym[i].zero_()
+
+    for rep in range(25):
+        for i in range(4):
+            step(i, False)
+        check(f"run {rep}")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(s):
+        with torch.cuda.graph(graph, stream=s):
+            for i in range(4):
+                step(i, False)
+    for rep in range(25):
+        graph.replay()
+        check(f"replay {rep}")
+    assert qk.qk_device_faults() == 0
