@@ -141,7 +141,12 @@ def declared_symbols() -> list[str]:
 
 def _ptr(t):
     """A tensor's device address (an address or None as it is)."""
-    return t if t is None or isinstance(t, int) else t.data_ptr()
+    if t is None:
+        return None
+    try:   # a tensor, nearly always: no type test
+        return t.data_ptr()
+    except AttributeError:
+        return t
 
 
 _raw_stream = None   # device index -> torch's current stream as an address
