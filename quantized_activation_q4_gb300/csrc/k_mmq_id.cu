@@ -46,7 +46,8 @@
 //   - the single warps' loops in one elected thread, the MMA thread looking at the next stage's barrier
 //     before it issues this one's MMAs 92 / 276; eight converter warps for sixteen 88 / 242;
 //   - the plan read and weights in flight while dequant_pairs_kernel runs 84 / 237 (of which that kernel takes
-//     9 / 31, mostly the writing of 21 / 168 MB).
+//     9 / 31, mostly the writing of 21 / 168 MB); a group's scales loaded once for its blocks 84 / 229.
+// Those are bursts; over seconds the 4096 rows draw the GPU's 1400 W and take 266 at 1550 MHz.
 // What is left: with the conversion's arithmetic taken out 73 / 197, with two MMAs a stage of eight 82 / 212, with
 // both 70 / 173; the tensor pipe is 22% / 59% active, the issue slots 59% / 68%. A stage's hand-overs from role
 // to role cost about 450 cycles that no arrangement tried here hides:
