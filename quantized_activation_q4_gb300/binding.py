@@ -157,8 +157,9 @@ def _find_raw_stream():
     where torch offers it."""
     global _raw_stream
     import torch
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    _raw_stream = ((lambda: raw(torch.cuda.current_device())) if raw is not None
+    torch.cuda.current_device()   # initialises CUDA, once
+    raw, dev = (getattr(torch._C, n, None) for n in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
+    _raw_stream = ((lambda: raw(dev())) if raw is not None and dev is not None
                    else (lambda: torch.cuda.current_stream().cuda_stream))
     return _raw_stream
 
