@@ -212,12 +212,12 @@ __device__ __forceinline__ void load_words(Words &w, const uint8_t *img_row, int
         w.lo[jb] = w.hi[jb] = 0;
         if (img_row && chunk * UNIT_COLS + jb * QB < K) {
             const uint8_t *blk = img_row + (int64_t)(4 * chunk + jb) * Q8_1_BYTES;
-            w.lo[jb] = __ldg(reinterpret_cast<const unsigned int *>(blk + 4 + 4 * t));
-            w.hi[jb] = __ldg(reinterpret_cast<const unsigned int *>(blk + 20 + 4 * t));
+            w.lo[jb] = ld_prev(reinterpret_cast<const uint32_t *>(blk + 4 + 4 * t));
+            w.hi[jb] = ld_prev(reinterpret_cast<const uint32_t *>(blk + 20 + 4 * t));
         }
     }
     if (img_row && chunk * UNIT_COLS + t * QB < K)
-        w.ds = __ldg(reinterpret_cast<const unsigned int *>(img_row + (int64_t)(4 * chunk + t) * Q8_1_BYTES));
+        w.ds = ld_prev(reinterpret_cast<const uint32_t *>(img_row + (int64_t)(4 * chunk + t) * Q8_1_BYTES));
 }
 template <int G>
 __device__ __forceinline__ void make_rec(Rec<G> &r, const Words &w, int lane) {
@@ -270,7 +270,7 @@ __device__ __forceinline__ void find_pass(const int *pre, int E, int q, int &e, 
     first = 8 * (q - pre[lo]);
 }
 __device__ __forceinline__ int clamped_count(const GArgs &a, int e) {
-    const int c = __ldg(a.counts + e), pairs = a.T * a.k;
+    const int c = ld_prev(a.counts + e), pairs = a.T * a.k;
     return c < 0 ? 0 : (c > pairs ? pairs : c);
 }
 
@@ -459,10 +459,10 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) mmvq_g_kernel(const __
         if (ROUTED) {
             int e, first;
             find_pass(pre, a.E, q, e, first);
-            const int64_t pos = (int64_t)__ldg(a.offsets + e) + first + lane;
+            const int64_t pos = (int64_t)ld_prev(a.offsets + e) + first + lane;
             const int pairs = a.T * a.k;
             if (first + lane < clamped_count(a, e) && pos >= 0 && pos < pairs) {
-                const int pr = __ldg(a.items + pos);
+                const int pr = ld_prev(a.items + pos);
                 if (pr >= 0 && pr < pairs) {
                     out = pr;
                     row = a.per_pair ? pr : pr / a.k;

@@ -55,10 +55,23 @@ constexpr int Q8_0_BYTES = 34;
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// Reads of what an earlier kernel of the stream may have written, after pdl_wait. Not by __ldg nor through const
+// __restrict__ pointers: those may become non-coherent loads, which are for memory that nothing writes while the
+// kernel runs, and a kernel that starts early runs while its predecessor writes. (With them a routed matvec in a
+// captured graph took the counts of the replay before.)
+__device__ __forceinline__ uint32_t ld_prev(const uint32_t *p) {
+    uint32_t v;
+    asm volatile("ld.global.u32 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ int32_t ld_prev(const int32_t *p) {
+    return (int32_t)ld_prev(reinterpret_cast<const uint32_t *>(p));
+}
+
 // Live rows: min(rows, max(0, *live)), or rows when no pointer is given.
 __device__ __forceinline__ int live_rows(const int32_t *live, int rows) {
     if (!live) return rows;
-    int n = __ldg(live);
+    int n = ld_prev(live);
     return n < 0 ? 0 : (n > rows ? rows : n);
 }
 
