@@ -104,7 +104,7 @@ __device__ __forceinline__ Tile tile_of(const MmqArgs &a, int tau) {
 // grid (T, ceil(4 kb / 256)), tokens on x: thread j of CTA (t, y) takes word w = j & 3 of block
 // b = 64 y + j / 4 of token t: codes 4w .. 4w+3 and 16+4w .. 16+4w+3 -> f16 q * d_a at columns
 // 2w, 2w+1 (halves 4w .. 4w+3) and 8+2w, 9+2w (halves 16+4w ..), the K order of the A stages.
-__global__ void __launch_bounds__(256) dequant_b_kernel(const int8_t *__restrict__ qs, const uint16_t *__restrict__ d,
+__global__ void __launch_bounds__(256) dequant_b_kernel(const int8_t *qs, const uint16_t *d,
                                                         int64_t row_blocks, int T, int kb, __half *__restrict__ B) {
     pdl_trigger();
     pdl_wait();

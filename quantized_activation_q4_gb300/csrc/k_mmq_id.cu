@@ -305,16 +305,15 @@ __device__ __forceinline__ uint4 load_words(const uint8_t *unit, int quad, int j
 
 // A warp per plan position: row pos of the activations from the image row of the pair there, eight
 // blocks per step (lane l: word l & 3 of block l / 4).
-__global__ void __launch_bounds__(256) dequant_pairs_kernel(const int8_t *__restrict__ qs,
-                                                            const uint16_t *__restrict__ d, int64_t row_blocks,
-                                                            const int32_t *__restrict__ offsets,
-                                                            const int32_t *__restrict__ items, int E, int pairs, int k,
-                                                            int per_pair, int kb, int64_t pitch, __half *__restrict__ B) {
+__global__ void __launch_bounds__(256) dequant_pairs_kernel(const int8_t *qs, const uint16_t *d, int64_t row_blocks,
+                                                            const int32_t *offsets, const int32_t *items, int E,
+                                                            int pairs, int k, int per_pair, int kb, int64_t pitch,
+                                                            __half *__restrict__ B) {
     pdl_wait();
     pdl_trigger();   // after the wait: when mmq_id_kernel starts, the kernel that wrote the plan has completed
     const int pos = blockIdx.x * 8 + (threadIdx.x >> 5), w = threadIdx.x & 3, b0 = (threadIdx.x & 31) >> 2;
-    if (pos >= pairs || pos >= __ldg(offsets + E)) return;   // positions past the plan hold no pair
-    const int p = __ldg(items + pos);
+    if (pos >= pairs || pos >= ld_prev(offsets + E)) return;   // positions past the plan hold no pair
+    const int p = ld_prev(items + pos);
     if (p < 0 || p >= pairs) return;
     const int64_t first = (per_pair ? p : p / k) * row_blocks;
     __half *dst = B + pos * pitch;

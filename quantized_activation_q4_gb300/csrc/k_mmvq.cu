@@ -109,7 +109,7 @@ __device__ __forceinline__ uint4 ldg_stream16(const void *p) {
     return v;
 }
 __device__ __forceinline__ uint32_t ld_img4(const uint8_t *p) {
-    return __ldg(reinterpret_cast<const unsigned int *>(p));
+    return ld_prev(reinterpret_cast<const uint32_t *>(p));
 }
 __device__ __forceinline__ __half2 as_h2(uint32_t v) { return *reinterpret_cast<__half2 *>(&v); }
 __device__ __forceinline__ void mbar_init(uint32_t a, uint32_t count) {
@@ -953,10 +953,10 @@ __device__ __forceinline__ IdItem id_item(const IdArgs &a, const int32_t *live_e
 // Pair idx of expert e's planned pairs, or -1: past the expert's count, outside the items
 // array (offsets not from a plan of this bucket), or not a pair of this bucket.
 __device__ __forceinline__ int plan_pair(const IdArgs &a, int e, int idx) {
-    const int n_items = __ldg(a.counts + e);
-    const int64_t at = (int64_t)__ldg(a.offsets + e) + idx;
+    const int n_items = ld_prev(a.counts + e);
+    const int64_t at = (int64_t)ld_prev(a.offsets + e) + idx;
     if (idx >= n_items || at < 0 || at >= (int64_t)a.rows * a.k) return -1;
-    const int p = __ldg(a.items + at);
+    const int p = ld_prev(a.items + at);
     return p < 0 || p / a.k >= a.rows ? -1 : p;
 }
 
@@ -999,7 +999,7 @@ __global__ void __launch_bounds__(ID_THREADS, 2) mmvq_id_kernel(const __grid_con
         e = 32 * c + lane;
         // a count outside [0, rows * k] (not from a plan of this bucket) is clamped, so the work
         // stays bounded; plan_pair keeps every read inside items
-        const int cnt = e < a.E ? min(max(__ldg(a.counts + e), 0), a.rows * a.k) : 0;
+        const int cnt = e < a.E ? min(max(ld_prev(a.counts + e), 0), a.rows * a.k) : 0;
         passes = cnt > 0 ? (cnt + 7) / 8 : 0;
     };
     {

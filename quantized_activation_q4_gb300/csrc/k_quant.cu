@@ -25,11 +25,11 @@ constexpr unsigned FULL = 0xffffffffu;
 // a bound: elements at index >= n read as 0).
 __device__ __forceinline__ void load4(const float *p, int n, float v[4]) {
     if (n >= 4 && (reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
-        float4 t = __ldg(reinterpret_cast<const float4 *>(p));
+        const float4 t = ld_prev(reinterpret_cast<const float4 *>(p));
         v[0] = t.x; v[1] = t.y; v[2] = t.z; v[3] = t.w;
     } else {
 #pragma unroll
-        for (int i = 0; i < 4; i++) v[i] = i < n ? __ldg(p + i) : 0.0f;
+        for (int i = 0; i < 4; i++) v[i] = i < n ? ld_prev(p + i) : 0.0f;
     }
 }
 
@@ -97,7 +97,7 @@ __device__ __forceinline__ void put_q8_1(uint8_t *blk, int j8, float d, uint32_t
 // ceil(row_blocks / 16) (more rows in flight per SM, few idle lanes), wider rows 256 threads
 // with QPB = 4. Every block is quantised on its own, so the bytes do not depend on the shape.
 template <bool Q81, int QPB, int NT = 256>
-__global__ void __launch_bounds__(NT) quantize_kernel(const float *__restrict__ x, int K,
+__global__ void __launch_bounds__(NT) quantize_kernel(const float *x, int K,
                                                        int64_t x_stride, uint8_t *__restrict__ out,
                                                        int8_t *__restrict__ qs, uint16_t *__restrict__ dh,
                                                        int64_t row_blocks, int T, const int32_t *live) {
@@ -152,8 +152,8 @@ constexpr int RMS_ROWS_FOR_SMALL = 256;   // rows from which the 256-thread shap
 // prefill layout that qk_mmq reads.
 template <int NT, int ITEMS, bool Q81>
 __global__ void __launch_bounds__(NT, RMS_THREADS / NT) rmsnorm_q8_1_kernel(
-    const float *__restrict__ x, int K, int64_t x_stride, int kind, const float *__restrict__ w,
-    const float *__restrict__ bias, float scale, float eps, float *__restrict__ y, int64_t y_stride,
+    const float *x, int K, int64_t x_stride, int kind, const float *w,
+    const float *bias, float scale, float eps, float *__restrict__ y, int64_t y_stride,
     uint8_t *__restrict__ img, int8_t *__restrict__ qs, uint16_t *__restrict__ dh, int64_t row_blocks, int T,
     const int32_t *live) {
     constexpr bool EARLY = ITEMS <= 2;   // registers for the weight and bias next to the row
@@ -284,7 +284,7 @@ __device__ __forceinline__ float glu_out(int kind, float g, float u, float alpha
 
 // grid (T, ceil(N/1024)), 256 threads; thread i of CTA (t, cy) handles columns 1024*cy + 4i of row t.
 __global__ void __launch_bounds__(256) glu_q8_1_kernel(
-    int kind, int layout, const float *__restrict__ a, int64_t a_stride, const float *__restrict__ b,
+    int kind, int layout, const float *a, int64_t a_stride, const float *b,
     int64_t b_stride, int N, float *__restrict__ out, int64_t out_stride, uint8_t *__restrict__ img,
     int64_t row_blocks, int T, float alpha, float limit, const int32_t *live) {
     pdl_trigger();
@@ -432,16 +432,16 @@ struct Raw8 {
         const uint8_t *q = static_cast<const uint8_t *>(p) + i * (BF16 ? 2 : 4);
         if (wide) {
 #pragma unroll
-            for (int h = 0; h < (BF16 ? 1 : 2); h++) w[h] = __ldg(reinterpret_cast<const uint4 *>(q) + h);
+            for (int h = 0; h < (BF16 ? 1 : 2); h++) w[h] = ld_prev(reinterpret_cast<const uint4 *>(q) + h);
         } else {
             uint32_t x[BF16 ? 4 : 8];
 #pragma unroll
             for (int j = 0; j < (BF16 ? 4 : 8); j++) {
                 if (BF16)
-                    x[j] = __ldg(reinterpret_cast<const unsigned short *>(q) + 2 * j) |
-                           (uint32_t)__ldg(reinterpret_cast<const unsigned short *>(q) + 2 * j + 1) << 16;
+                    x[j] = ld_prev(reinterpret_cast<const uint16_t *>(q) + 2 * j) |
+                           (uint32_t)ld_prev(reinterpret_cast<const uint16_t *>(q) + 2 * j + 1) << 16;
                 else
-                    x[j] = __ldg(reinterpret_cast<const unsigned int *>(q) + j);
+                    x[j] = ld_prev(reinterpret_cast<const uint32_t *>(q) + j);
             }
 #pragma unroll
             for (int h = 0; h < (BF16 ? 1 : 2); h++) w[h] = make_uint4(x[4 * h], x[4 * h + 1], x[4 * h + 2], x[4 * h + 3]);
@@ -461,7 +461,7 @@ struct Raw8 {
 // row_mul = ceil(2^16 / blocks of a row), exact for the quotients of 0..63 here.
 template <int KIND, bool BF16>
 __global__ void __launch_bounds__(256, BF16 ? 6 : 4) glu_q8_0_kernel(
-    int layout, bool wide, const void *__restrict__ a, int64_t a_stride, const void *__restrict__ b, int64_t b_stride,
+    int layout, bool wide, const void *a, int64_t a_stride, const void *b, int64_t b_stride,
     int N, float *__restrict__ out, int64_t out_stride, int8_t *__restrict__ qs, uint16_t *__restrict__ dh,
     int64_t row_blocks, int T, int rows_per_cta, uint32_t row_mul, int step_row, int step_blk, float alpha, float limit,
     const int32_t *live) {

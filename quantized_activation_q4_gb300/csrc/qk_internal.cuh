@@ -55,10 +55,10 @@ constexpr int Q8_0_BYTES = 34;
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-// Reads of what an earlier kernel of the stream may have written, after pdl_wait. Not by __ldg nor through const
-// __restrict__ pointers: those may become non-coherent loads, which are for memory that nothing writes while the
-// kernel runs, and a kernel that starts early runs while its predecessor writes. (With them a routed matvec in a
-// captured graph took the counts of the replay before.)
+// Reads of what an earlier kernel of the stream may have written, after pdl_wait (plain reads through pointers without
+// __restrict__ do as well). Not by __ldg nor through const __restrict__ pointers: those may become non-coherent loads,
+// which are for memory that nothing writes while the kernel runs, and a kernel that starts early runs while its
+// predecessor writes. (With them a routed matvec in a captured graph took the counts of the replay before.)
 __device__ __forceinline__ uint32_t ld_prev(const uint32_t *p) {
     uint32_t v;
     asm volatile("ld.global.u32 %0, [%1];" : "=r"(v) : "l"(p));
@@ -66,6 +66,29 @@ __device__ __forceinline__ uint32_t ld_prev(const uint32_t *p) {
 }
 __device__ __forceinline__ int32_t ld_prev(const int32_t *p) {
     return (int32_t)ld_prev(reinterpret_cast<const uint32_t *>(p));
+}
+__device__ __forceinline__ float ld_prev(const float *p) {
+    return __uint_as_float(ld_prev(reinterpret_cast<const uint32_t *>(p)));
+}
+__device__ __forceinline__ uint16_t ld_prev(const uint16_t *p) {
+    uint16_t v;
+    asm volatile("ld.global.u16 %0, [%1];" : "=h"(v) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint2 ld_prev(const uint2 *p) {
+    uint2 v;
+    asm volatile("ld.global.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint4 ld_prev(const uint4 *p) {
+    uint4 v;
+    asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ float4 ld_prev(const float4 *p) {
+    float4 v;
+    asm volatile("ld.global.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p));
+    return v;
 }
 
 // Live rows: min(rows, max(0, *live)), or rows when no pointer is given.

@@ -120,12 +120,12 @@ __device__ __forceinline__ uint2 b_word(uint32_t v, __half2 d2) {
 
 // Word w of an image block (codes 4w .. 4w+3 and 16+4w .. 16+4w+3) -> f16 q * d_a at dst's columns 2w,
 // 2w+1 (halves 4w .. 4w+3) and 8+2w, 9+2w (halves 16+4w ..), the K order of the A stages.
-__device__ __forceinline__ void dequant_word(const int8_t *__restrict__ qs, const uint16_t *__restrict__ d, int64_t block,
+__device__ __forceinline__ void dequant_word(const int8_t *qs, const uint16_t *d, int64_t block,
                                              int w, __half *dst) {
     const int8_t *src = qs + block * QB;
-    const uint32_t lo = __ldg(reinterpret_cast<const unsigned int *>(src + 4 * w));
-    const uint32_t hi = __ldg(reinterpret_cast<const unsigned int *>(src + 16 + 4 * w));
-    const __half dah = __ushort_as_half(__ldg(d + block));
+    const uint32_t lo = ld_prev(reinterpret_cast<const uint32_t *>(src + 4 * w));
+    const uint32_t hi = ld_prev(reinterpret_cast<const uint32_t *>(src + 16 + 4 * w));
+    const __half dah = __ushort_as_half(ld_prev(d + block));
     const __half2 d2 = __halves2half2(dah, dah);
     *reinterpret_cast<uint2 *>(dst + 4 * w) = b_word(lo, d2);
     *reinterpret_cast<uint2 *>(dst + 16 + 4 * w) = b_word(hi, d2);
