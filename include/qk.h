@@ -433,7 +433,10 @@ typedef struct qk_proj_id {
  * output of qk_moe_plan; ids is not needed. A plan from anywhere else gives
  * unspecified outputs but no read outside counts, offsets and items: counts
  * are clamped to [0, rows * k] and an item position outside items, or a pair
- * outside the bucket, is skipped.
+ * outside the bucket, is skipped. On a given device a pair's output bits follow
+ * from its image row, its expert's weights, k and the sizes (N, K) of the call's
+ * projections: the live count, the bucket and other pairs' routes do not
+ * change them.
  *   rows: bucket rows (image rows >= rows never read); n_proj 1..8
  * Errors: QK_ERR_ARG, QK_ERR_UNSUPPORTED (n_experts > 1024), QK_ERR_SHAPE,
  * QK_ERR_ALIAS (also an output over counts, offsets or items).

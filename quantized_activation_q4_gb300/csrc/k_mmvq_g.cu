@@ -94,7 +94,7 @@ struct GArgs {
     int64_t img_row_bytes;
     const int32_t *live, *counts, *offsets, *items;
     int T, k, E, per_pair, n_proj;   // T: tokens, or bucket rows of a routed call
-    int wk_log2, held;               // wk = 1 << wk_log2 warps share a strip (ordinary calls); chunks of fragments
+    int wk_log2, held;               // wk = 1 << wk_log2 warps share a strip; chunks of fragments
     GProj p[MAX_PROJ];
 };
 
@@ -279,19 +279,44 @@ __host__ __device__ inline int row_blocks_of(int N, int wk_log2) {
     const int strips = (N + STRIP_ROWS - 1) / STRIP_ROWS, wr_log2 = (WARPS == FEW_WARPS ? 3 : 4) - wk_log2;
     return (strips + (1 << wr_log2) - 1) >> wr_log2;
 }
-// Warps over rows; over K as well (two, four.. to a strip) while that leaves CTAs without work or the last
-// round of items more than a tenth empty, and a warp has two chunks of K.
+// Whether 2 << wk_log2 warps may share a strip: there are so many, and each has two chunks of K.
 template <int WARPS>
-__host__ __device__ inline int choose_wk(const GArgs &a, uint32_t passes, uint32_t clusters) {
-    for (int wk = 0;; wk++) {
-        uint32_t items = 0;   // below 2^31 (qk_api.cu)
-        for (int j = 0; j < a.n_proj; j++) items += row_blocks_of<WARPS>(a.p[j].N, wk);
-        items *= passes;
-        const uint32_t rounds = (items + clusters - 1) / clusters;
-        if ((items >= clusters && (uint64_t)rounds * clusters * 10 <= (uint64_t)items * 11) || (WARPS >> wk) == 1 ||
-            (a.held >> (wk + 1)) < 2)
-            return wk;
+bool more_wk(const GArgs &a, int wk_log2) {
+    return (WARPS >> wk_log2) > 1 && (a.held >> (wk_log2 + 1)) >= 2;
+}
+template <int WARPS>
+int64_t row_blocks_of_all(const GArgs &a, int wk_log2) {
+    int64_t rbs = 0;
+    for (int j = 0; j < a.n_proj; j++) rbs += row_blocks_of<WARPS>(a.p[j].N, wk_log2);
+    return rbs;
+}
+// Ordinary calls: warps over rows; over K as well (two, four.. to a strip) while that leaves CTAs without work or the
+// last round of items more than a tenth empty.
+template <int WARPS>
+int choose_wk(const GArgs &a, int64_t clusters) {
+    int wk = 0;
+    for (; more_wk<WARPS>(a, wk); wk++) {
+        const int64_t items = row_blocks_of_all<WARPS>(a, wk), rounds = ceil_div(items, clusters);
+        if (items >= clusters && rounds * clusters * 10 <= items * 11) break;
     }
+    return wk;
+}
+// Routed calls: the split of K decides the order of a pair's sums, so it goes by the sizes and k alone and not by the
+// passes there are, which follow the live count, the bucket and other rows' routes. Many warps to a strip serve one
+// token, few serve many passes: the fewest whose items at one row (k passes) reach half of the resident CTAs.
+// us at 1, 2, 4, 8 warps to a strip, * the choice, and last by the passes there are with the rule for ordinary calls:
+//   2560 -> 2 x 768, 8 of 128 experts:   1 row 24, 16, 12.1*, 14.3 (14.8); 4 rows 25, 23, 22.0*, 26 (26.6);
+//                                        16 rows 38.8, 38.5, 39.3*, 47 (42.0); 64 rows 65, 62, 69*, 84 (65.2)
+//   768 -> 2560, 8 of 128:               1 row 12.0, 9.4* (9.6); 16 rows 26.0, 27.6* (28.2); 64 rows 42, 47* (47)
+//   4096 -> 512, 2 of 8:                 1 row 30, 18.5, 12.7, 9.6, 7.6 with sixteen* (8.2)
+//   4096 -> 2 x 14336, 2 of 8:           1 row 33.9*, 36, 33, 36 (33.1); 8 rows 81*, 85, 89, 100 (81)
+//   7168 -> 2 x 2048, 8 of 256:          1 row 52 with one, 31.9* (43); 8 rows 147, 150* (146)
+//   14336 -> 4096 (slots), 2 of 8:       1 row 50, 30, 20.4* (31); 8 rows 53, 48, 45*, 53 (60)
+template <int WARPS>
+int choose_routed_wk(const GArgs &a, int64_t clusters) {
+    int wk = 0;
+    while (more_wk<WARPS>(a, wk) && 2 * a.k * row_blocks_of_all<WARPS>(a, wk) < clusters) wk++;
+    return wk;
 }
 __device__ __forceinline__ void cluster_arrive() {
     __syncwarp();
@@ -368,11 +393,8 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) mmvq_g_kernel(const __
         }
     }
     __syncthreads();
-    int wk_log2 = a.wk_log2;
-    if (ROUTED) {
-        passes = n_pass;
-        wk_log2 = choose_wk<WARPS>(a, passes, clusters);
-    }
+    const int wk_log2 = a.wk_log2;
+    if (ROUTED) passes = n_pass;
     if (threadIdx.x == 0) {
         int rbs = 0;
         for (int j = 0; j < a.n_proj; j++) {
@@ -681,22 +703,14 @@ int resident_clusters(int split) {
     return n;
 }
 
-template <int WARPS>
-int64_t row_blocks_of_all(const GArgs &a, int wk_log2) {
-    int64_t rbs = 0;
-    for (int j = 0; j < a.n_proj; j++) rbs += row_blocks_of<WARPS>(a.p[j].N, wk_log2);
-    return rbs;
-}
-
 template <int G, bool ROUTED, int WARPS>
 qk_status launch_form(GArgs &a, int64_t passes, int split, int chunks, cudaStream_t s) {
     const int64_t resident = resident_clusters<G, ROUTED, WARPS>(split);
     if (resident < 1) return fail(QK_ERR_CUDA, "mmvq: no cluster of %d CTAs fits", split);
     const int share = (int)ceil_div(chunks, split);
     a.held = share < max_chunks(WARPS) ? share : max_chunks(WARPS);
-    a.wk_log2 = choose_wk<WARPS>(a, (uint32_t)passes, (uint32_t)resident);   // a routed kernel chooses again by the passes there are
-    constexpr int MOST_WK = WARPS == FEW_WARPS ? 3 : 4;
-    const int64_t items = passes * row_blocks_of_all<WARPS>(a, ROUTED ? MOST_WK : a.wk_log2);   // fit an int (qk_api.cu)
+    a.wk_log2 = ROUTED ? choose_routed_wk<WARPS>(a, resident) : choose_wk<WARPS>(a, resident);
+    const int64_t items = passes * row_blocks_of_all<WARPS>(a, a.wk_log2);   // fit an int (qk_api.cu)
     const int clusters = (int)(items < resident ? items : resident);
     const size_t smem = a.held * sizeof(Rec<G>) + 2 * WARPS * RED * sizeof(float) + (ROUTED ? (a.E + 1) * 4 : 0);
     auto kernel = mmvq_g_kernel<G, ROUTED, WARPS>;
@@ -734,10 +748,14 @@ qk_status launch_matvec(GArgs &a, int64_t passes, cudaStream_t s) {
     //   else sixteen warps, and K shared only as far as its fragments do not fit one CTA: 8192 -> 4096:
     //     17 / 10.2 / 12.4, 8192 -> 16384: 35 / 24 / 38; 18944 -> 16384 in clusters of 1, 2, 3, 4, 8 CTAs of
     //     sixteen: 84, 84, 43, 75, 60 (one and two make fragments for every item anew).
+    // A routed call never shares K for want of units: a pair's sums would be added in another order where the bucket
+    // has more rows. Sixteen warps to a strip do as well (4096 -> 512, 2 of 8, 1 row: 8.2 in clusters, 7.6).
+    // Routed calls with eight or sixteen warps where eight would hold K's 21 to 34 chunks too: 2688 -> 2 x 1408, 4 of
+    // 60, 8 rows 28.2 / 28.1; 4096 -> 2 x 1536, 2 of 8, 4 rows 18.0 / 17.0; 4096 -> 2 x 14336, 2 of 8, 8 rows 88 / 81.
     int64_t units = 0;
     for (int j = 0; j < a.n_proj; j++) units += ceil_div(a.p[j].N, STRIP_ROWS) * a.p[j].chunks;
     if (chunks <= SHORT_CHUNKS) return launch_form<G, ROUTED, FEW_WARPS>(a, passes, 1, chunks, s);
-    if (passes * units < 2 * MANY_WARPS * sm_count()) {
+    if (!ROUTED && units < 2 * MANY_WARPS * sm_count()) {
         int split = 1;
         for (int q = 2; q <= 8 && q <= chunks; q++)
             if (ceil_div(chunks, q) * q * 10 <= (int64_t)chunks * 11) split = q;
