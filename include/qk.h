@@ -390,9 +390,11 @@ QK_API qk_status qk_topk_route(const float *logits, int64_t rows, int32_t E, int
  * first live*k pairs only).
  *   pairs p = row*k + slot for rows < live; expert ids[p]
  *   counts [E]   pairs per expert
- *   offsets[E+1] exclusive scan of counts, offsets[E] = live*k
- *   items  [rows*k] positions 0..live*k-1 hold the pairs grouped by expert,
- *          ascending p within each expert; positions past live*k untouched
+ *   offsets[E+1] exclusive scan of counts, offsets[E] = the planned pairs
+ *   items  [rows*k] positions 0..offsets[E]-1 hold the pairs grouped by expert,
+ *          ascending p within each expert; positions from there on untouched
+ * Pairs whose id is outside [0, E) are left out. Without such pairs (as with
+ * qk_topk_route's ids) offsets[E] = live*k.
  * One launch for any width, also for rows = 0 or a live count of 0 (zero
  * counts and offsets). Errors: QK_ERR_ARG, QK_ERR_UNSUPPORTED (E > 1024),
  * QK_ERR_ALIAS.
@@ -453,8 +455,12 @@ QK_API qk_status qk_mmvq_id(const void *img, int64_t img_row_blocks, int64_t row
  * evidence" table, the per-slot routed components "K8192 / 32 slots / T8" and
  * "K2560 / 128 slots / T8"). img has rows * k rows.
  * In a routed FFN the per-pair image comes from qk_glu_q8_1 over the rows * k
- * gate/up output rows; passing offsets + E (the plan's count of planned pairs,
- * live * k) as that call's d_live_rows leaves the padding pairs untouched.
+ * gate/up output rows; passing offsets + E (live * k where the plan leaves no
+ * live pair out) as that call's d_live_rows leaves the padding pairs untouched.
+ * Where ids outside [0, E) leave pairs out, offsets[E] is smaller, while planned
+ * pairs reach up to live * k: that call is then given a count of live * k, and
+ * the rows of the pairs left out, which no projection writes, hold what the
+ * caller put there when qk_moe_combine sums them (zeros, say).
  * Errors: as qk_mmvq_id.
  */
 QK_API qk_status qk_mmvq_id_slots(const void *img, int64_t img_row_blocks, int64_t rows, int32_t k,
@@ -627,7 +633,8 @@ QK_API qk_status qk_mmq_id(const int8_t *qs, const uint16_t *d, int64_t row_bloc
 /*
  * qk_mmq_id_slots -- qk_mmq_id with one image row per pair: y[p][:] = W_e *
  * image row p (the down projection of a routed FFN, whose planes come from
- * qk_glu_q8_0 over the rows * k pair rows with offsets + E as its d_live_rows).
+ * qk_glu_q8_0 over the rows * k pair rows with offsets + E as its d_live_rows,
+ * or a count of live * k where the plan leaves pairs out: see qk_mmvq_id_slots).
  * The image has rows * k rows. Errors: as qk_mmq_id.
  */
 QK_API qk_status qk_mmq_id_slots(const int8_t *qs, const uint16_t *d, int64_t row_blocks, int64_t rows, int32_t k,
