@@ -314,7 +314,7 @@ typedef struct qk_proj {
  *   img  [T][img_row_blocks] Q8_1; every projection's K <= 32*img_row_blocks
  *   T    1..8 image rows (tokens); rows >= *d_live_rows are not written
  *   projs host array of n_proj (1..8) descriptors; outputs must not share a
- *        byte. Outputs with one y_stride may be disjoint column windows of
+ *        byte, nor one with any projection's weights. Outputs with one y_stride may be disjoint column windows of
  *        one buffer (q, k and v as columns of a fused [T][Nq+Nk+Nv] output).
  *   ws   device workspace of at least qk_mmvq_workspace_bytes(n_proj, projs)
  *        bytes, 16-byte aligned, ZEROED ONCE before its first use (e.g. by
@@ -520,7 +520,7 @@ QK_API qk_status qk_glu_q8_0(qk_glu_kind kind, qk_glu_layout layout, qk_elem ele
  *   qs [T][row_blocks*32] int8 and d [T][row_blocks] half: qk_quantize_q8_0
  *   C[t][n] = sum_b d_w[n][b] * d_a[t][b] * sum_{i in b} w_i * q_i
  *   (Q4_0: w_i = nibble - 8) written to projs[j].y ([T][y_stride] F32);
- *   outputs must not share a byte (disjoint column windows of one buffer
+ *   outputs must not share a byte, nor one with any weights (disjoint column windows of one buffer
  *   with one y_stride are allowed, as for qk_mmvq)
  * Runs on the tensor cores with binary16 operands (nibble - 8) * d_w and
  * q * d_a, each rounded once, accumulated in binary32: within about 2^-11
@@ -613,7 +613,7 @@ typedef struct qk_proj_id16 {
  * the routed products. Activations and weights beyond binary16's range (65504)
  * become infinities, as for qk_mmq.
  *   projs  host array of n_proj (1..8) descriptors with one n_experts; outputs
- *          must not share a byte (disjoint column windows of one buffer with one
+ *          must not share a byte, nor one with any weights (disjoint column windows of one buffer with one
  *          y_stride are allowed: gate and up as the packed rows of a GLU)
  *   ws     workspace of qk_mmq_id_workspace_bytes bytes, 128-byte aligned:
  *          scratch, no state kept. Calls that may run concurrently need separate

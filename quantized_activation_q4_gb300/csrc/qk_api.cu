@@ -63,6 +63,15 @@ static qk_status check_proj_common(int32_t wtype, const void *w, int64_t N, int6
     return QK_OK;
 }
 
+// No output lies over any projection's weights: CTAs read the one while others write the other.
+template <typename YSpan, typename WSpan>
+static qk_status outputs_off_weights(int32_t n_proj, YSpan y_of, WSpan w_of) {
+    for (int j = 0; j < n_proj; j++)
+        for (int i = 0; i < n_proj; i++)
+            REQUIRE(!overlap(y_of(j), w_of(i)), QK_ERR_ALIAS, "y of projection %d overlaps the weights of projection %d", j, i);
+    return QK_OK;
+}
+
 namespace qk {
 // Every check of qk_mmvq except those of the workspace: the image, T, the
 // projections, their outputs and aliasing between them.
@@ -80,14 +89,15 @@ qk_status mmvq_validate(const void *img, int64_t img_row_blocks, int64_t T, int3
         REQUIRE(p.y && aligned(p.y, 4), QK_ERR_ARG, "projection %d: y is null or misaligned", j);
         REQUIRE(p.y_stride >= p.N, QK_ERR_SHAPE, "projection %d: y_stride < N", j);
         Span sy = span(p.y, rows_span(T, p.y_stride * 4, p.N * 4));
-        Span sw = span(p.w, (size_t)packed_bytes(p.wtype, p.N, p.K));
-        REQUIRE(!overlap(sy, si) && !overlap(sy, sw), QK_ERR_ALIAS, "projection %d: y overlaps img or w", j);
+        REQUIRE(!overlap(sy, si), QK_ERR_ALIAS, "projection %d: y overlaps img", j);
         for (int i = 0; i < j; i++) {
             REQUIRE(!rows_overlap(projs[i].y, projs[i].y_stride * 4, projs[i].N * 4, p.y, p.y_stride * 4, p.N * 4, T),
                     QK_ERR_ALIAS, "outputs of projections %d and %d overlap", i, j);
         }
     }
-    return QK_OK;
+    return outputs_off_weights(
+        n_proj, [&](int j) { return span(projs[j].y, rows_span(T, projs[j].y_stride * 4, projs[j].N * 4)); },
+        [&](int j) { return span(projs[j].w, (size_t)packed_bytes(projs[j].wtype, projs[j].N, projs[j].K)); });
 }
 }  // namespace qk
 
@@ -464,14 +474,17 @@ static qk_status mmvq_id_common(const void *img, int64_t img_row_blocks, int64_t
         REQUIRE(p.y && aligned(p.y, 4), QK_ERR_ARG, "projection %d: y is null or misaligned", j);
         REQUIRE(projs[0].n_experts == p.n_experts, QK_ERR_ARG, "projections disagree on n_experts");
         Span sy = span(p.y, (size_t)(rows * k * p.N * 4));
-        Span sw = span(p.w, (size_t)packed_bytes(p.wtype, p.N, p.K) * p.n_experts);
-        REQUIRE(!overlap(sy, si) && !overlap(sy, sw), QK_ERR_ALIAS, "projection %d: y overlaps img or w", j);
+        REQUIRE(!overlap(sy, si), QK_ERR_ALIAS, "projection %d: y overlaps img", j);
         REQUIRE(!overlap(sy, plan[0]) && !overlap(sy, plan[1]) && !overlap(sy, plan[2]), QK_ERR_ALIAS,
                 "projection %d: y overlaps counts, offsets or items", j);
         for (int i = 0; i < j; i++)
             REQUIRE(!overlap(sy, span(projs[i].y, (size_t)(rows * k * projs[i].N * 4))), QK_ERR_ALIAS,
                     "outputs of projections %d and %d overlap", i, j);
     }
+    const qk_status alias = outputs_off_weights(
+        n_proj, [&](int j) { return span(projs[j].y, (size_t)(rows * k * projs[j].N * 4)); },
+        [&](int j) { return span(projs[j].w, (size_t)packed_bytes(projs[j].wtype, projs[j].N, projs[j].K) * E); });
+    if (alias != QK_OK) return alias;
     // the routed kernels count their work items in int: (passes of any plan) x (row tiles or strips) < 2^31
     int64_t tiles = 0;
     for (int j = 0; j < n_proj; j++) tiles += ceil_div(projs[j].N, group_scaled(projs[j].wtype) ? STRIP_ROWS : UNIT_ROWS);
@@ -608,13 +621,17 @@ qk_status qk_mmq(const int8_t *qs, const uint16_t *d, int64_t row_blocks, int64_
         if (st != QK_OK) return st;
         REQUIRE(p.wtype == QK_W_Q4_0, QK_ERR_UNSUPPORTED, "qk_mmq takes Q4_0 weights");
         REQUIRE(p.y && p.y_stride >= p.N, QK_ERR_SHAPE, "projection %d: y null or y_stride < N", j);
+        REQUIRE(aligned(p.y, 4), QK_ERR_ARG, "projection %d: y is misaligned", j);
         Span sy = span(p.y, rows_span(T, p.y_stride * 4, p.N * 4));
-        REQUIRE(!overlap(sy, sq) && !overlap(sy, sd) && !overlap(sy, span(p.w, (size_t)packed_bytes(p.wtype, p.N, p.K))),
-                QK_ERR_ALIAS, "projection %d: y overlaps an input", j);
+        REQUIRE(!overlap(sy, sq) && !overlap(sy, sd), QK_ERR_ALIAS, "projection %d: y overlaps the image", j);
         for (int i = 0; i < j; i++)
             REQUIRE(!rows_overlap(projs[i].y, projs[i].y_stride * 4, projs[i].N * 4, p.y, p.y_stride * 4, p.N * 4, T),
                     QK_ERR_ALIAS, "outputs of projections %d and %d overlap", i, j);
     }
+    const qk_status alias = outputs_off_weights(
+        n_proj, [&](int j) { return span(projs[j].y, rows_span(T, projs[j].y_stride * 4, projs[j].N * 4)); },
+        [&](int j) { return span(projs[j].w, (size_t)packed_bytes(projs[j].wtype, projs[j].N, projs[j].K)); });
+    if (alias != QK_OK) return alias;
     const size_t need = qk_mmq_workspace_bytes(T, n_proj, projs);
     REQUIRE(ws && aligned(ws, 128), QK_ERR_WORKSPACE, "workspace null or not 128-byte aligned");
     REQUIRE(ws_bytes >= need, QK_ERR_WORKSPACE, "workspace %zu < %zu bytes", ws_bytes, need);
@@ -662,8 +679,6 @@ static qk_status mmq_id_common(const int8_t *qs, const uint16_t *d, int64_t row_
         REQUIRE(p.y && aligned(p.y, 2), QK_ERR_ARG, "projection %d: y is null or misaligned", j);
         REQUIRE(p.y_stride >= p.N, QK_ERR_SHAPE, "projection %d: y_stride < N", j);
         const Span sy = span(p.y, rows_span(pairs, p.y_stride * 2, p.N * 2));
-        REQUIRE(!overlap(sy, span(p.w, (size_t)(packed_bytes(p.wtype, p.N, p.K) * E))), QK_ERR_ALIAS,
-                "projection %d: y overlaps its weights", j);
         for (int i = 0; i < 5; i++)
             REQUIRE(!overlap(sy, ins[i]), QK_ERR_ALIAS, "projection %d: y overlaps the image or the plan", j);
         for (int i = 0; i < j; i++)
@@ -671,11 +686,10 @@ static qk_status mmq_id_common(const int8_t *qs, const uint16_t *d, int64_t row_
                     QK_ERR_ALIAS, "outputs of projections %d and %d overlap", i, j);
         tiles += ceil_div(p.N, UNIT_ROWS);
     }
-    for (int j = 0; j < n_proj; j++)
-        for (int i = 0; i < n_proj; i++)
-            REQUIRE(i == j || !overlap(span(projs[j].y, rows_span(pairs, projs[j].y_stride * 2, projs[j].N * 2)),
-                                       span(projs[i].w, (size_t)(packed_bytes(projs[i].wtype, projs[i].N, projs[i].K) * E))),
-                    QK_ERR_ALIAS, "y of projection %d overlaps the weights of projection %d", j, i);
+    const qk_status alias = outputs_off_weights(
+        n_proj, [&](int j) { return span(projs[j].y, rows_span(pairs, projs[j].y_stride * 2, projs[j].N * 2)); },
+        [&](int j) { return span(projs[j].w, (size_t)(packed_bytes(projs[j].wtype, projs[j].N, projs[j].K) * E)); });
+    if (alias != QK_OK) return alias;
     // work items (passes of any plan x row tiles) are counted in int
     REQUIRE((pairs / 128 + E) * tiles < (1LL << 31), QK_ERR_UNSUPPORTED, "rows * k * row tiles too large for one launch");
     const size_t need = qk_mmq_id_workspace_bytes(rows, k, n_proj, projs);
