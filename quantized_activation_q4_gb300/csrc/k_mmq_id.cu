@@ -14,10 +14,10 @@
 // plain tile; then mmq_id_kernel.
 //
 // Work items are (expert, 128-row weight tile, pass): a pass is up to 128 of the expert's pairs. An
-// expert with c pairs has ceil(c / 128) passes of nearly equal size, so that no pass is a small
-// remainder, and a pass of n pairs runs MMAs of N = n rounded up to 16 columns: the tensor work follows
-// the ragged counts. Items are taken round-robin, passes fastest, so that the CTAs that run at one
-// time share weight tiles through L2. Every CTA derives the item list from the counts.
+// expert with c pairs has ceil(c / 128) passes whose sizes differ by less than 32 (qk_passes.cuh), so that
+// no pass is a small remainder, and a pass of n pairs runs MMAs of N = n rounded up to 16 columns: the
+// tensor work follows the ragged counts. Items are taken round-robin, passes fastest, so that the CTAs
+// that run at one time share weight tiles through L2. Every CTA derives the item list from the counts.
 //
 // A stage is 128 K elements: A as 64 tensor-memory columns, B as two 64-column slabs. The accumulator is
 // double: the next item's MMAs run while one is read.
@@ -63,6 +63,7 @@
 #include <cuda_bf16.h>
 
 #include "qk_internal.cuh"
+#include "qk_passes.cuh"
 #include "qk_tc.cuh"
 
 namespace qk {
@@ -71,7 +72,7 @@ namespace {
 constexpr int MAX_PROJ = 8;
 constexpr int MAX_E = 1024;
 constexpr int TM = 128;              // weight rows per item (MMA M)
-constexpr int TN = 128;              // most pairs of a pass (MMA N)
+constexpr int TN = PASS_MOST;        // most pairs of a pass (MMA N)
 constexpr int KC = 64;               // K elements of one slab of activations (a 128-byte swizzle row)
 constexpr int SK = 128;              // K elements per stage
 constexpr int NS = 4;                // stages: A in tensor memory, B in shared memory
@@ -162,10 +163,8 @@ struct Pairs {
     int n;
 };
 __device__ __forceinline__ Pairs pairs_of(const IdArgs &a, const Item &t) {
-    const int cnt = clamped_count(a, t.e);
-    const int per = ((cnt + t.passes - 1) / t.passes + 15) & ~15;   // <= TN: passes = ceil(cnt / TN)
-    const int start = t.pass * per;
-    return {(int64_t)__ldcg(a.offsets + t.e) + start, min(per, cnt - start)};
+    const PassRange r = pass_range(clamped_count(a, t.e), t.passes, t.pass);
+    return {(int64_t)__ldcg(a.offsets + t.e) + r.start, r.n};
 }
 // The pair at plan position pos, -1 outside the plan or the bucket (a plan from elsewhere).
 __device__ __forceinline__ int pair_at(const IdArgs &a, int64_t pos) {
@@ -371,7 +370,7 @@ __global__ void __launch_bounds__(THREADS, 1) mmq_id_kernel(const __grid_constan
         // this bucket have at most pairs / TN + E passes; counts with more are refused (fault bit 1).
         const int per = (a.E + 31) / 32, e0 = min(a.E, lane * per), e1 = min(a.E, e0 + per);
         int64_t sum = 0;
-        for (int e = e0; e < e1; e++) sum += (clamped_count(a, e) + TN - 1) / TN;
+        for (int e = e0; e < e1; e++) sum += passes_of(clamped_count(a, e));
         int64_t incl = sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -383,7 +382,7 @@ __global__ void __launch_bounds__(THREADS, 1) mmq_id_kernel(const __grid_constan
         int64_t at = incl - sum;
         for (int e = e0; e < e1; e++) {
             pre[e] = sound ? (int)at : 0;
-            at += (clamped_count(a, e) + TN - 1) / TN;
+            at += passes_of(clamped_count(a, e));
         }
         if (lane == 31) {
             pre[a.E] = sound ? (int)total : 0;
