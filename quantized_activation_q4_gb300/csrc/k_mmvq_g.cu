@@ -7,6 +7,7 @@
 // Every block sum is exact (integers); the sums over blocks and groups are binary32.
 
 #include <atomic>
+#include <cstdlib>
 
 #include "qk_internal.cuh"
 
@@ -81,7 +82,8 @@ constexpr int FEW_WARPS = 8, MANY_WARPS = 16;
 __host__ __device__ constexpr int max_chunks(int warps) { return warps == FEW_WARPS ? 34 : 72; }
 constexpr int SHORT_CHUNKS = 20;     // K up to 2560
 constexpr int PFD = 2;               // chunks ahead on their way into L2 (4, 8 or 16 were no faster)
-constexpr uint32_t SPIN_LIMIT = 1u << 16, SUSPEND_NS = 20000;   // a wait gives up after about a second
+constexpr uint32_t SUSPEND_NS = 20000;
+constexpr int WAIT_TRIES = 1 << 16;  // a wait gives up after about a second; QK_MMVQ_G_WAIT_TRIES overrides it (tests)
 
 struct GProj {
     const uint8_t *w;
@@ -94,6 +96,7 @@ struct GArgs {
     int64_t img_row_bytes;
     const int32_t *live, *counts, *offsets, *items;
     int T, k, E, per_pair, n_proj;   // T: tokens, or bucket rows of a routed call
+    int wait_tries;                  // looks of up to SUSPEND_NS at a barrier before a wait gives up
     int wk_log2, held;               // wk = 1 << wk_log2 warps share a strip; chunks of fragments
     GProj p[MAX_PROJ];
 };
@@ -339,6 +342,7 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) mmvq_g_kernel(const __
     float *red = reinterpret_cast<float *>(rec + a.held);   // [2][WARPS][RED]
     int *pre = reinterpret_cast<int *>(red + 2 * WARPS * RED);    // [E + 1], routed calls
     __shared__ __align__(8) uint64_t written;   // a CTA that sums alone: its warps' arrivals, item after item
+    __shared__ int gave_up;   // a warp's wait has run out
     __shared__ int tok_row[2][8], tok_out[4][8], warp_passes[WARPS], n_pass, share_lo[MAX_PROJ], share_hi[MAX_PROJ], rb_base[MAX_PROJ + 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint32_t rank, split;
@@ -347,7 +351,10 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) mmvq_g_kernel(const __
     const int clusters = gridDim.x / split, cluster = blockIdx.x / split;
     pdl_trigger();
     const uint32_t bar = (uint32_t)__cvta_generic_to_shared(&written);
-    if (threadIdx.x == 0) asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(WARPS) : "memory");
+    if (threadIdx.x == 0) {
+        asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(WARPS) : "memory");
+        gave_up = 0;
+    }
     if (threadIdx.x < a.n_proj) {   // this CTA's chunks of K (chunks < 2^24)
         const uint32_t n = a.p[threadIdx.x].chunks;
         share_lo[threadIdx.x] = n * rank / split;
@@ -504,24 +511,31 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) mmvq_g_kernel(const __
             if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
         }
     };
-    auto await_sums = [&](int n) {   // the n-th announcement of every warp (of the cluster)
+    // The n-th announcement of every warp (of the cluster). False when it did not come, and from then on for every
+    // warp: none sums, stores or announces any more, they walk through the items left only for the barriers around the
+    // fragments. Nothing is stored that was not summed in full.
+    auto await_sums = [&](int n) {
         if (split > 1) {
             cluster_wait();
-            return;
+            return true;
         }
-        for (uint32_t i = 0;; i++) {
+        for (int i = 0; i < a.wait_tries; i++) {
+            const int stop = *const_cast<volatile int *>(&gave_up);
             uint32_t ok;
             asm volatile(
                 "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
                 : "=r"(ok)
                 : "r"(bar), "r"(n & 1), "r"(SUSPEND_NS)
                 : "memory");
-            if (__all_sync(FULL, ok)) break;
-            if (i == SPIN_LIMIT) {
-                if (lane == 0) atomicOr(&g_mmvq_g_faults, 1u);
-                break;
-            }
+            if (__all_sync(FULL, ok && !stop)) return true;
+            if (__any_sync(FULL, stop)) break;
         }
+        if (lane == 0) {
+            atomicOr(&g_mmvq_g_faults, 1u);
+            *const_cast<volatile int *>(&gave_up) = 1;
+        }
+        __syncwarp();
+        return false;
     };
     // An item's sums over wk and over the cluster, in the order of K: the wr strips' 256 each, spread over
     // the cluster's threads; rows run fastest.
@@ -623,27 +637,26 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) mmvq_g_kernel(const __
         // Warps announce an item's partial sums and wait for the others' an item later, so that none stands
         // still for the slowest. When the wait for item it - 1 is over, item it - 2 has been summed by all,
         // and its buffer may be written.
-        if (it > it0) {
-            await_sums(it - 1 - it0);
-            sum_item(it - 1, last_pass, last_at);
-        }
+        const bool go = it == it0 || await_sums(it - 1 - it0);
+        if (it > it0 && go) sum_item(it - 1, last_pass, last_at);
         last_pass = pass;
         last_at = at;
-        float *out = red + (it & 1) * WARPS * RED + warp * RED;   // [token][32 rows]
-        const int g = lane >> 2, t2 = 2 * (lane & 3);
+        if (go) {
+            float *out = red + (it & 1) * WARPS * RED + warp * RED;   // [token][32 rows]
+            const int g = lane >> 2, t2 = 2 * (lane & 3);
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-            float v0, v1;
-            unpack2(y[i], v0, v1);
-            out[t2 * RED_STRIDE + g + 8 * i] = v0;
-            out[(t2 + 1) * RED_STRIDE + g + 8 * i] = v1;
+            for (int i = 0; i < 4; i++) {
+                float v0, v1;
+                unpack2(y[i], v0, v1);
+                out[t2 * RED_STRIDE + g + 8 * i] = v0;
+                out[(t2 + 1) * RED_STRIDE + g + 8 * i] = v1;
+            }
+            announce();
         }
-        announce();
         next_place(pass, at);
     }
     if (it1 > it0) {
-        await_sums(it1 - 1 - it0);
-        sum_item(it1 - 1, last_pass, last_at);
+        if (await_sums(it1 - 1 - it0)) sum_item(it1 - 1, last_pass, last_at);
         if (split > 1) {   // no CTA leaves while another may read its sums
             cluster_arrive();
             cluster_wait();
@@ -653,9 +666,14 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) mmvq_g_kernel(const __
 
 template <typename Proj>
 void fill(GArgs &a, const uint8_t *img, int64_t row_blocks, int n_proj, const Proj *projs) {
+    static const int wait_tries = [] {
+        const char *e = getenv("QK_MMVQ_G_WAIT_TRIES");
+        return e ? atoi(e) : WAIT_TRIES;
+    }();
     a.img = img;
     a.img_row_bytes = row_blocks * Q8_1_BYTES;
     a.n_proj = n_proj;
+    a.wait_tries = wait_tries;
     for (int j = 0; j < n_proj; j++) {
         GProj &p = a.p[j];
         p.w = static_cast<const uint8_t *>(projs[j].w);
