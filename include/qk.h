@@ -309,8 +309,12 @@ typedef struct qk_proj {
  *   Q4_0: y += d_w * (d_a * D - 8 * s_a),  D = sum nibble_i * q_i
  *   Q8_0: y += d_w * d_a * D,              D = sum w_i * q_i
  * and per group g of the group-scaled types (the blocks b inside it):
- *   y += d_g * sum_b d_a * D_b,            D_b = sum (nibble_i - z_g) * q_i
- * (the image's s is not read; every D is exact, the sums are binary32).
+ *   y += d_g * (sum_b d_a * D_b - (z_g - 8) * sum_b d_a * S_b),
+ *                                          D_b = sum (nibble_i - 8) * q_i, S_b = sum q_i
+ * (the image's s is not read; every D and S is exact, the rest is binary32). So y
+ * of the group-scaled types is within (K/G + G/32 + 32) * 2^-24 of the sum over
+ * the blocks of |d_g * d_a| * (|D_b| + |z_g - 8| * |S_b|), and weights whose
+ * nibbles equal a zero point other than 8 add up to nothing only within that.
  *   img  [T][img_row_blocks] Q8_1; every projection's K <= 32*img_row_blocks
  *   T    1..8 image rows (tokens); rows >= *d_live_rows are not written
  *   projs host array of n_proj (1..8) descriptors; outputs must not share a
