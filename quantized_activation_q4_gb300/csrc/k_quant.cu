@@ -14,6 +14,8 @@
 // binary32 with IEEE division (no fast-math in this file), the codes use
 // round-to-nearest-even and the halves use __float2half_rn.
 
+#include <cfloat>
+
 #include "qk_internal.cuh"
 
 namespace qk {
@@ -500,7 +502,7 @@ __global__ void __launch_bounds__(256, BF16 ? 6 : 4) glu_q8_0_kernel(
             u[h].load(a, layout == QK_GLU_PACKED ? first + N : first, wide);
     }
     const int n_live = live_rows(live, T);
-    const float alpha_log2e = alpha * LOG2E;
+    const float alpha_log2e = fminf(fmaxf(alpha * LOG2E, -FLT_MAX), FLT_MAX);   // finite: a gate of zero stays zero
 #pragma unroll
     for (int h = 0; h < 2; h++) {
         F2 v[4];
