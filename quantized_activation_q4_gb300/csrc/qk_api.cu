@@ -648,7 +648,10 @@ qk_status qk_mmq(const int8_t *qs, const uint16_t *d, int64_t row_blocks, int64_
 size_t qk_mmq_id_workspace_bytes(int64_t rows, int32_t k, int32_t n_proj, const qk_proj_id16 *projs) {
     if (rows < 1 || rows > (1 << 24) || k < 1 || k > 64 || n_proj < 1 || n_proj > 8 || !projs) return 0;
     int64_t kmax = 0;
-    for (int j = 0; j < n_proj; j++) kmax = projs[j].K > kmax ? projs[j].K : kmax;
+    for (int j = 0; j < n_proj; j++) {
+        if (projs[j].K < QB || projs[j].K > MOST_NK) return 0;
+        kmax = projs[j].K > kmax ? projs[j].K : kmax;
+    }
     return (size_t)mmq_id_workspace_bytes(rows * k, kmax);
 }
 
