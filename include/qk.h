@@ -524,8 +524,8 @@ QK_API qk_status qk_glu_q8_0(qk_glu_kind kind, qk_glu_layout layout, qk_elem ele
  *   qs [T][row_blocks*32] int8 and d [T][row_blocks] half: qk_quantize_q8_0
  *   C[t][n] = sum_b d_w[n][b] * d_a[t][b] * sum_{i in b} w_i * q_i
  *   (Q4_0: w_i = nibble - 8) written to projs[j].y ([T][y_stride] F32);
- *   outputs must not share a byte, nor one with any weights (disjoint column windows of one buffer
- *   with one y_stride are allowed, as for qk_mmvq)
+ *   outputs must not share a byte, nor one with any weights (disjoint column
+ *   windows of one buffer with one y_stride are allowed, as for qk_mmvq)
  * Runs on the tensor cores with binary16 operands (nibble - 8) * d_w and
  * q * d_a, each rounded once, accumulated in binary32: within about 2^-11
  * relative per product of the exact block form (NMSE ~1e-7).
@@ -616,9 +616,18 @@ typedef struct qk_proj_id16 {
  * operands' rounding stays well below); 16-bit rows halve the traffic between
  * the routed products. Activations and weights beyond binary16's range (65504)
  * become infinities, as for qk_mmq.
+ * Which call for which bucket (QK_W_Q4_G128, us of qk_mmvq_id / qk_mmq_id): it goes
+ * by the pairs per expert, rows * k / E, and by K. Fewer than 2 are faster by
+ * qk_mmvq_id, 16 and more by this call; in between short K turns first:
+ *   768 -> 2560, 128 experts (slots)   1: 27.8 / 27.7,  2: 36.0 / 34.6,  4: 47 / 40
+ *   2560 -> 2 x 768, 128 experts       2: 51 / 55,      4: 69 / 68,      8: 98 / 73
+ *   4096 -> 2 x 14336, 8 experts       4: 99 / 136,     8: 140 / 140,   16: 191 / 141
+ *   7168 -> 2 x 2048, 256 experts      4: 622 / 773,    8: 948 / 890
+ *   14336 -> 4096, 8 experts (slots)   8: 86 / 106,    16: 115 / 107,   32: 204 / 108
  *   projs  host array of n_proj (1..8) descriptors with one n_experts; outputs
- *          must not share a byte, nor one with any weights (disjoint column windows of one buffer with one
- *          y_stride are allowed: gate and up as the packed rows of a GLU)
+ *          must not share a byte, nor one with any weights (disjoint column windows
+ *          of one buffer with one y_stride are allowed: gate and up as the packed
+ *          rows of a GLU)
  *   ws     workspace of qk_mmq_id_workspace_bytes bytes, 128-byte aligned:
  *          scratch, no state kept. Calls that may run concurrently need separate
  *          ones.
