@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(256) dequant_b_kernel(const int8_t *qs, const 
     pdl_wait();
     const int t = blockIdx.x, w = threadIdx.x & 3, b = blockIdx.y * 64 + (threadIdx.x >> 2);
     if (b >= kb) return;
-    dequant_word(qs, d, (int64_t)t * row_blocks + b, w, B + ((int64_t)t * kb + b) * QB);
+    dequant_word(image_word(qs, d, (int64_t)t * row_blocks + b, w), w, B + ((int64_t)t * kb + b) * QB);
 }
 
 // ------------------------------------------------------------------ the GEMM

@@ -316,8 +316,15 @@ __global__ void __launch_bounds__(256) dequant_pairs_kernel(const int8_t *qs, co
     if (p < 0 || p >= pairs) return;
     const int64_t first = (per_pair ? p : p / k) * row_blocks;
     __half *dst = B + pos * pitch;
-#pragma unroll 4
-    for (int b = b0; b < kb; b += 8) dequant_word(qs, d, first + b, w, dst + (int64_t)b * QB);
+    for (int b = b0; b < kb; b += 32) {   // four loads in flight
+        ImageWord x[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            if (b + 8 * i < kb) x[i] = image_word(qs, d, first + b + 8 * i, w);
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            if (b + 8 * i < kb) dequant_word(x[i], w, dst + (int64_t)(b + 8 * i) * QB);
+    }
 }
 
 template <int WT>

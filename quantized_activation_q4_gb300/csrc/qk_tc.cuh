@@ -118,17 +118,22 @@ __device__ __forceinline__ uint2 b_word(uint32_t v, __half2 d2) {
     return make_uint2(b_pair(u, 0x4240u, d2), b_pair(u, 0x4341u, d2));
 }
 
-// Word w of an image block (codes 4w .. 4w+3 and 16+4w .. 16+4w+3) -> f16 q * d_a at dst's columns 2w,
-// 2w+1 (halves 4w .. 4w+3) and 8+2w, 9+2w (halves 16+4w ..), the K order of the A stages.
-__device__ __forceinline__ void dequant_word(const int8_t *qs, const uint16_t *d, int64_t block,
-                                             int w, __half *dst) {
-    const int8_t *src = qs + block * QB;
-    const uint32_t lo = ld_prev(reinterpret_cast<const uint32_t *>(src + 4 * w));
-    const uint32_t hi = ld_prev(reinterpret_cast<const uint32_t *>(src + 16 + 4 * w));
-    const __half dah = __ushort_as_half(ld_prev(d + block));
+// Word w of an image block (codes 4w .. 4w+3 and 16+4w .. 16+4w+3) and the block's scale
+struct ImageWord {
+    uint32_t lo, hi;
+    uint16_t d;
+};
+__device__ __forceinline__ ImageWord image_word(const int8_t *qs, const uint16_t *d, int64_t block, int w) {
+    const uint32_t *src = reinterpret_cast<const uint32_t *>(qs + block * QB);
+    return {ld_prev(src + w), ld_prev(src + 4 + w), ld_prev(d + block)};
+}
+// -> f16 q * d_a at dst's columns 2w, 2w+1 (halves 4w .. 4w+3) and 8+2w, 9+2w (halves 16+4w ..), the K order of the
+// A stages
+__device__ __forceinline__ void dequant_word(const ImageWord &x, int w, __half *dst) {
+    const __half dah = __ushort_as_half(x.d);
     const __half2 d2 = __halves2half2(dah, dah);
-    *reinterpret_cast<uint2 *>(dst + 4 * w) = b_word(lo, d2);
-    *reinterpret_cast<uint2 *>(dst + 16 + 4 * w) = b_word(hi, d2);
+    *reinterpret_cast<uint2 *>(dst + 4 * w) = b_word(x.lo, d2);
+    *reinterpret_cast<uint2 *>(dst + 16 + 4 * w) = b_word(x.hi, d2);
 }
 
 inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
