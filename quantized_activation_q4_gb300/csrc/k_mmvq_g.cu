@@ -72,8 +72,8 @@ __global__ void __launch_bounds__(256) pack_g_kernel(const uint8_t *__restrict__
 // shares it and sums in distributed shared memory; the release of a cluster's barrier waits for the weight
 // loads in flight, so that an item of a cluster costs about 4 us and clusters pay only for few items
 // (launch_matvec has the figures).
-// 8192 -> 65536, four tokens: 55 us, 5.2 TB/s. Gate/up of 13 live rows, top 8 of 128 experts, 2560 -> 2 x 768: 42 us,
-// 3.8 TB/s. In both the products stream at 6 TB/s; the start and the fragments of K take 12 and 15 thousand
+// 8192 -> 65536, four tokens: 55 us, 5.2 TB/s. Gate/up of 13 live rows, top 8 of 128 experts, 2560 -> 2 x 768: 38 us,
+// 4.2 TB/s. In both the products stream at 6 TB/s; the start and the fragments of K take 12 and 15 thousand
 // cycles before them, an item's sums 1.6 thousand after.
 constexpr int RED_STRIDE = 36;       // floats between two tokens' 32 rows of partial sums: no bank conflicts
 constexpr int RED = 8 * RED_STRIDE;  // floats of one warp's partial sums
