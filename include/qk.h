@@ -655,6 +655,181 @@ QK_API qk_status qk_mmq_id_slots(const int8_t *qs, const uint16_t *d, int64_t ro
                                  const int32_t *offsets, const int32_t *items, void *ws, size_t ws_bytes,
                                  qk_stream stream);
 
+/* ------------------------------------------- the 4-bit key/value cache */
+
+/*
+ * Between q/k/v and the output projection: the keys and values of a layer in a
+ * paged cache of 4-bit blocks, and the attention that reads it.
+ *
+ * The cache is n_pages pages of page_tokens tokens, qk_kv_page_bytes bytes each:
+ *   [n_pages][n_kv_heads][page_tokens / 16] groups of 16 tokens of one head
+ * A value is (code - 8) * d, code 0..15, d a half per 32 columns of a token (the
+ * value form of QK_W_Q4_0). A group is 18 * D bytes (D = head_dim, nb = D / 32,
+ * W = min(4, nb)), in the order in which tensor-core fragments take it; token
+ * i = 0..15 of the group, column x, block b = x / 32:
+ *   k codes  byte ((b / W * 16 + i) * 4 + x % 16 / 4) * 4 W + b % W * 4 + x % 4,
+ *            low nibble for x % 32 < 16, else high
+ *   k scales half i * nb + b at byte 8 D
+ *   v codes  byte ((x / 64 * 8 + x % 8) * 4 + i % 8 / 2) * 16 + x / 16 % 4 * 4 +
+ *            2 * (i % 2) + i / 8 at byte 9 D, low nibble for x % 16 < 8, else high
+ *   v scales half (i % 8 / 2 * nb + b) * 4 + i % 2 + i / 8 * 2 at byte 17 D
+ * A token's place is a slot: page * page_tokens + its place in the page. A token
+ * never shares a byte with another, so tokens can be written in any order. Pages
+ * need no initialisation: what no token was written to is never used.
+ */
+typedef struct qk_kv_cache {
+    void *pages;         /* n_pages * qk_kv_page_bytes(...), 16-byte aligned */
+    int64_t n_pages;     /* n_pages * page_tokens <= 2^31 - 1 */
+    int32_t page_tokens; /* a multiple of 16, 16..4096 */
+    int32_t n_kv_heads;  /* 1..256 */
+    int32_t head_dim;    /* 64, 128 or 256 */
+    int32_t reserved;    /* 0 */
+} qk_kv_cache;
+
+/* Bytes of one page (0 for arguments out of range). */
+QK_API size_t qk_kv_page_bytes(int32_t page_tokens, int32_t n_kv_heads, int32_t head_dim);
+
+typedef enum qk_rope_kind {
+    QK_ROPE_HALVES = 0,  /* pair i is columns i and i + dims / 2 */
+    QK_ROPE_ADJACENT = 1 /* pair i is columns 2 i and 2 i + 1    */
+} qk_rope_kind;
+
+/*
+ * Rotation by positions with one or more axes (a sequence; time, height and
+ * width). Pair i of token t turns by the angle
+ *   sum over axes a of positions[a][t] * freqs[a][i]
+ * so a pair that belongs to one axis has frequency 0 on the others. The angle is
+ * reduced exactly enough that far positions (any int32) cost no accuracy: its sine and
+ * cosine are within 2^-22 of those of the sum of exact products.
+ */
+typedef struct qk_rope {
+    int32_t kind;             /* qk_rope_kind */
+    int32_t dims;             /* rotated columns 0..dims-1 of a head: a multiple of 8, 8..head_dim; the others stay */
+    int32_t n_axes;           /* 1..4 */
+    int32_t reserved;         /* 0 */
+    const int32_t *positions; /* [n_axes][T] */
+    const float *freqs;       /* [n_axes][dims / 2], radians a position */
+} qk_rope;
+
+/*
+ * qk_kv_append -- the q, k and v rows of T tokens, q and k rotated on the way: q
+ * to rows for the attention, k and v to the tokens' slots of the cache.
+ *   elem   type of the q, k and v rows; strides in elements. They may be column
+ *          windows of one buffer (the fused output of a q/k/v projection)
+ *   q      [T][q_stride], n_heads heads of head_dim; NULL with n_heads = 0 when
+ *          only k and v are wanted
+ *   k, v   [T][k_stride], [T][v_stride], n_kv_heads heads of head_dim
+ *   slots  [T] int32; a token whose slot is negative or past the cache is not
+ *          stored (its q row is written). Slots of one call are distinct: of
+ *          tokens that share one, either's bytes may end up in it, mixed.
+ *   rope   NULL: nothing is rotated
+ *   q_out  [T][q_out_stride] of type q_elem: the rotated q, binary32 arithmetic,
+ *          rounded once
+ * Per block of 32 columns of a (rotated) k or v head, in binary32: e = the value
+ * of the largest magnitude (of equal ones the first), d = e / -8 clamped to
+ * +-65504, code = clamp(rint(x / d) + 8, 0, 15), ties to even; all codes are 8
+ * where e = 0. NaN is stored as 0. d is stored rounded to half.
+ * Rows >= *d_live_rows are not read, stored or written. T = 0 launches nothing.
+ * Errors: QK_ERR_ARG, QK_ERR_SHAPE (strides too small), QK_ERR_UNSUPPORTED
+ * (head_dim), QK_ERR_ALIAS.
+ */
+QK_API qk_status qk_kv_append(const qk_kv_cache *cache, qk_elem elem, const void *q, int64_t q_stride, int32_t n_heads,
+                              const void *k, int64_t k_stride, const void *v, int64_t v_stride, int64_t T,
+                              const int32_t *slots, const qk_rope *rope, qk_elem q_elem, void *q_out,
+                              int64_t q_out_stride, const int32_t *d_live_rows, qk_stream stream);
+
+/*
+ * qk_kv_read -- the values of n cached tokens as rows: out[r] = the k heads of the
+ * token in slots[r], then its v heads ([n][out_stride], 2 * n_kv_heads * head_dim
+ * columns of type elem; (code - 8) * d is exact in binary32 and rounded once to
+ * bfloat16). Rows whose slot is negative or past the cache, and rows >=
+ * *d_live_rows, are not written. n = 0 launches nothing. Errors: as qk_kv_append.
+ */
+QK_API qk_status qk_kv_read(const qk_kv_cache *cache, const int32_t *slots, int64_t n, qk_elem elem, void *out,
+                            int64_t out_stride, const int32_t *d_live_rows, qk_stream stream);
+
+/*
+ * What both attention calls read and write. Query heads h * G .. h * G + G - 1
+ * (G = n_heads / n_kv_heads) read key/value head h. Sequence b has its first
+ * kv_lens[b] keys in the pages page_table[b][0], [1], ... (page_tokens each); its
+ * query rows are its newest tokens, stored before the call: of n rows, row i sees
+ * the keys below kv_lens[b] - n + i + 1, and with a window only the last `window`
+ * of them. For every row and head, over the visible keys:
+ *   out = sum_j exp(s_j) v_j / (sum_j exp(s_j) + exp(sink)),  s_j = scale * q . k_j
+ * A row that sees no key is 0. Lengths are clamped to what the page table (and
+ * max_kv) can hold; keys on a page outside [0, n_pages) are not visible. What the
+ * cache holds behind a sequence's last key may be anything, NaN and infinite
+ * scales included.
+ */
+typedef struct qk_attn {
+    const void *q;             /* [rows][q_stride], n_heads heads of head_dim (qk_kv_append's q_out) */
+    int32_t q_elem;            /* qk_elem */
+    int32_t n_heads;           /* a multiple of n_kv_heads, at most 1024 */
+    int64_t q_stride;          /* in elements */
+    const int32_t *page_table; /* [B][table_stride] */
+    int64_t table_stride;      /* pages a sequence can have */
+    const int32_t *kv_lens;    /* [B] */
+    float scale;               /* finite, > 0 */
+    int32_t window;            /* 0: none */
+    const float *sinks;        /* [n_heads] extra logits (not scaled), or NULL */
+    void *out;                 /* [rows][out_stride] of type out_elem, or NULL when only the image is wanted */
+    int32_t out_elem;          /* qk_elem */
+    int32_t reserved;          /* 0 */
+    int64_t out_stride;        /* in elements */
+} qk_attn;
+
+/*
+ * qk_attn_decode -- attention of T = 1..8 new tokens of each of B sequences (a
+ * decode step; drafted tokens checked at once), row b * T + i for token i of
+ * sequence b, with the Q8_1 image of the output for the output projection
+ * (qk_mmvq).
+ *   img  [B * T][img_row_blocks] Q8_1 blocks of the output in binary32 (as
+ *        qk_quantize_q8_1 of binary32 `out` rows makes them; blocks past
+ *        n_heads * head_dim / 32 are zero), or NULL. One of out and img at least.
+ *   d_live_rows: the number of live SEQUENCES of the bucket B
+ *   ws   qk_attn_decode_workspace_bytes bytes, 16-byte aligned; scratch, no state
+ *        kept, no initialisation. Calls that may run concurrently need separate
+ *        ones.
+ * Products run on the tensor cores with binary16 operands (queries scaled by a
+ * power of two per row and rounded once; weights exp(s - max) * d rounded twice)
+ * and binary32 sums: within about 2^-10 of the sum of the magnitudes.
+ * The keys of all sequences are shared out over the device by their lengths, so an
+ * output's last bits depend on the lengths of the whole call (not on the run).
+ * Errors: QK_ERR_ARG, QK_ERR_SHAPE, QK_ERR_UNSUPPORTED (T > 8, head_dim, n_heads),
+ * QK_ERR_ALIAS, QK_ERR_WORKSPACE. B = 0 launches nothing.
+ */
+QK_API size_t qk_attn_decode_workspace_bytes(const qk_kv_cache *cache, int32_t n_heads, int64_t B, int32_t T);
+QK_API qk_status qk_attn_decode(const qk_kv_cache *cache, const qk_attn *attn, int64_t B, int32_t T, void *img,
+                                int64_t img_row_blocks, const int32_t *d_live_rows, void *ws, size_t ws_bytes,
+                                qk_stream stream);
+
+/*
+ * qk_attn_prefill -- the same attention for prompts and chunks of prompts, with
+ * the Q8_0 planes of the output (qk_mmq).
+ *   rows       bucket rows of q and of the outputs
+ *   q_offsets  [B + 1] int32 on the device, ascending: sequence b has the rows
+ *              q_offsets[b] .. q_offsets[b+1] - 1 (clamped to [0, rows]); other
+ *              rows are not written
+ *   max_kv     no sequence has more keys (longer lengths are clamped to it);
+ *              1 .. table_stride * page_tokens. Sizes the workspace.
+ *   qs, d      [rows][row_blocks * 32] codes (16-byte aligned) and [rows][row_blocks]
+ *              half scales, as qk_quantize_q8_0 of binary32 `out` rows makes them
+ *              (blocks past n_heads * head_dim / 32 are zero), or both NULL
+ *   d_live_rows: the number of live SEQUENCES of B
+ *   ws         qk_attn_prefill_workspace_bytes bytes, 128-byte aligned: the keys
+ *              and values of the call in binary16. Scratch, no state kept.
+ * Runs on the tensor cores (tcgen05) with binary16 operands: keys and values
+ * (code - 8) * d, queries scaled by a power of two per row, weights exp(s - max),
+ * each rounded once, with binary32 sums. Keys and values beyond binary16's range
+ * (65504) become infinities. Errors: as qk_attn_decode, and B > 65535 or rows >
+ * 2^24 (QK_ERR_UNSUPPORTED). rows = 0 or B = 0 launches nothing.
+ */
+QK_API size_t qk_attn_prefill_workspace_bytes(const qk_kv_cache *cache, int64_t B, int64_t max_kv);
+QK_API qk_status qk_attn_prefill(const qk_kv_cache *cache, const qk_attn *attn, int64_t B, int64_t rows,
+                                 const int32_t *q_offsets, int64_t max_kv, int8_t *qs, uint16_t *d,
+                                 int64_t row_blocks, const int32_t *d_live_rows, void *ws, size_t ws_bytes,
+                                 qk_stream stream);
+
 #ifdef __cplusplus
 }
 #endif

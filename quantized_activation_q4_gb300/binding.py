@@ -26,6 +26,7 @@ GLU = {"swiglu": 0, "geglu_tanh": 1, "reglu": 2, "geglu_erf": 3, "geglu_quick": 
 LAYOUT = {"separate": 0, "packed": 1, "packed_swapped": 2}
 WTYPE = {"q4_0": 0, "q8_0": 1, "q4_g64": 2, "q4_g128": 3}
 ELEM = {"f32": 0, "bf16": 1}
+ROPE = {"halves": 0, "adjacent": 1}
 Q8_1_BLOCK_BYTES = 36
 
 
@@ -59,6 +60,24 @@ class qk_image_memo(C.Structure):
 
 
 MEMO_Q8_0, MEMO_Q8_1 = 1, 2
+
+
+class qk_kv_cache(C.Structure):
+    _fields_ = [("pages", C.c_void_p), ("n_pages", C.c_int64), ("page_tokens", C.c_int32), ("n_kv_heads", C.c_int32),
+                ("head_dim", C.c_int32), ("reserved", C.c_int32)]
+
+
+class qk_rope(C.Structure):
+    _fields_ = [("kind", C.c_int32), ("dims", C.c_int32), ("n_axes", C.c_int32), ("reserved", C.c_int32),
+                ("positions", C.c_void_p), ("freqs", C.c_void_p)]
+
+
+class qk_attn(C.Structure):
+    _fields_ = [("q", C.c_void_p), ("q_elem", C.c_int32), ("n_heads", C.c_int32), ("q_stride", C.c_int64),
+                ("page_table", C.c_void_p), ("table_stride", C.c_int64), ("kv_lens", C.c_void_p), ("scale", C.c_float),
+                ("window", C.c_int32), ("sinks", C.c_void_p), ("out", C.c_void_p), ("out_elem", C.c_int32),
+                ("reserved", C.c_int32), ("out_stride", C.c_int64)]
+
 
 _lock = threading.Lock()
 _lib = None
@@ -101,6 +120,14 @@ _SIGS = {
     "qk_mmq_id_workspace_bytes": ([I64, I32, I32, C.POINTER(qk_proj_id16)], SZ),
     "qk_mmq_id": ([P, P, I64, I64, I32, I32, C.POINTER(qk_proj_id16), P, P, P, P, SZ, P], C.c_int),
     "qk_mmq_id_slots": ([P, P, I64, I64, I32, I32, C.POINTER(qk_proj_id16), P, P, P, P, SZ, P], C.c_int),
+    "qk_kv_page_bytes": ([I32, I32, I32], SZ),
+    "qk_kv_append": ([C.POINTER(qk_kv_cache), C.c_int, P, I64, I32, P, I64, P, I64, I64, P, C.POINTER(qk_rope), C.c_int,
+                      P, I64, P, P], C.c_int),
+    "qk_kv_read": ([C.POINTER(qk_kv_cache), P, I64, C.c_int, P, I64, P, P], C.c_int),
+    "qk_attn_decode_workspace_bytes": ([C.POINTER(qk_kv_cache), I32, I64, I32], SZ),
+    "qk_attn_decode": ([C.POINTER(qk_kv_cache), C.POINTER(qk_attn), I64, I32, P, I64, P, P, SZ, P], C.c_int),
+    "qk_attn_prefill_workspace_bytes": ([C.POINTER(qk_kv_cache), I64, I64], SZ),
+    "qk_attn_prefill": ([C.POINTER(qk_kv_cache), C.POINTER(qk_attn), I64, I64, P, I64, P, P, I64, P, P, SZ, P], C.c_int),
     "qk_mmq": ([P, P, I64, I64, I32, C.POINTER(qk_proj), P, C.c_size_t, P], C.c_int),
 }
 
@@ -382,3 +409,61 @@ def qk_moe_plan(ids, rows, k, E, counts, offsets, items, d_live_rows=None, strea
 def qk_route_plan(logits, rows, E, k, ids, wts, counts, offsets, items, d_live_rows=None, stream=None):
     _check("qk_route_plan", load().qk_route_plan(_ptr(logits), rows, E, k, _ptr(ids), _ptr(wts), _ptr(counts),
                                                  _ptr(offsets), _ptr(items), _ptr(d_live_rows), _stream(stream)))
+
+
+# ------------------------------------------------------------------ the 4-bit key/value cache
+def qk_kv_page_bytes(page_tokens, n_kv_heads, head_dim) -> int:
+    return int(load().qk_kv_page_bytes(page_tokens, n_kv_heads, head_dim))
+
+
+def make_kv_cache(pages, n_pages, page_tokens, n_kv_heads, head_dim) -> qk_kv_cache:
+    return qk_kv_cache(_ptr(pages), n_pages, page_tokens, n_kv_heads, head_dim, 0)
+
+
+def make_rope(kind, dims, n_axes, positions, freqs) -> qk_rope:
+    kind = ROPE[kind] if isinstance(kind, str) else int(kind)
+    return qk_rope(kind, dims, n_axes, 0, _ptr(positions), _ptr(freqs))
+
+
+def make_attn(q, q_elem, q_stride, n_heads, page_table, table_stride, kv_lens, scale, window=0, sinks=None, out=None,
+              out_elem="f32", out_stride=0) -> qk_attn:
+    q_elem = ELEM[q_elem] if isinstance(q_elem, str) else int(q_elem)
+    out_elem = ELEM[out_elem] if isinstance(out_elem, str) else int(out_elem)
+    return qk_attn(_ptr(q), q_elem, n_heads, q_stride, _ptr(page_table), table_stride, _ptr(kv_lens), float(scale),
+                   window, _ptr(sinks), _ptr(out), out_elem, 0, out_stride)
+
+
+def qk_kv_append(cache, elem, q, q_stride, n_heads, k, k_stride, v, v_stride, T, slots, rope, q_elem, q_out,
+                 q_out_stride, d_live_rows=None, stream=None):
+    elem = ELEM[elem] if isinstance(elem, str) else int(elem)
+    q_elem = ELEM[q_elem] if isinstance(q_elem, str) else int(q_elem)
+    _check("qk_kv_append", load().qk_kv_append(C.byref(cache), elem, _ptr(q), q_stride, n_heads, _ptr(k), k_stride,
+                                               _ptr(v), v_stride, T, _ptr(slots),
+                                               None if rope is None else C.byref(rope), q_elem, _ptr(q_out),
+                                               q_out_stride, _ptr(d_live_rows), _stream(stream)))
+
+
+def qk_kv_read(cache, slots, n, elem, out, out_stride, d_live_rows=None, stream=None):
+    elem = ELEM[elem] if isinstance(elem, str) else int(elem)
+    _check("qk_kv_read", load().qk_kv_read(C.byref(cache), _ptr(slots), n, elem, _ptr(out), out_stride,
+                                           _ptr(d_live_rows), _stream(stream)))
+
+
+def qk_attn_decode_workspace_bytes(cache, n_heads, B, T) -> int:
+    return int(load().qk_attn_decode_workspace_bytes(C.byref(cache), n_heads, B, T))
+
+
+def qk_attn_decode(cache, attn, B, T, img, img_row_blocks, ws, ws_bytes, d_live_rows=None, stream=None):
+    _check("qk_attn_decode", load().qk_attn_decode(C.byref(cache), C.byref(attn), B, T, _ptr(img), img_row_blocks,
+                                                   _ptr(d_live_rows), _ptr(ws), ws_bytes, _stream(stream)))
+
+
+def qk_attn_prefill_workspace_bytes(cache, B, max_kv) -> int:
+    return int(load().qk_attn_prefill_workspace_bytes(C.byref(cache), B, max_kv))
+
+
+def qk_attn_prefill(cache, attn, B, rows, q_offsets, max_kv, qs, d, row_blocks, ws, ws_bytes, d_live_rows=None,
+                    stream=None):
+    _check("qk_attn_prefill", load().qk_attn_prefill(C.byref(cache), C.byref(attn), B, rows, _ptr(q_offsets), max_kv,
+                                                     _ptr(qs), _ptr(d), row_blocks, _ptr(d_live_rows), _ptr(ws),
+                                                     ws_bytes, _stream(stream)))

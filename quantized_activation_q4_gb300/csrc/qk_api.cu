@@ -6,6 +6,7 @@
 // Aliasing outputs are refused (llama.cpp PR #117 "activation image
 // emission", Coverage: unsafe input/output aliases keep the original path).
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdarg>
@@ -13,6 +14,7 @@
 #include <cstring>
 
 #include "qk_internal.cuh"
+#include "qk_kv.cuh"
 
 namespace qk {
 
@@ -718,6 +720,214 @@ qk_status qk_mmq_id_slots(const int8_t *qs, const uint16_t *d, int64_t row_block
                           int32_t n_proj, const qk_proj_id16 *projs, const int32_t *counts, const int32_t *offsets,
                           const int32_t *items, void *ws, size_t ws_bytes, qk_stream stream) {
     return mmq_id_common(qs, d, row_blocks, rows, k, n_proj, projs, counts, offsets, items, ws, ws_bytes, true, stream);
+}
+
+// ------------------------------------------------------------------ the 4-bit key/value cache
+static bool kv_shape(int32_t page_tokens, int32_t n_kv_heads, int32_t head_dim) {
+    return page_tokens >= GROUP && page_tokens <= 4096 && page_tokens % GROUP == 0 && n_kv_heads >= 1 &&
+           n_kv_heads <= 256 && (head_dim == 64 || head_dim == 128 || head_dim == 256);
+}
+
+size_t qk_kv_page_bytes(int32_t page_tokens, int32_t n_kv_heads, int32_t head_dim) {
+    if (!kv_shape(page_tokens, n_kv_heads, head_dim)) return 0;
+    return (size_t)page_tokens / GROUP * n_kv_heads * group_bytes(head_dim);
+}
+
+static qk_status check_cache(const qk_kv_cache *c) {
+    REQUIRE(c, QK_ERR_ARG, "cache is null");
+    REQUIRE(c->head_dim == 64 || c->head_dim == 128 || c->head_dim == 256, QK_ERR_UNSUPPORTED,
+            "head_dim=%d is not 64, 128 or 256", (int)c->head_dim);
+    REQUIRE(kv_shape(c->page_tokens, c->n_kv_heads, c->head_dim), QK_ERR_ARG,
+            "page_tokens=%d (a multiple of 16, 16..4096) or n_kv_heads=%d (1..256) out of range", (int)c->page_tokens,
+            (int)c->n_kv_heads);
+    REQUIRE(c->n_pages >= 1 && c->n_pages <= INT32_MAX / c->page_tokens, QK_ERR_ARG,
+            "n_pages=%lld out of range (n_pages * page_tokens <= 2^31 - 1)", (long long)c->n_pages);
+    REQUIRE(c->pages && aligned(c->pages, 16), QK_ERR_ARG, "pages is null or not 16-byte aligned");
+    return QK_OK;
+}
+static Span cache_span(const qk_kv_cache *c) {
+    return span(c->pages, (size_t)c->n_pages * qk_kv_page_bytes(c->page_tokens, c->n_kv_heads, c->head_dim));
+}
+static bool elem_ok(int32_t e) { return e == QK_ELEM_F32 || e == QK_ELEM_BF16; }
+static unsigned elem_bytes(int32_t e) { return e == QK_ELEM_F32 ? 4 : 2; }
+constexpr int64_t MOST_STRIDE = INT64_C(1) << 36;   // 2^24 rows * stride * 4 bytes stay inside 64 bits
+
+qk_status qk_kv_append(const qk_kv_cache *cache, qk_elem elem, const void *q, int64_t q_stride, int32_t n_heads,
+                       const void *k, int64_t k_stride, const void *v, int64_t v_stride, int64_t T, const int32_t *slots,
+                       const qk_rope *rope, qk_elem q_elem, void *q_out, int64_t q_out_stride,
+                       const int32_t *d_live_rows, qk_stream stream) {
+    const qk_status st = check_cache(cache);
+    if (st != QK_OK) return st;
+    const int64_t D = cache->head_dim, kv = D * cache->n_kv_heads, qw = D * n_heads;
+    REQUIRE(elem_ok(elem) && elem_ok(q_elem), QK_ERR_ARG, "bad element type");
+    REQUIRE(T >= 0 && T <= (1 << 24), QK_ERR_ARG, "T=%lld out of range (0..2^24)", (long long)T);
+    REQUIRE(n_heads >= 0 && n_heads <= 1024, QK_ERR_ARG, "n_heads=%d out of range", (int)n_heads);
+    REQUIRE((k && v && slots) || T == 0, QK_ERR_ARG, "k, v or slots is null");
+    REQUIRE(n_heads == 0 || T == 0 || (q && q_out), QK_ERR_ARG, "q or q_out is null");
+    const unsigned e = elem_bytes(elem), qe = elem_bytes(q_elem);
+    REQUIRE(aligned(k, e) && aligned(v, e) && aligned(slots, 4) && (n_heads == 0 || (aligned(q, e) && aligned(q_out, qe))),
+            QK_ERR_ARG, "misaligned pointer");
+    REQUIRE(k_stride >= kv && v_stride >= kv && (n_heads == 0 || (q_stride >= qw && q_out_stride >= qw)), QK_ERR_SHAPE,
+            "a stride is smaller than its heads");
+    REQUIRE(k_stride <= MOST_STRIDE && v_stride <= MOST_STRIDE &&
+                (n_heads == 0 || (q_stride <= MOST_STRIDE && q_out_stride <= MOST_STRIDE)),
+            QK_ERR_ARG, "a stride is out of range");
+    KvRope r = {};
+    if (rope) {
+        REQUIRE(rope->kind == QK_ROPE_HALVES || rope->kind == QK_ROPE_ADJACENT, QK_ERR_ARG, "bad rope kind %d",
+                (int)rope->kind);
+        REQUIRE(rope->dims >= 8 && rope->dims <= D && rope->dims % 8 == 0, QK_ERR_SHAPE,
+                "rope dims=%d is not a multiple of 8 in 8..head_dim", (int)rope->dims);
+        REQUIRE(rope->n_axes >= 1 && rope->n_axes <= 4, QK_ERR_ARG, "n_axes=%d not in 1..4", (int)rope->n_axes);
+        REQUIRE((rope->positions && rope->freqs) || T == 0, QK_ERR_ARG, "positions or freqs is null");
+        REQUIRE(aligned(rope->positions, 4) && aligned(rope->freqs, 4), QK_ERR_ARG, "positions or freqs misaligned");
+        r = {rope->kind, rope->dims, rope->n_axes, rope->positions, rope->freqs};
+    }
+    if (T == 0) return QK_OK;
+    const Span outs[2] = {cache_span(cache), span(n_heads ? q_out : nullptr, n_heads ? rows_span(T, q_out_stride * qe, qw * qe) : 0)};
+    const Span ins[7] = {span(n_heads ? q : nullptr, n_heads ? rows_span(T, q_stride * e, qw * e) : 0),
+                         span(k, rows_span(T, k_stride * e, kv * e)),
+                         span(v, rows_span(T, v_stride * e, kv * e)),
+                         span(slots, (size_t)T * 4),
+                         span(r.positions, (size_t)r.n_axes * T * 4),
+                         span(r.freqs, (size_t)r.n_axes * (r.dims / 2) * 4),
+                         span(d_live_rows, d_live_rows ? 4 : 0)};
+    REQUIRE(!overlap(outs[0], outs[1]), QK_ERR_ALIAS, "q_out overlaps the cache");
+    for (const Span &o : outs)
+        for (const Span &i : ins) REQUIRE(!overlap(o, i), QK_ERR_ALIAS, "the cache or q_out overlaps an input");
+    return launch_kv_append(kv_cache(cache), elem, q, q_stride, n_heads, k, k_stride, v, v_stride, (int)T, slots, r, q_elem,
+                            q_out, q_out_stride, d_live_rows, (cudaStream_t)stream);
+}
+
+qk_status qk_kv_read(const qk_kv_cache *cache, const int32_t *slots, int64_t n, qk_elem elem, void *out,
+                     int64_t out_stride, const int32_t *d_live_rows, qk_stream stream) {
+    const qk_status st = check_cache(cache);
+    if (st != QK_OK) return st;
+    const int64_t width = 2LL * cache->n_kv_heads * cache->head_dim;
+    REQUIRE(elem_ok(elem), QK_ERR_ARG, "bad element type %d", (int)elem);
+    REQUIRE(n >= 0 && n <= (1 << 24), QK_ERR_ARG, "n=%lld out of range (0..2^24)", (long long)n);
+    REQUIRE((slots && out) || n == 0, QK_ERR_ARG, "slots or out is null");
+    REQUIRE(aligned(slots, 4) && aligned(out, elem_bytes(elem)), QK_ERR_ARG, "misaligned pointer");
+    REQUIRE(out_stride >= width, QK_ERR_SHAPE, "out_stride=%lld < %lld", (long long)out_stride, (long long)width);
+    REQUIRE(out_stride <= MOST_STRIDE, QK_ERR_ARG, "out_stride is out of range");
+    if (n == 0) return QK_OK;
+    const Span so = span(out, rows_span(n, out_stride * elem_bytes(elem), width * elem_bytes(elem)));
+    REQUIRE(!overlap(so, cache_span(cache)) && !overlap(so, span(slots, (size_t)n * 4)) &&
+                !overlap(so, span(d_live_rows, d_live_rows ? 4 : 0)),
+            QK_ERR_ALIAS, "out overlaps an input");
+    return launch_kv_read(kv_cache(cache), slots, (int)n, elem, out, out_stride, d_live_rows, (cudaStream_t)stream);
+}
+
+// ------------------------------------------------------------------ attention
+struct AttnSpans {
+    Span in[6], out;
+};
+// What both calls have in common: rows of q and out, the page table of B sequences.
+static qk_status check_attn(const qk_kv_cache *cache, const qk_attn *a, int64_t B, int64_t rows, bool image,
+                            int64_t row_blocks, const int32_t *live, AttnSpans *sp) {
+    REQUIRE(a, QK_ERR_ARG, "attn is null");
+    REQUIRE(elem_ok(a->q_elem) && (!a->out || elem_ok(a->out_elem)), QK_ERR_ARG, "bad element type");
+    REQUIRE(a->n_heads >= 1 && a->n_heads <= 1024 && a->n_heads % cache->n_kv_heads == 0, QK_ERR_UNSUPPORTED,
+            "n_heads=%d is not a multiple of n_kv_heads=%d up to 1024", (int)a->n_heads, (int)cache->n_kv_heads);
+    REQUIRE(std::isfinite(a->scale) && a->scale > 0.0f, QK_ERR_ARG, "scale must be positive and finite");
+    REQUIRE(a->window >= 0, QK_ERR_ARG, "window < 0");
+    const bool none = rows == 0 || B == 0;
+    REQUIRE(none || (a->q && a->page_table && a->kv_lens), QK_ERR_ARG, "q, page_table or kv_lens is null");
+    REQUIRE(none || a->out || image, QK_ERR_ARG, "neither out nor an image is wanted");
+    const unsigned qe = elem_bytes(a->q_elem), oe = elem_bytes(a->out_elem);
+    REQUIRE(aligned(a->q, qe) && aligned(a->out, oe) && aligned(a->page_table, 4) && aligned(a->kv_lens, 4) &&
+                aligned(a->sinks, 4),
+            QK_ERR_ARG, "misaligned pointer");
+    const int64_t width = (int64_t)a->n_heads * cache->head_dim;
+    REQUIRE(a->q_stride >= width && (!a->out || a->out_stride >= width), QK_ERR_SHAPE, "a stride is smaller than its heads");
+    REQUIRE(a->q_stride <= MOST_STRIDE && (!a->out || a->out_stride <= MOST_STRIDE), QK_ERR_ARG, "a stride is out of range");
+    REQUIRE(a->table_stride >= 1 && a->table_stride <= INT32_MAX / cache->page_tokens, QK_ERR_ARG,
+            "table_stride=%lld out of range (table_stride * page_tokens <= 2^31 - 1)", (long long)a->table_stride);
+    REQUIRE(!image || row_blocks >= width / QB, QK_ERR_SHAPE, "the image row (%lld blocks) is smaller than the heads",
+            (long long)row_blocks);
+    REQUIRE(!image || row_blocks <= (1 << 20), QK_ERR_ARG, "image row blocks > 2^20");
+    sp->in[0] = cache_span(cache);
+    sp->in[1] = span(a->q, rows_span(rows, a->q_stride * qe, width * qe));
+    sp->in[2] = span(a->page_table, (size_t)(B * a->table_stride * 4));
+    sp->in[3] = span(a->kv_lens, (size_t)B * 4);
+    sp->in[4] = span(a->sinks, a->sinks ? (size_t)a->n_heads * 4 : 0);
+    sp->in[5] = span(live, live ? 4 : 0);
+    sp->out = span(a->out, a->out ? rows_span(rows, a->out_stride * oe, width * oe) : 0);
+    REQUIRE(none || std::none_of(sp->in, sp->in + 6, [&](Span i) { return overlap(sp->out, i); }), QK_ERR_ALIAS,
+            "out overlaps an input");
+    return QK_OK;
+}
+
+size_t qk_attn_decode_workspace_bytes(const qk_kv_cache *cache, int32_t n_heads, int64_t B, int32_t T) {
+    if (!cache || !kv_shape(cache->page_tokens, cache->n_kv_heads, cache->head_dim) || n_heads < 1 || n_heads > 1024 ||
+        n_heads % cache->n_kv_heads || B < 0 || B > (1 << 20) || T < 1 || T > 8)
+        return 0;
+    return (size_t)attn_decode_workspace_bytes(cache->n_kv_heads, cache->head_dim, n_heads, B, T);
+}
+
+qk_status qk_attn_decode(const qk_kv_cache *cache, const qk_attn *attn, int64_t B, int32_t T, void *img,
+                         int64_t img_row_blocks, const int32_t *d_live_rows, void *ws, size_t ws_bytes, qk_stream stream) {
+    qk_status st = check_cache(cache);
+    if (st != QK_OK) return st;
+    REQUIRE(B >= 0 && B <= (1 << 20), QK_ERR_ARG, "B=%lld out of range (0..2^20)", (long long)B);
+    REQUIRE(T >= 1, QK_ERR_ARG, "T < 1");
+    REQUIRE(T <= 8, QK_ERR_UNSUPPORTED, "T=%d > 8 (use qk_attn_prefill)", (int)T);
+    AttnSpans sp;
+    st = check_attn(cache, attn, B, B * T, img != nullptr, img_row_blocks, d_live_rows, &sp);
+    if (st != QK_OK) return st;
+    REQUIRE(aligned(img, 4), QK_ERR_ARG, "img not 4-byte aligned");
+    if (B == 0) return QK_OK;
+    const Span si = span(img, img ? (size_t)(B * T * img_row_blocks * Q8_1_BYTES) : 0);
+    const size_t need = qk_attn_decode_workspace_bytes(cache, attn->n_heads, B, T);
+    REQUIRE(ws && aligned(ws, 16), QK_ERR_WORKSPACE, "workspace null or not 16-byte aligned");
+    REQUIRE(ws_bytes >= need, QK_ERR_WORKSPACE, "workspace %zu < %zu bytes", ws_bytes, need);
+    const Span sw = span(ws, need);
+    REQUIRE(!overlap(si, sp.out) && !overlap(sw, si) && !overlap(sw, sp.out), QK_ERR_ALIAS,
+            "out, img and the workspace overlap");
+    for (const Span &i : sp.in)
+        REQUIRE(!overlap(si, i) && !overlap(sw, i), QK_ERR_ALIAS, "img or the workspace overlaps an input");
+    return launch_attn_decode(kv_cache(cache), *attn, (int)B, T, static_cast<uint8_t *>(img), img_row_blocks, d_live_rows,
+                              ws, (cudaStream_t)stream);
+}
+
+size_t qk_attn_prefill_workspace_bytes(const qk_kv_cache *cache, int64_t B, int64_t max_kv) {
+    if (!cache || !kv_shape(cache->page_tokens, cache->n_kv_heads, cache->head_dim) || B < 0 || B > 65535 || max_kv < 1 ||
+        max_kv > INT32_MAX)
+        return 0;
+    return (size_t)attn_prefill_workspace_bytes(cache->n_kv_heads, cache->head_dim, B, max_kv);
+}
+
+qk_status qk_attn_prefill(const qk_kv_cache *cache, const qk_attn *attn, int64_t B, int64_t rows,
+                          const int32_t *q_offsets, int64_t max_kv, int8_t *qs, uint16_t *d, int64_t row_blocks,
+                          const int32_t *d_live_rows, void *ws, size_t ws_bytes, qk_stream stream) {
+    qk_status st = check_cache(cache);
+    if (st != QK_OK) return st;
+    REQUIRE(B >= 0 && rows >= 0, QK_ERR_ARG, "B or rows < 0");
+    REQUIRE(B <= 65535 && rows <= (1 << 24), QK_ERR_UNSUPPORTED, "B=%lld > 65535 or rows=%lld > 2^24", (long long)B,
+            (long long)rows);
+    REQUIRE((qs != nullptr) == (d != nullptr), QK_ERR_ARG, "one of qs and d is null");
+    AttnSpans sp;
+    st = check_attn(cache, attn, B, rows, qs != nullptr, row_blocks, d_live_rows, &sp);
+    if (st != QK_OK) return st;
+    REQUIRE(max_kv >= 1 && max_kv <= attn->table_stride * cache->page_tokens, QK_ERR_ARG,
+            "max_kv=%lld not in 1..table_stride * page_tokens", (long long)max_kv);
+    REQUIRE(aligned(qs, 16) && aligned(d, 4) && aligned(q_offsets, 4), QK_ERR_ARG,
+            "misaligned pointer (qs must be 16-byte, d 4-byte aligned)");
+    if (B == 0 || rows == 0) return QK_OK;
+    REQUIRE(q_offsets, QK_ERR_ARG, "q_offsets is null");
+    const size_t need = qk_attn_prefill_workspace_bytes(cache, B, max_kv);
+    REQUIRE(ws && aligned(ws, 128), QK_ERR_WORKSPACE, "workspace null or not 128-byte aligned");
+    REQUIRE(ws_bytes >= need, QK_ERR_WORKSPACE, "workspace %zu < %zu bytes", ws_bytes, need);
+    const Span outs[4] = {sp.out, span(qs, qs ? (size_t)(rows * row_blocks * QB) : 0),
+                          span(d, d ? (size_t)(rows * row_blocks * 2) : 0), span(ws, need)};
+    for (int o = 0; o < 4; o++) {
+        for (const Span &i : sp.in) REQUIRE(!overlap(outs[o], i), QK_ERR_ALIAS, "an output or the workspace overlaps an input");
+        REQUIRE(!overlap(outs[o], span(q_offsets, (size_t)(B + 1) * 4)), QK_ERR_ALIAS,
+                "an output or the workspace overlaps q_offsets");
+        for (int i = 0; i < o; i++) REQUIRE(!overlap(outs[o], outs[i]), QK_ERR_ALIAS, "outputs and the workspace overlap");
+    }
+    return launch_attn_prefill(kv_cache(cache), *attn, (int)B, (int)rows, q_offsets, (int)max_kv, qs, d, row_blocks,
+                               d_live_rows, ws, (cudaStream_t)stream);
 }
 
 }  // extern "C"

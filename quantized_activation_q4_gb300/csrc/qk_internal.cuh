@@ -75,6 +75,11 @@ __device__ __forceinline__ uint16_t ld_prev(const uint16_t *p) {
     asm volatile("ld.global.u16 %0, [%1];" : "=h"(v) : "l"(p));
     return v;
 }
+__device__ __forceinline__ uint8_t ld_prev(const uint8_t *p) {
+    uint32_t v;
+    asm volatile("ld.global.u8 %0, [%1];" : "=r"(v) : "l"(p));
+    return (uint8_t)v;
+}
 __device__ __forceinline__ uint2 ld_prev(const uint2 *p) {
     uint2 v;
     asm volatile("ld.global.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
