@@ -767,7 +767,7 @@ typedef struct qk_attn {
     int32_t n_heads;           /* a multiple of n_kv_heads, at most 1024 */
     int64_t q_stride;          /* in elements */
     const int32_t *page_table; /* [B][table_stride] */
-    int64_t table_stride;      /* pages a sequence can have */
+    int64_t table_stride;      /* pages a sequence can have; table_stride * page_tokens <= 2^30 */
     const int32_t *kv_lens;    /* [B] */
     float scale;               /* finite, > 0 */
     int32_t window;            /* 0: none */

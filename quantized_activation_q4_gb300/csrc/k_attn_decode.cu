@@ -1,0 +1,740 @@
+// Attention of a few new tokens of many sequences over the 4-bit cache (qk_attn_decode).
+//
+// attn_decode_kernel: one pass over the keys and values. A tile is 128 tokens of one sequence and key/value head; the
+// tiles of all sequences, in the order (sequence, head, token), are cut into equal shares, one for each resident CTA, so
+// sequences of any lengths fill the device. Four warps take 32 tokens of a tile each, with a running maximum, sum and
+// output of their own; at the end of a segment (a share's part of one sequence and head) they meet and leave one partial
+// result. attn_combine_kernel adds the partial results of a head in the order of its tokens, so outputs do not depend on
+// the run, and writes rows and image.
+//
+// The tokens of a group are the rows (M) of the products, up to 8 NT query columns (query heads of the key/value head
+// times new tokens) their columns (N), so a group of seven heads wastes an eighth and not half. With the scales outside
+// of the products the operands are the codes themselves:
+//   S[token][column] = sum over blocks b of d_k[token][b] * (sum over the block of (code - 8) * q)
+//   O[x][column]    += sum over tokens of (code - 8) * (P[token][column] * d_v[token][block of x])
+// A nibble becomes a half by one logic operation (1024 + code, or 64 + code in a high nibble). For S the bias leaves as the
+// initial accumulator, -(1032 or 72) * sum q, once per segment; for O it is subtracted (the weights' sum would cancel
+// catastrophically over long sequences). Queries are divided by a power of two to stay inside binary16, whatever their
+// size. Weights are kept at up to 2^14 times their value, so those down to 2^-28 of the largest keep binary16's precision;
+// where a value's scale is 2 or more, its exponent joins the running maximum.
+//
+// Bound by instruction issue next to memory: 2304 bytes of cache (16 tokens of a head of 128) cost about 205 warp
+// instructions, which at full issue would be 13 TB/s.
+
+#include <algorithm>
+
+#include "qk_kv.cuh"
+#include "qk_tc.cuh"
+
+namespace qk {
+namespace {
+
+constexpr unsigned FULL = 0xffffffffu;
+constexpr float LOG2E = 1.4426950408889634f;
+constexpr int WARPS = 4;
+constexpr int WARP_TOKENS = 2 * GROUP;
+constexpr int TILE = WARPS * WARP_TOKENS;   // tokens
+constexpr float HEADROOM = 8.0f;    // the reference maximum moves when a logit is 2^8 above it
+constexpr float LIFT = 6.0f;        // weights are held times 2^6 below the reference: at most 2^14
+constexpr int MAX_CTAS = 1024;      // of one launch; sizes the workspace
+
+// column tiles of 8 a CTA takes at most
+__host__ __device__ constexpr int column_tiles(int D) { return D == 256 ? 1 : 2; }
+__host__ __device__ constexpr int stages(int D, int NT) { return D == 64 ? 4 : NT == 2 ? 3 : 3; }
+
+struct DecodeArgs {
+    KvCache c;
+    qk_attn a;
+    int B, T, G, groups;   // groups: CTAs that share a tile, each with its own columns
+    const int32_t *live;
+    float *acc;            // [slot][groups][8 NT][D]
+    float2 *ml;            // [slot][groups][8 NT]: reference maximum, sum of weights
+    int64_t *plan;         // [0] tiles of a share, [1 + b] tiles before sequence b
+};
+
+// ---------------------------------------------------------------- the tiles of a sequence
+struct Sequence {
+    int len, base, tiles;   // keys, first token that a tile covers (a multiple of 16), tiles of one head
+};
+__device__ __forceinline__ Sequence sequence_of(const DecodeArgs &p, int b) {
+    const int64_t most = p.a.table_stride * p.c.page_tokens;
+    Sequence s;
+    s.len = (int)min((int64_t)max(ld_prev(p.a.kv_lens + b), 0), most);
+    const int first_end = s.len - p.T + 1;
+    s.base = p.a.window > 0 ? max(0, first_end - p.a.window) & ~(GROUP - 1) : 0;
+    s.tiles = (s.len - s.base + TILE - 1) / TILE;   // lengths are at most 2^30
+    return s;
+}
+
+// Sum over a CTA of 128 threads of one value each, and the sum of the threads before.
+__device__ __forceinline__ int64_t scan128(int64_t v, int64_t *before, int64_t *smem) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t x = v;
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+        const int64_t y = __shfl_up_sync(FULL, x, m);
+        if (lane >= m) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) smem[warp] = x;
+    __syncthreads();
+    int64_t total = 0, base = 0;
+#pragma unroll
+    for (int w = 0; w < WARPS; w++) {
+        if (w < warp) base += smem[w];
+        total += smem[w];
+    }
+    *before = base + x - v;
+    return total;
+}
+
+// ---------------------------------------------------------------- fragments
+__device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                      uint32_t b1, const float (&c)[4]) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
+}
+__device__ __forceinline__ uint32_t lo_half(uint32_t w) { return (w & 0x000F000Fu) | 0x64006400u; }   // 1024 + code
+__device__ __forceinline__ uint32_t hi_half(uint32_t w) { return (w & 0x00F000F0u) | 0x54005400u; }   // 64 + code
+__device__ __forceinline__ uint32_t sub2(uint32_t v, uint32_t bias) {
+    const __half2 r = __hsub2(half2_bits(v), half2_bits(bias));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
+    const __half2 r = __hmul2(half2_bits(a), half2_bits(b));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    const __half2 r = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+    return v;
+}
+template <int N>
+__device__ __forceinline__ void lds_words(uint32_t a, uint32_t (&w)[N]) {
+    if constexpr (N == 1) {
+        w[0] = lds32(a);
+    } else if constexpr (N == 2) {
+        const uint2 v = lds64(a);
+        w[0] = v.x, w[1] = v.y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 4) {
+            const uint4 v = lds128(a + 4 * i);
+            w[i] = v.x, w[i + 1] = v.y, w[i + 2] = v.z, w[i + 3] = v.w;
+        }
+    }
+}
+
+// The queries of a segment's columns as B operands, and what the scores need besides.
+template <int D, int NT>
+struct Queries {
+    static constexpr int NB = D / 32;
+    uint32_t b[NB][NT][2][2];    // [block][column tile][low, high nibbles][register]
+    float start[NB][NT][2];      // -(bias * sum of the block's queries), columns 2t and 2t + 1
+    float scale[NT][2];          // scale * log2 e * the queries' power of two
+};
+template <int D, int NT>
+__device__ __forceinline__ void load_queries(Queries<D, NT> &q, const DecodeArgs &p, int b, int h, int column0, bool wide) {
+    constexpr int NB = D / 32;
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int n = 0; n < NT; n++) {
+        const int col = column0 + 8 * n + g;
+        const bool there = col < p.T * p.G;
+        const int i = there ? col / p.G : 0, head = h * p.G + (there ? col % p.G : 0);
+        const int64_t at = ((int64_t)b * p.T + i) * p.a.q_stride + (int64_t)head * D;
+        float4 x[NB][2];
+        float top = 0.0f;
+#pragma unroll
+        for (int k = 0; k < NB; k++)
+#pragma unroll
+            for (int e = 0; e < 2; e++) {
+                const int64_t o = at + 32 * k + 16 * e + 4 * t;
+                x[k][e] = p.a.q_elem == QK_ELEM_F32
+                              ? load_row4(static_cast<const float *>(p.a.q) + o, wide)
+                              : load_row4(static_cast<const __nv_bfloat16 *>(p.a.q) + o, wide);
+                if (!there) x[k][e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                top = fmaxf(top, fmaxf(fmaxf(fabsf(x[k][e].x), fabsf(x[k][e].y)), fmaxf(fabsf(x[k][e].z), fabsf(x[k][e].w))));
+            }
+        top = fmaxf(top, __shfl_xor_sync(FULL, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(FULL, top, 2));
+        // 2^e is above the largest magnitude; its inverse stays a normal number
+        const int e2 = min(max((int)(__float_as_uint(top) >> 23) - 126, -100), 100);
+        const float down = __uint_as_float((uint32_t)(127 - e2) << 23), up = __uint_as_float((uint32_t)(127 + e2) << 23);
+        const float c = p.a.scale * LOG2E * up;   // (0 where the queries are 0 and it underflows: so are the scores)
+#pragma unroll
+        for (int k = 0; k < NB; k++) {
+            float bias = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 2; e++) {
+                const __half2 v0 = __floats2half2_rn(x[k][e].x * down, x[k][e].z * down);   // nibbles of bytes 0 and 2
+                const __half2 v1 = __floats2half2_rn(x[k][e].y * down, x[k][e].w * down);   // 1 and 3
+                q.b[k][n][e][0] = *reinterpret_cast<const uint32_t *>(&v0);
+                q.b[k][n][e][1] = *reinterpret_cast<const uint32_t *>(&v1);
+                const float2 f0 = __half22float2(v0), f1 = __half22float2(v1);
+                bias = fmaf(e ? -72.0f : -1032.0f, (f0.x + f0.y) + (f1.x + f1.y), bias);
+            }
+            bias += __shfl_xor_sync(FULL, bias, 1);
+            bias += __shfl_xor_sync(FULL, bias, 2);
+            q.start[k][n][0] = __shfl_sync(FULL, bias, 8 * t);
+            q.start[k][n][1] = __shfl_sync(FULL, bias, 8 * t + 4);
+        }
+        q.scale[n][0] = __shfl_sync(FULL, c, 8 * t);
+        q.scale[n][1] = __shfl_sync(FULL, c, 8 * t + 4);
+    }
+}
+
+// ---------------------------------------------------------------- the pass
+// A walk over the tiles of a share: (sequence, head, tile), sequences without keys left out.
+struct Walk {
+    int b, h, tile;
+    Sequence s;
+};
+__device__ __forceinline__ void next_tile(Walk &w, const DecodeArgs &p, int live) {
+    if (++w.tile < w.s.tiles) return;
+    w.tile = 0;
+    if (++w.h < p.c.Hkv) return;
+    w.h = 0;
+    do {
+        w.b++;
+        if (w.b < live) w.s = sequence_of(p, w.b);
+    } while (w.b < live && w.s.tiles == 0);
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(WARPS * 32, NT == 1 ? (D == 256 ? 2 : 4) : (D == 64 ? 3 : 2))
+attn_decode_kernel(const __grid_constant__ DecodeArgs p, bool wide) {
+    constexpr int NB = D / 32, S = stages(D, NT), GB = group_bytes(D), MT = D / 16, W = NB < 4 ? NB : 4;
+    constexpr int STAGE = 2 * GB, PITCH = D + 4;
+    static_assert(8 * PITCH * 4 <= STAGE, "a warp's partial outputs fit its stage");
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ int64_t scan[WARPS];
+    __shared__ int64_t found[2];
+    __shared__ float2 meet[WARPS][8];
+    __shared__ uint8_t use[WARPS][S][2];
+    __shared__ __align__(8) uint64_t bars[WARPS][S];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int share = blockIdx.x / p.groups, cg = blockIdx.x % p.groups, shares = gridDim.x / p.groups;
+    const int column0 = cg * 8 * NT;
+    const uint32_t ring = smem_u32(smem) + warp * S * STAGE, bar0 = smem_u32(&bars[warp][0]);
+    if (lane < S) mbar_init(bar0 + 8 * lane, 2);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    pdl_trigger();
+    pdl_wait();
+    const int live = live_rows(p.live, p.B);
+
+    // tiles of all sequences, then the place of this share's first
+    int64_t total = 0, before = 0;
+    for (int b0 = 0; b0 < live; b0 += WARPS * 32) {
+        const int b = b0 + threadIdx.x;
+        const int64_t n = b < live ? (int64_t)sequence_of(p, b).tiles * p.c.Hkv : 0;
+        const int64_t sum = scan128(n, &before, scan);
+        if (blockIdx.x == 0 && b < live) p.plan[1 + b] = total + before;
+        total += sum;
+    }
+    const int64_t each = max((int64_t)1, (total + shares - 1) / shares);
+    if (blockIdx.x == 0 && threadIdx.x == 0) p.plan[0] = each;
+    const int64_t first = share * each;
+    int64_t left = min(each, total - first);
+    if (left <= 0) return;
+    {
+        int64_t at = 0;
+        for (int b0 = 0; b0 < live; b0 += WARPS * 32) {
+            const int b = b0 + threadIdx.x;
+            const int64_t n = b < live ? (int64_t)sequence_of(p, b).tiles * p.c.Hkv : 0;
+            const int64_t sum = scan128(n, &before, scan);
+            if (first >= at + before && first < at + before + n) {
+                found[0] = b;
+                found[1] = first - at - before;
+            }
+            at += sum;
+            if (first < at) break;
+        }
+        __syncthreads();
+    }
+    Walk now;
+    now.b = (int)found[0];
+    now.s = sequence_of(p, now.b);
+    now.h = (int)(found[1] / now.s.tiles);
+    now.tile = (int)(found[1] % now.s.tiles);
+
+    // what is on its way: lanes 0 and 1 copy one group each
+    Walk ahead = now;
+    int64_t to_issue = left;
+    int page = -1, token = 0;   // of the next tile to issue
+    bool ok = true;
+    const auto look_up = [&]() {
+        token = ahead.s.base + ahead.tile * TILE + warp * WARP_TOKENS + lane * GROUP;
+        page = -1;
+        if (lane < 2 && to_issue > 0 && token < ahead.s.len)
+            page = ld_prev(p.a.page_table + ahead.b * p.a.table_stride + token / p.c.page_tokens);
+    };
+    const auto issue = [&](int stage) {
+        if (to_issue <= 0 || !ok) return;
+        if (lane < 2) {
+            const bool good = page >= 0 && page < p.c.n_pages;
+            use[warp][stage][lane] = good;
+            if (good) {
+                mbar_expect_tx(bar0 + 8 * stage, GB);
+                bulk_g2s(ring + stage * STAGE + lane * GB, group_at(p.c, page, ahead.h, token % p.c.page_tokens), GB,
+                         bar0 + 8 * stage);
+            } else {
+                mbar_arrive(bar0 + 8 * stage);
+            }
+        }
+        to_issue--;
+        if (to_issue > 0) next_tile(ahead, p, live);
+        look_up();
+    };
+    __syncwarp();
+    look_up();
+#pragma unroll
+    for (int s = 0; s < S; s++) issue(s);
+
+    float o[MT][NT][4], ref[NT][2], sum[NT][2], off[NT][2];
+    Queries<D, NT> q;
+    int lift_e = 0;       // exponent of the largest value scale so far (0 while all are below 2)
+    bool fresh = true;    // a segment begins
+    int stage = 0;
+    uint32_t parity = 0;
+    for (;; left--) {
+        if (fresh) {
+            load_queries<D, NT>(q, p, now.b, now.h, column0, wide);
+#pragma unroll
+            for (int n = 0; n < NT; n++)
+#pragma unroll
+                for (int e = 0; e < 2; e++) {
+                    ref[n][e] = -INFINITY;
+                    off[n][e] = 0.0f;
+                    sum[n][e] = 0.0f;
+                }
+#pragma unroll
+            for (int m = 0; m < MT; m++)
+#pragma unroll
+                for (int n = 0; n < NT; n++)
+#pragma unroll
+                    for (int e = 0; e < 4; e++) o[m][n][e] = 0.0f;
+            lift_e = 0;
+            fresh = false;
+        }
+        if (ok) ok = mbar_wait(bar0 + 8 * stage, parity);
+        const uint32_t buf = ring + stage * STAGE;
+        const int token0 = now.s.base + now.tile * TILE + warp * WARP_TOKENS;
+        const int end0 = now.s.len - p.T + 1;   // keys that the first of the new tokens sees
+        // scores of both groups, times log2 e
+        float s[2][NT][4];
+        bool used[2];
+#pragma unroll
+        for (int r = 0; r < 2; r++) {
+            used[r] = ok && use[warp][stage][r];
+#pragma unroll
+            for (int n = 0; n < NT; n++)
+#pragma unroll
+                for (int e = 0; e < 4; e++) s[r][n][e] = used[r] ? 0.0f : -INFINITY;
+            if (!used[r]) continue;
+            const uint32_t grp = buf + r * GB;
+            uint32_t dk[2][NB / 2];
+            lds_words<NB / 2>(grp + 8 * D + 2 * NB * g, dk[0]);
+            lds_words<NB / 2>(grp + 8 * D + 2 * NB * (g + 8), dk[1]);
+#pragma unroll
+            for (int bq = 0; bq < NB / W; bq++) {
+                uint32_t w0[W], w1[W];
+                lds_words<W>(grp + ((bq * GROUP + g) * 4 + t) * 4 * W, w0);
+                lds_words<W>(grp + ((bq * GROUP + g + 8) * 4 + t) * 4 * W, w1);
+#pragma unroll
+                for (int k = 0; k < W; k++) {
+                    const int b = bq * W + k;
+                    const float2 p0 = __half22float2(half2_bits(dk[0][b / 2])), p1 = __half22float2(half2_bits(dk[1][b / 2]));
+                    const float d0 = b & 1 ? p0.y : p0.x, d1 = b & 1 ? p1.y : p1.x;
+                    const uint32_t x0 = w0[k], x1 = w1[k], y0 = x0 >> 8, y1 = x1 >> 8;
+#pragma unroll
+                    for (int n = 0; n < NT; n++) {
+                        const float c[4] = {q.start[b][n][0], q.start[b][n][1], q.start[b][n][0], q.start[b][n][1]};
+                        float a[4];
+                        mma16(a, lo_half(x0), lo_half(x1), lo_half(y0), lo_half(y1), q.b[b][n][0][0], q.b[b][n][0][1], c);
+                        mma16(a, hi_half(x0), hi_half(x1), hi_half(y0), hi_half(y1), q.b[b][n][1][0], q.b[b][n][1][1], a);
+                        s[r][n][0] = fmaf(d0, a[0], s[r][n][0]);
+                        s[r][n][1] = fmaf(d0, a[1], s[r][n][1]);
+                        s[r][n][2] = fmaf(d1, a[2], s[r][n][2]);
+                        s[r][n][3] = fmaf(d1, a[3], s[r][n][3]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < NT; n++)
+#pragma unroll
+                for (int e = 0; e < 4; e++) s[r][n][e] *= q.scale[n][e & 1];
+            const int j = token0 + r * GROUP;
+            if (j + GROUP > end0 || (p.a.window > 0 && j < now.s.len - p.a.window)) {   // some query does not see some key
+#pragma unroll
+                for (int n = 0; n < NT; n++)
+#pragma unroll
+                    for (int e = 0; e < 2; e++) {
+                        const int end = end0 + (column0 + 8 * n + 2 * t + e) / p.G;
+                        const int begin = p.a.window > 0 ? end - p.a.window : 0;
+                        if (j + g >= end || j + g < begin || j + g >= now.s.len) s[r][n][e] = -INFINITY;
+                        if (j + g + 8 >= end || j + g + 8 < begin || j + g + 8 >= now.s.len) s[r][n][2 + e] = -INFINITY;
+                    }
+            }
+        }
+        // the columns' maxima; the reference moves only far
+        float top[NT][2];
+        bool move = false;
+#pragma unroll
+        for (int n = 0; n < NT; n++)
+#pragma unroll
+            for (int e = 0; e < 2; e++) {
+                float m = fmaxf(fmaxf(s[0][n][e], s[0][n][2 + e]), fmaxf(s[1][n][e], s[1][n][2 + e]));
+                m = fmaxf(m, __shfl_xor_sync(FULL, m, 4));
+                m = fmaxf(m, __shfl_xor_sync(FULL, m, 8));
+                m = fmaxf(m, __shfl_xor_sync(FULL, m, 16));
+                top[n][e] = m;
+                move |= m - ref[n][e] > HEADROOM;   // (no: both are minus infinity)
+            }
+        // the values' scales (zero behind the last key, where the cache may hold anything)
+        uint32_t dv[2][NB][2], any = 0;
+#pragma unroll
+        for (int r = 0; r < 2; r++) {
+            if (!used[r]) continue;
+            uint32_t w[2 * NB];
+            lds_words<2 * NB>(buf + r * GB + 17 * D + t * 8 * NB, w);
+            const int j = token0 + r * GROUP + 2 * t;
+            uint32_t k0 = FULL, k1 = FULL;
+            if (j + GROUP > now.s.len) {
+                k0 = (j < now.s.len ? 0xffffu : 0) | (j + 1 < now.s.len ? 0xffff0000u : 0);
+                k1 = (j + 8 < now.s.len ? 0xffffu : 0) | (j + 9 < now.s.len ? 0xffff0000u : 0);
+            }
+#pragma unroll
+            for (int b = 0; b < NB; b++) {
+                dv[r][b][0] = w[2 * b] & k0;
+                dv[r][b][1] = w[2 * b + 1] & k1;
+                any |= dv[r][b][0] | dv[r][b][1];
+            }
+        }
+        const bool large = (any & 0x40004000u) != 0;   // a scale of 2 or more
+        int e_new = lift_e;
+        if (__any_sync(FULL, move || large)) {
+            if (__any_sync(FULL, large)) {
+                float m = 0.0f;
+#pragma unroll
+                for (int r = 0; r < 2; r++)
+#pragma unroll
+                    for (int b = 0; b < NB; b++)
+#pragma unroll
+                        for (int x = 0; x < 2; x++)
+                            if (used[r]) {
+                                const float2 f = __half22float2(__habs2(half2_bits(dv[r][b][x])));
+                                m = fmaxf(m, fmaxf(f.x, f.y));
+                            }
+#pragma unroll
+                for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, x));
+                e_new = min(max(e_new, (int)(__float_as_uint(m) >> 23) - 127), 16);
+            }
+        }
+        if (__any_sync(FULL, move) || e_new != lift_e) {
+#pragma unroll
+            for (int n = 0; n < NT; n++)
+#pragma unroll
+                for (int e = 0; e < 2; e++) {
+                    const float r = fmaxf(ref[n][e], top[n][e]);
+                    const float down = ref[n][e] == -INFINITY ? 0.0f : ex2(ref[n][e] - r + (float)(lift_e - e_new));
+                    ref[n][e] = r;
+                    off[n][e] = r == -INFINITY ? 0.0f : __fadd_ru(r, (float)e_new - LIFT);   // never below: weights stay under 2^14
+                    sum[n][e] *= down;
+#pragma unroll
+                    for (int m = 0; m < MT; m++) {
+                        o[m][n][e] *= down;
+                        o[m][n][2 + e] *= down;
+                    }
+                }
+            lift_e = e_new;
+        }
+#pragma unroll
+        for (int r = 0; r < 2; r++) {
+            if (!used[r]) continue;
+            const uint32_t grp = buf + r * GB;
+            uint32_t pt[NT][2];   // weights of query g: tokens 2t, 2t + 1 and 2t + 8, 2t + 9
+#pragma unroll
+            for (int n = 0; n < NT; n++) {
+                float w[4];
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    w[e] = ex2(s[r][n][e] - off[n][e & 1]);
+                    sum[n][e & 1] += w[e];
+                }
+                pt[n][0] = transpose8(pack2(w[0], w[1]));
+                pt[n][1] = transpose8(pack2(w[2], w[3]));
+            }
+#pragma unroll
+            for (int mq = 0; mq < MT / 4; mq++) {
+                uint32_t w[4];
+                lds_words<4>(grp + 9 * D + ((mq * 8 + g) * 4 + t) * 16, w);
+#pragma unroll
+                for (int bb = 0; bb < 2; bb++) {
+                    const int b = 2 * mq + bb;
+                    uint32_t pb[NT][2];
+#pragma unroll
+                    for (int n = 0; n < NT; n++) {
+                        pb[n][0] = mul2(pt[n][0], dv[r][b][0]);
+                        pb[n][1] = mul2(pt[n][1], dv[r][b][1]);
+                    }
+#pragma unroll
+                    for (int mm = 0; mm < 2; mm++) {
+                        const uint32_t x = w[2 * bb + mm], y = x >> 8;
+                        const uint32_t a0 = sub2(lo_half(x), 0x64086408u), a1 = sub2(hi_half(x), 0x54805480u);
+                        const uint32_t a2 = sub2(lo_half(y), 0x64086408u), a3 = sub2(hi_half(y), 0x54805480u);
+#pragma unroll
+                        for (int n = 0; n < NT; n++)
+                            mma16(o[2 * b + mm][n], a0, a1, a2, a3, pb[n][0], pb[n][1], o[2 * b + mm][n]);
+                    }
+                }
+            }
+        }
+        __syncwarp();   // the stage is read
+        if (left == 1 || now.tile + 1 == now.s.tiles) {
+            // the segment ends here: one partial result of the four warps, through the stages just read
+            const int64_t slot = ((int64_t)now.b * p.c.Hkv + now.h + share) * p.groups + cg;
+#pragma unroll
+            for (int n = 0; n < NT; n++) {
+#pragma unroll
+                for (int e = 0; e < 2; e++) {
+                    float l = sum[n][e];
+                    l += __shfl_xor_sync(FULL, l, 4);
+                    l += __shfl_xor_sync(FULL, l, 8);
+                    l += __shfl_xor_sync(FULL, l, 16);
+                    if (g == 0) meet[warp][2 * t + e] = make_float2(ref[n][e] == -INFINITY ? -INFINITY : off[n][e], l);
+                }
+                __syncthreads();
+                float down[2];
+#pragma unroll
+                for (int e = 0; e < 2; e++) {
+                    float m = -INFINITY;
+#pragma unroll
+                    for (int w = 0; w < WARPS; w++) m = fmaxf(m, meet[w][2 * t + e].x);
+                    down[e] = ref[n][e] == -INFINITY ? 0.0f : ex2(off[n][e] - m);
+                }
+                float *mine = reinterpret_cast<float *>(smem + (warp * S + stage) * STAGE);
+#pragma unroll
+                for (int m = 0; m < MT; m++)
+#pragma unroll
+                    for (int e = 0; e < 4; e++)
+                        mine[(2 * t + (e & 1)) * PITCH + 16 * m + 8 * (e >> 1) + g] = o[m][n][e] * down[e & 1];
+                __syncthreads();
+                const float *all = reinterpret_cast<const float *>(smem + stage * STAGE);
+                constexpr int STEP = S * STAGE / 4;   // floats from one warp's stage to the next one's
+                float *out = p.acc + (slot * NT + n) * 8 * D;
+                for (int i = threadIdx.x; i < 8 * D; i += WARPS * 32) {
+                    const int at = i / D * PITCH + i % D;
+                    out[i] = (all[at] + all[at + STEP]) + (all[at + 2 * STEP] + all[at + 3 * STEP]);
+                }
+                if (threadIdx.x < 8) {
+                    float m = -INFINITY, l = 0.0f;
+#pragma unroll
+                    for (int w = 0; w < WARPS; w++) m = fmaxf(m, meet[w][threadIdx.x].x);
+#pragma unroll
+                    for (int w = 0; w < WARPS; w++) {
+                        const float2 v = meet[w][threadIdx.x];
+                        l += v.x == -INFINITY ? 0.0f : v.y * ex2(v.x - m);
+                    }
+                    p.ml[(slot * NT + n) * 8 + threadIdx.x] = make_float2(m, l);
+                }
+                __syncthreads();
+            }
+            fresh = true;
+        }
+        if (left == 1) break;
+        next_tile(now, p, live);
+        // the stage was read and written by plain accesses; the next copy into it comes after them
+        if (fresh) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        issue(stage);
+        if (++stage == S) {
+            stage = 0;
+            parity ^= 1;
+        }
+    }
+    if (!ok)   // a wait ran out: no copy may land after the CTA has gone
+        for (int s = 0; s < S; s++)
+            if (!mbar_wait(bar0 + 8 * s, parity)) break;
+}
+
+// ---------------------------------------------------------------- joining
+struct JoinArgs {
+    DecodeArgs p;
+    uint8_t *img;
+    int64_t row_blocks;
+    int NT;
+};
+// One CTA per (row, query head): its head's partial results in order, four at a time; then rows and image.
+template <int D>
+__global__ void __launch_bounds__(128) attn_combine_kernel(const __grid_constant__ JoinArgs a) {
+    constexpr int NB = D / 32;
+    __shared__ float part[WARPS][D];
+    __shared__ float2 stat[WARPS];
+    pdl_trigger();
+    pdl_wait();
+    const DecodeArgs &p = a.p;
+    const int head = blockIdx.x, row = blockIdx.y * gridDim.z + blockIdx.z;
+    const int b = row / p.T, i = row % p.T, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (b >= p.B || b >= live_rows(p.live, p.B)) return;
+    const int h = head / p.G, col = i * p.G + head % p.G;
+    const Sequence s = sequence_of(p, b);
+    const float sink = p.a.sinks ? ld_prev(p.a.sinks + head) * LOG2E : -INFINITY;
+    float top = -INFINITY, l = 0.0f, o[NB];
+#pragma unroll
+    for (int k = 0; k < NB; k++) o[k] = 0.0f;
+    if (s.tiles > 0) {
+        const int64_t each = ld_prev(p.plan);
+        const int64_t lo = ld_prev(p.plan + 1 + b) + (int64_t)h * s.tiles;
+        const int64_t c0 = lo / each, c1 = (lo + s.tiles - 1) / each;
+        const int64_t seg = (int64_t)b * p.c.Hkv + h;
+        const int n = col / 8, cg = n / a.NT, in = n % a.NT * 8 + col % 8;
+        const auto at = [&](int64_t c) { return ((seg + c) * p.groups + cg) * a.NT * 8 + in; };
+        for (int64_t c = c0 + warp; c <= c1; c += WARPS) {
+            const float m = ld_prev(&p.ml[at(c)].x), v = ld_prev(&p.ml[at(c)].y);
+            float x[NB];
+#pragma unroll
+            for (int k = 0; k < NB; k++) x[k] = ld_prev(p.acc + at(c) * D + 32 * k + lane);
+            if (m == -INFINITY) continue;
+            const float now = fmaxf(top, m), old = top == -INFINITY ? 0.0f : ex2(top - now), f = ex2(m - now);
+            top = now;
+            l = l * old + v * f;
+#pragma unroll
+            for (int k = 0; k < NB; k++) o[k] = o[k] * old + x[k] * f;
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < NB; k++) part[warp][32 * k + lane] = o[k];
+    if (lane == 0) stat[warp] = make_float2(top, l);
+    __syncthreads();
+    top = sink;
+#pragma unroll
+    for (int w = 0; w < WARPS; w++) top = fmaxf(top, stat[w].x);
+    float f[WARPS], total = sink == -INFINITY ? 0.0f : ex2(sink - top);
+#pragma unroll
+    for (int w = 0; w < WARPS; w++) {
+        f[w] = stat[w].x == -INFINITY ? 0.0f : ex2(stat[w].x - top);
+        total = fmaf(stat[w].y, f[w], total);
+    }
+    const float inv = total > 0.0f ? 1.0f / total : 0.0f;
+    for (int k = warp; k < NB; k += WARPS) {
+        float y = 0.0f;
+#pragma unroll
+        for (int w = 0; w < WARPS; w++) y = fmaf(part[w][32 * k + lane], f[w], y);
+        y *= inv;
+        const int64_t to = row * p.a.out_stride + (int64_t)head * D + 32 * k + lane;
+        if (p.a.out && p.a.out_elem == QK_ELEM_F32) static_cast<float *>(p.a.out)[to] = y;
+        if (p.a.out && p.a.out_elem == QK_ELEM_BF16) static_cast<__nv_bfloat16 *>(p.a.out)[to] = __float2bfloat16_rn(y);
+        if (!a.img) continue;
+        float m = fabsf(y);
+#pragma unroll
+        for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, x));
+        const float d = m / 127.0f;
+        const int code = m != 0.0f ? __float2int_rn(y / d) : 0;
+        const int sum = __reduce_add_sync(FULL, code);
+        uint8_t *block = a.img + (row * a.row_blocks + (int64_t)head * NB + k) * Q8_1_BYTES;
+        block[4 + lane] = (uint8_t)code;
+        if (lane == 0)
+            *reinterpret_cast<__half2 *>(block) = __halves2half2(__float2half_rn(d), __float2half_rn(d * (float)sum));
+    }
+    if (a.img && head == p.a.n_heads - 1) {   // the blocks behind the heads
+        uint32_t *rest = reinterpret_cast<uint32_t *>(a.img + (row * a.row_blocks + (int64_t)p.a.n_heads * NB) * Q8_1_BYTES);
+        const int64_t words = (a.row_blocks - (int64_t)p.a.n_heads * NB) * (Q8_1_BYTES / 4);
+        for (int64_t x = threadIdx.x; x < words; x += 128) rest[x] = 0;
+    }
+}
+
+struct Layout {
+    int NT, groups;
+    int64_t slots, acc, ml, plan, bytes;
+};
+Layout layout_of(int Hkv, int D, int n_heads, int64_t B, int T) {
+    Layout l;
+    const int tiles = (T * (n_heads / Hkv) + 7) / 8;
+    l.NT = tiles < column_tiles(D) ? tiles : column_tiles(D);
+    l.groups = (tiles + l.NT - 1) / l.NT;
+    // segments and shares interleave, so (segment + share) names each part of a segment once
+    l.slots = (B * Hkv + MAX_CTAS) * l.groups;
+    l.acc = 0;
+    l.ml = l.acc + l.slots * l.NT * 8 * D * 4;
+    l.plan = l.ml + l.slots * l.NT * 8 * 8;
+    l.bytes = l.plan + (1 + B) * 8;
+    return l;
+}
+
+template <int D, int NT>
+qk_status launch_pass(const DecodeArgs &p, cudaStream_t s) {
+    constexpr int smem = WARPS * stages(D, NT) * 2 * group_bytes(D);
+    constexpr int per_sm = NT == 1 ? (D == 256 ? 2 : 4) : (D == 64 ? 3 : 2);
+    static bool ready[64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return fail(QK_ERR_CUDA, "attn_decode: no device");
+    if (!ready[dev]) {
+        const cudaError_t e =
+            cudaFuncSetAttribute(attn_decode_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return fail(QK_ERR_CUDA, "attn_decode: %s", cudaGetErrorString(e));
+        ready[dev] = true;
+    }
+    const int shares = std::max(1, std::min(per_sm * sm_count(), MAX_CTAS) / p.groups);
+    const bool wide = row_wide(p.a.q, p.a.q_stride, p.a.q_elem);
+    return launch_pdl("attn_decode", attn_decode_kernel<D, NT>, dim3((unsigned)shares * p.groups), dim3(WARPS * 32), smem, s,
+                      p, wide);
+}
+
+}  // namespace
+
+int64_t attn_decode_workspace_bytes(int Hkv, int D, int n_heads, int64_t B, int T) {
+    return layout_of(Hkv, D, n_heads, B, T).bytes;
+}
+
+qk_status launch_attn_decode(const KvCache &c, const qk_attn &a, int B, int T, uint8_t *img, int64_t row_blocks,
+                             const int32_t *live, void *ws, cudaStream_t s) {
+    const Layout l = layout_of(c.Hkv, c.D, a.n_heads, B, T);
+    uint8_t *w = static_cast<uint8_t *>(ws);
+    const DecodeArgs p = {c, a, B, T, a.n_heads / c.Hkv, l.groups, live, reinterpret_cast<float *>(w + l.acc),
+                          reinterpret_cast<float2 *>(w + l.ml), reinterpret_cast<int64_t *>(w + l.plan)};
+    qk_status st = c.D == 256  ? launch_pass<256, 1>(p, s)
+                   : c.D == 64 ? (l.NT == 1 ? launch_pass<64, 1>(p, s) : launch_pass<64, 2>(p, s))
+                               : (l.NT == 1 ? launch_pass<128, 1>(p, s) : launch_pass<128, 2>(p, s));
+    if (st != QK_OK) return st;
+    const int rows = B * T, z = rows > 65535 ? 128 : 1;
+    const JoinArgs j = {p, img, row_blocks, l.NT};
+    auto *combine = c.D == 64 ? attn_combine_kernel<64> : c.D == 128 ? attn_combine_kernel<128> : attn_combine_kernel<256>;
+    return launch_pdl("attn_combine", combine, dim3(a.n_heads, (unsigned)ceil_div(rows, z), z), dim3(128), 0, s, j);
+}
+
+qk_status read_attn_decode_faults(uint32_t *faults) {
+    unsigned int v = 0, zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(&v, g_tc_faults, sizeof v);
+    if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_tc_faults, &zero, sizeof zero);
+    if (e != cudaSuccess) return fail(QK_ERR_CUDA, "qk_device_faults: %s", cudaGetErrorString(e));
+    *faults = v;
+    return QK_OK;
+}
+
+}  // namespace qk

@@ -146,13 +146,8 @@ qk_status launch_rows(const KvCache &c, const qk_attn &a, const Rows &R, const I
 
 }  // namespace
 
-int64_t attn_decode_workspace_bytes(int, int, int, int64_t, int) { return 16; }
 int64_t attn_prefill_workspace_bytes(int, int, int64_t, int64_t) { return 128; }
 
-qk_status launch_attn_decode(const KvCache &c, const qk_attn &a, int B, int T, uint8_t *img, int64_t row_blocks,
-                             const int32_t *live, void *, cudaStream_t s) {
-    return launch_rows(c, a, {B, T, B * T, INT32_MAX, nullptr}, {img, nullptr, nullptr, row_blocks}, live, s);
-}
 qk_status launch_attn_prefill(const KvCache &c, const qk_attn &a, int B, int rows, const int32_t *q_offsets, int max_kv,
                               int8_t *qs, uint16_t *d, int64_t row_blocks, const int32_t *live, void *, cudaStream_t s) {
     return launch_rows(c, a, {B, 0, rows, max_kv, q_offsets}, {nullptr, qs, d, row_blocks}, live, s);

@@ -396,12 +396,13 @@ size_t qk_mmvq_workspace_bytes(int32_t n_proj, const qk_proj *projs) {
 
 qk_status qk_device_faults(uint32_t *faults) {
     REQUIRE(faults, QK_ERR_ARG, "faults is null");
-    uint32_t a = 0, b = 0, c = 0, d = 0;
+    uint32_t a = 0, b = 0, c = 0, d = 0, e = 0;
     qk_status st = read_device_faults(&a);
     if (st == QK_OK) st = read_mmq_faults(&b);
     if (st == QK_OK) st = read_mmq_id_faults(&c);
     if (st == QK_OK) st = read_mmvq_g_faults(&d);
-    *faults = a | b | c | d;
+    if (st == QK_OK) st = read_attn_decode_faults(&e);
+    *faults = a | b | c | d | e;
     return st;
 }
 
@@ -841,8 +842,8 @@ static qk_status check_attn(const qk_kv_cache *cache, const qk_attn *a, int64_t 
     const int64_t width = (int64_t)a->n_heads * cache->head_dim;
     REQUIRE(a->q_stride >= width && (!a->out || a->out_stride >= width), QK_ERR_SHAPE, "a stride is smaller than its heads");
     REQUIRE(a->q_stride <= MOST_STRIDE && (!a->out || a->out_stride <= MOST_STRIDE), QK_ERR_ARG, "a stride is out of range");
-    REQUIRE(a->table_stride >= 1 && a->table_stride <= INT32_MAX / cache->page_tokens, QK_ERR_ARG,
-            "table_stride=%lld out of range (table_stride * page_tokens <= 2^31 - 1)", (long long)a->table_stride);
+    REQUIRE(a->table_stride >= 1 && a->table_stride <= (1 << 30) / cache->page_tokens, QK_ERR_ARG,
+            "table_stride=%lld out of range (table_stride * page_tokens <= 2^30)", (long long)a->table_stride);
     REQUIRE(!image || row_blocks >= width / QB, QK_ERR_SHAPE, "the image row (%lld blocks) is smaller than the heads",
             (long long)row_blocks);
     REQUIRE(!image || row_blocks <= (1 << 20), QK_ERR_ARG, "image row blocks > 2^20");

@@ -67,6 +67,11 @@ __device__ __forceinline__ uint32_t ld_prev(const uint32_t *p) {
 __device__ __forceinline__ int32_t ld_prev(const int32_t *p) {
     return (int32_t)ld_prev(reinterpret_cast<const uint32_t *>(p));
 }
+__device__ __forceinline__ int64_t ld_prev(const int64_t *p) {
+    int64_t v;
+    asm volatile("ld.global.s64 %0, [%1];" : "=l"(v) : "l"(p));
+    return v;
+}
 __device__ __forceinline__ float ld_prev(const float *p) {
     return __uint_as_float(ld_prev(reinterpret_cast<const uint32_t *>(p)));
 }
