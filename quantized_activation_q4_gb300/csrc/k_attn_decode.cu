@@ -342,7 +342,7 @@ attn_decode_kernel(const __grid_constant__ DecodeArgs p, bool wide) {
             lift_e = 0;
             fresh = false;
         }
-        if (ok) ok = mbar_wait(bar0 + 8 * stage, parity);
+        if (ok) ok = __all_sync(FULL, mbar_wait(bar0 + 8 * stage, parity));
         const uint32_t buf = ring + stage * STAGE;
         const int token0 = now.s.base + now.tile * TILE + warp * WARP_TOKENS;
         const int end0 = now.s.len - p.T + 1;   // keys that the first of the new tokens sees

@@ -1,156 +1,638 @@
-// Attention over the 4-bit key/value cache, its output's Q8 image beside the rows.
+// Attention of prompts and chunks of prompts over the 4-bit cache (qk_attn_prefill), on tcgen05.
 //
-// One warp per (query row, head): lane l holds columns 32 b + l of the query and of the output, keys one after another
-// with a running maximum and sum.
+// attn_stage_kernel turns the call's pages into binary16 once: keys [token][column] and values transposed
+// [column][token], each (code - 8) * d rounded once, so that both products read their second operand K-major by plain
+// tensor copies. Inside a group of 16 the tokens are in the order of the value codes' words (position 4 t + s is token
+// 2 t + s % 2 + 8 (s / 2)), in both, so that the words are unpacked without exchanges; the mask undoes it.
+//
+// attn_prefill_kernel: a CTA takes 128 rows (query token, head of the group) a tile, two tiles where the output fits
+// (head_dim 64 and 128), of one sequence and key/value head, and walks over the keys that they see in steps of BN. For
+// each tile S = Q K^T goes to tensor memory; one thread a row reads it, keeps the running maximum and sum, and writes the
+// weights back over it in binary16, the first operand of O += P V. While one tile's threads are at it, the tensor cores
+// work on the other's products. O is rescaled only when a row's maximum grew by more than 2^8.
+//
+// Bound by the tensor cores and, nearly as much, by the exponentials: 2 * 128 * 128 * D products a step and tile take 1024
+// cycles at D = 128, its 16384 exponentials 1024 at 16 a cycle.
+
+#include <algorithm>
 
 #include "qk_kv.cuh"
+#include "qk_tc.cuh"
 
 namespace qk {
 namespace {
 
 constexpr unsigned FULL = 0xffffffffu;
 constexpr float LOG2E = 1.4426950408889634f;
+constexpr int ROWS = 128;           // rows of a tile: lanes of tensor memory
+constexpr int PAD = 128;            // staged lengths are whole multiples
+constexpr float HEADROOM = 8.0f;    // the reference maximum moves when a logit is 2^8 above it
+constexpr float LIFT = 6.0f;        // weights are held times 2^6 below the reference: at most 2^14
 
-struct Rows {   // decode: T rows a sequence; prefill: offsets
-    int B, T, rows, max_kv;
-    const int32_t *offsets;
-};
-struct Image {
-    uint8_t *img;    // Q8_1 blocks
-    int8_t *qs;      // or Q8_0 planes
+struct PrefillArgs {
+    CUtensorMap kmap, vmap;   // keys [B Hkv Lpad][D], values [B Hkv D][Lpad]
+    KvCache c;
+    qk_attn a;
+    int B, rows, G, max_kv, lpad;
+    const int32_t *offsets, *live;
+    __half *k, *v;
+    uint8_t *there;           // [B][lpad / 16] whether a group's page exists
+    int8_t *qs;
     uint16_t *d;
     int64_t row_blocks;
+    bool q_wide, out_wide;
 };
 
-__device__ __forceinline__ float load_q(const void *q, int elem, int64_t at) {
-    if (elem == QK_ELEM_F32) return ld_prev(static_cast<const float *>(q) + at);
-    return __uint_as_float((uint32_t)ld_prev(static_cast<const uint16_t *>(q) + at) << 16);
+// Rows and keys of a sequence.
+struct Span1 {
+    int first, n, len, base;   // first row, rows, keys, first key that any row sees (a multiple of 128)
+};
+__device__ __forceinline__ Span1 span_of(const PrefillArgs &p, int b) {
+    Span1 s;
+    s.first = min(max(ld_prev(p.offsets + b), 0), p.rows);
+    s.n = max(0, min(max(ld_prev(p.offsets + b + 1), 0), p.rows) - s.first);
+    s.len = min(max(ld_prev(p.a.kv_lens + b), 0), p.max_kv);
+    s.base = p.a.window > 0 ? max(0, s.len - s.n + 1 - p.a.window) & ~(PAD - 1) : 0;
+    return s;
 }
 
-template <int NB>
-__global__ void __launch_bounds__(128) attn_rows_kernel(KvCache c, qk_attn a, Rows R, Image im, const int32_t *live) {
+// ---------------------------------------------------------------- staging
+__device__ __forceinline__ uint32_t value2(uint32_t v, uint32_t bias, __half2 d) {
+    const __half2 r = __hmul2(__hsub2(half2_bits(v), half2_bits(bias)), d);
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+__device__ __forceinline__ uint32_t lo_half(uint32_t w) { return (w & 0x000F000Fu) | 0x64006400u; }   // 1024 + code
+__device__ __forceinline__ uint32_t hi_half(uint32_t w) { return (w & 0x00F000F0u) | 0x54005400u; }   // 64 + code
+constexpr uint32_t LO_BIAS = 0x64086408u, HI_BIAS = 0x54805480u;
+
+// CTA (x, head, b): 64 tokens of a head. A warp takes a group; a lane takes words (block, t) of k and (column tile, t) of v.
+template <int D>
+__global__ void __launch_bounds__(128) attn_stage_kernel(const __grid_constant__ PrefillArgs p) {
+    constexpr int NB = D / 32, W = NB < 4 ? NB : 4;
     pdl_trigger();
     pdl_wait();
-    const int64_t unit = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31, D = 32 * NB;
-    const int row = (int)(unit / a.n_heads), head = (int)(unit % a.n_heads);
-    if (row >= R.rows) return;
-    int b, i, n;
-    if (R.offsets) {
-        b = -1;
-        for (int s = 0; s < R.B; s++) {
-            const int lo = min(max(ld_prev(R.offsets + s), 0), R.rows), hi = min(max(ld_prev(R.offsets + s + 1), 0), R.rows);
-            if (row >= lo && row < hi) {
-                b = s;
-                i = row - lo;
-                n = hi - lo;
-                break;
+    const int b = blockIdx.z, h = blockIdx.y, lane = threadIdx.x & 31;
+    const int token = (blockIdx.x * 4 + (threadIdx.x >> 5)) * GROUP;
+    if (b >= live_rows(p.live, p.B)) return;
+    const Span1 s = span_of(p, b);
+    if (s.n == 0 || token < s.base || token >= (s.len + PAD - 1) / PAD * PAD) return;
+    int page = -1;
+    if (token < s.len) page = ld_prev(p.a.page_table + b * p.a.table_stride + token / p.c.page_tokens);
+    const bool good = page >= 0 && page < p.c.n_pages;
+    if (h == 0 && lane == 0) p.there[(int64_t)b * (p.lpad / GROUP) + token / GROUP] = good;
+    const uint8_t *g = good ? group_at(p.c, page, h, token % p.c.page_tokens) : nullptr;
+    const int64_t seg = (int64_t)b * p.c.Hkv + h;
+    __half *k = p.k + (seg * p.lpad + token) * D, *v = p.v + seg * D * p.lpad + token;
+    // keys: token i goes to position 4 (i % 8 / 2) + i % 2 + i / 8 * 2
+#pragma unroll
+    for (int x = lane; x < GROUP * 4 * (NB / W); x += 32) {
+        const int t = x & 3, i = x / 4 % GROUP, bq = x / (4 * GROUP);
+        const int row = 4 * (i % 8 / 2) + i % 2 + i / 8 * 2;
+        const bool keep = good && token + i < s.len;
+#pragma unroll
+        for (int e = 0; e < W; e++) {
+            const int blk = bq * W + e;
+            uint2 lo = make_uint2(0, 0), hi = make_uint2(0, 0);
+            if (keep) {
+                const uint32_t w = ld_prev(reinterpret_cast<const uint32_t *>(g + k_word_at(D, i, blk, t))), w8 = w >> 8;
+                const __half d = __ushort_as_half(ld_prev(reinterpret_cast<const uint16_t *>(g + k_scale_at(D, i, blk))));
+                const __half2 d2 = __halves2half2(d, d);
+                const uint32_t a = value2(lo_half(w), LO_BIAS, d2), c = value2(lo_half(w8), LO_BIAS, d2);   // 0 2, 1 3
+                const uint32_t y = value2(hi_half(w), HI_BIAS, d2), z = value2(hi_half(w8), HI_BIAS, d2);
+                lo = make_uint2(__byte_perm(a, c, 0x5410), __byte_perm(a, c, 0x7632));
+                hi = make_uint2(__byte_perm(y, z, 0x5410), __byte_perm(y, z, 0x7632));
             }
-        }
-        if (b < 0) return;
-    } else {
-        b = row / R.T;
-        i = row % R.T;
-        n = R.T;
-    }
-    if (b >= live_rows(live, R.B)) return;
-    const int64_t most = min((int64_t)R.max_kv, a.table_stride * c.page_tokens);
-    const int len = (int)min((int64_t)max(ld_prev(a.kv_lens + b), 0), most);
-    const int end = len - n + i + 1;
-    const int begin = a.window > 0 ? max(0, end - a.window) : 0;
-    const int kv_head = head / (a.n_heads / c.Hkv);
-    float q[NB], o[NB];
-#pragma unroll
-    for (int k = 0; k < NB; k++) {
-        q[k] = load_q(a.q, a.q_elem, row * a.q_stride + (int64_t)head * D + 32 * k + lane) * (a.scale * LOG2E);
-        o[k] = 0.0f;
-    }
-    float top = -INFINITY, sum = 0.0f;
-    for (int j = begin; j < end; j++) {
-        const int page = ld_prev(a.page_table + b * a.table_stride + j / c.page_tokens);
-        if (page < 0 || page >= c.n_pages) continue;
-        const int in_page = j % c.page_tokens, i16 = in_page % GROUP;
-        const uint8_t *g = group_at(c, page, kv_head, in_page);
-        float s = 0.0f;
-#pragma unroll
-        for (int k = 0; k < NB; k++) {
-            const int w = ld_prev(g + k_word_at(D, i16, k, lane % 16 / 4) + lane % 4);
-            const float d = __half2float(__ushort_as_half(ld_prev(reinterpret_cast<const uint16_t *>(g + k_scale_at(D, i16, k)))));
-            s = fmaf((float)((lane < 16 ? w & 15 : w >> 4) - 8) * d, q[k], s);
-        }
-#pragma unroll
-        for (int m = 16; m; m >>= 1) s += __shfl_xor_sync(FULL, s, m);
-        const float now = fmaxf(top, s), old = exp2f(top - now), p = exp2f(s - now);
-        top = now;
-        sum = sum * old + p;
-#pragma unroll
-        for (int k = 0; k < NB; k++) {
-            const int w = ld_prev(g + v_byte_at(D, i16, 2 * k + lane / 16, lane % 8));
-            const float d = __half2float(__ushort_as_half(ld_prev(reinterpret_cast<const uint16_t *>(g + v_scale_at(D, i16, k)))));
-            o[k] = fmaf((float)((lane % 16 < 8 ? w & 15 : w >> 4) - 8) * d, p, o[k] * old);
+            __half *to = k + row * D + 32 * blk + 4 * t;
+            *reinterpret_cast<uint2 *>(to) = lo;
+            *reinterpret_cast<uint2 *>(to + 16) = hi;
         }
     }
-    if (a.sinks) {
-        const float s = ld_prev(a.sinks + head) * LOG2E, now = fmaxf(top, s);
-        const float old = top == -INFINITY ? 0.0f : exp2f(top - now);
-        sum = sum * old + exp2f(s - now);
+    // values: a word holds the tokens of positions 4 t .. 4 t + 3 of columns 16 m + u and 16 m + 8 + u
 #pragma unroll
-        for (int k = 0; k < NB; k++) o[k] *= old;
-    }
-    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+    for (int x = lane; x < D / 64 * 32; x += 32) {
+        const int t = x & 3, u = x / 4 % 8, mq = x / 32;
+        const bool k0 = token + 2 * t < s.len, k1 = token + 2 * t + 1 < s.len, k2 = token + 2 * t + 8 < s.len,
+                   k3 = token + 2 * t + 9 < s.len;
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (good) w = ld_prev(reinterpret_cast<const uint4 *>(g + 9 * D + x * 16));
+        const uint32_t words[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-    for (int k = 0; k < NB; k++) {
-        const float y = o[k] * inv;
-        const int64_t at = row * a.out_stride + (int64_t)head * D + 32 * k + lane;
-        if (a.out && a.out_elem == QK_ELEM_F32) static_cast<float *>(a.out)[at] = y;
-        if (a.out && a.out_elem == QK_ELEM_BF16) static_cast<__nv_bfloat16 *>(a.out)[at] = __float2bfloat16_rn(y);
-        float m = fabsf(y);
-#pragma unroll
-        for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, x));
-        const float d = m / 127.0f;
-        const int code = m != 0.0f ? __float2int_rn(y / d) : 0;
-        int total = code;
-#pragma unroll
-        for (int x = 16; x; x >>= 1) total += __shfl_xor_sync(FULL, total, x);
-        const int64_t block = row * im.row_blocks + head * NB + k;
-        if (im.img) {
-            im.img[block * Q8_1_BYTES + 4 + lane] = (uint8_t)code;
-            if (lane == 0)
-                *reinterpret_cast<__half2 *>(im.img + block * Q8_1_BYTES) =
-                    __halves2half2(__float2half_rn(d), __float2half_rn(d * (float)total));
-        }
-        if (im.qs) {
-            im.qs[block * QB + lane] = (int8_t)code;
-            if (lane == 0) im.d[block] = __half_as_ushort(__float2half_rn(d));
+        for (int e = 0; e < 4; e++) {
+            const int m = mq * 4 + e;
+            uint2 d = make_uint2(0, 0);
+            if (good) d = ld_prev(reinterpret_cast<const uint2 *>(g + 17 * D + (t * NB + m / 2) * 8));
+            // (a scale behind the last key may be anything: it is taken as 0)
+            d.x &= (k0 ? 0xffffu : 0) | (k1 ? 0xffff0000u : 0);
+            d.y &= (k2 ? 0xffffu : 0) | (k3 ? 0xffff0000u : 0);
+            const uint32_t y = words[e], y8 = y >> 8;
+            __half *to = v + (int64_t)(16 * m + u) * p.lpad + 4 * t;
+            *reinterpret_cast<uint2 *>(to) =
+                make_uint2(value2(lo_half(y), LO_BIAS, half2_bits(d.x)), value2(lo_half(y8), LO_BIAS, half2_bits(d.y)));
+            *reinterpret_cast<uint2 *>(to + (int64_t)8 * p.lpad) =
+                make_uint2(value2(hi_half(y), HI_BIAS, half2_bits(d.x)), value2(hi_half(y8), HI_BIAS, half2_bits(d.y)));
         }
     }
-    if (head == a.n_heads - 1)   // the blocks behind the heads
-        for (int64_t block = row * im.row_blocks + a.n_heads * NB; block < (row + 1) * im.row_blocks; block++) {
-            if (im.img) {
-                im.img[block * Q8_1_BYTES + 4 + lane] = 0;
-                if (lane == 0) *reinterpret_cast<uint32_t *>(im.img + block * Q8_1_BYTES) = 0;
-            }
-            if (im.qs) {
-                im.qs[block * QB + lane] = 0;
-                if (lane == 0) im.d[block] = 0;
-            }
-        }
 }
 
-qk_status launch_rows(const KvCache &c, const qk_attn &a, const Rows &R, const Image &im, const int32_t *live,
-                      cudaStream_t s) {
-    const dim3 grid((unsigned)ceil_div((int64_t)R.rows * a.n_heads, 4));
-    auto *kernel = c.D == 64 ? attn_rows_kernel<2> : c.D == 128 ? attn_rows_kernel<4> : attn_rows_kernel<8>;
-    return launch_pdl("attn", kernel, grid, dim3(128), 0, s, c, a, R, im, live);
+// ---------------------------------------------------------------- attention
+// D (tensor memory) (+)= A (shared memory) x B (shared memory)
+__device__ __forceinline__ void tc_mma_ss(uint32_t tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(tmem),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t a, uint32_t *v) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
+          "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
+          "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(a));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t a, const uint32_t *v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(a),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
+        "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
+        "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+        : "memory");
+}
+// (the loaded registers pass through, so that no use of them moves up)
+__device__ __forceinline__ void tmem_wait_ld(uint32_t *v) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]), "+r"(v[8]),
+                   "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]), "+r"(v[16]),
+                   "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]), "+r"(v[24]),
+                   "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]), "+r"(v[30]), "+r"(v[31])
+                 :
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    const __half2 r = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+template <int D>
+struct Shape {
+    static constexpr int TILES = D == 256 ? 1 : 2;       // row tiles of a CTA
+    static constexpr int BN = D == 256 ? 64 : 128;       // keys of a step
+    static constexpr int STAGES = 2;
+    static constexpr int Q_BYTES = ROWS * D * 2;         // one tile; chunks of 64 columns, 16 KB each
+    static constexpr int K_BYTES = BN * D * 2;
+    static constexpr int V_BYTES = D * BN * 2;
+    static constexpr int O_TMEM = 256;                   // S (then P) of tile i at 128 i, O at 256 + D i
+    static constexpr int OFF_K = TILES * Q_BYTES;
+    static constexpr int OFF_V = OFF_K + STAGES * K_BYTES;
+    static constexpr int OFF_SCALE = OFF_V + STAGES * V_BYTES;   // a row's factor
+    static constexpr int OFF_BAR = OFF_SCALE + TILES * ROWS * 4;
+    // q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2], done
+    static constexpr int N_BARS = 1 + 4 * STAGES + 3 * 2 + 1;
+    static constexpr int SMEM = OFF_BAR + 8 * N_BARS + 16 + 1024;
+    static constexpr int THREADS = (4 * TILES + 2) * 32;
+    static_assert(SMEM <= 227 * 1024, "shared memory");
+    static_assert(O_TMEM + TILES * D <= 512, "tensor memory");
+};
+
+template <int D>
+__global__ void __launch_bounds__(Shape<D>::THREADS, 1) attn_prefill_kernel(const __grid_constant__ PrefillArgs p) {
+    using Z = Shape<D>;
+    constexpr int BN = Z::BN, TILES = Z::TILES, NB = D / 32;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ int64_t where[2];   // sequence, tile in it
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    const uint32_t sbase = smem_u32(smem);
+    const uint32_t q_full = sbase + Z::OFF_BAR, k_full = q_full + 8, k_empty = k_full + 16, v_full = k_empty + 16,
+                   v_empty = v_full + 16, s_full = v_empty + 16, p_full = s_full + 16, o_full = p_full + 16,
+                   done = o_full + 16;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + Z::OFF_BAR + 8 * Z::N_BARS);
+    float *factor = reinterpret_cast<float *>(smem + Z::OFF_SCALE);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int TMA_WARP = 4 * TILES, MMA_WARP = TMA_WARP + 1;
+
+    if (threadIdx.x == 0) {
+        where[0] = -1;
+        mbar_init(q_full, TILES * ROWS);
+        for (int s = 0; s < 2; s++) {
+            mbar_init(k_full + 8 * s, 1);
+            mbar_init(k_empty + 8 * s, 1);
+            mbar_init(v_full + 8 * s, 1);
+            mbar_init(v_empty + 8 * s, 1);
+            mbar_init(s_full + 8 * s, 1);
+            mbar_init(p_full + 8 * s, ROWS);
+            mbar_init(o_full + 8 * s, 1);
+        }
+        mbar_init(done, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncthreads();
+    pdl_trigger();
+    pdl_wait();
+    // Which rows: tiles are counted from the last sequence's last (a causal tile sees the more keys the later it is, and
+    // the long ones go first), heads side by side.
+    const int h = blockIdx.x % p.c.Hkv, live = live_rows(p.live, p.B);
+    constexpr int CTA_ROWS = TILES * ROWS;
+    {
+        int64_t skip = blockIdx.x / p.c.Hkv;
+        if (warp == 0) {
+            for (int hi = live; hi > 0; hi -= 32) {
+                const int b = hi - 1 - lane;
+                const int64_t n = b >= 0 ? ((int64_t)span_of(p, b).n * p.G + CTA_ROWS - 1) / CTA_ROWS : 0;
+                int64_t x = n;
+#pragma unroll
+                for (int m = 1; m < 32; m <<= 1) {
+                    const int64_t y = __shfl_up_sync(FULL, x, m);
+                    if (lane >= m) x += y;
+                }
+                if (skip < x && skip >= x - n) {
+                    where[0] = b;
+                    where[1] = n - 1 - (skip - (x - n));
+                }
+                const int64_t sum = __shfl_sync(FULL, x, 31);
+                if (skip < sum) break;
+                skip -= sum;
+            }
+        }
+    }
+    __syncthreads();
+    const int b = (int)where[0];
+    if (b < 0) return;
+    const Span1 sq = span_of(p, b);
+    const int64_t row0 = where[1] * CTA_ROWS;                       // of the sequence's n * G rows
+    const int64_t row_last = min(row0 + CTA_ROWS, (int64_t)sq.n * p.G) - 1;
+    // keys that any of the rows sees, from a step's beginning
+    const int end = sq.len - sq.n + (int)(row_last / p.G) + 1;
+    int begin = 0;
+    if (p.a.window > 0) begin = max(0, sq.len - sq.n + (int)(row0 / p.G) + 1 - p.a.window) / BN * BN;
+    const int steps = end > begin ? (end - begin + BN - 1) / BN : 0;
+
+    if (warp == MMA_WARP) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_slot))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const int64_t seg = (int64_t)b * p.c.Hkv + h;
+
+    if (warp == TMA_WARP) {   // ---------------- copies
+        if (lane == 0) {
+            int j = 0;
+            for (; j < steps; j++) {
+                const uint32_t s = j % 2, par = (j / 2 - 1) & 1u;
+                const int kv = begin + j * BN;
+                if (j >= 2 && !mbar_wait(k_empty + 8 * s, par)) break;
+                mbar_expect_tx(k_full + 8 * s, Z::K_BYTES);
+                for (int x = 0; x < D / 64; x++)
+                    tma_2d(sbase + Z::OFF_K + s * Z::K_BYTES + x * BN * 128, &p.kmap, 64 * x, (int)(seg * p.lpad) + kv,
+                           k_full + 8 * s);
+                if (j >= 2 && !mbar_wait(v_empty + 8 * s, par)) {
+                    mbar_wait(k_full + 8 * s, (j / 2) & 1u);
+                    break;
+                }
+                mbar_expect_tx(v_full + 8 * s, Z::V_BYTES);
+                for (int x = 0; x < BN / 64; x++)
+                    tma_2d(sbase + Z::OFF_V + s * Z::V_BYTES + x * D * 128, &p.vmap, kv + 64 * x, (int)(seg * D),
+                           v_full + 8 * s);
+            }
+            // every copy has landed before the CTA can go, also after a wait ran out
+            for (int x = j > 2 ? j - 2 : 0; x < j; x++)
+                if (!mbar_wait(k_full + 8 * (x % 2), (x / 2) & 1u) || !mbar_wait(v_full + 8 * (x % 2), (x / 2) & 1u)) break;
+        }
+    } else if (warp == MMA_WARP) {   // ---------------- products
+        if (lane == 0) {
+            bool ok = steps > 0 && mbar_wait(q_full, 0);
+            const auto scores = [&](int i, int j) {   // S of tile i, step j
+                const uint32_t qa = sbase + i * Z::Q_BYTES, ka = sbase + Z::OFF_K + (j % 2) * Z::K_BYTES;
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ks++)
+                    tc_mma_ss(tmem + 128 * i, sdesc(qa + (ks >> 2) * ROWS * 128 + 32 * (ks & 3)),
+                              sdesc(ka + (ks >> 2) * BN * 128 + 32 * (ks & 3)), mma_idesc(BN), ks != 0);
+                tc_commit(s_full + 8 * i);
+            };
+            const auto outputs = [&](int i, int j) {
+                const uint32_t va = sbase + Z::OFF_V + (j % 2) * Z::V_BYTES;
+#pragma unroll
+                for (int ks = 0; ks < BN / 16; ks++)
+                    tc_mma(tmem + Z::O_TMEM + D * i, tmem + 128 * i + 8 * ks, sdesc(va + (ks >> 2) * D * 128 + 32 * (ks & 3)),
+                           mma_idesc(D), (j | ks) != 0);
+            };
+            if (ok) {
+                tc_fence_after();
+                ok = mbar_wait(k_full, 0);
+                if (ok) {
+                    tc_fence_after();
+#pragma unroll
+                    for (int i = 0; i < TILES; i++) scores(i, 0);
+                    tc_commit(k_empty);
+                }
+            }
+            for (int j = 0; j < steps && ok; j++) {
+                ok = mbar_wait(v_full + 8 * (j % 2), (j / 2) & 1u);
+                if (ok && j + 1 < steps) ok = mbar_wait(k_full + 8 * ((j + 1) % 2), ((j + 1) / 2) & 1u);
+                if (!ok) break;
+#pragma unroll
+                for (int i = 0; i < TILES; i++) {
+                    if (ok) ok = mbar_wait(p_full + 8 * i, j & 1u);
+                    if (!ok) break;
+                    tc_fence_after();
+                    outputs(i, j);
+                    if (j + 1 < steps)
+                        scores(i, j + 1);
+                    else
+                        tc_commit(o_full + 8 * i);
+                }
+                if (!ok) break;
+                tc_commit(v_empty + 8 * (j % 2));
+                if (j + 1 < steps) tc_commit(k_empty + 8 * ((j + 1) % 2));
+            }
+            tc_commit(done);   // no product is under way when the tensor memory is freed
+            mbar_wait(done, 0);
+        }
+    } else {   // ---------------- a thread a row
+        const int i = warp / 4, quad = warp & 3, r = 32 * quad + lane;
+        const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
+        const uint32_t st = lanes + 128 * i, ot = lanes + Z::O_TMEM + D * i;
+        // queries: a row a warp and turn, its power of two taken out, in the layout of a K-major operand
+        if (steps > 0) {
+#pragma unroll 4
+            for (int x = 0; x < 32; x++) {
+                const int64_t rho = row0 + i * ROWS + 32 * quad + x;
+                const bool there = rho < (int64_t)sq.n * p.G;
+                float4 v[(NB + 3) / 4];
+                float top = 0.0f;
+                const int token = there ? (int)(rho / p.G) : 0, head = h * p.G + (there ? (int)(rho % p.G) : 0);
+                const int64_t at = (int64_t)(sq.first + token) * p.a.q_stride + (int64_t)head * D;
+#pragma unroll
+                for (int e = 0; e < (NB + 3) / 4; e++) {
+                    const int col = 128 * e + 4 * lane;
+                    v[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    if (there && col < D)
+                        v[e] = p.a.q_elem == QK_ELEM_F32
+                                   ? load_row4(static_cast<const float *>(p.a.q) + at + col, p.q_wide)
+                                   : load_row4(static_cast<const __nv_bfloat16 *>(p.a.q) + at + col, p.q_wide);
+                    top = fmaxf(top, fmaxf(fmaxf(fabsf(v[e].x), fabsf(v[e].y)), fmaxf(fabsf(v[e].z), fabsf(v[e].w))));
+                }
+#pragma unroll
+                for (int m = 16; m; m >>= 1) top = fmaxf(top, __shfl_xor_sync(FULL, top, m));
+                // 2^e2 is above the largest magnitude; its inverse stays a normal number
+                const int e2 = min(max((int)(__float_as_uint(top) >> 23) - 126, -100), 100), row = 32 * quad + x;
+                const float down = __uint_as_float((uint32_t)(127 - e2) << 23);
+                if (lane == 0) factor[i * ROWS + row] = fmaxf(p.a.scale * LOG2E * __uint_as_float((uint32_t)(127 + e2) << 23), 0x1p-126f);
+#pragma unroll
+                for (int e = 0; e < (NB + 3) / 4; e++) {
+                    const int col = 128 * e + 4 * lane;
+                    if (col < D) {
+                        const uint32_t off = (col / 64) * ROWS * 128 + row * 128 + (((col % 64 / 8) ^ (row & 7)) << 4) + (col % 8) * 2;
+                        *reinterpret_cast<uint2 *>(smem + i * Z::Q_BYTES + off) =
+                            make_uint2(pack2(v[e].x * down, v[e].y * down), pack2(v[e].z * down, v[e].w * down));
+                    }
+                }
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            mbar_arrive(q_full);
+        }
+        const int64_t rho = row0 + i * ROWS + r;
+        const bool there = rho < (int64_t)sq.n * p.G;
+        const int token = there ? (int)(rho / p.G) : sq.n - 1, head = h * p.G + (there ? (int)(rho % p.G) : 0);
+        const int my_end = sq.len - sq.n + token + 1, my_begin = p.a.window > 0 ? max(0, my_end - p.a.window) : 0;
+        const float c = steps > 0 ? factor[i * ROWS + r] : 0.0f;
+        float ref = -INFINITY, off = 0.0f, sum = 0.0f;
+        bool ok = true;
+        for (int j = 0; j < steps && ok; j++) {
+            const int kv = begin + j * BN;
+            ok = __all_sync(FULL, mbar_wait(s_full + 8 * i, j & 1u));
+            if (!ok) break;
+            tc_fence_after();
+            uint32_t sv[BN];
+#pragma unroll
+            for (int x = 0; x < BN; x += 32) tmem_ld32(st + x, sv + x);
+            // the step's groups whose page exists
+            uint32_t groups = 0;
+            const uint8_t *t8 = p.there + (int64_t)b * (p.lpad / GROUP) + kv / GROUP;
+            const uint32_t a0 = ld_prev(reinterpret_cast<const uint32_t *>(t8));
+            const uint32_t a1 = BN == 128 ? ld_prev(reinterpret_cast<const uint32_t *>(t8 + 4)) : 0x01010101u;
+#pragma unroll
+            for (int x = 0; x < BN; x += 32) tmem_wait_ld(sv + x);
+            const bool part = kv + BN > my_end || kv < my_begin || (a0 & a1) != 0x01010101u;
+            if (__any_sync(FULL, part)) {
+                groups = (a0 & 1) | (a0 >> 7 & 2) | (a0 >> 14 & 4) | (a0 >> 21 & 8) | (a1 & 1) << 4 | (a1 >> 7 & 2) << 4 |
+                         (a1 >> 14 & 4) << 4 | (a1 >> 21 & 8) << 4;
+#pragma unroll
+                for (int x = 0; x < BN; x++) {
+                    const int key = kv + x / 16 * 16 + x % 16 / 4 * 2 + x % 2 + x % 4 / 2 * 8;
+                    if (key >= my_end || key < my_begin || !(groups >> (x / 16) & 1)) sv[x] = 0xff800000u;
+                }
+            }
+            float top = -INFINITY;
+#pragma unroll
+            for (int x = 0; x < BN; x += 2) top = fmaxf(top, fmaxf(__uint_as_float(sv[x]), __uint_as_float(sv[x + 1])));
+            top = top == -INFINITY ? top : top * c;
+            const bool move = top - ref > HEADROOM;
+            if (__any_sync(FULL, move)) {
+                const float now = move ? top : ref;
+                const float down = ref == -INFINITY ? 0.0f : ex2(ref - now);
+                if (j > 0) {   // the step before has been added: its products came before these scores
+#pragma unroll 1
+                    for (int x = 0; x < D; x += 32) {
+                        uint32_t v[32];
+                        tmem_ld32(ot + x, v);
+                        tmem_wait_ld(v);
+#pragma unroll
+                        for (int y = 0; y < 32; y++) v[y] = __float_as_uint(__uint_as_float(v[y]) * down);
+                        tmem_st32(ot + x, v);
+                    }
+                }
+                sum *= down;
+                ref = now;
+                // a little above the maximum for huge logits, whose products with c round
+                off = now == -INFINITY ? 0.0f : fmaf(fabsf(now), 0x1p-22f, now) - LIFT;
+            }
+            float part_sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int x0 = 0; x0 < BN; x0 += 64) {
+                uint32_t w[32];
+#pragma unroll
+                for (int x = 0; x < 64; x += 2) {
+                    const float s0 = __uint_as_float(sv[x0 + x]), s1 = __uint_as_float(sv[x0 + x + 1]);
+                    const float p0 = ex2(fmaf(s0, c, -off)), p1 = ex2(fmaf(s1, c, -off));
+                    part_sum[x / 2 % 4] += p0 + p1;
+                    w[x / 2] = pack2(p0, p1);
+                }
+                tmem_st32(st + x0 / 2, w);
+            }
+            sum += (part_sum[0] + part_sum[1]) + (part_sum[2] + part_sum[3]);
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(p_full + 8 * i);
+        }
+        // outputs
+        if (ok && steps > 0) ok = __all_sync(FULL, mbar_wait(o_full + 8 * i, 0));
+        tc_fence_after();
+        if (p.a.sinks) {
+            const float sink = ld_prev(p.a.sinks + head) * LOG2E;
+            // the weights' unit is 2^off; a sink far above it takes all
+            const float lead = ref == -INFINITY ? sink : fmaxf(sink, off);
+            const float down = ref == -INFINITY ? 0.0f : ex2(off - lead);
+            const float total = sink == -INFINITY ? sum * down : fmaf(sum, down, ex2(sink - lead));
+            sum = down > 0.0f ? total / down : 0.0f;
+        }
+        const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+        const int64_t row = sq.first + token;
+#pragma unroll 1
+        for (int k = 0; k < NB; k++) {
+            float y[32];
+            if (steps > 0) {
+                uint32_t v[32];
+                tmem_ld32(ot + 32 * k, v);
+                tmem_wait_ld(v);
+#pragma unroll
+                for (int x = 0; x < 32; x++) y[x] = inv > 0.0f ? __uint_as_float(v[x]) * inv : 0.0f;
+            } else {
+#pragma unroll
+                for (int x = 0; x < 32; x++) y[x] = 0.0f;
+            }
+            if (there && ok) {
+                const int64_t at = row * p.a.out_stride + (int64_t)head * D + 32 * k;
+                if (p.a.out && p.a.out_elem == QK_ELEM_F32) {
+#pragma unroll
+                    for (int x = 0; x < 32; x += 4)
+                        store_row4(static_cast<float *>(p.a.out) + at + x, make_float4(y[x], y[x + 1], y[x + 2], y[x + 3]), p.out_wide);
+                } else if (p.a.out) {
+#pragma unroll
+                    for (int x = 0; x < 32; x += 4)
+                        store_row4(static_cast<__nv_bfloat16 *>(p.a.out) + at + x, make_float4(y[x], y[x + 1], y[x + 2], y[x + 3]),
+                                   p.out_wide);
+                }
+                if (p.qs) {
+                    float m = 0.0f;
+#pragma unroll
+                    for (int x = 0; x < 32; x++) m = fmaxf(m, fabsf(y[x]));
+                    const float d = m / 127.0f;
+                    const int64_t block = row * p.row_blocks + head * NB + k;
+                    uint32_t w[8];
+#pragma unroll
+                    for (int x = 0; x < 32; x++) {
+                        const int code = m != 0.0f ? __float2int_rn(y[x] / d) : 0;
+                        w[x / 4] = x % 4 ? w[x / 4] | (uint32_t)(code & 255) << (8 * (x % 4)) : (uint32_t)(code & 255);
+                    }
+                    uint4 *to = reinterpret_cast<uint4 *>(p.qs + block * QB);
+                    to[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                    to[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                    p.d[block] = __half_as_ushort(__float2half_rn(d));
+                }
+            }
+            __syncwarp();   // whole warps load from tensor memory
+        }
+        if (p.qs && there && ok && head == p.a.n_heads - 1)   // the blocks behind the heads
+            for (int64_t block = row * p.row_blocks + p.a.n_heads * NB; block < (row + 1) * p.row_blocks; block++) {
+                reinterpret_cast<uint4 *>(p.qs + block * QB)[0] = make_uint4(0, 0, 0, 0);
+                reinterpret_cast<uint4 *>(p.qs + block * QB)[1] = make_uint4(0, 0, 0, 0);
+                p.d[block] = 0;
+            }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == MMA_WARP)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+
+struct Staged {
+    int64_t lpad, k, v, there, bytes;
+};
+Staged staged_of(int Hkv, int D, int64_t B, int64_t max_kv) {
+    Staged l;
+    l.lpad = ceil_div(max_kv, PAD) * PAD;
+    l.k = 0;
+    l.v = l.k + B * Hkv * l.lpad * D * 2;
+    l.there = l.v + B * Hkv * l.lpad * D * 2;
+    l.bytes = l.there + ceil_div(B * l.lpad / GROUP, 128) * 128;
+    return l;
+}
+
+template <int D>
+qk_status launch_tc(PrefillArgs &p, const Staged &l, cudaStream_t s) {
+    using Z = Shape<D>;
+    static bool ready[64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return fail(QK_ERR_CUDA, "attn_prefill: no device");
+    if (!ready[dev]) {
+        const cudaError_t e =
+            cudaFuncSetAttribute(attn_prefill_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Z::SMEM);
+        if (e != cudaSuccess) return fail(QK_ERR_CUDA, "attn_prefill: %s", cudaGetErrorString(e));
+        ready[dev] = true;
+    }
+    const auto encode = tensor_map_encoder();
+    if (!encode) return fail(QK_ERR_CUDA, "attn_prefill: cuTensorMapEncodeTiled is not available");
+    const auto map = [&](CUtensorMap *m, void *base, int64_t cols, int64_t rows, int box_rows) {
+        const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, pitch[1] = {(cuuint64_t)cols * 2};
+        const cuuint32_t box[2] = {64, (cuuint32_t)box_rows}, step[2] = {1, 1};
+        return encode(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, base, dims, pitch, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                      CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    };
+    const int64_t segs = (int64_t)p.B * p.c.Hkv;
+    if (map(&p.kmap, p.k, D, segs * l.lpad, Z::BN) != CUDA_SUCCESS || map(&p.vmap, p.v, l.lpad, segs * D, D) != CUDA_SUCCESS)
+        return fail(QK_ERR_CUDA, "attn_prefill: tensor map encoding failed");
+    const qk_status st = launch_pdl("attn_stage", attn_stage_kernel<D>, dim3((unsigned)(l.lpad / 64), p.c.Hkv, p.B), dim3(128),
+                                    0, s, p);
+    if (st != QK_OK) return st;
+    // tiles of any split of the rows into B sequences
+    const int64_t tiles = ceil_div((int64_t)p.rows * p.G, Z::TILES * ROWS) + std::min(p.B, p.rows);
+    return launch_pdl("attn_prefill", attn_prefill_kernel<D>, dim3((unsigned)(tiles * p.c.Hkv)), dim3(Z::THREADS),
+                      (size_t)Z::SMEM, s, p);
 }
 
 }  // namespace
 
-int64_t attn_prefill_workspace_bytes(int, int, int64_t, int64_t) { return 128; }
+int64_t attn_prefill_workspace_bytes(int Hkv, int D, int64_t B, int64_t max_kv) { return staged_of(Hkv, D, B, max_kv).bytes; }
 
 qk_status launch_attn_prefill(const KvCache &c, const qk_attn &a, int B, int rows, const int32_t *q_offsets, int max_kv,
-                              int8_t *qs, uint16_t *d, int64_t row_blocks, const int32_t *live, void *, cudaStream_t s) {
-    return launch_rows(c, a, {B, 0, rows, max_kv, q_offsets}, {nullptr, qs, d, row_blocks}, live, s);
+                              int8_t *qs, uint16_t *d, int64_t row_blocks, const int32_t *live, void *ws, cudaStream_t s) {
+    const Staged l = staged_of(c.Hkv, c.D, B, max_kv);
+    uint8_t *w = static_cast<uint8_t *>(ws);
+    PrefillArgs p = {};
+    p.c = c;
+    p.a = a;
+    p.B = B;
+    p.rows = rows;
+    p.G = a.n_heads / c.Hkv;
+    p.max_kv = max_kv;
+    p.lpad = (int)l.lpad;
+    p.offsets = q_offsets;
+    p.live = live;
+    p.k = reinterpret_cast<__half *>(w + l.k);
+    p.v = reinterpret_cast<__half *>(w + l.v);
+    p.there = w + l.there;
+    p.qs = qs;
+    p.d = d;
+    p.row_blocks = row_blocks;
+    p.q_wide = row_wide(a.q, a.q_stride, a.q_elem);
+    p.out_wide = a.out && row_wide(a.out, a.out_stride, a.out_elem);
+    return c.D == 64 ? launch_tc<64>(p, l, s) : c.D == 128 ? launch_tc<128>(p, l, s) : launch_tc<256>(p, l, s);
+}
+
+qk_status read_attn_prefill_faults(uint32_t *faults) {
+    unsigned int v = 0, zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(&v, g_tc_faults, sizeof v);
+    if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_tc_faults, &zero, sizeof zero);
+    if (e != cudaSuccess) return fail(QK_ERR_CUDA, "qk_device_faults: %s", cudaGetErrorString(e));
+    *faults = v;
+    return QK_OK;
 }
 
 }  // namespace qk

@@ -396,13 +396,14 @@ size_t qk_mmvq_workspace_bytes(int32_t n_proj, const qk_proj *projs) {
 
 qk_status qk_device_faults(uint32_t *faults) {
     REQUIRE(faults, QK_ERR_ARG, "faults is null");
-    uint32_t a = 0, b = 0, c = 0, d = 0, e = 0;
+    uint32_t a = 0, b = 0, c = 0, d = 0, e = 0, f = 0;
     qk_status st = read_device_faults(&a);
     if (st == QK_OK) st = read_mmq_faults(&b);
     if (st == QK_OK) st = read_mmq_id_faults(&c);
     if (st == QK_OK) st = read_mmvq_g_faults(&d);
     if (st == QK_OK) st = read_attn_decode_faults(&e);
-    *faults = a | b | c | d | e;
+    if (st == QK_OK) st = read_attn_prefill_faults(&f);
+    *faults = a | b | c | d | e | f;
     return st;
 }
 
@@ -916,6 +917,10 @@ qk_status qk_attn_prefill(const qk_kv_cache *cache, const qk_attn *attn, int64_t
             "misaligned pointer (qs must be 16-byte, d 4-byte aligned)");
     if (B == 0 || rows == 0) return QK_OK;
     REQUIRE(q_offsets, QK_ERR_ARG, "q_offsets is null");
+    // rows of the staged keys and values are counted in int, and so are the CTAs
+    REQUIRE(B * cache->n_kv_heads * (max_kv + 127) < (1LL << 31) && B * cache->n_kv_heads * cache->head_dim < (1LL << 31) &&
+                rows * attn->n_heads / 128 + (B + 1) * cache->n_kv_heads < (1LL << 31),
+            QK_ERR_UNSUPPORTED, "B * n_kv_heads * max_kv or rows * n_heads too large for one launch");
     const size_t need = qk_attn_prefill_workspace_bytes(cache, B, max_kv);
     REQUIRE(ws && aligned(ws, 128), QK_ERR_WORKSPACE, "workspace null or not 128-byte aligned");
     REQUIRE(ws_bytes >= need, QK_ERR_WORKSPACE, "workspace %zu < %zu bytes", ws_bytes, need);
