@@ -40,7 +40,7 @@ struct PrefillArgs {
     int8_t *qs;
     uint16_t *d;
     int64_t row_blocks;
-    bool q_wide, out_wide;
+    bool q_wide, out_wide, out16;   // out16: bfloat16 rows start on 16-byte boundaries
 };
 
 // Rows and keys of a sequence.
@@ -163,6 +163,13 @@ __device__ __forceinline__ void tmem_st32(uint32_t a, const uint32_t *v) {
         "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
         : "memory");
 }
+__device__ __forceinline__ void tmem_st16(uint32_t a, const uint32_t *v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(a),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
 // (the loaded registers pass through, so that no use of them moves up)
 __device__ __forceinline__ void tmem_wait_ld(uint32_t *v) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
@@ -179,8 +186,34 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
+// two binary32 operations in one instruction
+__device__ __forceinline__ uint64_t two(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 apart(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     const __half2 r = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+    const __nv_bfloat162 r = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&r);
 }
 
@@ -197,8 +230,8 @@ struct Shape {
     static constexpr int OFF_V = OFF_K + STAGES * K_BYTES;
     static constexpr int OFF_SCALE = OFF_V + STAGES * V_BYTES;   // a row's factor
     static constexpr int OFF_BAR = OFF_SCALE + TILES * ROWS * 4;
-    // q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2], done
-    static constexpr int N_BARS = 1 + 4 * STAGES + 3 * 2 + 1;
+    // q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_half[2], p_full[2], o_full[2], done
+    static constexpr int N_BARS = 1 + 4 * STAGES + 4 * 2 + 1;
     static constexpr int SMEM = OFF_BAR + 8 * N_BARS + 16 + 1024;
     static constexpr int THREADS = (4 * TILES + 2) * 32;
     static_assert(SMEM <= 227 * 1024, "shared memory");
@@ -214,8 +247,8 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) attn_prefill_kernel(cons
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     const uint32_t sbase = smem_u32(smem);
     const uint32_t q_full = sbase + Z::OFF_BAR, k_full = q_full + 8, k_empty = k_full + 16, v_full = k_empty + 16,
-                   v_empty = v_full + 16, s_full = v_empty + 16, p_full = s_full + 16, o_full = p_full + 16,
-                   done = o_full + 16;
+                   v_empty = v_full + 16, s_full = v_empty + 16, p_half = s_full + 16, p_full = p_half + 16,
+                   o_full = p_full + 16, done = o_full + 16;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + Z::OFF_BAR + 8 * Z::N_BARS);
     float *factor = reinterpret_cast<float *>(smem + Z::OFF_SCALE);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -230,6 +263,7 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) attn_prefill_kernel(cons
             mbar_init(v_full + 8 * s, 1);
             mbar_init(v_empty + 8 * s, 1);
             mbar_init(s_full + 8 * s, 1);
+            mbar_init(p_half + 8 * s, ROWS);
             mbar_init(p_full + 8 * s, ROWS);
             mbar_init(o_full + 8 * s, 1);
         }
@@ -269,12 +303,12 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) attn_prefill_kernel(cons
     const int b = (int)where[0];
     if (b < 0) return;
     const Span1 sq = span_of(p, b);
-    const int64_t row0 = where[1] * CTA_ROWS;                       // of the sequence's n * G rows
-    const int64_t row_last = min(row0 + CTA_ROWS, (int64_t)sq.n * p.G) - 1;
+    const int rows_all = sq.n * p.G, row0 = (int)where[1] * CTA_ROWS;   // of the sequence's n * G rows
+    const int row_last = min(row0 + CTA_ROWS, rows_all) - 1;
     // keys that any of the rows sees, from a step's beginning
-    const int end = sq.len - sq.n + (int)(row_last / p.G) + 1;
+    const int end = sq.len - sq.n + row_last / p.G + 1;
     int begin = 0;
-    if (p.a.window > 0) begin = max(0, sq.len - sq.n + (int)(row0 / p.G) + 1 - p.a.window) / BN * BN;
+    if (p.a.window > 0) begin = max(0, sq.len - sq.n + row0 / p.G + 1 - p.a.window) / BN * BN;
     const int steps = end > begin ? (end - begin + BN - 1) / BN : 0;
 
     if (warp == MMA_WARP) {
@@ -289,7 +323,7 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) attn_prefill_kernel(cons
     const int64_t seg = (int64_t)b * p.c.Hkv + h;
 
     if (warp == TMA_WARP) {   // ---------------- copies
-        if (lane == 0) {
+        if (elect_one()) {
             int j = 0;
             for (; j < steps; j++) {
                 const uint32_t s = j % 2, par = (j / 2 - 1) & 1u;
@@ -313,7 +347,7 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) attn_prefill_kernel(cons
                 if (!mbar_wait(k_full + 8 * (x % 2), (x / 2) & 1u) || !mbar_wait(v_full + 8 * (x % 2), (x / 2) & 1u)) break;
         }
     } else if (warp == MMA_WARP) {   // ---------------- products
-        if (lane == 0) {
+        if (elect_one()) {
             bool ok = steps > 0 && mbar_wait(q_full, 0);
             const auto scores = [&](int i, int j) {   // S of tile i, step j
                 const uint32_t qa = sbase + i * Z::Q_BYTES, ka = sbase + Z::OFF_K + (j % 2) * Z::K_BYTES;
@@ -323,10 +357,10 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) attn_prefill_kernel(cons
                               sdesc(ka + (ks >> 2) * BN * 128 + 32 * (ks & 3)), mma_idesc(BN), ks != 0);
                 tc_commit(s_full + 8 * i);
             };
-            const auto outputs = [&](int i, int j) {
+            const auto outputs = [&](int i, int j, int half) {
                 const uint32_t va = sbase + Z::OFF_V + (j % 2) * Z::V_BYTES;
 #pragma unroll
-                for (int ks = 0; ks < BN / 16; ks++)
+                for (int ks = half * BN / 32; ks < (half + 1) * BN / 32; ks++)
                     tc_mma(tmem + Z::O_TMEM + D * i, tmem + 128 * i + 8 * ks, sdesc(va + (ks >> 2) * D * 128 + 32 * (ks & 3)),
                            mma_idesc(D), (j | ks) != 0);
             };
@@ -346,10 +380,14 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) attn_prefill_kernel(cons
                 if (!ok) break;
 #pragma unroll
                 for (int i = 0; i < TILES; i++) {
-                    if (ok) ok = mbar_wait(p_full + 8 * i, j & 1u);
+                    if (ok) ok = mbar_wait(p_half + 8 * i, j & 1u);
                     if (!ok) break;
                     tc_fence_after();
-                    outputs(i, j);
+                    outputs(i, j, 0);
+                    ok = mbar_wait(p_full + 8 * i, j & 1u);
+                    if (!ok) break;
+                    tc_fence_after();
+                    outputs(i, j, 1);
                     if (j + 1 < steps)
                         scores(i, j + 1);
                     else
@@ -366,49 +404,56 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) attn_prefill_kernel(cons
         const int i = warp / 4, quad = warp & 3, r = 32 * quad + lane;
         const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
         const uint32_t st = lanes + 128 * i, ot = lanes + Z::O_TMEM + D * i;
-        // queries: a row a warp and turn, its power of two taken out, in the layout of a K-major operand
+        // queries: eight rows a warp and turn, four lanes a row, its power of two taken out, in the layout of a K-major
+        // operand
         if (steps > 0) {
-#pragma unroll 4
-            for (int x = 0; x < 32; x++) {
-                const int64_t rho = row0 + i * ROWS + 32 * quad + x;
-                const bool there = rho < (int64_t)sq.n * p.G;
-                float4 v[(NB + 3) / 4];
+            const int part = lane & 3;
+#pragma unroll 2
+            for (int x = 0; x < 4; x++) {
+                const int row = 32 * quad + 8 * x + (lane >> 2), rho = row0 + i * ROWS + row;
+                const bool there = rho < rows_all;
+                const int token = there ? rho / p.G : 0, head = h * p.G + (there ? rho - token * p.G : 0);
+                const int64_t at = (int64_t)(sq.first + token) * p.a.q_stride + (int64_t)head * D + 8 * part;
+                float4 v[D / 32][2];
                 float top = 0.0f;
-                const int token = there ? (int)(rho / p.G) : 0, head = h * p.G + (there ? (int)(rho % p.G) : 0);
-                const int64_t at = (int64_t)(sq.first + token) * p.a.q_stride + (int64_t)head * D;
 #pragma unroll
-                for (int e = 0; e < (NB + 3) / 4; e++) {
-                    const int col = 128 * e + 4 * lane;
-                    v[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    if (there && col < D)
-                        v[e] = p.a.q_elem == QK_ELEM_F32
-                                   ? load_row4(static_cast<const float *>(p.a.q) + at + col, p.q_wide)
-                                   : load_row4(static_cast<const __nv_bfloat16 *>(p.a.q) + at + col, p.q_wide);
-                    top = fmaxf(top, fmaxf(fmaxf(fabsf(v[e].x), fabsf(v[e].y)), fmaxf(fabsf(v[e].z), fabsf(v[e].w))));
-                }
+                for (int e = 0; e < D / 32; e++)
 #pragma unroll
-                for (int m = 16; m; m >>= 1) top = fmaxf(top, __shfl_xor_sync(FULL, top, m));
-                // 2^e2 is above the largest magnitude; its inverse stays a normal number
-                const int e2 = min(max((int)(__float_as_uint(top) >> 23) - 126, -100), 100), row = 32 * quad + x;
-                const float down = __uint_as_float((uint32_t)(127 - e2) << 23);
-                if (lane == 0) factor[i * ROWS + row] = fmaxf(p.a.scale * LOG2E * __uint_as_float((uint32_t)(127 + e2) << 23), 0x1p-126f);
-#pragma unroll
-                for (int e = 0; e < (NB + 3) / 4; e++) {
-                    const int col = 128 * e + 4 * lane;
-                    if (col < D) {
-                        const uint32_t off = (col / 64) * ROWS * 128 + row * 128 + (((col % 64 / 8) ^ (row & 7)) << 4) + (col % 8) * 2;
-                        *reinterpret_cast<uint2 *>(smem + i * Z::Q_BYTES + off) =
-                            make_uint2(pack2(v[e].x * down, v[e].y * down), pack2(v[e].z * down, v[e].w * down));
+                    for (int f = 0; f < 2; f++) {
+                        const int64_t o = at + 32 * e + 4 * f;
+                        v[e][f] = p.a.q_elem == QK_ELEM_F32 ? load_row4(static_cast<const float *>(p.a.q) + o, p.q_wide)
+                                                            : load_row4(static_cast<const __nv_bfloat16 *>(p.a.q) + o, p.q_wide);
                     }
+#pragma unroll
+                for (int e = 0; e < D / 32; e++)
+#pragma unroll
+                    for (int f = 0; f < 2; f++) {
+                        if (!there) v[e][f] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        top = fmaxf(top, fmaxf(fmaxf(fabsf(v[e][f].x), fabsf(v[e][f].y)), fmaxf(fabsf(v[e][f].z), fabsf(v[e][f].w))));
+                    }
+                top = fmaxf(top, __shfl_xor_sync(FULL, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(FULL, top, 2));
+                // 2^e2 is above the largest magnitude; its inverse stays a normal number
+                const int e2 = min(max((int)(__float_as_uint(top) >> 23) - 126, -100), 100);
+                const float down = __uint_as_float((uint32_t)(127 - e2) << 23);
+                if (part == 0)
+                    factor[i * ROWS + row] = fmaxf(p.a.scale * LOG2E * __uint_as_float((uint32_t)(127 + e2) << 23), 0x1p-126f);
+#pragma unroll
+                for (int e = 0; e < D / 32; e++) {
+                    const int unit = 4 * e + part;   // of 8 columns
+                    const float4 a = v[e][0], c = v[e][1];
+                    *reinterpret_cast<uint4 *>(smem + i * Z::Q_BYTES + (unit / 8) * ROWS * 128 + row * 128 + (((unit & 7) ^ (row & 7)) << 4)) =
+                        make_uint4(pack2(a.x * down, a.y * down), pack2(a.z * down, a.w * down), pack2(c.x * down, c.y * down),
+                                   pack2(c.z * down, c.w * down));
                 }
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             mbar_arrive(q_full);
         }
-        const int64_t rho = row0 + i * ROWS + r;
-        const bool there = rho < (int64_t)sq.n * p.G;
-        const int token = there ? (int)(rho / p.G) : sq.n - 1, head = h * p.G + (there ? (int)(rho % p.G) : 0);
+        const int rho = row0 + i * ROWS + r;
+        const bool there = rho < rows_all;
+        const int token = there ? rho / p.G : sq.n - 1, head = h * p.G + (there ? rho - token * p.G : 0);
         const int my_end = sq.len - sq.n + token + 1, my_begin = p.a.window > 0 ? max(0, my_end - p.a.window) : 0;
         const float c = steps > 0 ? factor[i * ROWS + r] : 0.0f;
         float ref = -INFINITY, off = 0.0f, sum = 0.0f;
@@ -438,9 +483,17 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) attn_prefill_kernel(cons
                     if (key >= my_end || key < my_begin || !(groups >> (x / 16) & 1)) sv[x] = 0xff800000u;
                 }
             }
-            float top = -INFINITY;
+            float tops[8];
 #pragma unroll
-            for (int x = 0; x < BN; x += 2) top = fmaxf(top, fmaxf(__uint_as_float(sv[x]), __uint_as_float(sv[x + 1])));
+            for (int x = 0; x < 8; x++) tops[x] = __uint_as_float(sv[x]);
+#pragma unroll
+            for (int x = 8; x < BN; x += 16)
+#pragma unroll
+                for (int y = 0; y < 8; y++)
+                    tops[y] = x + 8 < BN ? fmaxf(fmaxf(tops[y], __uint_as_float(sv[x + y])), __uint_as_float(sv[x + 8 + y]))
+                                         : fmaxf(tops[y], __uint_as_float(sv[x + y]));
+            float top = fmaxf(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])),
+                              fmaxf(fmaxf(tops[4], tops[5]), fmaxf(tops[6], tops[7])));
             top = top == -INFINITY ? top : top * c;
             const bool move = top - ref > HEADROOM;
             if (__any_sync(FULL, move)) {
@@ -462,20 +515,27 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) attn_prefill_kernel(cons
                 // a little above the maximum for huge logits, whose products with c round
                 off = now == -INFINITY ? 0.0f : fmaf(fabsf(now), 0x1p-22f, now) - LIFT;
             }
-            float part_sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            uint64_t sums[4] = {0, 0, 0, 0};
+            const uint64_t c2 = two(c, c), off2 = two(-off, -off);
 #pragma unroll
-            for (int x0 = 0; x0 < BN; x0 += 64) {
-                uint32_t w[32];
+            for (int x0 = 0; x0 < BN; x0 += 32) {
+                uint32_t w[16];
 #pragma unroll
-                for (int x = 0; x < 64; x += 2) {
-                    const float s0 = __uint_as_float(sv[x0 + x]), s1 = __uint_as_float(sv[x0 + x + 1]);
-                    const float p0 = ex2(fmaf(s0, c, -off)), p1 = ex2(fmaf(s1, c, -off));
-                    part_sum[x / 2 % 4] += p0 + p1;
+                for (int x = 0; x < 32; x += 2) {
+                    const float2 e = apart(fma2(two(__uint_as_float(sv[x0 + x]), __uint_as_float(sv[x0 + x + 1])), c2, off2));
+                    const float p0 = ex2(e.x), p1 = ex2(e.y);
+                    sums[x / 2 % 4] = add2(sums[x / 2 % 4], two(p0, p1));
                     w[x / 2] = pack2(p0, p1);
                 }
-                tmem_st32(st + x0 / 2, w);
+                tmem_st16(st + x0 / 2, w);
+                if (x0 + 32 == BN / 2) {   // the first half of the products can begin
+                    tmem_wait_st();
+                    tc_fence_before();
+                    mbar_arrive(p_half + 8 * i);
+                }
             }
-            sum += (part_sum[0] + part_sum[1]) + (part_sum[2] + part_sum[3]);
+            const float2 all = apart(add2(add2(sums[0], sums[1]), add2(sums[2], sums[3])));
+            sum += all.x + all.y;
             tmem_wait_st();
             tc_fence_before();
             mbar_arrive(p_full + 8 * i);
@@ -514,20 +574,32 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) attn_prefill_kernel(cons
                         store_row4(static_cast<float *>(p.a.out) + at + x, make_float4(y[x], y[x + 1], y[x + 2], y[x + 3]), p.out_wide);
                 } else if (p.a.out) {
 #pragma unroll
-                    for (int x = 0; x < 32; x += 4)
-                        store_row4(static_cast<__nv_bfloat16 *>(p.a.out) + at + x, make_float4(y[x], y[x + 1], y[x + 2], y[x + 3]),
-                                   p.out_wide);
+                    for (int x = 0; x < 32; x += 8) {
+                        __nv_bfloat16 *to = static_cast<__nv_bfloat16 *>(p.a.out) + at + x;
+                        if (p.out16) {
+                            *reinterpret_cast<uint4 *>(to) = make_uint4(bf16x2(y[x], y[x + 1]), bf16x2(y[x + 2], y[x + 3]),
+                                                                        bf16x2(y[x + 4], y[x + 5]), bf16x2(y[x + 6], y[x + 7]));
+                        } else {
+                            store_row4(to, make_float4(y[x], y[x + 1], y[x + 2], y[x + 3]), p.out_wide);
+                            store_row4(to + 4, make_float4(y[x + 4], y[x + 5], y[x + 6], y[x + 7]), p.out_wide);
+                        }
+                    }
                 }
                 if (p.qs) {
                     float m = 0.0f;
 #pragma unroll
                     for (int x = 0; x < 32; x++) m = fmaxf(m, fabsf(y[x]));
-                    const float d = m / 127.0f;
+                    const float d = m / 127.0f, r = 1.0f / d;
                     const int64_t block = row * p.row_blocks + head * NB + k;
                     uint32_t w[8];
 #pragma unroll
                     for (int x = 0; x < 32; x++) {
-                        const int code = m != 0.0f ? __float2int_rn(y[x] / d) : 0;
+                        // rint(y / d): the product with 1 / d is within 127 * 2^-22 of the quotient, so a division next
+                        // to ties alone
+                        const float z = y[x] * r;
+                        float code_f = rintf(z);
+                        if (fabsf(fabsf(z - code_f) - 0.5f) < 1e-4f || m < 0x1p-100f) code_f = rintf(y[x] / d);
+                        const int code = m != 0.0f ? (int)code_f : 0;
                         w[x / 4] = x % 4 ? w[x / 4] | (uint32_t)(code & 255) << (8 * (x % 4)) : (uint32_t)(code & 255);
                     }
                     uint4 *to = reinterpret_cast<uint4 *>(p.qs + block * QB);
@@ -622,6 +694,7 @@ qk_status launch_attn_prefill(const KvCache &c, const qk_attn &a, int B, int row
     p.d = d;
     p.row_blocks = row_blocks;
     p.q_wide = row_wide(a.q, a.q_stride, a.q_elem);
+    p.out16 = a.out && reinterpret_cast<uintptr_t>(a.out) % 16 == 0 && a.out_stride % 8 == 0;
     p.out_wide = a.out && row_wide(a.out, a.out_stride, a.out_elem);
     return c.D == 64 ? launch_tc<64>(p, l, s) : c.D == 128 ? launch_tc<128>(p, l, s) : launch_tc<256>(p, l, s);
 }

@@ -173,14 +173,6 @@ __device__ __forceinline__ int pair_at(const IdArgs &a, int64_t pos) {
     return p >= 0 && p < a.pairs ? p : -1;
 }
 
-// One lane of a converged warp. Tensor copies, MMAs and commits take their operands from uniform
-// registers: under elect.sync the compiler issues them directly (an MMA about 17 cycles), under a
-// test of the lane number in a loop over the lanes (about 150).
-__device__ __forceinline__ bool elect_one() {
-    uint32_t p;
-    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
-    return p != 0;
-}
 // Whether the phase is complete, without waiting.
 __device__ __forceinline__ bool mbar_test(uint32_t a, uint32_t parity) {
     uint32_t ok;

@@ -919,7 +919,7 @@ qk_status qk_attn_prefill(const qk_kv_cache *cache, const qk_attn *attn, int64_t
     REQUIRE(q_offsets, QK_ERR_ARG, "q_offsets is null");
     // rows of the staged keys and values are counted in int, and so are the CTAs
     REQUIRE(B * cache->n_kv_heads * (max_kv + 127) < (1LL << 31) && B * cache->n_kv_heads * cache->head_dim < (1LL << 31) &&
-                rows * attn->n_heads / 128 + (B + 1) * cache->n_kv_heads < (1LL << 31),
+                (rows + 256 * B) * attn->n_heads < (1LL << 31),
             QK_ERR_UNSUPPORTED, "B * n_kv_heads * max_kv or rows * n_heads too large for one launch");
     const size_t need = qk_attn_prefill_workspace_bytes(cache, B, max_kv);
     REQUIRE(ws && aligned(ws, 128), QK_ERR_WORKSPACE, "workspace null or not 128-byte aligned");

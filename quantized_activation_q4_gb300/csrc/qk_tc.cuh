@@ -73,6 +73,14 @@ __device__ __forceinline__ void tc_mma(uint32_t tmem, uint32_t a_tmem, uint64_t 
         "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate)
         : "memory");
 }
+// One lane of a converged warp. Tensor copies, MMAs and commits take their operands from uniform
+// registers: under elect.sync the compiler issues them directly (an MMA about 17 cycles), under a
+// test of the lane number in a loop over the lanes (about 150).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+    return p != 0;
+}
 __device__ __forceinline__ void tc_commit(uint32_t mbar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(mbar)
                  : "memory");
