@@ -135,13 +135,42 @@ __global__ void __launch_bounds__(128) attn_stage_kernel(const __grid_constant__
 }
 
 // ---------------------------------------------------------------- attention
-// D (tensor memory) (+)= A (shared memory) x B (shared memory)
-__device__ __forceinline__ void tc_mma_ss(uint32_t tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// Products with K-major operands in shared memory, 128-byte swizzle (sdesc): the descriptors' low words plus a constant,
+// put together where they are used (held ready as 64-bit words they cost the kernel its registers).
+__device__ __forceinline__ uint32_t sdesc_low(uint32_t addr) { return ((addr & 0x3FFFFu) >> 4) | (1u << 16); }
+constexpr uint32_t SDESC_HIGH = (1024u >> 4) | (1u << 14) | (2u << 29);
+template <int A, int B>   // D (tensor memory) (+)= A (shared memory) x B (shared memory), A and B bytes further on
+__device__ __forceinline__ void mma_ss(uint32_t tmem, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(tmem),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        "{\n .reg .pred p;\n .reg .b32 x, y;\n .reg .b64 da, db;\n setp.ne.u32 p, %4, 0;\n"
+        " add.u32 x, %1, %5;\n add.u32 y, %2, %6;\n mov.b64 da, {x, %7};\n mov.b64 db, {y, %7};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n}\n" ::"r"(tmem),
+        "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(A >> 4), "n"(B >> 4), "n"(SDESC_HIGH)
         : "memory");
+}
+template <int A, int B>   // the same with A in tensor memory, A columns further on
+__device__ __forceinline__ void mma_ts(uint32_t tmem, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n .reg .pred p;\n .reg .b32 x, y;\n .reg .b64 db;\n setp.ne.u32 p, %4, 0;\n"
+        " add.u32 x, %1, %5;\n add.u32 y, %2, %6;\n mov.b64 db, {y, %7};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [x], db, %3, p;\n}\n" ::"r"(tmem),
+        "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(A), "n"(B >> 4), "n"(SDESC_HIGH)
+        : "memory");
+}
+// K = 16 * N of S = Q K^T from step KS on; of O += P V
+template <int D, int BN, int KS, int N>
+__device__ __forceinline__ void mma_scores(uint32_t tmem, uint32_t q, uint32_t k) {
+    if constexpr (N > 0) {
+        mma_ss<(KS >> 2) * ROWS * 128 + 32 * (KS & 3), (KS >> 2) * BN * 128 + 32 * (KS & 3)>(tmem, q, k, mma_idesc(BN), KS != 0);
+        mma_scores<D, BN, KS + 1, N - 1>(tmem, q, k);
+    }
+}
+template <int D, int KS, int N>
+__device__ __forceinline__ void mma_outputs(uint32_t tmem, uint32_t p, uint32_t v, uint32_t accumulate) {
+    if constexpr (N > 0) {
+        mma_ts<8 * KS, (KS >> 2) * D * 128 + 32 * (KS & 3)>(tmem, p, v, mma_idesc(D), accumulate);
+        mma_outputs<D, KS + 1, N - 1>(tmem, p, v, 1);
+    }
 }
 __device__ __forceinline__ void tmem_ld32(uint32_t a, uint32_t *v) {
     asm volatile(
@@ -153,22 +182,16 @@ __device__ __forceinline__ void tmem_ld32(uint32_t a, uint32_t *v) {
           "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
         : "r"(a));
 }
-__device__ __forceinline__ void tmem_st32(uint32_t a, const uint32_t *v) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
-        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(a),
-        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
-        "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
-        "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
-        : "memory");
+__device__ __forceinline__ void tmem_ld8(uint32_t a, uint32_t *v) {   // waits
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n tcgen05.wait::ld.sync.aligned;"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                 : "r"(a)
+                 : "memory");
 }
-__device__ __forceinline__ void tmem_st16(uint32_t a, const uint32_t *v) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(a),
-        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
-        : "memory");
+__device__ __forceinline__ void tmem_st8(uint32_t a, const uint32_t *v) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(a), "r"(v[0]), "r"(v[1]),
+                 "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
 }
 // (the loaded registers pass through, so that no use of them moves up)
 __device__ __forceinline__ void tmem_wait_ld(uint32_t *v) {
@@ -229,11 +252,12 @@ struct Shape {
     static constexpr int OFF_K = TILES * Q_BYTES;
     static constexpr int OFF_V = OFF_K + STAGES * K_BYTES;
     static constexpr int OFF_SCALE = OFF_V + STAGES * V_BYTES;   // a row's factor
-    static constexpr int OFF_BAR = OFF_SCALE + TILES * ROWS * 4;
+    static constexpr int OFF_TOP = OFF_SCALE + TILES * ROWS * 4;   // the two halves' maxima, two steps
+    static constexpr int OFF_BAR = OFF_TOP + TILES * 2 * 2 * ROWS * 4;
     // q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_half[2], p_full[2], o_full[2], done
     static constexpr int N_BARS = 1 + 4 * STAGES + 4 * 2 + 1;
     static constexpr int SMEM = OFF_BAR + 8 * N_BARS + 16 + 1024;
-    static constexpr int THREADS = (4 * TILES + 2) * 32;
+    static constexpr int THREADS = (8 * TILES + 2) * 32;   // two threads a row, a warp for copies, one for products
     static_assert(SMEM <= 227 * 1024, "shared memory");
     static_assert(O_TMEM + TILES * D <= 512, "tensor memory");
 };
@@ -252,18 +276,18 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) attn_prefill_kernel(cons
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + Z::OFF_BAR + 8 * Z::N_BARS);
     float *factor = reinterpret_cast<float *>(smem + Z::OFF_SCALE);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    constexpr int TMA_WARP = 4 * TILES, MMA_WARP = TMA_WARP + 1;
+    constexpr int TMA_WARP = 8 * TILES, MMA_WARP = TMA_WARP + 1, HALF = BN / 2;
 
     if (threadIdx.x == 0) {
         where[0] = -1;
-        mbar_init(q_full, TILES * ROWS);
+        mbar_init(q_full, TILES * 2 * ROWS);
         for (int s = 0; s < 2; s++) {
             mbar_init(k_full + 8 * s, 1);
             mbar_init(k_empty + 8 * s, 1);
             mbar_init(v_full + 8 * s, 1);
             mbar_init(v_empty + 8 * s, 1);
             mbar_init(s_full + 8 * s, 1);
-            mbar_init(p_half + 8 * s, ROWS);
+            mbar_init(p_half + 8 * s, ROWS);   // the weights of a step's first and second half
             mbar_init(p_full + 8 * s, ROWS);
             mbar_init(o_full + 8 * s, 1);
         }
@@ -349,20 +373,10 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) attn_prefill_kernel(cons
     } else if (warp == MMA_WARP) {   // ---------------- products
         if (elect_one()) {
             bool ok = steps > 0 && mbar_wait(q_full, 0);
+            const uint32_t q0 = sdesc_low(sbase), k0 = sdesc_low(sbase + Z::OFF_K), v0 = sdesc_low(sbase + Z::OFF_V);
             const auto scores = [&](int i, int j) {   // S of tile i, step j
-                const uint32_t qa = sbase + i * Z::Q_BYTES, ka = sbase + Z::OFF_K + (j % 2) * Z::K_BYTES;
-#pragma unroll
-                for (int ks = 0; ks < D / 16; ks++)
-                    tc_mma_ss(tmem + 128 * i, sdesc(qa + (ks >> 2) * ROWS * 128 + 32 * (ks & 3)),
-                              sdesc(ka + (ks >> 2) * BN * 128 + 32 * (ks & 3)), mma_idesc(BN), ks != 0);
+                mma_scores<D, BN, 0, D / 16>(tmem + 128 * i, q0 + i * (Z::Q_BYTES >> 4), k0 + (j % 2) * (Z::K_BYTES >> 4));
                 tc_commit(s_full + 8 * i);
-            };
-            const auto outputs = [&](int i, int j, int half) {
-                const uint32_t va = sbase + Z::OFF_V + (j % 2) * Z::V_BYTES;
-#pragma unroll
-                for (int ks = half * BN / 32; ks < (half + 1) * BN / 32; ks++)
-                    tc_mma(tmem + Z::O_TMEM + D * i, tmem + 128 * i + 8 * ks, sdesc(va + (ks >> 2) * D * 128 + 32 * (ks & 3)),
-                           mma_idesc(D), (j | ks) != 0);
             };
             if (ok) {
                 tc_fence_after();
@@ -383,11 +397,11 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) attn_prefill_kernel(cons
                     if (ok) ok = mbar_wait(p_half + 8 * i, j & 1u);
                     if (!ok) break;
                     tc_fence_after();
-                    outputs(i, j, 0);
+                    mma_outputs<D, 0, BN / 32>(tmem + Z::O_TMEM + D * i, tmem + 128 * i, v0 + (j % 2) * (Z::V_BYTES >> 4), j != 0);
                     ok = mbar_wait(p_full + 8 * i, j & 1u);
                     if (!ok) break;
                     tc_fence_after();
-                    outputs(i, j, 1);
+                    mma_outputs<D, BN / 32, BN / 32>(tmem + Z::O_TMEM + D * i, tmem + 128 * i, v0 + (j % 2) * (Z::V_BYTES >> 4), 1);
                     if (j + 1 < steps)
                         scores(i, j + 1);
                     else
@@ -400,17 +414,17 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) attn_prefill_kernel(cons
             tc_commit(done);   // no product is under way when the tensor memory is freed
             mbar_wait(done, 0);
         }
-    } else {   // ---------------- a thread a row
-        const int i = warp / 4, quad = warp & 3, r = 32 * quad + lane;
+    } else if (warp < TMA_WARP) {   // ---------------- two threads a row, a half of a step's keys each
+        const int i = warp / 8, quad = warp & 3, hf = warp / 4 % 2, r = 32 * quad + lane;
         const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
         const uint32_t st = lanes + 128 * i, ot = lanes + Z::O_TMEM + D * i;
         // queries: eight rows a warp and turn, four lanes a row, its power of two taken out, in the layout of a K-major
         // operand
         if (steps > 0) {
             const int part = lane & 3;
-#pragma unroll 2
-            for (int x = 0; x < 4; x++) {
-                const int row = 32 * quad + 8 * x + (lane >> 2), rho = row0 + i * ROWS + row;
+#pragma unroll 1
+            for (int x = 0; x < 2; x++) {
+                const int row = 32 * quad + 16 * hf + 8 * x + (lane >> 2), rho = row0 + i * ROWS + row;
                 const bool there = rho < rows_all;
                 const int token = there ? rho / p.G : 0, head = h * p.G + (there ? rho - token * p.G : 0);
                 const int64_t at = (int64_t)(sq.first + token) * p.a.q_stride + (int64_t)head * D + 8 * part;
@@ -448,9 +462,13 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) attn_prefill_kernel(cons
                 }
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
             mbar_arrive(q_full);
         }
+        // the 256 threads of a tile meet
+        const auto meet = [&]() { asm volatile("bar.sync %0, 256;" ::"r"(1 + i) : "memory"); };
+        meet();   // the factors are written
+        float *const mine = reinterpret_cast<float *>(smem + Z::OFF_TOP) + (i * 2 + hf) * 2 * ROWS + r;
+        const float *const other = reinterpret_cast<float *>(smem + Z::OFF_TOP) + (i * 2 + 1 - hf) * 2 * ROWS + r;
         const int rho = row0 + i * ROWS + r;
         const bool there = rho < rows_all;
         const int token = there ? rho / p.G : sq.n - 1, head = h * p.G + (there ? rho - token * p.G : 0);
@@ -458,56 +476,59 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) attn_prefill_kernel(cons
         const float c = steps > 0 ? factor[i * ROWS + r] : 0.0f;
         float ref = -INFINITY, off = 0.0f, sum = 0.0f;
         bool ok = true;
-        for (int j = 0; j < steps && ok; j++) {
-            const int kv = begin + j * BN;
-            ok = __all_sync(FULL, mbar_wait(s_full + 8 * i, j & 1u));
-            if (!ok) break;
+        for (int j = 0; j < steps; j++) {   // (a wait that ran out goes on without work: both halves meet in every step)
+            const int kv = begin + j * BN + hf * HALF;
+            if (ok) ok = __all_sync(FULL, mbar_wait(s_full + 8 * i, j & 1u));
             tc_fence_after();
-            uint32_t sv[BN];
+            uint32_t sv[HALF];
+            // whether the pages of the keys exist, a byte a group
+            const uint8_t *there16 = p.there + (int64_t)b * (p.lpad / GROUP) + kv / GROUP;
+            const uint32_t exist = HALF == 64 ? ld_prev(reinterpret_cast<const uint32_t *>(there16))
+                                              : ld_prev(reinterpret_cast<const uint16_t *>(there16)) | 0x01010000u;
 #pragma unroll
-            for (int x = 0; x < BN; x += 32) tmem_ld32(st + x, sv + x);
-            // the step's groups whose page exists
-            uint32_t groups = 0;
-            const uint8_t *t8 = p.there + (int64_t)b * (p.lpad / GROUP) + kv / GROUP;
-            const uint32_t a0 = ld_prev(reinterpret_cast<const uint32_t *>(t8));
-            const uint32_t a1 = BN == 128 ? ld_prev(reinterpret_cast<const uint32_t *>(t8 + 4)) : 0x01010101u;
+            for (int x = 0; x < HALF; x += 32) tmem_ld32(st + hf * HALF + x, sv + x);
 #pragma unroll
-            for (int x = 0; x < BN; x += 32) tmem_wait_ld(sv + x);
-            const bool part = kv + BN > my_end || kv < my_begin || (a0 & a1) != 0x01010101u;
+            for (int x = 0; x < HALF; x += 32) tmem_wait_ld(sv + x);
+            const bool part = kv + HALF > my_end || kv < my_begin || exist != 0x01010101u;
             if (__any_sync(FULL, part)) {
-                groups = (a0 & 1) | (a0 >> 7 & 2) | (a0 >> 14 & 4) | (a0 >> 21 & 8) | (a1 & 1) << 4 | (a1 >> 7 & 2) << 4 |
-                         (a1 >> 14 & 4) << 4 | (a1 >> 21 & 8) << 4;
 #pragma unroll
-                for (int x = 0; x < BN; x++) {
+                for (int x = 0; x < HALF; x++) {
                     const int key = kv + x / 16 * 16 + x % 16 / 4 * 2 + x % 2 + x % 4 / 2 * 8;
-                    if (key >= my_end || key < my_begin || !(groups >> (x / 16) & 1)) sv[x] = 0xff800000u;
+                    if (key >= my_end || key < my_begin || !(exist >> (8 * (x / 16)) & 1)) sv[x] = 0xff800000u;
                 }
             }
             float tops[8];
 #pragma unroll
             for (int x = 0; x < 8; x++) tops[x] = __uint_as_float(sv[x]);
 #pragma unroll
-            for (int x = 8; x < BN; x += 16)
+            for (int x = 8; x < HALF; x += 16)
 #pragma unroll
                 for (int y = 0; y < 8; y++)
-                    tops[y] = x + 8 < BN ? fmaxf(fmaxf(tops[y], __uint_as_float(sv[x + y])), __uint_as_float(sv[x + 8 + y]))
-                                         : fmaxf(tops[y], __uint_as_float(sv[x + y]));
+                    tops[y] = x + 8 < HALF ? fmaxf(fmaxf(tops[y], __uint_as_float(sv[x + y])), __uint_as_float(sv[x + 8 + y]))
+                                           : fmaxf(tops[y], __uint_as_float(sv[x + y]));
             float top = fmaxf(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])),
                               fmaxf(fmaxf(tops[4], tops[5]), fmaxf(tops[6], tops[7])));
+            // the other half's maximum (where the weights go, the scores of both halves have been read)
+            mine[(j & 1) * ROWS] = top;
+            tc_fence_before();
+            meet();
+            tc_fence_after();
+            top = fmaxf(top, other[(j & 1) * ROWS]);
             top = top == -INFINITY ? top : top * c;
             const bool move = top - ref > HEADROOM;
             if (__any_sync(FULL, move)) {
                 const float now = move ? top : ref;
                 const float down = ref == -INFINITY ? 0.0f : ex2(ref - now);
-                if (j > 0) {   // the step before has been added: its products came before these scores
+                // the step before has been added: its products came before these scores. The first half's thread takes
+                // the whole row, since its weights start the next products
+                if (j > 0 && hf == 0) {
 #pragma unroll 1
-                    for (int x = 0; x < D; x += 32) {
-                        uint32_t v[32];
-                        tmem_ld32(ot + x, v);
-                        tmem_wait_ld(v);
+                    for (int x = 0; x < D; x += 8) {   // (few columns at once: the scores stay in registers)
+                        uint32_t v[8];
+                        tmem_ld8(ot + x, v);
 #pragma unroll
-                        for (int y = 0; y < 32; y++) v[y] = __float_as_uint(__uint_as_float(v[y]) * down);
-                        tmem_st32(ot + x, v);
+                        for (int y = 0; y < 8; y++) v[y] = __float_as_uint(__uint_as_float(v[y]) * down);
+                        tmem_st8(ot + x, v);
                     }
                 }
                 sum *= down;
@@ -515,32 +536,30 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) attn_prefill_kernel(cons
                 // a little above the maximum for huge logits, whose products with c round
                 off = now == -INFINITY ? 0.0f : fmaf(fabsf(now), 0x1p-22f, now) - LIFT;
             }
-            uint64_t sums[4] = {0, 0, 0, 0};
+            uint64_t sums[2] = {0, 0};
             const uint64_t c2 = two(c, c), off2 = two(-off, -off);
 #pragma unroll
-            for (int x0 = 0; x0 < BN; x0 += 32) {
-                uint32_t w[16];
+            for (int x0 = 0; x0 < HALF; x0 += 16) {
+                uint32_t w[8];
 #pragma unroll
-                for (int x = 0; x < 32; x += 2) {
+                for (int x = 0; x < 16; x += 2) {
                     const float2 e = apart(fma2(two(__uint_as_float(sv[x0 + x]), __uint_as_float(sv[x0 + x + 1])), c2, off2));
                     const float p0 = ex2(e.x), p1 = ex2(e.y);
-                    sums[x / 2 % 4] = add2(sums[x / 2 % 4], two(p0, p1));
+                    sums[x / 2 % 2] = add2(sums[x / 2 % 2], two(p0, p1));
                     w[x / 2] = pack2(p0, p1);
                 }
-                tmem_st16(st + x0 / 2, w);
-                if (x0 + 32 == BN / 2) {   // the first half of the products can begin
-                    tmem_wait_st();
-                    tc_fence_before();
-                    mbar_arrive(p_half + 8 * i);
-                }
+                tmem_st8(st + hf * (HALF / 2) + x0 / 2, w);
             }
-            const float2 all = apart(add2(add2(sums[0], sums[1]), add2(sums[2], sums[3])));
+            const float2 all = apart(add2(sums[0], sums[1]));
             sum += all.x + all.y;
             tmem_wait_st();
             tc_fence_before();
-            mbar_arrive(p_full + 8 * i);
+            mbar_arrive((hf ? p_full : p_half) + 8 * i);
         }
-        // outputs
+        // the row's sum, then its outputs: a half of the columns each
+        mine[(steps & 1) * ROWS] = sum;
+        meet();
+        sum += other[(steps & 1) * ROWS];
         if (ok && steps > 0) ok = __all_sync(FULL, mbar_wait(o_full + 8 * i, 0));
         tc_fence_after();
         if (p.a.sinks) {
@@ -554,7 +573,7 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) attn_prefill_kernel(cons
         const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
         const int64_t row = sq.first + token;
 #pragma unroll 1
-        for (int k = 0; k < NB; k++) {
+        for (int k = hf * NB / 2; k < (hf + 1) * NB / 2; k++) {
             float y[32];
             if (steps > 0) {
                 uint32_t v[32];
@@ -610,7 +629,7 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) attn_prefill_kernel(cons
             }
             __syncwarp();   // whole warps load from tensor memory
         }
-        if (p.qs && there && ok && head == p.a.n_heads - 1)   // the blocks behind the heads
+        if (p.qs && there && ok && hf && head == p.a.n_heads - 1)   // the blocks behind the heads
             for (int64_t block = row * p.row_blocks + p.a.n_heads * NB; block < (row + 1) * p.row_blocks; block++) {
                 reinterpret_cast<uint4 *>(p.qs + block * QB)[0] = make_uint4(0, 0, 0, 0);
                 reinterpret_cast<uint4 *>(p.qs + block * QB)[1] = make_uint4(0, 0, 0, 0);
