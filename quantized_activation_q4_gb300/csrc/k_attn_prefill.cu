@@ -41,6 +41,11 @@ struct PrefillArgs {
     uint16_t *d;
     int64_t row_blocks;
     bool q_wide, out_wide, out16;   // out16: bfloat16 rows start on 16-byte boundaries
+    // a tile's keys in `parts` shares of steps; with more than one, unnormalised outputs [CTA][row][D] and, for each
+    // row, the exponent of its weights' unit (minus infinity: no key) and their sum
+    int parts;
+    float *part_o;
+    float2 *part_ml;
 };
 
 // Rows and keys of a sequence.
@@ -54,6 +59,29 @@ __device__ __forceinline__ Span1 span_of(const PrefillArgs &p, int b) {
     s.len = min(max(ld_prev(p.a.kv_lens + b), 0), p.max_kv);
     s.base = p.a.window > 0 ? max(0, s.len - s.n + 1 - p.a.window) & ~(PAD - 1) : 0;
     return s;
+}
+
+// The tile of rows that a CTA takes: tiles are counted from the last sequence's last (a causal tile sees the more keys the
+// later it is, and the long ones go first). One warp looks; .x < 0: there are not so many.
+__device__ __forceinline__ int2 find_tile(const PrefillArgs &p, int64_t skip, int cta_rows) {
+    const int live = live_rows(p.live, p.B), lane = threadIdx.x & 31;
+    for (int hi = live; hi > 0; hi -= 32) {
+        const int b = hi - 1 - lane;
+        const int64_t n = b >= 0 ? ((int64_t)span_of(p, b).n * p.G + cta_rows - 1) / cta_rows : 0;
+        int64_t x = n;
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) {
+            const int64_t y = __shfl_up_sync(FULL, x, m);
+            if (lane >= m) x += y;
+        }
+        const uint32_t mine = __ballot_sync(FULL, skip < x && skip >= x - n);
+        if (mine) {
+            const int at = __ffs(mine) - 1, tile = (int)(n - 1 - (skip - (x - n)));
+            return make_int2(hi - 1 - at, __shfl_sync(FULL, tile, at));
+        }
+        skip -= __shfl_sync(FULL, x, 31);
+    }
+    return make_int2(-1, 0);
 }
 
 // ---------------------------------------------------------------- staging
@@ -267,7 +295,7 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) attn_prefill_kernel(cons
     using Z = Shape<D>;
     constexpr int BN = Z::BN, TILES = Z::TILES, NB = D / 32;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ int64_t where[2];   // sequence, tile in it
+    __shared__ int2 where;   // sequence, tile in it
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     const uint32_t sbase = smem_u32(smem);
     const uint32_t q_full = sbase + Z::OFF_BAR, k_full = q_full + 8, k_empty = k_full + 16, v_full = k_empty + 16,
@@ -279,7 +307,6 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) attn_prefill_kernel(cons
     constexpr int TMA_WARP = 8 * TILES, MMA_WARP = TMA_WARP + 1, HALF = BN / 2;
 
     if (threadIdx.x == 0) {
-        where[0] = -1;
         mbar_init(q_full, TILES * 2 * ROWS);
         for (int s = 0; s < 2; s++) {
             mbar_init(k_full + 8 * s, 1);
@@ -297,43 +324,28 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) attn_prefill_kernel(cons
     __syncthreads();
     pdl_trigger();
     pdl_wait();
-    // Which rows: tiles are counted from the last sequence's last (a causal tile sees the more keys the later it is, and
-    // the long ones go first), heads side by side.
-    const int h = blockIdx.x % p.c.Hkv, live = live_rows(p.live, p.B);
+    const int part = blockIdx.x % p.parts, h = blockIdx.x / p.parts % p.c.Hkv;
     constexpr int CTA_ROWS = TILES * ROWS;
-    {
-        int64_t skip = blockIdx.x / p.c.Hkv;
-        if (warp == 0) {
-            for (int hi = live; hi > 0; hi -= 32) {
-                const int b = hi - 1 - lane;
-                const int64_t n = b >= 0 ? ((int64_t)span_of(p, b).n * p.G + CTA_ROWS - 1) / CTA_ROWS : 0;
-                int64_t x = n;
-#pragma unroll
-                for (int m = 1; m < 32; m <<= 1) {
-                    const int64_t y = __shfl_up_sync(FULL, x, m);
-                    if (lane >= m) x += y;
-                }
-                if (skip < x && skip >= x - n) {
-                    where[0] = b;
-                    where[1] = n - 1 - (skip - (x - n));
-                }
-                const int64_t sum = __shfl_sync(FULL, x, 31);
-                if (skip < sum) break;
-                skip -= sum;
-            }
-        }
+    if (warp == 0) {
+        const int2 w = find_tile(p, blockIdx.x / p.parts / p.c.Hkv, CTA_ROWS);
+        if (lane == 0) where = w;
     }
     __syncthreads();
-    const int b = (int)where[0];
+    const int b = where.x;
     if (b < 0) return;
     const Span1 sq = span_of(p, b);
-    const int rows_all = sq.n * p.G, row0 = (int)where[1] * CTA_ROWS;   // of the sequence's n * G rows
+    const int rows_all = sq.n * p.G, row0 = where.y * CTA_ROWS;   // of the sequence's n * G rows
     const int row_last = min(row0 + CTA_ROWS, rows_all) - 1;
     // keys that any of the rows sees, from a step's beginning
     const int end = sq.len - sq.n + row_last / p.G + 1;
     int begin = 0;
     if (p.a.window > 0) begin = max(0, sq.len - sq.n + row0 / p.G + 1 - p.a.window) / BN * BN;
-    const int steps = end > begin ? (end - begin + BN - 1) / BN : 0;
+    int steps = end > begin ? (end - begin + BN - 1) / BN : 0;
+    if (p.parts > 1) {
+        const int from = (int)((int64_t)steps * part / p.parts), to = (int)((int64_t)steps * (part + 1) / p.parts);
+        begin += from * BN;
+        steps = to - from;
+    }
 
     if (warp == MMA_WARP) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_slot))
@@ -421,13 +433,13 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) attn_prefill_kernel(cons
         // queries: eight rows a warp and turn, four lanes a row, its power of two taken out, in the layout of a K-major
         // operand
         if (steps > 0) {
-            const int part = lane & 3;
+            const int unit0 = lane & 3;
 #pragma unroll 1
             for (int x = 0; x < 2; x++) {
                 const int row = 32 * quad + 16 * hf + 8 * x + (lane >> 2), rho = row0 + i * ROWS + row;
                 const bool there = rho < rows_all;
                 const int token = there ? rho / p.G : 0, head = h * p.G + (there ? rho - token * p.G : 0);
-                const int64_t at = (int64_t)(sq.first + token) * p.a.q_stride + (int64_t)head * D + 8 * part;
+                const int64_t at = (int64_t)(sq.first + token) * p.a.q_stride + (int64_t)head * D + 8 * unit0;
                 float4 v[D / 32][2];
                 float top = 0.0f;
 #pragma unroll
@@ -450,11 +462,11 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) attn_prefill_kernel(cons
                 // 2^e2 is above the largest magnitude; its inverse stays a normal number
                 const int e2 = min(max((int)(__float_as_uint(top) >> 23) - 126, -100), 100);
                 const float down = __uint_as_float((uint32_t)(127 - e2) << 23);
-                if (part == 0)
+                if (unit0 == 0)
                     factor[i * ROWS + row] = fmaxf(p.a.scale * LOG2E * __uint_as_float((uint32_t)(127 + e2) << 23), 0x1p-126f);
 #pragma unroll
                 for (int e = 0; e < D / 32; e++) {
-                    const int unit = 4 * e + part;   // of 8 columns
+                    const int unit = 4 * e + unit0;   // of 8 columns
                     const float4 a = v[e][0], c = v[e][1];
                     *reinterpret_cast<uint4 *>(smem + i * Z::Q_BYTES + (unit / 8) * ROWS * 128 + row * 128 + (((unit & 7) ^ (row & 7)) << 4)) =
                         make_uint4(pack2(a.x * down, a.y * down), pack2(a.z * down, a.w * down), pack2(c.x * down, c.y * down),
@@ -489,8 +501,8 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) attn_prefill_kernel(cons
             for (int x = 0; x < HALF; x += 32) tmem_ld32(st + hf * HALF + x, sv + x);
 #pragma unroll
             for (int x = 0; x < HALF; x += 32) tmem_wait_ld(sv + x);
-            const bool part = kv + HALF > my_end || kv < my_begin || exist != 0x01010101u;
-            if (__any_sync(FULL, part)) {
+            const bool hidden = kv + HALF > my_end || kv < my_begin || exist != 0x01010101u;
+            if (__any_sync(FULL, hidden)) {
 #pragma unroll
                 for (int x = 0; x < HALF; x++) {
                     const int key = kv + x / 16 * 16 + x % 16 / 4 * 2 + x % 2 + x % 4 / 2 * 8;
@@ -562,79 +574,96 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) attn_prefill_kernel(cons
         sum += other[(steps & 1) * ROWS];
         if (ok && steps > 0) ok = __all_sync(FULL, mbar_wait(o_full + 8 * i, 0));
         tc_fence_after();
-        if (p.a.sinks) {
-            const float sink = ld_prev(p.a.sinks + head) * LOG2E;
-            // the weights' unit is 2^off; a sink far above it takes all
-            const float lead = ref == -INFINITY ? sink : fmaxf(sink, off);
-            const float down = ref == -INFINITY ? 0.0f : ex2(off - lead);
-            const float total = sink == -INFINITY ? sum * down : fmaf(sum, down, ex2(sink - lead));
-            sum = down > 0.0f ? total / down : 0.0f;
-        }
-        const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-        const int64_t row = sq.first + token;
+        if (p.parts > 1) {   // what this share of the keys gives; attn_join_kernel goes on
+            const int64_t at = (int64_t)blockIdx.x * CTA_ROWS + i * ROWS + r;
+            if (hf == 0 && there && ok) p.part_ml[at] = make_float2(ref == -INFINITY ? -INFINITY : off, sum);
 #pragma unroll 1
-        for (int k = hf * NB / 2; k < (hf + 1) * NB / 2; k++) {
-            float y[32];
-            if (steps > 0) {
+            for (int k = hf * NB / 2; k < (hf + 1) * NB / 2 && steps > 0; k++) {
                 uint32_t v[32];
                 tmem_ld32(ot + 32 * k, v);
                 tmem_wait_ld(v);
+                if (there && ok) {
+                    uint4 *to = reinterpret_cast<uint4 *>(p.part_o + at * D + 32 * k);
 #pragma unroll
-                for (int x = 0; x < 32; x++) y[x] = inv > 0.0f ? __uint_as_float(v[x]) * inv : 0.0f;
-            } else {
-#pragma unroll
-                for (int x = 0; x < 32; x++) y[x] = 0.0f;
+                    for (int x = 0; x < 8; x++) to[x] = make_uint4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
+                }
+                __syncwarp();   // whole warps load from tensor memory
             }
-            if (there && ok) {
-                const int64_t at = row * p.a.out_stride + (int64_t)head * D + 32 * k;
-                if (p.a.out && p.a.out_elem == QK_ELEM_F32) {
+        } else {
+            if (p.a.sinks) {
+                const float sink = ld_prev(p.a.sinks + head) * LOG2E;
+                // the weights' unit is 2^off; a sink far above it takes all
+                const float lead = ref == -INFINITY ? sink : fmaxf(sink, off);
+                const float down = ref == -INFINITY ? 0.0f : ex2(off - lead);
+                const float total = sink == -INFINITY ? sum * down : fmaf(sum, down, ex2(sink - lead));
+                sum = down > 0.0f ? total / down : 0.0f;
+            }
+            const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+            const int64_t row = sq.first + token;
+#pragma unroll 1
+            for (int k = hf * NB / 2; k < (hf + 1) * NB / 2; k++) {
+                float y[32];
+                if (steps > 0) {
+                    uint32_t v[32];
+                    tmem_ld32(ot + 32 * k, v);
+                    tmem_wait_ld(v);
 #pragma unroll
-                    for (int x = 0; x < 32; x += 4)
-                        store_row4(static_cast<float *>(p.a.out) + at + x, make_float4(y[x], y[x + 1], y[x + 2], y[x + 3]), p.out_wide);
-                } else if (p.a.out) {
+                    for (int x = 0; x < 32; x++) y[x] = inv > 0.0f ? __uint_as_float(v[x]) * inv : 0.0f;
+                } else {
 #pragma unroll
-                    for (int x = 0; x < 32; x += 8) {
-                        __nv_bfloat16 *to = static_cast<__nv_bfloat16 *>(p.a.out) + at + x;
-                        if (p.out16) {
-                            *reinterpret_cast<uint4 *>(to) = make_uint4(bf16x2(y[x], y[x + 1]), bf16x2(y[x + 2], y[x + 3]),
-                                                                        bf16x2(y[x + 4], y[x + 5]), bf16x2(y[x + 6], y[x + 7]));
-                        } else {
-                            store_row4(to, make_float4(y[x], y[x + 1], y[x + 2], y[x + 3]), p.out_wide);
-                            store_row4(to + 4, make_float4(y[x + 4], y[x + 5], y[x + 6], y[x + 7]), p.out_wide);
+                    for (int x = 0; x < 32; x++) y[x] = 0.0f;
+                }
+                if (there && ok) {
+                    const int64_t at = row * p.a.out_stride + (int64_t)head * D + 32 * k;
+                    if (p.a.out && p.a.out_elem == QK_ELEM_F32) {
+#pragma unroll
+                        for (int x = 0; x < 32; x += 4)
+                            store_row4(static_cast<float *>(p.a.out) + at + x, make_float4(y[x], y[x + 1], y[x + 2], y[x + 3]), p.out_wide);
+                    } else if (p.a.out) {
+#pragma unroll
+                        for (int x = 0; x < 32; x += 8) {
+                            __nv_bfloat16 *to = static_cast<__nv_bfloat16 *>(p.a.out) + at + x;
+                            if (p.out16) {
+                                *reinterpret_cast<uint4 *>(to) = make_uint4(bf16x2(y[x], y[x + 1]), bf16x2(y[x + 2], y[x + 3]),
+                                                                            bf16x2(y[x + 4], y[x + 5]), bf16x2(y[x + 6], y[x + 7]));
+                            } else {
+                                store_row4(to, make_float4(y[x], y[x + 1], y[x + 2], y[x + 3]), p.out_wide);
+                                store_row4(to + 4, make_float4(y[x + 4], y[x + 5], y[x + 6], y[x + 7]), p.out_wide);
+                            }
                         }
                     }
-                }
-                if (p.qs) {
-                    float m = 0.0f;
+                    if (p.qs) {
+                        float m = 0.0f;
 #pragma unroll
-                    for (int x = 0; x < 32; x++) m = fmaxf(m, fabsf(y[x]));
-                    const float d = m / 127.0f, r = 1.0f / d;
-                    const int64_t block = row * p.row_blocks + head * NB + k;
-                    uint32_t w[8];
+                        for (int x = 0; x < 32; x++) m = fmaxf(m, fabsf(y[x]));
+                        const float d = m / 127.0f, r = 1.0f / d;
+                        const int64_t block = row * p.row_blocks + head * NB + k;
+                        uint32_t w[8];
 #pragma unroll
-                    for (int x = 0; x < 32; x++) {
-                        // rint(y / d): the product with 1 / d is within 127 * 2^-22 of the quotient, so a division next
-                        // to ties alone
-                        const float z = y[x] * r;
-                        float code_f = rintf(z);
-                        if (fabsf(fabsf(z - code_f) - 0.5f) < 1e-4f || m < 0x1p-100f) code_f = rintf(y[x] / d);
-                        const int code = m != 0.0f ? (int)code_f : 0;
-                        w[x / 4] = x % 4 ? w[x / 4] | (uint32_t)(code & 255) << (8 * (x % 4)) : (uint32_t)(code & 255);
+                        for (int x = 0; x < 32; x++) {
+                            // rint(y / d): the product with 1 / d is within 127 * 2^-22 of the quotient, so a division next
+                            // to ties alone
+                            const float z = y[x] * r;
+                            float code_f = rintf(z);
+                            if (fabsf(fabsf(z - code_f) - 0.5f) < 1e-4f || m < 0x1p-100f) code_f = rintf(y[x] / d);
+                            const int code = m != 0.0f ? (int)code_f : 0;
+                            w[x / 4] = x % 4 ? w[x / 4] | (uint32_t)(code & 255) << (8 * (x % 4)) : (uint32_t)(code & 255);
+                        }
+                        uint4 *to = reinterpret_cast<uint4 *>(p.qs + block * QB);
+                        to[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                        to[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                        p.d[block] = __half_as_ushort(__float2half_rn(d));
                     }
-                    uint4 *to = reinterpret_cast<uint4 *>(p.qs + block * QB);
-                    to[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                    to[1] = make_uint4(w[4], w[5], w[6], w[7]);
-                    p.d[block] = __half_as_ushort(__float2half_rn(d));
                 }
+                __syncwarp();   // whole warps load from tensor memory
             }
-            __syncwarp();   // whole warps load from tensor memory
+            if (p.qs && there && ok && hf && head == p.a.n_heads - 1)   // the blocks behind the heads
+                for (int64_t block = row * p.row_blocks + p.a.n_heads * NB; block < (row + 1) * p.row_blocks; block++) {
+                    reinterpret_cast<uint4 *>(p.qs + block * QB)[0] = make_uint4(0, 0, 0, 0);
+                    reinterpret_cast<uint4 *>(p.qs + block * QB)[1] = make_uint4(0, 0, 0, 0);
+                    p.d[block] = 0;
+                }
         }
-        if (p.qs && there && ok && hf && head == p.a.n_heads - 1)   // the blocks behind the heads
-            for (int64_t block = row * p.row_blocks + p.a.n_heads * NB; block < (row + 1) * p.row_blocks; block++) {
-                reinterpret_cast<uint4 *>(p.qs + block * QB)[0] = make_uint4(0, 0, 0, 0);
-                reinterpret_cast<uint4 *>(p.qs + block * QB)[1] = make_uint4(0, 0, 0, 0);
-                p.d[block] = 0;
-            }
     }
     tc_fence_before();
     __syncthreads();
@@ -643,8 +672,63 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) attn_prefill_kernel(cons
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
+// Tiles whose keys were shared out: one warp a row adds the shares in their order.
+template <int D>
+__global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ PrefillArgs p) {
+    constexpr int NB = D / 32, CTA_ROWS = Shape<D>::TILES * ROWS;
+    pdl_trigger();
+    pdl_wait();
+    const int2 w = find_tile(p, blockIdx.x / p.c.Hkv, CTA_ROWS);
+    if (w.x < 0) return;
+    const Span1 sq = span_of(p, w.x);
+    const int h = blockIdx.x % p.c.Hkv, lane = threadIdx.x & 31, r = blockIdx.y * 8 + (threadIdx.x >> 5);
+    const int rho = w.y * CTA_ROWS + r;
+    if (rho >= sq.n * p.G) return;
+    const int token = rho / p.G, head = h * p.G + rho % p.G;
+    float top = p.a.sinks ? ld_prev(p.a.sinks + head) * LOG2E : -INFINITY, o[NB];
+    float sum = top == -INFINITY ? 0.0f : 1.0f;
+#pragma unroll
+    for (int k = 0; k < NB; k++) o[k] = 0.0f;
+    for (int i = 0; i < p.parts; i++) {
+        const int64_t at = ((int64_t)blockIdx.x * p.parts + i) * CTA_ROWS + r;
+        const float m = ld_prev(&p.part_ml[at].x), v = ld_prev(&p.part_ml[at].y);
+        if (m == -INFINITY) continue;
+        const float now = fmaxf(top, m), old = top == -INFINITY ? 0.0f : ex2(top - now), f = ex2(m - now);
+        top = now;
+        sum = sum * old + v * f;
+#pragma unroll
+        for (int k = 0; k < NB; k++) o[k] = o[k] * old + ld_prev(p.part_o + at * D + 32 * k + lane) * f;
+    }
+    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+    const int64_t row = sq.first + token;
+#pragma unroll
+    for (int k = 0; k < NB; k++) {
+        const float y = o[k] * inv;
+        const int64_t to = row * p.a.out_stride + (int64_t)head * D + 32 * k + lane;
+        if (p.a.out && p.a.out_elem == QK_ELEM_F32) static_cast<float *>(p.a.out)[to] = y;
+        if (p.a.out && p.a.out_elem == QK_ELEM_BF16) static_cast<__nv_bfloat16 *>(p.a.out)[to] = __float2bfloat16_rn(y);
+        if (!p.qs) continue;
+        float m = fabsf(y);
+#pragma unroll
+        for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, x));
+        const float d = m / 127.0f;
+        const int64_t block = row * p.row_blocks + head * NB + k;
+        p.qs[block * QB + lane] = (int8_t)(m != 0.0f ? __float2int_rn(y / d) : 0);
+        if (lane == 0) p.d[block] = __half_as_ushort(__float2half_rn(d));
+    }
+    if (p.qs && head == p.a.n_heads - 1)   // the blocks behind the heads
+        for (int64_t block = row * p.row_blocks + p.a.n_heads * NB; block < (row + 1) * p.row_blocks; block++) {
+            p.qs[block * QB + lane] = 0;
+            if (lane == 0) p.d[block] = 0;
+        }
+}
+
+// Shares of keys are for calls with fewer tiles than the device has room for; PART_CTAS bounds their number and so the
+// workspace, and no call whose sequences are all shorter than PART_KEYS has any.
+constexpr int PART_CTAS = 640, PART_KEYS = 2048;
+
 struct Staged {
-    int64_t lpad, k, v, there, bytes;
+    int64_t lpad, k, v, there, part_o, part_ml, bytes;
 };
 Staged staged_of(int Hkv, int D, int64_t B, int64_t max_kv) {
     Staged l;
@@ -652,7 +736,10 @@ Staged staged_of(int Hkv, int D, int64_t B, int64_t max_kv) {
     l.k = 0;
     l.v = l.k + B * Hkv * l.lpad * D * 2;
     l.there = l.v + B * Hkv * l.lpad * D * 2;
-    l.bytes = l.there + ceil_div(B * l.lpad / GROUP, 128) * 128;
+    l.part_o = l.there + ceil_div(B * l.lpad / GROUP, 128) * 128;
+    const int64_t rows = max_kv < PART_KEYS ? 0 : (int64_t)PART_CTAS * ROWS * (D == 256 ? 1 : 2);
+    l.part_ml = l.part_o + rows * D * 4;
+    l.bytes = l.part_ml + rows * 8;
     return l;
 }
 
@@ -683,9 +770,22 @@ qk_status launch_tc(PrefillArgs &p, const Staged &l, cudaStream_t s) {
                                     0, s, p);
     if (st != QK_OK) return st;
     // tiles of any split of the rows into B sequences
-    const int64_t tiles = ceil_div((int64_t)p.rows * p.G, Z::TILES * ROWS) + std::min(p.B, p.rows);
-    return launch_pdl("attn_prefill", attn_prefill_kernel<D>, dim3((unsigned)(tiles * p.c.Hkv)), dim3(Z::THREADS),
-                      (size_t)Z::SMEM, s, p);
+    const int64_t tiles = (ceil_div((int64_t)p.rows * p.G, Z::TILES * ROWS) + std::min(p.B, p.rows) - 1) * p.c.Hkv;
+    // Shares of keys: so many that rounds of CTAs times (steps of a share + what a CTA spends around them, about 8 steps)
+    // is least, for keys as many as max_kv; a share is 4 steps at least.
+    p.parts = 1;
+    if (p.max_kv >= PART_KEYS) {
+        const int64_t steps = ceil_div(p.max_kv, Z::BN), sms = sm_count();
+        int64_t best = INT64_MAX;
+        for (int n = 1; n == 1 || (n * tiles <= PART_CTAS && n * 4 <= steps); n++) {
+            const int64_t cost = ceil_div(n * tiles, sms) * (ceil_div(steps, n) + 8 + (n > 1 ? 4 : 0));
+            if (cost < best) best = cost, p.parts = n;
+        }
+    }
+    const qk_status ran = launch_pdl("attn_prefill", attn_prefill_kernel<D>, dim3((unsigned)(tiles * p.parts)), dim3(Z::THREADS),
+                                     (size_t)Z::SMEM, s, p);
+    if (ran != QK_OK || p.parts == 1) return ran;
+    return launch_pdl("attn_join", attn_join_kernel<D>, dim3((unsigned)tiles, Z::TILES * ROWS / 8), dim3(256), 0, s, p);
 }
 
 }  // namespace
@@ -709,6 +809,8 @@ qk_status launch_attn_prefill(const KvCache &c, const qk_attn &a, int B, int row
     p.k = reinterpret_cast<__half *>(w + l.k);
     p.v = reinterpret_cast<__half *>(w + l.v);
     p.there = w + l.there;
+    p.part_o = reinterpret_cast<float *>(w + l.part_o);
+    p.part_ml = reinterpret_cast<float2 *>(w + l.part_ml);
     p.qs = qs;
     p.d = d;
     p.row_blocks = row_blocks;

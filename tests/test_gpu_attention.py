@@ -178,3 +178,24 @@ def test_same_call_same_bytes(call):
     a, b = (run_attention(geo, pages, table, lens, q, [T] * 5, "bf16", 0.1, 0, None, "f32", False, call)[0]
             for _ in range(2))
     assert np.array_equal(a, b)
+
+
+@pytest.mark.parametrize("D,Hkv,G,P", [(64, 2, 3, 64), (128, 1, 7, 16), (256, 1, 2, 128)])
+@pytest.mark.parametrize("window,sinks", [(0, False), (1500, True), (0, True)])
+def test_prefill_behind_a_long_past(D, Hkv, G, P, window, sinks):
+    """Few rows and many keys: the keys of a tile are shared out and joined again, some shares of them empty."""
+    rng = np.random.default_rng(D + window)
+    rows, past = [9, 70, 1, 3], [4000, 2300, 0, 100]
+    lens = [n + p for n, p in zip(rows, past)]
+    geo, pages, table = case(rng, D, Hkv, P, lens)
+    table[1, 3] = -1
+    q = queries(rng, sum(rows), Hkv * G, D, "bf16")
+    s = rng.normal(size=Hkv * G).astype(np.float32) * 3 if sinks else None
+    out, img = run_attention(geo, pages, table, lens, q, rows, "bf16", D ** -0.5, window, s, "f32", True, "prefill",
+                             spare_blocks=1)
+    want, parts = expected(geo, pages, table, lens, q, rows, D ** -0.5, window, s)
+    check(out, want, bound_of(parts, True), "f32")
+    image_is_of(img, out)
+    low, _ = run_attention(geo, pages, table, lens, q, rows, "bf16", D ** -0.5, window, s, "bf16", False, "prefill", live=3)
+    n = sum(rows[:3])
+    assert np.array_equal(low[:n], bf16(out[:n])) and np.isnan(low[n:]).all()
