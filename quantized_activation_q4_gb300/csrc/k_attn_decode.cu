@@ -89,17 +89,64 @@ __device__ __forceinline__ int64_t scan128(int64_t v, int64_t *before, int64_t *
 }
 
 // ---------------------------------------------------------------- fragments
-__device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                      uint32_t b1, const float (&c)[4]) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
-        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
+// Words of one block of two token rows (8 apart) times a column tile's queries: 16 tokens x 32 columns. The conversions and
+// the two MMAs are one asm block, so that the halves land in the operand registers without moves.
+template <int NT>
+__device__ __forceinline__ void block_scores(float (&d)[NT][4], uint32_t x0, uint32_t x1, const uint32_t (&q)[NT][2][2],
+                                             const float (&start)[NT][4]) {
+    static_assert(NT == 1 || NT == 2, "column tiles");
+    if constexpr (NT == 1) {
+        asm("{\n .reg .b32 y0, y1, p0, p1, p2, p3, r0, r1, r2, r3;\n"
+            " shr.u32 y0, %4, 8;\n shr.u32 y1, %5, 8;\n"
+            " lop3.b32 p0, %4, 0x000F000F, 0x64006400, 0xEA;\n lop3.b32 p1, %5, 0x000F000F, 0x64006400, 0xEA;\n"
+            " lop3.b32 p2, y0, 0x000F000F, 0x64006400, 0xEA;\n lop3.b32 p3, y1, 0x000F000F, 0x64006400, 0xEA;\n"
+            " mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {p0,p1,p2,p3}, {%6,%7}, {%10,%11,%12,%13};\n"
+            " lop3.b32 r0, %4, 0x00F000F0, 0x54005400, 0xEA;\n lop3.b32 r1, %5, 0x00F000F0, 0x54005400, 0xEA;\n"
+            " lop3.b32 r2, y0, 0x00F000F0, 0x54005400, 0xEA;\n lop3.b32 r3, y1, 0x00F000F0, 0x54005400, 0xEA;\n"
+            " mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {r0,r1,r2,r3}, {%8,%9}, {%0,%1,%2,%3};\n}\n"
+            : "=&f"(d[0][0]), "=&f"(d[0][1]), "=&f"(d[0][2]), "=&f"(d[0][3])
+            : "r"(x0), "r"(x1), "r"(q[0][0][0]), "r"(q[0][0][1]), "r"(q[0][1][0]), "r"(q[0][1][1]), "f"(start[0][0]),
+              "f"(start[0][1]), "f"(start[0][2]), "f"(start[0][3]));
+    } else {
+        asm("{\n .reg .b32 y0, y1, p0, p1, p2, p3, r0, r1, r2, r3;\n"
+            " shr.u32 y0, %8, 8;\n shr.u32 y1, %9, 8;\n"
+            " lop3.b32 p0, %8, 0x000F000F, 0x64006400, 0xEA;\n lop3.b32 p1, %9, 0x000F000F, 0x64006400, 0xEA;\n"
+            " lop3.b32 p2, y0, 0x000F000F, 0x64006400, 0xEA;\n lop3.b32 p3, y1, 0x000F000F, 0x64006400, 0xEA;\n"
+            " mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {p0,p1,p2,p3}, {%10,%11}, {%18,%19,%20,%21};\n"
+            " mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%4,%5,%6,%7}, {p0,p1,p2,p3}, {%14,%15}, {%22,%23,%24,%25};\n"
+            " lop3.b32 r0, %8, 0x00F000F0, 0x54005400, 0xEA;\n lop3.b32 r1, %9, 0x00F000F0, 0x54005400, 0xEA;\n"
+            " lop3.b32 r2, y0, 0x00F000F0, 0x54005400, 0xEA;\n lop3.b32 r3, y1, 0x00F000F0, 0x54005400, 0xEA;\n"
+            " mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {r0,r1,r2,r3}, {%12,%13}, {%0,%1,%2,%3};\n"
+            " mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%4,%5,%6,%7}, {r0,r1,r2,r3}, {%16,%17}, {%4,%5,%6,%7};\n}\n"
+            : "=&f"(d[0][0]), "=&f"(d[0][1]), "=&f"(d[0][2]), "=&f"(d[0][3]), "=&f"(d[1][0]), "=&f"(d[1][1]), "=&f"(d[1][2]),
+              "=&f"(d[1][3])
+            : "r"(x0), "r"(x1), "r"(q[0][0][0]), "r"(q[0][0][1]), "r"(q[0][1][0]), "r"(q[0][1][1]), "r"(q[1][0][0]),
+              "r"(q[1][0][1]), "r"(q[1][1][0]), "r"(q[1][1][1]), "f"(start[0][0]), "f"(start[0][1]), "f"(start[0][2]),
+              "f"(start[0][3]), "f"(start[1][0]), "f"(start[1][1]), "f"(start[1][2]), "f"(start[1][3]));
+    }
 }
-__device__ __forceinline__ uint32_t lo_half(uint32_t w) { return (w & 0x000F000Fu) | 0x64006400u; }   // 1024 + code
-__device__ __forceinline__ uint32_t hi_half(uint32_t w) { return (w & 0x00F000F0u) | 0x54005400u; }   // 64 + code
-__device__ __forceinline__ uint32_t sub2(uint32_t v, uint32_t bias) {
-    const __half2 r = __hsub2(half2_bits(v), half2_bits(bias));
-    return *reinterpret_cast<const uint32_t *>(&r);
+// A word of value codes (four tokens of columns u and u + 8 of a column tile of 16) times the weights: o += (code - 8) p
+template <int NT>
+__device__ __forceinline__ void word_outputs(float (&o)[NT][4], uint32_t x, const uint32_t (&p)[NT][2]) {
+    if constexpr (NT == 1) {
+        asm("{\n .reg .b32 y, p0, p1, p2, p3;\n shr.u32 y, %4, 8;\n"
+            " lop3.b32 p0, %4, 0x000F000F, 0x64006400, 0xEA;\n lop3.b32 p1, %4, 0x00F000F0, 0x54005400, 0xEA;\n"
+            " lop3.b32 p2, y, 0x000F000F, 0x64006400, 0xEA;\n lop3.b32 p3, y, 0x00F000F0, 0x54005400, 0xEA;\n"
+            " sub.f16x2 p0, p0, %7;\n sub.f16x2 p1, p1, %8;\n sub.f16x2 p2, p2, %7;\n sub.f16x2 p3, p3, %8;\n"
+            " mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {p0,p1,p2,p3}, {%5,%6}, {%0,%1,%2,%3};\n}\n"
+            : "+f"(o[0][0]), "+f"(o[0][1]), "+f"(o[0][2]), "+f"(o[0][3])
+            : "r"(x), "r"(p[0][0]), "r"(p[0][1]), "r"(0x64086408u), "r"(0x54805480u));
+    } else {
+        asm("{\n .reg .b32 y, p0, p1, p2, p3;\n shr.u32 y, %8, 8;\n"
+            " lop3.b32 p0, %8, 0x000F000F, 0x64006400, 0xEA;\n lop3.b32 p1, %8, 0x00F000F0, 0x54005400, 0xEA;\n"
+            " lop3.b32 p2, y, 0x000F000F, 0x64006400, 0xEA;\n lop3.b32 p3, y, 0x00F000F0, 0x54005400, 0xEA;\n"
+            " sub.f16x2 p0, p0, %13;\n sub.f16x2 p1, p1, %14;\n sub.f16x2 p2, p2, %13;\n sub.f16x2 p3, p3, %14;\n"
+            " mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {p0,p1,p2,p3}, {%9,%10}, {%0,%1,%2,%3};\n"
+            " mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%4,%5,%6,%7}, {p0,p1,p2,p3}, {%11,%12}, {%4,%5,%6,%7};\n}\n"
+            : "+f"(o[0][0]), "+f"(o[0][1]), "+f"(o[0][2]), "+f"(o[0][3]), "+f"(o[1][0]), "+f"(o[1][1]), "+f"(o[1][2]),
+              "+f"(o[1][3])
+            : "r"(x), "r"(p[0][0]), "r"(p[0][1]), "r"(p[1][0]), "r"(p[1][1]), "r"(0x64086408u), "r"(0x54805480u));
+    }
 }
 __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
     const __half2 r = __hmul2(half2_bits(a), half2_bits(b));
@@ -155,7 +202,7 @@ template <int D, int NT>
 struct Queries {
     static constexpr int NB = D / 32;
     uint32_t b[NB][NT][2][2];    // [block][column tile][low, high nibbles][register]
-    float start[NB][NT][2];      // -(bias * sum of the block's queries), columns 2t and 2t + 1
+    float start[NB][NT][4];      // -(bias * sum of the block's queries), columns 2t and 2t + 1, twice
     float scale[NT][2];          // scale * log2 e * the queries' power of two
 };
 template <int D, int NT>
@@ -201,8 +248,8 @@ __device__ __forceinline__ void load_queries(Queries<D, NT> &q, const DecodeArgs
             }
             bias += __shfl_xor_sync(FULL, bias, 1);
             bias += __shfl_xor_sync(FULL, bias, 2);
-            q.start[k][n][0] = __shfl_sync(FULL, bias, 8 * t);
-            q.start[k][n][1] = __shfl_sync(FULL, bias, 8 * t + 4);
+            q.start[k][n][0] = q.start[k][n][2] = __shfl_sync(FULL, bias, 8 * t);
+            q.start[k][n][1] = q.start[k][n][3] = __shfl_sync(FULL, bias, 8 * t + 4);
         }
         q.scale[n][0] = __shfl_sync(FULL, c, 8 * t);
         q.scale[n][1] = __shfl_sync(FULL, c, 8 * t + 4);
@@ -227,7 +274,7 @@ __device__ __forceinline__ void next_tile(Walk &w, const DecodeArgs &p, int live
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(WARPS * 32, NT == 1 ? (D == 256 ? 2 : 4) : (D == 64 ? 3 : 2))
+__global__ void __launch_bounds__(WARPS * 32, NT == 1 ? (D == 256 ? 2 : 3) : (D == 64 ? 3 : 2))
 attn_decode_kernel(const __grid_constant__ DecodeArgs p, bool wide) {
     constexpr int NB = D / 32, S = stages(D, NT), GB = group_bytes(D), MT = D / 16, W = NB < 4 ? NB : 4;
     constexpr int STAGE = 2 * GB, PITCH = D + 4;
@@ -352,11 +399,6 @@ attn_decode_kernel(const __grid_constant__ DecodeArgs p, bool wide) {
 #pragma unroll
         for (int r = 0; r < 2; r++) {
             used[r] = ok && use[warp][stage][r];
-#pragma unroll
-            for (int n = 0; n < NT; n++)
-#pragma unroll
-                for (int e = 0; e < 4; e++) s[r][n][e] = used[r] ? 0.0f : -INFINITY;
-            if (!used[r]) continue;
             const uint32_t grp = buf + r * GB;
             uint32_t dk[2][NB / 2];
             lds_words<NB / 2>(grp + 8 * D + 2 * NB * g, dk[0]);
@@ -371,36 +413,38 @@ attn_decode_kernel(const __grid_constant__ DecodeArgs p, bool wide) {
                     const int b = bq * W + k;
                     const float2 p0 = __half22float2(half2_bits(dk[0][b / 2])), p1 = __half22float2(half2_bits(dk[1][b / 2]));
                     const float d0 = b & 1 ? p0.y : p0.x, d1 = b & 1 ? p1.y : p1.x;
-                    const uint32_t x0 = w0[k], x1 = w1[k], y0 = x0 >> 8, y1 = x1 >> 8;
+                    float a[NT][4];
+                    block_scores<NT>(a, w0[k], w1[k], q.b[b], q.start[b]);
 #pragma unroll
-                    for (int n = 0; n < NT; n++) {
-                        const float c[4] = {q.start[b][n][0], q.start[b][n][1], q.start[b][n][0], q.start[b][n][1]};
-                        float a[4];
-                        mma16(a, lo_half(x0), lo_half(x1), lo_half(y0), lo_half(y1), q.b[b][n][0][0], q.b[b][n][0][1], c);
-                        mma16(a, hi_half(x0), hi_half(x1), hi_half(y0), hi_half(y1), q.b[b][n][1][0], q.b[b][n][1][1], a);
-                        s[r][n][0] = fmaf(d0, a[0], s[r][n][0]);
-                        s[r][n][1] = fmaf(d0, a[1], s[r][n][1]);
-                        s[r][n][2] = fmaf(d1, a[2], s[r][n][2]);
-                        s[r][n][3] = fmaf(d1, a[3], s[r][n][3]);
-                    }
+                    for (int n = 0; n < NT; n++)
+#pragma unroll
+                        for (int e = 0; e < 4; e++)
+                            s[r][n][e] = b == 0 ? (e < 2 ? d0 : d1) * a[n][e] : fmaf(e < 2 ? d0 : d1, a[n][e], s[r][n][e]);
                 }
             }
 #pragma unroll
             for (int n = 0; n < NT; n++)
 #pragma unroll
                 for (int e = 0; e < 4; e++) s[r][n][e] *= q.scale[n][e & 1];
-            const int j = token0 + r * GROUP;
-            if (j + GROUP > end0 || (p.a.window > 0 && j < now.s.len - p.a.window)) {   // some query does not see some key
+        }
+        // some query does not see some key, or a group's page does not exist (what its stage holds is masked)
+        const bool whole = used[0] && used[1] && token0 + WARP_TOKENS <= end0 &&
+                           (p.a.window == 0 || token0 >= now.s.len - p.a.window);
+        if (!whole) {
 #pragma unroll
-                for (int n = 0; n < NT; n++)
+            for (int n = 0; n < NT; n++)
 #pragma unroll
-                    for (int e = 0; e < 2; e++) {
-                        const int end = end0 + (column0 + 8 * n + 2 * t + e) / p.G;
-                        const int begin = p.a.window > 0 ? end - p.a.window : 0;
-                        if (j + g >= end || j + g < begin || j + g >= now.s.len) s[r][n][e] = -INFINITY;
-                        if (j + g + 8 >= end || j + g + 8 < begin || j + g + 8 >= now.s.len) s[r][n][2 + e] = -INFINITY;
-                    }
-            }
+                for (int e = 0; e < 2; e++) {
+                    const int end = min(end0 + (column0 + 8 * n + 2 * t + e) / p.G, now.s.len);
+                    const int begin = p.a.window > 0 ? end - p.a.window : 0;
+#pragma unroll
+                    for (int r = 0; r < 2; r++)
+#pragma unroll
+                        for (int f = 0; f < 2; f++) {
+                            const int j = token0 + r * GROUP + 8 * f + g;
+                            if (!used[r] || j >= end || j < begin) s[r][n][2 * f + e] = -INFINITY;
+                        }
+                }
         }
         // the columns' maxima; the reference moves only far
         float top[NT][2];
@@ -420,22 +464,25 @@ attn_decode_kernel(const __grid_constant__ DecodeArgs p, bool wide) {
         uint32_t dv[2][NB][2], any = 0;
 #pragma unroll
         for (int r = 0; r < 2; r++) {
-            if (!used[r]) continue;
             uint32_t w[2 * NB];
             lds_words<2 * NB>(buf + r * GB + 17 * D + t * 8 * NB, w);
-            const int j = token0 + r * GROUP + 2 * t;
-            uint32_t k0 = FULL, k1 = FULL;
-            if (j + GROUP > now.s.len) {
-                k0 = (j < now.s.len ? 0xffffu : 0) | (j + 1 < now.s.len ? 0xffff0000u : 0);
-                k1 = (j + 8 < now.s.len ? 0xffffu : 0) | (j + 9 < now.s.len ? 0xffff0000u : 0);
-            }
 #pragma unroll
-            for (int b = 0; b < NB; b++) {
-                dv[r][b][0] = w[2 * b] & k0;
-                dv[r][b][1] = w[2 * b + 1] & k1;
-                any |= dv[r][b][0] | dv[r][b][1];
+            for (int b = 0; b < NB; b++) dv[r][b][0] = w[2 * b], dv[r][b][1] = w[2 * b + 1];
+        }
+        if (!whole) {
+#pragma unroll
+            for (int r = 0; r < 2; r++) {
+                const int j = token0 + r * GROUP + 2 * t, len = used[r] ? now.s.len : 0;
+                const uint32_t k0 = (j < len ? 0xffffu : 0) | (j + 1 < len ? 0xffff0000u : 0);
+                const uint32_t k1 = (j + 8 < len ? 0xffffu : 0) | (j + 9 < len ? 0xffff0000u : 0);
+#pragma unroll
+                for (int b = 0; b < NB; b++) dv[r][b][0] &= k0, dv[r][b][1] &= k1;
             }
         }
+#pragma unroll
+        for (int r = 0; r < 2; r++)
+#pragma unroll
+            for (int b = 0; b < NB; b++) any |= dv[r][b][0] | dv[r][b][1];
         const bool large = (any & 0x40004000u) != 0;   // a scale of 2 or more
         int e_new = lift_e;
         if (__any_sync(FULL, move || large)) {
@@ -446,11 +493,10 @@ attn_decode_kernel(const __grid_constant__ DecodeArgs p, bool wide) {
 #pragma unroll
                     for (int b = 0; b < NB; b++)
 #pragma unroll
-                        for (int x = 0; x < 2; x++)
-                            if (used[r]) {
-                                const float2 f = __half22float2(__habs2(half2_bits(dv[r][b][x])));
-                                m = fmaxf(m, fmaxf(f.x, f.y));
-                            }
+                        for (int x = 0; x < 2; x++) {
+                            const float2 f = __half22float2(__habs2(half2_bits(dv[r][b][x])));
+                            m = fmaxf(m, fmaxf(f.x, f.y));
+                        }
 #pragma unroll
                 for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, x));
                 e_new = min(max(e_new, (int)(__float_as_uint(m) >> 23) - 127), 16);
@@ -476,7 +522,6 @@ attn_decode_kernel(const __grid_constant__ DecodeArgs p, bool wide) {
         }
 #pragma unroll
         for (int r = 0; r < 2; r++) {
-            if (!used[r]) continue;
             const uint32_t grp = buf + r * GB;
             uint32_t pt[NT][2];   // weights of query g: tokens 2t, 2t + 1 and 2t + 8, 2t + 9
 #pragma unroll
@@ -504,14 +549,7 @@ attn_decode_kernel(const __grid_constant__ DecodeArgs p, bool wide) {
                         pb[n][1] = mul2(pt[n][1], dv[r][b][1]);
                     }
 #pragma unroll
-                    for (int mm = 0; mm < 2; mm++) {
-                        const uint32_t x = w[2 * bb + mm], y = x >> 8;
-                        const uint32_t a0 = sub2(lo_half(x), 0x64086408u), a1 = sub2(hi_half(x), 0x54805480u);
-                        const uint32_t a2 = sub2(lo_half(y), 0x64086408u), a3 = sub2(hi_half(y), 0x54805480u);
-#pragma unroll
-                        for (int n = 0; n < NT; n++)
-                            mma16(o[2 * b + mm][n], a0, a1, a2, a3, pb[n][0], pb[n][1], o[2 * b + mm][n]);
-                    }
+                    for (int mm = 0; mm < 2; mm++) word_outputs<NT>(o[2 * b + mm], w[2 * bb + mm], pb);
                 }
             }
         }
@@ -690,7 +728,7 @@ Layout layout_of(int Hkv, int D, int n_heads, int64_t B, int T) {
 template <int D, int NT>
 qk_status launch_pass(const DecodeArgs &p, cudaStream_t s) {
     constexpr int smem = WARPS * stages(D, NT) * 2 * group_bytes(D);
-    constexpr int per_sm = NT == 1 ? (D == 256 ? 2 : 4) : (D == 64 ? 3 : 2);
+    constexpr int per_sm = NT == 1 ? (D == 256 ? 2 : 3) : (D == 64 ? 3 : 2);
     static bool ready[64] = {};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return fail(QK_ERR_CUDA, "attn_decode: no device");
