@@ -31,8 +31,9 @@ namespace {
 
 constexpr unsigned FULL = 0xffffffffu;
 constexpr float LOG2E = 1.4426950408889634f;
-constexpr int WARPS = 4;
-constexpr int WARP_TOKENS = 2 * GROUP;
+constexpr int WARPS = 2;
+constexpr int GROUPS = 4;                   // of a warp's share of a tile
+constexpr int WARP_TOKENS = GROUPS * GROUP;
 constexpr int TILE = WARPS * WARP_TOKENS;   // tokens
 constexpr float HEADROOM = 8.0f;    // the reference maximum moves when a logit is 2^8 above it
 constexpr float LIFT = 6.0f;        // weights are held times 2^6 below the reference: at most 2^14
@@ -40,12 +41,15 @@ constexpr int MAX_CTAS = 1024;      // of one launch; sizes the workspace
 
 // column tiles of 8 a CTA takes at most
 __host__ __device__ constexpr int column_tiles(int D) { return D == 256 ? 1 : 2; }
-__host__ __device__ constexpr int stages(int D, int NT) { return D == 64 ? 4 : NT == 2 ? 3 : 3; }
+__host__ __device__ constexpr int stages(int D) { return D == 64 ? 4 : 2; }
+// CTAs of an SM, by registers and shared memory
+__host__ __device__ constexpr int per_sm(int D, int NT) { return D == 256 ? 3 : NT == 2 ? (D == 64 ? 5 : 4) : 6; }
 
 struct DecodeArgs {
     KvCache c;
     qk_attn a;
     int B, T, G, groups;   // groups: CTAs that share a tile, each with its own columns
+    int tile_pages, tile_rest;   // TILE / page_tokens, TILE % page_tokens
     const int32_t *live;
     float *acc;            // [slot][groups][8 NT][D]
     float2 *ml;            // [slot][groups][8 NT]: reference maximum, sum of weights
@@ -66,8 +70,8 @@ __device__ __forceinline__ Sequence sequence_of(const DecodeArgs &p, int b) {
     return s;
 }
 
-// Sum over a CTA of 128 threads of one value each, and the sum of the threads before.
-__device__ __forceinline__ int64_t scan128(int64_t v, int64_t *before, int64_t *smem) {
+// Sum over a CTA of one value a thread, and the sum of the threads before.
+__device__ __forceinline__ int64_t scan_cta(int64_t v, int64_t *before, int64_t *smem) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int64_t x = v;
 #pragma unroll
@@ -274,22 +278,22 @@ __device__ __forceinline__ void next_tile(Walk &w, const DecodeArgs &p, int live
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(WARPS * 32, NT == 1 ? (D == 256 ? 2 : 3) : (D == 64 ? 3 : 2))
+__global__ void __launch_bounds__(WARPS * 32, per_sm(D, NT))
 attn_decode_kernel(const __grid_constant__ DecodeArgs p, bool wide) {
-    constexpr int NB = D / 32, S = stages(D, NT), GB = group_bytes(D), MT = D / 16, W = NB < 4 ? NB : 4;
-    constexpr int STAGE = 2 * GB, PITCH = D + 4;
+    constexpr int NB = D / 32, S = stages(D), GB = group_bytes(D), MT = D / 16, W = NB < 4 ? NB : 4;
+    constexpr int STAGE = GROUPS * GB, PITCH = D + 4;
     static_assert(8 * PITCH * 4 <= STAGE, "a warp's partial outputs fit its stage");
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int64_t scan[WARPS];
     __shared__ int64_t found[2];
     __shared__ float2 meet[WARPS][8];
-    __shared__ uint8_t use[WARPS][S][2];
+    __shared__ __align__(4) uint8_t use[WARPS][S][GROUPS];
     __shared__ __align__(8) uint64_t bars[WARPS][S];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int share = blockIdx.x / p.groups, cg = blockIdx.x % p.groups, shares = gridDim.x / p.groups;
     const int column0 = cg * 8 * NT;
     const uint32_t ring = smem_u32(smem) + warp * S * STAGE, bar0 = smem_u32(&bars[warp][0]);
-    if (lane < S) mbar_init(bar0 + 8 * lane, 2);
+    if (lane < S) mbar_init(bar0 + 8 * lane, GROUPS);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     pdl_trigger();
     pdl_wait();
@@ -300,7 +304,7 @@ attn_decode_kernel(const __grid_constant__ DecodeArgs p, bool wide) {
     for (int b0 = 0; b0 < live; b0 += WARPS * 32) {
         const int b = b0 + threadIdx.x;
         const int64_t n = b < live ? (int64_t)sequence_of(p, b).tiles * p.c.Hkv : 0;
-        const int64_t sum = scan128(n, &before, scan);
+        const int64_t sum = scan_cta(n, &before, scan);
         if (blockIdx.x == 0 && b < live) p.plan[1 + b] = total + before;
         total += sum;
     }
@@ -314,7 +318,7 @@ attn_decode_kernel(const __grid_constant__ DecodeArgs p, bool wide) {
         for (int b0 = 0; b0 < live; b0 += WARPS * 32) {
             const int b = b0 + threadIdx.x;
             const int64_t n = b < live ? (int64_t)sequence_of(p, b).tiles * p.c.Hkv : 0;
-            const int64_t sum = scan128(n, &before, scan);
+            const int64_t sum = scan_cta(n, &before, scan);
             if (first >= at + before && first < at + before + n) {
                 found[0] = b;
                 found[1] = first - at - before;
@@ -330,35 +334,50 @@ attn_decode_kernel(const __grid_constant__ DecodeArgs p, bool wide) {
     now.h = (int)(found[1] / now.s.tiles);
     now.tile = (int)(found[1] % now.s.tiles);
 
-    // what is on its way: lanes 0 and 1 copy one group each
+    // what is on its way: the first lanes copy a group each
     Walk ahead = now;
     int64_t to_issue = left;
-    int page = -1, token = 0;   // of the next tile to issue
+    int page = -1, in_page = 0, table_at = 0, token = 0;   // of the next tile to issue
     bool ok = true;
-    const auto look_up = [&]() {
+    const auto place = [&]() {   // of the first tile in a segment
         token = ahead.s.base + ahead.tile * TILE + warp * WARP_TOKENS + lane * GROUP;
+        table_at = token / p.c.page_tokens;
+        in_page = token - table_at * p.c.page_tokens;
+    };
+    const auto look_up = [&]() {
         page = -1;
-        if (lane < 2 && to_issue > 0 && token < ahead.s.len)
-            page = ld_prev(p.a.page_table + ahead.b * p.a.table_stride + token / p.c.page_tokens);
+        if (lane < GROUPS && token < ahead.s.len)
+            page = ld_prev(p.a.page_table + ahead.b * p.a.table_stride + table_at);
     };
     const auto issue = [&](int stage) {
         if (to_issue <= 0 || !ok) return;
-        if (lane < 2) {
+        if (lane < GROUPS) {
             const bool good = page >= 0 && page < p.c.n_pages;
             use[warp][stage][lane] = good;
             if (good) {
                 mbar_expect_tx(bar0 + 8 * stage, GB);
-                bulk_g2s(ring + stage * STAGE + lane * GB, group_at(p.c, page, ahead.h, token % p.c.page_tokens), GB,
-                         bar0 + 8 * stage);
+                bulk_g2s(ring + stage * STAGE + lane * GB, group_at(p.c, page, ahead.h, in_page), GB, bar0 + 8 * stage);
             } else {
                 mbar_arrive(bar0 + 8 * stage);
             }
         }
-        to_issue--;
-        if (to_issue > 0) next_tile(ahead, p, live);
+        if (--to_issue <= 0) return;
+        next_tile(ahead, p, live);
+        if (ahead.tile == 0) {
+            place();
+        } else {   // a tile further on
+            token += TILE;
+            table_at += p.tile_pages;
+            in_page += p.tile_rest;
+            if (in_page >= p.c.page_tokens) {
+                in_page -= p.c.page_tokens;
+                table_at++;
+            }
+        }
         look_up();
     };
     __syncwarp();
+    place();
     look_up();
 #pragma unroll
     for (int s = 0; s < S; s++) issue(s);
@@ -393,12 +412,12 @@ attn_decode_kernel(const __grid_constant__ DecodeArgs p, bool wide) {
         const uint32_t buf = ring + stage * STAGE;
         const int token0 = now.s.base + now.tile * TILE + warp * WARP_TOKENS;
         const int end0 = now.s.len - p.T + 1;   // keys that the first of the new tokens sees
-        // scores of both groups, times log2 e
-        float s[2][NT][4];
-        bool used[2];
+        // scores, times log2 e
+        float s[GROUPS][NT][4];
+        uint32_t used = 0, any = 0;
+        if (ok) used = *reinterpret_cast<const uint32_t *>(&use[warp][stage][0]);   // a byte a group
 #pragma unroll
-        for (int r = 0; r < 2; r++) {
-            used[r] = ok && use[warp][stage][r];
+        for (int r = 0; r < GROUPS; r++) {
             const uint32_t grp = buf + r * GB;
             uint32_t dk[2][NB / 2];
             lds_words<NB / 2>(grp + 8 * D + 2 * NB * g, dk[0]);
@@ -428,7 +447,7 @@ attn_decode_kernel(const __grid_constant__ DecodeArgs p, bool wide) {
                 for (int e = 0; e < 4; e++) s[r][n][e] *= q.scale[n][e & 1];
         }
         // some query does not see some key, or a group's page does not exist (what its stage holds is masked)
-        const bool whole = used[0] && used[1] && token0 + WARP_TOKENS <= end0 &&
+        const bool whole = used == 0x01010101u && token0 + WARP_TOKENS <= end0 &&
                            (p.a.window == 0 || token0 >= now.s.len - p.a.window);
         if (!whole) {
 #pragma unroll
@@ -438,11 +457,11 @@ attn_decode_kernel(const __grid_constant__ DecodeArgs p, bool wide) {
                     const int end = min(end0 + (column0 + 8 * n + 2 * t + e) / p.G, now.s.len);
                     const int begin = p.a.window > 0 ? end - p.a.window : 0;
 #pragma unroll
-                    for (int r = 0; r < 2; r++)
+                    for (int r = 0; r < GROUPS; r++)
 #pragma unroll
                         for (int f = 0; f < 2; f++) {
                             const int j = token0 + r * GROUP + 8 * f + g;
-                            if (!used[r] || j >= end || j < begin) s[r][n][2 * f + e] = -INFINITY;
+                            if (!(used >> (8 * r) & 1) || j >= end || j < begin) s[r][n][2 * f + e] = -INFINITY;
                         }
                 }
         }
@@ -453,50 +472,48 @@ attn_decode_kernel(const __grid_constant__ DecodeArgs p, bool wide) {
         for (int n = 0; n < NT; n++)
 #pragma unroll
             for (int e = 0; e < 2; e++) {
-                float m = fmaxf(fmaxf(s[0][n][e], s[0][n][2 + e]), fmaxf(s[1][n][e], s[1][n][2 + e]));
+                float m = fmaxf(s[0][n][e], s[0][n][2 + e]);
+#pragma unroll
+                for (int r = 1; r < GROUPS; r++) m = fmaxf(fmaxf(m, s[r][n][e]), s[r][n][2 + e]);
                 m = fmaxf(m, __shfl_xor_sync(FULL, m, 4));
                 m = fmaxf(m, __shfl_xor_sync(FULL, m, 8));
                 m = fmaxf(m, __shfl_xor_sync(FULL, m, 16));
                 top[n][e] = m;
                 move |= m - ref[n][e] > HEADROOM;   // (no: both are minus infinity)
             }
-        // the values' scales (zero behind the last key, where the cache may hold anything)
-        uint32_t dv[2][NB][2], any = 0;
-#pragma unroll
-        for (int r = 0; r < 2; r++) {
-            uint32_t w[2 * NB];
-            lds_words<2 * NB>(buf + r * GB + 17 * D + t * 8 * NB, w);
-#pragma unroll
-            for (int b = 0; b < NB; b++) dv[r][b][0] = w[2 * b], dv[r][b][1] = w[2 * b + 1];
-        }
-        if (!whole) {
-#pragma unroll
-            for (int r = 0; r < 2; r++) {
-                const int j = token0 + r * GROUP + 2 * t, len = used[r] ? now.s.len : 0;
+        // the values' scales of a group: zero behind the last key, where the cache may hold anything
+        const auto value_scales = [&](int r, uint32_t (&dv)[2 * NB]) {
+            lds_words<2 * NB>(buf + r * GB + 17 * D + t * 8 * NB, dv);
+            if (!whole) {
+                const int j = token0 + r * GROUP + 2 * t, len = used >> (8 * r) & 1 ? now.s.len : 0;
                 const uint32_t k0 = (j < len ? 0xffffu : 0) | (j + 1 < len ? 0xffff0000u : 0);
                 const uint32_t k1 = (j + 8 < len ? 0xffffu : 0) | (j + 9 < len ? 0xffff0000u : 0);
 #pragma unroll
-                for (int b = 0; b < NB; b++) dv[r][b][0] &= k0, dv[r][b][1] &= k1;
+                for (int b = 0; b < NB; b++) dv[2 * b] &= k0, dv[2 * b + 1] &= k1;
             }
+        };
+#pragma unroll
+        for (int r = 0; r < GROUPS; r++) {
+            uint32_t dv[2 * NB];
+            value_scales(r, dv);
+#pragma unroll
+            for (int b = 0; b < NB; b++) any |= dv[2 * b] | dv[2 * b + 1];
         }
-#pragma unroll
-        for (int r = 0; r < 2; r++)
-#pragma unroll
-            for (int b = 0; b < NB; b++) any |= dv[r][b][0] | dv[r][b][1];
         const bool large = (any & 0x40004000u) != 0;   // a scale of 2 or more
         int e_new = lift_e;
         if (__any_sync(FULL, move || large)) {
             if (__any_sync(FULL, large)) {
                 float m = 0.0f;
+#pragma unroll 1
+                for (int r = 0; r < GROUPS; r++) {
+                    uint32_t dv[2 * NB];
+                    value_scales(r, dv);
 #pragma unroll
-                for (int r = 0; r < 2; r++)
-#pragma unroll
-                    for (int b = 0; b < NB; b++)
-#pragma unroll
-                        for (int x = 0; x < 2; x++) {
-                            const float2 f = __half22float2(__habs2(half2_bits(dv[r][b][x])));
-                            m = fmaxf(m, fmaxf(f.x, f.y));
-                        }
+                    for (int x = 0; x < 2 * NB; x++) {
+                        const float2 f = __half22float2(__habs2(half2_bits(dv[x])));
+                        m = fmaxf(m, fmaxf(f.x, f.y));
+                    }
+                }
 #pragma unroll
                 for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, x));
                 e_new = min(max(e_new, (int)(__float_as_uint(m) >> 23) - 127), 16);
@@ -521,8 +538,10 @@ attn_decode_kernel(const __grid_constant__ DecodeArgs p, bool wide) {
             lift_e = e_new;
         }
 #pragma unroll
-        for (int r = 0; r < 2; r++) {
+        for (int r = 0; r < GROUPS; r++) {
             const uint32_t grp = buf + r * GB;
+            uint32_t dv[2 * NB];
+            value_scales(r, dv);
             uint32_t pt[NT][2];   // weights of query g: tokens 2t, 2t + 1 and 2t + 8, 2t + 9
 #pragma unroll
             for (int n = 0; n < NT; n++) {
@@ -545,8 +564,8 @@ attn_decode_kernel(const __grid_constant__ DecodeArgs p, bool wide) {
                     uint32_t pb[NT][2];
 #pragma unroll
                     for (int n = 0; n < NT; n++) {
-                        pb[n][0] = mul2(pt[n][0], dv[r][b][0]);
-                        pb[n][1] = mul2(pt[n][1], dv[r][b][1]);
+                        pb[n][0] = mul2(pt[n][0], dv[2 * b]);
+                        pb[n][1] = mul2(pt[n][1], dv[2 * b + 1]);
                     }
 #pragma unroll
                     for (int mm = 0; mm < 2; mm++) word_outputs<NT>(o[2 * b + mm], w[2 * bb + mm], pb);
@@ -555,7 +574,7 @@ attn_decode_kernel(const __grid_constant__ DecodeArgs p, bool wide) {
         }
         __syncwarp();   // the stage is read
         if (left == 1 || now.tile + 1 == now.s.tiles) {
-            // the segment ends here: one partial result of the four warps, through the stages just read
+            // the segment ends here: one partial result of the warps, through the stages just read
             const int64_t slot = ((int64_t)now.b * p.c.Hkv + now.h + share) * p.groups + cg;
 #pragma unroll
             for (int n = 0; n < NT; n++) {
@@ -588,7 +607,10 @@ attn_decode_kernel(const __grid_constant__ DecodeArgs p, bool wide) {
                 float *out = p.acc + (slot * NT + n) * 8 * D;
                 for (int i = threadIdx.x; i < 8 * D; i += WARPS * 32) {
                     const int at = i / D * PITCH + i % D;
-                    out[i] = (all[at] + all[at + STEP]) + (all[at + 2 * STEP] + all[at + 3 * STEP]);
+                    float v = all[at];
+#pragma unroll
+                    for (int w = 1; w < WARPS; w++) v += all[at + w * STEP];
+                    out[i] = v;
                 }
                 if (threadIdx.x < 8) {
                     float m = -INFINITY, l = 0.0f;
@@ -629,11 +651,12 @@ struct JoinArgs {
     int NT;
 };
 // One CTA per (row, query head): its head's partial results in order, four at a time; then rows and image.
+constexpr int JOIN_WARPS = 4;
 template <int D>
-__global__ void __launch_bounds__(128) attn_combine_kernel(const __grid_constant__ JoinArgs a) {
+__global__ void __launch_bounds__(JOIN_WARPS * 32) attn_combine_kernel(const __grid_constant__ JoinArgs a) {
     constexpr int NB = D / 32;
-    __shared__ float part[WARPS][D];
-    __shared__ float2 stat[WARPS];
+    __shared__ float part[JOIN_WARPS][D];
+    __shared__ float2 stat[JOIN_WARPS];
     pdl_trigger();
     pdl_wait();
     const DecodeArgs &p = a.p;
@@ -653,7 +676,7 @@ __global__ void __launch_bounds__(128) attn_combine_kernel(const __grid_constant
         const int64_t seg = (int64_t)b * p.c.Hkv + h;
         const int n = col / 8, cg = n / a.NT, in = n % a.NT * 8 + col % 8;
         const auto at = [&](int64_t c) { return ((seg + c) * p.groups + cg) * a.NT * 8 + in; };
-        for (int64_t c = c0 + warp; c <= c1; c += WARPS) {
+        for (int64_t c = c0 + warp; c <= c1; c += JOIN_WARPS) {
             const float m = ld_prev(&p.ml[at(c)].x), v = ld_prev(&p.ml[at(c)].y);
             float x[NB];
 #pragma unroll
@@ -672,18 +695,18 @@ __global__ void __launch_bounds__(128) attn_combine_kernel(const __grid_constant
     __syncthreads();
     top = sink;
 #pragma unroll
-    for (int w = 0; w < WARPS; w++) top = fmaxf(top, stat[w].x);
-    float f[WARPS], total = sink == -INFINITY ? 0.0f : ex2(sink - top);
+    for (int w = 0; w < JOIN_WARPS; w++) top = fmaxf(top, stat[w].x);
+    float f[JOIN_WARPS], total = sink == -INFINITY ? 0.0f : ex2(sink - top);
 #pragma unroll
-    for (int w = 0; w < WARPS; w++) {
+    for (int w = 0; w < JOIN_WARPS; w++) {
         f[w] = stat[w].x == -INFINITY ? 0.0f : ex2(stat[w].x - top);
         total = fmaf(stat[w].y, f[w], total);
     }
     const float inv = total > 0.0f ? 1.0f / total : 0.0f;
-    for (int k = warp; k < NB; k += WARPS) {
+    for (int k = warp; k < NB; k += JOIN_WARPS) {
         float y = 0.0f;
 #pragma unroll
-        for (int w = 0; w < WARPS; w++) y = fmaf(part[w][32 * k + lane], f[w], y);
+        for (int w = 0; w < JOIN_WARPS; w++) y = fmaf(part[w][32 * k + lane], f[w], y);
         y *= inv;
         const int64_t to = row * p.a.out_stride + (int64_t)head * D + 32 * k + lane;
         if (p.a.out && p.a.out_elem == QK_ELEM_F32) static_cast<float *>(p.a.out)[to] = y;
@@ -727,8 +750,7 @@ Layout layout_of(int Hkv, int D, int n_heads, int64_t B, int T) {
 
 template <int D, int NT>
 qk_status launch_pass(const DecodeArgs &p, cudaStream_t s) {
-    constexpr int smem = WARPS * stages(D, NT) * 2 * group_bytes(D);
-    constexpr int per_sm = NT == 1 ? (D == 256 ? 2 : 3) : (D == 64 ? 3 : 2);
+    constexpr int smem = WARPS * stages(D) * GROUPS * group_bytes(D);
     static bool ready[64] = {};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return fail(QK_ERR_CUDA, "attn_decode: no device");
@@ -738,7 +760,7 @@ qk_status launch_pass(const DecodeArgs &p, cudaStream_t s) {
         if (e != cudaSuccess) return fail(QK_ERR_CUDA, "attn_decode: %s", cudaGetErrorString(e));
         ready[dev] = true;
     }
-    const int shares = std::max(1, std::min(per_sm * sm_count(), MAX_CTAS) / p.groups);
+    const int shares = std::max(1, std::min(per_sm(D, NT) * sm_count(), MAX_CTAS) / p.groups);
     const bool wide = row_wide(p.a.q, p.a.q_stride, p.a.q_elem);
     return launch_pdl("attn_decode", attn_decode_kernel<D, NT>, dim3((unsigned)shares * p.groups), dim3(WARPS * 32), smem, s,
                       p, wide);
@@ -754,7 +776,7 @@ qk_status launch_attn_decode(const KvCache &c, const qk_attn &a, int B, int T, u
                              const int32_t *live, void *ws, cudaStream_t s) {
     const Layout l = layout_of(c.Hkv, c.D, a.n_heads, B, T);
     uint8_t *w = static_cast<uint8_t *>(ws);
-    const DecodeArgs p = {c, a, B, T, a.n_heads / c.Hkv, l.groups, live, reinterpret_cast<float *>(w + l.acc),
+    const DecodeArgs p = {c, a, B, T, a.n_heads / c.Hkv, l.groups, TILE / c.page_tokens, TILE % c.page_tokens, live, reinterpret_cast<float *>(w + l.acc),
                           reinterpret_cast<float2 *>(w + l.ml), reinterpret_cast<int64_t *>(w + l.plan)};
     qk_status st = c.D == 256  ? launch_pass<256, 1>(p, s)
                    : c.D == 64 ? (l.NT == 1 ? launch_pass<64, 1>(p, s) : launch_pass<64, 2>(p, s))
