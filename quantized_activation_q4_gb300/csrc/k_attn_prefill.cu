@@ -117,14 +117,25 @@ __global__ void __launch_bounds__(128) attn_stage_kernel(const __grid_constant__
         const int t = x & 3, i = x / 4 % GROUP, bq = x / (4 * GROUP);
         const int row = 4 * (i % 8 / 2) + i % 2 + i / 8 * 2;
         const bool keep = good && token + i < s.len;
+        uint32_t words[W], scales[W / 2];   // of W blocks side by side
+        if (keep) {
+            const uint8_t *kw = g + k_word_at(D, i, bq * W, t), *ks = g + k_scale_at(D, i, bq * W);
+            if constexpr (W == 4) {
+                const uint4 a = ld_prev(reinterpret_cast<const uint4 *>(kw));
+                const uint2 d = ld_prev(reinterpret_cast<const uint2 *>(ks));
+                words[0] = a.x, words[1] = a.y, words[2] = a.z, words[3] = a.w, scales[0] = d.x, scales[1] = d.y;
+            } else {
+                const uint2 a = ld_prev(reinterpret_cast<const uint2 *>(kw));
+                words[0] = a.x, words[1] = a.y, scales[0] = ld_prev(reinterpret_cast<const uint32_t *>(ks));
+            }
+        }
 #pragma unroll
         for (int e = 0; e < W; e++) {
             const int blk = bq * W + e;
             uint2 lo = make_uint2(0, 0), hi = make_uint2(0, 0);
             if (keep) {
-                const uint32_t w = ld_prev(reinterpret_cast<const uint32_t *>(g + k_word_at(D, i, blk, t))), w8 = w >> 8;
-                const __half d = __ushort_as_half(ld_prev(reinterpret_cast<const uint16_t *>(g + k_scale_at(D, i, blk))));
-                const __half2 d2 = __halves2half2(d, d);
+                const uint32_t w = words[e], w8 = w >> 8;
+                const __half2 ds = half2_bits(scales[e / 2]), d2 = e & 1 ? __high2half2(ds) : __low2half2(ds);
                 const uint32_t a = value2(lo_half(w), LO_BIAS, d2), c = value2(lo_half(w8), LO_BIAS, d2);   // 0 2, 1 3
                 const uint32_t y = value2(hi_half(w), HI_BIAS, d2), z = value2(hi_half(w8), HI_BIAS, d2);
                 lo = make_uint2(__byte_perm(a, c, 0x5410), __byte_perm(a, c, 0x7632));
@@ -141,14 +152,16 @@ __global__ void __launch_bounds__(128) attn_stage_kernel(const __grid_constant__
         const int t = x & 3, u = x / 4 % 8, mq = x / 32;
         const bool k0 = token + 2 * t < s.len, k1 = token + 2 * t + 1 < s.len, k2 = token + 2 * t + 8 < s.len,
                    k3 = token + 2 * t + 9 < s.len;
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (good) w = ld_prev(reinterpret_cast<const uint4 *>(g + 9 * D + x * 16));
+        uint4 w = make_uint4(0, 0, 0, 0), d4 = w;   // two blocks' scales
+        if (good) {
+            w = ld_prev(reinterpret_cast<const uint4 *>(g + 9 * D + x * 16));
+            d4 = ld_prev(reinterpret_cast<const uint4 *>(g + 17 * D + (t * NB + 2 * mq) * 8));
+        }
         const uint32_t words[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
         for (int e = 0; e < 4; e++) {
             const int m = mq * 4 + e;
-            uint2 d = make_uint2(0, 0);
-            if (good) d = ld_prev(reinterpret_cast<const uint2 *>(g + 17 * D + (t * NB + m / 2) * 8));
+            uint2 d = e < 2 ? make_uint2(d4.x, d4.y) : make_uint2(d4.z, d4.w);
             // (a scale behind the last key may be anything: it is taken as 0)
             d.x &= (k0 ? 0xffffu : 0) | (k1 ? 0xffff0000u : 0);
             d.y &= (k2 ? 0xffffu : 0) | (k3 ? 0xffff0000u : 0);

@@ -170,6 +170,36 @@ def test_read(D, Hkv, P, elem):
     assert np.array_equal(got[keep, :width], want)
 
 
+@pytest.mark.parametrize("T,live", [(700, 699), (2050, 2049)])
+@pytest.mark.parametrize("kind", ["halves", "adjacent"])
+def test_many_tokens_are_stored_as_few_are(T, live, kind):
+    """Calls of many tokens take other launch shapes: the same bytes as calls of fifty."""
+    import torch
+    rng = np.random.default_rng(T)
+    geo, Hq = (40, 64, 2, 64), 5
+    n_pages, P, Hkv, D = geo
+    x = torch.from_numpy(rows(rng, T, Hq + 2 * Hkv, D, "f32").reshape(T, -1)).cuda()
+    width = x.shape[1]
+    slots = torch.from_numpy(rng.permutation(n_pages * P)[:T].astype(np.int32)).cuda()
+    pos = torch.from_numpy(rng.integers(0, 100000, (2, T)).astype(np.int32)).cuda()
+    freqs = torch.from_numpy(rng.uniform(0, 1, (2, 24)).astype(np.float32)).cuda()
+    got = []
+    for step in (T, 50):
+        pages = torch.full((n_pages * qk.qk_kv_page_bytes(P, Hkv, D),), 0x5A, dtype=torch.uint8, device="cuda")
+        q = torch.full((T, Hq * D), float("nan"), device="cuda")
+        for t in range(0, T, step):
+            n = min(step, T - t)
+            part = pos[:, t:t + n].contiguous()
+            lv = torch.tensor([live - t], dtype=torch.int32, device="cuda")
+            qk.qk_kv_append(qk.make_kv_cache(pages, *geo), "f32", x[t:], width, Hq, x[t:, Hq * D:], width,
+                            x[t:, (Hq + Hkv) * D:], width, n, slots[t:], qk.make_rope(kind, 48, 2, part, freqs), "f32", q[t:],
+                            Hq * D, lv)
+            torch.cuda.synchronize()
+        got.append((pages, q))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1][:live], got[1][1][:live])
+    assert torch.isnan(got[0][1][live:]).all()
+
+
 def test_pages_past_four_gigabytes():
     """Offsets past 32 bits: a cache of 4.5 GB, its first and last pages."""
     import torch
