@@ -281,6 +281,90 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
     return *reinterpret_cast<const uint32_t *>(&r);
 }
 
+// Eight elements of a row, as loaded.
+template <typename Q>
+struct Row8 {
+    float4 a, b;
+    __device__ __forceinline__ void clear() { a = b = make_float4(0.0f, 0.0f, 0.0f, 0.0f); }
+    __device__ __forceinline__ void load(const float *p, bool wide) {
+        a = load_row4(p, wide);
+        b = load_row4(p + 4, wide);
+    }
+    __device__ __forceinline__ float4 low() const { return a; }
+    __device__ __forceinline__ float4 high() const { return b; }
+};
+template <>
+struct Row8<__nv_bfloat16> {
+    uint2 a, b;
+    __device__ __forceinline__ void clear() { a = b = make_uint2(0, 0); }
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p, bool wide) {
+        a = load_bf16x4(p, wide);
+        b = load_bf16x4(p + 4, wide);
+    }
+    __device__ __forceinline__ float4 low() const { return bf16x4(a); }
+    __device__ __forceinline__ float4 high() const { return bf16x4(b); }
+};
+// 16 rows of a tile's queries, from row `row` on: binary16 of q / 2^e with 2^e above the row's largest magnitude, and what
+// the scores are multiplied with, scale * log2 e * 2^e. `first`: the sequence's first row, `rho`: the tile's first of its
+// rows_all rows (token, head).
+template <int D, typename Q>
+__device__ __forceinline__ void load_queries(const PrefillArgs &p, const Q *q, int first, int h, int rho, int rows_all,
+                                             int row, uint8_t *tile, float *factor) {
+    constexpr int LANES = D / 8, TURN = 32 / LANES;   // of a row; rows of a turn
+    const int lane = threadIdx.x & 31, unit = lane % LANES;
+    constexpr int AHEAD = (sizeof(Q) == 2 ? 8 : 4) < 16 / TURN ? (sizeof(Q) == 2 ? 8 : 4) : 16 / TURN;   // turns loaded together
+#pragma unroll 1
+    for (int x0 = 0; x0 < 16; x0 += TURN * AHEAD) {
+        Row8<Q> v[AHEAD];
+#pragma unroll
+        for (int x = 0; x < AHEAD; x++) {
+            const int r = rho + row + x0 + x * TURN + lane / LANES;
+            v[x].clear();
+            if (r < rows_all) {
+                const int token = r / p.G, head = h * p.G + r - token * p.G;
+                v[x].load(q + (int64_t)(first + token) * p.a.q_stride + (int64_t)head * D + 8 * unit, p.q_wide);
+            }
+        }
+#pragma unroll
+        for (int x = 0; x < AHEAD; x++) {
+            const int r = row + x0 + x * TURN + lane / LANES;
+            const float4 a = v[x].low(), c = v[x].high();
+            float top = fmaxf(fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(a.z), fabsf(a.w))),
+                              fmaxf(fmaxf(fabsf(c.x), fabsf(c.y)), fmaxf(fabsf(c.z), fabsf(c.w))));
+#pragma unroll
+            for (int m = 1; m < LANES; m <<= 1) top = fmaxf(top, __shfl_xor_sync(FULL, top, m));
+            // (the inverse of the power of two stays a normal number)
+            const int e = min(max((int)(__float_as_uint(top) >> 23) - 126, -100), 100);
+            const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+            if (unit == 0) factor[r] = fmaxf(p.a.scale * LOG2E * __uint_as_float((uint32_t)(127 + e) << 23), 0x1p-126f);
+            *reinterpret_cast<uint4 *>(tile + (unit / 8) * ROWS * 128 + r * 128 + (((unit & 7) ^ (r & 7)) << 4)) =
+                make_uint4(pack2(a.x * down, a.y * down), pack2(a.z * down, a.w * down), pack2(c.x * down, c.y * down),
+                           pack2(c.z * down, c.w * down));
+        }
+    }
+}
+
+// A warp's 32 rows of W bytes, put into shared memory a row a lane, to global memory: 16 bytes a lane, whole rows a store.
+// A row's unit c is at c ^ (row % units) so that neither side meets bank conflicts. base + off: the lane's own row.
+template <int CH>
+__device__ __forceinline__ uint8_t *staged(uint8_t *rows, int row, int c) {
+    return rows + row * CH + ((c ^ (row % (CH / 16))) << 4);
+}
+template <int CH, int W>
+__device__ __forceinline__ void store_rows(uint8_t *rows, uint8_t *base, int64_t off, bool there) {
+    constexpr int LANES = W / 16;
+    const int lane = threadIdx.x & 31;
+    __syncwarp();
+#pragma unroll 4
+    for (int r0 = 0; r0 < 32; r0 += 32 / LANES) {
+        const int r = r0 + lane / LANES, c = lane % LANES;
+        const uint4 v = *reinterpret_cast<const uint4 *>(staged<CH>(rows, r, c));
+        const int64_t o = __shfl_sync(FULL, off, r);
+        if (__shfl_sync(FULL, (int)there, r)) *reinterpret_cast<uint4 *>(base + o + 16 * c) = v;
+    }
+    __syncwarp();
+}
+
 template <int D>
 struct Shape {
     static constexpr int TILES = D == 256 ? 1 : 2;       // row tiles of a CTA
@@ -443,54 +527,20 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) attn_prefill_kernel(cons
         const int i = warp / 8, quad = warp & 3, hf = warp / 4 % 2, r = 32 * quad + lane;
         const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
         const uint32_t st = lanes + 128 * i, ot = lanes + Z::O_TMEM + D * i;
-        // queries: eight rows a warp and turn, four lanes a row, its power of two taken out, in the layout of a K-major
-        // operand
+        // queries: eight columns a lane, so that a load takes whole rows; a row's power of two taken out; in the layout of a
+        // K-major operand
         if (steps > 0) {
-            const int unit0 = lane & 3;
-#pragma unroll 1
-            for (int x = 0; x < 2; x++) {
-                const int row = 32 * quad + 16 * hf + 8 * x + (lane >> 2), rho = row0 + i * ROWS + row;
-                const bool there = rho < rows_all;
-                const int token = there ? rho / p.G : 0, head = h * p.G + (there ? rho - token * p.G : 0);
-                const int64_t at = (int64_t)(sq.first + token) * p.a.q_stride + (int64_t)head * D + 8 * unit0;
-                float4 v[D / 32][2];
-                float top = 0.0f;
-#pragma unroll
-                for (int e = 0; e < D / 32; e++)
-#pragma unroll
-                    for (int f = 0; f < 2; f++) {
-                        const int64_t o = at + 32 * e + 4 * f;
-                        v[e][f] = p.a.q_elem == QK_ELEM_F32 ? load_row4(static_cast<const float *>(p.a.q) + o, p.q_wide)
-                                                            : load_row4(static_cast<const __nv_bfloat16 *>(p.a.q) + o, p.q_wide);
-                    }
-#pragma unroll
-                for (int e = 0; e < D / 32; e++)
-#pragma unroll
-                    for (int f = 0; f < 2; f++) {
-                        if (!there) v[e][f] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                        top = fmaxf(top, fmaxf(fmaxf(fabsf(v[e][f].x), fabsf(v[e][f].y)), fmaxf(fabsf(v[e][f].z), fabsf(v[e][f].w))));
-                    }
-                top = fmaxf(top, __shfl_xor_sync(FULL, top, 1));
-                top = fmaxf(top, __shfl_xor_sync(FULL, top, 2));
-                // 2^e2 is above the largest magnitude; its inverse stays a normal number
-                const int e2 = min(max((int)(__float_as_uint(top) >> 23) - 126, -100), 100);
-                const float down = __uint_as_float((uint32_t)(127 - e2) << 23);
-                if (unit0 == 0)
-                    factor[i * ROWS + row] = fmaxf(p.a.scale * LOG2E * __uint_as_float((uint32_t)(127 + e2) << 23), 0x1p-126f);
-#pragma unroll
-                for (int e = 0; e < D / 32; e++) {
-                    const int unit = 4 * e + unit0;   // of 8 columns
-                    const float4 a = v[e][0], c = v[e][1];
-                    *reinterpret_cast<uint4 *>(smem + i * Z::Q_BYTES + (unit / 8) * ROWS * 128 + row * 128 + (((unit & 7) ^ (row & 7)) << 4)) =
-                        make_uint4(pack2(a.x * down, a.y * down), pack2(a.z * down, a.w * down), pack2(c.x * down, c.y * down),
-                                   pack2(c.z * down, c.w * down));
-                }
-            }
+            if (p.a.q_elem == QK_ELEM_F32)
+                load_queries<D>(p, static_cast<const float *>(p.a.q), sq.first, h, row0 + i * ROWS, rows_all, 32 * quad + 16 * hf,
+                                smem + i * Z::Q_BYTES, factor + i * ROWS);
+            else
+                load_queries<D>(p, static_cast<const __nv_bfloat16 *>(p.a.q), sq.first, h, row0 + i * ROWS, rows_all,
+                                32 * quad + 16 * hf, smem + i * Z::Q_BYTES, factor + i * ROWS);
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             mbar_arrive(q_full);
         }
-        // the 256 threads of a tile meet
-        const auto meet = [&]() { asm volatile("bar.sync %0, 256;" ::"r"(1 + i) : "memory"); };
+        // the two warps of 32 rows meet (what one reads of tensor memory and the other writes are these rows' lanes)
+        const auto meet = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + 4 * i + quad) : "memory"); };
         meet();   // the factors are written
         float *const mine = reinterpret_cast<float *>(smem + Z::OFF_TOP) + (i * 2 + hf) * 2 * ROWS + r;
         const float *const other = reinterpret_cast<float *>(smem + Z::OFF_TOP) + (i * 2 + 1 - hf) * 2 * ROWS + r;
@@ -587,6 +637,21 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) attn_prefill_kernel(cons
         sum += other[(steps & 1) * ROWS];
         if (ok && steps > 0) ok = __all_sync(FULL, mbar_wait(o_full + 8 * i, 0));
         tc_fence_after();
+        // Rows go through the shared memory of the tile's queries, which no product reads any more: D bytes a row for each warp,
+        // half a head in bfloat16 or codes, a quarter of one in binary32.
+        constexpr int CH = D;
+        uint8_t *const rows = smem + i * Z::Q_BYTES + (warp & 7) * 32 * CH;
+        const auto store_block = [&](const float (&y)[32], uint8_t *base, int64_t off, bool mine) {   // binary32
+            constexpr int PIECE = CH < 128 ? 16 : 32;   // (at D = 64 a row has 64 bytes)
+#pragma unroll
+            for (int x0 = 0; x0 < 32; x0 += PIECE) {
+#pragma unroll
+                for (int x = 0; x < PIECE; x += 4)
+                    *reinterpret_cast<float4 *>(staged<CH>(rows, lane, x / 4)) =
+                        make_float4(y[x0 + x], y[x0 + x + 1], y[x0 + x + 2], y[x0 + x + 3]);
+                store_rows<CH, PIECE * 4>(rows, base, off + x0 * 4, mine);
+            }
+        };
         if (p.parts > 1) {   // what this share of the keys gives; attn_join_kernel goes on
             const int64_t at = (int64_t)blockIdx.x * CTA_ROWS + i * ROWS + r;
             if (hf == 0 && there && ok) p.part_ml[at] = make_float2(ref == -INFINITY ? -INFINITY : off, sum);
@@ -595,12 +660,10 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) attn_prefill_kernel(cons
                 uint32_t v[32];
                 tmem_ld32(ot + 32 * k, v);
                 tmem_wait_ld(v);
-                if (there && ok) {
-                    uint4 *to = reinterpret_cast<uint4 *>(p.part_o + at * D + 32 * k);
+                float y[32];
 #pragma unroll
-                    for (int x = 0; x < 8; x++) to[x] = make_uint4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
-                }
-                __syncwarp();   // whole warps load from tensor memory
+                for (int x = 0; x < 32; x++) y[x] = __uint_as_float(v[x]);
+                store_block(y, reinterpret_cast<uint8_t *>(p.part_o), (at * D + 32 * k) * 4, there && ok);
             }
         } else {
             if (p.a.sinks) {
@@ -613,62 +676,92 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) attn_prefill_kernel(cons
             }
             const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
             const int64_t row = sq.first + token;
-#pragma unroll 1
-            for (int k = hf * NB / 2; k < (hf + 1) * NB / 2; k++) {
-                float y[32];
+            const bool any = steps > 0 && inv > 0.0f, mine_ok = there && ok;
+            const int k0 = hf * NB / 2;
+            const auto block_of = [&](int k, float (&y)[32]) {
                 if (steps > 0) {
                     uint32_t v[32];
                     tmem_ld32(ot + 32 * k, v);
                     tmem_wait_ld(v);
 #pragma unroll
-                    for (int x = 0; x < 32; x++) y[x] = inv > 0.0f ? __uint_as_float(v[x]) * inv : 0.0f;
+                    for (int x = 0; x < 32; x++) y[x] = any ? __uint_as_float(v[x]) * inv : 0.0f;
                 } else {
 #pragma unroll
                     for (int x = 0; x < 32; x++) y[x] = 0.0f;
                 }
-                if (there && ok) {
-                    const int64_t at = row * p.a.out_stride + (int64_t)head * D + 32 * k;
-                    if (p.a.out && p.a.out_elem == QK_ELEM_F32) {
+            };
+            const int64_t at = row * p.a.out_stride + (int64_t)head * D + 32 * k0;
+            if (p.a.out && p.a.out_elem == QK_ELEM_BF16) {
+                uint16_t *const out = static_cast<uint16_t *>(p.a.out);
+#pragma unroll 1
+                for (int k = 0; k < NB / 2; k++) {
+                    float y[32];
+                    block_of(k0 + k, y);
 #pragma unroll
-                        for (int x = 0; x < 32; x += 4)
-                            store_row4(static_cast<float *>(p.a.out) + at + x, make_float4(y[x], y[x + 1], y[x + 2], y[x + 3]), p.out_wide);
-                    } else if (p.a.out) {
+                    for (int x = 0; x < 32; x += 8) {
+                        const uint4 w = make_uint4(bf16x2(y[x], y[x + 1]), bf16x2(y[x + 2], y[x + 3]), bf16x2(y[x + 4], y[x + 5]),
+                                                   bf16x2(y[x + 6], y[x + 7]));
+                        if (p.out16) {
+                            *reinterpret_cast<uint4 *>(staged<CH>(rows, lane, 4 * k + x / 8)) = w;
+                        } else if (mine_ok) {
+                            const uint32_t words[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-                        for (int x = 0; x < 32; x += 8) {
-                            __nv_bfloat16 *to = static_cast<__nv_bfloat16 *>(p.a.out) + at + x;
-                            if (p.out16) {
-                                *reinterpret_cast<uint4 *>(to) = make_uint4(bf16x2(y[x], y[x + 1]), bf16x2(y[x + 2], y[x + 3]),
-                                                                            bf16x2(y[x + 4], y[x + 5]), bf16x2(y[x + 6], y[x + 7]));
-                            } else {
-                                store_row4(to, make_float4(y[x], y[x + 1], y[x + 2], y[x + 3]), p.out_wide);
-                                store_row4(to + 4, make_float4(y[x + 4], y[x + 5], y[x + 6], y[x + 7]), p.out_wide);
-                            }
+                            for (int e = 0; e < 8; e++) out[at + 32 * k + x + e] = (uint16_t)(words[e / 2] >> (16 * (e & 1)));
                         }
                     }
-                    if (p.qs) {
-                        float m = 0.0f;
+                    __syncwarp();   // whole warps load from tensor memory
+                }
+                if (p.out16) store_rows<CH, CH>(rows, static_cast<uint8_t *>(p.a.out), at * 2, mine_ok);
+            } else if (p.a.out) {
+#pragma unroll 1
+                for (int k = 0; k < NB / 2; k++) {
+                    float y[32];
+                    block_of(k0 + k, y);
+                    float *const out = static_cast<float *>(p.a.out) + at + 32 * k;
+                    if (p.out_wide) {
+                        store_block(y, static_cast<uint8_t *>(p.a.out), (at + 32 * k) * 4, mine_ok);
+                    } else {
+                        if (mine_ok)
 #pragma unroll
-                        for (int x = 0; x < 32; x++) m = fmaxf(m, fabsf(y[x]));
-                        const float d = m / 127.0f, r = 1.0f / d;
-                        const int64_t block = row * p.row_blocks + head * NB + k;
-                        uint32_t w[8];
-#pragma unroll
-                        for (int x = 0; x < 32; x++) {
-                            // rint(y / d): the product with 1 / d is within 127 * 2^-22 of the quotient, so a division next
-                            // to ties alone
-                            const float z = y[x] * r;
-                            float code_f = rintf(z);
-                            if (fabsf(fabsf(z - code_f) - 0.5f) < 1e-4f || m < 0x1p-100f) code_f = rintf(y[x] / d);
-                            const int code = m != 0.0f ? (int)code_f : 0;
-                            w[x / 4] = x % 4 ? w[x / 4] | (uint32_t)(code & 255) << (8 * (x % 4)) : (uint32_t)(code & 255);
-                        }
-                        uint4 *to = reinterpret_cast<uint4 *>(p.qs + block * QB);
-                        to[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                        to[1] = make_uint4(w[4], w[5], w[6], w[7]);
-                        p.d[block] = __half_as_ushort(__float2half_rn(d));
+                            for (int x = 0; x < 32; x++) out[x] = y[x];
+                        __syncwarp();   // whole warps load from tensor memory
                     }
                 }
-                __syncwarp();   // whole warps load from tensor memory
+            }
+            if (p.qs) {
+                const int64_t block0 = row * p.row_blocks + head * NB + k0;
+#pragma unroll 1
+                for (int k = 0; k < NB / 2; k++) {
+                    float y[32], m = 0.0f;
+                    block_of(k0 + k, y);
+#pragma unroll
+                    for (int x = 0; x < 32; x++) m = fmaxf(m, fabsf(y[x]));
+                    const float d = m / 127.0f, rcp = 1.0f / d;
+                    // rint(y / d): the product with 1 / d is within 127 * 2^-22 of the quotient, so divisions only where one
+                    // of the block is next to a tie
+                    bool tie = m < 0x1p-100f;
+                    uint32_t w[8] = {};
+#pragma unroll
+                    for (int x = 0; x < 32; x++) {
+                        const float z = y[x] * rcp, code = rintf(z);
+                        tie |= fabsf(fabsf(z - code) - 0.5f) < 1e-4f;
+                        w[x / 4] |= (uint32_t)((int)code & 255) << (8 * (x % 4));
+                    }
+                    if (tie) {
+#pragma unroll
+                        for (int x = 0; x < 32; x += 4) {
+                            w[x / 4] = 0;
+#pragma unroll
+                            for (int e = 0; e < 4; e++)
+                                if (m != 0.0f) w[x / 4] |= (uint32_t)((int)rintf(y[x + e] / d) & 255) << (8 * e);
+                        }
+                    }
+                    *reinterpret_cast<uint4 *>(staged<CH>(rows, lane, 2 * k)) = make_uint4(w[0], w[1], w[2], w[3]);
+                    *reinterpret_cast<uint4 *>(staged<CH>(rows, lane, 2 * k + 1)) = make_uint4(w[4], w[5], w[6], w[7]);
+                    if (mine_ok) p.d[block0 + k] = __half_as_ushort(__float2half_rn(d));
+                    __syncwarp();   // whole warps load from tensor memory
+                }
+                store_rows<CH, CH / 2>(rows, reinterpret_cast<uint8_t *>(p.qs), block0 * QB, mine_ok);
             }
             if (p.qs && there && ok && hf && head == p.a.n_heads - 1)   // the blocks behind the heads
                 for (int64_t block = row * p.row_blocks + p.a.n_heads * NB; block < (row + 1) * p.row_blocks; block++) {

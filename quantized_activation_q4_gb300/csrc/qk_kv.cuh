@@ -44,18 +44,16 @@ __device__ __forceinline__ float4 load_row4(const float *p, bool wide) {
     if (wide) return ld_prev(reinterpret_cast<const float4 *>(p));
     return make_float4(ld_prev(p), ld_prev(p + 1), ld_prev(p + 2), ld_prev(p + 3));
 }
-__device__ __forceinline__ float4 load_row4(const __nv_bfloat16 *p, bool wide) {
+__device__ __forceinline__ uint2 load_bf16x4(const __nv_bfloat16 *p, bool wide) {
     const uint16_t *s = reinterpret_cast<const uint16_t *>(p);
-    uint2 v;
-    if (wide) {
-        v = ld_prev(reinterpret_cast<const uint2 *>(p));
-    } else {
-        v.x = ld_prev(s) | (uint32_t)ld_prev(s + 1) << 16;
-        v.y = ld_prev(s + 2) | (uint32_t)ld_prev(s + 3) << 16;
-    }
+    if (wide) return ld_prev(reinterpret_cast<const uint2 *>(p));
+    return make_uint2(ld_prev(s) | (uint32_t)ld_prev(s + 1) << 16, ld_prev(s + 2) | (uint32_t)ld_prev(s + 3) << 16);
+}
+__device__ __forceinline__ float4 bf16x4(uint2 v) {
     return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u), __uint_as_float(v.y << 16),
                        __uint_as_float(v.y & 0xffff0000u));
 }
+__device__ __forceinline__ float4 load_row4(const __nv_bfloat16 *p, bool wide) { return bf16x4(load_bf16x4(p, wide)); }
 __device__ __forceinline__ void store_row4(float *p, float4 v, bool wide) {
     if (wide) {
         *reinterpret_cast<float4 *>(p) = v;
