@@ -299,11 +299,16 @@ attn_decode_kernel(const __grid_constant__ DecodeArgs p, bool wide) {
     pdl_wait();
     const int live = live_rows(p.live, p.B);
 
-    // tiles of all sequences, then the place of this share's first
-    int64_t total = 0, before = 0;
-    for (int b0 = 0; b0 < live; b0 += WARPS * 32) {
+    // Tiles of all sequences, then the place of this share's first. Of up to WARPS * 32 sequences a thread keeps its own
+    // from the one look to the other. (Lengths are loaded beside the live count.)
+    int64_t total = 0, before = 0, n = 0;
+    const auto tiles_of = [&](int b) {
+        const int tiles = b < p.B ? sequence_of(p, b).tiles : 0;
+        return b < live ? (int64_t)tiles * p.c.Hkv : 0;
+    };
+    for (int b0 = 0; b0 < p.B; b0 += WARPS * 32) {
         const int b = b0 + threadIdx.x;
-        const int64_t n = b < live ? (int64_t)sequence_of(p, b).tiles * p.c.Hkv : 0;
+        n = tiles_of(b);
         const int64_t sum = scan_cta(n, &before, scan);
         if (blockIdx.x == 0 && b < live) p.plan[1 + b] = total + before;
         total += sum;
@@ -315,10 +320,13 @@ attn_decode_kernel(const __grid_constant__ DecodeArgs p, bool wide) {
     if (left <= 0) return;
     {
         int64_t at = 0;
-        for (int b0 = 0; b0 < live; b0 += WARPS * 32) {
+        for (int b0 = 0; b0 < p.B; b0 += WARPS * 32) {
             const int b = b0 + threadIdx.x;
-            const int64_t n = b < live ? (int64_t)sequence_of(p, b).tiles * p.c.Hkv : 0;
-            const int64_t sum = scan_cta(n, &before, scan);
+            int64_t sum = total;
+            if (p.B > WARPS * 32) {
+                n = tiles_of(b);
+                sum = scan_cta(n, &before, scan);
+            }
             if (first >= at + before && first < at + before + n) {
                 found[0] = b;
                 found[1] = first - at - before;
@@ -662,16 +670,19 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) attn_combine_kernel(const __g
     const DecodeArgs &p = a.p;
     const int head = blockIdx.x, row = blockIdx.y * gridDim.z + blockIdx.z;
     const int b = row / p.T, i = row % p.T, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    if (b >= p.B || b >= live_rows(p.live, p.B)) return;
+    if (b >= p.B) return;
     const int h = head / p.G, col = i * p.G + head % p.G;
+    // (loaded together: the live count, the length, the sink and the plan, which holds something for live sequences alone)
+    const int live = live_rows(p.live, p.B);
     const Sequence s = sequence_of(p, b);
     const float sink = p.a.sinks ? ld_prev(p.a.sinks + head) * LOG2E : -INFINITY;
+    const int64_t each = ld_prev(p.plan), tiles_before = ld_prev(p.plan + 1 + b);
+    if (b >= live) return;
     float top = -INFINITY, l = 0.0f, o[NB];
 #pragma unroll
     for (int k = 0; k < NB; k++) o[k] = 0.0f;
     if (s.tiles > 0) {
-        const int64_t each = ld_prev(p.plan);
-        const int64_t lo = ld_prev(p.plan + 1 + b) + (int64_t)h * s.tiles;
+        const int64_t lo = tiles_before + (int64_t)h * s.tiles;
         const int64_t c0 = lo / each, c1 = (lo + s.tiles - 1) / each;
         const int64_t seg = (int64_t)b * p.c.Hkv + h;
         const int n = col / 8, cg = n / a.NT, in = n % a.NT * 8 + col % 8;
