@@ -658,13 +658,15 @@ struct JoinArgs {
     int64_t row_blocks;
     int NT;
 };
-// One CTA per (row, query head): its head's partial results in order, four at a time; then rows and image.
+// One CTA per (row, query head): the statistics of all partial results first, then their outputs in order, four warps side
+// by side with several loads under way; then rows and image.
 constexpr int JOIN_WARPS = 4;
 template <int D>
 __global__ void __launch_bounds__(JOIN_WARPS * 32) attn_combine_kernel(const __grid_constant__ JoinArgs a) {
     constexpr int NB = D / 32;
     __shared__ float part[JOIN_WARPS][D];
-    __shared__ float2 stat[JOIN_WARPS];
+    __shared__ float2 stat[MAX_CTAS];   // maximum and sum, then the factor, of each partial result
+    __shared__ float reduce[JOIN_WARPS];
     pdl_trigger();
     pdl_wait();
     const DecodeArgs &p = a.p;
@@ -678,46 +680,58 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) attn_combine_kernel(const __g
     const float sink = p.a.sinks ? ld_prev(p.a.sinks + head) * LOG2E : -INFINITY;
     const int64_t each = ld_prev(p.plan), tiles_before = ld_prev(p.plan + 1 + b);
     if (b >= live) return;
-    float top = -INFINITY, l = 0.0f, o[NB];
+    const int64_t lo = tiles_before + (int64_t)h * s.tiles, c0 = s.tiles > 0 ? lo / each : 0;
+    const int count = s.tiles > 0 ? (int)((lo + s.tiles - 1) / each - c0) + 1 : 0;
+    const int n = col / 8, cg = n / a.NT;
+    const int64_t step = (int64_t)p.groups * a.NT * 8;   // from one partial result to the next
+    const int64_t at = (((int64_t)b * p.c.Hkv + h + c0) * p.groups + cg) * a.NT * 8 + n % a.NT * 8 + col % 8;
+    const auto over_cta = [&](float v, bool largest) {
+#pragma unroll
+        for (int m = 16; m; m >>= 1) {
+            const float w = __shfl_xor_sync(FULL, v, m);
+            v = largest ? fmaxf(v, w) : v + w;
+        }
+        __syncthreads();
+        if (lane == 0) reduce[warp] = v;
+        __syncthreads();
+        v = reduce[0];
+#pragma unroll
+        for (int w = 1; w < JOIN_WARPS; w++) v = largest ? fmaxf(v, reduce[w]) : v + reduce[w];
+        return v;
+    };
+    float top = sink;
+    for (int c = threadIdx.x; c < count; c += JOIN_WARPS * 32) {
+        const float2 v = make_float2(ld_prev(&p.ml[at + c * step].x), ld_prev(&p.ml[at + c * step].y));
+        stat[c] = v;
+        top = fmaxf(top, v.x);
+    }
+    top = over_cta(top, true);
+    float total = 0.0f;
+    for (int c = threadIdx.x; c < count; c += JOIN_WARPS * 32) {
+        const float2 v = stat[c];
+        const float f = v.x == -INFINITY ? 0.0f : ex2(v.x - top);
+        stat[c].x = f;
+        total = fmaf(v.y, f, total);
+    }
+    total = over_cta(total, false);   // (the barriers in it also end the writing of the factors)
+    if (sink != -INFINITY) total += ex2(sink - top);
+    const float inv = total > 0.0f ? 1.0f / total : 0.0f;
+    float o[NB];
 #pragma unroll
     for (int k = 0; k < NB; k++) o[k] = 0.0f;
-    if (s.tiles > 0) {
-        const int64_t lo = tiles_before + (int64_t)h * s.tiles;
-        const int64_t c0 = lo / each, c1 = (lo + s.tiles - 1) / each;
-        const int64_t seg = (int64_t)b * p.c.Hkv + h;
-        const int n = col / 8, cg = n / a.NT, in = n % a.NT * 8 + col % 8;
-        const auto at = [&](int64_t c) { return ((seg + c) * p.groups + cg) * a.NT * 8 + in; };
-        for (int64_t c = c0 + warp; c <= c1; c += JOIN_WARPS) {
-            const float m = ld_prev(&p.ml[at(c)].x), v = ld_prev(&p.ml[at(c)].y);
-            float x[NB];
+#pragma unroll 4
+    for (int c = warp; c < count; c += JOIN_WARPS) {
+        const float f = stat[c].x;
 #pragma unroll
-            for (int k = 0; k < NB; k++) x[k] = ld_prev(p.acc + at(c) * D + 32 * k + lane);
-            if (m == -INFINITY) continue;
-            const float now = fmaxf(top, m), old = top == -INFINITY ? 0.0f : ex2(top - now), f = ex2(m - now);
-            top = now;
-            l = l * old + v * f;
-#pragma unroll
-            for (int k = 0; k < NB; k++) o[k] = o[k] * old + x[k] * f;
-        }
+        for (int k = 0; k < NB; k++) o[k] = fmaf(ld_prev(p.acc + (at + c * step) * D + 32 * k + lane), f, o[k]);
     }
 #pragma unroll
     for (int k = 0; k < NB; k++) part[warp][32 * k + lane] = o[k];
-    if (lane == 0) stat[warp] = make_float2(top, l);
     __syncthreads();
-    top = sink;
-#pragma unroll
-    for (int w = 0; w < JOIN_WARPS; w++) top = fmaxf(top, stat[w].x);
-    float f[JOIN_WARPS], total = sink == -INFINITY ? 0.0f : ex2(sink - top);
-#pragma unroll
-    for (int w = 0; w < JOIN_WARPS; w++) {
-        f[w] = stat[w].x == -INFINITY ? 0.0f : ex2(stat[w].x - top);
-        total = fmaf(stat[w].y, f[w], total);
-    }
-    const float inv = total > 0.0f ? 1.0f / total : 0.0f;
     for (int k = warp; k < NB; k += JOIN_WARPS) {
         float y = 0.0f;
 #pragma unroll
-        for (int w = 0; w < JOIN_WARPS; w++) y = fmaf(part[w][32 * k + lane], f[w], y);
+        for (int w = 0; w < JOIN_WARPS; w++) y += part[w][32 * k + lane];
         y *= inv;
         const int64_t to = row * p.a.out_stride + (int64_t)head * D + 32 * k + lane;
         if (p.a.out && p.a.out_elem == QK_ELEM_F32) static_cast<float *>(p.a.out)[to] = y;

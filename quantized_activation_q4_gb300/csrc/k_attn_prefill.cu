@@ -791,20 +791,38 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
     const int rho = w.y * CTA_ROWS + r;
     if (rho >= sq.n * p.G) return;
     const int token = rho / p.G, head = h * p.G + rho % p.G;
-    float top = p.a.sinks ? ld_prev(p.a.sinks + head) * LOG2E : -INFINITY, o[NB];
-    float sum = top == -INFINITY ? 0.0f : 1.0f;
+    const float sink = p.a.sinks ? ld_prev(p.a.sinks + head) * LOG2E : -INFINITY;
+    const int64_t at = (int64_t)blockIdx.x * p.parts * CTA_ROWS + r;
+    float top = sink, sum = 0.0f, o[NB];
 #pragma unroll
     for (int k = 0; k < NB; k++) o[k] = 0.0f;
-    for (int i = 0; i < p.parts; i++) {
-        const int64_t at = ((int64_t)blockIdx.x * p.parts + i) * CTA_ROWS + r;
-        const float m = ld_prev(&p.part_ml[at].x), v = ld_prev(&p.part_ml[at].y);
-        if (m == -INFINITY) continue;
-        const float now = fmaxf(top, m), old = top == -INFINITY ? 0.0f : ex2(top - now), f = ex2(m - now);
-        top = now;
-        sum = sum * old + v * f;
+    for (int i0 = 0; i0 < p.parts; i0 += 32) {   // a lane a share
+        const bool mine = i0 + lane < p.parts;
+        const float2 *ml = p.part_ml + at + (int64_t)(i0 + lane) * CTA_ROWS;
+        const float m = mine ? ld_prev(&ml->x) : -INFINITY, l = mine ? ld_prev(&ml->y) : 0.0f;
+        float now = m;
 #pragma unroll
-        for (int k = 0; k < NB; k++) o[k] = o[k] * old + ld_prev(p.part_o + at * D + 32 * k + lane) * f;
+        for (int x = 16; x; x >>= 1) now = fmaxf(now, __shfl_xor_sync(FULL, now, x));
+        now = fmaxf(now, top);
+        if (now == -INFINITY) continue;
+        const float old = top == -INFINITY ? 0.0f : ex2(top - now), f = m == -INFINITY ? 0.0f : ex2(m - now);
+        top = now;
+        float add = l * f;
+#pragma unroll
+        for (int x = 16; x; x >>= 1) add += __shfl_xor_sync(FULL, add, x);
+        sum = fmaf(sum, old, add);
+#pragma unroll
+        for (int k = 0; k < NB; k++) o[k] *= old;
+        const int some = min(32, p.parts - i0);
+#pragma unroll 4
+        for (int i = 0; i < some; i++) {
+            const float g = __shfl_sync(FULL, f, i);
+            const float *from = p.part_o + (at + (int64_t)(i0 + i) * CTA_ROWS) * D + lane;
+#pragma unroll
+            for (int k = 0; k < NB; k++) o[k] = fmaf(g > 0.0f ? ld_prev(from + 32 * k) : 0.0f, g, o[k]);   // (a share without keys has no outputs)
+        }
     }
+    if (sink != -INFINITY) sum += ex2(sink - top);
     const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
     const int64_t row = sq.first + token;
 #pragma unroll
