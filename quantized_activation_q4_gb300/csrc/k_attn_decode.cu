@@ -660,12 +660,14 @@ struct JoinArgs {
 };
 // One CTA per (row, query head): the statistics of all partial results first, then their outputs in order, four warps side
 // by side with several loads under way; then rows and image.
+// Factors are worked out by every warp that needs one and not kept in shared memory: its CTAs start early, beside those of
+// the pass that leave an SM, and with 3.2 or 10 KB instead of 2.2 they held up the passes of calls in a row (64 sequences of
+// 8192 keys: 94 us a call for 74).
 constexpr int JOIN_WARPS = 4;
 template <int D>
 __global__ void __launch_bounds__(JOIN_WARPS * 32) attn_combine_kernel(const __grid_constant__ JoinArgs a) {
     constexpr int NB = D / 32;
     __shared__ float part[JOIN_WARPS][D];
-    __shared__ float2 stat[MAX_CTAS];   // maximum and sum, then the factor, of each partial result
     __shared__ float reduce[JOIN_WARPS];
     pdl_trigger();
     pdl_wait();
@@ -700,20 +702,18 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) attn_combine_kernel(const __g
         return v;
     };
     float top = sink;
-    for (int c = threadIdx.x; c < count; c += JOIN_WARPS * 32) {
-        const float2 v = make_float2(ld_prev(&p.ml[at + c * step].x), ld_prev(&p.ml[at + c * step].y));
-        stat[c] = v;
-        top = fmaxf(top, v.x);
-    }
+    for (int c = threadIdx.x; c < count; c += JOIN_WARPS * 32) top = fmaxf(top, ld_prev(&p.ml[at + c * step].x));
     top = over_cta(top, true);
     float total = 0.0f;
+    const auto factor = [&](int c) {
+        const float m = ld_prev(&p.ml[at + c * step].x);
+        return m == -INFINITY ? 0.0f : ex2(m - top);
+    };
     for (int c = threadIdx.x; c < count; c += JOIN_WARPS * 32) {
-        const float2 v = stat[c];
-        const float f = v.x == -INFINITY ? 0.0f : ex2(v.x - top);
-        stat[c].x = f;
-        total = fmaf(v.y, f, total);
+        const float f = factor(c);
+        total = fmaf(ld_prev(&p.ml[at + c * step].y), f, total);
     }
-    total = over_cta(total, false);   // (the barriers in it also end the writing of the factors)
+    total = over_cta(total, false);
     if (sink != -INFINITY) total += ex2(sink - top);
     const float inv = total > 0.0f ? 1.0f / total : 0.0f;
     float o[NB];
@@ -721,7 +721,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) attn_combine_kernel(const __g
     for (int k = 0; k < NB; k++) o[k] = 0.0f;
 #pragma unroll 4
     for (int c = warp; c < count; c += JOIN_WARPS) {
-        const float f = stat[c].x;
+        const float f = factor(c);
 #pragma unroll
         for (int k = 0; k < NB; k++) o[k] = fmaf(ld_prev(p.acc + (at + c * step) * D + 32 * k + lane), f, o[k]);
     }
