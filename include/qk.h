@@ -137,7 +137,8 @@ QK_API uint64_t qk_launch_count(void);
  * Device-side fault word of the current device, then cleared. Bit 0: a
  * kernel's bounded wait on a shared-memory barrier gave up (the kernel then
  * stopped early and its outputs are not valid). Covers qk_mmvq, qk_mmvq_id,
- * qk_mmq and qk_mmq_id, each with its variants. Bit 1: a routed projection's
+ * qk_mmq and qk_mmq_id, each with its variants, qk_attn_decode and
+ * qk_attn_prefill. Bit 1: a routed projection's
  * counts held more passes than any plan of its bucket can (not the output of
  * qk_moe_plan); it did no work.
  * Synchronises the device.
@@ -756,7 +757,7 @@ QK_API qk_status qk_kv_read(const qk_kv_cache *cache, const int32_t *slots, int6
  * the keys below kv_lens[b] - n + i + 1, and with a window only the last `window`
  * of them. For every row and head, over the visible keys:
  *   out = sum_j exp(s_j) v_j / (sum_j exp(s_j) + exp(sink)),  s_j = scale * q . k_j
- * A row that sees no key is 0. Lengths are clamped to what the page table (and
+ * A row that sees no key is 0. NaN in a query row and head makes that row and head NaN. Lengths are clamped to what the page table (and
  * max_kv) can hold; keys on a page outside [0, n_pages) are not visible. What the
  * cache holds behind a sequence's last key may be anything, NaN and infinite
  * scales included.
@@ -771,7 +772,7 @@ typedef struct qk_attn {
     const int32_t *kv_lens;    /* [B] */
     float scale;               /* finite, > 0 */
     int32_t window;            /* 0: none */
-    const float *sinks;        /* [n_heads] extra logits (not scaled), or NULL */
+    const float *sinks;        /* [n_heads] extra logits (not scaled), finite or minus infinity; or NULL */
     void *out;                 /* [rows][out_stride] of type out_elem, or NULL when only the image is wanted */
     int32_t out_elem;          /* qk_elem */
     int32_t reserved;          /* 0 */

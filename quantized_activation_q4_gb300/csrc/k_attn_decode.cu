@@ -395,7 +395,8 @@ attn_decode_kernel(const __grid_constant__ DecodeArgs p, bool wide) {
     int lift_e = 0;       // exponent of the largest value scale so far (0 while all are below 2)
     bool fresh = true;    // a segment begins
     int stage = 0;
-    uint32_t parity = 0;
+    uint32_t parity = 0, late_parity = 0;
+    int late = 0;         // where a wait ran out
     for (;; left--) {
         if (fresh) {
             load_queries<D, NT>(q, p, now.b, now.h, column0, wide);
@@ -416,7 +417,10 @@ attn_decode_kernel(const __grid_constant__ DecodeArgs p, bool wide) {
             lift_e = 0;
             fresh = false;
         }
-        if (ok) ok = __all_sync(FULL, mbar_wait(bar0 + 8 * stage, parity));
+        if (ok) {
+            ok = __all_sync(FULL, mbar_wait(bar0 + 8 * stage, parity));
+            if (!ok) late = stage, late_parity = parity;
+        }
         const uint32_t buf = ring + stage * STAGE;
         const int token0 = now.s.base + now.tile * TILE + warp * WARP_TOKENS;
         const int end0 = now.s.len - p.T + 1;   // keys that the first of the new tokens sees
@@ -646,9 +650,9 @@ attn_decode_kernel(const __grid_constant__ DecodeArgs p, bool wide) {
             parity ^= 1;
         }
     }
-    if (!ok)   // a wait ran out: no copy may land after the CTA has gone
-        for (int s = 0; s < S; s++)
-            if (!mbar_wait(bar0 + 8 * s, parity)) break;
+    if (!ok)   // a wait ran out (nothing was issued since): no copy may land after the CTA has gone
+        for (int k = late; k < late + S; k++)
+            if (!mbar_wait(bar0 + 8 * (k % S), k < S ? late_parity : late_parity ^ 1)) break;
 }
 
 // ---------------------------------------------------------------- joining
@@ -715,7 +719,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) attn_combine_kernel(const __g
     }
     total = over_cta(total, false);
     if (sink != -INFINITY) total += ex2(sink - top);
-    const float inv = total > 0.0f ? 1.0f / total : 0.0f;
+    const float inv = total == 0.0f ? 0.0f : 1.0f / total;   // no key and no sink: 0
     float o[NB];
 #pragma unroll
     for (int k = 0; k < NB; k++) o[k] = 0.0f;
@@ -807,7 +811,7 @@ qk_status launch_attn_decode(const KvCache &c, const qk_attn &a, int B, int T, u
                    : c.D == 64 ? (l.NT == 1 ? launch_pass<64, 1>(p, s) : launch_pass<64, 2>(p, s))
                                : (l.NT == 1 ? launch_pass<128, 1>(p, s) : launch_pass<128, 2>(p, s));
     if (st != QK_OK) return st;
-    const int rows = B * T, z = rows > 65535 ? 128 : 1;
+    const int rows = B * T, z = rows > 65535 ? 256 : 1;
     const JoinArgs j = {p, img, row_blocks, l.NT};
     auto *combine = c.D == 64 ? attn_combine_kernel<64> : c.D == 128 ? attn_combine_kernel<128> : attn_combine_kernel<256>;
     return launch_pdl("attn_combine", combine, dim3(a.n_heads, (unsigned)ceil_div(rows, z), z), dim3(128), 0, s, j);

@@ -672,11 +672,11 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) attn_prefill_kernel(cons
                 const float lead = ref == -INFINITY ? sink : fmaxf(sink, off);
                 const float down = ref == -INFINITY ? 0.0f : ex2(off - lead);
                 const float total = sink == -INFINITY ? sum * down : fmaf(sum, down, ex2(sink - lead));
-                sum = down > 0.0f ? total / down : 0.0f;
+                sum = down == 0.0f ? 0.0f : total / down;
             }
-            const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;   // no key: 0
             const int64_t row = sq.first + token;
-            const bool any = steps > 0 && inv > 0.0f, mine_ok = there && ok;
+            const bool any = steps > 0 && inv != 0.0f, mine_ok = there && ok;
             const int k0 = hf * NB / 2;
             const auto block_of = [&](int k, float (&y)[32]) {
                 if (steps > 0) {
@@ -823,7 +823,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
         }
     }
     if (sink != -INFINITY) sum += ex2(sink - top);
-    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
     const int64_t row = sq.first + token;
 #pragma unroll
     for (int k = 0; k < NB; k++) {

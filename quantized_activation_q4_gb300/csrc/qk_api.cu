@@ -821,6 +821,7 @@ qk_status qk_kv_read(const qk_kv_cache *cache, const int32_t *slots, int64_t n, 
 }
 
 // ------------------------------------------------------------------ attention
+constexpr int32_t MOST_KEYS = 1 << 30;   // of a sequence: places of keys stay inside an int
 struct AttnSpans {
     Span in[6], out;
 };
@@ -843,7 +844,7 @@ static qk_status check_attn(const qk_kv_cache *cache, const qk_attn *a, int64_t 
     const int64_t width = (int64_t)a->n_heads * cache->head_dim;
     REQUIRE(a->q_stride >= width && (!a->out || a->out_stride >= width), QK_ERR_SHAPE, "a stride is smaller than its heads");
     REQUIRE(a->q_stride <= MOST_STRIDE && (!a->out || a->out_stride <= MOST_STRIDE), QK_ERR_ARG, "a stride is out of range");
-    REQUIRE(a->table_stride >= 1 && a->table_stride <= (1 << 30) / cache->page_tokens, QK_ERR_ARG,
+    REQUIRE(a->table_stride >= 1 && a->table_stride <= MOST_KEYS / cache->page_tokens, QK_ERR_ARG,
             "table_stride=%lld out of range (table_stride * page_tokens <= 2^30)", (long long)a->table_stride);
     REQUIRE(!image || row_blocks >= width / QB, QK_ERR_SHAPE, "the image row (%lld blocks) is smaller than the heads",
             (long long)row_blocks);
@@ -888,7 +889,9 @@ qk_status qk_attn_decode(const qk_kv_cache *cache, const qk_attn *attn, int64_t 
             "out, img and the workspace overlap");
     for (const Span &i : sp.in)
         REQUIRE(!overlap(si, i) && !overlap(sw, i), QK_ERR_ALIAS, "img or the workspace overlaps an input");
-    return launch_attn_decode(kv_cache(cache), *attn, (int)B, T, static_cast<uint8_t *>(img), img_row_blocks, d_live_rows,
+    qk_attn a = *attn;
+    if (a.window >= MOST_KEYS) a.window = 0;   // no sequence has as many
+    return launch_attn_decode(kv_cache(cache), a, (int)B, T, static_cast<uint8_t *>(img), img_row_blocks, d_live_rows,
                               ws, (cudaStream_t)stream);
 }
 
@@ -932,7 +935,9 @@ qk_status qk_attn_prefill(const qk_kv_cache *cache, const qk_attn *attn, int64_t
                 "an output or the workspace overlaps q_offsets");
         for (int i = 0; i < o; i++) REQUIRE(!overlap(outs[o], outs[i]), QK_ERR_ALIAS, "outputs and the workspace overlap");
     }
-    return launch_attn_prefill(kv_cache(cache), *attn, (int)B, (int)rows, q_offsets, (int)max_kv, qs, d, row_blocks,
+    qk_attn a = *attn;
+    if (a.window >= MOST_KEYS) a.window = 0;   // no sequence has as many
+    return launch_attn_prefill(kv_cache(cache), a, (int)B, (int)rows, q_offsets, (int)max_kv, qs, d, row_blocks,
                                d_live_rows, ws, (cudaStream_t)stream);
 }
 
