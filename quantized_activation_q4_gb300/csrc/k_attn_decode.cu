@@ -23,74 +23,21 @@
 
 #include <algorithm>
 
-#include "qk_kv.cuh"
-#include "qk_tc.cuh"
+#include "qk_decode.cuh"
 
 namespace qk {
 namespace {
 
-constexpr unsigned FULL = 0xffffffffu;
-constexpr float LOG2E = 1.4426950408889634f;
 constexpr int WARPS = 2;
 constexpr int GROUPS = 4;                   // of a warp's share of a tile
 constexpr int WARP_TOKENS = GROUPS * GROUP;
 constexpr int TILE = WARPS * WARP_TOKENS;   // tokens
-constexpr float HEADROOM = 8.0f;    // the reference maximum moves when a logit is 2^8 above it
-constexpr float LIFT = 6.0f;        // weights are held times 2^6 below the reference: at most 2^14
-constexpr int MAX_CTAS = 1024;      // of one launch; sizes the workspace
 
 // column tiles of 8 a CTA takes at most
 __host__ __device__ constexpr int column_tiles(int D) { return D == 256 ? 1 : 2; }
 __host__ __device__ constexpr int stages(int D) { return D == 64 ? 4 : 2; }
 // CTAs of an SM, by registers and shared memory
 __host__ __device__ constexpr int per_sm(int D, int NT) { return D == 256 ? 3 : NT == 2 ? (D == 64 ? 5 : 4) : 6; }
-
-struct DecodeArgs {
-    KvCache c;
-    qk_attn a;
-    int B, T, G, groups;   // groups: CTAs that share a tile, each with its own columns
-    int tile_pages, tile_rest;   // TILE / page_tokens, TILE % page_tokens
-    const int32_t *live;
-    float *acc;            // [slot][groups][8 NT][D]
-    float2 *ml;            // [slot][groups][8 NT]: reference maximum, sum of weights
-    int64_t *plan;         // [0] tiles of a share, [1 + b] tiles before sequence b
-};
-
-// ---------------------------------------------------------------- the tiles of a sequence
-struct Sequence {
-    int len, base, tiles;   // keys, first token that a tile covers (a multiple of 16), tiles of one head
-};
-__device__ __forceinline__ Sequence sequence_of(const DecodeArgs &p, int b) {
-    const int64_t most = p.a.table_stride * p.c.page_tokens;
-    Sequence s;
-    s.len = (int)min((int64_t)max(ld_prev(p.a.kv_lens + b), 0), most);
-    const int first_end = s.len - p.T + 1;
-    s.base = p.a.window > 0 ? max(0, first_end - p.a.window) & ~(GROUP - 1) : 0;
-    s.tiles = (s.len - s.base + TILE - 1) / TILE;   // lengths are at most 2^30
-    return s;
-}
-
-// Sum over a CTA of one value a thread, and the sum of the threads before.
-__device__ __forceinline__ int64_t scan_cta(int64_t v, int64_t *before, int64_t *smem) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int64_t x = v;
-#pragma unroll
-    for (int m = 1; m < 32; m <<= 1) {
-        const int64_t y = __shfl_up_sync(FULL, x, m);
-        if (lane >= m) x += y;
-    }
-    __syncthreads();
-    if (lane == 31) smem[warp] = x;
-    __syncthreads();
-    int64_t total = 0, base = 0;
-#pragma unroll
-    for (int w = 0; w < WARPS; w++) {
-        if (w < warp) base += smem[w];
-        total += smem[w];
-    }
-    *before = base + x - v;
-    return total;
-}
 
 // ---------------------------------------------------------------- fragments
 // Words of one block of two token rows (8 apart) times a column tile's queries: 16 tokens x 32 columns. The conversions and
@@ -152,55 +99,6 @@ __device__ __forceinline__ void word_outputs(float (&o)[NT][4], uint32_t x, cons
             : "r"(x), "r"(p[0][0]), "r"(p[0][1]), "r"(p[1][0]), "r"(p[1][1]), "r"(0x64086408u), "r"(0x54805480u));
     }
 }
-__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
-    const __half2 r = __hmul2(half2_bits(a), half2_bits(b));
-    return *reinterpret_cast<const uint32_t *>(&r);
-}
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-    const __half2 r = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&r);
-}
-__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
-    uint32_t r;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
-    return r;
-}
-__device__ __forceinline__ float ex2(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-    uint32_t v;
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
-    return v;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-    uint2 v;
-    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
-    return v;
-}
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-    return v;
-}
-template <int N>
-__device__ __forceinline__ void lds_words(uint32_t a, uint32_t (&w)[N]) {
-    if constexpr (N == 1) {
-        w[0] = lds32(a);
-    } else if constexpr (N == 2) {
-        const uint2 v = lds64(a);
-        w[0] = v.x, w[1] = v.y;
-    } else {
-#pragma unroll
-        for (int i = 0; i < N; i += 4) {
-            const uint4 v = lds128(a + 4 * i);
-            w[i] = v.x, w[i + 1] = v.y, w[i + 2] = v.z, w[i + 3] = v.w;
-        }
-    }
-}
-
 // The queries of a segment's columns as B operands, and what the scores need besides.
 template <int D, int NT>
 struct Queries {
@@ -261,22 +159,6 @@ __device__ __forceinline__ void load_queries(Queries<D, NT> &q, const DecodeArgs
 }
 
 // ---------------------------------------------------------------- the pass
-// A walk over the tiles of a share: (sequence, head, tile), sequences without keys left out.
-struct Walk {
-    int b, h, tile;
-    Sequence s;
-};
-__device__ __forceinline__ void next_tile(Walk &w, const DecodeArgs &p, int live) {
-    if (++w.tile < w.s.tiles) return;
-    w.tile = 0;
-    if (++w.h < p.c.Hkv) return;
-    w.h = 0;
-    do {
-        w.b++;
-        if (w.b < live) w.s = sequence_of(p, w.b);
-    } while (w.b < live && w.s.tiles == 0);
-}
-
 template <int D, int NT>
 __global__ void __launch_bounds__(WARPS * 32, per_sm(D, NT))
 attn_decode_kernel(const __grid_constant__ DecodeArgs p, bool wide) {
@@ -299,48 +181,9 @@ attn_decode_kernel(const __grid_constant__ DecodeArgs p, bool wide) {
     pdl_wait();
     const int live = live_rows(p.live, p.B);
 
-    // Tiles of all sequences, then the place of this share's first. Of up to WARPS * 32 sequences a thread keeps its own
-    // from the one look to the other. (Lengths are loaded beside the live count.)
-    int64_t total = 0, before = 0, n = 0;
-    const auto tiles_of = [&](int b) {
-        const int tiles = b < p.B ? sequence_of(p, b).tiles : 0;
-        return b < live ? (int64_t)tiles * p.c.Hkv : 0;
-    };
-    for (int b0 = 0; b0 < p.B; b0 += WARPS * 32) {
-        const int b = b0 + threadIdx.x;
-        n = tiles_of(b);
-        const int64_t sum = scan_cta(n, &before, scan);
-        if (blockIdx.x == 0 && b < live) p.plan[1 + b] = total + before;
-        total += sum;
-    }
-    const int64_t each = max((int64_t)1, (total + shares - 1) / shares);
-    if (blockIdx.x == 0 && threadIdx.x == 0) p.plan[0] = each;
-    const int64_t first = share * each;
-    int64_t left = min(each, total - first);
-    if (left <= 0) return;
-    {
-        int64_t at = 0;
-        for (int b0 = 0; b0 < p.B; b0 += WARPS * 32) {
-            const int b = b0 + threadIdx.x;
-            int64_t sum = total;
-            if (p.B > WARPS * 32) {
-                n = tiles_of(b);
-                sum = scan_cta(n, &before, scan);
-            }
-            if (first >= at + before && first < at + before + n) {
-                found[0] = b;
-                found[1] = first - at - before;
-            }
-            at += sum;
-            if (first < at) break;
-        }
-        __syncthreads();
-    }
     Walk now;
-    now.b = (int)found[0];
-    now.s = sequence_of(p, now.b);
-    now.h = (int)(found[1] / now.s.tiles);
-    now.tile = (int)(found[1] % now.s.tiles);
+    int64_t left = share_of<WARPS, TILE>(p, live, share, shares, scan, found, now);
+    if (left <= 0) return;
 
     // what is on its way: the first lanes copy a group each
     Walk ahead = now;
@@ -370,7 +213,7 @@ attn_decode_kernel(const __grid_constant__ DecodeArgs p, bool wide) {
             }
         }
         if (--to_issue <= 0) return;
-        next_tile(ahead, p, live);
+        next_tile<TILE>(ahead, p, live);
         if (ahead.tile == 0) {
             place();
         } else {   // a tile further on
@@ -640,7 +483,7 @@ attn_decode_kernel(const __grid_constant__ DecodeArgs p, bool wide) {
             fresh = true;
         }
         if (left == 1) break;
-        next_tile(now, p, live);
+        next_tile<TILE>(now, p, live);
         // the stage was read and written by plain accesses; the next copy into it comes after them
         if (fresh) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
@@ -660,7 +503,7 @@ struct JoinArgs {
     DecodeArgs p;
     uint8_t *img;
     int64_t row_blocks;
-    int NT;
+    int NT, tile;
 };
 // One CTA per (row, query head): the statistics of all partial results first, then their outputs in order, four warps side
 // by side with several loads under way; then rows and image.
@@ -682,7 +525,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) attn_combine_kernel(const __g
     const int h = head / p.G, col = i * p.G + head % p.G;
     // (loaded together: the live count, the length, the sink and the plan, which holds something for live sequences alone)
     const int live = live_rows(p.live, p.B);
-    const Sequence s = sequence_of(p, b);
+    const Sequence s = a.tile == TILE ? sequence_of<TILE>(p, b) : sequence_of<WIDE_TILE>(p, b);
     const float sink = p.a.sinks ? ld_prev(p.a.sinks + head) * LOG2E : -INFINITY;
     const int64_t each = ld_prev(p.plan), tiles_before = ld_prev(p.plan + 1 + b);
     if (b >= live) return;
@@ -760,14 +603,16 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) attn_combine_kernel(const __g
 }
 
 struct Layout {
-    int NT, groups;
+    int NT, groups, tile;   // tile: of the kernel that the call takes
     int64_t slots, acc, ml, plan, bytes;
 };
 Layout layout_of(int Hkv, int D, int n_heads, int64_t B, int T) {
     Layout l;
-    const int tiles = (T * (n_heads / Hkv) + 7) / 8;
-    l.NT = tiles < column_tiles(D) ? tiles : column_tiles(D);
+    const int tiles = (T * (n_heads / Hkv) + 7) / 8;   // of 8 columns
+    const bool wide = tiles > column_tiles(D);
+    l.NT = wide ? (tiles > 2 ? WIDE_COLUMNS : 2) : tiles;
     l.groups = (tiles + l.NT - 1) / l.NT;
+    l.tile = wide ? WIDE_TILE : TILE;
     // segments and shares interleave, so (segment + share) names each part of a segment once
     l.slots = (B * Hkv + MAX_CTAS) * l.groups;
     l.acc = 0;
@@ -805,14 +650,15 @@ qk_status launch_attn_decode(const KvCache &c, const qk_attn &a, int B, int T, u
                              const int32_t *live, void *ws, cudaStream_t s) {
     const Layout l = layout_of(c.Hkv, c.D, a.n_heads, B, T);
     uint8_t *w = static_cast<uint8_t *>(ws);
-    const DecodeArgs p = {c, a, B, T, a.n_heads / c.Hkv, l.groups, TILE / c.page_tokens, TILE % c.page_tokens, live, reinterpret_cast<float *>(w + l.acc),
+    const DecodeArgs p = {c, a, B, T, a.n_heads / c.Hkv, l.groups, l.tile / c.page_tokens, l.tile % c.page_tokens, live, reinterpret_cast<float *>(w + l.acc),
                           reinterpret_cast<float2 *>(w + l.ml), reinterpret_cast<int64_t *>(w + l.plan)};
-    qk_status st = c.D == 256  ? launch_pass<256, 1>(p, s)
+    qk_status st = l.tile != TILE ? launch_attn_wide(p, l.NT, s)
+                   : c.D == 256  ? launch_pass<256, 1>(p, s)
                    : c.D == 64 ? (l.NT == 1 ? launch_pass<64, 1>(p, s) : launch_pass<64, 2>(p, s))
                                : (l.NT == 1 ? launch_pass<128, 1>(p, s) : launch_pass<128, 2>(p, s));
     if (st != QK_OK) return st;
     const int rows = B * T, z = rows > 65535 ? 256 : 1;
-    const JoinArgs j = {p, img, row_blocks, l.NT};
+    const JoinArgs j = {p, img, row_blocks, l.NT, l.tile};
     auto *combine = c.D == 64 ? attn_combine_kernel<64> : c.D == 128 ? attn_combine_kernel<128> : attn_combine_kernel<256>;
     return launch_pdl("attn_combine", combine, dim3(a.n_heads, (unsigned)ceil_div(rows, z), z), dim3(128), 0, s, j);
 }

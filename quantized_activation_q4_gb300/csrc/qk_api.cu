@@ -396,14 +396,15 @@ size_t qk_mmvq_workspace_bytes(int32_t n_proj, const qk_proj *projs) {
 
 qk_status qk_device_faults(uint32_t *faults) {
     REQUIRE(faults, QK_ERR_ARG, "faults is null");
-    uint32_t a = 0, b = 0, c = 0, d = 0, e = 0, f = 0;
+    uint32_t a = 0, b = 0, c = 0, d = 0, e = 0, f = 0, g = 0;
     qk_status st = read_device_faults(&a);
     if (st == QK_OK) st = read_mmq_faults(&b);
     if (st == QK_OK) st = read_mmq_id_faults(&c);
     if (st == QK_OK) st = read_mmvq_g_faults(&d);
     if (st == QK_OK) st = read_attn_decode_faults(&e);
     if (st == QK_OK) st = read_attn_prefill_faults(&f);
-    *faults = a | b | c | d | e | f;
+    if (st == QK_OK) st = read_attn_wide_faults(&g);
+    *faults = a | b | c | d | e | f | g;
     return st;
 }
 

@@ -96,6 +96,7 @@ qk_status launch_kv_read(const KvCache &c, const int32_t *slots, int n, int elem
 qk_status launch_attn_decode(const KvCache &c, const qk_attn &a, int B, int T, uint8_t *img, int64_t row_blocks,
                              const int32_t *live, void *ws, cudaStream_t s);
 qk_status read_attn_decode_faults(uint32_t *faults);
+qk_status read_attn_wide_faults(uint32_t *faults);
 qk_status read_attn_prefill_faults(uint32_t *faults);
 int64_t attn_decode_workspace_bytes(int Hkv, int D, int n_heads, int64_t B, int T);
 qk_status launch_attn_prefill(const KvCache &c, const qk_attn &a, int B, int rows, const int32_t *q_offsets, int max_kv,
