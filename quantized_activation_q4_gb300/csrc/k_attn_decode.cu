@@ -177,7 +177,8 @@ attn_decode_kernel(const __grid_constant__ DecodeArgs p, bool wide) {
     const uint32_t ring = smem_u32(smem) + warp * S * STAGE, bar0 = smem_u32(&bars[warp][0]);
     if (lane < S) mbar_init(bar0 + 8 * lane, GROUPS);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    pdl_trigger();
+    // (No early start of the next kernel: the join's CTAs, waiting on SMs that are done, held up the passes of calls in a row;
+    // 64 sequences of 8192 keys took 93 us a call for 71.)
     pdl_wait();
     const int live = live_rows(p.live, p.B);
 
@@ -320,7 +321,7 @@ attn_decode_kernel(const __grid_constant__ DecodeArgs p, bool wide) {
                         }
                 }
         }
-        // the columns' maxima; the reference moves only far
+        // the lane's maxima of its columns; the reference moves only far
         float top[NT][2];
         bool move = false;
 #pragma unroll
@@ -330,9 +331,6 @@ attn_decode_kernel(const __grid_constant__ DecodeArgs p, bool wide) {
                 float m = fmaxf(s[0][n][e], s[0][n][2 + e]);
 #pragma unroll
                 for (int r = 1; r < GROUPS; r++) m = fmaxf(fmaxf(m, s[r][n][e]), s[r][n][2 + e]);
-                m = fmaxf(m, __shfl_xor_sync(FULL, m, 4));
-                m = fmaxf(m, __shfl_xor_sync(FULL, m, 8));
-                m = fmaxf(m, __shfl_xor_sync(FULL, m, 16));
                 top[n][e] = m;
                 move |= m - ref[n][e] > HEADROOM;   // (no: both are minus infinity)
             }
@@ -379,7 +377,11 @@ attn_decode_kernel(const __grid_constant__ DecodeArgs p, bool wide) {
             for (int n = 0; n < NT; n++)
 #pragma unroll
                 for (int e = 0; e < 2; e++) {
-                    const float r = fmaxf(ref[n][e], top[n][e]);
+                    float m = top[n][e];
+                    m = fmaxf(m, __shfl_xor_sync(FULL, m, 4));
+                    m = fmaxf(m, __shfl_xor_sync(FULL, m, 8));
+                    m = fmaxf(m, __shfl_xor_sync(FULL, m, 16));
+                    const float r = fmaxf(ref[n][e], m);
                     const float down = ref[n][e] == -INFINITY ? 0.0f : ex2(ref[n][e] - r + (float)(lift_e - e_new));
                     ref[n][e] = r;
                     off[n][e] = r == -INFINITY ? 0.0f : __fadd_ru(r, (float)e_new - LIFT);   // never below: weights stay under 2^14
@@ -505,11 +507,36 @@ struct JoinArgs {
     int64_t row_blocks;
     int NT, tile;
 };
+// A lane's column of block k of a head: its row and image.
+template <int NB>
+__device__ __forceinline__ void put_block(const JoinArgs &a, int row, int head, int k, float y) {
+    const qk_attn &out = a.p.a;
+    const int lane = threadIdx.x & 31;
+    const int64_t to = row * out.out_stride + (int64_t)head * 32 * NB + 32 * k + lane;
+    if (out.out && out.out_elem == QK_ELEM_F32) static_cast<float *>(out.out)[to] = y;
+    if (out.out && out.out_elem == QK_ELEM_BF16) static_cast<__nv_bfloat16 *>(out.out)[to] = __float2bfloat16_rn(y);
+    if (!a.img) return;
+    float m = fabsf(y);
+#pragma unroll
+    for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, x));
+    const float d = m / 127.0f;
+    const int code = m != 0.0f ? __float2int_rn(y / d) : 0;
+    const int sum = __reduce_add_sync(FULL, code);
+    uint8_t *block = a.img + (row * a.row_blocks + (int64_t)head * NB + k) * Q8_1_BYTES;
+    block[4 + lane] = (uint8_t)code;
+    if (lane == 0) *reinterpret_cast<__half2 *>(block) = __halves2half2(__float2half_rn(d), __float2half_rn(d * (float)sum));
+}
+// The blocks behind a row's heads, by the last head's threads.
+template <int NB>
+__device__ __forceinline__ void clear_behind(const JoinArgs &a, int row, int thread, int threads) {
+    if (!a.img) return;
+    uint32_t *rest = reinterpret_cast<uint32_t *>(a.img + (row * a.row_blocks + (int64_t)a.p.a.n_heads * NB) * Q8_1_BYTES);
+    const int64_t words = (a.row_blocks - (int64_t)a.p.a.n_heads * NB) * (Q8_1_BYTES / 4);
+    for (int64_t x = thread; x < words; x += threads) rest[x] = 0;
+}
+
 // One CTA per (row, query head): the statistics of all partial results first, then their outputs in order, four warps side
 // by side with several loads under way; then rows and image.
-// Factors are worked out by every warp that needs one and not kept in shared memory: its CTAs start early, beside those of
-// the pass that leave an SM, and with 3.2 or 10 KB instead of 2.2 they held up the passes of calls in a row (64 sequences of
-// 8192 keys: 94 us a call for 74).
 constexpr int JOIN_WARPS = 4;
 template <int D>
 __global__ void __launch_bounds__(JOIN_WARPS * 32) attn_combine_kernel(const __grid_constant__ JoinArgs a) {
@@ -519,7 +546,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) attn_combine_kernel(const __g
     pdl_trigger();
     pdl_wait();
     const DecodeArgs &p = a.p;
-    const int head = blockIdx.x, row = blockIdx.y * gridDim.z + blockIdx.z;
+    const int head = blockIdx.x, row = blockIdx.y;
     const int b = row / p.T, i = row % p.T, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (b >= p.B) return;
     const int h = head / p.G, col = i * p.G + head % p.G;
@@ -579,27 +606,66 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) attn_combine_kernel(const __g
         float y = 0.0f;
 #pragma unroll
         for (int w = 0; w < JOIN_WARPS; w++) y += part[w][32 * k + lane];
-        y *= inv;
-        const int64_t to = row * p.a.out_stride + (int64_t)head * D + 32 * k + lane;
-        if (p.a.out && p.a.out_elem == QK_ELEM_F32) static_cast<float *>(p.a.out)[to] = y;
-        if (p.a.out && p.a.out_elem == QK_ELEM_BF16) static_cast<__nv_bfloat16 *>(p.a.out)[to] = __float2bfloat16_rn(y);
-        if (!a.img) continue;
-        float m = fabsf(y);
+        put_block<NB>(a, row, head, k, y * inv);
+    }
+    if (head == p.a.n_heads - 1) clear_behind<NB>(a, row, threadIdx.x, JOIN_WARPS * 32);
+}
+
+// Many rows and heads, few partial results of each: a warp a head, 32 statistics at once.
+template <int D>
+__global__ void __launch_bounds__(128) attn_combine_warps_kernel(const __grid_constant__ JoinArgs a) {
+    constexpr int NB = D / 32;
+    pdl_trigger();
+    pdl_wait();
+    const DecodeArgs &p = a.p;
+    const int64_t unit = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+    const int row = (int)(unit / p.a.n_heads), head = (int)(unit - (int64_t)row * p.a.n_heads), lane = threadIdx.x & 31;
+    const int b = row / p.T, i = row - b * p.T;
+    if (b >= p.B) return;
+    const int live = live_rows(p.live, p.B);
+    const Sequence s = a.tile == TILE ? sequence_of<TILE>(p, b) : sequence_of<WIDE_TILE>(p, b);
+    const float sink = p.a.sinks ? ld_prev(p.a.sinks + head) * LOG2E : -INFINITY;
+    const int64_t each = ld_prev(p.plan), tiles_before = ld_prev(p.plan + 1 + b);
+    if (b >= live) return;
+    const int h = head / p.G, col = i * p.G + head - h * p.G;
+    const int64_t lo = tiles_before + (int64_t)h * s.tiles, c0 = s.tiles > 0 ? lo / each : 0;
+    const int count = s.tiles > 0 ? (int)((lo + s.tiles - 1) / each - c0) + 1 : 0;
+    const int n = col / 8, cg = n / a.NT;
+    const int64_t step = (int64_t)p.groups * a.NT * 8;   // from one partial result to the next
+    const int64_t at = (((int64_t)b * p.c.Hkv + h + c0) * p.groups + cg) * a.NT * 8 + n % a.NT * 8 + col % 8;
+    float top = sink, total = 0.0f, o[NB];
 #pragma unroll
-        for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, x));
-        const float d = m / 127.0f;
-        const int code = m != 0.0f ? __float2int_rn(y / d) : 0;
-        const int sum = __reduce_add_sync(FULL, code);
-        uint8_t *block = a.img + (row * a.row_blocks + (int64_t)head * NB + k) * Q8_1_BYTES;
-        block[4 + lane] = (uint8_t)code;
-        if (lane == 0)
-            *reinterpret_cast<__half2 *>(block) = __halves2half2(__float2half_rn(d), __float2half_rn(d * (float)sum));
+    for (int k = 0; k < NB; k++) o[k] = 0.0f;
+    for (int first = 0; first < count; first += 32) {
+        const bool mine = first + lane < count;
+        const float2 *ml = p.ml + at + (int64_t)(first + lane) * step;
+        const float m = mine ? ld_prev(&ml->x) : -INFINITY, l = mine ? ld_prev(&ml->y) : 0.0f;
+        float now = m;
+#pragma unroll
+        for (int x = 16; x; x >>= 1) now = fmaxf(now, __shfl_xor_sync(FULL, now, x));
+        now = fmaxf(now, top);
+        if (now == -INFINITY) continue;
+        const float old = top == -INFINITY ? 0.0f : ex2(top - now), f = m == -INFINITY ? 0.0f : ex2(m - now);
+        top = now;
+        float add = l * f;
+#pragma unroll
+        for (int x = 16; x; x >>= 1) add += __shfl_xor_sync(FULL, add, x);
+        total = fmaf(total, old, add);
+#pragma unroll
+        for (int k = 0; k < NB; k++) o[k] *= old;
+        const int some = min(32, count - first);
+#pragma unroll 4
+        for (int c = 0; c < some; c++) {
+            const float g = __shfl_sync(FULL, f, c);
+#pragma unroll
+            for (int k = 0; k < NB; k++) o[k] = fmaf(ld_prev(p.acc + (at + (first + c) * step) * D + 32 * k + lane), g, o[k]);
+        }
     }
-    if (a.img && head == p.a.n_heads - 1) {   // the blocks behind the heads
-        uint32_t *rest = reinterpret_cast<uint32_t *>(a.img + (row * a.row_blocks + (int64_t)p.a.n_heads * NB) * Q8_1_BYTES);
-        const int64_t words = (a.row_blocks - (int64_t)p.a.n_heads * NB) * (Q8_1_BYTES / 4);
-        for (int64_t x = threadIdx.x; x < words; x += 128) rest[x] = 0;
-    }
+    if (sink != -INFINITY) total += ex2(sink - top);
+    const float inv = total == 0.0f ? 0.0f : 1.0f / total;   // no key and no sink: 0
+#pragma unroll
+    for (int k = 0; k < NB; k++) put_block<NB>(a, row, head, k, o[k] * inv);
+    if (head == p.a.n_heads - 1) clear_behind<NB>(a, row, lane, 32);
 }
 
 struct Layout {
@@ -657,10 +723,19 @@ qk_status launch_attn_decode(const KvCache &c, const qk_attn &a, int B, int T, u
                    : c.D == 64 ? (l.NT == 1 ? launch_pass<64, 1>(p, s) : launch_pass<64, 2>(p, s))
                                : (l.NT == 1 ? launch_pass<128, 1>(p, s) : launch_pass<128, 2>(p, s));
     if (st != QK_OK) return st;
-    const int rows = B * T, z = rows > 65535 ? 256 : 1;
+    const int rows = B * T;
     const JoinArgs j = {p, img, row_blocks, l.NT, l.tile};
+    // Many heads: a warp each (16 x 8 rows of 32 heads, 4 partial results: 12 us by CTAs); few: a CTA each, for many
+    // partial results (8 rows of 28 heads, 60 of them).
+    const int64_t heads = (int64_t)rows * a.n_heads;
+    if (heads >= 1024) {
+        auto *combine = c.D == 64    ? attn_combine_warps_kernel<64>
+                        : c.D == 128 ? attn_combine_warps_kernel<128>
+                                     : attn_combine_warps_kernel<256>;
+        return launch_pdl("attn_combine", combine, dim3((unsigned)ceil_div(heads, 4)), dim3(128), 0, s, j);
+    }
     auto *combine = c.D == 64 ? attn_combine_kernel<64> : c.D == 128 ? attn_combine_kernel<128> : attn_combine_kernel<256>;
-    return launch_pdl("attn_combine", combine, dim3(a.n_heads, (unsigned)ceil_div(rows, z), z), dim3(128), 0, s, j);
+    return launch_pdl("attn_combine", combine, dim3(a.n_heads, (unsigned)rows), dim3(128), 0, s, j);
 }
 
 qk_status read_attn_decode_faults(uint32_t *faults) {

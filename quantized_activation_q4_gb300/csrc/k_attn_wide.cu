@@ -78,7 +78,7 @@ attn_wide_kernel(const __grid_constant__ DecodeArgs p, bool wide) {
     if (threadIdx.x < S) mbar_init(bar0 + 8 * threadIdx.x, WARPS);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     __syncthreads();
-    pdl_trigger();
+    // (no early start of the next kernel: see k_attn_decode.cu)
     pdl_wait();
     const int live = live_rows(p.live, p.B);
     Walk now;

@@ -876,6 +876,7 @@ qk_status qk_attn_decode(const qk_kv_cache *cache, const qk_attn *attn, int64_t 
     REQUIRE(B >= 0 && B <= (1 << 20), QK_ERR_ARG, "B=%lld out of range (0..2^20)", (long long)B);
     REQUIRE(T >= 1, QK_ERR_ARG, "T < 1");
     REQUIRE(T <= 8, QK_ERR_UNSUPPORTED, "T=%d > 8 (use qk_attn_prefill)", (int)T);
+    REQUIRE(!attn || B * T * (int64_t)attn->n_heads <= INT32_MAX, QK_ERR_UNSUPPORTED, "B * T * n_heads too large for one launch");
     AttnSpans sp;
     st = check_attn(cache, attn, B, B * T, img != nullptr, img_row_blocks, d_live_rows, &sp);
     if (st != QK_OK) return st;

@@ -102,6 +102,8 @@ def test_decode(lib):
     assert decode(img=Y + 64) == 3 and decode(img=X) == 3 and decode(img=PAGES) == 3 and decode(img=LIVE, live=LIVE) == 3
     assert decode(ws=None) == 4 and decode(ws=WS + 8) == 4 and decode(n=0) == 4
     assert decode(ws=Y) == 3 and decode(ws=X) == 3 and decode(ws=IMG, img=IMG) == 3 and decode(ws=TAB) == 3
+    many = attn(n_heads=1024, q_stride=1 << 17, out_stride=1 << 17)
+    assert decode(a=many, B=1 << 20, T=8) == 5
     assert decode(B=0) == 0 and decode(B=0, a=attn(q=None, page_table=None, kv_lens=None, out=None), ws=None) == 0
     need = lib.qk_attn_decode_workspace_bytes(C.byref(cache()), 4, 2, 1)
     assert need > 0 and decode(n=need - 1) == 4
