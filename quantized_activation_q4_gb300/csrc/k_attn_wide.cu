@@ -40,6 +40,11 @@ __device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uin
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void mma16_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+}
 // Nibbles of bytes 0 and 2 of a word (low, high) less the bias of the exponents, exactly the codes less 8.
 __device__ __forceinline__ uint32_t low_codes(uint32_t w) {
     const uint32_t v = (w & 0x000F000Fu) | 0x64006400u;
@@ -206,6 +211,7 @@ attn_wide_kernel(const __grid_constant__ DecodeArgs p, bool wide) {
         // the scores of the warp's group, times log2 e
         float s[NT][4];
         {
+            uint64_t s2[NT][2];   // two columns each
             uint32_t dk[2][NB / 2];
             lds_words<NB / 2>(mine + 8 * D + 2 * NB * g, dk[0]);
             lds_words<NB / 2>(mine + 8 * D + 2 * NB * (g + 8), dk[1]);
@@ -219,26 +225,31 @@ attn_wide_kernel(const __grid_constant__ DecodeArgs p, bool wide) {
                     const int b = bq * Z::W + k;
                     const float2 p0 = __half22float2(half2_bits(dk[0][b / 2])), p1 = __half22float2(half2_bits(dk[1][b / 2]));
                     const float d0 = b & 1 ? p0.y : p0.x, d1 = b & 1 ? p1.y : p1.x;
+                    const uint64_t dd0 = two(d0, d0), dd1 = two(d1, d1);
                     const uint32_t lo[4] = {low_codes(w0[k]), low_codes(w1[k]), low_codes(w0[k] >> 8), low_codes(w1[k] >> 8)};
                     const uint32_t hi[4] = {high_codes(w0[k]), high_codes(w1[k]), high_codes(w0[k] >> 8), high_codes(w1[k] >> 8)};
 #pragma unroll
                     for (int n = 0; n < NT; n++) {
                         const uint4 q = lds128(q_at + ((b * NT + n) * 32 + lane) * 16);
-                        float a[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                        mma16(a, lo, q.x, q.y);
+                        float a[4];
+                        mma16_first(a, lo, q.x, q.y);
                         mma16(a, hi, q.z, q.w);
-#pragma unroll
-                        for (int e = 0; e < 4; e++)
-                            s[n][e] = b == 0 ? (e < 2 ? d0 : d1) * a[e] : fmaf(e < 2 ? d0 : d1, a[e], s[n][e]);
+                        const uint64_t a0 = two(a[0], a[1]), a1 = two(a[2], a[3]);
+                        s2[n][0] = fma2(dd0, a0, b == 0 ? 0 : s2[n][0]);
+                        s2[n][1] = fma2(dd1, a1, b == 0 ? 0 : s2[n][1]);
                     }
                 }
             }
+#pragma unroll
+            for (int n = 0; n < NT; n++)
+#pragma unroll
+                for (int f = 0; f < 2; f++) {
+                    const float2 x = apart(s2[n][f]);
+                    s[n][2 * f] = x.x * scale[n][0];
+                    s[n][2 * f + 1] = x.y * scale[n][1];
+                }
         }
         bool move = false;
-#pragma unroll
-        for (int n = 0; n < NT; n++)
-#pragma unroll
-            for (int e = 0; e < 4; e++) s[n][e] *= scale[n][e & 1];
         if (!whole) {
 #pragma unroll
             for (int n = 0; n < NT; n++)
