@@ -1,11 +1,10 @@
 // Attention of a few new tokens of many sequences over the 4-bit cache (qk_attn_decode).
 //
-// attn_decode_kernel: one pass over the keys and values. A tile is 128 tokens of one sequence and key/value head; the
-// tiles of all sequences, in the order (sequence, head, token), are cut into equal shares, one for each resident CTA, so
-// sequences of any lengths fill the device. Four warps take 32 tokens of a tile each, with a running maximum, sum and
-// output of their own; at the end of a segment (a share's part of one sequence and head) they meet and leave one partial
-// result. attn_combine_kernel adds the partial results of a head in the order of its tokens, so outputs do not depend on
-// the run, and writes rows and image.
+// attn_decode_kernel: one pass over the keys and values. The tiles of all sequences, in the order (sequence, head, token),
+// are cut into equal shares, one for each resident CTA, so sequences of any lengths fill the device. A CTA's warps take a
+// part of a tile each, with a running maximum, sum and output of their own; at the end of a segment (a share's part of one
+// sequence and head) they meet and leave one partial result. attn_combine_kernel adds the partial results of a head in the
+// order of its tokens, so outputs do not depend on the run, and writes rows and image.
 //
 // The tokens of a group are the rows (M) of the products, up to 8 NT query columns (query heads of the key/value head
 // times new tokens) their columns (N), so a group of seven heads wastes an eighth and not half. With the scales outside
@@ -18,8 +17,13 @@
 // size. Weights are kept at up to 2^14 times their value, so those down to 2^-28 of the largest keep binary16's precision;
 // where a value's scale is 2 or more, its exponent joins the running maximum.
 //
-// Bound by instruction issue next to memory: 2304 bytes of cache (16 tokens of a head of 128) cost about 205 warp
-// instructions, which at full issue would be 13 TB/s.
+// A tile is 128 tokens, 64 for each of two warps (four groups: the barrier, the votes and the places of pages are paid for
+// once; with 32 tokens a warp and tile 64 sequences of 8192 keys took 84 us for 71). Six CTAs an SM by registers (168) and
+// shared memory (two stages a warp).
+//
+// Bound by instruction issue next to memory: 2304 bytes of cache (16 tokens of a head of 128) cost 292 warp instructions, at
+// full issue 9 TB/s. 64 sequences of 8192 keys, 28 heads over 4 of 128: 71 us = 4.3 TB/s, 64% of the measured copy rate (issue
+// 54% active, the logic pipe 42%).
 
 #include <algorithm>
 

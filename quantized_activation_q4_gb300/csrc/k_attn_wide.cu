@@ -8,9 +8,10 @@
 // which they learn from each other by the barrier that the exchange needs anyway. Codes are converted exactly for both
 // products (the bias of the scores as an initial accumulator would need more registers than there are).
 //
-// Bound by instruction issue: a group of 16 tokens of a head of 128 costs about 450 warp instructions for 32 columns, where
-// two CTAs of 16 columns spent 920. 16 sequences of 1500 to 9000 tokens with 8 new tokens, 32 heads over 8: see the table of
-// times beside launch_attn_wide.
+// Bound by instruction issue: a group of 16 tokens of a head of 128 costs 890 warp instructions for 32 columns (the scales'
+// products, exponentials and moves of 32 columns more than the conversion), at 52% issue. 16 sequences of 1500 to 9000
+// tokens with 8 new tokens each, 32 heads over 8: 57 us and 8 for the join; two CTAs of 16 columns in k_attn_decode.cu's
+// kernel took 66.
 
 #include <algorithm>
 
