@@ -199,3 +199,39 @@ def test_prefill_behind_a_long_past(D, Hkv, G, P, window, sinks):
     low, _ = run_attention(geo, pages, table, lens, q, rows, "bf16", D ** -0.5, window, s, "bf16", False, "prefill", live=3)
     n = sum(rows[:3])
     assert np.array_equal(low[:n], bf16(out[:n])) and np.isnan(low[n:]).all()
+
+
+@pytest.mark.parametrize("D,Hkv,G,P,T", [(128, 2, 4, 64, 8), (64, 1, 16, 16, 2), (256, 2, 4, 32, 4), (256, 1, 8, 128, 2),
+                                         (128, 1, 11, 48, 7)])
+@pytest.mark.parametrize("window", [0, 700])
+def test_decode_of_many_columns_over_long_sequences(D, Hkv, G, P, T, window):
+    """More than 16 query columns (8 at head_dim 256), sequences longer than a share of the keys, sinks, a lost page."""
+    rng = np.random.default_rng(D + G + T)
+    lens = [5000, 3, 2600, 64, 0, 1300]
+    geo, pages, table = case(rng, D, Hkv, P, lens)
+    table[0, 2] = geo[0] + 7
+    q = queries(rng, len(lens) * T, Hkv * G, D, "bf16")
+    s = rng.normal(size=Hkv * G).astype(np.float32) * 2
+    rows = [T] * len(lens)
+    out, img = run_attention(geo, pages, table, lens, q, rows, "bf16", D ** -0.5, window, s, "f32", True, "decode", live=5,
+                             spare_blocks=1)
+    n = 5 * T
+    want, parts = expected(geo, pages, table, lens, q, rows, D ** -0.5, window, s)
+    check(out[:n], want[:n], bound_of(parts, False)[:n], "f32")
+    assert np.isnan(out[n:]).all() and (img[n:] == 0xA5).all()
+    image_is_of(img[:n], out[:n])
+
+
+@pytest.mark.parametrize("call", ["decode", "prefill"])
+def test_sequences_that_share_pages(call):
+    """A prefix whose pages several sequences have in their tables."""
+    rng = np.random.default_rng(31)
+    D, Hkv, G, P, T = 128, 2, 3, 32, 3
+    lens = [300, 290, 128]
+    geo, pages, table = case(rng, D, Hkv, P, lens)
+    table[1, :4] = table[0, :4]
+    table[2, :4] = table[0, :4]
+    q = queries(rng, 9, Hkv * G, D, "f32")
+    out, _ = run_attention(geo, pages, table, lens, q, [T] * 3, "f32", 0.1, 0, None, "f32", False, call)
+    want, parts = expected(geo, pages, table, lens, q, [T] * 3, 0.1, 0, None)
+    check(out, want, bound_of(parts, call == "prefill"), "f32")

@@ -8,7 +8,7 @@ from oracle import oracle as O
 from quantized_activation_q4_gb300 import binding as qk
 from quantized_activation_q4_gb300 import synth
 from tests.gpu_helpers import pack_weight
-from tests.kv_helpers import HB16, bf16, decode_error
+from tests.kv_helpers import HB16, bf16, decode_error, random_pages
 
 pytestmark = pytest.mark.gpu
 
@@ -197,3 +197,38 @@ def test_two_streams_with_their_own_workspaces():
     for (pre, dec), want in zip(layers, alone):
         for got, w in zip((pre.out, pre.oqs, pre.o, dec.out, dec.oimg, dec.o), want):
             assert torch.equal(got, w)
+
+
+def test_a_captured_prompt_replayed_with_other_splits_of_its_rows():
+    """One captured prefill of a bucket of rows: the sequences' rows and lengths change between replays."""
+    import torch
+    weights = (pack_weight(synth.q4_0_weight(71, WIDTH, K), "q4_0", WIDTH, K),
+               pack_weight(synth.q4_0_weight(72, K, HQ * D), "q4_0", K, HQ * D))
+    geo = (24, P, HKV, D)
+    # some of the splits have pasts that no row of theirs stored: what the pages hold then
+    start = torch.from_numpy(random_pages(np.random.default_rng(9), geo).reshape(-1)).cuda()
+    pages = start.clone()
+    table = np.random.default_rng(3).permutation(24).reshape(2, 12)
+    L = Layer(70, pages, geo, 2, 90, weights)
+    splits = [([60, 30], [60, 30]), ([1, 89], [1, 150]), ([45, 45], [180, 45]), ([90, 0], [192, 0])]
+    kept = []
+    for i, (rows, lens) in enumerate(splits):
+        L.feed(i, rows, lens, table)
+        L.prompt()
+        check_attention(L, rows, lens, table, True)
+        kept.append((L.out.clone(), L.oqs.clone(), L.od.clone(), L.o.clone(), pages.clone()))
+    pages.copy_(start)
+    g = torch.cuda.CUDAGraph()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        with torch.cuda.graph(g, stream=side):
+            L.prompt()
+    torch.cuda.current_stream().wait_stream(side)
+    for i, (rows, lens) in enumerate(splits):
+        L.feed(i, rows, lens, table)
+        g.replay()
+        torch.cuda.synchronize()
+        for got, want in zip((L.out, L.oqs, L.od, L.o, pages), kept[i]):
+            assert torch.equal(got, want)
+    assert qk.qk_device_faults() == 0
