@@ -818,7 +818,9 @@ QK_API qk_status qk_attn_decode(const qk_kv_cache *cache, const qk_attn *attn, i
  *              (blocks past n_heads * head_dim / 32 are zero), or both NULL
  *   d_live_rows: the number of live SEQUENCES of B
  *   ws         qk_attn_prefill_workspace_bytes bytes, 128-byte aligned: the keys
- *              and values of the call in binary16. Scratch, no state kept.
+ *              and values of the call in binary16 and, for max_kv from 2048 on,
+ *              partial outputs of calls with few rows (84 MB at head_dim 128).
+ *              Scratch, no state kept.
  * Runs on the tensor cores (tcgen05) with binary16 operands: keys and values
  * (code - 8) * d, queries scaled by a power of two per row, weights exp(s - max),
  * each rounded once, with binary32 sums. Keys and values beyond binary16's range

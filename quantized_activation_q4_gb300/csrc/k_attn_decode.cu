@@ -679,6 +679,11 @@ struct Layout {
 Layout layout_of(int Hkv, int D, int n_heads, int64_t B, int T) {
     Layout l;
     const int tiles = (T * (n_heads / Hkv) + 7) / 8;   // of 8 columns
+    // Up to 16 columns (8 at head_dim 256, for the registers of the output) take this file's kernel, more the wide one.
+    // Both sides, us, this file's / the wide one's:
+    //   32 sequences of 8192 keys: 16 columns, D = 128, 2 kv heads 46 / 48; 14, D = 128, 4: 67 / 75; 16, D = 64, 8: 73 / 94
+    //   16 sequences of 8192 keys, D = 256: 8 columns, 4 kv heads 58 / 75; 16, 2 (two CTAs of 8 here): 54 / 51
+    //   16 sequences of 1500 to 9000 keys, 8 kv heads, 32 columns (two CTAs of 16 here): D = 128 69 / 65, D = 64 47 / 45
     const bool wide = tiles > column_tiles(D);
     l.NT = wide ? (tiles > 2 ? WIDE_COLUMNS : 2) : tiles;
     l.groups = (tiles + l.NT - 1) / l.NT;
@@ -729,8 +734,9 @@ qk_status launch_attn_decode(const KvCache &c, const qk_attn &a, int B, int T, u
     if (st != QK_OK) return st;
     const int rows = B * T;
     const JoinArgs j = {p, img, row_blocks, l.NT, l.tile};
-    // Many heads: a warp each (16 x 8 rows of 32 heads, 4 partial results: 12 us by CTAs); few: a CTA each, for many
-    // partial results (8 rows of 28 heads, 60 of them).
+    // Many heads have few partial results each: a warp a head; few heads have many: a CTA a head. Whole calls, us, by CTAs /
+    // by warps: 32 heads behind 131072 keys 46 / 82, 224 behind 2000 13.0 / 18.1, 512 behind 8192 43.0 / 45.1, 1024 behind
+    // 8192 69.2 / 69.7, 1792 behind 8192 71.1 / 70.5, 4096 of 1500 to 9000 keys (head_dim 128) 68.5 / 65.2.
     const int64_t heads = (int64_t)rows * a.n_heads;
     if (heads >= 1024) {
         auto *combine = c.D == 64    ? attn_combine_warps_kernel<64>
