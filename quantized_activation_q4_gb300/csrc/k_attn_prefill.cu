@@ -787,7 +787,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
 #pragma unroll
         for (int x = 16; x; x >>= 1) now = fmaxf(now, __shfl_xor_sync(FULL, now, x));
         now = fmaxf(now, top);
-        if (now == -INFINITY) continue;
+        // (no keys so far: factors 0, and what a NaN query left goes on)
         const float old = top == -INFINITY ? 0.0f : ex2(top - now), f = m == -INFINITY ? 0.0f : ex2(m - now);
         top = now;
         float add = l * f;

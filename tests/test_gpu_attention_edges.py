@@ -137,3 +137,29 @@ def test_values_of_large_and_small_scales():
         want, parts = expected(geo, pages, table, lens, q, [T, T], 0.1, 0, None)
         # binary16 holds a weight times a scale to 2^-25 of 2^14 / the largest scale at least: far below the bound here
         check(out, want, bound_of(parts, call == "prefill"), "f32", call)
+
+
+@pytest.mark.parametrize("sinks", [False, True])
+@pytest.mark.parametrize("call,D,Hkv,G,lens,n", [
+    ("prefill", 128, 2, 4, [4000, 0, 2500], 3),        # few rows behind many keys: shares of the keys, joined
+    ("prefill", 256, 1, 2, [2048, 3, 3333], 5),
+    ("decode", 128, 4, 8, [700, 0, 90] + [300] * 29, 2),   # 2048 heads of rows: the join of many
+    ("decode", 64, 1, 4, [9000, 1, 0], 1),             # the join of few, many partial results
+    ("decode", 128, 1, 8, [2000, 5, 0], 8),            # many columns
+])
+def test_nan_stays_in_its_row_and_head_over_joined_keys(call, D, Hkv, G, lens, n, sinks):
+    rng = np.random.default_rng(D + n)
+    geo, pages, table = case(rng, D, Hkv, 32, lens)
+    rows = n * len(lens)
+    q = queries(rng, rows, Hkv * G, D, "f32")
+    sink = rng.standard_normal(Hkv * G).astype(np.float32) if sinks else None
+    clean, _ = run_attention(geo, pages, table, lens, q, [n] * len(lens), "f32", 0.1, 0, sink, "f32", False, call)
+    assert np.isfinite(clean).all()
+    at = [(0, Hkv * G - 1), (n - 1, 0)]                # a row and head of the longest sequence
+    for i, h in at:
+        q[i, h, 33] = np.nan
+    got, _ = run_attention(geo, pages, table, lens, q, [n] * len(lens), "f32", 0.1, 0, sink, "f32", False, call)
+    for i, h in at:
+        assert np.isnan(got[i, h]).all()
+        got[i, h] = clean[i, h]
+    assert np.array_equal(got, clean)
