@@ -480,7 +480,7 @@ attn_decode_kernel(const __grid_constant__ DecodeArgs p, bool wide) {
 #pragma unroll
                     for (int w = 0; w < WARPS; w++) {
                         const float2 v = meet[w][threadIdx.x];
-                        l += v.x == -INFINITY ? 0.0f : v.y * ex2(v.x - m);
+                        l += v.y * (v.x == -INFINITY ? 0.0f : ex2(v.x - m));   // (NaN stays)
                     }
                     p.ml[(slot * NT + n) * 8 + threadIdx.x] = make_float2(m, l);
                 }
@@ -648,7 +648,10 @@ __global__ void __launch_bounds__(128) attn_combine_warps_kernel(const __grid_co
 #pragma unroll
         for (int x = 16; x; x >>= 1) now = fmaxf(now, __shfl_xor_sync(FULL, now, x));
         now = fmaxf(now, top);
-        // (no keys so far: factors 0, and what a NaN query left goes on)
+        if (now == -INFINITY) {   // no keys so far: sums of 0, or NaN by the query
+            if (__any_sync(FULL, l != l)) total = NAN;
+            continue;
+        }
         const float old = top == -INFINITY ? 0.0f : ex2(top - now), f = m == -INFINITY ? 0.0f : ex2(m - now);
         top = now;
         float add = l * f;

@@ -787,7 +787,10 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
 #pragma unroll
         for (int x = 16; x; x >>= 1) now = fmaxf(now, __shfl_xor_sync(FULL, now, x));
         now = fmaxf(now, top);
-        // (no keys so far: factors 0, and what a NaN query left goes on)
+        if (now == -INFINITY) {   // no keys so far: sums of 0, or NaN by the query
+            if (__any_sync(FULL, l != l)) sum = NAN;
+            continue;
+        }
         const float old = top == -INFINITY ? 0.0f : ex2(top - now), f = m == -INFINITY ? 0.0f : ex2(m - now);
         top = now;
         float add = l * f;

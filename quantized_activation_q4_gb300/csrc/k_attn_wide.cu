@@ -10,8 +10,8 @@
 //
 // Bound by instruction issue: a group of 16 tokens of a head of 128 costs 890 warp instructions for 32 columns (the scales'
 // products, exponentials and moves of 32 columns more than the conversion), at 52% issue. 16 sequences of 1500 to 9000
-// tokens with 8 new tokens each, 32 heads over 8: 57 us and 8 for the join; with two CTAs of 16 columns in k_attn_decode.cu's
-// kernel the call takes 69. The conversions and products in one asm block, as there, spilled registers and took 66.
+// tokens with 8 new tokens each, 32 heads over 8: 57 us and 9 for the join; with two CTAs of 16 columns in k_attn_decode.cu's
+// kernel the call takes 69. The conversions and products in one asm block, as there, spilled registers and took a microsecond more.
 
 #include <algorithm>
 
