@@ -655,7 +655,7 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) attn_prefill_kernel(cons
                 const float lead = ref == -INFINITY ? sink : fmaxf(sink, off);
                 const float down = ref == -INFINITY ? 0.0f : ex2(off - lead);
                 const float total = sink == -INFINITY ? sum * down : fmaf(sum, down, ex2(sink - lead));
-                sum = down == 0.0f ? 0.0f : total / down;
+                if (total == total) sum = down == 0.0f ? 0.0f : total / down;   // (a NaN row has no reference: its sum stays NaN)
             }
             const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;   // no key: 0
             const int64_t row = sq.first + token;
