@@ -715,10 +715,11 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) attn_prefill_kernel(cons
                 const int64_t block0 = row * p.row_blocks + head * NB + k0;
 #pragma unroll 1
                 for (int k = 0; k < NB / 2; k++) {
-                    float y[32], m = 0.0f;
+                    float y[32];
                     block_of(k0 + k, y);
+                    float m = fabsf(y[0]);   // (a NaN row is NaN throughout: its scales are)
 #pragma unroll
-                    for (int x = 0; x < 32; x++) m = fmaxf(m, fabsf(y[x]));
+                    for (int x = 1; x < 32; x++) m = fmaxf(m, fabsf(y[x]));
                     const float d = m / 127.0f, rcp = 1.0f / d;
                     // rint(y / d): the product with 1 / d is within 127 * 2^-22 of the quotient, so divisions only where one
                     // of the block is next to a tie

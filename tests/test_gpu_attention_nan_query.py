@@ -1,7 +1,8 @@
-"""A NaN in a query row and head makes that row and head NaN, whatever the sinks."""
+"""A NaN in a query row and head makes that row and head NaN, whatever the sinks, in rows, image and planes."""
 import numpy as np
 import pytest
 
+from quantized_activation_q4_gb300 import binding as qk
 from tests.kv_helpers import run_attention
 from tests.test_gpu_attention import case, queries
 
@@ -35,3 +36,36 @@ def test_with_sinks(call, kind, D, Hkv, G, lens, n):
         assert np.isnan(got[i, h]).all()
         got[i, h] = clean[i, h]
     assert np.array_equal(got, clean)
+
+
+@pytest.mark.parametrize("call", ["decode", "prefill"])
+@pytest.mark.parametrize("kind", ["none", "finite"])
+@pytest.mark.parametrize("long", [False, True])   # long: the prefill's keys are shared out and joined
+@pytest.mark.parametrize("D,Hkv,G,lens,n", SHAPES)
+def test_image_is_the_quantisers_of_a_nan_row(call, kind, long, D, Hkv, G, lens, n):
+    """The image or planes alone (no rows wanted) are what the library's quantiser makes of the rows, NaN ones among them."""
+    import torch
+    lens = [x + 2100 if long and x else x for x in lens]
+    geo, pages, table, q, sink = inputs(D, Hkv, G, lens, n, kind)
+    q[0, 0, 5], q[n, 1, D - 1] = np.nan, np.nan
+    run = lambda out_elem, image: run_attention(geo, pages, table, lens, q, [n] * len(lens), "f32", 0.1, 0, sink, out_elem,
+                                                image, call, spare_blocks=1)
+    out, _ = run("f32", False)
+    assert np.isnan(out[0, 0]).all() and np.isnan(out[n, 1]).all()
+    _, img = run(None, True)
+    rows, K = out.shape[0], out.shape[1] * D
+    blocks = K // 32 + 1
+    x = torch.from_numpy(out.reshape(rows, K)).cuda()
+    if call == "decode":
+        want = torch.zeros((rows, blocks, 36), dtype=torch.uint8, device="cuda")
+        qk.qk_quantize_q8_1(x, rows, K, K, want, blocks)
+        torch.cuda.synchronize()
+        assert np.array_equal(img, want.cpu().numpy())
+    else:
+        qs = torch.zeros((rows, blocks * 32), dtype=torch.int8, device="cuda")
+        d = torch.zeros((rows, blocks), dtype=torch.int16, device="cuda")
+        qk.qk_quantize_q8_0(x, rows, K, K, qs, d, blocks)
+        torch.cuda.synchronize()
+        assert np.array_equal(img[0], qs.cpu().numpy()) and np.array_equal(img[1], d.cpu().numpy().view(np.uint16))
+        nan = np.isnan(img[1].view(np.float16))
+        assert nan[0, :D // 32].all() and nan[n, D // 32:2 * D // 32].all() and nan.sum() == 2 * D // 32
