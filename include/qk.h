@@ -824,7 +824,7 @@ QK_API qk_status qk_attn_decode(const qk_kv_cache *cache, const qk_attn *attn, i
  * Runs on the tensor cores (tcgen05) with binary16 operands: keys and values
  * (code - 8) * d, queries scaled by a power of two per row, weights exp(s - max),
  * each rounded once, with binary32 sums. Keys and values beyond binary16's range
- * (65504) become infinities. Errors: as qk_attn_decode, and B > 65535 or rows >
+ * are taken as +-65504, its largest. Errors: as qk_attn_decode, and B > 65535 or rows >
  * 2^24 (QK_ERR_UNSUPPORTED). rows = 0 or B = 0 launches nothing.
  */
 QK_API size_t qk_attn_prefill_workspace_bytes(const qk_kv_cache *cache, int64_t B, int64_t max_kv);

@@ -1,7 +1,7 @@
 // Attention of prompts and chunks of prompts over the 4-bit cache (qk_attn_prefill), on tcgen05.
 //
 // attn_stage_kernel turns the call's pages into binary16 once: keys [token][column] and values transposed
-// [column][token], each (code - 8) * d rounded once, so that both products read their second operand K-major by plain
+// [column][token], each (code - 8) * d rounded once and held to +-65504, so that both products read their second operand K-major by plain
 // tensor copies. Inside a group of 16 the tokens are in the order of the value codes' words (position 4 t + s is token
 // 2 t + s % 2 + 8 (s / 2)), in both, so that the words are unpacked without exchanges; the mask undoes it.
 //
@@ -89,8 +89,11 @@ __device__ __forceinline__ int2 find_tile(const PrefillArgs &p, int64_t skip, in
 }
 
 // ---------------------------------------------------------------- staging
+// (code - 8) * d, at most binary16's largest value: an infinity would reach rows that do not see its key, as weight 0 times
+// infinity.
 __device__ __forceinline__ uint32_t value2(uint32_t v, uint32_t bias, __half2 d) {
-    const __half2 r = __hmul2(__hsub2(half2_bits(v), half2_bits(bias)), d);
+    const __half2 most = half2_bits(0x7bff7bffu), x = __hmul2(__hsub2(half2_bits(v), half2_bits(bias)), d);
+    const __half2 r = __hmax2(__hmin2(x, most), __hneg2(most));
     return *reinterpret_cast<const uint32_t *>(&r);
 }
 __device__ __forceinline__ uint32_t lo_half(uint32_t w) { return (w & 0x000F000Fu) | 0x64006400u; }   // 1024 + code
