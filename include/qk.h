@@ -757,10 +757,11 @@ QK_API qk_status qk_kv_read(const qk_kv_cache *cache, const int32_t *slots, int6
  * the keys below kv_lens[b] - n + i + 1, and with a window only the last `window`
  * of them. For every row and head, over the visible keys:
  *   out = sum_j exp(s_j) v_j / (sum_j exp(s_j) + exp(sink)),  s_j = scale * q . k_j
- * A row that sees no key is 0. NaN in a query row and head makes that row and head NaN. Lengths are clamped to what the page table (and
- * max_kv) can hold; keys on a page outside [0, n_pages) are not visible. What the
- * cache holds behind a sequence's last key may be anything, NaN and infinite
- * scales included.
+ * A row that sees no key is 0. NaN in a query row and head makes that row and
+ * head NaN. Lengths are clamped to what the page table (and max_kv) can hold; keys
+ * on a page outside [0, n_pages) are not visible. What the cache holds behind a
+ * sequence's last key, or in front of the first key that any of its rows sees, may
+ * be anything, NaN and infinite scales included.
  */
 typedef struct qk_attn {
     const void *q;             /* [rows][q_stride], n_heads heads of head_dim (qk_kv_append's q_out) */

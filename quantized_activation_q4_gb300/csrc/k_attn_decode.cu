@@ -272,6 +272,7 @@ attn_decode_kernel(const __grid_constant__ DecodeArgs p, bool wide) {
         const uint32_t buf = ring + stage * STAGE;
         const int token0 = now.s.base + now.tile * TILE + warp * WARP_TOKENS;
         const int end0 = now.s.len - p.T + 1;   // keys that the first of the new tokens sees
+        const int begin0 = p.a.window > 0 ? end0 - p.a.window : 0;   // no token sees a key below
         // scores, times log2 e
         float s[GROUPS][NT][4];
         uint32_t used = 0, any = 0;
@@ -338,13 +339,14 @@ attn_decode_kernel(const __grid_constant__ DecodeArgs p, bool wide) {
                 top[n][e] = m;
                 move |= m - ref[n][e] > HEADROOM;   // (no: both are minus infinity)
             }
-        // the values' scales of a group: zero behind the last key, where the cache may hold anything
+        // the values' scales of a group: zero for keys that no token sees, where the cache may hold anything
         const auto value_scales = [&](int r, uint32_t (&dv)[2 * NB]) {
             lds_words<2 * NB>(buf + r * GB + 17 * D + t * 8 * NB, dv);
             if (!whole) {
                 const int j = token0 + r * GROUP + 2 * t, len = used >> (8 * r) & 1 ? now.s.len : 0;
-                const uint32_t k0 = (j < len ? 0xffffu : 0) | (j + 1 < len ? 0xffff0000u : 0);
-                const uint32_t k1 = (j + 8 < len ? 0xffffu : 0) | (j + 9 < len ? 0xffff0000u : 0);
+                const auto seen = [&](int i) { return i >= begin0 && i < len; };
+                const uint32_t k0 = (seen(j) ? 0xffffu : 0) | (seen(j + 1) ? 0xffff0000u : 0);
+                const uint32_t k1 = (seen(j + 8) ? 0xffffu : 0) | (seen(j + 9) ? 0xffff0000u : 0);
 #pragma unroll
                 for (int b = 0; b < NB; b++) dv[2 * b] &= k0, dv[2 * b + 1] &= k1;
             }

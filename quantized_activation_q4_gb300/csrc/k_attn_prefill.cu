@@ -54,14 +54,15 @@ struct PrefillArgs {
 
 // Rows and keys of a sequence.
 struct Span1 {
-    int first, n, len, base;   // first row, rows, keys, first key that any row sees (a multiple of 128)
+    int first, n, len, seen, base;   // first row, rows, keys, first key that any row sees, that one rounded down to 128
 };
 __device__ __forceinline__ Span1 span_of(const PrefillArgs &p, int b) {
     Span1 s;
     s.first = min(max(ld_prev(p.offsets + b), 0), p.rows);
     s.n = max(0, min(max(ld_prev(p.offsets + b + 1), 0), p.rows) - s.first);
     s.len = min(max(ld_prev(p.a.kv_lens + b), 0), p.max_kv);
-    s.base = p.a.window > 0 ? max(0, s.len - s.n + 1 - p.a.window) & ~(PAD - 1) : 0;
+    s.seen = p.a.window > 0 ? max(0, s.len - s.n + 1 - p.a.window) : 0;
+    s.base = s.seen & ~(PAD - 1);
     return s;
 }
 
@@ -123,7 +124,7 @@ __global__ void __launch_bounds__(128) attn_stage_kernel(const __grid_constant__
     for (int x = lane; x < GROUP * 4 * (NB / W); x += 32) {
         const int t = x & 3, i = x / 4 % GROUP, bq = x / (4 * GROUP);
         const int row = 4 * (i % 8 / 2) + i % 2 + i / 8 * 2;
-        const bool keep = good && token + i < s.len;
+        const bool keep = good && token + i < s.len && token + i >= s.seen;
         uint32_t words[W], scales[W / 2];   // of W blocks side by side
         if (keep) {
             const uint8_t *kw = g + k_word_at(D, i, bq * W, t), *ks = g + k_scale_at(D, i, bq * W);
@@ -157,8 +158,8 @@ __global__ void __launch_bounds__(128) attn_stage_kernel(const __grid_constant__
 #pragma unroll
     for (int x = lane; x < D / 64 * 32; x += 32) {
         const int t = x & 3, u = x / 4 % 8, mq = x / 32;
-        const bool k0 = token + 2 * t < s.len, k1 = token + 2 * t + 1 < s.len, k2 = token + 2 * t + 8 < s.len,
-                   k3 = token + 2 * t + 9 < s.len;
+        const auto seen = [&](int j) { return j >= s.seen && j < s.len; };
+        const bool k0 = seen(token + 2 * t), k1 = seen(token + 2 * t + 1), k2 = seen(token + 2 * t + 8), k3 = seen(token + 2 * t + 9);
         uint4 w = make_uint4(0, 0, 0, 0), d4 = w;   // two blocks' scales
         if (good) {
             w = ld_prev(reinterpret_cast<const uint4 *>(g + 9 * D + x * 16));
@@ -169,7 +170,7 @@ __global__ void __launch_bounds__(128) attn_stage_kernel(const __grid_constant__
         for (int e = 0; e < 4; e++) {
             const int m = mq * 4 + e;
             uint2 d = e < 2 ? make_uint2(d4.x, d4.y) : make_uint2(d4.z, d4.w);
-            // (a scale behind the last key may be anything: it is taken as 0)
+            // (a scale behind the last key or in front of the first that is seen may be anything: it is taken as 0)
             d.x &= (k0 ? 0xffffu : 0) | (k1 ? 0xffff0000u : 0);
             d.y &= (k2 ? 0xffffu : 0) | (k3 ? 0xffff0000u : 0);
             const uint32_t y = words[e], y8 = y >> 8;

@@ -206,6 +206,7 @@ attn_wide_kernel(const __grid_constant__ DecodeArgs p, bool wide) {
         const uint32_t buf = ring + stage * Z::STAGE, mine = buf + warp * GB;
         const int token0 = now.s.base + now.tile * TILE;
         const int end0 = now.s.len - p.T + 1;   // keys that the first of the new tokens sees
+        const int begin0 = p.a.window > 0 ? end0 - p.a.window : 0;   // no token sees a key below
         const uint32_t used = ok ? *reinterpret_cast<const uint32_t *>(&use[stage][0]) : 0;   // a byte a group
         const bool whole = used == 0x01010101u && token0 + TILE <= end0 && (p.a.window == 0 || token0 >= now.s.len - p.a.window);
 
@@ -269,14 +270,15 @@ attn_wide_kernel(const __grid_constant__ DecodeArgs p, bool wide) {
         for (int n = 0; n < NT; n++)
 #pragma unroll
             for (int e = 0; e < 2; e++) move |= fmaxf(s[n][e], s[n][2 + e]) - ref[n][e] > HEADROOM;   // (no: both minus infinity)
-        // the values' scales of a block, tokens 2t, 2t + 1 and 2t + 8, 2t + 9 of a group: zero behind the last key, where the
-        // cache may hold anything
+        // the values' scales of a block, tokens 2t, 2t + 1 and 2t + 8, 2t + 9 of a group: zero for keys that no token sees,
+        // where the cache may hold anything
         const auto value_scales = [&](int r, int b) {
             uint2 d = lds64(buf + r * GB + 17 * D + (t * NB + b) * 8);
             if (!whole) {
                 const int j = token0 + r * GROUP + 2 * t, len = used >> (8 * r) & 1 ? now.s.len : 0;
-                d.x &= (j < len ? 0xffffu : 0) | (j + 1 < len ? 0xffff0000u : 0);
-                d.y &= (j + 8 < len ? 0xffffu : 0) | (j + 9 < len ? 0xffff0000u : 0);
+                const auto seen = [&](int i) { return i >= begin0 && i < len; };
+                d.x &= (seen(j) ? 0xffffu : 0) | (seen(j + 1) ? 0xffff0000u : 0);
+                d.y &= (seen(j + 8) ? 0xffffu : 0) | (seen(j + 9) ? 0xffff0000u : 0);
             }
             return d;
         };

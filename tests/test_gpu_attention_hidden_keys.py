@@ -3,7 +3,7 @@ import numpy as np
 import pytest
 
 from oracle import kv as OK
-from tests.kv_helpers import decode_error, run_attention
+from tests.kv_helpers import bound_of, decode_error, expected, poison, run_attention
 from tests.test_gpu_attention import case, check, queries
 
 pytestmark = pytest.mark.gpu
@@ -57,3 +57,24 @@ def test_large_keys(D):
     kk = np.clip(k[slots], -HALF_MAX, HALF_MAX)
     want, parts = OK.attention(q.astype(np.float64), kk, v[slots], np.ones(100, bool), n, 1e-6)
     check(out, want, decode_error(v[slots], want, parts, G, True), "f32")
+
+
+@pytest.mark.parametrize("call,D,Hkv,G,n", [
+    ("prefill", 128, 2, 4, 10), ("prefill", 64, 1, 3, 130), ("prefill", 256, 1, 2, 70),
+    ("decode", 128, 2, 4, 1), ("decode", 64, 1, 16, 1), ("decode", 256, 1, 4, 2), ("decode", 128, 1, 8, 8),
+])
+@pytest.mark.parametrize("window", [1, 40, 77])
+def test_nothing_in_front_of_the_first_visible_key_is_used(call, D, Hkv, G, n, window):
+    """Scales of NaN and infinity at every token below the first that any row sees, in its group of 16 too."""
+    rng = np.random.default_rng(D + window + n)
+    lens = [300, 1000, 170, n]
+    geo, pages, table = case(rng, D, Hkv, 16, lens)
+    seen = []
+    for b, length in enumerate(lens):
+        j = np.arange(max(0, length - n + 1 - window), length)
+        seen.append(table[b, j // 16].astype(np.int64) * 16 + j % 16)
+    poison(pages, geo, np.concatenate(seen))
+    q = queries(rng, n * len(lens), Hkv * G, D, "f32")
+    out, _ = run_attention(geo, pages, table, lens, q, [n] * len(lens), "f32", 0.1, window, None, "f32", False, call)
+    want, parts = expected(geo, pages, table, lens, q, [n] * len(lens), 0.1, window, None)
+    check(out, want, bound_of(parts, call == "prefill"), "f32")
