@@ -771,7 +771,7 @@ typedef struct qk_attn {
     const int32_t *page_table; /* [B][table_stride] */
     int64_t table_stride;      /* pages a sequence can have; table_stride * page_tokens <= 2^30 */
     const int32_t *kv_lens;    /* [B] */
-    float scale;               /* finite, > 0 */
+    float scale;               /* finite, > 0; 3 * scale * the largest |q| of a row and head has to be finite in binary32 */
     int32_t window;            /* 0: none */
     const float *sinks;        /* [n_heads] extra logits (not scaled), finite or minus infinity; or NULL */
     void *out;                 /* [rows][out_stride] of type out_elem, or NULL when only the image is wanted */

@@ -136,10 +136,10 @@ __device__ __forceinline__ void load_queries(Queries<D, NT> &q, const DecodeArgs
             }
         top = fmaxf(top, __shfl_xor_sync(FULL, top, 1));
         top = fmaxf(top, __shfl_xor_sync(FULL, top, 2));
-        // 2^e is above the largest magnitude; its inverse stays a normal number
-        const int e2 = min(max((int)(__float_as_uint(top) >> 23) - 126, -100), 100);
+        // 2^e is above the largest magnitude (above a quarter of it from 2^126 on); it and its inverse are normal numbers
+        const int e2 = min(max((int)(__float_as_uint(top) >> 23) - 126, -126), 126);
         const float down = __uint_as_float((uint32_t)(127 - e2) << 23), up = __uint_as_float((uint32_t)(127 + e2) << 23);
-        const float c = p.a.scale * LOG2E * up;   // (0 where the queries are 0 and it underflows: so are the scores)
+        const float c = p.a.scale * up * LOG2E;   // (0 where the queries are 0 and it underflows: so are the scores)
 #pragma unroll
         for (int k = 0; k < NB; k++) {
             float bias = 0.0f;

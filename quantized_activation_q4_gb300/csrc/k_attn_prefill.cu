@@ -320,10 +320,10 @@ __device__ __forceinline__ void load_queries(const PrefillArgs &p, const Q *q, i
                               fmaxf(fmaxf(fabsf(c.x), fabsf(c.y)), fmaxf(fabsf(c.z), fabsf(c.w))));
 #pragma unroll
             for (int m = 1; m < LANES; m <<= 1) top = fmaxf(top, __shfl_xor_sync(FULL, top, m));
-            // (the inverse of the power of two stays a normal number)
-            const int e = min(max((int)(__float_as_uint(top) >> 23) - 126, -100), 100);
+            // (2^e and its inverse are normal numbers: from 2^126 on it is above a quarter of the magnitude)
+            const int e = min(max((int)(__float_as_uint(top) >> 23) - 126, -126), 126);
             const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-            if (unit == 0) factor[r] = fmaxf(p.a.scale * LOG2E * __uint_as_float((uint32_t)(127 + e) << 23), 0x1p-126f);
+            if (unit == 0) factor[r] = fmaxf(p.a.scale * __uint_as_float((uint32_t)(127 + e) << 23) * LOG2E, 0x1p-126f);
             *reinterpret_cast<uint4 *>(tile + (unit / 8) * ROWS * 128 + r * 128 + (((unit & 7) ^ (r & 7)) << 4)) =
                 make_uint4(pack2(a.x * down, a.y * down), pack2(a.z * down, a.w * down), pack2(c.x * down, c.y * down),
                            pack2(c.z * down, c.w * down));

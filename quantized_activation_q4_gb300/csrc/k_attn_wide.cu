@@ -169,10 +169,10 @@ attn_wide_kernel(const __grid_constant__ DecodeArgs p, bool wide) {
                     }
                 top = fmaxf(top, __shfl_xor_sync(FULL, top, 1));
                 top = fmaxf(top, __shfl_xor_sync(FULL, top, 2));
-                // 2^e is above the largest magnitude; its inverse stays a normal number
-                const int e2 = min(max((int)(__float_as_uint(top) >> 23) - 126, -100), 100);
+                // 2^e is above the largest magnitude (above a quarter of it from 2^126 on); it and its inverse are normal numbers
+                const int e2 = min(max((int)(__float_as_uint(top) >> 23) - 126, -126), 126);
                 const float down = __uint_as_float((uint32_t)(127 - e2) << 23);
-                if (t == 0) column_scale[8 * n + g] = p.a.scale * LOG2E * __uint_as_float((uint32_t)(127 + e2) << 23);
+                if (t == 0) column_scale[8 * n + g] = p.a.scale * __uint_as_float((uint32_t)(127 + e2) << 23) * LOG2E;
 #pragma unroll
                 for (int k = 0; k < NB; k++) {
                     const float4 x = part(k, 0), y = part(k, 1);
