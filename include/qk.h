@@ -757,6 +757,8 @@ QK_API qk_status qk_kv_read(const qk_kv_cache *cache, const int32_t *slots, int6
  * the keys below kv_lens[b] - n + i + 1, and with a window only the last `window`
  * of them. For every row and head, over the visible keys:
  *   out = sum_j exp(s_j) v_j / (sum_j exp(s_j) + exp(sink)),  s_j = scale * q . k_j
+ * Logits have to be finite in binary32 (times log2 e). From about 2^22 on, logits
+ * closer to the largest than their rounding may share its weight.
  * A row that sees no key is 0. NaN in a query row and head makes that row and
  * head NaN. Lengths are clamped to what the page table (and max_kv) can hold; keys
  * on a page outside [0, n_pages) are not visible. What the cache holds behind a

@@ -32,6 +32,7 @@ constexpr int ROWS = 128;           // rows of a tile: lanes of tensor memory
 constexpr int PAD = 128;            // staged lengths are whole multiples
 constexpr float HEADROOM = 8.0f;    // the reference maximum moves when a logit is 2^8 above it
 constexpr float LIFT = 6.0f;        // weights are held times 2^6 below the reference: at most 2^14
+constexpr float UNLIFT = 0x1p-6f;
 
 struct PrefillArgs {
     CUtensorMap kmap, vmap;   // keys [B Hkv Lpad][D], values [B Hkv D][Lpad]
@@ -46,7 +47,7 @@ struct PrefillArgs {
     int64_t row_blocks;
     bool q_wide, out_wide, out16;   // out16: bfloat16 rows start on 16-byte boundaries
     // a tile's keys in `parts` shares of steps; with more than one, unnormalised outputs [CTA][row][D] and, for each
-    // row, the exponent of its weights' unit (minus infinity: no key) and their sum
+    // row, its reference (minus infinity: no key) and the sum of the weights relative to it
     int parts;
     float *part_o;
     float2 *part_ml;
@@ -181,6 +182,19 @@ __global__ void __launch_bounds__(128) attn_stage_kernel(const __grid_constant__
                 make_uint2(value2(hi_half(y), HI_BIAS, half2_bits(d.x)), value2(hi_half(y8), HI_BIAS, half2_bits(d.y)));
         }
     }
+}
+
+// Logits (times log2 e) far from 0. A score is off by 2^-11 of its terms (its operands are binary16), so beyond 2^22 which of
+// nearly equal logits is the larger is not known, and one number holds neither such a reference with the lift of the weights
+// nor a score's product with the row's factor to a unit. While a row's reference is beyond, its factor is less by the power
+// of two that brings the reference below: logits within about 2^-18 of it share the weight, all others get none.
+__device__ __forceinline__ float far_factor(float reference) {
+    const int e = (int)(__float_as_uint(reference) >> 23 & 255) - (127 + 21);
+    return e > 0 && reference != -INFINITY ? __uint_as_float((uint32_t)(127 - e) << 23) : 1.0f;
+}
+// a / b of numbers that differ by a power of two alone
+__device__ __forceinline__ float power_ratio(float a, float b) {
+    return __uint_as_float(0x3f800000u + __float_as_uint(a) - __float_as_uint(b));
 }
 
 // ---------------------------------------------------------------- attention
@@ -364,8 +378,8 @@ struct Shape {
     static constexpr int OFF_K = TILES * Q_BYTES;
     static constexpr int OFF_V = OFF_K + STAGES * K_BYTES;
     static constexpr int OFF_SCALE = OFF_V + STAGES * V_BYTES;   // a row's factor
-    static constexpr int OFF_TOP = OFF_SCALE + TILES * ROWS * 4;   // the two halves' maxima, two steps
-    static constexpr int OFF_BAR = OFF_TOP + TILES * 2 * 2 * ROWS * 4;
+    static constexpr int OFF_TOP = OFF_SCALE + TILES * ROWS * 4;   // a thread's maxima of two steps, and its row's factor
+    static constexpr int OFF_BAR = OFF_TOP + TILES * 2 * 3 * ROWS * 4;
     // q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_half[2], p_full[2], o_full[2], done
     static constexpr int N_BARS = 1 + 4 * STAGES + 4 * 2 + 1;
     static constexpr int SMEM = OFF_BAR + 8 * N_BARS + 16 + 1024;
@@ -529,14 +543,14 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) attn_prefill_kernel(cons
         // the two warps of 32 rows meet (what one reads of tensor memory and the other writes are these rows' lanes)
         const auto meet = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + 4 * i + quad) : "memory"); };
         meet();   // the factors are written
-        float *const mine = reinterpret_cast<float *>(smem + Z::OFF_TOP) + (i * 2 + hf) * 2 * ROWS + r;
-        const float *const other = reinterpret_cast<float *>(smem + Z::OFF_TOP) + (i * 2 + 1 - hf) * 2 * ROWS + r;
+        float *const mine = reinterpret_cast<float *>(smem + Z::OFF_TOP) + (i * 2 + hf) * 3 * ROWS + r;
+        const float *const other = reinterpret_cast<float *>(smem + Z::OFF_TOP) + (i * 2 + 1 - hf) * 3 * ROWS + r;
         const int rho = row0 + i * ROWS + r;
         const bool there = rho < rows_all;
         const int token = there ? rho / p.G : sq.n - 1, head = h * p.G + (there ? rho - token * p.G : 0);
         const int my_end = sq.len - sq.n + token + 1, my_begin = p.a.window > 0 ? max(0, my_end - p.a.window) : 0;
-        const float c = steps > 0 ? factor[i * ROWS + r] : 0.0f;
-        float ref = -INFINITY, off = 0.0f, sum = 0.0f;
+        mine[2 * ROWS] = steps > 0 ? factor[i * ROWS + r] : 1.0f;
+        float c = mine[2 * ROWS], ref = -INFINITY, off = 0.0f, sum = 0.0f;   // c: the factor, or less by far_factor
         bool ok = true;
         for (int j = 0; j < steps; j++) {   // (a wait that ran out goes on without work: both halves meet in every step)
             const int kv = begin + j * BN + hf * HALF;
@@ -594,9 +608,10 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) attn_prefill_kernel(cons
                     }
                 }
                 sum *= down;
-                ref = now;
-                // a little above the maximum for huge logits, whose products with c round
-                off = now == -INFINITY ? 0.0f : fmaf(fabsf(now), 0x1p-22f, now) - LIFT;
+                const float c0 = mine[2 * ROWS], logit = now * power_ratio(c0, c), f = far_factor(logit);
+                c = c0 * f;
+                ref = logit * f;
+                off = ref == -INFINITY ? 0.0f : ref - LIFT;
             }
             uint64_t sums[2] = {0, 0};
             const uint64_t c2 = two(c, c), off2 = two(-off, -off);
@@ -618,6 +633,7 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) attn_prefill_kernel(cons
             tc_fence_before();
             mbar_arrive((hf ? p_full : p_half) + 8 * i);
         }
+        ref *= power_ratio(mine[2 * ROWS], c);
         // the row's sum, then its outputs: a half of the columns each
         mine[(steps & 1) * ROWS] = sum;
         meet();
@@ -641,7 +657,7 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) attn_prefill_kernel(cons
         };
         if (p.parts > 1) {   // what this share of the keys gives; attn_join_kernel goes on
             const int64_t at = (int64_t)blockIdx.x * CTA_ROWS + i * ROWS + r;
-            if (hf == 0 && there && ok) p.part_ml[at] = make_float2(ref == -INFINITY ? -INFINITY : off, sum);
+            if (hf == 0 && there && ok) p.part_ml[at] = make_float2(ref, sum * UNLIFT);
 #pragma unroll 1
             for (int k = hf * NB / 2; k < (hf + 1) * NB / 2 && steps > 0; k++) {
                 uint32_t v[32];
@@ -649,19 +665,18 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) attn_prefill_kernel(cons
                 tmem_wait_ld(v);
                 float y[32];
 #pragma unroll
-                for (int x = 0; x < 32; x++) y[x] = __uint_as_float(v[x]);
+                for (int x = 0; x < 32; x++) y[x] = __uint_as_float(v[x]) * UNLIFT;
                 store_block(y, reinterpret_cast<uint8_t *>(p.part_o), (at * D + 32 * k) * 4, there && ok);
             }
         } else {
+            float inv = sum == 0.0f ? 0.0f : 1.0f / sum;   // no key: 0
             if (p.a.sinks) {
                 const float sink = ld_prev(p.a.sinks + head) * LOG2E;
-                // the weights' unit is 2^off; a sink far above it takes all
-                const float lead = ref == -INFINITY ? sink : fmaxf(sink, off);
-                const float down = ref == -INFINITY ? 0.0f : ex2(off - lead);
+                // relative to the larger of reference and sink: one far above the other takes all
+                const float lead = fmaxf(sink, ref), down = ref == -INFINITY ? 0.0f : ex2(ref - lead) * UNLIFT;
                 const float total = sink == -INFINITY ? sum * down : fmaf(sum, down, ex2(sink - lead));
-                if (total == total) sum = down == 0.0f ? 0.0f : total / down;   // (a NaN row has no reference: its sum stays NaN)
+                inv = total == 0.0f ? 0.0f : down / total;   // (a NaN row has no reference: its sum stays NaN)
             }
-            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;   // no key: 0
             const int64_t row = sq.first + token;
             const bool any = steps > 0 && inv != 0.0f, mine_ok = there && ok;
             const int k0 = hf * NB / 2;
