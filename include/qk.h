@@ -796,7 +796,9 @@ typedef struct qk_attn {
  *        ones.
  * Products run on the tensor cores with binary16 operands (queries scaled by a
  * power of two per row and rounded once; weights exp(s - max) * d rounded twice)
- * and binary32 sums: within about 2^-10 of the sum of the magnitudes.
+ * and binary32 sums: within about 2^-10 of the sum of the magnitudes, and for each
+ * key 2^-28 of the largest weight times the largest value more (2^-25 where block
+ * scales of values reach 64).
  * The keys of all sequences are shared out over the device by their lengths, so an
  * output's last bits depend on the lengths of the whole call (not on the run).
  * Errors: QK_ERR_ARG, QK_ERR_SHAPE, QK_ERR_UNSUPPORTED (T > 8, head_dim, n_heads),

@@ -14,8 +14,8 @@
 // A nibble becomes a half by one logic operation (1024 + code, or 64 + code in a high nibble). For S the bias leaves as the
 // initial accumulator, -(1032 or 72) * sum q, once per segment; for O it is subtracted (the weights' sum would cancel
 // catastrophically over long sequences). Queries are divided by a power of two to stay inside binary16, whatever their
-// size. Weights are kept at up to 2^14 times their value, so those down to 2^-28 of the largest keep binary16's precision;
-// where a value's scale is 2 or more, its exponent joins the running maximum.
+// size. Weights are held as 2^6 at the reference and up to 2^14, those below 2^-20 of the reference to 2^-31 of it; what
+// happens where the values' scales are not between 2^-3 and 2 is in qk_decode.cuh.
 //
 // A tile is 128 tokens, 64 for each of two warps (four groups: the barrier, the votes and the places of pages are paid for
 // once; with 32 tokens a warp and tile 64 sequences of 8192 keys took 84 us for 71). Six CTAs an SM by registers (168) and
@@ -240,7 +240,7 @@ attn_decode_kernel(const __grid_constant__ DecodeArgs p, bool wide) {
 
     float o[MT][NT][4], ref[NT][2], sum[NT][2], off[NT][2];
     Queries<D, NT> q;
-    int lift_e = 0;       // exponent of the largest value scale so far (0 while all are below 2)
+    int top_e = SMALLEST;   // exponent of the largest value scale so far
     bool fresh = true;    // a segment begins
     int stage = 0;
     uint32_t parity = 0, late_parity = 0;
@@ -262,7 +262,7 @@ attn_decode_kernel(const __grid_constant__ DecodeArgs p, bool wide) {
                 for (int n = 0; n < NT; n++)
 #pragma unroll
                     for (int e = 0; e < 4; e++) o[m][n][e] = 0.0f;
-            lift_e = 0;
+            top_e = SMALLEST;
             fresh = false;
         }
         if (ok) {
@@ -339,18 +339,12 @@ attn_decode_kernel(const __grid_constant__ DecodeArgs p, bool wide) {
                 top[n][e] = m;
                 move |= m - ref[n][e] > HEADROOM;   // (no: both are minus infinity)
             }
-        // the values' scales of a group: zero for keys that no token sees, where the cache may hold anything
-        const auto value_scales = [&](int r, uint32_t (&dv)[2 * NB]) {
-            lds_words<2 * NB>(buf + r * GB + 17 * D + t * 8 * NB, dv);
-            if (!whole) {
-                const int j = token0 + r * GROUP + 2 * t, len = used >> (8 * r) & 1 ? now.s.len : 0;
-                const auto seen = [&](int i) { return i >= begin0 && i < len; };
-                const uint32_t k0 = (seen(j) ? 0xffffu : 0) | (seen(j + 1) ? 0xffff0000u : 0);
-                const uint32_t k1 = (seen(j + 8) ? 0xffffu : 0) | (seen(j + 9) ? 0xffff0000u : 0);
-#pragma unroll
-                for (int b = 0; b < NB; b++) dv[2 * b] &= k0, dv[2 * b + 1] &= k1;
-            }
-        };
+        // the values' scales
+        if (!whole)
+#pragma unroll 1
+            for (int r = 0; r < GROUPS; r++)
+                hide_scales<NB>(buf + r * GB + 17 * D, token0 + r * GROUP, begin0, used >> (8 * r) & 1 ? now.s.len : 0);
+        const auto value_scales = [&](int r, uint32_t (&dv)[2 * NB]) { lds_words<2 * NB>(buf + r * GB + 17 * D + t * 8 * NB, dv); };
 #pragma unroll
         for (int r = 0; r < GROUPS; r++) {
             uint32_t dv[2 * NB];
@@ -358,27 +352,25 @@ attn_decode_kernel(const __grid_constant__ DecodeArgs p, bool wide) {
 #pragma unroll
             for (int b = 0; b < NB; b++) any |= dv[2 * b] | dv[2 * b + 1];
         }
-        const bool large = (any & 0x40004000u) != 0;   // a scale of 2 or more
-        int e_new = lift_e;
+        const bool large = (any & 0x40004000u) != 0 || !usual(top_e);   // a scale of 2 or more, or unusual ones so far
+        int e_new = top_e;
         if (__any_sync(FULL, move || large)) {
             if (__any_sync(FULL, large)) {
-                float m = 0.0f;
+                __half2 m = half2_bits(0);
 #pragma unroll 1
                 for (int r = 0; r < GROUPS; r++) {
                     uint32_t dv[2 * NB];
                     value_scales(r, dv);
 #pragma unroll
-                    for (int x = 0; x < 2 * NB; x++) {
-                        const float2 f = __half22float2(__habs2(half2_bits(dv[x])));
-                        m = fmaxf(m, fmaxf(f.x, f.y));
-                    }
+                    for (int x = 0; x < 2 * NB; x++) m = __hmax2(m, __habs2(half2_bits(dv[x])));
                 }
-#pragma unroll
-                for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, x));
-                e_new = min(max(e_new, (int)(__float_as_uint(m) >> 23) - 127), 16);
+                e_new = largest_exponent(m, top_e);
+                if (!usual(e_new))
+#pragma unroll 1
+                    for (int r = 0; r < GROUPS; r++) boost_scales<NB>(buf + r * GB + 17 * D, boost_of(e_new));
             }
         }
-        if (__any_sync(FULL, move) || e_new != lift_e) {
+        if (__any_sync(FULL, move) || e_new != top_e) {
 #pragma unroll
             for (int n = 0; n < NT; n++)
 #pragma unroll
@@ -388,9 +380,11 @@ attn_decode_kernel(const __grid_constant__ DecodeArgs p, bool wide) {
                     m = fmaxf(m, __shfl_xor_sync(FULL, m, 8));
                     m = fmaxf(m, __shfl_xor_sync(FULL, m, 16));
                     const float r = fmaxf(ref[n][e], m);
-                    const float down = ref[n][e] == -INFINITY ? 0.0f : ex2(ref[n][e] - r + (float)(lift_e - e_new));
+                    // (rounded up, never below: weights stay under 2^14)
+                    const float unit = r == -INFINITY ? 0.0f : __fadd_ru(r, (float)lift_of(e_new) - LIFT);
+                    const float down = ref[n][e] == -INFINITY ? 0.0f : ex2(off[n][e] - unit);
                     ref[n][e] = r;
-                    off[n][e] = r == -INFINITY ? 0.0f : __fadd_ru(r, (float)e_new - LIFT);   // never below: weights stay under 2^14
+                    off[n][e] = unit;
                     sum[n][e] *= down;
 #pragma unroll
                     for (int m = 0; m < MT; m++) {
@@ -398,7 +392,16 @@ attn_decode_kernel(const __grid_constant__ DecodeArgs p, bool wide) {
                         o[m][n][2 + e] *= down;
                     }
                 }
-            lift_e = e_new;
+            if (boost_of(e_new) != boost_of(top_e)) {
+                const float change = power_of_two(boost_of(e_new) - boost_of(top_e));
+#pragma unroll
+                for (int m = 0; m < MT; m++)
+#pragma unroll
+                    for (int n = 0; n < NT; n++)
+#pragma unroll
+                        for (int e = 0; e < 4; e++) o[m][n][e] *= change;
+            }
+            top_e = e_new;
         }
 #pragma unroll
         for (int r = 0; r < GROUPS; r++) {
@@ -456,7 +459,7 @@ attn_decode_kernel(const __grid_constant__ DecodeArgs p, bool wide) {
                     float m = -INFINITY;
 #pragma unroll
                     for (int w = 0; w < WARPS; w++) m = fmaxf(m, meet[w][2 * t + e].x);
-                    down[e] = ref[n][e] == -INFINITY ? 0.0f : ex2(off[n][e] - m);
+                    down[e] = ref[n][e] == -INFINITY ? 0.0f : ex2(off[n][e] - m) * power_of_two(-boost_of(top_e));
                 }
                 float *mine = reinterpret_cast<float *>(smem + (warp * S + stage) * STAGE);
 #pragma unroll

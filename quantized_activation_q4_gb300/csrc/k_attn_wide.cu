@@ -74,7 +74,7 @@ attn_wide_kernel(const __grid_constant__ DecodeArgs p, bool wide) {
     __shared__ int64_t found[2];
     __shared__ float column_scale[8 * NT];
     __shared__ float meet[WARPS][8 * NT];   // a column's largest score, or its sum, of each warp
-    __shared__ float scales[WARPS];         // the largest scale of the values
+    __shared__ int exponents[WARPS];        // of the largest scale of the values
     __shared__ __align__(4) uint8_t use[S][WARPS];
     __shared__ __align__(8) uint64_t bars[S];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -139,7 +139,7 @@ attn_wide_kernel(const __grid_constant__ DecodeArgs p, bool wide) {
     for (int s = 0; s < S; s++) issue(s);
 
     float o[MT][NT][4], scale[NT][2], ref[NT][2], sum[NT][2], off[NT][2];
-    int lift_e = 0;       // exponent of the largest value scale so far (0 while all are below 2)
+    int top_e = SMALLEST;   // exponent of the largest value scale so far
     bool fresh = true;    // a segment begins
     int stage = 0, buffer = 0, late = 0;
     int left_behind = -1;   // the stage of the tile before
@@ -196,7 +196,7 @@ attn_wide_kernel(const __grid_constant__ DecodeArgs p, bool wide) {
                 for (int n = 0; n < NT; n++)
 #pragma unroll
                     for (int e = 0; e < 4; e++) o[m][n][e] = 0.0f;
-            lift_e = 0;
+            top_e = SMALLEST;
             fresh = false;
         }
         if (ok) {
@@ -270,28 +270,19 @@ attn_wide_kernel(const __grid_constant__ DecodeArgs p, bool wide) {
         for (int n = 0; n < NT; n++)
 #pragma unroll
             for (int e = 0; e < 2; e++) move |= fmaxf(s[n][e], s[n][2 + e]) - ref[n][e] > HEADROOM;   // (no: both minus infinity)
-        // the values' scales of a block, tokens 2t, 2t + 1 and 2t + 8, 2t + 9 of a group: zero for keys that no token sees,
-        // where the cache may hold anything
-        const auto value_scales = [&](int r, int b) {
-            uint2 d = lds64(buf + r * GB + 17 * D + (t * NB + b) * 8);
-            if (!whole) {
-                const int j = token0 + r * GROUP + 2 * t, len = used >> (8 * r) & 1 ? now.s.len : 0;
-                const auto seen = [&](int i) { return i >= begin0 && i < len; };
-                d.x &= (seen(j) ? 0xffffu : 0) | (seen(j + 1) ? 0xffff0000u : 0);
-                d.y &= (seen(j + 8) ? 0xffffu : 0) | (seen(j + 9) ? 0xffff0000u : 0);
-            }
-            return d;
-        };
+        // the values' scales of a block, tokens 2t, 2t + 1 and 2t + 8, 2t + 9 of a group
+        if (!whole) hide_scales<NB>(mine + 17 * D, token0 + warp * GROUP, begin0, used >> (8 * warp) & 1 ? now.s.len : 0);
+        const auto value_scales = [&](int r, int b) { return lds64(buf + r * GB + 17 * D + (t * NB + b) * 8); };
         uint32_t any = 0;   // of the warp's group: bit 14 of a half is set from 2 on
 #pragma unroll
         for (int b = 0; b < NB; b++) {
             const uint2 d = value_scales(warp, b);
             any |= d.x | d.y;
         }
-        const bool large = (any & 0x40004000u) != 0;
+        const bool large = (any & 0x40004000u) != 0 || !usual(top_e);   // a scale of 2 or more, or unusual ones so far
         // All warps meet: what the tile before left in shared memory has been read, and whether something moves.
         if (__syncthreads_or(move || large)) {
-            float top[NT][2], m = 0.0f;
+            float top[NT][2];
 #pragma unroll
             for (int n = 0; n < NT; n++)
 #pragma unroll
@@ -302,20 +293,19 @@ attn_wide_kernel(const __grid_constant__ DecodeArgs p, bool wide) {
                     x = fmaxf(x, __shfl_xor_sync(FULL, x, 16));
                     if (g == 0) meet[warp][8 * n + 2 * t + e] = x;
                 }
-#pragma unroll 1
+            __half2 m = half2_bits(0);
+#pragma unroll
             for (int b = 0; b < NB; b++) {
                 const uint2 d = value_scales(warp, b);
-                const float2 x = __half22float2(__habs2(half2_bits(d.x))), y = __half22float2(__habs2(half2_bits(d.y)));
-                m = fmaxf(m, fmaxf(fmaxf(x.x, x.y), fmaxf(y.x, y.y)));
+                m = __hmax2(m, __hmax2(__habs2(half2_bits(d.x)), __habs2(half2_bits(d.y))));
             }
-#pragma unroll
-            for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, x));
-            if (lane == 0) scales[warp] = m;
+            const int mine_e = largest_exponent(m, top_e);
+            if (lane == 0) exponents[warp] = mine_e;
             __syncthreads();
-            int e_new = lift_e;
+            int e_new = top_e;
 #pragma unroll
             for (int w = 0; w < WARPS; w++) {
-                if (scales[w] >= 2.0f) e_new = min(max(e_new, (int)(__float_as_uint(scales[w]) >> 23) - 127), 16);
+                e_new = max(e_new, exponents[w]);
 #pragma unroll
                 for (int n = 0; n < NT; n++)
 #pragma unroll
@@ -329,9 +319,11 @@ attn_wide_kernel(const __grid_constant__ DecodeArgs p, bool wide) {
 #pragma unroll
                 for (int e = 0; e < 2; e++) {
                     const float r = fmaxf(ref[n][e], top[n][e]);
-                    const float down = ref[n][e] == -INFINITY ? 0.0f : ex2(ref[n][e] - r + (float)(lift_e - e_new));
+                    // (rounded up, never below: weights stay under 2^14)
+                    const float unit = r == -INFINITY ? 0.0f : __fadd_ru(r, (float)lift_of(e_new) - LIFT);
+                    const float down = ref[n][e] == -INFINITY ? 0.0f : ex2(off[n][e] - unit);
                     ref[n][e] = r;
-                    off[n][e] = r == -INFINITY ? 0.0f : __fadd_ru(r, (float)e_new - LIFT);   // never below: weights stay under 2^14
+                    off[n][e] = unit;
                     sum[n][e] *= down;
 #pragma unroll
                     for (int x = 0; x < MT; x++) {
@@ -339,7 +331,17 @@ attn_wide_kernel(const __grid_constant__ DecodeArgs p, bool wide) {
                         o[x][n][2 + e] *= down;
                     }
                 }
-            lift_e = e_new;
+            if (boost_of(e_new) != boost_of(top_e)) {
+                const float change = power_of_two(boost_of(e_new) - boost_of(top_e));
+#pragma unroll
+                for (int x = 0; x < MT; x++)
+#pragma unroll
+                    for (int n = 0; n < NT; n++)
+#pragma unroll
+                        for (int e = 0; e < 4; e++) o[x][n][e] *= change;
+            }
+            top_e = e_new;
+            if (!usual(top_e)) boost_scales<NB>(mine + 17 * D, boost_of(top_e));   // (read by others after the next barrier)
         }
         // the tile before has been read by all: its stage is filled again
         if (left_behind >= 0) issue(left_behind);
@@ -409,7 +411,8 @@ attn_wide_kernel(const __grid_constant__ DecodeArgs p, bool wide) {
                 for (int n = 0; n < NT; n++)
 #pragma unroll
                     for (int e = 0; e < 4; e++)
-                        p.acc[(slot * NT * 8 + 8 * n + 2 * t + (e & 1)) * D + 16 * (warp * MT + m) + 8 * (e >> 1) + g] = o[m][n][e];
+                        p.acc[(slot * NT * 8 + 8 * n + 2 * t + (e & 1)) * D + 16 * (warp * MT + m) + 8 * (e >> 1) + g] =
+                            o[m][n][e] * power_of_two(-boost_of(top_e));
             fresh = true;
         }
         if (left == 1) break;

@@ -175,6 +175,52 @@ __device__ __forceinline__ void lds_words(uint32_t a, uint32_t (&w)[N]) {
     }
 }
 
+// ---------------------------------------------------------------- sizes of the values
+// The second product's operand is weight times scale in binary16, whose least step is 2^-24. `top` is the exponent of the
+// largest scale seen in the segment. Weights are 2^(LIFT - lift) at the reference, scales are taken times 2^boost:
+//   top        lift    boost           a key's product, next to that of the reference's weight and scale 2^top, is off by
+//   below -3   0       -top            2^-31 (a product of boosted scales is exact)
+//   -3 .. 6    0 .. 6  0               2^-28, less where scales are larger
+//   above 6    6       6 - top         2^-31, and its weight by 2^-25
+// and by 2^-10 of itself. So products stay below 2^15, and the offset of the weights is never above the reference: of huge
+// logits one number holds only one of both, and weights would be lost with a higher one. Before the first key top is least.
+constexpr int SMALLEST = -24, USUAL = -3;
+__device__ __forceinline__ int lift_of(int top) { return min(max(top, 0), (int)LIFT); }
+__device__ __forceinline__ bool usual(int top) { return top >= USUAL && top <= (int)LIFT; }
+__device__ __forceinline__ int boost_of(int top) { return usual(top) ? 0 : lift_of(top) - top; }
+// The exponent of the largest magnitude in a warp of half pairs, or `least` if that is larger.
+__device__ __forceinline__ int largest_exponent(__half2 m, int least) {
+#pragma unroll
+    for (int x = 16; x; x >>= 1) m = __hmax2(m, __shfl_xor_sync(FULL, m, x));
+    return max(least, (int)(__float_as_uint(fmaxf(__low2float(m), __high2float(m))) >> 23) - 127);
+}
+__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+// Rewrites the values' scales of a group in shared memory (rarely needed, so the products' loop has nothing of it): `to` gets
+// a pair and the place of its first token in the group. The next copy into the stage comes after the fence.
+template <int NB, typename F>
+__device__ __forceinline__ void rewrite_scales(uint32_t at, F to) {
+#pragma unroll
+    for (int x = threadIdx.x & 31; x < 8 * NB; x += 32) {
+        const uint32_t v = to(lds32(at + 4 * x), x / (2 * NB) * 2 + x % 2 * 8);
+        asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + 4 * x), "r"(v) : "memory");
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+}
+// Zero for keys that no token sees (seen are [begin, end)): there the cache may hold anything.
+template <int NB>
+__device__ __forceinline__ void hide_scales(uint32_t at, int token, int begin, int end) {
+    rewrite_scales<NB>(at, [=](uint32_t v, int i) {
+        const int j = token + i;
+        return v & ((j >= begin && j < end ? 0xffffu : 0) | (j + 1 >= begin && j + 1 < end ? 0xffff0000u : 0));
+    });
+}
+// Times 2^boost, -10..24, in two steps for what binary16 does not hold.
+template <int NB>
+__device__ __forceinline__ void boost_scales(uint32_t at, int boost) {
+    const float first = power_of_two(min(boost, 15)), rest = power_of_two(boost - min(boost, 15));
+    rewrite_scales<NB>(at, [=](uint32_t v, int) { return mul2(mul2(v, pack2(first, first)), pack2(rest, rest)); });
+}
 
 }  // namespace
 

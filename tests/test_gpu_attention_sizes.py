@@ -45,7 +45,7 @@ def test_rows_of_extreme_queries(call, D, Hkv, G, n, size, scale):
     check(out, want, bound_of(parts, call == "prefill") + least_steps(parts, want.shape), "f32")
 
 
-@pytest.mark.parametrize("call,D,Hkv,G,n,lens", [s + ([150, 33, 700],) for s in SHAPES[4:]] + [
+@pytest.mark.parametrize("call,D,Hkv,G,n,lens", [s + ([150, 33, 700],) for s in SHAPES] + [
     ("prefill", 128, 1, 2, 3, [4000, 20, 2300])])             # (the last: keys shared out and joined)
 @pytest.mark.parametrize("power", [10, 20, 26, 60])
 @pytest.mark.parametrize("kind", ["both signs", "negative"])
