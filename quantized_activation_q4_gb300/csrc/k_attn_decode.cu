@@ -275,7 +275,7 @@ attn_decode_kernel(const __grid_constant__ DecodeArgs p, bool wide) {
         const int begin0 = p.a.window > 0 ? end0 - p.a.window : 0;   // no token sees a key below
         // scores, times log2 e
         float s[GROUPS][NT][4];
-        uint32_t used = 0, any = 0;
+        uint32_t used = 0;
         if (ok) used = *reinterpret_cast<const uint32_t *>(&use[warp][stage][0]);   // a byte a group
 #pragma unroll
         for (int r = 0; r < GROUPS; r++) {
@@ -339,35 +339,14 @@ attn_decode_kernel(const __grid_constant__ DecodeArgs p, bool wide) {
                 top[n][e] = m;
                 move |= m - ref[n][e] > HEADROOM;   // (no: both are minus infinity)
             }
-        // the values' scales
-        if (!whole)
-#pragma unroll 1
-            for (int r = 0; r < GROUPS; r++)
-                hide_scales<NB>(buf + r * GB + 17 * D, token0 + r * GROUP, begin0, used >> (8 * r) & 1 ? now.s.len : 0);
-        const auto value_scales = [&](int r, uint32_t (&dv)[2 * NB]) { lds_words<2 * NB>(buf + r * GB + 17 * D + t * 8 * NB, dv); };
-#pragma unroll
-        for (int r = 0; r < GROUPS; r++) {
-            uint32_t dv[2 * NB];
-            value_scales(r, dv);
-#pragma unroll
-            for (int b = 0; b < NB; b++) any |= dv[2 * b] | dv[2 * b + 1];
-        }
-        const bool large = (any & 0x40004000u) != 0 || !usual(top_e);   // a scale of 2 or more, or unusual ones so far
+        const uint32_t scales = buf + 17 * D;   // the values', of the first group
+        if (!whole) hide_scales<NB, GROUPS>(scales, begin0 - token0, now.s.len - token0, used);
+        const bool large = large_scales<NB, GROUPS>(scales) || !usual(top_e);   // a scale of 2 or more, or unusual ones so far
         int e_new = top_e;
         if (__any_sync(FULL, move || large)) {
             if (__any_sync(FULL, large)) {
-                __half2 m = half2_bits(0);
-#pragma unroll 1
-                for (int r = 0; r < GROUPS; r++) {
-                    uint32_t dv[2 * NB];
-                    value_scales(r, dv);
-#pragma unroll
-                    for (int x = 0; x < 2 * NB; x++) m = __hmax2(m, __habs2(half2_bits(dv[x])));
-                }
-                e_new = largest_exponent(m, top_e);
-                if (!usual(e_new))
-#pragma unroll 1
-                    for (int r = 0; r < GROUPS; r++) boost_scales<NB>(buf + r * GB + 17 * D, boost_of(e_new));
+                e_new = largest_exponent<NB, GROUPS>(scales, top_e);
+                if (!usual(e_new)) boost_scales<NB, GROUPS>(scales, boost_of(e_new));
             }
         }
         if (__any_sync(FULL, move) || e_new != top_e) {
@@ -407,7 +386,7 @@ attn_decode_kernel(const __grid_constant__ DecodeArgs p, bool wide) {
         for (int r = 0; r < GROUPS; r++) {
             const uint32_t grp = buf + r * GB;
             uint32_t dv[2 * NB];
-            value_scales(r, dv);
+            lds_words<2 * NB>(scales + r * GB + t * 8 * NB, dv);
             uint32_t pt[NT][2];   // weights of query g: tokens 2t, 2t + 1 and 2t + 8, 2t + 9
 #pragma unroll
             for (int n = 0; n < NT; n++) {

@@ -270,16 +270,9 @@ attn_wide_kernel(const __grid_constant__ DecodeArgs p, bool wide) {
         for (int n = 0; n < NT; n++)
 #pragma unroll
             for (int e = 0; e < 2; e++) move |= fmaxf(s[n][e], s[n][2 + e]) - ref[n][e] > HEADROOM;   // (no: both minus infinity)
-        // the values' scales of a block, tokens 2t, 2t + 1 and 2t + 8, 2t + 9 of a group
-        if (!whole) hide_scales<NB>(mine + 17 * D, token0 + warp * GROUP, begin0, used >> (8 * warp) & 1 ? now.s.len : 0);
-        const auto value_scales = [&](int r, int b) { return lds64(buf + r * GB + 17 * D + (t * NB + b) * 8); };
-        uint32_t any = 0;   // of the warp's group: bit 14 of a half is set from 2 on
-#pragma unroll
-        for (int b = 0; b < NB; b++) {
-            const uint2 d = value_scales(warp, b);
-            any |= d.x | d.y;
-        }
-        const bool large = (any & 0x40004000u) != 0 || !usual(top_e);   // a scale of 2 or more, or unusual ones so far
+        const uint32_t scales = mine + 17 * D;   // the values', of the warp's group
+        if (!whole) hide_scales<NB, 1>(scales, begin0 - token0 - warp * GROUP, now.s.len - token0 - warp * GROUP, used >> (8 * warp));
+        const bool large = large_scales<NB, 1>(scales) || !usual(top_e);   // a scale of 2 or more, or unusual ones so far
         // All warps meet: what the tile before left in shared memory has been read, and whether something moves.
         if (__syncthreads_or(move || large)) {
             float top[NT][2];
@@ -293,13 +286,7 @@ attn_wide_kernel(const __grid_constant__ DecodeArgs p, bool wide) {
                     x = fmaxf(x, __shfl_xor_sync(FULL, x, 16));
                     if (g == 0) meet[warp][8 * n + 2 * t + e] = x;
                 }
-            __half2 m = half2_bits(0);
-#pragma unroll
-            for (int b = 0; b < NB; b++) {
-                const uint2 d = value_scales(warp, b);
-                m = __hmax2(m, __hmax2(__habs2(half2_bits(d.x)), __habs2(half2_bits(d.y))));
-            }
-            const int mine_e = largest_exponent(m, top_e);
+            const int mine_e = largest_exponent<NB, 1>(scales, top_e);
             if (lane == 0) exponents[warp] = mine_e;
             __syncthreads();
             int e_new = top_e;
@@ -341,7 +328,7 @@ attn_wide_kernel(const __grid_constant__ DecodeArgs p, bool wide) {
                         for (int e = 0; e < 4; e++) o[x][n][e] *= change;
             }
             top_e = e_new;
-            if (!usual(top_e)) boost_scales<NB>(mine + 17 * D, boost_of(top_e));   // (read by others after the next barrier)
+            if (!usual(top_e)) boost_scales<NB, 1>(scales, boost_of(top_e));   // (read by others after the next barrier)
         }
         // the tile before has been read by all: its stage is filled again
         if (left_behind >= 0) issue(left_behind);
@@ -367,7 +354,7 @@ attn_wide_kernel(const __grid_constant__ DecodeArgs p, bool wide) {
             lds_words<MT>(buf + r * GB + 9 * D + ((warp * MT / 4 * 8 + g) * 4 + t) * 16 + warp * MT % 4 * 4, x);
 #pragma unroll
             for (int b = 0; b < (MT + 1) / 2; b++) {
-                const uint2 d = value_scales(r, warp * MT / 2 + b);
+                const uint2 d = lds64(buf + r * GB + 17 * D + (t * NB + warp * MT / 2 + b) * 8);   // tokens 2t, 2t + 1; 2t + 8, 2t + 9
                 uint32_t pb[NT][2];
 #pragma unroll
                 for (int n = 0; n < NT; n++) pb[n][0] = mul2(pt[n].x, d.x), pb[n][1] = mul2(pt[n].y, d.y);

@@ -188,38 +188,58 @@ constexpr int SMALLEST = -24, USUAL = -3;
 __device__ __forceinline__ int lift_of(int top) { return min(max(top, 0), (int)LIFT); }
 __device__ __forceinline__ bool usual(int top) { return top >= USUAL && top <= (int)LIFT; }
 __device__ __forceinline__ int boost_of(int top) { return usual(top) ? 0 : lift_of(top) - top; }
-// The exponent of the largest magnitude in a warp of half pairs, or `least` if that is larger.
-__device__ __forceinline__ int largest_exponent(__half2 m, int least) {
+__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+// The values' scales of N groups side by side in shared memory, a pair a lane and turn: `f` gets its address and the place of
+// its first token. `at`: the first group's scales.
+template <int NB, int N, typename F>
+__device__ __forceinline__ void each_scales(uint32_t at, F f) {
+    constexpr int PAIRS = 8 * NB;   // of a group
+#pragma unroll
+    for (int x0 = 0; x0 < N * PAIRS; x0 += 32) {
+        const int x = x0 + (threadIdx.x & 31), y = x % PAIRS;
+        if (N * PAIRS % 32 == 0 || x < N * PAIRS)
+            f(at + x / PAIRS * group_bytes(32 * NB) + 4 * y, x / PAIRS * GROUP + y / (2 * NB) * 2 + y % 2 * 8);
+    }
+}
+// Whether one of them is 2 or more: bit 14 of a half is set from there on. (A lane's own alone.)
+template <int NB, int N>
+__device__ __forceinline__ bool large_scales(uint32_t at) {
+    uint32_t any = 0;
+    each_scales<NB, N>(at, [&](uint32_t a, int) { any |= lds32(a); });
+    return (any & 0x40004000u) != 0;
+}
+// The exponent of the largest one, or `least` if that is larger.
+template <int NB, int N>
+__device__ __forceinline__ int largest_exponent(uint32_t at, int least) {
+    __half2 m = half2_bits(0);
+    each_scales<NB, N>(at, [&](uint32_t a, int) { m = __hmax2(m, __habs2(half2_bits(lds32(a)))); });
 #pragma unroll
     for (int x = 16; x; x >>= 1) m = __hmax2(m, __shfl_xor_sync(FULL, m, x));
     return max(least, (int)(__float_as_uint(fmaxf(__low2float(m), __high2float(m))) >> 23) - 127);
 }
-__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
-// Rewrites the values' scales of a group in shared memory (rarely needed, so the products' loop has nothing of it): `to` gets
-// a pair and the place of its first token in the group. The next copy into the stage comes after the fence.
-template <int NB, typename F>
+// Rewrites them (rarely needed, so the products' loop has nothing of it). The next copy into the stage comes after the fence.
+template <int NB, int N, typename F>
 __device__ __forceinline__ void rewrite_scales(uint32_t at, F to) {
-#pragma unroll
-    for (int x = threadIdx.x & 31; x < 8 * NB; x += 32) {
-        const uint32_t v = to(lds32(at + 4 * x), x / (2 * NB) * 2 + x % 2 * 8);
-        asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + 4 * x), "r"(v) : "memory");
-    }
+    each_scales<NB, N>(at, [&](uint32_t a, int token) {
+        asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(to(lds32(a), token)) : "memory");
+    });
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncwarp();
 }
-// Zero for keys that no token sees (seen are [begin, end)): there the cache may hold anything.
-template <int NB>
-__device__ __forceinline__ void hide_scales(uint32_t at, int token, int begin, int end) {
-    rewrite_scales<NB>(at, [=](uint32_t v, int i) {
-        const int j = token + i;
-        return v & ((j >= begin && j < end ? 0xffffu : 0) | (j + 1 >= begin && j + 1 < end ? 0xffff0000u : 0));
+// Zero for keys that no token sees: there the cache may hold anything. Seen are [begin, end) of the groups in `used` (a byte
+// each), counted from the first group's first token.
+template <int NB, int N>
+__device__ __forceinline__ void hide_scales(uint32_t at, int begin, int end, uint32_t used) {
+    rewrite_scales<NB, N>(at, [=](uint32_t v, int i) {
+        const uint32_t seen = (i >= begin && i < end ? 0xffffu : 0) | (i + 1 >= begin && i + 1 < end ? 0xffff0000u : 0);
+        return used >> (8 * (i / GROUP)) & 1 ? v & seen : 0;
     });
 }
 // Times 2^boost, -10..24, in two steps for what binary16 does not hold.
-template <int NB>
+template <int NB, int N>
 __device__ __forceinline__ void boost_scales(uint32_t at, int boost) {
     const float first = power_of_two(min(boost, 15)), rest = power_of_two(boost - min(boost, 15));
-    rewrite_scales<NB>(at, [=](uint32_t v, int) { return mul2(mul2(v, pack2(first, first)), pack2(rest, rest)); });
+    rewrite_scales<NB, N>(at, [=](uint32_t v, int) { return mul2(mul2(v, pack2(first, first)), pack2(rest, rest)); });
 }
 
 }  // namespace
