@@ -823,14 +823,19 @@ QK_API qk_status qk_attn_decode(const qk_kv_cache *cache, const qk_attn *attn, i
  *              (blocks past n_heads * head_dim / 32 are zero), or both NULL
  *   d_live_rows: the number of live SEQUENCES of B
  *   ws         qk_attn_prefill_workspace_bytes bytes, 128-byte aligned: the keys
- *              and values of the call in binary16 and, for max_kv from 2048 on,
- *              partial outputs of calls with few rows (84 MB at head_dim 128).
+ *              and values of the call in binary16 (4 * head_dim bytes for each of
+ *              B * n_kv_heads * max_kv, max_kv rounded up to 128: it goes by the
+ *              longest sequence) and, for max_kv from 2048 on, partial outputs of
+ *              calls with few rows (84 MB at head_dim 128).
  *              Scratch, no state kept.
  * Runs on the tensor cores (tcgen05) with binary16 operands: keys and values
  * (code - 8) * d, queries scaled by a power of two per row, weights exp(s - max),
  * each rounded once, with binary32 sums. Keys and values beyond binary16's range
- * are taken as +-65504, its largest. Errors: as qk_attn_decode, and B > 65535 or rows >
- * 2^24 (QK_ERR_UNSUPPORTED). rows = 0 or B = 0 launches nothing.
+ * are taken as +-65504, its largest. The roundings are not those of the decode, so
+ * the same rows differ in their last bits between the two calls; they depend on
+ * rows, B, max_kv and the lengths (by which keys are shared out), not on the run.
+ * Errors: as qk_attn_decode, and B > 65535 or rows > 2^24 (QK_ERR_UNSUPPORTED).
+ * rows = 0 or B = 0 launches nothing.
  */
 QK_API size_t qk_attn_prefill_workspace_bytes(const qk_kv_cache *cache, int64_t B, int64_t max_kv);
 QK_API qk_status qk_attn_prefill(const qk_kv_cache *cache, const qk_attn *attn, int64_t B, int64_t rows,

@@ -18,12 +18,13 @@
 // happens where the values' scales are not between 2^-3 and 2 is in qk_decode.cuh.
 //
 // A tile is 128 tokens, 64 for each of two warps (four groups: the barrier, the votes and the places of pages are paid for
-// once; with 32 tokens a warp and tile 64 sequences of 8192 keys took 84 us for 71). Six CTAs an SM by registers (168) and
-// shared memory (two stages a warp).
+// once; with 32 tokens a warp and tile 64 sequences of 8192 keys took 84 us for 71 when it was chosen). Six CTAs an SM by
+// registers (168) and shared memory (two stages a warp).
 //
-// Bound by instruction issue next to memory: 2304 bytes of cache (16 tokens of a head of 128) cost 292 warp instructions, at
-// full issue 9 TB/s. 64 sequences of 8192 keys, 28 heads over 4 of 128: 71 us = 4.3 TB/s, 64% of the measured copy rate (issue
-// 54% active, the logic pipe 42%).
+// 2304 bytes of cache (16 tokens of a head of 128) cost 279 warp instructions, at full issue 9.4 TB/s. 64 sequences of 8192
+// keys, 28 heads over 4 of 128: 67.5 us = 4.5 TB/s, 67% of the measured copy rate. Neither is full (issue 55% active): most
+// stalls are the fixed latency of dependent instructions (1.1 warps an issue), copies and page numbers (0.75) and the math
+// pipes (0.6).
 
 #include <algorithm>
 
@@ -182,7 +183,7 @@ attn_decode_kernel(const __grid_constant__ DecodeArgs p, bool wide) {
     if (lane < S) mbar_init(bar0 + 8 * lane, GROUPS);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     // (No early start of the next kernel: the join's CTAs, waiting on SMs that are done, held up the passes of calls in a row;
-    // 64 sequences of 8192 keys took 93 us a call for 71.)
+    // 64 sequences of 8192 keys took 93 us a call for 71 then.)
     pdl_wait();
     const int live = live_rows(p.live, p.B);
 
@@ -667,10 +668,12 @@ Layout layout_of(int Hkv, int D, int n_heads, int64_t B, int T) {
     Layout l;
     const int tiles = (T * (n_heads / Hkv) + 7) / 8;   // of 8 columns
     // Up to 16 columns (8 at head_dim 256, for the registers of the output) take this file's kernel, more the wide one.
-    // Both sides, us, this file's / the wide one's:
-    //   32 sequences of 8192 keys: 16 columns, D = 128, 2 kv heads 46 / 48; 14, D = 128, 4: 67 / 75; 16, D = 64, 8: 73 / 94
-    //   16 sequences of 8192 keys, D = 256: 8 columns, 4 kv heads 58 / 75; 16, 2 (two CTAs of 8 here): 54 / 51
-    //   16 sequences of 1500 to 9000 keys, 8 kv heads, 32 columns (two CTAs of 16 here): D = 128 69 / 65, D = 64 47 / 45
+    // Both sides, us, this file's (CTAs of up to 16 columns, 8 at D = 256) / the wide one's (32; 16 at D = 256 if they do):
+    //   32 sequences of 8192 keys: 16 columns, D = 128, 2 kv heads 45 / 61; 14, D = 128, 4: 65 / 97; 16, D = 64, 8: 70 / 115
+    //   16 sequences of 8192 keys, D = 256: 8 columns, 4 kv heads 55 / 70; 16, 2: 51 / 48
+    //   16 sequences of 1500 to 9000 keys: 17, 24, 32 columns of 8 kv heads, D = 64 49.5, 50.2, 50.5 / 47.9, 48.8, 49.3;
+    //   D = 128 72.8, 73.7, 73.1 / 73.5, 74.9, 74.9; D = 256, 4 kv heads: 12 columns 62 / 55, 32: 102 / 70
+    // At D = 128 it is close: 2 sequences of 2000 keys, 32 columns of 8 kv heads 16.0 / 17.1, 64 of 1000, 20 columns 78 / 65.
     const bool wide = tiles > column_tiles(D);
     l.NT = wide ? (tiles > 2 ? WIDE_COLUMNS : 2) : tiles;
     l.groups = (tiles + l.NT - 1) / l.NT;
@@ -722,8 +725,8 @@ qk_status launch_attn_decode(const KvCache &c, const qk_attn &a, int B, int T, u
     const int rows = B * T;
     const JoinArgs j = {p, img, row_blocks, l.NT, l.tile};
     // Many heads have few partial results each: a warp a head; few heads have many: a CTA a head. Whole calls, us, by CTAs /
-    // by warps: 32 heads behind 131072 keys 46 / 82, 224 behind 2000 13.0 / 18.1, 512 behind 8192 43.0 / 45.1, 1024 behind
-    // 8192 69.2 / 69.7, 1792 behind 8192 71.1 / 70.5, 4096 of 1500 to 9000 keys (head_dim 128) 68.5 / 65.2.
+    // by warps: 32 heads behind 131072 keys 62 / 114, 224 behind 2000 12.7 / 18.7, 512 behind 8192 30.0 / 34.5, 1024 behind
+    // 8192 42.5 / 44.7, 1792 behind 8192 67.7 / 67.2, 4096 of 1500 to 9000 keys (32 columns of 128) 78.3 / 75.0.
     const int64_t heads = (int64_t)rows * a.n_heads;
     if (heads >= 1024) {
         auto *combine = c.D == 64    ? attn_combine_warps_kernel<64>

@@ -1,9 +1,9 @@
 // Attention of prompts and chunks of prompts over the 4-bit cache (qk_attn_prefill), on tcgen05.
 //
 // attn_stage_kernel turns the call's pages into binary16 once: keys [token][column] and values transposed
-// [column][token], each (code - 8) * d rounded once and held to +-65504, so that both products read their second operand K-major by plain
-// tensor copies. Inside a group of 16 the tokens are in the order of the value codes' words (position 4 t + s is token
-// 2 t + s % 2 + 8 (s / 2)), in both, so that the words are unpacked without exchanges; the mask undoes it.
+// [column][token], each (code - 8) * d rounded once and held to +-65504, so that both products read their second operand
+// K-major by plain tensor copies. Inside a group of 16 the tokens are in the order of the value codes' words (position 4 t + s
+// is token 2 t + s % 2 + 8 (s / 2)), in both, so that the words are unpacked without exchanges; the mask undoes it.
 //
 // attn_prefill_kernel: a CTA takes 128 rows (query token, head of the group) a tile, two tiles where the output fits
 // (head_dim 64 and 128), of one sequence and key/value head, and walks over the keys that they see in steps of BN. For
@@ -14,7 +14,7 @@
 //
 // Bound by the tensor cores and, nearly as much, by the chain scores - weights - products of a tile: at D = 128 a step of two
 // tiles takes 3040 cycles, the products alone 2400 (2048 at their peak rate). 1024 rows of 28 heads over 4 behind 32000 keys:
-// 312 us = 1.53 PFLOP/s (tensor pipe 67% active) and 35 for staging and join, 68% of the measured bf16 rate in all; 3325 rows
+// 314 us = 1.52 PFLOP/s (tensor pipe 68% active) and 35 for staging and join, 68% of the measured bf16 rate in all; 3325 rows
 // without a past: 91 us and 7. What the steps gave there (us): one thread a row 127, two 97; products issued under
 // elect.sync and not by lane 0 176 -> 127; rescaling eight columns at a time 228 -> 97 (with 32 the scores spilled).
 
@@ -903,7 +903,7 @@ qk_status launch_tc(PrefillArgs &p, const Staged &l, cudaStream_t s) {
     const int64_t tiles = (ceil_div((int64_t)p.rows * p.G, Z::TILES * ROWS) + std::min(p.B, p.rows) - 1) * p.c.Hkv;
     // Shares of keys: so many that rounds of CTAs times (steps of a share + what a CTA spends around them, about 8 steps)
     // is least, for keys as many as max_kv; a share is 4 steps at least. Whole calls, us, unshared / shared: 64 rows of 32
-    // heads over 8 behind 60000 keys 722 / 124, 300 behind 4000 65 / 48, 1024 of 28 over 4 behind 32000 398 / 369.
+    // heads over 8 behind 60000 keys 714 / 125, 300 behind 4000 66 / 49, 1024 of 28 over 4 behind 32000 392 / 343.
     p.parts = 1;
     if (p.max_kv >= PART_KEYS) {
         const int64_t steps = ceil_div(p.max_kv, Z::BN), sms = sm_count();

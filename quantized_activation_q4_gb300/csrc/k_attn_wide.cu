@@ -8,10 +8,12 @@
 // which they learn from each other by the barrier that the exchange needs anyway. Codes are converted exactly for both
 // products (the bias of the scores as an initial accumulator would need more registers than there are).
 //
-// Bound by instruction issue: a group of 16 tokens of a head of 128 costs 890 warp instructions for 32 columns (the scales'
-// products, exponentials and moves of 32 columns more than the conversion), at 52% issue. 16 sequences of 1500 to 9000
-// tokens with 8 new tokens each, 32 heads over 8: 57 us and 9 for the join; with two CTAs of 16 columns in k_attn_decode.cu's
-// kernel the call takes 69. The conversions and products in one asm block, as there, spilled registers and took a microsecond more.
+// A group of 16 tokens of a head of 128 costs 874 warp instructions for 32 columns (the scales' products, exponentials and
+// moves of 32 columns more than the conversion), issued half of the time (50%); most stalls are the fixed latency of dependent
+// instructions (1.9 warps an issue), then copies (1.0) and shared memory (0.8). 16 sequences of 1500 to 9000 tokens with 8 new
+// tokens each, 32 heads over 8: 67.2 us with the join; two CTAs of 16 columns in k_attn_decode.cu's kernel 66.0 (the rule at
+// layout_of has both sides over more shapes). The conversions and products in one asm block, as there, spilled registers and
+// took a microsecond more.
 
 #include <algorithm>
 

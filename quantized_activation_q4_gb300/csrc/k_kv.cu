@@ -4,8 +4,8 @@
 //   kv_read_kernel    the values of cached tokens as rows
 //
 // Append reads a token's q, k and v rows once, writes q once and 9/16 byte a cached value. 3325 tokens of 28 + 8 heads of 128
-// with three axes: 25 us, 3.1 TB/s; bound by issue (5000 warp instructions a token, 58% active) and by the barrier behind the
-// angles. Four quads a thread in any head 43 us, four tokens a CTA 65 (registers). Read of 16384 tokens of 8 heads: 21 us,
+// with three axes: 25 us, 3.1 TB/s; 5000 warp instructions a token, issued 58% of the time; the largest stall is the barrier
+// behind the angles, which few threads work out. Four quads a thread in any head 43 us, four tokens a CTA 65 (registers). Read of 16384 tokens of 8 heads: 21 us,
 // 4.1 TB/s; one token and quad a thread 67.
 // A block of 32 columns is handled by 8 consecutive lanes, 4 columns each; its codes meet their nibble partners by one
 // shuffle (columns 16 apart for k, 8 apart for v). Arithmetic is binary32 with IEEE division.
